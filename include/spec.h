@@ -87,7 +87,11 @@ typedef enum {
     SPEC_OP_BRANCH_PLAN = 4,
     SPEC_OP_VERIFY_TOPK = 5,
     SPEC_OP_TREE_VERIFY = 6,
-    SPEC_OP_DRAFT_TOPK = 7
+    SPEC_OP_DRAFT_TOPK = 7,
+    /* 8 is not an operation */
+    SPEC_OP_PROCESS_LOGITS = 9,
+    SPEC_OP_TOP_LOGITS = 10,
+    SPEC_OP_DISTILL = 11
 } spec_op;
 
 /* Device status flags (OR-ed into the workspace status word). */
@@ -104,6 +108,11 @@ typedef enum {
 #define SPEC_MAX_TOP_K 32      /* spec_verify_topk: largest top_k                  */
 #define SPEC_MAX_V_DRAFT_TOPK (1 << 19)   /* spec_draft_block_topk: vocabulary size */
 #define SPEC_MAX_TREE_NODES 1024  /* spec_tree_select / spec_tree_verify: nodes per tree */
+#define SPEC_MAX_HISTORY (1 << 19)    /* spec_process_logits: tokens of one history  */
+#define SPEC_MAX_BIASES 2047          /* spec_process_logits: biased tokens per request */
+#define SPEC_MAX_TEACHER 128          /* spec_top_logits / spec_distill: entries per row */
+#define SPEC_MAX_V_TEACHER (1 << 20)  /* spec_top_logits / spec_distill: vocabulary size */
+#define SPEC_MAX_TEACHER_ROWS (1 << 24)   /* spec_top_logits / spec_distill: rows       */
 
 /*
  * spec_workspace_bytes - workspace size for one operation (host only, pure).
@@ -116,6 +125,10 @@ typedef enum {
  *          SPEC_OP_TREE_VERIFY: B = trees, gamma = nodes per tree (0 allowed, up to
  *          SPEC_MAX_TREE_NODES), V, r unused.
  *          SPEC_OP_DRAFT_TOPK: B requests, V entries (gamma and r unused).
+ *          SPEC_OP_PROCESS_LOGITS: the status word only (pass B requests, gamma = rows
+ *          per request, V, r = 0).
+ *          SPEC_OP_TOP_LOGITS / SPEC_OP_DISTILL: B = rows, gamma = entries per row, V,
+ *          r unused.
  *          For SPEC_OP_DRAFT the size covers one launch's slice of requests, which
  *          spec_draft_block reuses across the slices of a larger batch.
  * Returns 0 for arguments outside the supported ranges.
@@ -556,6 +569,115 @@ spec_status spec_tree_verify(const void *target_logits, spec_dtype target_dtype,
                              int32_t *n_accepted_out, int32_t *path_out, int32_t *committed_out,
                              int32_t *bonus_out, void *workspace, size_t workspace_bytes,
                              spec_stream_t stream);
+
+/*
+ * spec_process_logits - penalties for repeated tokens, biases, temperature and grammar
+ * masks on the logits rows of a block, before they are verified (or drafted from).
+ *
+ * Request b has a history h[0:n] (its prompt h[0:m], then what was generated) and block
+ * tokens x_1..x_{R-1}; row j = 0..R-1 is the distribution after h[0:n] ++ x_1..x_j, so in
+ * a block every drafted token already counts for the rows behind it, as it would have in
+ * token-by-token decoding.  With c(v) the occurrences of v in h[m:n] ++ x_1..x_j and
+ * seen(v) = c(v) > 0 or v in h[0:m], in this order:
+ *     y = l(v)
+ *     y = seen(v) ? (y > 0 ? y / repetition : y * repetition) : y
+ *     y = y - (frequency * c(v) + presence * [c(v) > 0])
+ *     y = y + bias(v)
+ *     y = y / temperature
+ *     out(v) = mask bit v ? y : -inf
+ * in float32, rounded once to the rows' type.
+ *   logits        [B, R] rows of V entries, consecutive rows ld entries apart (ld >= V;
+ *                 ld = V is the contiguous layout), dtype float32 or bf16.
+ *   out           the same layout; may be logits itself.
+ *   history       int32 [B, Lmax] (NULL when Lmax = 0).
+ *   lengths       int32 [B]: n (NULL: Lmax for every request).
+ *   prompt_lengths  int32 [B]: m (NULL: 0, everything counts as generated).
+ *   block         int32 [B, R-1] (NULL: rows see the history only).
+ *   repetition, frequency, presence, temperature
+ *                 float32 [B], each NULL for none (1, 0, 0, 1).
+ *   bias_ids, bias_values   int32 / float32 [B, n_bias]: tokens and what is added to their
+ *                 logits; id -1 is an empty slot; a token listed twice takes its last slot.
+ *   mask          32-bit words [B, mask_rows, (V + 31) / 32], bit v % 32 of word v / 32
+ *                 set where v is allowed; mask_rows = R, or 1 for a mask that all of a
+ *                 request's rows share (NULL: everything is allowed).
+ *   workspace     spec_workspace_bytes(SPEC_OP_PROCESS_LOGITS, B, R, V, 0): the status word.
+ * A masked entry is -inf whatever it held (NaN, +inf); a row whose mask leaves nothing is
+ * all -inf, which verification reports as a row without a distribution.  A token outside
+ * [0, V) (a bias id below -1) or a length outside its range raises flag TOKEN and counts
+ * for nothing; a repetition or temperature that is not positive and finite, or a frequency
+ * or presence that is not finite, makes the request's allowed entries NaN (flag NONFINITE).
+ * Limits: 1 <= B <= 65535, 1 <= R <= SPEC_MAX_GAMMA + 1, 1 <= V <= SPEC_MAX_V,
+ * 0 <= Lmax <= SPEC_MAX_HISTORY, 0 <= n_bias <= SPEC_MAX_BIASES, V <= ld < 2^31.
+ */
+spec_status spec_process_logits(const void *logits, spec_dtype dtype, int B, int R, int V, int ld,
+                                const int32_t *history, int Lmax, const int32_t *lengths,
+                                const int32_t *prompt_lengths, const int32_t *block,
+                                const float *repetition, const float *frequency, const float *presence,
+                                const float *temperature, const int32_t *bias_ids,
+                                const float *bias_values, int n_bias, const uint32_t *mask,
+                                int mask_rows, void *out, void *workspace, size_t workspace_bytes,
+                                spec_stream_t stream);
+
+/*
+ * spec_top_logits - each row's K largest logits and the log-sum-exp of the rest: a
+ * teacher row in the compact form that spec_distill reads.
+ *
+ * For a row z and temperature t:
+ *     ids, values   the K largest entries, descending, ties to the lowest index; values
+ *                   are the logits as they are (not divided by t).  An entry of -inf is
+ *                   never taken: slots left over hold id -1 and value -inf.
+ *     tail          ln sum exp(z_v / t) over the entries not taken (-inf when none is left)
+ *     lse           ln sum exp(z_v / t) over all entries
+ *   logits      [rows] rows of V entries, ld entries apart (ld >= V), float32 or bf16.
+ *   values_out  float32 [rows, K]; ids_out int32 [rows, K]; tail_out float32 [rows];
+ *               lse_out float32 [rows] (nullable).
+ *   workspace   spec_workspace_bytes(SPEC_OP_TOP_LOGITS, rows, K, V, 0).
+ * A row that holds NaN or +inf gets ids -1 and NaN in the other outputs, a row with no
+ * finite entry ids -1 and -inf (flag NONFINITE for both).
+ * Limits: 1 <= rows <= SPEC_MAX_TEACHER_ROWS, 1 <= K <= SPEC_MAX_TEACHER,
+ * 1 <= V <= SPEC_MAX_V_TEACHER, V <= ld < 2^31, temperature positive and finite.
+ */
+spec_status spec_top_logits(const void *logits, spec_dtype dtype, int rows, int V, int ld, int K,
+                            float temperature, float *values_out, int32_t *ids_out, float *tail_out,
+                            float *lse_out, void *workspace, size_t workspace_bytes,
+                            spec_stream_t stream);
+
+/*
+ * spec_distill - distillation of a drafter's rows from a teacher's top logits: the loss,
+ * and its gradient on request.
+ *
+ * A row's teacher is a distribution over K + 1 buckets, its K named entries and the rest of
+ * the vocabulary: p = softmax(values_1 / t, .., values_K / t, tail).  With q the student's
+ * softmax(z / t), q_k its probability of the k-th named entry and q_T its mass on the
+ * entries that no id names,
+ *     loss = sum_k p_k ln(p_k / q_k) + p_T ln(p_T / q_T)       (0 ln 0 = 0)
+ *     grad = weight * d loss / d z:
+ *            (weight / t) (q_v - p_k)               v named by slot k
+ *            (weight / t) q_v (1 - p_T / q_T)       otherwise
+ * Without tail (NULL, or -inf in a row) the teacher is renormalised over its named entries.
+ * One named entry of value 0 and no tail is the cross entropy with a hard label.
+ *   student     [rows] rows of V entries, ld entries apart (ld >= V), float32 or bf16.
+ *   values      [rows, K] float32 or bf16 (spec_top_logits' values); ids int32 [rows, K],
+ *               id -1 an empty slot, the others distinct.
+ *   tail        float32 [rows] (spec_top_logits' tail at the same t), nullable.
+ *   weight      float32 [rows], nullable (1).  A row of weight 0 is not read: its loss, lse
+ *               and gradient are 0.
+ *   loss_out    float32 [rows], not weighted; lse_out float32 [rows] (nullable):
+ *               ln sum exp(z_v / t).
+ *   grad_out    the student's layout and type; NULL for the loss alone; may be student
+ *               itself, which it then replaces.
+ *   workspace   spec_workspace_bytes(SPEC_OP_DISTILL, rows, K, V, 0).
+ * A row whose teacher has no entry (every id -1, no tail) has loss 0 and gradient 0.  A
+ * student row with NaN, +inf or no finite entry, and a teacher row with NaN or +inf, gets
+ * NaN in its outputs (flag NONFINITE); an id outside [-1, V) or listed twice does too (flag
+ * TOKEN).  Where the teacher gives mass to what the student rules out, the loss is +inf.
+ * Limits: those of spec_top_logits.
+ */
+spec_status spec_distill(const void *student, spec_dtype dtype, int rows, int V, int ld,
+                         const void *values, spec_dtype values_dtype, const int32_t *ids, int K,
+                         const float *tail, const float *weight, float temperature, float *loss_out,
+                         float *lse_out, void *grad_out, void *workspace, size_t workspace_bytes,
+                         spec_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -28,9 +28,13 @@ the pages step by step, in their order and notation:
 * ``schedule`` - the DSpark verify budget: per-request pass products of the confidences,
   the budget given to the most likely positions across the batch, the throughput
   against a cost curve.
+* ``process`` - penalties for repeated tokens, biases, temperature and grammar masks on the
+  logits rows of a block.
+* ``teacher`` - a row's largest logits with the log-sum-exp of the rest, and the
+  distillation loss and gradient from them.
 
 Pins (tests that tie each function to the pages or to mathematics rather than to
 itself) live in ``tests/test_oracle_*.py``; each function's docstring names them.
 """
 
-from . import philox, draft, verify, e2etv, schedule, anchors, topk, tree  # noqa: F401
+from . import philox, draft, verify, e2etv, schedule, anchors, topk, tree, process, teacher  # noqa: F401

@@ -27,6 +27,7 @@ STATUS = {
 F32, BF16 = 0, 1
 OP_DRAFT, OP_VERIFY, OP_E2ETV, OP_DRAFT_VERIFY, OP_BRANCH_PLAN, OP_VERIFY_TOPK, OP_TREE_VERIFY, OP_DRAFT_TOPK = (
     0, 1, 2, 3, 4, 5, 6, 7)
+OP_PROCESS_LOGITS, OP_TOP_LOGITS, OP_DISTILL = 9, 10, 11
 DEV_TIMEOUT, DEV_NONFINITE, DEV_TOKEN = 1, 2, 4
 
 # C signatures of include/spec.h, as ctypes types
@@ -57,6 +58,12 @@ SIGNATURES = {
     "spec_draft_block_topk": (_i32, [_vp, _i32, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32, ctypes.c_double,
                                      _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
     "spec_tree_verify": (_i32, [_vp, _i32, _vp, _vp, _vp, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "spec_process_logits": (_i32, [_vp, _i32, _i32, _i32, _i32, _i32, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                                   _vp, _vp, _i32, _vp, _i32, _vp, _vp, _sz, _vp]),
+    "spec_top_logits": (_i32, [_vp, _i32, _i32, _i32, _i32, _i32, ctypes.c_float, _vp, _vp, _vp, _vp, _vp, _sz,
+                               _vp]),
+    "spec_distill": (_i32, [_vp, _i32, _i32, _i32, _i32, _vp, _i32, _vp, _i32, _vp, _vp, ctypes.c_float, _vp, _vp,
+                            _vp, _vp, _sz, _vp]),
 }
 
 _lib = None
@@ -138,6 +145,54 @@ def _need(t, name, device=None, dtype=None, shape=None):
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if shape is not None and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    return t
+
+
+def _need_rows(t, name, device=None):
+    """Like _need for logits rows [..., V] that may lie further apart than V entries:
+    returns the row stride.  The leading dimensions must be evenly spaced."""
+    if t is None:
+        raise ValueError(f"{name} is required")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (the library has no CPU path)")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dim() < 2:
+        raise ValueError(f"{name} must be at least [rows, V]")
+    V, ld, rows = t.shape[-1], 0, 1
+    if V > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must have its entries next to one another (stride 1)")
+    for n, st in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+        if n == 1:
+            continue
+        if ld == 0:
+            ld = st // rows if st % rows == 0 else 0
+        if ld < V or st != rows * ld:
+            raise ValueError(f"{name} must have evenly spaced rows at least V entries apart, got strides {t.stride()}")
+        rows *= n
+    return ld or V
+
+
+def _made_on(stream):
+    """What a call allocates belongs to the stream it runs on."""
+    torch = _torch()
+    return torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream())
+
+
+def _rows_like(t, ld):
+    """Uninitialised rows of t's shape, dtype and row stride."""
+    torch = _torch()
+    V = t.shape[-1]
+    if ld == V:
+        return torch.empty(t.shape, dtype=t.dtype, device=t.device)
+    return torch.empty((*t.shape[:-1], ld), dtype=t.dtype, device=t.device)[..., :V]
+
+
+def _need_same_rows(t, name, like, ld):
+    if t.dtype != like.dtype or tuple(t.shape) != tuple(like.shape):
+        raise ValueError(f"{name} must be {like.dtype} {tuple(like.shape)}, got {t.dtype} {tuple(t.shape)}")
+    if _need_rows(t, name, like.device) != ld and t.numel() > t.shape[-1]:
+        raise ValueError(f"{name} must have the row stride {ld}")
     return t
 
 
@@ -508,5 +563,138 @@ def draft_block_topk(logits, anchor, U, Wt, top_k, top_p, seeds, ws=None, out=No
                                      V, int(top_k), float(top_p), _ptr(seeds), _ptr(out["tokens"]), _ptr(out["conf"]),
                                      _ptr(out.get("qtok")), _ptr(ws), ws.numel(), _stream(stream))
     _check(code, "spec_draft_block_topk")
+    out["ws"] = ws
+    return out
+
+
+# ---------------------------------------------------------------------------------
+# the rows before verification, and what a drafter learns from them
+# ---------------------------------------------------------------------------------
+def process_logits(logits, history=None, lengths=None, prompt_lengths=None, block=None, repetition=None,
+                   frequency=None, presence=None, bias_ids=None, bias_values=None, mask=None, temperature=None,
+                   ws=None, out=None, stream=None):
+    """spec_process_logits.  logits [B, R, V] f32/bf16 (rows may lie further apart than V);
+    history int32 [B, Lmax], lengths and prompt_lengths int32 [B]; block int32 [B, R - 1],
+    the block's tokens; repetition, frequency, presence, temperature float32 [B]; bias_ids
+    int32 and bias_values float32 [B, n]; mask int32 [B, R, ceil(V / 32)] or, shared by a
+    request's rows, [B, ceil(V / 32)], a set bit for an allowed token.  Every one of them
+    but logits may be None.  ``out=dict(logits=...)`` may be logits itself.  Returns a dict
+    of device tensors: logits."""
+    torch = _torch()
+    lib = load()
+    ld = _need_rows(logits, "logits")
+    if logits.dim() != 3:
+        raise ValueError("logits must be [B, R, V]")
+    dev = logits.device
+    B, R, V = logits.shape
+    Lmax = 0
+    if history is not None:
+        _need(history, "history", dev, torch.int32)
+        if history.dim() != 2 or history.shape[0] != B:
+            raise ValueError(f"history must be [{B}, Lmax], got {tuple(history.shape)}")
+        Lmax = history.shape[1]
+    for t, name in ((lengths, "lengths"), (prompt_lengths, "prompt_lengths")):
+        if t is not None:
+            _need(t, name, dev, torch.int32, (B,))
+    if block is not None:
+        _need(block, "block", dev, torch.int32, (B, R - 1))
+    for t, name in ((repetition, "repetition"), (frequency, "frequency"), (presence, "presence"),
+                    (temperature, "temperature")):
+        if t is not None:
+            _need(t, name, dev, torch.float32, (B,))
+    nb = 0
+    if (bias_ids is None) != (bias_values is None):
+        raise ValueError("bias_ids and bias_values go together")
+    if bias_ids is not None:
+        _need(bias_ids, "bias_ids", dev, torch.int32)
+        if bias_ids.dim() != 2 or bias_ids.shape[0] != B:
+            raise ValueError(f"bias_ids must be [{B}, n], got {tuple(bias_ids.shape)}")
+        nb = bias_ids.shape[1]
+        _need(bias_values, "bias_values", dev, torch.float32, (B, nb))
+    mask_rows = 1
+    if mask is not None:
+        W = (V + 31) // 32
+        if mask.dim() == 3:
+            mask_rows = R
+        _need(mask, "mask", dev, torch.int32, (B, R, W) if mask.dim() == 3 else (B, W))
+    if out is None:
+        with _made_on(stream):
+            out = dict(logits=_rows_like(logits, ld))
+    _need_same_rows(out["logits"], "out", logits, ld)
+    if ws is None:
+        with _made_on(stream):
+            ws = workspace(OP_PROCESS_LOGITS, B, R, V, 0, dev, stream)
+    code = lib.spec_process_logits(
+        _ptr(logits), _dtype_code(logits), B, R, V, ld, _ptr(history if Lmax else None), Lmax, _ptr(lengths),
+        _ptr(prompt_lengths), _ptr(block if R > 1 else None), _ptr(repetition), _ptr(frequency), _ptr(presence),
+        _ptr(temperature), _ptr(bias_ids if nb else None), _ptr(bias_values if nb else None), nb, _ptr(mask),
+        mask_rows, _ptr(out["logits"]), _ptr(ws), ws.numel(), _stream(stream))
+    _check(code, "spec_process_logits")
+    out["ws"] = ws
+    return out
+
+
+def top_logits(logits, k, temperature=1.0, ws=None, out=None, stream=None):
+    """spec_top_logits.  logits [..., V] f32/bf16 (rows may lie further apart than V).
+    Returns a dict of device tensors: values float32 and ids int32 [..., k], tail and lse
+    float32 [...]."""
+    torch = _torch()
+    lib = load()
+    ld = _need_rows(logits, "logits")
+    dev = logits.device
+    lead, V, k = tuple(logits.shape[:-1]), logits.shape[-1], int(k)
+    rows = logits.numel() // V if V else 0
+    if out is None:
+        with _made_on(stream):
+            out = dict(values=torch.empty((*lead, max(k, 0)), dtype=torch.float32, device=dev),
+                       ids=torch.empty((*lead, max(k, 0)), dtype=torch.int32, device=dev),
+                       tail=torch.empty(lead, dtype=torch.float32, device=dev),
+                       lse=torch.empty(lead, dtype=torch.float32, device=dev))
+    if ws is None:
+        with _made_on(stream):
+            ws = workspace(OP_TOP_LOGITS, rows, k, V, 0, dev, stream)
+    code = lib.spec_top_logits(_ptr(logits), _dtype_code(logits), rows, V, ld, k, float(temperature),
+                               _ptr(out["values"]), _ptr(out["ids"]), _ptr(out["tail"]), _ptr(out.get("lse")),
+                               _ptr(ws), ws.numel(), _stream(stream))
+    _check(code, "spec_top_logits")
+    out["ws"] = ws
+    return out
+
+
+def distill(student, values, ids, tail=None, weight=None, temperature=1.0, grad=False, ws=None, out=None,
+            stream=None):
+    """spec_distill.  student [..., V] f32/bf16 (rows may lie further apart than V); values
+    f32/bf16 and ids int32 [..., K]; tail and weight float32 [...] or None.  Returns a dict
+    of device tensors: loss and lse float32 [...] and, with ``grad``, grad of the student's
+    type and layout (``out["grad"]`` may be student itself)."""
+    torch = _torch()
+    lib = load()
+    ld = _need_rows(student, "student")
+    dev = student.device
+    lead, V = tuple(student.shape[:-1]), student.shape[-1]
+    rows = student.numel() // V if V else 0
+    _need(ids, "ids", dev, torch.int32)
+    K = ids.shape[-1] if ids.dim() else 0
+    _need(ids, "ids", dev, torch.int32, (*lead, K))
+    _need(values, "values", dev, None, (*lead, K))
+    for t, name in ((tail, "tail"), (weight, "weight")):
+        if t is not None:
+            _need(t, name, dev, torch.float32, lead)
+    if out is None:
+        with _made_on(stream):
+            out = dict(loss=torch.empty(lead, dtype=torch.float32, device=dev),
+                       lse=torch.empty(lead, dtype=torch.float32, device=dev))
+            if grad:
+                out["grad"] = _rows_like(student, ld)
+    if grad:
+        _need_same_rows(out["grad"], "grad", student, ld)
+    if ws is None:
+        with _made_on(stream):
+            ws = workspace(OP_DISTILL, rows, K, V, 0, dev, stream)
+    code = lib.spec_distill(_ptr(student), _dtype_code(student), rows, V, ld, _ptr(values), _dtype_code(values),
+                            _ptr(ids), K, _ptr(tail), _ptr(weight), float(temperature), _ptr(out["loss"]),
+                            _ptr(out.get("lse")), _ptr(out["grad"] if grad else None), _ptr(ws), ws.numel(),
+                            _stream(stream))
+    _check(code, "spec_distill")
     out["ws"] = ws
     return out

@@ -52,6 +52,16 @@ size_t spec_workspace_bytes(spec_op op, int B, int gamma, int V, int r) {
         if (B < 1 || B > 65535 || gamma < 0 || gamma > SPEC_MAX_TREE_NODES || V < 1 || V > SPEC_MAX_V) return 0;
         return tree_verify_workspace_bytes(B, gamma);
     }
+    if (op == SPEC_OP_PROCESS_LOGITS) {   // gamma is the number of rows per request
+        if (B < 1 || B > 65535 || gamma < 1 || gamma > SPEC_MAX_GAMMA + 1 || V < 1 || V > SPEC_MAX_V) return 0;
+        return kWsHeaderBytes;
+    }
+    if (op == SPEC_OP_TOP_LOGITS || op == SPEC_OP_DISTILL) {   // B rows, gamma entries per row
+        if (B < 1 || B > SPEC_MAX_TEACHER_ROWS || gamma < 1 || gamma > SPEC_MAX_TEACHER || V < 1 ||
+            V > SPEC_MAX_V_TEACHER)
+            return 0;
+        return op == SPEC_OP_TOP_LOGITS ? top_logits_workspace_bytes(B, V) : distill_workspace_bytes(B, gamma, V);
+    }
     if (B < 1 || gamma < 1 || gamma > SPEC_MAX_GAMMA || V < 1 || V > SPEC_MAX_V) return 0;
     switch (op) {
         case SPEC_OP_DRAFT:
@@ -492,6 +502,111 @@ spec_status spec_verify_topk(const void* target_logits, spec_dtype target_dtype,
     p.bonus_out = bonus_out;
     p.near_out = near_tie_out;
     return cuda_status(verify_topk_launch(p, workspace, (cudaStream_t)stream));
+}
+
+spec_status spec_process_logits(const void* logits, spec_dtype dtype, int B, int R, int V, int ld,
+                                const int32_t* history, int Lmax, const int32_t* lengths,
+                                const int32_t* prompt_lengths, const int32_t* block, const float* repetition,
+                                const float* frequency, const float* presence, const float* temperature,
+                                const int32_t* bias_ids, const float* bias_values, int n_bias, const uint32_t* mask,
+                                int mask_rows, void* out, void* workspace, size_t workspace_bytes,
+                                spec_stream_t stream) {
+    if (!dtype_ok(dtype)) return SPEC_ERR_DTYPE;
+    if (B < 1 || B > 65535 || R < 1 || R > SPEC_MAX_GAMMA + 1 || V < 1 || V > SPEC_MAX_V || ld < V || Lmax < 0 ||
+        Lmax > SPEC_MAX_HISTORY || n_bias < 0 || n_bias > SPEC_MAX_BIASES)
+        return SPEC_ERR_SHAPE;
+    if (mask && mask_rows != 1 && mask_rows != R) return SPEC_ERR_SHAPE;
+    if (!logits || !out || (Lmax > 0 && !history) || (n_bias > 0 && (!bias_ids || !bias_values)))
+        return SPEC_ERR_INVALID_ARG;
+    if (!aligned16(logits) || !aligned16(out)) return SPEC_ERR_ALIGN;
+    if (!workspace || workspace_bytes < kWsHeaderBytes) return SPEC_ERR_WORKSPACE;
+    ProcessParams p;
+    memset(&p, 0, sizeof(p));
+    p.logits = logits;
+    p.out = out;
+    p.dtype = dtype;
+    p.B = B;
+    p.R = R;
+    p.V = V;
+    p.ld = ld;
+    p.history = history;
+    p.Lmax = Lmax;
+    p.lengths = lengths;
+    p.prompt_lengths = prompt_lengths;
+    p.block = R > 1 ? block : nullptr;
+    p.repetition = repetition;
+    p.frequency = frequency;
+    p.presence = presence;
+    p.temperature = temperature;
+    p.bias_ids = bias_ids;
+    p.bias_values = bias_values;
+    p.nb = n_bias;
+    p.mask = mask;
+    p.mask_rows = mask_rows;
+    p.mask_words = (V + 31) / 32;
+    p.status = &reinterpret_cast<WsHeader*>(workspace)->status;
+    return cuda_status(process_launch(p, (cudaStream_t)stream));
+}
+
+spec_status spec_top_logits(const void* logits, spec_dtype dtype, int rows, int V, int ld, int K, float temperature,
+                            float* values_out, int32_t* ids_out, float* tail_out, float* lse_out, void* workspace,
+                            size_t workspace_bytes, spec_stream_t stream) {
+    if (!dtype_ok(dtype)) return SPEC_ERR_DTYPE;
+    if (rows < 1 || rows > SPEC_MAX_TEACHER_ROWS || K < 1 || K > SPEC_MAX_TEACHER || V < 1 ||
+        V > SPEC_MAX_V_TEACHER || ld < V)
+        return SPEC_ERR_SHAPE;
+    if (!(temperature > 0.0f && temperature < INFINITY)) return SPEC_ERR_INVALID_ARG;
+    if (!logits || !values_out || !ids_out || !tail_out) return SPEC_ERR_INVALID_ARG;
+    if (!aligned16(logits)) return SPEC_ERR_ALIGN;
+    if (!workspace || workspace_bytes < top_logits_workspace_bytes(rows, V)) return SPEC_ERR_WORKSPACE;
+    TopLogitsParams p;
+    memset(&p, 0, sizeof(p));
+    p.logits = logits;
+    p.dtype = dtype;
+    p.rows = rows;
+    p.V = V;
+    p.ld = ld;
+    p.K = K;
+    p.scale = (float)(1.4426950408889634074 / (double)temperature);
+    p.inv_t = (float)(1.0 / (double)temperature);
+    p.values_out = values_out;
+    p.ids_out = ids_out;
+    p.tail_out = tail_out;
+    p.lse_out = lse_out;
+    return cuda_status(top_logits_launch(p, workspace, (cudaStream_t)stream));
+}
+
+spec_status spec_distill(const void* student, spec_dtype dtype, int rows, int V, int ld, const void* values,
+                         spec_dtype values_dtype, const int32_t* ids, int K, const float* tail, const float* weight,
+                         float temperature, float* loss_out, float* lse_out, void* grad_out, void* workspace,
+                         size_t workspace_bytes, spec_stream_t stream) {
+    if (!dtype_ok(dtype) || !dtype_ok(values_dtype)) return SPEC_ERR_DTYPE;
+    if (rows < 1 || rows > SPEC_MAX_TEACHER_ROWS || K < 1 || K > SPEC_MAX_TEACHER || V < 1 ||
+        V > SPEC_MAX_V_TEACHER || ld < V)
+        return SPEC_ERR_SHAPE;
+    if (!(temperature > 0.0f && temperature < INFINITY)) return SPEC_ERR_INVALID_ARG;
+    if (!student || !values || !ids || !loss_out) return SPEC_ERR_INVALID_ARG;
+    if (!aligned16(student) || !aligned16(grad_out)) return SPEC_ERR_ALIGN;
+    if (!workspace || workspace_bytes < distill_workspace_bytes(rows, K, V)) return SPEC_ERR_WORKSPACE;
+    DistillParams p;
+    memset(&p, 0, sizeof(p));
+    p.student = student;
+    p.dtype = dtype;
+    p.rows = rows;
+    p.V = V;
+    p.ld = ld;
+    p.K = K;
+    p.values = values;
+    p.values_dtype = values_dtype;
+    p.ids = ids;
+    p.tail = tail;
+    p.weight = weight;
+    p.scale = (float)(1.4426950408889634074 / (double)temperature);
+    p.inv_t = (float)(1.0 / (double)temperature);
+    p.loss_out = loss_out;
+    p.lse_out = lse_out;
+    p.grad_out = grad_out;
+    return cuda_status(distill_launch(p, workspace, (cudaStream_t)stream));
 }
 
 }  // extern "C"

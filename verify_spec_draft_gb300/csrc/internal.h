@@ -213,6 +213,75 @@ struct TreeVerifyParams {
 size_t tree_verify_workspace_bytes(int n_trees, int n_nodes);
 cudaError_t tree_verify_launch(TreeVerifyParams& p, void* ws, cudaStream_t stream);
 
+// spec_process_logits
+struct ProcessParams {
+    const void* logits;        // rows of `ld` entries apart, V used
+    void* out;                 // the same layout (may be logits itself)
+    int dtype;
+    int B, R, V, ld;
+    const int32_t* history;    // [B, Lmax]
+    int Lmax;
+    const int32_t* lengths;    // [B] (nullable: Lmax)
+    const int32_t* prompt_lengths;   // [B] (nullable: 0)
+    const int32_t* block;      // [B, R - 1] (nullable)
+    const float* repetition;   // [B] each nullable
+    const float* frequency;
+    const float* presence;
+    const float* temperature;
+    const int32_t* bias_ids;   // [B, nb]
+    const float* bias_values;  // [B, nb]
+    int nb;
+    const uint32_t* mask;      // [B, mask_rows, mask_words] (nullable)
+    int mask_rows, mask_words;
+    unsigned* status;
+    // chosen at launch
+    int seg;                   // vocabulary entries per CTA (a multiple of its threads)
+    int n_seg, n_row_split;
+};
+cudaError_t process_launch(ProcessParams p, cudaStream_t stream);
+
+// spec_top_logits
+struct TopLogitsParams {
+    const void* logits;        // rows of `ld` entries apart, V used
+    int dtype;
+    int rows, V, ld, K;
+    float scale, inv_t;        // log2(e) / temperature, 1 / temperature
+    float* values_out;         // [rows, K]
+    int32_t* ids_out;          // [rows, K]
+    float* tail_out;           // [rows]
+    float* lse_out;            // [rows] (nullable)
+    unsigned* status;
+    // chosen at launch
+    int n_blocks, pieces;
+    float2* blocks;            // [rows, n_blocks] (maximum, sum)
+};
+size_t top_logits_workspace_bytes(int rows, int V);
+cudaError_t top_logits_launch(TopLogitsParams p, void* ws, cudaStream_t stream);
+
+// spec_distill
+struct DistillParams {
+    const void* student;       // rows of `ld` entries apart, V used
+    int dtype;
+    int rows, V, ld, K;
+    const void* values;        // [rows, K]
+    int values_dtype;
+    const int32_t* ids;        // [rows, K]
+    const float* tail;         // [rows] (nullable: no rest)
+    const float* weight;       // [rows] (nullable: 1)
+    float scale, inv_t;        // log2(e) / temperature, 1 / temperature
+    float* loss_out;           // [rows]
+    float* lse_out;            // [rows] (nullable)
+    void* grad_out;            // student's layout (nullable; may be student itself)
+    unsigned* status;
+    // chosen at launch
+    int pieces;
+    float2* parts;             // [rows, pieces] (maximum, sum) of the entries no id names
+    float4* stats;             // [rows] maximum, coefficient, row skipped
+    float* named_grad;         // [rows, K]
+};
+size_t distill_workspace_bytes(int rows, int K, int V);
+cudaError_t distill_launch(DistillParams p, void* ws, cudaStream_t stream);
+
 int device_sm_count();
 
 cudaError_t verify_budget_launch(const float* conf, int B, int gamma, int budget, const float* cost,
