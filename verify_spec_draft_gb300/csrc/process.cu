@@ -21,6 +21,7 @@
 namespace spec {
 
 constexpr int kProcThreads = 256;
+constexpr int kProcOcc = 4;   // CTAs per SM
 constexpr uint32_t kCountBits = 20, kCountMask = (1u << kCountBits) - 1u;
 constexpr uint32_t kSlotMask = 0x7ffu, kInPrompt = 0x80000000u;
 
@@ -29,130 +30,293 @@ __device__ __forceinline__ uint32_t bits_at(const uint32_t* w, int e) {
     return __funnelshift_r(w[e >> 5], w[(e >> 5) + 1], e & 31);
 }
 
+// The kernel's shared memory: a word per entry of the segment, a bit per entry (and a word
+// more, which bits_at reads), the block's tokens.
+__host__ __device__ inline size_t process_smem(int seg) {
+    return ((size_t)seg + seg / 32 + 1 + SPEC_MAX_GAMMA) * sizeof(uint32_t);
+}
+
+constexpr int kProcBatch = 4;   // words a thread holds while it waits for the ones behind
+
+// The words of a segment of a row.  ALIGNED: the segment starts on 16 bytes and is a whole
+// number of words, as every segment does when rows are whole words apart and V is whole words.
+template <typename T, bool ALIGNED>
+struct SegWords {
+    static constexpr int E = 16 / (int)sizeof(T);
+    RowWords<T> r;
+    __device__ __forceinline__ SegWords(const T* row, int len) : r(row, len) {}
+    __device__ __forceinline__ int n() const { return ALIGNED ? r.V / E : r.n; }
+    __device__ __forceinline__ int entry(int i) const { return ALIGNED ? i * E : r.entry(i); }
+    __device__ __forceinline__ uint4 load(int i) const {
+        if (!ALIGNED) return r.load(i);
+        uint4 v;
+        asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                     : "l"(reinterpret_cast<const uint4*>(r.p) + i) : "memory");
+        return v;
+    }
+    __device__ __forceinline__ void store(T* q, int i, const uint4& w) const {
+        if (!ALIGNED) return r.store(q, i, w);
+        asm volatile("st.global.L1::no_allocate.v4.u32 [%0], {%1,%2,%3,%4};"
+                     :: "l"(reinterpret_cast<uint4*>(q) + i), "r"(w.x), "r"(w.y), "r"(w.z), "r"(w.w) : "memory");
+    }
+    // the mask bits of word i, bit k for entry k; `left` words of mask from the segment's first
+    __device__ __forceinline__ uint32_t allowed(const uint32_t* mask, int left, int i) const {
+        if (ALIGNED) {
+            const uint8_t* m = reinterpret_cast<const uint8_t*>(mask);
+            return E == 8 ? (uint32_t)__ldg(m + i) : ((uint32_t)__ldg(m + (i >> 1)) >> (4 * (i & 1))) & 15u;
+        }
+        const int e = entry(i), e0 = max(e, 0), at = e0 & 31;
+        const uint32_t lo = __ldg(mask + (e0 >> 5));
+        const uint32_t hi = at + E > 32 && (e0 >> 5) + 1 < left ? __ldg(mask + (e0 >> 5) + 1) : 0u;
+        return (__funnelshift_r(lo, hi, at) << (e0 - e)) & ((1u << E) - 1u);
+    }
+    // the bits of word i that are set in the segment's bit string
+    __device__ __forceinline__ uint32_t touched(const uint32_t* bits, int i) const {
+        if (ALIGNED) {
+            const uint8_t* m = reinterpret_cast<const uint8_t*>(bits);
+            return E == 8 ? (uint32_t)m[i] : ((uint32_t)m[i >> 1] >> (4 * (i & 1))) & 15u;
+        }
+        const int e = entry(i), e0 = max(e, 0);
+        const int behind = min(E, r.V - e);   // entries of the word up to the row's end
+        return (bits_at(bits, e0) << (e0 - e)) & ((1u << behind) - 1u);
+    }
+};
+
+// One batch of a row: the words kProcThreads apart from word i0 + tid, and their mask bits,
+// a byte per word.
+template <typename T, bool ALIGNED>
+struct ProcBatch {
+    uint4 w[kProcBatch];
+    uint32_t allowed;
+    __device__ __forceinline__ void load(const SegWords<T, ALIGNED>& in, const uint32_t* mask, int mask_left, int i0) {
+        allowed = 0xffffffffu;
+#pragma unroll
+        for (int q = 0; q < kProcBatch; ++q) {
+            const int i = i0 + q * kProcThreads + (int)threadIdx.x;
+            if (i < in.n()) w[q] = in.load(i);
+        }
+        if (mask) {
+            allowed = 0u;
+#pragma unroll
+            for (int q = 0; q < kProcBatch; ++q) {
+                const int i = i0 + q * kProcThreads + (int)threadIdx.x;
+                if (i < in.n()) allowed |= in.allowed(mask, mask_left, i) << (8 * q);
+            }
+        }
+    }
+};
+
+// A word's entries times f, rounded to T.
 template <typename T>
-__global__ void __launch_bounds__(kProcThreads) process_kernel(ProcessParams p) {
-    constexpr int E = 16 / (int)sizeof(T);
+__device__ __forceinline__ uint4 word_scaled(const uint4& w, float f) {
+    const uint32_t h[4] = {w.x, w.y, w.z, w.w};
+    uint32_t o[4];
+    const f2x ff = f2_pack(f, f);
+    if constexpr (sizeof(T) == 2) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const float2 y = f2_unpack(f2_mul(bf2_widen(h[r]), ff));
+            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(o[r]) : "f"(y.y), "f"(y.x));
+        }
+    } else {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) o[r] = __float_as_uint(__uint_as_float(h[r]) * f);
+    }
+    return make_uint4(o[0], o[1], o[2], o[3]);
+}
+// -inf where the word's bit is clear.
+template <typename T>
+__device__ __forceinline__ uint4 word_masked(const uint4& w, uint32_t allowed) {
+    uint32_t h[4] = {w.x, w.y, w.z, w.w};
+    if constexpr (sizeof(T) == 2) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            // bits 2r and 2r + 1 to bits 15 and 31, then each over its half word
+            const uint32_t v = (allowed & 0xffu) * ((1u << (15 - 2 * r)) | (1u << (30 - 2 * r)));
+            uint32_t m;   // bytes 1 and 3 by their top bits (prmt's sign replication), twice each
+            asm("prmt.b32 %0, %1, 0, 0xbb99;" : "=r"(m) : "r"(v));
+            h[r] = (h[r] & m) | (NegInf<T>::word & ~m);
+        }
+    } else {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) h[r] = (allowed >> r) & 1u ? h[r] : NegInf<T>::word;
+    }
+    return make_uint4(h[0], h[1], h[2], h[3]);
+}
+
+template <typename T, bool ALIGNED>
+__global__ void __launch_bounds__(kProcThreads, kProcOcc) process_kernel(ProcessParams p) {
     extern __shared__ __align__(16) uint32_t s_proc[];
-    uint32_t* s_state = s_proc;              // [seg]
-    uint32_t* s_bits = s_proc + p.seg;       // [seg / 32 + 1]
-    const int b = blockIdx.x / (p.n_seg * p.n_row_split);
-    const int rem = blockIdx.x - b * (p.n_seg * p.n_row_split);
-    const int rs = rem / p.n_seg, sg = rem - rs * p.n_seg;
+    uint32_t* s_state = s_proc;                                            // [seg]
+    uint32_t* s_bits = s_proc + p.seg;                                     // [seg / 32 + 1]
+    int32_t* s_blk = reinterpret_cast<int32_t*>(s_bits + p.seg / 32 + 1);  // [R - 1]
+    // segment by segment: the first ones, where frequent tokens tend to be, start first
+    const int per_seg = p.B * p.n_row_split;
+    const int sg = blockIdx.x / per_seg, rem = blockIdx.x - sg * per_seg;
+    const int b = rem / p.n_row_split, rs = rem - b * p.n_row_split;
     const int c0 = sg * p.seg;
     const int len = min(p.seg, p.V - c0);
     const int j0 = (int)((long)p.R * rs / p.n_row_split), j1 = (int)((long)p.R * (rs + 1) / p.n_row_split);
     const int tid = threadIdx.x;
     const bool report = sg == 0 && rs == 0;   // one CTA per request raises its flags
 
+    const int mask_left = p.mask_words - (c0 >> 5);   // words from the segment's first
+    auto row_at = [&](int j) {
+        return SegWords<T, ALIGNED>(reinterpret_cast<const T*>(p.logits) + ((long)b * p.R + j) * p.ld + c0, len);
+    };
+    auto mask_at = [&](int j) -> const uint32_t* {
+        if (!p.mask) return nullptr;
+        return p.mask + (p.mask_rows == 1 ? (long)b : (long)b * p.R + j) * p.mask_words + (c0 >> 5);
+    };
+    // the first batch is on its way while the history is scanned
+    ProcBatch<T, ALIGNED> cur, nxt;
+    cur.load(row_at(j0), mask_at(j0), mask_left, 0);
+
     const float rep = p.repetition ? p.repetition[b] : 1.0f;
     const float freq = p.frequency ? p.frequency[b] : 0.0f;
     const float pres = p.presence ? p.presence[b] : 0.0f;
     const float temp = p.temperature ? p.temperature[b] : 1.0f;
-    const bool valid = rep > 0.0f && rep < INFINITY && temp > 0.0f && temp < INFINITY && fabsf(freq) < INFINITY &&
-                       fabsf(pres) < INFINITY;
     int n = p.lengths ? p.lengths[b] : p.Lmax, m = p.prompt_lengths ? p.prompt_lengths[b] : 0;
     bool bad_token = n < 0 || n > p.Lmax || m < 0 || m > n;
     n = max(0, min(n, p.Lmax));
     m = max(0, min(m, n));
-    const float rinv = 1.0f / rep, tinv = 1.0f / temp;
 
-    for (int i = tid; i < p.seg; i += kProcThreads) s_state[i] = 0u;
+    for (int i = tid; i < (p.seg + p.seg / 32) / 4; i += kProcThreads)   // state and bits, 16 bytes at a time
+        reinterpret_cast<uint4*>(s_state)[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (tid == 0) s_bits[p.seg / 32] = 0u;
+    if (p.block && tid < p.R - 1) s_blk[tid] = p.block[(long)b * (p.R - 1) + tid];
     __syncthreads();
+    auto mark = [&](int at) { atomicOr(&s_bits[at >> 5], 1u << (at & 31)); };
     if (p.nb > 0) {
         for (int i = tid; i < p.nb; i += kProcThreads) {
             const int id = p.bias_ids[(long)b * p.nb + i];
-            if ((unsigned)(id - c0) < (unsigned)len) atomicMax(&s_state[id - c0], (uint32_t)(i + 1) << kCountBits);
+            if ((unsigned)(id - c0) < (unsigned)len) {
+                atomicMax(&s_state[id - c0], (uint32_t)(i + 1) << kCountBits);
+                mark(id - c0);
+            }
             bad_token |= id < -1 || id >= p.V;
         }
         __syncthreads();
     }
-    const int32_t* hist = p.history + (long)b * p.Lmax;
-    for (int i = tid; i < n; i += kProcThreads) {
-        const int t = hist[i];
+    auto count = [&](int t, int i) {
         if ((unsigned)(t - c0) < (unsigned)len) {
             if (i < m) atomicOr(&s_state[t - c0], kInPrompt);
             else atomicAdd(&s_state[t - c0], 1u);
+            mark(t - c0);
         }
         bad_token |= (unsigned)t >= (unsigned)p.V;
+    };
+    const int32_t* hist = p.history + (long)b * p.Lmax;
+    const int n4 = p.hist_vec ? n / 4 : 0;   // whole 16-byte words of tokens
+#pragma unroll 4
+    for (int i = tid; i < n4; i += kProcThreads) {
+        const int4 t = __ldg(reinterpret_cast<const int4*>(hist) + i);
+        count(t.x, 4 * i);
+        count(t.y, 4 * i + 1);
+        count(t.z, 4 * i + 2);
+        count(t.w, 4 * i + 3);
     }
-    const int32_t* blk = p.block + (long)b * (p.R - 1);
-    for (int i = tid; i < p.R - 1 && p.block; i += kProcThreads) {
-        const int t = blk[i];
-        if (i < j0 && (unsigned)(t - c0) < (unsigned)len) atomicAdd(&s_state[t - c0], 1u);
-        bad_token |= (unsigned)t >= (unsigned)p.V;
+    for (int i = 4 * n4 + tid; i < n; i += kProcThreads) count(__ldg(hist + i), i);
+    if (p.block && tid < p.R - 1) {
+        if (tid < j0) count(s_blk[tid], p.Lmax);   // drafted before this CTA's first row
+        else bad_token |= (unsigned)s_blk[tid] >= (unsigned)p.V;
     }
+    const bool valid = rep > 0.0f && rep < INFINITY && temp > 0.0f && temp < INFINITY && fabsf(freq) < INFINITY &&
+                       fabsf(pres) < INFINITY;
     if (report && bad_token) atomicOr(p.status, SPEC_DEV_TOKEN);
     if (report && !valid && tid == 0) atomicOr(p.status, SPEC_DEV_NONFINITE);
-    __syncthreads();
-    for (int i = tid; i < p.seg; i += kProcThreads) {   // seg is a multiple of kProcThreads
-        const unsigned w = __ballot_sync(0xffffffffu, s_state[i] != 0u);
-        if ((tid & 31) == 0) s_bits[i >> 5] = w;
-    }
-    if (tid == 0) s_bits[p.seg >> 5] = 0u;
+    const float rinv = 1.0f / rep, tinv = valid ? 1.0f / temp : NAN;
     __syncthreads();
 
     for (int j = j0; j < j1; ++j) {
         if (j > j0 && p.block) {
-            __syncthreads();   // row j - 1 has been read
-            const int t = blk[j - 1];
-            if (tid == 0 && (unsigned)(t - c0) < (unsigned)len) {
-                s_state[t - c0] += 1u;
-                s_bits[(t - c0) >> 5] |= 1u << ((t - c0) & 31);
-            }
-            __syncthreads();
-        }
-        const long row = (long)b * p.R + j;
-        const RowWords<T> in(reinterpret_cast<const T*>(p.logits) + row * p.ld + c0, len);
-        T* out = reinterpret_cast<T*>(p.out) + row * p.ld + c0;
-        const uint32_t* mask =
-            p.mask ? p.mask + ((p.mask_rows == 1 ? (long)b : row) * p.mask_words) + (c0 >> 5) : nullptr;
-        const int mask_left = p.mask_words - (c0 >> 5);   // words from the segment's first
-        for (int i = tid; i < in.n; i += kProcThreads) {
-            const int e = in.entry(i);
-            uint4 w = in.load(i);
-            const int e0 = max(e, 0);
-            // bit k of `touched` and `allowed` is entry e0 + k
-            uint32_t touched = bits_at(s_bits, e0);
-            uint32_t allowed = 0xffffffffu;
-            if (mask) {
-                const int mw = e0 >> 5;
-                const uint32_t lo = __ldg(mask + mw);
-                const uint32_t hi = mw + 1 < mask_left ? __ldg(mask + mw + 1) : 0u;
-                allowed = __funnelshift_r(lo, hi, e0 & 31);
-            }
-            touched <<= e0 - e;
-            allowed <<= e0 - e;
-            float y[E];
-#pragma unroll
-            for (int k = 0; k < E; ++k) {
-                float x = word_entry<T>(w, k);
-                if ((touched >> k) & 1u && e + k >= 0 && e + k < len) {
-                    const uint32_t st = s_state[e + k];
-                    const uint32_t c = st & kCountMask, slot = (st >> kCountBits) & kSlotMask;
-                    if (st & (kInPrompt | kCountMask)) x = x > 0.0f ? x * rinv : x * rep;
-                    x -= fmaf(freq, (float)c, c ? pres : 0.0f);
-                    if (slot) x += p.bias_values[(long)b * p.nb + slot - 1];
+            const int at = s_blk[j - 1] - c0;
+            if ((unsigned)at < (unsigned)len) {   // the same for every thread
+                __syncthreads();                  // row j - 1 has been read
+                if (tid == 0) {
+                    s_state[at] += 1u;
+                    s_bits[at >> 5] |= 1u << (at & 31);
                 }
-                x *= tinv;
-                if (!valid) x = NAN;
-                y[k] = (allowed >> k) & 1u ? x : -INFINITY;
+                __syncthreads();
             }
-            w = word_of<T>(y);
-            in.store(out, i, w);
+        }
+        const SegWords<T, ALIGNED> in = row_at(j);
+        T* out = reinterpret_cast<T*>(p.out) + ((long)b * p.R + j) * p.ld + c0;
+        for (int i0 = 0; i0 < in.n(); i0 += kProcThreads * kProcBatch) {
+            // the batch behind: of this row, or the next row's first
+            if (i0 + kProcThreads * kProcBatch < in.n()) nxt.load(in, mask_at(j), mask_left, i0 + kProcThreads * kProcBatch);
+            else if (j + 1 < j1) nxt.load(row_at(j + 1), mask_at(j + 1), mask_left, 0);
+#pragma unroll
+            for (int q = 0; q < kProcBatch; ++q) {
+                const int i = i0 + q * kProcThreads + tid;
+                if (i >= in.n()) break;
+                const uint32_t allowed = cur.allowed >> (8 * q);
+                uint4 o = tinv == 1.0f ? cur.w[q] : word_scaled<T>(cur.w[q], tinv);
+                // entries that have something on them, one by one
+                uint32_t touched = in.touched(s_bits, i);
+                while (touched) {
+                    const int k = __ffs(touched) - 1;
+                    touched &= touched - 1u;
+                    const uint32_t st = s_state[in.entry(i) + k];
+                    const uint32_t c = st & kCountMask;
+                    float x = word_pick<T>(cur.w[q], k);
+                    if (st & (kInPrompt | kCountMask)) x *= x > 0.0f ? rinv : rep;
+                    x -= fmaf(freq, (float)c, c ? pres : 0.0f);
+                    const uint32_t slot = (st >> kCountBits) & kSlotMask;
+                    if (slot) x += __ldg(p.bias_values + (long)b * p.nb + slot - 1);
+                    word_put<T>(o, k, x * tinv);
+                }
+                if (p.mask) o = word_masked<T>(o, allowed);
+                in.store(out, i, o);
+            }
+            cur = nxt;
         }
     }
 }
 
+// Work split.  A CTA takes a segment of the vocabulary for a range of rows; its time is its
+// words, and what it costs to scan the history once.  All CTAs are equal, so the time is
+// (waves of resident CTAs) x (words of one): the split with the least of it is taken, among
+// equals the one with the fewest CTAs (each scans the history).
 cudaError_t process_launch(ProcessParams p, cudaStream_t stream) {
-    p.seg = 8192;
-    p.n_seg = (p.V + p.seg - 1) / p.seg;
-    p.n_row_split = 1;
-    const size_t smem = ((size_t)p.seg + p.seg / 32 + 1) * sizeof(uint32_t);
+    const int E = p.dtype == SPEC_BF16 ? 8 : 4;
+    constexpr int kMaxSeg = 13824;   // 56 KB of state and bits: four CTAs of an SM
+    const long slots = (long)device_sm_count() * kProcOcc;
+    const long scan = 64 + (p.Lmax + p.nb) / 8;   // the scan, in words that stream in the same time
+    const int least = (p.V + kMaxSeg - 1) / kMaxSeg;
+    const int most = (p.V + 128 * E - 1) / (128 * E) > least ? (p.V + 128 * E - 1) / (128 * E) : least;
+    long best = -1;
+    for (int split = 1; split <= p.R; ++split) {
+        for (int waves = 1; waves <= 4; ++waves) {
+            long n = slots * waves / ((long)p.B * split);
+            n = n < least ? least : (n > most ? most : n);
+            const int seg = (int)((p.V + n - 1) / n + 127) / 128 * 128;
+            n = (p.V + seg - 1) / seg;
+            const long ctas = n * split * p.B;
+            const long cost = (ctas + slots - 1) / slots * ((long)((p.R + split - 1) / split) * (seg / E) + scan);
+            if (best < 0 || cost < best) {
+                best = cost;
+                p.seg = seg;
+                p.n_seg = (int)n;
+                p.n_row_split = split;
+            }
+        }
+    }
+    p.hist_vec = p.Lmax % 4 == 0 && (reinterpret_cast<uintptr_t>(p.history) & 15u) == 0;
+    const size_t smem = process_smem(p.seg);
     const long grid = (long)p.B * p.n_seg * p.n_row_split;
     if (grid > 0x7fffffffL) return cudaErrorInvalidConfiguration;
-    if (p.dtype == SPEC_BF16) process_kernel<bf16_t><<<(unsigned)grid, kProcThreads, smem, stream>>>(p);
-    else process_kernel<float><<<(unsigned)grid, kProcThreads, smem, stream>>>(p);
-    return cudaGetLastError();
+    const bool aligned = p.ld % E == 0 && p.V % E == 0;
+    const void* kern = p.dtype == SPEC_BF16
+                           ? (aligned ? (const void*)process_kernel<bf16_t, true> : (const void*)process_kernel<bf16_t, false>)
+                           : (aligned ? (const void*)process_kernel<float, true> : (const void*)process_kernel<float, false>);
+    if (smem > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+    }
+    void* args[] = {&p};
+    return cudaLaunchKernel(kern, dim3((unsigned)grid), dim3(kProcThreads), args, smem, stream);
 }
 
 }  // namespace spec
