@@ -8,13 +8,15 @@
 //     y += bias(v);  y /= T;  y = -inf where the row's mask bit is 0.
 //
 // A CTA owns a segment of the vocabulary for some rows of one request.  It scans the
-// request's history once and keeps one 32-bit word per entry of the segment in shared
-// memory:
-//     bit 31 in the prompt | bits 20..30 bias slot + 1 | bits 0..19 count
-// and one bit per entry that says whether the word is non-zero.  Rows are then streamed:
-// a 16-byte word of logits whose bits are all clear (nearly all of them) only takes the
-// temperature and the mask.  Between rows the next block token is added to the counts,
-// so a history is scanned once per segment and not once per row.
+// request's history once, counting in shared memory with one 32-bit word per entry of the
+// segment,
+//     bit 31 in the prompt | bits 20..30 bias slot + 1 | bits 0..19 count,
+// and then replaces each word by what the entry gets added, A = (bias - penalty) / T, with
+// one bit per entry for "has something on it" and one for "seen".  Rows are then streamed:
+// a 16-byte word of logits whose first bits are all clear (nearly all of them) only takes
+// the temperature and the mask, the others one FFMA per entry, l * (1/T, rho/T or 1/(rho T))
+// + A.  Between rows the next block token's entry is renewed, so a history is scanned once
+// per segment and not once per row.
 #include "internal.h"
 #include "row_words.cuh"
 
@@ -30,10 +32,11 @@ __device__ __forceinline__ uint32_t bits_at(const uint32_t* w, int e) {
     return __funnelshift_r(w[e >> 5], w[(e >> 5) + 1], e & 31);
 }
 
-// The kernel's shared memory: a word per entry of the segment, a bit per entry (and a word
-// more, which bits_at reads), the block's tokens.
+// The kernel's shared memory: a word per entry of the segment, two strings of a bit per entry
+// (and a word more, which bits_at reads), and for the block's tokens the token, its count
+// and its bias.
 __host__ __device__ inline size_t process_smem(int seg) {
-    return ((size_t)seg + seg / 32 + 1 + SPEC_MAX_GAMMA) * sizeof(uint32_t);
+    return ((size_t)seg + 2 * (seg / 32 + 4) + 3 * SPEC_MAX_GAMMA) * sizeof(uint32_t);
 }
 
 constexpr int kProcBatch = 4;   // words a thread holds while it waits for the ones behind
@@ -71,8 +74,24 @@ struct SegWords {
         const uint32_t hi = at + E > 32 && (e0 >> 5) + 1 < left ? __ldg(mask + (e0 >> 5) + 1) : 0u;
         return (__funnelshift_r(lo, hi, at) << (e0 - e)) & ((1u << E) - 1u);
     }
+    // the entries of word i in the segment's array
+    __device__ __forceinline__ void floats(const float* a, int i, float (&o)[E]) const {
+#pragma unroll
+        for (int k = 0; k < E; k += 4) {
+            if (ALIGNED) {
+                const float4 v = *reinterpret_cast<const float4*>(a + i * E + k);
+                o[k] = v.x; o[k + 1] = v.y; o[k + 2] = v.z; o[k + 3] = v.w;
+            } else {
+#pragma unroll
+                for (int h = k; h < k + 4; ++h) {
+                    const int e = entry(i) + h;
+                    o[h] = e >= 0 && e < r.V ? a[e] : 0.0f;
+                }
+            }
+        }
+    }
     // the bits of word i that are set in the segment's bit string
-    __device__ __forceinline__ uint32_t touched(const uint32_t* bits, int i) const {
+    __device__ __forceinline__ uint32_t bits(const uint32_t* bits, int i) const {
         if (ALIGNED) {
             const uint8_t* m = reinterpret_cast<const uint8_t*>(bits);
             return E == 8 ? (uint32_t)m[i] : ((uint32_t)m[i >> 1] >> (4 * (i & 1))) & 15u;
@@ -147,10 +166,15 @@ __device__ __forceinline__ uint4 word_masked(const uint4& w, uint32_t allowed) {
 
 template <typename T, bool ALIGNED>
 __global__ void __launch_bounds__(kProcThreads, kProcOcc) process_kernel(ProcessParams p) {
+    constexpr int E = 16 / (int)sizeof(T);
     extern __shared__ __align__(16) uint32_t s_proc[];
     uint32_t* s_state = s_proc;                                            // [seg]
-    uint32_t* s_bits = s_proc + p.seg;                                     // [seg / 32 + 1]
-    int32_t* s_blk = reinterpret_cast<int32_t*>(s_bits + p.seg / 32 + 1);  // [R - 1]
+    float* s_add = reinterpret_cast<float*>(s_proc);                       // the same words, later
+    uint32_t* s_bits = s_proc + p.seg;                                     // [seg / 32 + 1] has something
+    uint32_t* s_seen = s_bits + p.seg / 32 + 4;                            // [seg / 32 + 1]
+    int32_t* s_blk = reinterpret_cast<int32_t*>(s_seen + p.seg / 32 + 4);  // [R - 1] tokens
+    int32_t* s_cnt = s_blk + SPEC_MAX_GAMMA;                               // [R - 1] counts once drafted
+    float* s_bias = reinterpret_cast<float*>(s_cnt + SPEC_MAX_GAMMA);      // [R - 1]
     // segment by segment: the first ones, where frequent tokens tend to be, start first
     const int per_seg = p.B * p.n_row_split;
     const int sg = blockIdx.x / per_seg, rem = blockIdx.x - sg * per_seg;
@@ -182,9 +206,9 @@ __global__ void __launch_bounds__(kProcThreads, kProcOcc) process_kernel(Process
     n = max(0, min(n, p.Lmax));
     m = max(0, min(m, n));
 
-    for (int i = tid; i < (p.seg + p.seg / 32) / 4; i += kProcThreads)   // state and bits, 16 bytes at a time
+    // words and bits, 16 bytes at a time
+    for (int i = tid; i < (p.seg + 2 * (p.seg / 32 + 4)) / 4; i += kProcThreads)
         reinterpret_cast<uint4*>(s_state)[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (tid == 0) s_bits[p.seg / 32] = 0u;
     if (p.block && tid < p.R - 1) s_blk[tid] = p.block[(long)b * (p.R - 1) + tid];
     __syncthreads();
     auto mark = [&](int at) { atomicOr(&s_bits[at >> 5], 1u << (at & 31)); };
@@ -226,7 +250,27 @@ __global__ void __launch_bounds__(kProcThreads, kProcOcc) process_kernel(Process
                        fabsf(pres) < INFINITY;
     if (report && bad_token) atomicOr(p.status, SPEC_DEV_TOKEN);
     if (report && !valid && tid == 0) atomicOr(p.status, SPEC_DEV_NONFINITE);
-    const float rinv = 1.0f / rep, tinv = valid ? 1.0f / temp : NAN;
+    const float tinv = valid ? 1.0f / temp : NAN;
+    const float f_pos = tinv / rep, f_neg = tinv * rep;   // a seen entry's factor, by its sign
+    __syncthreads();
+    auto bias_of = [&](uint32_t st) {
+        const uint32_t slot = (st >> kCountBits) & kSlotMask;
+        return slot ? __ldg(p.bias_values + (long)b * p.nb + slot - 1) : 0.0f;
+    };
+    if (p.block && tid >= j0 && tid < j1 - 1 && (unsigned)(s_blk[tid] - c0) < (unsigned)len) {
+        const uint32_t st = s_state[s_blk[tid] - c0];
+        int c = (int)(st & kCountMask) + 1;
+        for (int i = j0; i < tid; ++i) c += s_blk[i] == s_blk[tid] ? 1 : 0;
+        s_cnt[tid] = c;
+        s_bias[tid] = bias_of(st);
+    }
+    __syncthreads();
+    for (int i = tid; i < p.seg; i += kProcThreads) {   // seg is whole warps: no partial ballot
+        const uint32_t st = s_state[i], c = st & kCountMask;
+        const unsigned seen = __ballot_sync(0xffffffffu, (st & (kInPrompt | kCountMask)) != 0u);
+        if (st) s_add[i] = (bias_of(st) - fmaf(freq, (float)c, c ? pres : 0.0f)) * tinv;
+        if ((tid & 31) == 0) s_seen[i >> 5] = seen;
+    }
     __syncthreads();
 
     for (int j = j0; j < j1; ++j) {
@@ -235,8 +279,9 @@ __global__ void __launch_bounds__(kProcThreads, kProcOcc) process_kernel(Process
             if ((unsigned)at < (unsigned)len) {   // the same for every thread
                 __syncthreads();                  // row j - 1 has been read
                 if (tid == 0) {
-                    s_state[at] += 1u;
+                    s_add[at] = (s_bias[j - 1] - fmaf(freq, (float)s_cnt[j - 1], pres)) * tinv;
                     s_bits[at >> 5] |= 1u << (at & 31);
+                    s_seen[at >> 5] |= 1u << (at & 31);
                 }
                 __syncthreads();
             }
@@ -252,20 +297,19 @@ __global__ void __launch_bounds__(kProcThreads, kProcOcc) process_kernel(Process
                 const int i = i0 + q * kProcThreads + tid;
                 if (i >= in.n()) break;
                 const uint32_t allowed = cur.allowed >> (8 * q);
-                uint4 o = tinv == 1.0f ? cur.w[q] : word_scaled<T>(cur.w[q], tinv);
-                // entries that have something on them, one by one
-                uint32_t touched = in.touched(s_bits, i);
-                while (touched) {
-                    const int k = __ffs(touched) - 1;
-                    touched &= touched - 1u;
-                    const uint32_t st = s_state[in.entry(i) + k];
-                    const uint32_t c = st & kCountMask;
-                    float x = word_pick<T>(cur.w[q], k);
-                    if (st & (kInPrompt | kCountMask)) x *= x > 0.0f ? rinv : rep;
-                    x -= fmaf(freq, (float)c, c ? pres : 0.0f);
-                    const uint32_t slot = (st >> kCountBits) & kSlotMask;
-                    if (slot) x += __ldg(p.bias_values + (long)b * p.nb + slot - 1);
-                    word_put<T>(o, k, x * tinv);
+                uint4 o;
+                if (in.bits(s_bits, i)) {
+                    const uint32_t seen = in.bits(s_seen, i);
+                    float add[E], y[E];
+                    in.floats(s_add, i, add);
+#pragma unroll
+                    for (int k = 0; k < E; ++k) {
+                        const float x = word_entry<T>(cur.w[q], k);
+                        y[k] = fmaf(x, (seen >> k) & 1u ? (x > 0.0f ? f_pos : f_neg) : tinv, add[k]);
+                    }
+                    o = word_of<T>(y);
+                } else {
+                    o = tinv == 1.0f ? cur.w[q] : word_scaled<T>(cur.w[q], tinv);
                 }
                 if (p.mask) o = word_masked<T>(o, allowed);
                 in.store(out, i, o);
@@ -281,7 +325,7 @@ __global__ void __launch_bounds__(kProcThreads, kProcOcc) process_kernel(Process
 // equals the one with the fewest CTAs (each scans the history).
 cudaError_t process_launch(ProcessParams p, cudaStream_t stream) {
     const int E = p.dtype == SPEC_BF16 ? 8 : 4;
-    constexpr int kMaxSeg = 13824;   // 56 KB of state and bits: four CTAs of an SM
+    constexpr int kMaxSeg = 13184;   // 56 KB of shared memory: four CTAs of an SM
     const long slots = (long)device_sm_count() * kProcOcc;
     const long scan = 64 + (p.Lmax + p.nb) / 8;   // the scan, in words that stream in the same time
     const int least = (p.V + kMaxSeg - 1) / kMaxSeg;

@@ -77,30 +77,6 @@ __device__ __forceinline__ float word_entry(const uint4& w, int k) {
     return __uint_as_float(h[k & 3]);
 }
 
-// The same for a k known at run time only, and entry k replaced by a float.
-template <typename T>
-__device__ __forceinline__ float word_pick(const uint4& w, int k) {
-    const int r = sizeof(T) == 2 ? k >> 1 : k;
-    const uint32_t h = (r & 2) ? ((r & 1) ? w.w : w.z) : ((r & 1) ? w.y : w.x);
-    if (sizeof(T) == 2) return __uint_as_float((k & 1) ? (h & 0xffff0000u) : (h << 16));
-    return __uint_as_float(h);
-}
-template <typename T>
-__device__ __forceinline__ void word_put(uint4& w, int k, float x) {
-    const int r = sizeof(T) == 2 ? k >> 1 : k;
-    uint32_t keep = 0u, v = __float_as_uint(x);
-    if (sizeof(T) == 2) {
-        v = (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(x));
-        v |= v << 16;
-        keep = (k & 1) ? 0x0000ffffu : 0xffff0000u;
-    }
-    v &= ~keep;
-    if (r == 0) w.x = (w.x & keep) | v;
-    if (r == 1) w.y = (w.y & keep) | v;
-    if (r == 2) w.z = (w.z & keep) | v;
-    if (r == 3) w.w = (w.w & keep) | v;
-}
-
 // E floats rounded (to nearest even for bf16) into a word.
 template <typename T>
 __device__ __forceinline__ uint4 word_of(const float (&x)[16 / sizeof(T)]) {
