@@ -60,7 +60,7 @@ size_t spec_workspace_bytes(spec_op op, int B, int gamma, int V, int r) {
         if (B < 1 || B > SPEC_MAX_TEACHER_ROWS || gamma < 1 || gamma > SPEC_MAX_TEACHER || V < 1 ||
             V > SPEC_MAX_V_TEACHER)
             return 0;
-        return op == SPEC_OP_TOP_LOGITS ? top_logits_workspace_bytes(B, V) : distill_workspace_bytes(B, gamma, V);
+        return op == SPEC_OP_TOP_LOGITS ? top_logits_workspace_bytes(B, V) : distill_workspace_bytes(B, V);
     }
     if (B < 1 || gamma < 1 || gamma > SPEC_MAX_GAMMA || V < 1 || V > SPEC_MAX_V) return 0;
     switch (op) {
@@ -587,7 +587,7 @@ spec_status spec_distill(const void* student, spec_dtype dtype, int rows, int V,
     if (!(temperature > 0.0f && temperature < INFINITY)) return SPEC_ERR_INVALID_ARG;
     if (!student || !values || !ids || !loss_out) return SPEC_ERR_INVALID_ARG;
     if (!aligned16(student) || !aligned16(grad_out)) return SPEC_ERR_ALIGN;
-    if (!workspace || workspace_bytes < distill_workspace_bytes(rows, K, V)) return SPEC_ERR_WORKSPACE;
+    if (!workspace || workspace_bytes < distill_workspace_bytes(rows, V)) return SPEC_ERR_WORKSPACE;
     DistillParams p;
     memset(&p, 0, sizeof(p));
     p.student = student;

@@ -123,12 +123,10 @@ __global__ void __launch_bounds__(SPEC_MAX_TEACHER) distill_finish_kernel(Distil
     __shared__ int s_id[SPEC_MAX_TEACHER];
     const int row = blockIdx.x, tid = threadIdx.x;
     const float wt = p.weight ? p.weight[row] : 1.0f;
-    float4* st = p.stats + row;
     if (wt == 0.0f) {   // the row does not count and is not read
         if (tid == 0) {
             p.loss_out[row] = 0.0f;
             if (p.lse_out) p.lse_out[row] = 0.0f;
-            *st = make_float4(0.0f, 0.0f, 1.0f, 0.0f);
         }
         return;
     }
@@ -173,93 +171,557 @@ __global__ void __launch_bounds__(SPEC_MAX_TEACHER) distill_finish_kernel(Distil
     float l = pk > 0.0f ? pk * ((ak - lP) - ((z - M) * p.inv_t - lZ)) : 0.0f;
     if (tid == 0 && pT > 0.0f) l += pT * ((aT - lP) - (logf(ST) - lZ));
     const float loss = cta_sum_f(l, s_f);
-    const float g = wt * p.inv_t;
     const bool bad = bad_row || nbad > 0;
-    if (p.grad_out && tid < p.K) {
-        const float d = taught ? (qe / Z - pk) * g : 0.0f;
-        p.named_grad[(long)row * p.K + tid] = bad ? NAN : d;
-    }
     if (tid == 0) {
         p.loss_out[row] = bad ? NAN : loss;
         if (p.lse_out) p.lse_out[row] = bad ? NAN : fmaf(M, p.inv_t, lZ);
-        const float cT = taught ? g * (1.0f / Z - (ST > 0.0f ? pT / ST : 0.0f)) : 0.0f;
-        *st = make_float4(bad ? 0.0f : M, bad ? NAN : cT, 0.0f, 0.0f);
         if (nbad) atomicOr(p.status, SPEC_DEV_TOKEN);
         if (bad_row) atomicOr(p.status, SPEC_DEV_NONFINITE);
     }
 }
 
-// The gradient: the weight times the row's coefficient, then the named entries.
+// ---------------------------------------------------------------------------------
+// Loss and gradient in one pass over the row.
+//
+// A row is split over a group of G CTAs; each holds its slice in shared memory from the read
+// to the write of the gradient, so the logits are read once and the gradient is written once.
+// The warps of a CTA have four jobs and meet at mbarriers only:
+//   dense     A(i): the slice's (maximum, sum) over the entries that no id names;
+//             B(i): every logit in the slot becomes its gradient, 2^((z - m) c) times one
+//             factor.  In the order A(0) A(1) B(0) A(2) B(1) ..
+//   exchange  posts the slice's statistics, waits for the other slices', forms the factor
+//   entries   one thread per teacher entry: takes the named logits out of the slice (-inf),
+//             the teacher's row, the loss, and puts the named entries' gradients in after B(i)
+//   copies    slices in and out
+// So the row behind is reduced while the statistics of the row before travel (2000 to 4000
+// cycles on a loaded memory system, about as long as A and B), and three slots keep one
+// slice arriving and one leaving meanwhile.
+//
+// The exchange: a record per CTA in global memory, each 64-bit word a value and a tag that no
+// earlier row or call has used, so a word is valid when its tag is and nothing else has to
+// be ordered.  A record's place is used again two exchanges later: a CTA that posts the
+// (j + 1)th has seen every post of the jth, and each came after its CTA had read the
+// (j - 1)th.  In place of the logits the gradient is safe for the same reason: a slice is
+// written after every record of its row has arrived, and a record holds what was read.
+// ---------------------------------------------------------------------------------
+constexpr int kFuseDense = 256;                            // threads of the dense warps
+constexpr int kFuseNamed = SPEC_MAX_TEACHER;               // threads of the entries' warps
+constexpr int kFuseThreads = kFuseDense + kFuseNamed + 64; // and a warp each to exchange and to copy
+constexpr int kDenseWarps = kFuseDense / 32, kNamedWarps = kFuseNamed / 32;
+constexpr int kFuseOcc = 2;                                // CTAs per SM
+constexpr int kFuseBatch = 4;                              // words a dense thread holds at once
+constexpr int kFuseSlice = 2048;                           // most words of a slice (32 KB)
+constexpr int kFuseSlots = 3;                              // slices in shared memory
+constexpr int kFuseRecord = 4;                             // words of a record
+constexpr int kFuseRing = 2;                               // exchanges a record's place lasts
+constexpr int kFuseMaxCtas = 512;
+constexpr uint32_t kBadToken = 0x7fc0dead;                 // a NaN that says: a bad id
+
+struct FuseHeader {
+    unsigned epoch;    // tags up to here have been used
+    unsigned exits;    // CTAs that have left (0 between calls)
+    unsigned pad[62];
+};
+
+__device__ __forceinline__ void post_word(unsigned long long* p, float v, unsigned tag) {
+    asm volatile("st.relaxed.gpu.global.u64 [%0], %1;"
+                 :: "l"(p), "l"(((unsigned long long)tag << 32) | __float_as_uint(v)) : "memory");
+}
+__device__ __forceinline__ unsigned long long peek_word(const unsigned long long* p) {
+    unsigned long long v;
+    asm volatile("ld.relaxed.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(p) : "memory");
+    return v;
+}
+__device__ __forceinline__ void bulk_s2g(void* dst, const void* src, unsigned bytes) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;"
+                 :: "l"(dst), "r"(smem_u32(src)), "r"(bytes) : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+__device__ __forceinline__ void bulk_s2g_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void bulk_s2g_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+__device__ __forceinline__ void named_sync() { asm volatile("bar.sync 1, %0;" :: "n"(kFuseNamed) : "memory"); }
+
+// (maximum, sum of 2^((x - maximum) c)) pairs merged over the N lanes that differ in their
+// low bits; NaN shows in the maximum.
+template <int N>
+__device__ __forceinline__ float2 stat_lanes(float2 v, float c) {
+    float m = v.x;
+#pragma unroll
+    for (int o = N / 2; o > 0; o >>= 1) m = f_max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+    float s = v.x == -INFINITY ? 0.0f : v.y * ex2((v.x - m) * c);
+#pragma unroll
+    for (int o = N / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    return make_float2(m, s);
+}
+__device__ __forceinline__ float2 stat_merge(float2 a, float2 b, float c) {
+    const float m = f_max_nan(a.x, b.x);
+    float s = 0.0f;
+    if (a.x != -INFINITY) s += a.y * ex2((a.x - m) * c);
+    if (b.x != -INFINITY) s += b.y * ex2((b.x - m) * c);
+    return make_float2(m, s);
+}
+
+// What is known of a row once its slices' statistics are together.
+struct FuseRow {
+    float ref;        // unnamed entries: gradient 2^((z - ref) c) factor
+    float factor;
+    float M, Z;       // all entries: maximum, sum
+    float mT, sT;     // the unnamed ones'
+    float top, P;     // the teacher's normaliser
+    int skip, bad;
+};
+
+// The slice of a row that one CTA holds: words [0, n) of it, whole words [a, b).
 template <typename T>
-__global__ void __launch_bounds__(kDistThreads) distill_grad_kernel(DistillParams p) {
+struct Slice {
+    RowWords<T> in;
+    int first, n, a, b;
+    __device__ __forceinline__ Slice(const T* row, int V, int first_, int most) : in(row, V), first(first_) {
+        n = max(0, min(in.n - first, most));
+        a = n > 0 && !in.whole(first) ? 1 : 0;
+        b = n > a && !in.whole(first + n - 1) ? n - 1 : max(n, a);
+    }
+};
+
+template <typename T>
+__global__ void __launch_bounds__(kFuseThreads, kFuseOcc) distill_fused_kernel(DistillParams p) {
     constexpr int E = 16 / (int)sizeof(T);
-    const int row = blockIdx.x / p.pieces, piece = blockIdx.x - row * p.pieces;
-    const int tid = threadIdx.x;
-    const RowWords<T> in(reinterpret_cast<const T*>(p.student) + (long)row * p.ld, p.V);
-    T* out = reinterpret_cast<T*>(p.grad_out) + (long)row * p.ld;
-    const int w0 = piece * kDistPiece;
-    const float4 st = p.stats[row];
-    const bool skip = st.z != 0.0f, nan = isnan(st.y);
-    uint4 w[kDistWords];
-#pragma unroll
-    for (int q = 0; q < kDistWords; ++q) {
-        const int i = w0 + q * kDistThreads + tid;
-        if (i < in.n && !skip) w[q] = in.load(i);
-    }
-#pragma unroll
-    for (int q = 0; q < kDistWords; ++q) {
-        const int i = w0 + q * kDistThreads + tid;
-        if (i >= in.n) continue;
-        float d[E];
-#pragma unroll
-        for (int k = 0; k < E; ++k) {
-            d[k] = skip ? 0.0f : ex2((word_entry<T>(w[q], k) - st.x) * p.scale) * st.y;
-            if (nan) d[k] = NAN;
+    extern __shared__ __align__(128) uint8_t s_slots[];
+    // full: a slice has arrived; ready: its named entries are out; reduced: A is done; stated:
+    // the teacher's statistics are there; known: the row's FuseRow is; dense: B is done;
+    // fixed: the named entries' gradients are in.  A barrier's place comes back after two rows
+    // (slots: three): what a waiter waits for always needs, through the others, that it has
+    // left the wait two (three) rows before.
+    __shared__ __align__(8) uint64_t s_full[kFuseSlots], s_fixed[kFuseSlots];
+    __shared__ __align__(8) uint64_t s_ready[2], s_reduced[2], s_stated[2], s_known[2], s_dense[2];
+    __shared__ uint32_t s_bits[kFuseSlice * E / 32];         // the slice's entries named so far
+    __shared__ float2 s_tail[2][kDenseWarps], s_top[2][kNamedWarps], s_teach[2][kNamedWarps];
+    __shared__ float s_loss[kNamedWarps], s_wt[2], s_aT[2];
+    __shared__ int s_flag[2];
+    __shared__ FuseRow s_row[2];
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int group = blockIdx.x / p.group_size, rank = blockIdx.x - group * p.group_size;
+    const int n_it = (p.rows - group + p.n_groups - 1) / p.n_groups;
+    const float c = p.scale;
+    const unsigned epoch = *(volatile unsigned*)&p.fuse->epoch;
+
+    auto row_of = [&](int i) { return group + i * p.n_groups; };
+    auto slice_of = [&](int i) {
+        return Slice<T>(reinterpret_cast<const T*>(p.student) + (long)row_of(i) * p.ld, p.V, rank * p.slice, p.slice);
+    };
+    auto grad_of = [&](int i) { return reinterpret_cast<T*>(p.grad_out) + (long)row_of(i) * p.ld; };
+    auto slot_of = [&](int i) { return reinterpret_cast<uint4*>(s_slots) + (size_t)(i % kFuseSlots) * p.slice; };
+
+    if (tid == 0) {
+        for (int q = 0; q < kFuseSlots; ++q) {
+            mbar_init(&s_full[q], 1);
+            mbar_init(&s_fixed[q], kFuseNamed);
         }
-        in.store(out, i, word_of<T>(d));
+        for (int q = 0; q < 2; ++q) {
+            mbar_init(&s_ready[q], kFuseNamed);
+            mbar_init(&s_reduced[q], kDenseWarps);
+            mbar_init(&s_stated[q], kNamedWarps);
+            mbar_init(&s_known[q], 1);
+            mbar_init(&s_dense[q], kDenseWarps);
+            s_flag[q] = 0;
+        }
+        fence_mbar_init();
     }
-    if (skip || nan) return;
-    __syncthreads();   // the piece is written; its named entries replace what is there
-    const int e0 = in.entry(w0);
-    for (int k = tid; k < p.K; k += kDistThreads) {
-        const int id = p.ids[(long)row * p.K + k];
-        if (id < 0 || (unsigned)(id - e0) >= (unsigned)(kDistPiece * E)) continue;
-        const float d = p.named_grad[(long)row * p.K + k];
-        if (sizeof(T) == 2) out[id] = (T)__bfloat16_as_ushort(__float2bfloat16_rn(d));
-        else out[id] = (T)d;
+    for (int i = tid; i < kFuseSlice * E / 32; i += kFuseThreads) s_bits[i] = 0u;
+    __syncthreads();
+    bool dead = false;   // a wait ran out: nothing more is waited for
+    auto wait = [&](uint64_t* bar, int phase) {
+        if (!mbar_wait(bar, phase & 1, p.status, dead ? 0ull : kWaitLimitNs)) dead = true;
+    };
+
+    if (tid < kFuseDense) {
+        // ------------------------------------------------------------------ dense
+        const int warp = tid >> 5;
+        const f2x cc = f2_pack(c, c);
+        for (int i = 0; i <= n_it; ++i) {
+            if (i < n_it) {   // A(i)
+                const int n = slice_of(i).n;
+                const uint4* slot = slot_of(i);
+                wait(&s_full[i % kFuseSlots], i / kFuseSlots);
+                wait(&s_ready[i & 1], i >> 1);
+                if (s_wt[i & 1] != 0.0f) {
+                    float m = -INFINITY, s = 0.0f;
+                    for (int l0 = 0; l0 < n; l0 += kFuseDense * kFuseBatch) {
+                        uint4 w[kFuseBatch];
+                        const uint32_t ninf = NegInf<T>::word;
+                        float bm = -INFINITY;
+#pragma unroll
+                        for (int q = 0; q < kFuseBatch; ++q) {
+                            const int l = l0 + q * kFuseDense + tid;
+                            w[q] = l < n ? slot[l] : make_uint4(ninf, ninf, ninf, ninf);
+                        }
+#pragma unroll
+                        for (int q = 0; q < kFuseBatch; ++q) bm = f_max_nan(bm, u4_max_nan<sizeof(T)>(w[q]));
+                        // a thread's own running maximum; a batch of -inf adds nothing
+                        bm = f_max_nan(bm, m);
+                        if (bm != m) {
+                            s = m == -INFINITY ? 0.0f : s * ex2((m - bm) * c);
+                            m = bm;
+                        }
+                        const float ref = m == -INFINITY ? 0.0f : m;
+                        const f2x mm = f2_pack(-ref, -ref);
+                        f2x acc[2] = {f2_pack(s, 0.0f), f2_pack(0.0f, 0.0f)};
+#pragma unroll
+                        for (int q = 0; q < kFuseBatch; ++q) {
+#pragma unroll
+                            for (int k = 0; k < E; k += 2)
+                                acc[(k >> 1) & 1] = f2_add(acc[(k >> 1) & 1],
+                                    f2_ex2(f2_mul(f2_add(f2_pack(word_entry<T>(w[q], k), word_entry<T>(w[q], k + 1)), mm), cc)));
+                        }
+                        const float2 a0 = f2_unpack(acc[0]), a1 = f2_unpack(acc[1]);
+                        s = (a0.x + a0.y) + (a1.x + a1.y);
+                    }
+                    const float2 t = stat_lanes<32>(make_float2(m, s), c);
+                    if (lane == 0) s_tail[i & 1][warp] = t;
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive1(&s_reduced[i & 1]);
+            }
+            if (i >= 1) {     // B(i - 1)
+                const int j = i - 1, n = slice_of(j).n;
+                uint4* slot = slot_of(j);
+                wait(&s_known[j & 1], j >> 1);
+                const float ref = s_row[j & 1].ref, f = s_row[j & 1].factor;
+                const bool skip = s_row[j & 1].skip;
+                const f2x mm = f2_pack(-ref, -ref), ff = f2_pack(f, f);
+#pragma unroll 4
+                for (int l = tid; l < n; l += kFuseDense) {
+                    uint4 w = make_uint4(0u, 0u, 0u, 0u);
+                    if (!skip) {
+                        w = slot[l];
+                        float d[E];
+#pragma unroll
+                        for (int k = 0; k < E; k += 2) {
+                            const float2 y = f2_unpack(f2_mul(
+                                f2_ex2(f2_mul(f2_add(f2_pack(word_entry<T>(w, k), word_entry<T>(w, k + 1)), mm), cc)), ff));
+                            d[k] = y.x;
+                            d[k + 1] = y.y;
+                        }
+                        w = word_of<T>(d);
+                    }
+                    slot[l] = w;
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive1(&s_dense[j & 1]);
+            }
+        }
+    } else if (tid < kFuseDense + kFuseNamed) {
+        // ---------------------------------------------------------------- entries
+        const int k = tid - kFuseDense, warp = k >> 5;
+        // thread k's teacher entry of a row, the student's logit there (where it is known), its
+        // place in the slice (-1 outside), and what the row's entries share
+        struct Entry { int id; float a, z; int at; float wt, aT; };
+        auto load = [&](int i, Entry& e) {
+            e.id = e.at = -1;
+            e.a = e.z = e.aT = -INFINITY;
+            e.wt = 0.0f;
+            if (i >= n_it) return;
+            const int row = row_of(i);
+            e.wt = p.weight ? p.weight[row] : 1.0f;
+            if (p.tail) e.aT = p.tail[row];
+            if (k >= p.K) return;
+            const long at = (long)row * p.K + k;
+            e.id = p.ids[at];
+            e.a = p.values_dtype == SPEC_BF16 ? to_float(reinterpret_cast<const bf16_t*>(p.values)[at])
+                                              : reinterpret_cast<const float*>(p.values)[at];
+        };
+        auto known_id = [&](const Entry& e) { return e.id >= 0 && e.id < p.V; };
+        // slice 0 forms the loss, so it reads all of its row's named logits
+        auto gather = [&](int i, Entry& e) {
+            if (i >= n_it || rank != 0 || !known_id(e) || e.wt == 0.0f) return;
+            const T* z = reinterpret_cast<const T*>(p.student) + (long)row_of(i) * p.ld + e.id;
+            if (sizeof(T) == 2) e.z = to_float((bf16_t)*reinterpret_cast<const volatile unsigned short*>(z));
+            else e.z = to_float(*reinterpret_cast<const volatile float*>(z));
+        };
+        // the named entries out of the slice, the teacher's statistics
+        auto prepare = [&](int i, Entry& e) {
+            const int par = i & 1;
+            const Slice<T> sl = slice_of(i);
+            const int at = e.id - sl.in.entry(sl.first);
+            e.at = known_id(e) && at >= 0 && at < sl.n * E ? at : -1;
+            int f = 0;
+            if (e.at >= 0 && (atomicOr(&s_bits[at >> 5], 1u << (at & 31)) >> (at & 31)) & 1u) f = 1;   // listed twice
+            if (k == 0) {
+                s_wt[par] = e.wt;
+                s_aT[par] = e.aT;
+            }
+            wait(&s_full[i % kFuseSlots], i / kFuseSlots);
+            if (e.at >= 0 && e.wt != 0.0f) {
+                T* x = reinterpret_cast<T*>(slot_of(i)) + e.at;
+                e.z = to_float(*x);
+                *x = sizeof(T) == 2 ? (T)0xff80u : (T)-INFINITY;
+            }
+            mbar_arrive1(&s_ready[par]);
+            if (e.wt != 0.0f) {
+                const float a = known_id(e) ? e.a * p.inv_t : -INFINITY;
+                const float2 t = stat_lanes<32>(make_float2(a, 1.0f), kLog2e);
+                const float2 z = stat_lanes<32>(make_float2(rank == 0 ? e.z : -INFINITY, 1.0f), c);
+                if (lane == 0) {
+                    s_teach[par][warp] = t;
+                    s_top[par][warp] = z;
+                }
+                if (rank == 0) {
+                    f |= (e.id < -1 || e.id >= p.V) ? 1 : 0;
+                    if (!(a < INFINITY) || !(e.aT < INFINITY) || !(fabsf(e.wt) < INFINITY)) f |= 2;
+                }
+                if (f) atomicOr(&s_flag[par], f);
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive1(&s_stated[par]);
+            named_sync();   // every entry's bit has been looked at
+            if (e.at >= 0) s_bits[e.at >> 5] = 0u;
+        };
+        Entry cur, nxt, far;
+        load(0, cur);
+        load(1, nxt);
+        load(2, far);
+        gather(0, cur);
+        prepare(0, cur);
+        gather(1, nxt);
+        for (int i = 0; i < n_it; ++i) {
+            const int row = row_of(i), par = i & 1;
+            const bool skip = cur.wt == 0.0f;
+            named_sync();   // the bits are clear again
+            if (i + 1 < n_it) prepare(i + 1, nxt);
+            gather(i + 2, far);
+            Entry more;
+            load(i + 3, more);
+            wait(&s_known[par], i >> 1);
+            const FuseRow r = s_row[par];
+            float d = 0.0f;
+            if (!skip) {
+                const bool taught = r.top > -INFINITY;
+                const float lt = known_id(cur) && taught ? fmaf(cur.a, p.inv_t, -r.top) : -INFINITY;
+                const float pk = taught ? __expf(lt) / r.P : 0.0f;
+                d = r.bad ? NAN : (taught ? (ex2((cur.z - r.M) * c) / r.Z - pk) * (cur.wt * p.inv_t) : 0.0f);
+                if (rank == 0) {
+                    const float lP = logf(r.P), lZ = logf(r.Z);
+                    const float pT = taught ? __expf(cur.aT - r.top) / r.P : 0.0f;
+                    float l = pk > 0.0f ? pk * ((lt - lP) - ((cur.z - r.M) * p.inv_t - lZ)) : 0.0f;
+                    if (k == 0 && pT > 0.0f) {
+                        const float lq = r.mT > -INFINITY ? fmaf(r.mT - r.M, p.inv_t, logf(r.sT)) - lZ : -INFINITY;
+                        l += pT * (((cur.aT - r.top) - lP) - lq);
+                    }
+                    l = warp_sum(l);
+                    if (lane == 0) s_loss[warp] = l;
+                }
+            }
+            if (rank == 0) {
+                named_sync();
+                if (k == 0) {
+                    float l = s_loss[0];
+                    for (int q = 1; q < kNamedWarps; ++q) l += s_loss[q];
+                    p.loss_out[row] = skip ? 0.0f : (r.bad ? NAN : l);
+                    if (p.lse_out) p.lse_out[row] = skip ? 0.0f : (r.bad ? NAN : fmaf(r.M, p.inv_t, logf(r.Z)));
+                }
+            }
+            wait(&s_dense[par], i >> 1);
+            if (cur.at >= 0 && !skip) {
+                T* x = reinterpret_cast<T*>(slot_of(i)) + cur.at;
+                if (sizeof(T) == 2) *x = (T)__bfloat16_as_ushort(__float2bfloat16_rn(d));
+                else *x = (T)d;
+            }
+            fence_proxy_async_smem();
+            mbar_arrive1(&s_fixed[i % kFuseSlots]);
+            cur = nxt;
+            nxt = far;
+            far = more;
+        }
+    } else if (tid < kFuseDense + kFuseNamed + 32) {
+        // --------------------------------------------------------------- exchange
+        unsigned long long* recs = p.records + (size_t)group * kFuseRing * p.group_size * kFuseRecord;
+        const float2 none = make_float2(-INFINITY, 0.0f);
+        unsigned live = 0;       // exchanges so far: rows that count
+        for (int i = 0; i < n_it; ++i) {
+            const int par = i & 1;
+            wait(&s_stated[par], i >> 1);
+            const float wt = s_wt[par], aT = s_aT[par];
+            const bool skip = wt == 0.0f;
+            // the teacher's normaliser, and the named logits' (slice 0 has them)
+            const float2 tt = stat_lanes<8>(skip ? none : ((lane & 7) < kNamedWarps ? s_teach[par][lane & 7] : ((lane & 7) == kNamedWarps ? make_float2(aT, 1.0f) : none)), kLog2e);
+            const float2 nn = stat_lanes<4>(skip ? none : s_top[par][lane & 3], c);
+            static_assert(kNamedWarps == 4 && kDenseWarps <= 16, "the lanes' layout");
+            const int flag = s_flag[par];
+            float2 T2 = none, N2 = none;
+            bool token = false, late = false;
+            wait(&s_reduced[par], i >> 1);
+            if (!skip) {
+                unsigned long long* rec = recs + (size_t)(live % kFuseRing) * p.group_size * kFuseRecord;
+                const unsigned tag = epoch + 1u + live;
+                ++live;
+                float2 t = stat_lanes<16>((lane & 15) < kDenseWarps ? s_tail[par][lane & 15] : none, c);
+                if (flag || dead) t.x = flag & 1 ? __uint_as_float(kBadToken) : NAN;
+                if (lane < (rank == 0 ? 4 : 2))
+                    post_word(rec + (size_t)rank * kFuseRecord + lane, lane == 0 ? t.x : (lane == 1 ? t.y : (lane == 2 ? nn.x : nn.y)), tag);
+                const unsigned long long t0 = global_timer_ns();
+                for (int r = lane; r < p.group_size; r += 32) {
+                    unsigned long long v[kFuseRecord] = {0ull, 0ull, 0ull, 0ull};
+                    const unsigned long long* src = rec + (size_t)r * kFuseRecord;
+                    unsigned spins = 0;
+                    while (true) {
+                        bool here = true;
+#pragma unroll
+                        for (int q = 0; q < kFuseRecord; ++q)
+                            if (q < 2 || r == 0) v[q] = peek_word(src + q);
+#pragma unroll
+                        for (int q = 0; q < kFuseRecord; ++q)
+                            if (q < 2 || r == 0) here &= (unsigned)(v[q] >> 32) == tag;
+                        if (here) break;
+                        if (dead || late || (((++spins) & 63u) == 0 && global_timer_ns() - t0 > kWaitLimitNs)) {
+                            late = true;
+                            break;
+                        }
+                    }
+                    token |= (uint32_t)v[0] == kBadToken;
+                    T2 = stat_merge(T2, make_float2(__uint_as_float((uint32_t)v[0]), __uint_as_float((uint32_t)v[1])), c);
+                    if (r == 0) N2 = make_float2(__uint_as_float((uint32_t)v[2]), __uint_as_float((uint32_t)v[3]));
+                }
+                late = __any_sync(0xffffffffu, late);
+                token = __any_sync(0xffffffffu, token);
+                if (late) dead = true;
+                T2 = stat_lanes<32>(T2, c);
+                N2.x = __shfl_sync(0xffffffffu, N2.x, 0);
+                N2.y = __shfl_sync(0xffffffffu, N2.y, 0);
+            }
+            if (lane == 0) {
+                const float2 A = stat_merge(T2, N2, c);
+                const bool bad = !skip && (late || !(A.x < INFINITY) || A.x == -INFINITY);
+                const bool taught = tt.x > -INFINITY, some = T2.x > -INFINITY;
+                const float pT = taught ? __fdividef(__expf(aT - tt.x), tt.y) : 0.0f;
+                FuseRow r;
+                r.ref = some ? T2.x : 0.0f;
+                r.factor = 0.0f;
+                if (taught && some)
+                    r.factor = wt * p.inv_t * (__fdividef(ex2((T2.x - A.x) * c), A.y) - (pT > 0.0f ? __fdividef(pT, T2.y) : 0.0f));
+                if (bad) r.factor = NAN;
+                r.M = A.x;
+                r.Z = A.y;
+                r.mT = T2.x;
+                r.sT = T2.y;
+                r.top = tt.x;
+                r.P = tt.y;
+                r.skip = skip;
+                r.bad = bad;
+                s_row[par] = r;
+                s_flag[par] = 0;
+                mbar_arrive1(&s_known[par]);
+                unsigned raise = 0u;
+                if (flag & 1) raise |= SPEC_DEV_TOKEN;
+                if ((flag & 2) || (bad && rank == 0 && !token && !late)) raise |= SPEC_DEV_NONFINITE;
+                if (late) raise |= SPEC_DEV_TIMEOUT;
+                if (raise) atomicOr(p.status, raise);
+            }
+            __syncwarp();
+        }
+    } else {
+        // ----------------------------------------------------------------- copies
+        auto issue = [&](int i) {   // the warp: row i's slice on its way to its slot
+            uint64_t* bar = &s_full[i % kFuseSlots];
+            const Slice<T> sl = slice_of(i);
+            const bool on = !(p.weight && p.weight[row_of(i)] == 0.0f);
+            if (on && lane < 2) {   // the words that are not whole
+                const int l = lane == 0 ? 0 : sl.b;
+                if (lane == 0 ? sl.a > 0 : sl.b < sl.n) slot_of(i)[l] = sl.in.load(sl.first + l);
+            }
+            __syncwarp();
+            if (lane == 0) {
+                if (on && sl.a < sl.b) {
+                    const unsigned bytes = (unsigned)(sl.b - sl.a) * 16u;
+                    mbar_arrive_expect_tx(bar, bytes);
+                    bulk_g2s(slot_of(i) + sl.a, sl.in.p + sl.in.entry(sl.first + sl.a), bytes, bar);
+                } else {
+                    mbar_arrive1(bar);
+                }
+            }
+        };
+        for (int i = 0; i < kFuseSlots && i < n_it; ++i) issue(i);
+        for (int i = 0; i < n_it; ++i) {
+            wait(&s_fixed[i % kFuseSlots], i / kFuseSlots);
+            const Slice<T> sl = slice_of(i);
+            if (lane == 0 && sl.a < sl.b)
+                bulk_s2g(grad_of(i) + sl.in.entry(sl.first + sl.a), slot_of(i) + sl.a, (unsigned)(sl.b - sl.a) * 16u);
+            if (lane < 2) {
+                const int l = lane == 0 ? 0 : sl.b;
+                if (lane == 0 ? sl.a > 0 : sl.b < sl.n) sl.in.store(grad_of(i), sl.first + l, slot_of(i)[l]);
+            }
+            if (i + kFuseSlots < n_it) {
+                if (lane == 0) bulk_s2g_wait_read();
+                fence_proxy_async_smem();   // the words that were not whole, before the copy that may cover them
+                __syncwarp();
+                issue(i + kFuseSlots);
+            }
+        }
+        if (lane == 0) {
+            bulk_s2g_wait();
+            // the last CTA to leave retires the call's tags: its slices' gradients are out, so
+            // every record that it needed has been read
+            const unsigned n = p.n_groups * p.group_size;
+            if (atom_add_acq_rel(&p.fuse->exits, 1u) == n - 1u) {
+                atomicExch(&p.fuse->exits, 0u);
+                atomicExch(&p.fuse->epoch, epoch + (unsigned)((p.rows + p.n_groups - 1) / p.n_groups) + 1u);
+            }
+        }
     }
+}
+
+template <typename T>
+static cudaError_t fused_launch(DistillParams p, cudaStream_t stream) {
+    const int ctas = device_sm_count() * kFuseOcc < kFuseMaxCtas ? device_sm_count() * kFuseOcc : kFuseMaxCtas;
+    const int words = (p.V + 2 * (16 / (int)sizeof(T)) - 2) / (16 / (int)sizeof(T));   // whatever the row's offset
+    const int least = (words + kFuseSlice - 1) / kFuseSlice;
+    if (least > ctas) return cudaErrorInvalidConfiguration;
+    // as many rows at once as there are CTAs for, then the CTAs left over go to the groups,
+    // down to a slice of one word per dense thread
+    int groups = ctas / least;
+    if (groups > p.rows) groups = p.rows;
+    int size = ctas / groups;
+    const int most = (words + kFuseDense - 1) / kFuseDense;
+    if (size > most) size = most > least ? most : least;
+    p.n_groups = groups;
+    p.group_size = size;
+    p.slice = (words + size - 1) / size;
+    const size_t smem = (size_t)kFuseSlots * p.slice * 16;
+    const cudaError_t e = cudaFuncSetAttribute(distill_fused_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               kFuseSlots * kFuseSlice * 16);
+    if (e != cudaSuccess) return e;
+    void* args[] = {&p};
+    return cudaLaunchCooperativeKernel((const void*)distill_fused_kernel<T>, dim3(groups * size), dim3(kFuseThreads), args,
+                                       smem, stream);
 }
 
 static size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
-size_t distill_workspace_bytes(int rows, int K, int V) {
-    return kWsHeaderBytes + align256((size_t)rows * sizeof(float4)) +
-           align256((size_t)rows * distill_pieces(V, 4) * sizeof(float2)) + align256((size_t)rows * K * sizeof(float));
+constexpr size_t kFuseBytes = sizeof(FuseHeader) + sizeof(unsigned long long) * kFuseMaxCtas * kFuseRing * kFuseRecord;
+
+size_t distill_workspace_bytes(int rows, int V) {
+    return kWsHeaderBytes + align256(kFuseBytes) + align256((size_t)rows * distill_pieces(V, 4) * sizeof(float2));
 }
 
 template <typename T>
 static cudaError_t distill_typed(DistillParams p, cudaStream_t stream) {
+    if (p.grad_out) return fused_launch<T>(p, stream);
     p.pieces = distill_pieces(p.V, sizeof(T));
     const long grid = (long)p.rows * p.pieces;
     if (grid > 0x7fffffffL) return cudaErrorInvalidConfiguration;
     distill_scan_kernel<T><<<(unsigned)grid, kDistThreads, 0, stream>>>(p);
-    cudaError_t e = cudaGetLastError();
+    const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     distill_finish_kernel<T><<<p.rows, SPEC_MAX_TEACHER, 0, stream>>>(p);
-    e = cudaGetLastError();
-    if (e != cudaSuccess || !p.grad_out) return e;
-    distill_grad_kernel<T><<<(unsigned)grid, kDistThreads, 0, stream>>>(p);
     return cudaGetLastError();
 }
 
 cudaError_t distill_launch(DistillParams p, void* ws, cudaStream_t stream) {
     p.status = &reinterpret_cast<WsHeader*>(ws)->status;
     uint8_t* b = reinterpret_cast<uint8_t*>(ws) + kWsHeaderBytes;
-    p.stats = reinterpret_cast<float4*>(b);
-    b += align256((size_t)p.rows * sizeof(float4));
-    p.parts = reinterpret_cast<float2*>(b);
-    b += align256((size_t)p.rows * distill_pieces(p.V, 4) * sizeof(float2));
-    p.named_grad = reinterpret_cast<float*>(b);
+    p.fuse = reinterpret_cast<FuseHeader*>(b);
+    p.records = reinterpret_cast<unsigned long long*>(b + sizeof(FuseHeader));
+    p.parts = reinterpret_cast<float2*>(b + align256(kFuseBytes));
     return p.dtype == SPEC_BF16 ? distill_typed<bf16_t>(p, stream) : distill_typed<float>(p, stream);
 }
 

@@ -260,6 +260,7 @@ size_t top_logits_workspace_bytes(int rows, int V);
 cudaError_t top_logits_launch(TopLogitsParams p, void* ws, cudaStream_t stream);
 
 // spec_distill
+struct FuseHeader;
 struct DistillParams {
     const void* student;       // rows of `ld` entries apart, V used
     int dtype;
@@ -277,10 +278,13 @@ struct DistillParams {
     // chosen at launch
     int pieces;
     float2* parts;             // [rows, pieces] (maximum, sum) of the entries no id names
-    float4* stats;             // [rows] maximum, coefficient, row skipped
-    float* named_grad;         // [rows, K]
+    // with the gradient: groups of CTAs, a row at a time each
+    int n_groups, group_size;
+    int slice;                 // words of a row per CTA
+    FuseHeader* fuse;
+    unsigned long long* records;
 };
-size_t distill_workspace_bytes(int rows, int K, int V);
+size_t distill_workspace_bytes(int rows, int V);
 cudaError_t distill_launch(DistillParams p, void* ws, cudaStream_t stream);
 
 int device_sm_count();
