@@ -204,13 +204,13 @@ __global__ void __launch_bounds__(SPEC_MAX_TEACHER) distill_finish_kernel(Distil
 // (j - 1)th.  In place of the logits the gradient is safe for the same reason: a slice is
 // written after every record of its row has arrived, and a record holds what was read.
 // ---------------------------------------------------------------------------------
-constexpr int kFuseDense = 256;                            // threads of the dense warps
+constexpr int kFuseDense = 384;                            // threads of the dense warps
 constexpr int kFuseNamed = SPEC_MAX_TEACHER;               // threads of the entries' warps
 constexpr int kFuseThreads = kFuseDense + kFuseNamed + 64; // and a warp each to exchange and to copy
 constexpr int kDenseWarps = kFuseDense / 32, kNamedWarps = kFuseNamed / 32;
-constexpr int kFuseOcc = 2;                                // CTAs per SM
+constexpr int kFuseOcc = 1;                                // CTAs per SM
 constexpr int kFuseBatch = 4;                              // words a dense thread holds at once
-constexpr int kFuseSlice = 2048;                           // most words of a slice (32 KB)
+constexpr int kFuseSlice = 4480;                           // most words of a slice (70 KB)
 constexpr int kFuseSlots = 3;                              // slices in shared memory
 constexpr int kFuseRecord = 4;                             // words of a record
 constexpr int kFuseRing = 2;                               // exchanges a record's place lasts
