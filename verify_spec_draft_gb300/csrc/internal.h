@@ -254,6 +254,8 @@ struct TopLogitsParams {
     unsigned* status;
     // chosen at launch
     int n_blocks, pieces;
+    int batch;                 // blocks of a warp
+    unsigned* done;            // [rows] pieces finished (0 between calls)
     float2* blocks;            // [rows, n_blocks] (maximum, sum)
 };
 size_t top_logits_workspace_bytes(int rows, int V);

@@ -1,15 +1,19 @@
 // top_logits.cu - each row's K largest logits and the log-sum-exp of the rest
 // (spec_top_logits): a teacher row in the compact form that spec_distill reads.
 //
-// Two kernels.  top_scan_kernel streams the rows once: a warp-wide load (32 words of 16
-// bytes, 512 bytes) is a block, and each block leaves its maximum m and
-// s = sum 2^((x - m) log2e / t); the maximum is kept as it is and taken from x before the
-// scaling, so that rows filled with the type's lowest value neither overflow nor vanish.  top_pick_kernel, one CTA per row, works on the blocks:
-// at most K blocks can hold one of the K largest entries, namely those with the largest
-// maxima (equal maxima: the lower block first, since a lower block holds lower indices,
-// and ties go to the lowest index).  The same argument on the 16-byte words of those
-// blocks leaves at most K words, whose entries are ranked.  Nothing in it depends on how
-// the values are distributed: a constant row costs what any row costs.
+// One kernel.  CTAs stream pieces of the rows: a warp-wide load (32 words of 16 bytes, 512
+// bytes) is a block, and each block leaves its maximum m and s = sum 2^((x - m) log2e / t); the
+// maximum is kept as it is and taken from x before the scaling, so that rows filled with the
+// type's lowest value neither overflow nor vanish.  The CTA that finishes a row's last piece
+// picks: the K largest entries lie in blocks whose maxima are among the K largest, so a
+// bisection over the block maxima that ends as soon as K to K + 32 of them lie above the
+// pivot names the blocks to look at again, and the entries above the pivot (a few more than
+// K as a rule) are ranked.
+// Equal values need care: a row can hold thousands of entries at the pivot.  Where more
+// blocks or entries than there is room for lie at or above it, the choice is made exact:
+// the blocks (then the 16-byte words of those blocks) with the K largest maxima, equal ones by
+// the lower index, since a lower block holds lower indices and ties go to the lowest index.
+// That leaves at most K words, whatever the values.
 //
 // The rest's sum is made of the blocks that were not chosen and the entries of the chosen
 // ones that were not taken; it is never a difference of two sums, so a rest of 1e-12 of
@@ -21,8 +25,10 @@ namespace spec {
 
 constexpr int kTopThreads = 256;
 constexpr int kTopWarps = kTopThreads / 32;
-constexpr int kTopBlocksPerWarp = 8;                              // blocks a warp loads at once
-constexpr int kTopPiece = kTopWarps * kTopBlocksPerWarp;          // blocks of a CTA
+constexpr int kTopBatch = 8;                       // blocks a warp loads at once
+constexpr int kTopSlack = 32;                      // blocks beyond K that the bisection may leave
+constexpr int kTopBlkMax = SPEC_MAX_TEACHER + kTopSlack;
+constexpr int kTopCandMax = SPEC_MAX_TEACHER * 8;  // entries to rank
 
 // Blocks of a row of V entries, whatever its offset in its first word.
 __host__ __device__ inline int top_blocks(int V, int elt_bytes) {
@@ -31,36 +37,74 @@ __host__ __device__ inline int top_blocks(int V, int elt_bytes) {
 }
 
 __device__ __forceinline__ float warp_max_nan(float x) {
+    float r;
+    asm volatile("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// The sums over the warp of eight values per lane, two lanes' halves at a time: lane l ends
+// with the sum of value (l >> 2).
+__device__ __forceinline__ float warp_sum8(float (&v)[8]) {
+    const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) x = f_max_nan(x, __shfl_xor_sync(0xffffffffu, x, o));
-    return x;
+    for (int h = 4, o = 16; h >= 1; h >>= 1, o >>= 1) {
+        const bool up = lane & o;
+#pragma unroll
+        for (int i = 0; i < h; ++i) {
+            const float send = up ? v[i] : v[i + h], keep = up ? v[i + h] : v[i];
+            v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+        }
+    }
+    v[0] += __shfl_xor_sync(0xffffffffu, v[0], 2);
+    v[0] += __shfl_xor_sync(0xffffffffu, v[0], 1);
+    return v[0];
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kTopThreads) top_scan_kernel(TopLogitsParams p) {
+__device__ __forceinline__ void top_pick(const TopLogitsParams& p, int row, uint32_t* s_keys);
+
+// The blocks of one piece, then, in the CTA that finishes its row's last piece, the pick.
+template <typename T>
+__global__ void __launch_bounds__(kTopThreads) top_kernel(TopLogitsParams p) {
     constexpr int E = 16 / (int)sizeof(T);
+    extern __shared__ __align__(16) uint32_t s_keys[];   // [n_blocks]
     const int row = blockIdx.x / p.pieces, piece = blockIdx.x - row * p.pieces;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const RowWords<T> in(reinterpret_cast<const T*>(p.logits) + (long)row * p.ld, p.V);
-    const int blk0 = piece * kTopPiece + warp * kTopBlocksPerWarp;
+    const int blk0 = (piece * kTopWarps + warp) * p.batch;   // batch <= kTopBatch blocks of this warp
     const uint32_t ninf = NegInf<T>::word;
-    uint4 w[kTopBlocksPerWarp];
+    uint4 w[kTopBatch];
 #pragma unroll
-    for (int q = 0; q < kTopBlocksPerWarp; ++q) {
+    for (int q = 0; q < kTopBatch; ++q) {
         const int i = (blk0 + q) * 32 + lane;
-        w[q] = i < in.n ? in.load(i) : make_uint4(ninf, ninf, ninf, ninf);
+        w[q] = q < p.batch && i < in.n ? in.load(i) : make_uint4(ninf, ninf, ninf, ninf);
     }
+    float m[kTopBatch], s[kTopBatch];
 #pragma unroll
-    for (int q = 0; q < kTopBlocksPerWarp; ++q) {
-        const float m = warp_max_nan(u4_max_nan<sizeof(T)>(w[q]));
-        float s = 0.0f;
-        if (m > -INFINITY) {
+    for (int q = 0; q < kTopBatch; ++q) {
+        s[q] = 0.0f;
+        m[q] = -INFINITY;
+        if (q >= p.batch) continue;
+        m[q] = warp_max_nan(u4_max_nan<sizeof(T)>(w[q]));
+        const float ref = m[q] == -INFINITY ? 0.0f : m[q];
+        const f2x mm = f2_pack(-ref, -ref), cc = f2_pack(p.scale, p.scale);
+        f2x acc = f2_pack(0.0f, 0.0f);
 #pragma unroll
-            for (int k = 0; k < E; ++k) s += ex2((word_entry<T>(w[q], k) - m) * p.scale);
-        }
-        s = warp_sum(s);
-        if (lane == 0 && blk0 + q < p.n_blocks) p.blocks[(long)row * p.n_blocks + blk0 + q] = make_float2(m, s);
+        for (int k = 0; k < E; k += 2)
+            acc = f2_add(acc, f2_ex2(f2_mul(f2_add(f2_pack(word_entry<T>(w[q], k), word_entry<T>(w[q], k + 1)), mm), cc)));
+        const float2 a = f2_unpack(acc);
+        s[q] = a.x + a.y;
     }
+    const float sum = warp_sum8(s);
+    const int mine = lane >> 2;
+    float mx = m[0];
+#pragma unroll
+    for (int q = 1; q < kTopBatch; ++q) mx = mine == q ? m[q] : mx;
+    if ((lane & 3) == 0 && mine < p.batch && blk0 + mine < p.n_blocks)
+        __stcg(&p.blocks[(long)row * p.n_blocks + blk0 + mine], make_float2(mx, sum));
+    if (!last_block_done(&p.done[row], (unsigned)p.pieces)) return;
+    if (threadIdx.x == 0) p.done[row] = 0u;
+    top_pick<T>(p, row, s_keys);
 }
 
 // Sum of one int per thread over the CTA; `slot` alternates between calls.
@@ -156,35 +200,69 @@ __device__ __forceinline__ float run_log(const Run& r, float inv_t) {
     return r.s > 0.0f ? fmaf(r.m, inv_t, logf(r.s)) : -INFINITY;
 }
 
+// The indices of keys[0..n) at or above `t`, ascending, in list[] (at most `room`; the caller has
+// counted them).
+__device__ __forceinline__ void list_above(const uint32_t* keys, int n, uint32_t t, int* list, int* s_part, int& slot) {
+    const int per = (n + kTopThreads - 1) / kTopThreads;
+    const int lo = min(n, (int)threadIdx.x * per), hi = min(n, lo + per);
+    int cnt = 0;
+    for (int i = lo; i < hi; ++i) cnt += keys[i] >= t ? 1 : 0;
+    int at = cta_prefix(cnt, s_part, slot);
+    for (int i = lo; i < hi; ++i)
+        if (keys[i] >= t) list[at++] = i;
+    __syncthreads();
+}
+
 template <typename T>
-__global__ void __launch_bounds__(kTopThreads) top_pick_kernel(TopLogitsParams p) {
+__device__ __forceinline__ void top_pick(const TopLogitsParams& p, int row, uint32_t* s_keys) {
     constexpr int E = 16 / (int)sizeof(T);
-    constexpr int KM = SPEC_MAX_TEACHER;
-    extern __shared__ __align__(16) uint8_t s_top[];
-    uint4* s_words = reinterpret_cast<uint4*>(s_top);                                   // [K][32]
-    unsigned long long* s_cand = reinterpret_cast<unsigned long long*>(s_words + p.K * 32);   // [K * 8]
-    uint32_t* s_keys = reinterpret_cast<uint32_t*>(s_cand + p.K * 8);                    // [max(n_blocks, K * 32)]
-    __shared__ int s_blk[KM], s_word[KM], s_part[2 * kTopWarps], s_n, s_bad;
+    __shared__ unsigned long long s_cand[kTopCandMax];
+    __shared__ int s_blk[kTopBlkMax], s_part[2 * kTopWarps], s_n, s_bad;
+    __shared__ uint32_t s_lo, s_hi;
     __shared__ unsigned long long s_kth;
     __shared__ float2 s_run[kTopWarps];
-    const int row = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int K = p.K;
     const RowWords<T> in(reinterpret_cast<const T*>(p.logits) + (long)row * p.ld, p.V);
     const float2* blk = p.blocks + (long)row * p.n_blocks;
     float* values = p.values_out + (long)row * K;
     int32_t* ids = p.ids_out + (long)row * K;
+    const uint32_t ninf = NegInf<T>::word;
+    auto word_at = [&](int b, int l) {   // word l of block b
+        const int i = b * 32 + l;
+        return i < in.n ? in.load(i) : make_uint4(ninf, ninf, ninf, ninf);
+    };
     int slot = 0;
 
-    if (tid == 0) { s_n = 0; s_bad = 0; s_kth = 0ull; }
+    if (tid == 0) {
+        s_n = s_bad = 0;
+        s_kth = 0ull;
+        s_lo = 0xffffffffu;
+        s_hi = 0u;
+    }
     __syncthreads();
     bool bad = false;
+    uint32_t klo = 0xffffffffu, khi = 0u;
+    int cnt = 0;
     for (int i = tid; i < p.n_blocks; i += kTopThreads) {
-        const float m = blk[i].x;
+        const float m = __ldcg(&blk[i]).x;
         bad |= bad_logit(m);
-        s_keys[i] = value_key(m);
+        const uint32_t key = value_key(m);
+        s_keys[i] = key;
+        if (key) {
+            klo = min(klo, key);
+            khi = max(khi, key);
+            ++cnt;
+        }
+    }
+    klo = __reduce_min_sync(0xffffffffu, klo);
+    khi = __reduce_max_sync(0xffffffffu, khi);
+    if (lane == 0) {
+        atomicMin(&s_lo, klo);
+        atomicMax(&s_hi, khi);
     }
     if (bad) s_bad = 1;
-    __syncthreads();
+    int n_above = cta_sum(cnt, s_part, slot);   // blocks with a finite entry
     if (s_bad) {
         for (int k = tid; k < K; k += kTopThreads) { values[k] = NAN; ids[k] = -1; }
         if (tid == 0) {
@@ -194,42 +272,54 @@ __global__ void __launch_bounds__(kTopThreads) top_pick_kernel(TopLogitsParams p
         }
         return;
     }
-    uint32_t floor_key;
-    const int nb = pick_largest(s_keys, p.n_blocks, K, s_blk, floor_key, s_part, slot);
-    // the sum of the blocks that were not chosen
-    Run rest;
-    for (int i = tid; i < p.n_blocks; i += kTopThreads) {
-        int lo = 0, hi = nb;   // is i in the ascending list?
-        while (lo < hi) {
-            const int mid = (lo + hi) >> 1;
-            if (s_blk[mid] < i) lo = mid + 1;
-            else hi = mid;
+    // a pivot with K to K + kTopSlack blocks at or above it; count(lo) = n_above >= K > count(hi)
+    uint32_t lo = n_above ? s_lo : 1u, hi = n_above ? s_hi + 1u : 1u;
+    while (n_above > K + kTopSlack && hi - lo > 1u) {
+        const uint32_t mid = lo + (hi - lo) / 2u;
+        cnt = 0;
+        for (int i = tid; i < p.n_blocks; i += kTopThreads) cnt += s_keys[i] >= mid ? 1 : 0;
+        const int c = cta_sum(cnt, s_part, slot);
+        if (c >= K) { lo = mid; n_above = c; }
+        else hi = mid;
+    }
+    __syncthreads();
+    int nb = n_above;
+    uint32_t floor_key = nb >= K ? lo : 1u;   // fewer than K blocks bound nothing: every finite entry
+    if (n_above <= K + kTopSlack) list_above(s_keys, p.n_blocks, lo, s_blk, s_part, slot);
+    else nb = pick_largest(s_keys, p.n_blocks, K, s_blk, floor_key, s_part, slot);
+
+    // the entries at or above the pivot
+    auto gather = [&](int b, int l, uint32_t least) {
+        const uint4 w = word_at(b, l);
+        const float mx = u4_max_nan<sizeof(T)>(w);
+        if (mx == -INFINITY || value_key(mx) < least) return;
+#pragma unroll
+        for (int k = 0; k < E; ++k) {
+            const float x = word_entry<T>(w, k);
+            if (x > -INFINITY && value_key(x) >= least) {
+                const int at = atomicAdd(&s_n, 1);
+                if (at < kTopCandMax) s_cand[at] = argmax_key(x, (uint32_t)(in.entry(b * 32 + l) + k));
+            }
         }
-        if (lo < nb && s_blk[lo] == i) continue;
-        const float2 ms = blk[i];
-        rest.add(ms.x, ms.y, p.scale);
-    }
+    };
+    for (int q = warp; q < nb; q += kTopWarps) gather(s_blk[q], lane, floor_key);
     __syncthreads();
-    const uint32_t ninf = NegInf<T>::word;
-    for (int q = warp; q < nb; q += kTopWarps) {
-        const int i = s_blk[q] * 32 + lane;
-        const uint4 w = i < in.n ? in.load(i) : make_uint4(ninf, ninf, ninf, ninf);
-        s_words[q * 32 + lane] = w;
-        s_keys[q * 32 + lane] = value_key(u4_max_nan<sizeof(T)>(w));
+    int n = s_n;
+    if (n > kTopCandMax) {
+        // equal values in numbers: the K largest word maxima of (exactly) K blocks
+        __syncthreads();
+        if (nb > K) nb = pick_largest(s_keys, p.n_blocks, K, s_blk, floor_key, s_part, slot);
+        __syncthreads();
+        uint32_t* s_wkeys = s_keys + p.n_blocks;   // [K * 32]
+        int* s_word = reinterpret_cast<int*>(s_wkeys + K * 32);   // [K]
+        for (int q = warp; q < nb; q += kTopWarps) s_wkeys[q * 32 + lane] = value_key(u4_max_nan<sizeof(T)>(word_at(s_blk[q], lane)));
+        if (tid == 0) s_n = 0;
+        __syncthreads();
+        const int nw = pick_largest(s_wkeys, nb * 32, K, s_word, floor_key, s_part, slot);
+        for (int i = tid; i < nw; i += kTopThreads) gather(s_blk[s_word[i] >> 5], s_word[i] & 31, floor_key);
+        __syncthreads();
+        n = s_n;
     }
-    __syncthreads();
-    const int nw = pick_largest(s_keys, nb * 32, K, s_word, floor_key, s_part, slot);
-    for (int i = tid; i < nw * E; i += kTopThreads) {
-        const int q = s_word[i / E], k = i % E;
-        const float x = word_entry<T>(s_words[q], k);
-        const uint32_t vk = value_key(x);
-        if (vk != 0u && vk >= floor_key) {
-            const int e = in.entry(s_blk[q >> 5] * 32 + (q & 31)) + k;
-            s_cand[atomicAdd(&s_n, 1)] = argmax_key(x, (uint32_t)e);
-        }
-    }
-    __syncthreads();
-    const int n = s_n;
     for (int i = tid; i < n; i += kTopThreads) {
         const unsigned long long key = s_cand[i];
         int rank = 0;
@@ -243,12 +333,25 @@ __global__ void __launch_bounds__(kTopThreads) top_pick_kernel(TopLogitsParams p
     for (int k = n + tid; k < K; k += kTopThreads) { values[k] = -INFINITY; ids[k] = -1; }
     __syncthreads();
     const unsigned long long kth = s_kth;   // 0 when every finite entry was taken
-    Run taken;
-    for (int i = tid; i < nb * 32; i += kTopThreads) {
-        const int e = in.entry(s_blk[i >> 5] * 32 + (i & 31));
+    // the rest: blocks not looked at again, and the entries of the others that were not taken
+    Run rest, taken;
+    for (int i = tid; i < p.n_blocks; i += kTopThreads) {
+        int a = 0, b = nb;   // is i in the ascending list?
+        while (a < b) {
+            const int mid = (a + b) >> 1;
+            if (s_blk[mid] < i) a = mid + 1;
+            else b = mid;
+        }
+        if (a < nb && s_blk[a] == i) continue;
+        const float2 ms = __ldcg(&blk[i]);
+        rest.add(ms.x, ms.y, p.scale);
+    }
+    for (int q = warp; q < nb; q += kTopWarps) {
+        const uint4 w = word_at(s_blk[q], lane);
+        const int e = in.entry(s_blk[q] * 32 + lane);
 #pragma unroll
         for (int k = 0; k < E; ++k) {
-            const float x = word_entry<T>(s_words[i], k);
+            const float x = word_entry<T>(w, k);
             if (argmax_key(x, (uint32_t)(e + k)) >= kth) taken.add(x, 1.0f, p.scale);
             else rest.add(x, 1.0f, p.scale);
         }
@@ -263,30 +366,36 @@ __global__ void __launch_bounds__(kTopThreads) top_pick_kernel(TopLogitsParams p
     }
 }
 
+static size_t align256(size_t n) { return (n + 255) / 256 * 256; }
+
 size_t top_logits_workspace_bytes(int rows, int V) {
-    return kWsHeaderBytes + (size_t)rows * top_blocks(V, 4) * sizeof(float2);
+    return kWsHeaderBytes + align256((size_t)rows * sizeof(unsigned)) + (size_t)rows * top_blocks(V, 4) * sizeof(float2);
 }
 
 template <typename T>
 static cudaError_t top_launch(TopLogitsParams p, cudaStream_t stream) {
     p.n_blocks = top_blocks(p.V, sizeof(T));
-    p.pieces = (p.n_blocks + kTopPiece - 1) / kTopPiece;
+    // a warp's blocks: eight (the most loads in flight) unless that leaves SMs without a CTA
+    p.batch = kTopBatch;
+    while (p.batch > 1 && (long)p.rows * ((p.n_blocks + kTopWarps * p.batch - 1) / (kTopWarps * p.batch)) < device_sm_count())
+        p.batch /= 2;
+    p.pieces = (p.n_blocks + kTopWarps * p.batch - 1) / (kTopWarps * p.batch);
     const long grid = (long)p.rows * p.pieces;
     if (grid > 0x7fffffffL) return cudaErrorInvalidConfiguration;
-    top_scan_kernel<T><<<(unsigned)grid, kTopThreads, 0, stream>>>(p);
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    const int nkeys = p.n_blocks > p.K * 32 ? p.n_blocks : p.K * 32;
-    const size_t smem = (size_t)p.K * 32 * 16 + (size_t)p.K * 8 * 8 + (size_t)nkeys * 4;
-    const cudaError_t a = cudaFuncSetAttribute(top_pick_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (a != cudaSuccess) return a;
-    top_pick_kernel<T><<<p.rows, kTopThreads, smem, stream>>>(p);
+    const size_t smem = ((size_t)p.n_blocks + (size_t)p.K * 33) * 4;
+    if (smem > 32 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(top_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+    }
+    top_kernel<T><<<(unsigned)grid, kTopThreads, smem, stream>>>(p);
     return cudaGetLastError();
 }
 
 cudaError_t top_logits_launch(TopLogitsParams p, void* ws, cudaStream_t stream) {
     p.status = &reinterpret_cast<WsHeader*>(ws)->status;
-    p.blocks = reinterpret_cast<float2*>(reinterpret_cast<uint8_t*>(ws) + kWsHeaderBytes);
+    uint8_t* b = reinterpret_cast<uint8_t*>(ws) + kWsHeaderBytes;
+    p.done = reinterpret_cast<unsigned*>(b);
+    p.blocks = reinterpret_cast<float2*>(b + align256((size_t)p.rows * sizeof(unsigned)));
     return p.dtype == SPEC_BF16 ? top_launch<bf16_t>(p, stream) : top_launch<float>(p, stream);
 }
 
