@@ -60,6 +60,7 @@ __device__ __forceinline__ float warp_sum8(float (&v)[8]) {
     return v[0];
 }
 
+// s_keys: the blocks' keys [n_blocks] and sums [n_blocks], then room for 33 words per entry.
 template <typename T>
 __device__ __forceinline__ void top_pick(const TopLogitsParams& p, int row, uint32_t* s_keys);
 
@@ -67,7 +68,7 @@ __device__ __forceinline__ void top_pick(const TopLogitsParams& p, int row, uint
 template <typename T>
 __global__ void __launch_bounds__(kTopThreads) top_kernel(TopLogitsParams p) {
     constexpr int E = 16 / (int)sizeof(T);
-    extern __shared__ __align__(16) uint32_t s_keys[];   // [n_blocks]
+    extern __shared__ __align__(16) uint32_t s_keys[];
     const int row = blockIdx.x / p.pieces, piece = blockIdx.x - row * p.pieces;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const RowWords<T> in(reinterpret_cast<const T*>(p.logits) + (long)row * p.ld, p.V);
@@ -184,6 +185,22 @@ struct Run {
         m = x;
     }
 };
+// Every entry of a word with maximum mx.
+template <typename T>
+__device__ __forceinline__ void run_word(Run& r, const uint4& w, float mx, float c) {
+    if (mx == -INFINITY) return;
+    if (mx > r.m) {
+        r.s = r.m == -INFINITY ? 0.0f : r.s * ex2((r.m - mx) * c);
+        r.m = mx;
+    }
+    const f2x mm = f2_pack(-r.m, -r.m), cc = f2_pack(c, c);
+    f2x acc = f2_pack(r.s, 0.0f);
+#pragma unroll
+    for (int k = 0; k < 16 / (int)sizeof(T); k += 2)
+        acc = f2_add(acc, f2_ex2(f2_mul(f2_add(f2_pack(word_entry<T>(w, k), word_entry<T>(w, k + 1)), mm), cc)));
+    const float2 a = f2_unpack(acc);
+    r.s = a.x + a.y;
+}
 // The CTA's total, in every thread.
 __device__ __forceinline__ Run run_cta(Run r, float c, float2* s_run) {
     const float M = warp_max(r.m);
@@ -232,6 +249,7 @@ __device__ __forceinline__ void top_pick(const TopLogitsParams& p, int row, uint
         const int i = b * 32 + l;
         return i < in.n ? in.load(i) : make_uint4(ninf, ninf, ninf, ninf);
     };
+    float* s_sums = reinterpret_cast<float*>(s_keys + p.n_blocks);
     int slot = 0;
 
     if (tid == 0) {
@@ -245,10 +263,11 @@ __device__ __forceinline__ void top_pick(const TopLogitsParams& p, int row, uint
     uint32_t klo = 0xffffffffu, khi = 0u;
     int cnt = 0;
     for (int i = tid; i < p.n_blocks; i += kTopThreads) {
-        const float m = __ldcg(&blk[i]).x;
-        bad |= bad_logit(m);
-        const uint32_t key = value_key(m);
+        const float2 ms = __ldcg(&blk[i]);
+        bad |= bad_logit(ms.x);
+        const uint32_t key = value_key(ms.x);
         s_keys[i] = key;
+        s_sums[i] = ms.y;
         if (key) {
             klo = min(klo, key);
             khi = max(khi, key);
@@ -272,51 +291,84 @@ __device__ __forceinline__ void top_pick(const TopLogitsParams& p, int row, uint
         }
         return;
     }
-    // a pivot with K to K + kTopSlack blocks at or above it; count(lo) = n_above >= K > count(hi)
+    // a pivot with K to K + kTopSlack blocks at or above it: count(lo) = n_above >= K > count(hi),
+    // the range cut to a quarter at a time
     uint32_t lo = n_above ? s_lo : 1u, hi = n_above ? s_hi + 1u : 1u;
     while (n_above > K + kTopSlack && hi - lo > 1u) {
-        const uint32_t mid = lo + (hi - lo) / 2u;
-        cnt = 0;
-        for (int i = tid; i < p.n_blocks; i += kTopThreads) cnt += s_keys[i] >= mid ? 1 : 0;
-        const int c = cta_sum(cnt, s_part, slot);
-        if (c >= K) { lo = mid; n_above = c; }
-        else hi = mid;
+        const uint32_t d = (hi - lo) / 4u;
+        const uint32_t t1 = d ? lo + d : lo + 1u, t2 = d ? t1 + d : t1, t3 = d ? t2 + d : t1;
+        int c12 = 0, c3 = 0;
+        for (int i = tid; i < p.n_blocks; i += kTopThreads) {
+            const uint32_t key = s_keys[i];
+            c12 += (key >= t1 ? 1 : 0) + (key >= t2 ? 65536 : 0);
+            c3 += key >= t3 ? 1 : 0;
+        }
+        c12 = cta_sum(c12, s_part, slot);
+        c3 = cta_sum(c3, s_part, slot);
+        const int c1 = c12 & 0xffff, c2 = c12 >> 16;
+        if (c3 >= K) { lo = t3; n_above = c3; }
+        else if (c2 >= K) { lo = t2; n_above = c2; hi = t3; }
+        else if (c1 >= K) { lo = t1; n_above = c1; hi = t2; }
+        else hi = t1;
     }
     __syncthreads();
     int nb = n_above;
+    const bool exact_blocks = n_above > K + kTopSlack;
     uint32_t floor_key = nb >= K ? lo : 1u;   // fewer than K blocks bound nothing: every finite entry
-    if (n_above <= K + kTopSlack) list_above(s_keys, p.n_blocks, lo, s_blk, s_part, slot);
+    if (!exact_blocks) list_above(s_keys, p.n_blocks, lo, s_blk, s_part, slot);
     else nb = pick_largest(s_keys, p.n_blocks, K, s_blk, floor_key, s_part, slot);
 
-    // the entries at or above the pivot
-    auto gather = [&](int b, int l, uint32_t least) {
-        const uint4 w = word_at(b, l);
+    // the chosen blocks once more: entries at or above the pivot are candidates, the others
+    // belong to the rest
+    Run rest, taken;
+    auto gather = [&](int b, int l, const uint4& w, uint32_t least, bool count_rest) {
         const float mx = u4_max_nan<sizeof(T)>(w);
-        if (mx == -INFINITY || value_key(mx) < least) return;
+        if (mx == -INFINITY) return;
+        if (value_key(mx) < least) {
+            if (count_rest) run_word<T>(rest, w, mx, p.scale);
+            return;
+        }
 #pragma unroll
         for (int k = 0; k < E; ++k) {
             const float x = word_entry<T>(w, k);
             if (x > -INFINITY && value_key(x) >= least) {
                 const int at = atomicAdd(&s_n, 1);
                 if (at < kTopCandMax) s_cand[at] = argmax_key(x, (uint32_t)(in.entry(b * 32 + l) + k));
+            } else if (count_rest) {
+                rest.add(x, 1.0f, p.scale);
             }
         }
     };
-    for (int q = warp; q < nb; q += kTopWarps) gather(s_blk[q], lane, floor_key);
+    auto over_blocks = [&](auto&& body) {   // a warp's share of the chosen blocks, four loads at a time
+        for (int q0 = warp; q0 < nb; q0 += 4 * kTopWarps) {
+            uint4 w[4];
+#pragma unroll
+            for (int h = 0; h < 4; ++h)
+                if (q0 + h * kTopWarps < nb) w[h] = word_at(s_blk[q0 + h * kTopWarps], lane);
+#pragma unroll
+            for (int h = 0; h < 4; ++h)
+                if (q0 + h * kTopWarps < nb) body(q0 + h * kTopWarps, w[h]);
+        }
+    };
+    over_blocks([&](int q, const uint4& w) { gather(s_blk[q], lane, w, floor_key, true); });
     __syncthreads();
     int n = s_n;
-    if (n > kTopCandMax) {
+    const bool exact_words = n > kTopCandMax;
+    if (exact_words) {
         // equal values in numbers: the K largest word maxima of (exactly) K blocks
         __syncthreads();
         if (nb > K) nb = pick_largest(s_keys, p.n_blocks, K, s_blk, floor_key, s_part, slot);
         __syncthreads();
-        uint32_t* s_wkeys = s_keys + p.n_blocks;   // [K * 32]
+        uint32_t* s_wkeys = s_keys + 2 * p.n_blocks;              // [K * 32]
         int* s_word = reinterpret_cast<int*>(s_wkeys + K * 32);   // [K]
-        for (int q = warp; q < nb; q += kTopWarps) s_wkeys[q * 32 + lane] = value_key(u4_max_nan<sizeof(T)>(word_at(s_blk[q], lane)));
+        over_blocks([&](int q, const uint4& w) { s_wkeys[q * 32 + lane] = value_key(u4_max_nan<sizeof(T)>(w)); });
         if (tid == 0) s_n = 0;
         __syncthreads();
         const int nw = pick_largest(s_wkeys, nb * 32, K, s_word, floor_key, s_part, slot);
-        for (int i = tid; i < nw; i += kTopThreads) gather(s_blk[s_word[i] >> 5], s_word[i] & 31, floor_key);
+        for (int i = tid; i < nw; i += kTopThreads) {
+            const int b = s_blk[s_word[i] >> 5], l = s_word[i] & 31;
+            gather(b, l, word_at(b, l), floor_key, false);
+        }
         __syncthreads();
         n = s_n;
     }
@@ -324,37 +376,43 @@ __device__ __forceinline__ void top_pick(const TopLogitsParams& p, int row, uint
         const unsigned long long key = s_cand[i];
         int rank = 0;
         for (int j = 0; j < n; ++j) rank += s_cand[j] > key ? 1 : 0;
+        const float x = key_value(key);
         if (rank < K) {
-            values[rank] = key_value(key);
+            values[rank] = x;
             ids[rank] = (int)key_index(key);
             if (rank == K - 1) s_kth = key;
+            taken.add(x, 1.0f, p.scale);
+        } else if (!exact_words) {
+            rest.add(x, 1.0f, p.scale);
         }
     }
     for (int k = n + tid; k < K; k += kTopThreads) { values[k] = -INFINITY; ids[k] = -1; }
-    __syncthreads();
-    const unsigned long long kth = s_kth;   // 0 when every finite entry was taken
-    // the rest: blocks not looked at again, and the entries of the others that were not taken
-    Run rest, taken;
-    for (int i = tid; i < p.n_blocks; i += kTopThreads) {
-        int a = 0, b = nb;   // is i in the ascending list?
-        while (a < b) {
-            const int mid = (a + b) >> 1;
-            if (s_blk[mid] < i) a = mid + 1;
-            else b = mid;
-        }
-        if (a < nb && s_blk[a] == i) continue;
-        const float2 ms = __ldcg(&blk[i]);
-        rest.add(ms.x, ms.y, p.scale);
-    }
-    for (int q = warp; q < nb; q += kTopWarps) {
-        const uint4 w = word_at(s_blk[q], lane);
-        const int e = in.entry(s_blk[q] * 32 + lane);
+    if (exact_words) {   // the chosen blocks' entries that were not taken, over again
+        __syncthreads();
+        const unsigned long long kth = s_kth;   // 0 when every finite entry was taken
+        rest = Run();
+        over_blocks([&](int q, const uint4& w) {
+            const int e = in.entry(s_blk[q] * 32 + lane);
 #pragma unroll
-        for (int k = 0; k < E; ++k) {
-            const float x = word_entry<T>(w, k);
-            if (argmax_key(x, (uint32_t)(e + k)) >= kth) taken.add(x, 1.0f, p.scale);
-            else rest.add(x, 1.0f, p.scale);
+            for (int k = 0; k < E; ++k) {
+                const float x = word_entry<T>(w, k);
+                if (argmax_key(x, (uint32_t)(e + k)) < kth) rest.add(x, 1.0f, p.scale);
+            }
+        });
+    }
+    // the blocks that were not looked at again
+    for (int i = tid; i < p.n_blocks; i += kTopThreads) {
+        bool chosen = s_keys[i] >= lo;
+        if (exact_blocks || exact_words) {   // is i in the ascending list?
+            int a = 0, b = nb;
+            while (a < b) {
+                const int mid = (a + b) >> 1;
+                if (s_blk[mid] < i) a = mid + 1;
+                else b = mid;
+            }
+            chosen = a < nb && s_blk[a] == i;
         }
+        if (!chosen && s_keys[i]) rest.add(order_float(s_keys[i]), s_sums[i], p.scale);
     }
     const Run r = run_cta(rest, p.scale, s_run);
     Run a = run_cta(taken, p.scale, s_run);
@@ -382,7 +440,7 @@ static cudaError_t top_launch(TopLogitsParams p, cudaStream_t stream) {
     p.pieces = (p.n_blocks + kTopWarps * p.batch - 1) / (kTopWarps * p.batch);
     const long grid = (long)p.rows * p.pieces;
     if (grid > 0x7fffffffL) return cudaErrorInvalidConfiguration;
-    const size_t smem = ((size_t)p.n_blocks + (size_t)p.K * 33) * 4;
+    const size_t smem = ((size_t)p.n_blocks * 2 + (size_t)p.K * 33) * 4;
     if (smem > 32 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(top_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
