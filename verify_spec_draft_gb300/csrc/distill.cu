@@ -61,16 +61,7 @@ __global__ void __launch_bounds__(kDistThreads) distill_scan_kernel(DistillParam
     for (int q = 0; q < kDistWords; ++q) {
         const int at = (q * kDistThreads + tid) * E;
         const uint32_t named = (s_named[at >> 5] >> (at & 31)) & ((1u << E) - 1u);
-        if (named) {
-            uint32_t h[4] = {w[q].x, w[q].y, w[q].z, w[q].w};
-#pragma unroll
-            for (int k = 0; k < E; ++k) {
-                if (!((named >> k) & 1u)) continue;
-                if (sizeof(T) == 2) h[k >> 1] = (h[k >> 1] & ((k & 1) ? 0x0000ffffu : 0xffff0000u)) | ((k & 1) ? 0xff800000u : 0xff80u);
-                else h[k & 3] = 0xff800000u;
-            }
-            w[q] = make_uint4(h[0], h[1], h[2], h[3]);
-        }
+        if (named) w[q] = word_without<T>(w[q], named);
         m = f_max_nan(m, u4_max_nan<sizeof(T)>(w[q]));
     }
     // a NaN or +inf shows in the maximum

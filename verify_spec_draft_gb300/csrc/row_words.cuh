@@ -77,6 +77,19 @@ __device__ __forceinline__ float word_entry(const uint4& w, int k) {
     return __uint_as_float(h[k & 3]);
 }
 
+// -inf in the entries of a word whose bit is set.
+template <typename T>
+__device__ __forceinline__ uint4 word_without(const uint4& w, uint32_t bits) {
+    uint32_t h[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int k = 0; k < 16 / (int)sizeof(T); ++k) {
+        if (!((bits >> k) & 1u)) continue;
+        if (sizeof(T) == 2) h[k >> 1] = (k & 1) ? (h[k >> 1] & 0xffffu) | 0xff800000u : (h[k >> 1] & 0xffff0000u) | 0xff80u;
+        else h[k & 3] = 0xff800000u;
+    }
+    return make_uint4(h[0], h[1], h[2], h[3]);
+}
+
 // E floats rounded (to nearest even for bf16) into a word.
 template <typename T>
 __device__ __forceinline__ uint4 word_of(const float (&x)[16 / sizeof(T)]) {

@@ -175,6 +175,11 @@ __device__ __forceinline__ int pick_largest(const uint32_t* keys, int n, int K, 
 // A key that is 0 for -inf and grows with the value otherwise.
 __device__ __forceinline__ uint32_t value_key(float x) { return x > -INFINITY ? float_order(x) : 0u; }
 
+// The least value with at least this key.
+__device__ __forceinline__ float key_floor(uint32_t key) {
+    return key < float_order(-3.402823466e38f) ? -3.402823466e38f : order_float(key);
+}
+
 // Running maximum m and s = sum w 2^((x - m) c).
 struct Run {
     float m = -INFINITY, s = 0.0f;
@@ -201,32 +206,46 @@ __device__ __forceinline__ void run_word(Run& r, const uint4& w, float mx, float
     const float2 a = f2_unpack(acc);
     r.s = a.x + a.y;
 }
-// The CTA's total, in every thread.
-__device__ __forceinline__ Run run_cta(Run r, float c, float2* s_run) {
-    const float M = warp_max(r.m);
-    const float s = warp_sum(r.m == -INFINITY ? 0.0f : r.s * ex2((r.m - M) * c));
+// The CTA's totals of two runs, in the first warp.
+__device__ __forceinline__ void runs_cta(Run& x, Run& y, float c, float4* s_run) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const float mx = warp_max(x.m), my = warp_max(y.m);
+    const float sx = warp_sum(x.m == -INFINITY ? 0.0f : x.s * ex2((x.m - mx) * c));
+    const float sy = warp_sum(y.m == -INFINITY ? 0.0f : y.s * ex2((y.m - my) * c));
+    if (lane == 0) s_run[warp] = make_float4(mx, sx, my, sy);
     __syncthreads();
-    if ((threadIdx.x & 31) == 0) s_run[threadIdx.x >> 5] = make_float2(M, s);
-    __syncthreads();
-    Run t;
-    for (int i = 0; i < kTopWarps; ++i) t.add(s_run[i].x, s_run[i].y, c);
-    return t;
+    if (warp != 0) return;
+    const float4 v = lane < kTopWarps ? s_run[lane] : make_float4(-INFINITY, 0.0f, -INFINITY, 0.0f);
+    x.m = warp_max(v.x);
+    y.m = warp_max(v.z);
+    x.s = warp_sum(v.x == -INFINITY ? 0.0f : v.y * ex2((v.x - x.m) * c));
+    y.s = warp_sum(v.z == -INFINITY ? 0.0f : v.w * ex2((v.z - y.m) * c));
 }
 // ln of the sum
 __device__ __forceinline__ float run_log(const Run& r, float inv_t) {
     return r.s > 0.0f ? fmaf(r.m, inv_t, logf(r.s)) : -INFINITY;
 }
 
-// The indices of keys[0..n) at or above `t`, ascending, in list[] (at most `room`; the caller has
-// counted them).
-__device__ __forceinline__ void list_above(const uint32_t* keys, int n, uint32_t t, int* list, int* s_part, int& slot) {
-    const int per = (n + kTopThreads - 1) / kTopThreads;
-    const int lo = min(n, (int)threadIdx.x * per), hi = min(n, lo + per);
+// The indices of keys[0..n) at or above `t` in list[], in an order that depends on them alone.
+__device__ __forceinline__ void list_above(const uint32_t* keys, int n, uint32_t t, int* list, int* s_part) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int cnt = 0;
-    for (int i = lo; i < hi; ++i) cnt += keys[i] >= t ? 1 : 0;
-    int at = cta_prefix(cnt, s_part, slot);
-    for (int i = lo; i < hi; ++i)
-        if (keys[i] >= t) list[at++] = i;
+    for (int i0 = 0; i0 < n; i0 += kTopThreads) {
+        const int i = i0 + threadIdx.x;
+        cnt += __popc(__ballot_sync(0xffffffffu, i < n && keys[i] >= t));
+    }
+    __syncthreads();
+    if (lane == 0) s_part[warp] = cnt;
+    __syncthreads();
+    int at = 0;
+    for (int i = 0; i < warp; ++i) at += s_part[i];
+    for (int i0 = 0; i0 < n; i0 += kTopThreads) {
+        const int i = i0 + threadIdx.x;
+        const bool in = i < n && keys[i] >= t;
+        const unsigned who = __ballot_sync(0xffffffffu, in);
+        if (in) list[at + __popc(who & ((1u << lane) - 1u))] = i;
+        at += __popc(who);
+    }
     __syncthreads();
 }
 
@@ -234,10 +253,12 @@ template <typename T>
 __device__ __forceinline__ void top_pick(const TopLogitsParams& p, int row, uint32_t* s_keys) {
     constexpr int E = 16 / (int)sizeof(T);
     __shared__ unsigned long long s_cand[kTopCandMax];
+    __shared__ float s_sorted[kTopCandMax];
+    __shared__ int s_rank[kTopCandMax];
     __shared__ int s_blk[kTopBlkMax], s_part[2 * kTopWarps], s_n, s_bad;
     __shared__ uint32_t s_lo, s_hi;
     __shared__ unsigned long long s_kth;
-    __shared__ float2 s_run[kTopWarps];
+    __shared__ float4 s_run[kTopWarps];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int K = p.K;
     const RowWords<T> in(reinterpret_cast<const T*>(p.logits) + (long)row * p.ld, p.V);
@@ -315,29 +336,30 @@ __device__ __forceinline__ void top_pick(const TopLogitsParams& p, int row, uint
     int nb = n_above;
     const bool exact_blocks = n_above > K + kTopSlack;
     uint32_t floor_key = nb >= K ? lo : 1u;   // fewer than K blocks bound nothing: every finite entry
-    if (!exact_blocks) list_above(s_keys, p.n_blocks, lo, s_blk, s_part, slot);
+    if (!exact_blocks) list_above(s_keys, p.n_blocks, lo, s_blk, s_part);
     else nb = pick_largest(s_keys, p.n_blocks, K, s_blk, floor_key, s_part, slot);
 
     // the chosen blocks once more: entries at or above the pivot are candidates, the others
     // belong to the rest
     Run rest, taken;
-    auto gather = [&](int b, int l, const uint4& w, uint32_t least, bool count_rest) {
-        const float mx = u4_max_nan<sizeof(T)>(w);
-        if (mx == -INFINITY) return;
-        if (value_key(mx) < least) {
-            if (count_rest) run_word<T>(rest, w, mx, p.scale);
-            return;
-        }
+    auto gather = [&](int b, int l, uint4 w, float least, bool count_rest) {
+        float mx = u4_max_nan<sizeof(T)>(w);
+        if (mx >= least) {
+            uint32_t above = 0u;
 #pragma unroll
-        for (int k = 0; k < E; ++k) {
-            const float x = word_entry<T>(w, k);
-            if (x > -INFINITY && value_key(x) >= least) {
-                const int at = atomicAdd(&s_n, 1);
-                if (at < kTopCandMax) s_cand[at] = argmax_key(x, (uint32_t)(in.entry(b * 32 + l) + k));
-            } else if (count_rest) {
-                rest.add(x, 1.0f, p.scale);
-            }
+            for (int k = 0; k < E; ++k) above |= word_entry<T>(w, k) >= least ? 1u << k : 0u;
+            const int at = atomicAdd(&s_n, __popc(above));
+            int h = 0;
+#pragma unroll
+            for (int k = 0; k < E; ++k)
+                if ((above >> k) & 1u) {
+                    if (at + h < kTopCandMax) s_cand[at + h] = argmax_key(word_entry<T>(w, k), (uint32_t)(in.entry(b * 32 + l) + k));
+                    ++h;
+                }
+            w = word_without<T>(w, above);
+            mx = u4_max_nan<sizeof(T)>(w);
         }
+        if (count_rest) run_word<T>(rest, w, mx, p.scale);
     };
     auto over_blocks = [&](auto&& body) {   // a warp's share of the chosen blocks, four loads at a time
         for (int q0 = warp; q0 < nb; q0 += 4 * kTopWarps) {
@@ -350,14 +372,16 @@ __device__ __forceinline__ void top_pick(const TopLogitsParams& p, int row, uint
                 if (q0 + h * kTopWarps < nb) body(q0 + h * kTopWarps, w[h]);
         }
     };
-    over_blocks([&](int q, const uint4& w) { gather(s_blk[q], lane, w, floor_key, true); });
+    // (a key of 1 stands for the lowest float: every finite entry)
+    over_blocks([&](int q, const uint4& w) { gather(s_blk[q], lane, w, key_floor(floor_key), true); });
     __syncthreads();
     int n = s_n;
     const bool exact_words = n > kTopCandMax;
     if (exact_words) {
-        // equal values in numbers: the K largest word maxima of (exactly) K blocks
+        // equal values in numbers: the K largest word maxima of (exactly) K blocks, in the
+        // blocks' order
         __syncthreads();
-        if (nb > K) nb = pick_largest(s_keys, p.n_blocks, K, s_blk, floor_key, s_part, slot);
+        if (!exact_blocks) nb = pick_largest(s_keys, p.n_blocks, K, s_blk, floor_key, s_part, slot);
         __syncthreads();
         uint32_t* s_wkeys = s_keys + 2 * p.n_blocks;              // [K * 32]
         int* s_word = reinterpret_cast<int*>(s_wkeys + K * 32);   // [K]
@@ -367,28 +391,43 @@ __device__ __forceinline__ void top_pick(const TopLogitsParams& p, int row, uint
         const int nw = pick_largest(s_wkeys, nb * 32, K, s_word, floor_key, s_part, slot);
         for (int i = tid; i < nw; i += kTopThreads) {
             const int b = s_blk[s_word[i] >> 5], l = s_word[i] & 31;
-            gather(b, l, word_at(b, l), floor_key, false);
+            gather(b, l, word_at(b, l), key_floor(floor_key), false);
         }
         __syncthreads();
         n = s_n;
     }
-    for (int i = tid; i < n; i += kTopThreads) {
+    // ranks, a candidate's comparisons shared by two threads
+    for (int i = tid; i < n; i += kTopThreads) s_rank[i] = 0;
+    __syncthreads();
+    constexpr int kHalf = kTopThreads / 2;
+    const int j0 = tid < kHalf ? 0 : n / 2, j1 = tid < kHalf ? n / 2 : n;
+    for (int i = tid & (kHalf - 1); i < n; i += kHalf) {
         const unsigned long long key = s_cand[i];
         int rank = 0;
-        for (int j = 0; j < n; ++j) rank += s_cand[j] > key ? 1 : 0;
+#pragma unroll 8
+        for (int j = j0; j < j1; ++j) rank += s_cand[j] > key ? 1 : 0;
+        atomicAdd(&s_rank[i], rank);
+    }
+    __syncthreads();
+    for (int i = tid; i < n; i += kTopThreads) {
+        const unsigned long long key = s_cand[i];
+        const int rank = s_rank[i];
         const float x = key_value(key);
+        s_sorted[rank] = x;
         if (rank < K) {
             values[rank] = x;
             ids[rank] = (int)key_index(key);
             if (rank == K - 1) s_kth = key;
-            taken.add(x, 1.0f, p.scale);
-        } else if (!exact_words) {
-            rest.add(x, 1.0f, p.scale);
         }
+    }
+    __syncthreads();
+    // summed in the order of their ranks: the candidates came in any order
+    for (int i = tid; i < n; i += kTopThreads) {
+        if (i < K) taken.add(s_sorted[i], 1.0f, p.scale);
+        else if (!exact_words) rest.add(s_sorted[i], 1.0f, p.scale);
     }
     for (int k = n + tid; k < K; k += kTopThreads) { values[k] = -INFINITY; ids[k] = -1; }
     if (exact_words) {   // the chosen blocks' entries that were not taken, over again
-        __syncthreads();
         const unsigned long long kth = s_kth;   // 0 when every finite entry was taken
         rest = Run();
         over_blocks([&](int q, const uint4& w) {
@@ -414,13 +453,12 @@ __device__ __forceinline__ void top_pick(const TopLogitsParams& p, int row, uint
         }
         if (!chosen && s_keys[i]) rest.add(order_float(s_keys[i]), s_sums[i], p.scale);
     }
-    const Run r = run_cta(rest, p.scale, s_run);
-    Run a = run_cta(taken, p.scale, s_run);
+    runs_cta(rest, taken, p.scale, s_run);
     if (tid == 0) {
-        p.tail_out[row] = run_log(r, p.inv_t);
-        a.add(r.m, r.s, p.scale);
-        if (p.lse_out) p.lse_out[row] = run_log(a, p.inv_t);
-        if (!(a.s > 0.0f)) atomicOr(p.status, SPEC_DEV_NONFINITE);   // no finite entry
+        p.tail_out[row] = run_log(rest, p.inv_t);
+        taken.add(rest.m, rest.s, p.scale);
+        if (p.lse_out) p.lse_out[row] = run_log(taken, p.inv_t);
+        if (!(taken.s > 0.0f)) atomicOr(p.status, SPEC_DEV_NONFINITE);   // no finite entry
     }
 }
 
