@@ -255,6 +255,7 @@ struct TopLogitsParams {
     // chosen at launch
     int n_blocks, pieces;
     int batch;                 // blocks of a warp
+    int pick_apart;            // the picks are a launch of their own
     unsigned* done;            // [rows] pieces finished (0 between calls)
     float2* blocks;            // [rows, n_blocks] (maximum, sum)
 };

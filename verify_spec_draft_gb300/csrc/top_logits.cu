@@ -28,6 +28,7 @@ constexpr int kTopWarps = kTopThreads / 32;
 constexpr int kTopBatch = 8;                       // blocks a warp loads at once
 constexpr int kTopSlack = 32;                      // blocks beyond K that the bisection may leave
 constexpr int kTopBlkMax = SPEC_MAX_TEACHER + kTopSlack;
+constexpr int kTopApart = 32;                      // rows from which the picks are a launch of their own
 constexpr int kTopCandMax = SPEC_MAX_TEACHER * 8;  // entries to rank
 
 // Blocks of a row of V entries, whatever its offset in its first word.
@@ -103,9 +104,21 @@ __global__ void __launch_bounds__(kTopThreads) top_kernel(TopLogitsParams p) {
     for (int q = 1; q < kTopBatch; ++q) mx = mine == q ? m[q] : mx;
     if ((lane & 3) == 0 && mine < p.batch && blk0 + mine < p.n_blocks)
         __stcg(&p.blocks[(long)row * p.n_blocks + blk0 + mine], make_float2(mx, sum));
+    if (p.pick_apart) {
+        pdl_launch_dependents();
+        return;
+    }
     if (!last_block_done(&p.done[row], (unsigned)p.pieces)) return;
     if (threadIdx.x == 0) p.done[row] = 0u;
     top_pick<T>(p, row, s_keys);
+}
+
+// The picks of all rows, launched behind the scan as its programmatic dependent.
+template <typename T>
+__global__ void __launch_bounds__(kTopThreads) top_pick_kernel(TopLogitsParams p) {
+    extern __shared__ __align__(16) uint32_t s_keys[];
+    pdl_wait_primary();
+    top_pick<T>(p, blockIdx.x, s_keys);
 }
 
 // Sum of one int per thread over the CTA; `slot` alternates between calls.
@@ -479,12 +492,26 @@ static cudaError_t top_launch(TopLogitsParams p, cudaStream_t stream) {
     const long grid = (long)p.rows * p.pieces;
     if (grid > 0x7fffffffL) return cudaErrorInvalidConfiguration;
     const size_t smem = ((size_t)p.n_blocks * 2 + (size_t)p.K * 33) * 4;
-    if (smem > 32 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(top_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    p.pick_apart = p.rows >= kTopApart;
+    if (smem > 28 * 1024) {
+        const void* kern = p.pick_apart ? (const void*)top_pick_kernel<T> : (const void*)top_kernel<T>;
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
     }
-    top_kernel<T><<<(unsigned)grid, kTopThreads, smem, stream>>>(p);
-    return cudaGetLastError();
+    top_kernel<T><<<(unsigned)grid, kTopThreads, p.pick_apart ? 0 : smem, stream>>>(p);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess || !p.pick_apart) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)p.rows);
+    cfg.blockDim = dim3(kTopThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, top_pick_kernel<T>, p);
 }
 
 cudaError_t top_logits_launch(TopLogitsParams p, void* ws, cudaStream_t stream) {
