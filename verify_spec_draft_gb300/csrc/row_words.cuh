@@ -77,6 +77,15 @@ __device__ __forceinline__ float word_entry(const uint4& w, int k) {
     return __uint_as_float(h[k & 3]);
 }
 
+// The same for a k known at run time only.
+template <typename T>
+__device__ __forceinline__ float word_pick(const uint4& w, int k) {
+    const int r = sizeof(T) == 2 ? k >> 1 : k;
+    const uint32_t h = (r & 2) ? ((r & 1) ? w.w : w.z) : ((r & 1) ? w.y : w.x);
+    if (sizeof(T) == 2) return __uint_as_float((k & 1) ? (h & 0xffff0000u) : (h << 16));
+    return __uint_as_float(h);
+}
+
 // -inf in the entries of a word whose bit is set.
 template <typename T>
 __device__ __forceinline__ uint4 word_without(const uint4& w, uint32_t bits) {

@@ -203,21 +203,24 @@ struct Run {
         m = x;
     }
 };
-// Every entry of a word with maximum mx.
-template <typename T>
-__device__ __forceinline__ void run_word(Run& r, const uint4& w, float mx, float c) {
-    if (mx == -INFINITY) return;
+// Every entry of N words with maximum mx.
+template <typename T, int N>
+__device__ __forceinline__ void run_words(Run& r, const uint4 (&w)[N], float mx, float c) {
     if (mx > r.m) {
         r.s = r.m == -INFINITY ? 0.0f : r.s * ex2((r.m - mx) * c);
         r.m = mx;
     }
-    const f2x mm = f2_pack(-r.m, -r.m), cc = f2_pack(c, c);
-    f2x acc = f2_pack(r.s, 0.0f);
+    const float ref = r.m == -INFINITY ? 0.0f : r.m;
+    const f2x mm = f2_pack(-ref, -ref), cc = f2_pack(c, c);
+    f2x acc[2] = {f2_pack(r.s, 0.0f), f2_pack(0.0f, 0.0f)};
 #pragma unroll
-    for (int k = 0; k < 16 / (int)sizeof(T); k += 2)
-        acc = f2_add(acc, f2_ex2(f2_mul(f2_add(f2_pack(word_entry<T>(w, k), word_entry<T>(w, k + 1)), mm), cc)));
-    const float2 a = f2_unpack(acc);
-    r.s = a.x + a.y;
+    for (int h = 0; h < N; ++h)
+#pragma unroll
+        for (int k = 0; k < 16 / (int)sizeof(T); k += 2)
+            acc[(k >> 1) & 1] = f2_add(acc[(k >> 1) & 1],
+                f2_ex2(f2_mul(f2_add(f2_pack(word_entry<T>(w[h], k), word_entry<T>(w[h], k + 1)), mm), cc)));
+    const float2 x = f2_unpack(acc[0]), y = f2_unpack(acc[1]);
+    r.s = (x.x + x.y) + (y.x + y.y);
 }
 // The CTA's totals of two runs, in the first warp.
 __device__ __forceinline__ void runs_cta(Run& x, Run& y, float c, float4* s_run) {
@@ -355,38 +358,41 @@ __device__ __forceinline__ void top_pick(const TopLogitsParams& p, int row, uint
     // the chosen blocks once more: entries at or above the pivot are candidates, the others
     // belong to the rest
     Run rest, taken;
-    auto gather = [&](int b, int l, uint4 w, float least, bool count_rest) {
-        float mx = u4_max_nan<sizeof(T)>(w);
-        if (mx >= least) {
-            uint32_t above = 0u;
+    // word l of block b: its entries from `least` on are pushed; the word without them
+    auto push = [&](int b, int l, const uint4& w, float least) {
+        uint32_t above = 0u;
 #pragma unroll
-            for (int k = 0; k < E; ++k) above |= word_entry<T>(w, k) >= least ? 1u << k : 0u;
-            const int at = atomicAdd(&s_n, __popc(above));
-            int h = 0;
-#pragma unroll
-            for (int k = 0; k < E; ++k)
-                if ((above >> k) & 1u) {
-                    if (at + h < kTopCandMax) s_cand[at + h] = argmax_key(word_entry<T>(w, k), (uint32_t)(in.entry(b * 32 + l) + k));
-                    ++h;
-                }
-            w = word_without<T>(w, above);
-            mx = u4_max_nan<sizeof(T)>(w);
+        for (int k = 0; k < E; ++k) above |= word_entry<T>(w, k) >= least ? 1u << k : 0u;
+        int at = atomicAdd(&s_n, __popc(above));
+        for (uint32_t a = above; a; a &= a - 1u, ++at) {
+            const int k = __ffs(a) - 1;
+            if (at < kTopCandMax) s_cand[at] = argmax_key(word_pick<T>(w, k), (uint32_t)(in.entry(b * 32 + l) + k));
         }
-        if (count_rest) run_word<T>(rest, w, mx, p.scale);
+        return word_without<T>(w, above);
     };
     auto over_blocks = [&](auto&& body) {   // a warp's share of the chosen blocks, four loads at a time
         for (int q0 = warp; q0 < nb; q0 += 4 * kTopWarps) {
             uint4 w[4];
 #pragma unroll
             for (int h = 0; h < 4; ++h)
-                if (q0 + h * kTopWarps < nb) w[h] = word_at(s_blk[q0 + h * kTopWarps], lane);
-#pragma unroll
-            for (int h = 0; h < 4; ++h)
-                if (q0 + h * kTopWarps < nb) body(q0 + h * kTopWarps, w[h]);
+                w[h] = q0 + h * kTopWarps < nb ? word_at(s_blk[q0 + h * kTopWarps], lane) : make_uint4(ninf, ninf, ninf, ninf);
+            body(q0, w);
         }
     };
-    // (a key of 1 stands for the lowest float: every finite entry)
-    over_blocks([&](int q, const uint4& w) { gather(s_blk[q], lane, w, key_floor(floor_key), true); });
+    const float least = key_floor(floor_key);   // (a key of 1 stands for the lowest float: every finite entry)
+    over_blocks([&](int q0, uint4 (&w)[4]) {
+        float mx = -INFINITY;
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+            float wm = u4_max_nan<sizeof(T)>(w[h]);
+            if (wm >= least) {
+                w[h] = push(s_blk[q0 + h * kTopWarps], lane, w[h], least);
+                wm = u4_max_nan<sizeof(T)>(w[h]);
+            }
+            mx = fmaxf(mx, wm);
+        }
+        run_words<T, 4>(rest, w, mx, p.scale);
+    });
     __syncthreads();
     int n = s_n;
     const bool exact_words = n > kTopCandMax;
@@ -398,13 +404,16 @@ __device__ __forceinline__ void top_pick(const TopLogitsParams& p, int row, uint
         __syncthreads();
         uint32_t* s_wkeys = s_keys + 2 * p.n_blocks;              // [K * 32]
         int* s_word = reinterpret_cast<int*>(s_wkeys + K * 32);   // [K]
-        over_blocks([&](int q, const uint4& w) { s_wkeys[q * 32 + lane] = value_key(u4_max_nan<sizeof(T)>(w)); });
+        over_blocks([&](int q0, uint4 (&w)[4]) {
+            for (int h = 0; h < 4 && q0 + h * kTopWarps < nb; ++h)
+                s_wkeys[(q0 + h * kTopWarps) * 32 + lane] = value_key(u4_max_nan<sizeof(T)>(w[h]));
+        });
         if (tid == 0) s_n = 0;
         __syncthreads();
         const int nw = pick_largest(s_wkeys, nb * 32, K, s_word, floor_key, s_part, slot);
         for (int i = tid; i < nw; i += kTopThreads) {
             const int b = s_blk[s_word[i] >> 5], l = s_word[i] & 31;
-            gather(b, l, word_at(b, l), key_floor(floor_key), false);
+            push(b, l, word_at(b, l), key_floor(floor_key));
         }
         __syncthreads();
         n = s_n;
@@ -443,13 +452,20 @@ __device__ __forceinline__ void top_pick(const TopLogitsParams& p, int row, uint
     if (exact_words) {   // the chosen blocks' entries that were not taken, over again
         const unsigned long long kth = s_kth;   // 0 when every finite entry was taken
         rest = Run();
-        over_blocks([&](int q, const uint4& w) {
-            const int e = in.entry(s_blk[q] * 32 + lane);
+        over_blocks([&](int q0, uint4 (&w)[4]) {
+            float mx = -INFINITY;
 #pragma unroll
-            for (int k = 0; k < E; ++k) {
-                const float x = word_entry<T>(w, k);
-                if (argmax_key(x, (uint32_t)(e + k)) < kth) rest.add(x, 1.0f, p.scale);
+            for (int h = 0; h < 4; ++h) {
+                if (q0 + h * kTopWarps >= nb) continue;
+                const int e = in.entry(s_blk[q0 + h * kTopWarps] * 32 + lane);
+                uint32_t taken_bits = 0u;
+#pragma unroll
+                for (int k = 0; k < E; ++k)
+                    taken_bits |= argmax_key(word_entry<T>(w[h], k), (uint32_t)(e + k)) >= kth ? 1u << k : 0u;
+                w[h] = word_without<T>(w[h], taken_bits);
+                mx = fmaxf(mx, u4_max_nan<sizeof(T)>(w[h]));
             }
+            run_words<T, 4>(rest, w, mx, p.scale);
         });
     }
     // the blocks that were not looked at again
