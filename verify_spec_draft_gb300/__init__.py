@@ -158,25 +158,41 @@ def _need_rows(t, name, device=None):
         raise ValueError(f"{name} must be a CUDA tensor (the library has no CPU path)")
     if device is not None and t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if t.dim() < 2:
+    shape = t.shape
+    if len(shape) < 2:
         raise ValueError(f"{name} must be at least [rows, V]")
-    V, ld, rows = t.shape[-1], 0, 1
-    if V > 1 and t.stride(-1) != 1:
+    V, ld, rows, strides = shape[-1], 0, 1, t.stride()
+    if strides[-1] == 1 and strides[-2] == V and (len(shape) == 2 or (len(shape) == 3 and strides[0] == shape[1] * V)):
+        return V   # contiguous: nothing more to look at
+    if V > 1 and strides[-1] != 1:
         raise ValueError(f"{name} must have its entries next to one another (stride 1)")
-    for n, st in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+    for n, st in zip(reversed(shape[:-1]), reversed(strides[:-1])):
         if n == 1:
             continue
         if ld == 0:
             ld = st // rows if st % rows == 0 else 0
         if ld < V or st != rows * ld:
-            raise ValueError(f"{name} must have evenly spaced rows at least V entries apart, got strides {t.stride()}")
+            raise ValueError(f"{name} must have evenly spaced rows at least V entries apart, got strides {strides}")
         rows *= n
     return ld or V
 
 
+def _addr(t, name, device, dtype, shape):
+    """The address of an optional contiguous tensor, checked as _need does (which says what
+    is wrong); None for None."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+        _need(t, name, device, dtype, shape)
+    return t.data_ptr()
+
+
+_HERE = contextlib.nullcontext()
+
+
 def _made_on(stream):
     """What a call allocates belongs to the stream it runs on."""
-    return contextlib.nullcontext() if stream is None else _torch().cuda.stream(stream)
+    return _HERE if stream is None else _torch().cuda.stream(stream)
 
 
 def _rows_like(t, ld):
@@ -184,12 +200,12 @@ def _rows_like(t, ld):
     torch = _torch()
     V = t.shape[-1]
     if ld == V:
-        return torch.empty(t.shape, dtype=t.dtype, device=t.device)
+        return torch.empty_like(t, memory_format=torch.contiguous_format)
     return torch.empty((*t.shape[:-1], ld), dtype=t.dtype, device=t.device)[..., :V]
 
 
 def _need_same_rows(t, name, like, ld):
-    if t.dtype != like.dtype or tuple(t.shape) != tuple(like.shape):
+    if t.dtype is not like.dtype or t.shape != like.shape:
         raise ValueError(f"{name} must be {like.dtype} {tuple(like.shape)}, got {t.dtype} {tuple(t.shape)}")
     if _need_rows(t, name, like.device) != ld and t.numel() > t.shape[-1]:
         raise ValueError(f"{name} must have the row stride {ld}")
@@ -583,55 +599,49 @@ def process_logits(logits, history=None, lengths=None, prompt_lengths=None, bloc
     but logits may be None.  ``out=dict(logits=...)`` may be logits itself.  Returns a dict
     of device tensors: logits."""
     torch = _torch()
-    lib = load()
+    lib = _lib or load()
     ld = _need_rows(logits, "logits")
     if logits.dim() != 3:
         raise ValueError("logits must be [B, R, V]")
-    dev = logits.device
+    dev, i32, f32 = logits.device, torch.int32, torch.float32
     B, R, V = logits.shape
-    Lmax = 0
+    Lmax = nb = 0
     if history is not None:
-        _need(history, "history", dev, torch.int32)
-        if history.dim() != 2 or history.shape[0] != B:
+        if history.dim() != 2:
             raise ValueError(f"history must be [{B}, Lmax], got {tuple(history.shape)}")
         Lmax = history.shape[1]
-    for t, name in ((lengths, "lengths"), (prompt_lengths, "prompt_lengths")):
-        if t is not None:
-            _need(t, name, dev, torch.int32, (B,))
-    if block is not None:
-        _need(block, "block", dev, torch.int32, (B, R - 1))
-    for t, name in ((repetition, "repetition"), (frequency, "frequency"), (presence, "presence"),
-                    (temperature, "temperature")):
-        if t is not None:
-            _need(t, name, dev, torch.float32, (B,))
-    nb = 0
     if (bias_ids is None) != (bias_values is None):
         raise ValueError("bias_ids and bias_values go together")
     if bias_ids is not None:
-        _need(bias_ids, "bias_ids", dev, torch.int32)
-        if bias_ids.dim() != 2 or bias_ids.shape[0] != B:
+        if bias_ids.dim() != 2:
             raise ValueError(f"bias_ids must be [{B}, n], got {tuple(bias_ids.shape)}")
         nb = bias_ids.shape[1]
-        _need(bias_values, "bias_values", dev, torch.float32, (B, nb))
-    mask_rows = 1
-    if mask is not None:
-        W = (V + 31) // 32
-        if mask.dim() == 3:
-            mask_rows = R
-        _need(mask, "mask", dev, torch.int32, (B, R, W) if mask.dim() == 3 else (B, W))
+    W = (V + 31) // 32
+    mask_rows, masks = (R, (B, R, W)) if mask is not None and mask.dim() == 3 else (1, (B, W))
+    a_hist = _addr(history, "history", dev, i32, (B, Lmax))
+    a_block = _addr(block, "block", dev, i32, (B, R - 1))
+    a_ids = _addr(bias_ids, "bias_ids", dev, i32, (B, nb))
+    a_values = _addr(bias_values, "bias_values", dev, f32, (B, nb))
+    a_mask = _addr(mask, "mask", dev, i32, masks)
+    per = (B,)
+    args = (_addr(lengths, "lengths", dev, i32, per), _addr(prompt_lengths, "prompt_lengths", dev, i32, per),
+            a_block if R > 1 else None, _addr(repetition, "repetition", dev, f32, per),
+            _addr(frequency, "frequency", dev, f32, per), _addr(presence, "presence", dev, f32, per),
+            _addr(temperature, "temperature", dev, f32, per))
     if out is None:
         with _made_on(stream):
             out = dict(logits=_rows_like(logits, ld))
-    _need_same_rows(out["logits"], "out", logits, ld)
+    else:
+        _need_same_rows(out["logits"], "out", logits, ld)
     if ws is None:
         with _made_on(stream):
             ws = workspace(OP_PROCESS_LOGITS, B, R, V, 0, dev, stream)
     code = lib.spec_process_logits(
-        _ptr(logits), _dtype_code(logits), B, R, V, ld, _ptr(history if Lmax else None), Lmax, _ptr(lengths),
-        _ptr(prompt_lengths), _ptr(block if R > 1 else None), _ptr(repetition), _ptr(frequency), _ptr(presence),
-        _ptr(temperature), _ptr(bias_ids if nb else None), _ptr(bias_values if nb else None), nb, _ptr(mask),
-        mask_rows, _ptr(out["logits"]), _ptr(ws), ws.numel(), _stream(stream))
-    _check(code, "spec_process_logits")
+        logits.data_ptr(), _dtype_code(logits), B, R, V, ld, a_hist if Lmax else None, Lmax, *args,
+        a_ids if nb else None, a_values if nb else None, nb, a_mask, mask_rows, out["logits"].data_ptr(),
+        ws.data_ptr(), ws.numel(), _stream(stream))
+    if code != OK:
+        raise SpecError(code, "spec_process_logits")
     out["ws"] = ws
     return out
 
@@ -641,24 +651,27 @@ def top_logits(logits, k, temperature=1.0, ws=None, out=None, stream=None):
     Returns a dict of device tensors: values float32 and ids int32 [..., k], tail and lse
     float32 [...]."""
     torch = _torch()
-    lib = load()
+    lib = _lib or load()
     ld = _need_rows(logits, "logits")
-    dev = logits.device
-    lead, V, k = tuple(logits.shape[:-1]), logits.shape[-1], int(k)
+    dev, shape, k = logits.device, logits.shape, int(k)
+    lead, V = shape[:-1], shape[-1]
     rows = logits.numel() // V if V else 0
     if out is None:
         with _made_on(stream):
-            out = dict(values=torch.empty((*lead, max(k, 0)), dtype=torch.float32, device=dev),
-                       ids=torch.empty((*lead, max(k, 0)), dtype=torch.int32, device=dev),
+            sized = (*lead, max(k, 0))
+            out = dict(values=torch.empty(sized, dtype=torch.float32, device=dev),
+                       ids=torch.empty(sized, dtype=torch.int32, device=dev),
                        tail=torch.empty(lead, dtype=torch.float32, device=dev),
                        lse=torch.empty(lead, dtype=torch.float32, device=dev))
     if ws is None:
         with _made_on(stream):
             ws = workspace(OP_TOP_LOGITS, rows, k, V, 0, dev, stream)
-    code = lib.spec_top_logits(_ptr(logits), _dtype_code(logits), rows, V, ld, k, float(temperature),
-                               _ptr(out["values"]), _ptr(out["ids"]), _ptr(out["tail"]), _ptr(out.get("lse")),
-                               _ptr(ws), ws.numel(), _stream(stream))
-    _check(code, "spec_top_logits")
+    lse = out.get("lse")
+    code = lib.spec_top_logits(logits.data_ptr(), _dtype_code(logits), rows, V, ld, k, float(temperature),
+                               out["values"].data_ptr(), out["ids"].data_ptr(), out["tail"].data_ptr(),
+                               None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream))
+    if code != OK:
+        raise SpecError(code, "spec_top_logits")
     out["ws"] = ws
     return out
 
@@ -670,33 +683,34 @@ def distill(student, values, ids, tail=None, weight=None, temperature=1.0, grad=
     of device tensors: loss and lse float32 [...] and, with ``grad``, grad of the student's
     type and layout (``out["grad"]`` may be student itself)."""
     torch = _torch()
-    lib = load()
+    lib = _lib or load()
     ld = _need_rows(student, "student")
-    dev = student.device
-    lead, V = tuple(student.shape[:-1]), student.shape[-1]
+    dev, shape = student.device, student.shape
+    lead, V = shape[:-1], shape[-1]
     rows = student.numel() // V if V else 0
-    _need(ids, "ids", dev, torch.int32)
-    K = ids.shape[-1] if ids.dim() else 0
-    _need(ids, "ids", dev, torch.int32, (*lead, K))
-    _need(values, "values", dev, None, (*lead, K))
-    for t, name in ((tail, "tail"), (weight, "weight")):
-        if t is not None:
-            _need(t, name, dev, torch.float32, lead)
+    K = ids.shape[-1] if ids is not None and ids.dim() else 0
+    named = (*lead, K)
+    a_ids = _addr(_need(ids, "ids"), "ids", dev, torch.int32, named)
+    a_values = _addr(_need(values, "values"), "values", dev, values.dtype, named)
+    a_tail = _addr(tail, "tail", dev, torch.float32, lead)
+    a_weight = _addr(weight, "weight", dev, torch.float32, lead)
     if out is None:
         with _made_on(stream):
             out = dict(loss=torch.empty(lead, dtype=torch.float32, device=dev),
                        lse=torch.empty(lead, dtype=torch.float32, device=dev))
             if grad:
                 out["grad"] = _rows_like(student, ld)
-    if grad:
+    elif grad:
         _need_same_rows(out["grad"], "grad", student, ld)
     if ws is None:
         with _made_on(stream):
             ws = workspace(OP_DISTILL, rows, K, V, 0, dev, stream)
-    code = lib.spec_distill(_ptr(student), _dtype_code(student), rows, V, ld, _ptr(values), _dtype_code(values),
-                            _ptr(ids), K, _ptr(tail), _ptr(weight), float(temperature), _ptr(out["loss"]),
-                            _ptr(out.get("lse")), _ptr(out["grad"] if grad else None), _ptr(ws), ws.numel(),
-                            _stream(stream))
-    _check(code, "spec_distill")
+    lse = out.get("lse")
+    code = lib.spec_distill(student.data_ptr(), _dtype_code(student), rows, V, ld, a_values, _dtype_code(values),
+                            a_ids, K, a_tail, a_weight, float(temperature), out["loss"].data_ptr(),
+                            None if lse is None else lse.data_ptr(), out["grad"].data_ptr() if grad else None,
+                            ws.data_ptr(), ws.numel(), _stream(stream))
+    if code != OK:
+        raise SpecError(code, "spec_distill")
     out["ws"] = ws
     return out
