@@ -29,18 +29,75 @@ __host__ __device__ inline int distill_pieces(int V, int elt_bytes) {
     return ((V + 2 * E - 2) / E + kDistPiece - 1) / kDistPiece;
 }
 
-// Statistics of the entries that no id names, per piece.
+__device__ __forceinline__ float warp_max_nan(float x) {
+    float r;
+    asm volatile("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+    return r;
+}
+// (maximum, sum of 2^((x - maximum) c)) pairs merged over the N lanes that differ in their
+// low bits; NaN shows in the maximum.
+template <int N>
+__device__ __forceinline__ float2 stat_lanes(float2 v, float c) {
+    float m = v.x;
+#pragma unroll
+    for (int o = N / 2; o > 0; o >>= 1) m = f_max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+    float s = v.x == -INFINITY ? 0.0f : v.y * ex2((v.x - m) * c);
+#pragma unroll
+    for (int o = N / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    return make_float2(m, s);
+}
+__device__ __forceinline__ float2 stat_merge(float2 a, float2 b, float c) {
+    const float m = f_max_nan(a.x, b.x);
+    float s = 0.0f;
+    if (a.x != -INFINITY) s += a.y * ex2((a.x - m) * c);
+    if (b.x != -INFINITY) s += b.y * ex2((b.x - m) * c);
+    return make_float2(m, s);
+}
+
+constexpr uint32_t kBadToken = 0x7fc0dead;   // a NaN that says: an id is listed twice
+
+// A teacher entry's logarithm and share, and the loss from them.  `top`, P: the teacher's
+// normaliser, in units of 1; M, Z: the student's, in units of t; mT, sT: that of its
+// unnamed entries.
+struct RowStats { float M, Z, mT, sT, top, P; };
+__device__ __forceinline__ float entry_loss(const RowStats& r, float a, float z, float inv_t) {
+    const float lt = fmaf(a, inv_t, -r.top), pk = __expf(lt) / r.P;
+    return pk > 0.0f ? pk * ((lt - logf(r.P)) - ((z - r.M) * inv_t - logf(r.Z))) : 0.0f;
+}
+__device__ __forceinline__ float rest_loss(const RowStats& r, float aT, float inv_t) {
+    const float pT = __expf(aT - r.top) / r.P;
+    if (!(pT > 0.0f)) return 0.0f;
+    const float lq = r.mT > -INFINITY ? fmaf(r.mT - r.M, inv_t, logf(r.sT)) - logf(r.Z) : -INFINITY;
+    return pT * (((aT - r.top) - logf(r.P)) - lq);
+}
+
+// ---------------------------------------------------------------------------------
+// The loss alone: rows streamed once in pieces, (maximum, sum) of the entries that no id
+// names per piece; the CTA that finishes a row's last piece forms the loss.
+// ---------------------------------------------------------------------------------
 template <typename T>
-__global__ void __launch_bounds__(kDistThreads) distill_scan_kernel(DistillParams p) {
+__device__ __forceinline__ void distill_finish(const DistillParams& p, int row, float wt, int id);
+
+template <typename T>
+__global__ void __launch_bounds__(kDistThreads) distill_loss_kernel(DistillParams p) {
     constexpr int E = 16 / (int)sizeof(T);
     __shared__ uint32_t s_named[kDistPiece * E / 32];
     __shared__ float2 s_run[kDistWarps];
+    __shared__ int s_twice;
     const int row = blockIdx.x / p.pieces, piece = blockIdx.x - row * p.pieces;
-    if (p.weight && p.weight[row] == 0.0f) return;
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const float wt = p.weight ? p.weight[row] : 1.0f;
+    if (wt == 0.0f) {   // the row does not count and is not read
+        if (piece == 0 && tid == 0) {
+            p.loss_out[row] = 0.0f;
+            if (p.lse_out) p.lse_out[row] = 0.0f;
+        }
+        return;
+    }
     const RowWords<T> in(reinterpret_cast<const T*>(p.student) + (long)row * p.ld, p.V);
     const int w0 = piece * kDistPiece;
     const uint32_t ninf = NegInf<T>::word;
+    const int id = tid < p.K ? p.ids[(long)row * p.K + tid] : -1;
     uint4 w[kDistWords];
 #pragma unroll
     for (int q = 0; q < kDistWords; ++q) {
@@ -48,126 +105,103 @@ __global__ void __launch_bounds__(kDistThreads) distill_scan_kernel(DistillParam
         w[q] = i < in.n ? in.load(i) : make_uint4(ninf, ninf, ninf, ninf);
     }
     for (int i = tid; i < kDistPiece * E / 32; i += kDistThreads) s_named[i] = 0u;
+    if (tid == 0) s_twice = 0;
     __syncthreads();
-    const int e0 = in.entry(w0);
-    for (int k = tid; k < p.K; k += kDistThreads) {
-        const int id = p.ids[(long)row * p.K + k];
-        const unsigned at = (unsigned)(id - e0);
-        if (id >= 0 && id < p.V && at < (unsigned)(kDistPiece * E)) atomicOr(&s_named[at >> 5], 1u << (at & 31));
-    }
+    const unsigned at = (unsigned)(id - in.entry(w0));
+    if (id >= 0 && id < p.V && at < (unsigned)(kDistPiece * E) &&
+        (atomicOr(&s_named[at >> 5], 1u << (at & 31)) >> (at & 31)) & 1u)
+        s_twice = 1;
     __syncthreads();
     float m = -INFINITY;
 #pragma unroll
     for (int q = 0; q < kDistWords; ++q) {
-        const int at = (q * kDistThreads + tid) * E;
-        const uint32_t named = (s_named[at >> 5] >> (at & 31)) & ((1u << E) - 1u);
+        const int l = (q * kDistThreads + tid) * E;
+        const uint32_t named = (s_named[l >> 5] >> (l & 31)) & ((1u << E) - 1u);
         if (named) w[q] = word_without<T>(w[q], named);
         m = f_max_nan(m, u4_max_nan<sizeof(T)>(w[q]));
     }
-    // a NaN or +inf shows in the maximum
-    float s = 0.0f;
-    if (m > -INFINITY) {
+    m = warp_max_nan(m);   // a NaN or +inf shows in the maximum
+    const float ref = m == -INFINITY ? 0.0f : m;
+    const f2x mm = f2_pack(-ref, -ref), cc = f2_pack(p.scale, p.scale);
+    f2x acc[2] = {f2_pack(0.0f, 0.0f), f2_pack(0.0f, 0.0f)};
 #pragma unroll
-        for (int q = 0; q < kDistWords; ++q)
+    for (int q = 0; q < kDistWords; ++q)
 #pragma unroll
-            for (int k = 0; k < E; ++k) s += ex2((word_entry<T>(w[q], k) - m) * p.scale);
+        for (int k = 0; k < E; k += 2)
+            acc[(k >> 1) & 1] = f2_add(acc[(k >> 1) & 1],
+                f2_ex2(f2_mul(f2_add(f2_pack(word_entry<T>(w[q], k), word_entry<T>(w[q], k + 1)), mm), cc)));
+    const float2 a0 = f2_unpack(acc[0]), a1 = f2_unpack(acc[1]);
+    const float s = warp_sum((a0.x + a0.y) + (a1.x + a1.y));
+    if (lane == 0) s_run[tid >> 5] = make_float2(m, s);
+    __syncthreads();
+    if (tid < 32) {
+        float2 t = stat_lanes<kDistWarps>(s_run[lane % kDistWarps], p.scale);
+        if (s_twice) t.x = __uint_as_float(kBadToken);
+        if (lane == 0) __stcg(&p.parts[(long)row * p.pieces + piece], t);
     }
-    float M = m;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = f_max_nan(M, __shfl_xor_sync(0xffffffffu, M, o));
-    s = warp_sum(m == -INFINITY ? 0.0f : s * ex2((m - M) * p.scale));
-    if ((tid & 31) == 0) s_run[tid >> 5] = make_float2(M, s);
-    __syncthreads();
-    if (tid == 0) {
-        float CM = -INFINITY, cs = 0.0f;
-        for (int i = 0; i < kDistWarps; ++i) CM = f_max_nan(CM, s_run[i].x);
-        for (int i = 0; i < kDistWarps; ++i)
-            if (s_run[i].x != -INFINITY) cs += s_run[i].y * ex2((s_run[i].x - CM) * p.scale);
-        p.parts[(long)row * p.pieces + piece] = make_float2(CM, cs);
-    }
-}
-
-// One CTA per row: merges the pieces, forms the loss and what the gradient needs.
-__device__ __forceinline__ float cta_max_nan(float x, float* s_f) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) x = f_max_nan(x, __shfl_xor_sync(0xffffffffu, x, o));
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) s_f[threadIdx.x >> 5] = x;
-    __syncthreads();
-    x = s_f[0];
-    for (int i = 1; i < SPEC_MAX_TEACHER / 32; ++i) x = f_max_nan(x, s_f[i]);
-    return x;
-}
-__device__ __forceinline__ float cta_sum_f(float x, float* s_f) {
-    x = warp_sum(x);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) s_f[threadIdx.x >> 5] = x;
-    __syncthreads();
-    x = s_f[0];
-    for (int i = 1; i < SPEC_MAX_TEACHER / 32; ++i) x += s_f[i];
-    return x;
+    if (!last_block_done(&p.done[row], (unsigned)p.pieces)) return;
+    if (tid == 0) p.done[row] = 0u;
+    distill_finish<T>(p, row, wt, id);
 }
 
 template <typename T>
-__global__ void __launch_bounds__(SPEC_MAX_TEACHER) distill_finish_kernel(DistillParams p) {
-    __shared__ float s_f[SPEC_MAX_TEACHER / 32];
-    __shared__ int s_id[SPEC_MAX_TEACHER];
-    const int row = blockIdx.x, tid = threadIdx.x;
-    const float wt = p.weight ? p.weight[row] : 1.0f;
-    if (wt == 0.0f) {   // the row does not count and is not read
-        if (tid == 0) {
-            p.loss_out[row] = 0.0f;
-            if (p.lse_out) p.lse_out[row] = 0.0f;
-        }
-        return;
-    }
-    const T* zr = reinterpret_cast<const T*>(p.student) + (long)row * p.ld;
-    int id = -1;
-    float a = -INFINITY, z = -INFINITY;
-    if (tid < p.K) {
+__device__ __forceinline__ void distill_finish(const DistillParams& p, int row, float wt, int id) {
+    __shared__ float2 s_tail[kDistWarps], s_top[kDistWarps], s_teach[kDistWarps];
+    __shared__ float s_loss[kDistWarps];
+    __shared__ int s_flag;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const float2 none = make_float2(-INFINITY, 0.0f);
+    const bool there = id >= 0 && id < p.V;
+    float z = -INFINITY, a = -INFINITY;
+    if (there) {
+        const T* src = reinterpret_cast<const T*>(p.student) + (long)row * p.ld + id;
+        z = load_one(src);
         const long at = (long)row * p.K + tid;
-        id = p.ids[at];
         a = p.values_dtype == SPEC_BF16 ? to_float(reinterpret_cast<const bf16_t*>(p.values)[at])
                                         : reinterpret_cast<const float*>(p.values)[at];
     }
-    s_id[tid] = id;
-    __syncthreads();
-    bool bad_id = id < -1 || id >= p.V;
-    if (id >= 0)
-        for (int k = 0; k < tid; ++k) bad_id |= s_id[k] == id;
-    if (id < 0 || bad_id) a = -INFINITY;
-    else z = to_float(zr[id]);
-    const float at = p.tail ? p.tail[row] : -INFINITY;
-    const int nbad = __syncthreads_count(bad_id);
-    // student
-    float m = z;
-    for (int i = tid; i < p.pieces; i += SPEC_MAX_TEACHER) m = f_max_nan(m, p.parts[(long)row * p.pieces + i].x);
-    const float M = cta_max_nan(m, s_f);
-    float ss = 0.0f;
-    for (int i = tid; i < p.pieces; i += SPEC_MAX_TEACHER) {
-        const float2 ms = p.parts[(long)row * p.pieces + i];
-        if (ms.x != -INFINITY) ss += ms.y * ex2((ms.x - M) * p.scale);
+    const float aT = p.tail ? p.tail[row] : -INFINITY;
+    int flag = id < -1 || id >= p.V ? 1 : 0;
+    float2 t = none;
+    for (int i = tid; i < p.pieces; i += kDistThreads) {
+        const float2 v = __ldcg(&p.parts[(long)row * p.pieces + i]);
+        if (__float_as_uint(v.x) == kBadToken) flag |= 1;
+        t = stat_merge(t, v, p.scale);
     }
-    const bool no_row = !(M < INFINITY) || M == -INFINITY;
-    const float qe = no_row ? 0.0f : ex2((z - M) * p.scale);   // 0 for an absent entry
-    const float ST = cta_sum_f(ss, s_f);
-    const float Z = ST + cta_sum_f(qe, s_f);
-    // teacher, in units of 1 (the tail's)
-    const float top = cta_max_nan(f_max_nan(a * p.inv_t, at), s_f);
-    const bool taught = top != -INFINITY, bad_row = no_row || !(top < INFINITY) || !(fabsf(wt) < INFINITY);
-    const float ak = taught ? fmaf(a, p.inv_t, -top) : -INFINITY, aT = taught ? at - top : -INFINITY;
-    const float P = cta_sum_f(__expf(ak), s_f) + __expf(aT);
-    const float lP = logf(P), lZ = logf(Z);
-    const float pk = taught ? __expf(ak) / P : 0.0f, pT = taught ? __expf(aT) / P : 0.0f;
-    float l = pk > 0.0f ? pk * ((ak - lP) - ((z - M) * p.inv_t - lZ)) : 0.0f;
-    if (tid == 0 && pT > 0.0f) l += pT * ((aT - lP) - (logf(ST) - lZ));
-    const float loss = cta_sum_f(l, s_f);
-    const bool bad = bad_row || nbad > 0;
+    if (!(a * p.inv_t < INFINITY) || !(aT < INFINITY) || !(fabsf(wt) < INFINITY)) flag |= 2;
+    if (tid == 0) s_flag = 0;
+    t = stat_lanes<32>(t, p.scale);
+    const float2 n = stat_lanes<32>(make_float2(z, 1.0f), p.scale);
+    const float2 y = stat_lanes<32>(make_float2(a * p.inv_t, 1.0f), kLog2e);
+    if (lane == 0) {
+        s_tail[warp] = t;
+        s_top[warp] = n;
+        s_teach[warp] = y;
+    }
+    __syncthreads();
+    if (flag) atomicOr(&s_flag, flag);
+    // every warp puts the whole together
+    const float2 T2 = stat_lanes<kDistWarps>(s_tail[lane % kDistWarps], p.scale);
+    const float2 A = stat_merge(T2, stat_lanes<kDistWarps>(s_top[lane % kDistWarps], p.scale), p.scale);
+    const float2 N = stat_merge(stat_lanes<kDistWarps>(s_teach[lane % kDistWarps], kLog2e),
+                                aT == -INFINITY ? none : make_float2(aT, 1.0f), kLog2e);
+    const RowStats r = {A.x, A.y, T2.x, T2.y, N.x, N.y};
+    float l = 0.0f;
+    if (r.top > -INFINITY) {
+        if (there) l = entry_loss(r, a, z, p.inv_t);
+        if (tid == 0) l += rest_loss(r, aT, p.inv_t);
+    }
+    l = warp_sum(l);
+    if (lane == 0) s_loss[warp] = l;
+    __syncthreads();
     if (tid == 0) {
-        p.loss_out[row] = bad ? NAN : loss;
-        if (p.lse_out) p.lse_out[row] = bad ? NAN : fmaf(M, p.inv_t, lZ);
-        if (nbad) atomicOr(p.status, SPEC_DEV_TOKEN);
-        if (bad_row) atomicOr(p.status, SPEC_DEV_NONFINITE);
+        const bool bad = s_flag || !(A.x < INFINITY) || A.x == -INFINITY;
+        l = s_loss[0];
+        for (int i = 1; i < kDistWarps; ++i) l += s_loss[i];
+        p.loss_out[row] = bad ? NAN : l;
+        if (p.lse_out) p.lse_out[row] = bad ? NAN : fmaf(r.M, p.inv_t, logf(r.Z));
+        if (s_flag & 1) atomicOr(p.status, SPEC_DEV_TOKEN);
+        if ((s_flag & 2) || (bad && !(s_flag & 1))) atomicOr(p.status, SPEC_DEV_NONFINITE);
     }
 }
 
@@ -206,7 +240,6 @@ constexpr int kFuseSlots = 3;                              // slices in shared m
 constexpr int kFuseRecord = 4;                             // words of a record
 constexpr int kFuseRing = 2;                               // exchanges a record's place lasts
 constexpr int kFuseMaxCtas = 512;
-constexpr uint32_t kBadToken = 0x7fc0dead;                 // a NaN that says: a bad id
 
 struct FuseHeader {
     unsigned epoch;    // tags up to here have been used
@@ -231,26 +264,6 @@ __device__ __forceinline__ void bulk_s2g(void* dst, const void* src, unsigned by
 __device__ __forceinline__ void bulk_s2g_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 __device__ __forceinline__ void bulk_s2g_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 __device__ __forceinline__ void named_sync() { asm volatile("bar.sync 1, %0;" :: "n"(kFuseNamed) : "memory"); }
-
-// (maximum, sum of 2^((x - maximum) c)) pairs merged over the N lanes that differ in their
-// low bits; NaN shows in the maximum.
-template <int N>
-__device__ __forceinline__ float2 stat_lanes(float2 v, float c) {
-    float m = v.x;
-#pragma unroll
-    for (int o = N / 2; o > 0; o >>= 1) m = f_max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
-    float s = v.x == -INFINITY ? 0.0f : v.y * ex2((v.x - m) * c);
-#pragma unroll
-    for (int o = N / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    return make_float2(m, s);
-}
-__device__ __forceinline__ float2 stat_merge(float2 a, float2 b, float c) {
-    const float m = f_max_nan(a.x, b.x);
-    float s = 0.0f;
-    if (a.x != -INFINITY) s += a.y * ex2((a.x - m) * c);
-    if (b.x != -INFINITY) s += b.y * ex2((b.x - m) * c);
-    return make_float2(m, s);
-}
 
 // What is known of a row once its slices' statistics are together.
 struct FuseRow {
@@ -492,12 +505,11 @@ __global__ void __launch_bounds__(kFuseThreads, kFuseOcc) distill_fused_kernel(D
                 const float pk = taught ? __expf(lt) / r.P : 0.0f;
                 d = r.bad ? NAN : (taught ? (ex2((cur.z - r.M) * c) / r.Z - pk) * (cur.wt * p.inv_t) : 0.0f);
                 if (rank == 0) {
-                    const float lP = logf(r.P), lZ = logf(r.Z);
-                    const float pT = taught ? __expf(cur.aT - r.top) / r.P : 0.0f;
-                    float l = pk > 0.0f ? pk * ((lt - lP) - ((cur.z - r.M) * p.inv_t - lZ)) : 0.0f;
-                    if (k == 0 && pT > 0.0f) {
-                        const float lq = r.mT > -INFINITY ? fmaf(r.mT - r.M, p.inv_t, logf(r.sT)) - lZ : -INFINITY;
-                        l += pT * (((cur.aT - r.top) - lP) - lq);
+                    const RowStats st = {r.M, r.Z, r.mT, r.sT, r.top, r.P};
+                    float l = 0.0f;
+                    if (taught) {
+                        if (known_id(cur)) l = entry_loss(st, cur.a, cur.z, p.inv_t);
+                        if (k == 0) l += rest_loss(st, cur.aT, p.inv_t);
                     }
                     l = warp_sum(l);
                     if (lane == 0) s_loss[warp] = l;
@@ -691,7 +703,8 @@ static size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 constexpr size_t kFuseBytes = sizeof(FuseHeader) + sizeof(unsigned long long) * kFuseMaxCtas * kFuseRing * kFuseRecord;
 
 size_t distill_workspace_bytes(int rows, int V) {
-    return kWsHeaderBytes + align256(kFuseBytes) + align256((size_t)rows * distill_pieces(V, 4) * sizeof(float2));
+    return kWsHeaderBytes + align256(kFuseBytes) + align256((size_t)rows * sizeof(unsigned)) +
+           (size_t)rows * distill_pieces(V, 4) * sizeof(float2);
 }
 
 template <typename T>
@@ -700,10 +713,7 @@ static cudaError_t distill_typed(DistillParams p, cudaStream_t stream) {
     p.pieces = distill_pieces(p.V, sizeof(T));
     const long grid = (long)p.rows * p.pieces;
     if (grid > 0x7fffffffL) return cudaErrorInvalidConfiguration;
-    distill_scan_kernel<T><<<(unsigned)grid, kDistThreads, 0, stream>>>(p);
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    distill_finish_kernel<T><<<p.rows, SPEC_MAX_TEACHER, 0, stream>>>(p);
+    distill_loss_kernel<T><<<(unsigned)grid, kDistThreads, 0, stream>>>(p);
     return cudaGetLastError();
 }
 
@@ -712,7 +722,9 @@ cudaError_t distill_launch(DistillParams p, void* ws, cudaStream_t stream) {
     uint8_t* b = reinterpret_cast<uint8_t*>(ws) + kWsHeaderBytes;
     p.fuse = reinterpret_cast<FuseHeader*>(b);
     p.records = reinterpret_cast<unsigned long long*>(b + sizeof(FuseHeader));
-    p.parts = reinterpret_cast<float2*>(b + align256(kFuseBytes));
+    b += align256(kFuseBytes);
+    p.done = reinterpret_cast<unsigned*>(b);
+    p.parts = reinterpret_cast<float2*>(b + align256((size_t)p.rows * sizeof(unsigned)));
     return p.dtype == SPEC_BF16 ? distill_typed<bf16_t>(p, stream) : distill_typed<float>(p, stream);
 }
 

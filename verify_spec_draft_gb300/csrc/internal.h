@@ -279,7 +279,9 @@ struct DistillParams {
     void* grad_out;            // student's layout (nullable; may be student itself)
     unsigned* status;
     // chosen at launch
+    // the loss alone: pieces of a row, a CTA each
     int pieces;
+    unsigned* done;            // [rows] pieces finished (0 between calls)
     float2* parts;             // [rows, pieces] (maximum, sum) of the entries no id names
     // with the gradient: groups of CTAs, a row at a time each
     int n_groups, group_size;
