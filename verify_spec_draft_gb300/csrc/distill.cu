@@ -10,10 +10,9 @@
 // q_T is summed over the entries that no id names, never formed as 1 - sum q_k, so a rest
 // of 1e-9 still has its logarithm.
 //
-// Weights are 2^((z - m) log2e / t) with m the row's maximum, taken from z before the
-// scaling, so that rows filled with the type's lowest value neither overflow nor vanish.
-// Logarithms of p and q are differences from the two maxima, so the loss keeps float32's
-// absolute accuracy whatever the logits' offset.
+// Weights and sums are taken relative to a maximum (row_words.cuh), and logarithms of p and q
+// are differences from the two maxima, so the loss keeps float32's absolute accuracy
+// whatever the logits' offset.
 #include "internal.h"
 #include "row_words.cuh"
 
@@ -34,40 +33,58 @@ __device__ __forceinline__ float warp_max_nan(float x) {
     asm volatile("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
     return r;
 }
-// (maximum, sum of 2^((x - maximum) c)) pairs merged over the N lanes that differ in their
-// low bits; NaN shows in the maximum.
-template <int N>
-__device__ __forceinline__ float2 stat_lanes(float2 v, float c) {
-    float m = v.x;
-#pragma unroll
-    for (int o = N / 2; o > 0; o >>= 1) m = f_max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
-    float s = v.x == -INFINITY ? 0.0f : v.y * ex2((v.x - m) * c);
-#pragma unroll
-    for (int o = N / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    return make_float2(m, s);
-}
-__device__ __forceinline__ float2 stat_merge(float2 a, float2 b, float c) {
+// (maximum, sum of weights relative to it) pairs merged; NaN shows in the maximum.  ref_lanes: over
+// the N lanes that differ in their low bits.
+__device__ __forceinline__ float2 ref_merge(float2 a, float2 b, float c) {
     const float m = f_max_nan(a.x, b.x);
     float s = 0.0f;
-    if (a.x != -INFINITY) s += a.y * ex2((a.x - m) * c);
-    if (b.x != -INFINITY) s += b.y * ex2((b.x - m) * c);
+    if (a.x != -INFINITY) s += a.y * ex2(ref_diff(a.x, m, c));
+    if (b.x != -INFINITY) s += b.y * ex2(ref_diff(b.x, m, c));
     return make_float2(m, s);
 }
+template <int N>
+__device__ __forceinline__ float lanes_max_nan(float m) {
+#pragma unroll
+    for (int o = N / 2; o > 0; o >>= 1) m = f_max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+    return m;
+}
+template <int N>
+__device__ __forceinline__ float lanes_sum(float s) {
+#pragma unroll
+    for (int o = N / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    return s;
+}
+template <int N>
+__device__ __forceinline__ float2 ref_lanes(float2 v, float c) {
+    const float m = lanes_max_nan<N>(v.x);
+    return make_float2(m, lanes_sum<N>(v.x == -INFINITY ? 0.0f : v.y * ex2(ref_diff(v.x, m, c))));
+}
+// The pair of one entry per lane.
+__device__ __forceinline__ float2 ref_entries(float x, float c) {
+    const float m = lanes_max_nan<32>(x);
+    return make_float2(m, lanes_sum<32>(x == -INFINITY ? 0.0f : ex2(ref_rel(x, m, c))));
+}
+// The teacher's pairs: (maximum, sum of e^(x - maximum)).
+template <int N>
+__device__ __forceinline__ float2 teacher_lanes(float2 v) {
+    const float m = lanes_max_nan<N>(v.x);
+    return make_float2(m, lanes_sum<N>(v.x == -INFINITY ? 0.0f : v.y * __expf(v.x - m)));
+}
 
+constexpr float kLn2 = 0.69314718055994531f;
 constexpr uint32_t kBadToken = 0x7fc0dead;   // a NaN that says: an id is listed twice
 
-// A teacher entry's logarithm and share, and the loss from them.  `top`, P: the teacher's
-// normaliser, in units of 1; M, Z: the student's, in units of t; mT, sT: that of its
-// unnamed entries.
+// The loss of a named entry (teacher's logit a, student's z) and of the rest.  top, P: the
+// teacher's pair, in units of 1; (M, Z) the student's, (mT, sT) that of its unnamed entries.
 struct RowStats { float M, Z, mT, sT, top, P; };
-__device__ __forceinline__ float entry_loss(const RowStats& r, float a, float z, float inv_t) {
+__device__ __forceinline__ float entry_loss(const RowStats& r, float a, float z, float c, float inv_t) {
     const float lt = fmaf(a, inv_t, -r.top), pk = __expf(lt) / r.P;
-    return pk > 0.0f ? pk * ((lt - logf(r.P)) - ((z - r.M) * inv_t - logf(r.Z))) : 0.0f;
+    return pk > 0.0f ? pk * ((lt - logf(r.P)) - (ref_rel(z, r.M, c) - log2f(r.Z)) * kLn2) : 0.0f;
 }
-__device__ __forceinline__ float rest_loss(const RowStats& r, float aT, float inv_t) {
+__device__ __forceinline__ float rest_loss(const RowStats& r, float aT, float c) {
     const float pT = __expf(aT - r.top) / r.P;
     if (!(pT > 0.0f)) return 0.0f;
-    const float lq = r.mT > -INFINITY ? fmaf(r.mT - r.M, inv_t, logf(r.sT)) - logf(r.Z) : -INFINITY;
+    const float lq = r.mT > -INFINITY ? (ref_diff(r.mT, r.M, c) + log2f(r.sT) - log2f(r.Z)) * kLn2 : -INFINITY;
     return pT * (((aT - r.top) - logf(r.P)) - lq);
 }
 
@@ -78,11 +95,12 @@ __device__ __forceinline__ float rest_loss(const RowStats& r, float aT, float in
 template <typename T>
 __device__ __forceinline__ void distill_finish(const DistillParams& p, int row, float wt, int id);
 
-template <typename T>
+template <typename T, bool ALIGNED>
 __global__ void __launch_bounds__(kDistThreads) distill_loss_kernel(DistillParams p) {
     constexpr int E = 16 / (int)sizeof(T);
     __shared__ uint32_t s_named[kDistPiece * E / 32];
     __shared__ float2 s_run[kDistWarps];
+    __shared__ uint32_t s_any[kDistWarps];   // bit q: something is named among a warp's q-th words
     __shared__ int s_twice;
     const int row = blockIdx.x / p.pieces, piece = blockIdx.x - row * p.pieces;
     const int tid = threadIdx.x, lane = tid & 31;
@@ -94,48 +112,49 @@ __global__ void __launch_bounds__(kDistThreads) distill_loss_kernel(DistillParam
         }
         return;
     }
-    const RowWords<T> in(reinterpret_cast<const T*>(p.student) + (long)row * p.ld, p.V);
-    const int w0 = piece * kDistPiece;
+    const SegWords<T, ALIGNED> in(reinterpret_cast<const T*>(p.student) + (long)row * p.ld, p.V);
+    const int w0 = piece * kDistPiece, n = in.n();
     const uint32_t ninf = NegInf<T>::word;
     const int id = tid < p.K ? p.ids[(long)row * p.K + tid] : -1;
     uint4 w[kDistWords];
+    if (w0 + kDistPiece <= n) {
 #pragma unroll
-    for (int q = 0; q < kDistWords; ++q) {
-        const int i = w0 + q * kDistThreads + tid;
-        w[q] = i < in.n ? in.load(i) : make_uint4(ninf, ninf, ninf, ninf);
+        for (int q = 0; q < kDistWords; ++q) w[q] = in.load(w0 + q * kDistThreads + tid);
+    } else {
+#pragma unroll
+        for (int q = 0; q < kDistWords; ++q) {
+            const int i = w0 + q * kDistThreads + tid;
+            w[q] = i < n ? in.load(i) : make_uint4(ninf, ninf, ninf, ninf);
+        }
     }
     for (int i = tid; i < kDistPiece * E / 32; i += kDistThreads) s_named[i] = 0u;
+    if (tid < kDistWarps) s_any[tid] = 0u;
     if (tid == 0) s_twice = 0;
     __syncthreads();
     const unsigned at = (unsigned)(id - in.entry(w0));
-    if (id >= 0 && id < p.V && at < (unsigned)(kDistPiece * E) &&
-        (atomicOr(&s_named[at >> 5], 1u << (at & 31)) >> (at & 31)) & 1u)
-        s_twice = 1;
+    if (id >= 0 && id < p.V && at < (unsigned)(kDistPiece * E)) {
+        if ((atomicOr(&s_named[at >> 5], 1u << (at & 31)) >> (at & 31)) & 1u) s_twice = 1;
+        const int l = at / E;
+        atomicOr(&s_any[(l / 32) % kDistWarps], 1u << (l / kDistThreads));
+    }
     __syncthreads();
+    const uint32_t any = s_any[tid >> 5];
+    if (any) {
+#pragma unroll
+        for (int q = 0; q < kDistWords; ++q) {
+            const int l = (q * kDistThreads + tid) * E;
+            if ((any >> q) & 1u) w[q] = word_without<T>(w[q], (s_named[l >> 5] >> (l & 31)) & ((1u << E) - 1u));
+        }
+    }
     float m = -INFINITY;
 #pragma unroll
-    for (int q = 0; q < kDistWords; ++q) {
-        const int l = (q * kDistThreads + tid) * E;
-        const uint32_t named = (s_named[l >> 5] >> (l & 31)) & ((1u << E) - 1u);
-        if (named) w[q] = word_without<T>(w[q], named);
-        m = f_max_nan(m, u4_max_nan<sizeof(T)>(w[q]));
-    }
+    for (int q = 0; q < kDistWords; ++q) m = f_max_nan(m, u4_max_nan<sizeof(T)>(w[q]));
     m = warp_max_nan(m);   // a NaN or +inf shows in the maximum
-    const float ref = m == -INFINITY ? 0.0f : m;
-    const f2x mm = f2_pack(-ref, -ref), cc = f2_pack(p.scale, p.scale);
-    f2x acc[2] = {f2_pack(0.0f, 0.0f), f2_pack(0.0f, 0.0f)};
-#pragma unroll
-    for (int q = 0; q < kDistWords; ++q)
-#pragma unroll
-        for (int k = 0; k < E; k += 2)
-            acc[(k >> 1) & 1] = f2_add(acc[(k >> 1) & 1],
-                f2_ex2(f2_mul(f2_add(f2_pack(word_entry<T>(w[q], k), word_entry<T>(w[q], k + 1)), mm), cc)));
-    const float2 a0 = f2_unpack(acc[0]), a1 = f2_unpack(acc[1]);
-    const float s = warp_sum((a0.x + a0.y) + (a1.x + a1.y));
+    const float s = warp_sum(words_sum<T, kDistWords>(w, m, p.scale));
     if (lane == 0) s_run[tid >> 5] = make_float2(m, s);
     __syncthreads();
     if (tid < 32) {
-        float2 t = stat_lanes<kDistWarps>(s_run[lane % kDistWarps], p.scale);
+        float2 t = ref_lanes<kDistWarps>(s_run[lane % kDistWarps], p.scale);
         if (s_twice) t.x = __uint_as_float(kBadToken);
         if (lane == 0) __stcg(&p.parts[(long)row * p.pieces + piece], t);
     }
@@ -166,13 +185,13 @@ __device__ __forceinline__ void distill_finish(const DistillParams& p, int row, 
     for (int i = tid; i < p.pieces; i += kDistThreads) {
         const float2 v = __ldcg(&p.parts[(long)row * p.pieces + i]);
         if (__float_as_uint(v.x) == kBadToken) flag |= 1;
-        t = stat_merge(t, v, p.scale);
+        t = ref_merge(t, v, p.scale);
     }
     if (!(a * p.inv_t < INFINITY) || !(aT < INFINITY) || !(fabsf(wt) < INFINITY)) flag |= 2;
     if (tid == 0) s_flag = 0;
-    t = stat_lanes<32>(t, p.scale);
-    const float2 n = stat_lanes<32>(make_float2(z, 1.0f), p.scale);
-    const float2 y = stat_lanes<32>(make_float2(a * p.inv_t, 1.0f), kLog2e);
+    t = ref_lanes<32>(t, p.scale);
+    const float2 n = ref_entries(z, p.scale);
+    const float2 y = teacher_lanes<32>(make_float2(a * p.inv_t, 1.0f));
     if (lane == 0) {
         s_tail[warp] = t;
         s_top[warp] = n;
@@ -181,15 +200,15 @@ __device__ __forceinline__ void distill_finish(const DistillParams& p, int row, 
     __syncthreads();
     if (flag) atomicOr(&s_flag, flag);
     // every warp puts the whole together
-    const float2 T2 = stat_lanes<kDistWarps>(s_tail[lane % kDistWarps], p.scale);
-    const float2 A = stat_merge(T2, stat_lanes<kDistWarps>(s_top[lane % kDistWarps], p.scale), p.scale);
-    const float2 N = stat_merge(stat_lanes<kDistWarps>(s_teach[lane % kDistWarps], kLog2e),
-                                aT == -INFINITY ? none : make_float2(aT, 1.0f), kLog2e);
+    const float2 T2 = ref_lanes<kDistWarps>(s_tail[lane % kDistWarps], p.scale);
+    const float2 A = ref_merge(T2, ref_lanes<kDistWarps>(s_top[lane % kDistWarps], p.scale), p.scale);
+    const int w = lane & 15;
+    const float2 N = teacher_lanes<16>(w < kDistWarps ? s_teach[w] : (w == kDistWarps ? make_float2(aT, 1.0f) : none));
     const RowStats r = {A.x, A.y, T2.x, T2.y, N.x, N.y};
     float l = 0.0f;
     if (r.top > -INFINITY) {
-        if (there) l = entry_loss(r, a, z, p.inv_t);
-        if (tid == 0) l += rest_loss(r, aT, p.inv_t);
+        if (there) l = entry_loss(r, a, z, p.scale, p.inv_t);
+        if (tid == 0) l += rest_loss(r, aT, p.scale);
     }
     l = warp_sum(l);
     if (lane == 0) s_loss[warp] = l;
@@ -199,7 +218,7 @@ __device__ __forceinline__ void distill_finish(const DistillParams& p, int row, 
         l = s_loss[0];
         for (int i = 1; i < kDistWarps; ++i) l += s_loss[i];
         p.loss_out[row] = bad ? NAN : l;
-        if (p.lse_out) p.lse_out[row] = bad ? NAN : fmaf(r.M, p.inv_t, logf(r.Z));
+        if (p.lse_out) p.lse_out[row] = bad ? NAN : ref_log(r.M, r.Z, p.scale, p.inv_t);
         if (s_flag & 1) atomicOr(p.status, SPEC_DEV_TOKEN);
         if ((s_flag & 2) || (bad && !(s_flag & 1))) atomicOr(p.status, SPEC_DEV_NONFINITE);
     }
@@ -364,23 +383,12 @@ __global__ void __launch_bounds__(kFuseThreads, kFuseOcc) distill_fused_kernel(D
                         // a thread's own running maximum; a batch of -inf adds nothing
                         bm = f_max_nan(bm, m);
                         if (bm != m) {
-                            s = m == -INFINITY ? 0.0f : s * ex2((m - bm) * c);
+                            s = m == -INFINITY ? 0.0f : s * ex2(ref_diff(m, bm, c));
                             m = bm;
                         }
-                        const float ref = m == -INFINITY ? 0.0f : m;
-                        const f2x mm = f2_pack(-ref, -ref);
-                        f2x acc[2] = {f2_pack(s, 0.0f), f2_pack(0.0f, 0.0f)};
-#pragma unroll
-                        for (int q = 0; q < kFuseBatch; ++q) {
-#pragma unroll
-                            for (int k = 0; k < E; k += 2)
-                                acc[(k >> 1) & 1] = f2_add(acc[(k >> 1) & 1],
-                                    f2_ex2(f2_mul(f2_add(f2_pack(word_entry<T>(w[q], k), word_entry<T>(w[q], k + 1)), mm), cc)));
-                        }
-                        const float2 a0 = f2_unpack(acc[0]), a1 = f2_unpack(acc[1]);
-                        s = (a0.x + a0.y) + (a1.x + a1.y);
+                        s += words_sum<T, kFuseBatch>(w, m, c);
                     }
-                    const float2 t = stat_lanes<32>(make_float2(m, s), c);
+                    const float2 t = ref_lanes<32>(make_float2(m, s), c);
                     if (lane == 0) s_tail[i & 1][warp] = t;
                 }
                 __syncwarp();
@@ -390,25 +398,33 @@ __global__ void __launch_bounds__(kFuseThreads, kFuseOcc) distill_fused_kernel(D
                 const int j = i - 1, n = slice_of(j).n;
                 uint4* slot = slot_of(j);
                 wait(&s_known[j & 1], j >> 1);
-                const float ref = s_row[j & 1].ref, f = s_row[j & 1].factor;
-                const bool skip = s_row[j & 1].skip;
-                const f2x mm = f2_pack(-ref, -ref), ff = f2_pack(f, f);
+                const FuseRow& row = s_row[j & 1];
+                const float x = row.ref * c;
+                if (row.skip) {
+                    for (int l = tid; l < n; l += kFuseDense) slot[l] = make_uint4(0u, 0u, 0u, 0u);
+                } else if (x > -INFINITY) {
+                    const f2x mm = f2_pack(-x, -x), ff = f2_pack(row.factor, row.factor);
 #pragma unroll 4
-                for (int l = tid; l < n; l += kFuseDense) {
-                    uint4 w = make_uint4(0u, 0u, 0u, 0u);
-                    if (!skip) {
-                        w = slot[l];
+                    for (int l = tid; l < n; l += kFuseDense) {
+                        const uint4 w = slot[l];
                         float d[E];
 #pragma unroll
                         for (int k = 0; k < E; k += 2) {
                             const float2 y = f2_unpack(f2_mul(
-                                f2_ex2(f2_mul(f2_add(f2_pack(word_entry<T>(w, k), word_entry<T>(w, k + 1)), mm), cc)), ff));
+                                f2_ex2(f2_fma(f2_pack(word_entry<T>(w, k), word_entry<T>(w, k + 1)), cc, mm)), ff));
                             d[k] = y.x;
                             d[k + 1] = y.y;
                         }
-                        w = word_of<T>(d);
+                        slot[l] = word_of<T>(d);
                     }
-                    slot[l] = w;
+                } else {   // unnamed entries at the type's lowest value
+                    for (int l = tid; l < n; l += kFuseDense) {
+                        const uint4 w = slot[l];
+                        float d[E];
+#pragma unroll
+                        for (int k = 0; k < E; ++k) d[k] = ex2((word_entry<T>(w, k) - row.ref) * c) * row.factor;
+                        slot[l] = word_of<T>(d);
+                    }
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -464,8 +480,8 @@ __global__ void __launch_bounds__(kFuseThreads, kFuseOcc) distill_fused_kernel(D
             mbar_arrive1(&s_ready[par]);
             if (e.wt != 0.0f) {
                 const float a = known_id(e) ? e.a * p.inv_t : -INFINITY;
-                const float2 t = stat_lanes<32>(make_float2(a, 1.0f), kLog2e);
-                const float2 z = stat_lanes<32>(make_float2(rank == 0 ? e.z : -INFINITY, 1.0f), c);
+                const float2 t = teacher_lanes<32>(make_float2(a, 1.0f));
+                const float2 z = ref_entries(rank == 0 ? e.z : -INFINITY, c);
                 if (lane == 0) {
                     s_teach[par][warp] = t;
                     s_top[par][warp] = z;
@@ -503,13 +519,13 @@ __global__ void __launch_bounds__(kFuseThreads, kFuseOcc) distill_fused_kernel(D
                 const bool taught = r.top > -INFINITY;
                 const float lt = known_id(cur) && taught ? fmaf(cur.a, p.inv_t, -r.top) : -INFINITY;
                 const float pk = taught ? __expf(lt) / r.P : 0.0f;
-                d = r.bad ? NAN : (taught ? (ex2((cur.z - r.M) * c) / r.Z - pk) * (cur.wt * p.inv_t) : 0.0f);
+                d = r.bad ? NAN : (taught ? (ex2(ref_rel(cur.z, r.M, c)) / r.Z - pk) * (cur.wt * p.inv_t) : 0.0f);
                 if (rank == 0) {
                     const RowStats st = {r.M, r.Z, r.mT, r.sT, r.top, r.P};
                     float l = 0.0f;
                     if (taught) {
-                        if (known_id(cur)) l = entry_loss(st, cur.a, cur.z, p.inv_t);
-                        if (k == 0) l += rest_loss(st, cur.aT, p.inv_t);
+                        if (known_id(cur)) l = entry_loss(st, cur.a, cur.z, c, p.inv_t);
+                        if (k == 0) l += rest_loss(st, cur.aT, c);
                     }
                     l = warp_sum(l);
                     if (lane == 0) s_loss[warp] = l;
@@ -521,7 +537,7 @@ __global__ void __launch_bounds__(kFuseThreads, kFuseOcc) distill_fused_kernel(D
                     float l = s_loss[0];
                     for (int q = 1; q < kNamedWarps; ++q) l += s_loss[q];
                     p.loss_out[row] = skip ? 0.0f : (r.bad ? NAN : l);
-                    if (p.lse_out) p.lse_out[row] = skip ? 0.0f : (r.bad ? NAN : fmaf(r.M, p.inv_t, logf(r.Z)));
+                    if (p.lse_out) p.lse_out[row] = skip ? 0.0f : (r.bad ? NAN : ref_log(r.M, r.Z, p.scale, p.inv_t));
                 }
             }
             wait(&s_dense[par], i >> 1);
@@ -547,8 +563,8 @@ __global__ void __launch_bounds__(kFuseThreads, kFuseOcc) distill_fused_kernel(D
             const float wt = s_wt[par], aT = s_aT[par];
             const bool skip = wt == 0.0f;
             // the teacher's normaliser, and the named logits' (slice 0 has them)
-            const float2 tt = stat_lanes<8>(skip ? none : ((lane & 7) < kNamedWarps ? s_teach[par][lane & 7] : ((lane & 7) == kNamedWarps ? make_float2(aT, 1.0f) : none)), kLog2e);
-            const float2 nn = stat_lanes<4>(skip ? none : s_top[par][lane & 3], c);
+            const float2 tt = teacher_lanes<8>(skip ? none : ((lane & 7) < kNamedWarps ? s_teach[par][lane & 7] : ((lane & 7) == kNamedWarps ? make_float2(aT, 1.0f) : none)));
+            const float2 nn = ref_lanes<4>(skip ? none : s_top[par][lane & 3], c);
             static_assert(kNamedWarps == 4 && kDenseWarps <= 16, "the lanes' layout");
             const int flag = s_flag[par];
             float2 T2 = none, N2 = none;
@@ -558,7 +574,7 @@ __global__ void __launch_bounds__(kFuseThreads, kFuseOcc) distill_fused_kernel(D
                 unsigned long long* rec = recs + (size_t)(live % kFuseRing) * p.group_size * kFuseRecord;
                 const unsigned tag = epoch + 1u + live;
                 ++live;
-                float2 t = stat_lanes<16>((lane & 15) < kDenseWarps ? s_tail[par][lane & 15] : none, c);
+                float2 t = ref_lanes<16>((lane & 15) < kDenseWarps ? s_tail[par][lane & 15] : none, c);
                 if (flag || dead) t.x = flag & 1 ? __uint_as_float(kBadToken) : NAN;
                 if (lane < (rank == 0 ? 4 : 2))
                     post_word(rec + (size_t)rank * kFuseRecord + lane, lane == 0 ? t.x : (lane == 1 ? t.y : (lane == 2 ? nn.x : nn.y)), tag);
@@ -582,18 +598,18 @@ __global__ void __launch_bounds__(kFuseThreads, kFuseOcc) distill_fused_kernel(D
                         }
                     }
                     token |= (uint32_t)v[0] == kBadToken;
-                    T2 = stat_merge(T2, make_float2(__uint_as_float((uint32_t)v[0]), __uint_as_float((uint32_t)v[1])), c);
+                    T2 = ref_merge(T2, make_float2(__uint_as_float((uint32_t)v[0]), __uint_as_float((uint32_t)v[1])), c);
                     if (r == 0) N2 = make_float2(__uint_as_float((uint32_t)v[2]), __uint_as_float((uint32_t)v[3]));
                 }
                 late = __any_sync(0xffffffffu, late);
                 token = __any_sync(0xffffffffu, token);
                 if (late) dead = true;
-                T2 = stat_lanes<32>(T2, c);
+                T2 = ref_lanes<32>(T2, c);
                 N2.x = __shfl_sync(0xffffffffu, N2.x, 0);
                 N2.y = __shfl_sync(0xffffffffu, N2.y, 0);
             }
             if (lane == 0) {
-                const float2 A = stat_merge(T2, N2, c);
+                const float2 A = ref_merge(T2, N2, c);
                 const bool bad = !skip && (late || !(A.x < INFINITY) || A.x == -INFINITY);
                 const bool taught = tt.x > -INFINITY, some = T2.x > -INFINITY;
                 const float pT = taught ? __fdividef(__expf(aT - tt.x), tt.y) : 0.0f;
@@ -601,7 +617,7 @@ __global__ void __launch_bounds__(kFuseThreads, kFuseOcc) distill_fused_kernel(D
                 r.ref = some ? T2.x : 0.0f;
                 r.factor = 0.0f;
                 if (taught && some)
-                    r.factor = wt * p.inv_t * (__fdividef(ex2((T2.x - A.x) * c), A.y) - (pT > 0.0f ? __fdividef(pT, T2.y) : 0.0f));
+                    r.factor = wt * p.inv_t * (__fdividef(ex2(ref_diff(T2.x, A.x, c)), A.y) - (pT > 0.0f ? __fdividef(pT, T2.y) : 0.0f));
                 if (bad) r.factor = NAN;
                 r.M = A.x;
                 r.Z = A.y;
@@ -713,7 +729,8 @@ static cudaError_t distill_typed(DistillParams p, cudaStream_t stream) {
     p.pieces = distill_pieces(p.V, sizeof(T));
     const long grid = (long)p.rows * p.pieces;
     if (grid > 0x7fffffffL) return cudaErrorInvalidConfiguration;
-    distill_loss_kernel<T><<<(unsigned)grid, kDistThreads, 0, stream>>>(p);
+    if (SegWords<T, true>::fits(p.ld, p.V)) distill_loss_kernel<T, true><<<(unsigned)grid, kDistThreads, 0, stream>>>(p);
+    else distill_loss_kernel<T, false><<<(unsigned)grid, kDistThreads, 0, stream>>>(p);
     return cudaGetLastError();
 }
 

@@ -27,11 +27,6 @@ constexpr int kProcOcc = 4;   // CTAs per SM
 constexpr uint32_t kCountBits = 20, kCountMask = (1u << kCountBits) - 1u;
 constexpr uint32_t kSlotMask = 0x7ffu, kInPrompt = 0x80000000u;
 
-// Bits [e, e + 32) of a bit string, e >= 0 (one word past the end may be read).
-__device__ __forceinline__ uint32_t bits_at(const uint32_t* w, int e) {
-    return __funnelshift_r(w[e >> 5], w[(e >> 5) + 1], e & 31);
-}
-
 // The kernel's shared memory: a word per entry of the segment, two strings of a bit per entry
 // (and a word more, which bits_at reads), and for the block's tokens the token, its count
 // and its bias.
@@ -40,67 +35,6 @@ __host__ __device__ inline size_t process_smem(int seg) {
 }
 
 constexpr int kProcBatch = 4;   // words a thread holds while it waits for the ones behind
-
-// The words of a segment of a row.  ALIGNED: the segment starts on 16 bytes and is a whole
-// number of words, as every segment does when rows are whole words apart and V is whole words.
-template <typename T, bool ALIGNED>
-struct SegWords {
-    static constexpr int E = 16 / (int)sizeof(T);
-    RowWords<T> r;
-    __device__ __forceinline__ SegWords(const T* row, int len) : r(row, len) {}
-    __device__ __forceinline__ int n() const { return ALIGNED ? r.V / E : r.n; }
-    __device__ __forceinline__ int entry(int i) const { return ALIGNED ? i * E : r.entry(i); }
-    __device__ __forceinline__ uint4 load(int i) const {
-        if (!ALIGNED) return r.load(i);
-        uint4 v;
-        asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                     : "l"(reinterpret_cast<const uint4*>(r.p) + i) : "memory");
-        return v;
-    }
-    __device__ __forceinline__ void store(T* q, int i, const uint4& w) const {
-        if (!ALIGNED) return r.store(q, i, w);
-        asm volatile("st.global.L1::no_allocate.v4.u32 [%0], {%1,%2,%3,%4};"
-                     :: "l"(reinterpret_cast<uint4*>(q) + i), "r"(w.x), "r"(w.y), "r"(w.z), "r"(w.w) : "memory");
-    }
-    // the mask bits of word i, bit k for entry k; `left` words of mask from the segment's first
-    __device__ __forceinline__ uint32_t allowed(const uint32_t* mask, int left, int i) const {
-        if (ALIGNED) {
-            const uint8_t* m = reinterpret_cast<const uint8_t*>(mask);
-            return E == 8 ? (uint32_t)__ldg(m + i) : ((uint32_t)__ldg(m + (i >> 1)) >> (4 * (i & 1))) & 15u;
-        }
-        const int e = entry(i), e0 = max(e, 0), at = e0 & 31;
-        const uint32_t lo = __ldg(mask + (e0 >> 5));
-        const uint32_t hi = at + E > 32 && (e0 >> 5) + 1 < left ? __ldg(mask + (e0 >> 5) + 1) : 0u;
-        return (__funnelshift_r(lo, hi, at) << (e0 - e)) & ((1u << E) - 1u);
-    }
-    // the entries of word i in the segment's array
-    __device__ __forceinline__ void floats(const float* a, int i, float (&o)[E]) const {
-#pragma unroll
-        for (int k = 0; k < E; k += 4) {
-            if (ALIGNED) {
-                const float4 v = *reinterpret_cast<const float4*>(a + i * E + k);
-                o[k] = v.x; o[k + 1] = v.y; o[k + 2] = v.z; o[k + 3] = v.w;
-            } else {
-#pragma unroll
-                for (int h = k; h < k + 4; ++h) {
-                    const int e = entry(i) + h;
-                    o[h] = e >= 0 && e < r.V ? a[e] : 0.0f;
-                }
-            }
-        }
-    }
-    // the bits of word i that are set in the segment's bit string
-    __device__ __forceinline__ uint32_t bits(const uint32_t* bits, int i) const {
-        if (ALIGNED) {
-            const uint8_t* m = reinterpret_cast<const uint8_t*>(bits);
-            return E == 8 ? (uint32_t)m[i] : ((uint32_t)m[i >> 1] >> (4 * (i & 1))) & 15u;
-        }
-        const int e = entry(i), e0 = max(e, 0);
-        const int behind = min(E, r.V - e);   // entries of the word up to the row's end
-        return (bits_at(bits, e0) << (e0 - e)) & ((1u << behind) - 1u);
-    }
-};
 
 // One batch of a row: the words kProcThreads apart from word i0 + tid, and their mask bits,
 // a byte per word.

@@ -77,6 +77,115 @@ __device__ __forceinline__ float word_entry(const uint4& w, int k) {
     return __uint_as_float(h[k & 3]);
 }
 
+// Bits [e, e + 32) of a bit string, e >= 0 (one word past the end may be read).
+__device__ __forceinline__ uint32_t bits_at(const uint32_t* w, int e) {
+    return __funnelshift_r(w[e >> 5], w[(e >> 5) + 1], e & 31);
+}
+
+// The words of a row or of a segment of one.  ALIGNED: the segment starts on 16 bytes and is a whole
+// number of words, as every segment does when rows are whole words apart and V is whole words.
+template <typename T, bool ALIGNED>
+struct SegWords {
+    static constexpr int E = 16 / (int)sizeof(T);
+    RowWords<T> r;
+    __device__ __forceinline__ SegWords(const T* row, int len) : r(row, len) {}
+    static bool fits(int ld, int V) { return ld % E == 0 && V % E == 0; }
+    __device__ __forceinline__ int n() const { return ALIGNED ? r.V / E : r.n; }
+    __device__ __forceinline__ int entry(int i) const { return ALIGNED ? i * E : r.entry(i); }
+    __device__ __forceinline__ uint4 load(int i) const {
+        if (!ALIGNED) return r.load(i);
+        uint4 v;
+        asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                     : "l"(reinterpret_cast<const uint4*>(r.p) + i) : "memory");
+        return v;
+    }
+    __device__ __forceinline__ void store(T* q, int i, const uint4& w) const {
+        if (!ALIGNED) return r.store(q, i, w);
+        asm volatile("st.global.L1::no_allocate.v4.u32 [%0], {%1,%2,%3,%4};"
+                     :: "l"(reinterpret_cast<uint4*>(q) + i), "r"(w.x), "r"(w.y), "r"(w.z), "r"(w.w) : "memory");
+    }
+    // the mask bits of word i, bit k for entry k; `left` words of mask from the segment's first
+    __device__ __forceinline__ uint32_t allowed(const uint32_t* mask, int left, int i) const {
+        if (ALIGNED) {
+            const uint8_t* m = reinterpret_cast<const uint8_t*>(mask);
+            return E == 8 ? (uint32_t)__ldg(m + i) : ((uint32_t)__ldg(m + (i >> 1)) >> (4 * (i & 1))) & 15u;
+        }
+        const int e = entry(i), e0 = max(e, 0), at = e0 & 31;
+        const uint32_t lo = __ldg(mask + (e0 >> 5));
+        const uint32_t hi = at + E > 32 && (e0 >> 5) + 1 < left ? __ldg(mask + (e0 >> 5) + 1) : 0u;
+        return (__funnelshift_r(lo, hi, at) << (e0 - e)) & ((1u << E) - 1u);
+    }
+    // the entries of word i in the segment's array
+    __device__ __forceinline__ void floats(const float* a, int i, float (&o)[E]) const {
+#pragma unroll
+        for (int k = 0; k < E; k += 4) {
+            if (ALIGNED) {
+                const float4 v = *reinterpret_cast<const float4*>(a + i * E + k);
+                o[k] = v.x; o[k + 1] = v.y; o[k + 2] = v.z; o[k + 3] = v.w;
+            } else {
+#pragma unroll
+                for (int h = k; h < k + 4; ++h) {
+                    const int e = entry(i) + h;
+                    o[h] = e >= 0 && e < r.V ? a[e] : 0.0f;
+                }
+            }
+        }
+    }
+    // the bits of word i that are set in the segment's bit string
+    __device__ __forceinline__ uint32_t bits(const uint32_t* bits, int i) const {
+        if (ALIGNED) {
+            const uint8_t* m = reinterpret_cast<const uint8_t*>(bits);
+            return E == 8 ? (uint32_t)m[i] : ((uint32_t)m[i >> 1] >> (4 * (i & 1))) & 15u;
+        }
+        const int e = entry(i), e0 = max(e, 0);
+        const int behind = min(E, r.V - e);   // entries of the word up to the row's end
+        return (bits_at(bits, e0) << (e0 - e)) & ((1u << behind) - 1u);
+    }
+};
+
+// Weights relative to a reference, in base 2: entry x of a row scaled by c = log2(e) / t weighs
+// 2^(x c - m c), where m c is rounded once and x c is exact inside an FFMA (ref_rel).  Sums that
+// belong to different references are brought together by the difference of the same rounded
+// m c (ref_diff), so that rounding cancels.  A reference so low that m c overflows (a row
+// filled with the type's lowest value) takes differences before the scaling.
+__device__ __forceinline__ float ref_diff(float a, float b, float c) {   // log2 weight of a relative to b >= a
+    const float x = a * c, y = b * c;
+    return fminf(x, y) > -INFINITY ? x - y : (a - b) * c;
+}
+__device__ __forceinline__ float ref_rel(float x, float m, float c) {    // log2 weight of entry x relative to m >= x
+    const float y = m * c;
+    return y > -INFINITY ? fmaf(x, c, -y) : (x - m) * c;
+}
+__device__ __forceinline__ float ref_log(float m, float s, float c, float inv_t) {   // ln of s 2^(m c)
+    const float x = m * c;
+    return x > -INFINITY ? (x + log2f(s)) * 0.69314718055994531f : fmaf(m, inv_t, logf(s));
+}
+// The sum of the weights of N words relative to m (0 for m = -inf).
+template <typename T, int N>
+__device__ __forceinline__ float words_sum(const uint4 (&w)[N], float m, float c) {
+    const float x = m * c;
+    f2x acc[2] = {f2_pack(0.0f, 0.0f), f2_pack(0.0f, 0.0f)};
+    const f2x cc = f2_pack(c, c);
+    if (x > -INFINITY) {
+        const f2x mm = f2_pack(-x, -x);
+#pragma unroll
+        for (int h = 0; h < N; ++h)
+#pragma unroll
+            for (int k = 0; k < 16 / (int)sizeof(T); k += 2)
+                acc[(k >> 1) & 1] = f2_add(acc[(k >> 1) & 1],
+                    f2_ex2(f2_fma(f2_pack(word_entry<T>(w[h], k), word_entry<T>(w[h], k + 1)), cc, mm)));
+    } else if (m > -INFINITY) {
+        const f2x mm = f2_pack(-m, -m);
+        for (int h = 0; h < N; ++h)
+            for (int k = 0; k < 16 / (int)sizeof(T); k += 2)
+                acc[0] = f2_add(acc[0],
+                    f2_ex2(f2_mul(f2_add(f2_pack(word_entry<T>(w[h], k), word_entry<T>(w[h], k + 1)), mm), cc)));
+    }
+    const float2 a = f2_unpack(acc[0]), b = f2_unpack(acc[1]);
+    return (a.x + a.y) + (b.x + b.y);
+}
+
 // The same for a k known at run time only.
 template <typename T>
 __device__ __forceinline__ float word_pick(const uint4& w, int k) {
