@@ -18,9 +18,9 @@
 
 namespace spec {
 
-constexpr int kDistThreads = 256;
+constexpr int kDistThreads = 128;
 constexpr int kDistWarps = kDistThreads / 32;
-constexpr int kDistWords = 8;                              // words a thread holds
+constexpr int kDistWords = 12;                              // words a thread holds
 constexpr int kDistPiece = kDistThreads * kDistWords;      // words of a CTA
 
 __host__ __device__ inline int distill_pieces(int V, int elt_bytes) {

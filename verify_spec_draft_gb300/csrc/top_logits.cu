@@ -1,14 +1,12 @@
 // top_logits.cu - each row's K largest logits and the log-sum-exp of the rest
 // (spec_top_logits): a teacher row in the compact form that spec_distill reads.
 //
-// One kernel.  CTAs stream pieces of the rows: a warp-wide load (32 words of 16 bytes, 512
-// bytes) is a block, and each block leaves its maximum m and s = sum 2^((x - m) log2e / t); the
-// maximum is kept as it is and taken from x before the scaling, so that rows filled with the
-// type's lowest value neither overflow nor vanish.  The CTA that finishes a row's last piece
-// picks: the K largest entries lie in blocks whose maxima are among the K largest, so a
-// bisection over the block maxima that ends as soon as K to K + 32 of them lie above the
-// pivot names the blocks to look at again, and the entries above the pivot (a few more than
-// K as a rule) are ranked.
+// CTAs stream pieces of the rows: a warp-wide load (32 words of 16 bytes, 512 bytes) is a
+// block, and each block leaves its maximum and the sum of its weights relative to it
+// (row_words.cuh).  Then each row is picked from: the K largest entries lie in blocks whose
+// maxima are among the K largest, so a bisection over the block maxima that ends as soon as K
+// to K + 32 of them lie at or above the pivot names the blocks to look at again, and their
+// entries at or above the pivot (a few more than K as a rule) are ranked.
 // Equal values need care: a row can hold thousands of entries at the pivot.  Where more
 // blocks or entries than there is room for lie at or above it, the choice is made exact:
 // the blocks (then the 16-byte words of those blocks) with the K largest maxima, equal ones by
@@ -61,41 +59,37 @@ __device__ __forceinline__ float warp_sum8(float (&v)[8]) {
     return v[0];
 }
 
-// s_keys: the blocks' keys [n_blocks] and sums [n_blocks], then room for 33 words per entry.
+// s_keys: the blocks' keys [n_blocks] and sums [n_blocks], then room for 32 words per entry.
 template <typename T>
 __device__ __forceinline__ void top_pick(const TopLogitsParams& p, int row, uint32_t* s_keys);
 
 // The blocks of one piece, then, in the CTA that finishes its row's last piece, the pick.
-template <typename T>
+template <typename T, bool ALIGNED>
 __global__ void __launch_bounds__(kTopThreads) top_kernel(TopLogitsParams p) {
-    constexpr int E = 16 / (int)sizeof(T);
     extern __shared__ __align__(16) uint32_t s_keys[];
     const int row = blockIdx.x / p.pieces, piece = blockIdx.x - row * p.pieces;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const RowWords<T> in(reinterpret_cast<const T*>(p.logits) + (long)row * p.ld, p.V);
+    const SegWords<T, ALIGNED> in(reinterpret_cast<const T*>(p.logits) + (long)row * p.ld, p.V);
     const int blk0 = (piece * kTopWarps + warp) * p.batch;   // batch <= kTopBatch blocks of this warp
+    const int n = in.n();
     const uint32_t ninf = NegInf<T>::word;
     uint4 w[kTopBatch];
+    if (p.batch == kTopBatch && (blk0 + kTopBatch) * 32 <= n) {
 #pragma unroll
-    for (int q = 0; q < kTopBatch; ++q) {
-        const int i = (blk0 + q) * 32 + lane;
-        w[q] = q < p.batch && i < in.n ? in.load(i) : make_uint4(ninf, ninf, ninf, ninf);
+        for (int q = 0; q < kTopBatch; ++q) w[q] = in.load((blk0 + q) * 32 + lane);
+    } else {
+#pragma unroll
+        for (int q = 0; q < kTopBatch; ++q) {
+            const int i = (blk0 + q) * 32 + lane;
+            w[q] = q < p.batch && i < n ? in.load(i) : make_uint4(ninf, ninf, ninf, ninf);
+        }
     }
     float m[kTopBatch], s[kTopBatch];
 #pragma unroll
     for (int q = 0; q < kTopBatch; ++q) {
-        s[q] = 0.0f;
-        m[q] = -INFINITY;
-        if (q >= p.batch) continue;
         m[q] = warp_max_nan(u4_max_nan<sizeof(T)>(w[q]));
-        const float ref = m[q] == -INFINITY ? 0.0f : m[q];
-        const f2x mm = f2_pack(-ref, -ref), cc = f2_pack(p.scale, p.scale);
-        f2x acc = f2_pack(0.0f, 0.0f);
-#pragma unroll
-        for (int k = 0; k < E; k += 2)
-            acc = f2_add(acc, f2_ex2(f2_mul(f2_add(f2_pack(word_entry<T>(w[q], k), word_entry<T>(w[q], k + 1)), mm), cc)));
-        const float2 a = f2_unpack(acc);
-        s[q] = a.x + a.y;
+        const uint4 one[1] = {w[q]};
+        s[q] = words_sum<T, 1>(one, m[q], p.scale);
     }
     const float sum = warp_sum8(s);
     const int mine = lane >> 2;
@@ -193,53 +187,48 @@ __device__ __forceinline__ float key_floor(uint32_t key) {
     return key < float_order(-3.402823466e38f) ? -3.402823466e38f : order_float(key);
 }
 
-// Running maximum m and s = sum w 2^((x - m) c).
+// Running maximum m and the sum of weights relative to it.
 struct Run {
     float m = -INFINITY, s = 0.0f;
-    __device__ __forceinline__ void add(float x, float w, float c) {
-        if (x == -INFINITY) return;
-        if (x <= m) { s += w * ex2((x - m) * c); return; }
-        s = s * ex2((m - x) * c) + w;
+    __device__ __forceinline__ void raise(float x, float c) {
+        if (!(x > m)) return;
+        s = m == -INFINITY ? 0.0f : s * ex2(ref_diff(m, x, c));
         m = x;
     }
-};
-// Every entry of N words with maximum mx.
-template <typename T, int N>
-__device__ __forceinline__ void run_words(Run& r, const uint4 (&w)[N], float mx, float c) {
-    if (mx > r.m) {
-        r.s = r.m == -INFINITY ? 0.0f : r.s * ex2((r.m - mx) * c);
-        r.m = mx;
+    __device__ __forceinline__ void entry(float x, float c) {   // one entry
+        if (x == -INFINITY) return;
+        raise(x, c);
+        s += ex2(ref_rel(x, m, c));
     }
-    const float ref = r.m == -INFINITY ? 0.0f : r.m;
-    const f2x mm = f2_pack(-ref, -ref), cc = f2_pack(c, c);
-    f2x acc[2] = {f2_pack(r.s, 0.0f), f2_pack(0.0f, 0.0f)};
-#pragma unroll
-    for (int h = 0; h < N; ++h)
-#pragma unroll
-        for (int k = 0; k < 16 / (int)sizeof(T); k += 2)
-            acc[(k >> 1) & 1] = f2_add(acc[(k >> 1) & 1],
-                f2_ex2(f2_mul(f2_add(f2_pack(word_entry<T>(w[h], k), word_entry<T>(w[h], k + 1)), mm), cc)));
-    const float2 x = f2_unpack(acc[0]), y = f2_unpack(acc[1]);
-    r.s = (x.x + x.y) + (y.x + y.y);
-}
+    __device__ __forceinline__ void sum(float x, float w, float c) {   // a sum relative to x
+        if (x == -INFINITY) return;
+        raise(x, c);
+        s += w * ex2(ref_diff(x, m, c));
+    }
+    template <typename T, int N>
+    __device__ __forceinline__ void words(const uint4 (&w)[N], float mx, float c) {   // their maximum is mx
+        raise(mx, c);
+        s += words_sum<T, N>(w, m, c);
+    }
+};
 // The CTA's totals of two runs, in the first warp.
 __device__ __forceinline__ void runs_cta(Run& x, Run& y, float c, float4* s_run) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const float mx = warp_max(x.m), my = warp_max(y.m);
-    const float sx = warp_sum(x.m == -INFINITY ? 0.0f : x.s * ex2((x.m - mx) * c));
-    const float sy = warp_sum(y.m == -INFINITY ? 0.0f : y.s * ex2((y.m - my) * c));
+    const float sx = warp_sum(x.m == -INFINITY ? 0.0f : x.s * ex2(ref_diff(x.m, mx, c)));
+    const float sy = warp_sum(y.m == -INFINITY ? 0.0f : y.s * ex2(ref_diff(y.m, my, c)));
     if (lane == 0) s_run[warp] = make_float4(mx, sx, my, sy);
     __syncthreads();
     if (warp != 0) return;
     const float4 v = lane < kTopWarps ? s_run[lane] : make_float4(-INFINITY, 0.0f, -INFINITY, 0.0f);
     x.m = warp_max(v.x);
     y.m = warp_max(v.z);
-    x.s = warp_sum(v.x == -INFINITY ? 0.0f : v.y * ex2((v.x - x.m) * c));
-    y.s = warp_sum(v.z == -INFINITY ? 0.0f : v.w * ex2((v.z - y.m) * c));
+    x.s = warp_sum(v.x == -INFINITY ? 0.0f : v.y * ex2(ref_diff(v.x, x.m, c)));
+    y.s = warp_sum(v.z == -INFINITY ? 0.0f : v.w * ex2(ref_diff(v.z, y.m, c)));
 }
 // ln of the sum
-__device__ __forceinline__ float run_log(const Run& r, float inv_t) {
-    return r.s > 0.0f ? fmaf(r.m, inv_t, logf(r.s)) : -INFINITY;
+__device__ __forceinline__ float run_log(const Run& r, float c, float inv_t) {
+    return r.s > 0.0f ? ref_log(r.m, r.s, c, inv_t) : -INFINITY;
 }
 
 // The indices of keys[0..n) at or above `t` in list[], in an order that depends on them alone.
@@ -270,7 +259,8 @@ __device__ __forceinline__ void top_pick(const TopLogitsParams& p, int row, uint
     constexpr int E = 16 / (int)sizeof(T);
     __shared__ unsigned long long s_cand[kTopCandMax];
     __shared__ float s_sorted[kTopCandMax];
-    __shared__ int s_rank[kTopCandMax];
+    __shared__ int s_word[kTopCandMax];                      // words looked at; then the candidates' ranks
+    __shared__ unsigned s_hit[kTopBlkMax];
     __shared__ int s_blk[kTopBlkMax], s_part[2 * kTopWarps], s_n, s_bad;
     __shared__ uint32_t s_lo, s_hi;
     __shared__ unsigned long long s_kth;
@@ -358,7 +348,7 @@ __device__ __forceinline__ void top_pick(const TopLogitsParams& p, int row, uint
     // the chosen blocks once more: entries at or above the pivot are candidates, the others
     // belong to the rest
     Run rest, taken;
-    // word l of block b: its entries from `least` on are pushed; the word without them
+    // a word's entries from `least` on are pushed; the word without them
     auto push = [&](int b, int l, const uint4& w, float least) {
         uint32_t above = 0u;
 #pragma unroll
@@ -380,30 +370,43 @@ __device__ __forceinline__ void top_pick(const TopLogitsParams& p, int row, uint
         }
     };
     const float least = key_floor(floor_key);   // (a key of 1 stands for the lowest float: every finite entry)
+    // the words that hold such an entry are noted, the others summed
     over_blocks([&](int q0, uint4 (&w)[4]) {
         float mx = -INFINITY;
 #pragma unroll
         for (int h = 0; h < 4; ++h) {
-            float wm = u4_max_nan<sizeof(T)>(w[h]);
-            if (wm >= least) {
-                w[h] = push(s_blk[q0 + h * kTopWarps], lane, w[h], least);
-                wm = u4_max_nan<sizeof(T)>(w[h]);
-            }
-            mx = fmaxf(mx, wm);
+            const float wm = u4_max_nan<sizeof(T)>(w[h]);
+            const bool hit = wm >= least;
+            const unsigned who = __ballot_sync(0xffffffffu, hit);
+            if (lane == 0 && q0 + h * kTopWarps < nb) s_hit[q0 + h * kTopWarps] = who;
+            if (hit) w[h] = make_uint4(ninf, ninf, ninf, ninf);
+            else mx = fmaxf(mx, wm);
         }
-        run_words<T, 4>(rest, w, mx, p.scale);
+        rest.words<T, 4>(w, mx, p.scale);
     });
     __syncthreads();
+    // then looked at in parallel, a thread each, in the blocks' order
+    unsigned who = tid < nb ? s_hit[tid] : 0u;
+    const int n_hit = cta_sum(__popc(who), s_part, slot);
+    int at = cta_prefix(__popc(who), s_part, slot);
+    for (; who; who &= who - 1u, ++at)
+        if (at < kTopCandMax) s_word[at] = tid * 32 + __ffs(who) - 1;
+    __syncthreads();
+    for (int i = tid; i < n_hit && i < kTopCandMax; i += kTopThreads) {
+        const int b = s_blk[s_word[i] >> 5], l = s_word[i] & 31;
+        const uint4 one[1] = {push(b, l, word_at(b, l), least)};
+        rest.words<T, 1>(one, u4_max_nan<sizeof(T)>(one[0]), p.scale);
+    }
+    __syncthreads();
     int n = s_n;
-    const bool exact_words = n > kTopCandMax;
+    const bool exact_words = n > kTopCandMax || n_hit > kTopCandMax;
     if (exact_words) {
         // equal values in numbers: the K largest word maxima of (exactly) K blocks, in the
         // blocks' order
         __syncthreads();
         if (!exact_blocks) nb = pick_largest(s_keys, p.n_blocks, K, s_blk, floor_key, s_part, slot);
         __syncthreads();
-        uint32_t* s_wkeys = s_keys + 2 * p.n_blocks;              // [K * 32]
-        int* s_word = reinterpret_cast<int*>(s_wkeys + K * 32);   // [K]
+        uint32_t* s_wkeys = s_keys + 2 * p.n_blocks;   // [K * 32]
         over_blocks([&](int q0, uint4 (&w)[4]) {
             for (int h = 0; h < 4 && q0 + h * kTopWarps < nb; ++h)
                 s_wkeys[(q0 + h * kTopWarps) * 32 + lane] = value_key(u4_max_nan<sizeof(T)>(w[h]));
@@ -416,10 +419,10 @@ __device__ __forceinline__ void top_pick(const TopLogitsParams& p, int row, uint
             push(b, l, word_at(b, l), key_floor(floor_key));
         }
         __syncthreads();
-        n = s_n;
+        n = s_n;   // (s_word is free again)
     }
     // ranks, a candidate's comparisons shared by two threads
-    for (int i = tid; i < n; i += kTopThreads) s_rank[i] = 0;
+    for (int i = tid; i < n; i += kTopThreads) s_word[i] = 0;
     __syncthreads();
     constexpr int kHalf = kTopThreads / 2;
     const int j0 = tid < kHalf ? 0 : n / 2, j1 = tid < kHalf ? n / 2 : n;
@@ -428,12 +431,12 @@ __device__ __forceinline__ void top_pick(const TopLogitsParams& p, int row, uint
         int rank = 0;
 #pragma unroll 8
         for (int j = j0; j < j1; ++j) rank += s_cand[j] > key ? 1 : 0;
-        atomicAdd(&s_rank[i], rank);
+        atomicAdd(&s_word[i], rank);
     }
     __syncthreads();
     for (int i = tid; i < n; i += kTopThreads) {
         const unsigned long long key = s_cand[i];
-        const int rank = s_rank[i];
+        const int rank = s_word[i];
         const float x = key_value(key);
         s_sorted[rank] = x;
         if (rank < K) {
@@ -445,8 +448,8 @@ __device__ __forceinline__ void top_pick(const TopLogitsParams& p, int row, uint
     __syncthreads();
     // summed in the order of their ranks: the candidates came in any order
     for (int i = tid; i < n; i += kTopThreads) {
-        if (i < K) taken.add(s_sorted[i], 1.0f, p.scale);
-        else if (!exact_words) rest.add(s_sorted[i], 1.0f, p.scale);
+        if (i < K) taken.entry(s_sorted[i], p.scale);
+        else if (!exact_words) rest.entry(s_sorted[i], p.scale);
     }
     for (int k = n + tid; k < K; k += kTopThreads) { values[k] = -INFINITY; ids[k] = -1; }
     if (exact_words) {   // the chosen blocks' entries that were not taken, over again
@@ -465,7 +468,7 @@ __device__ __forceinline__ void top_pick(const TopLogitsParams& p, int row, uint
                 w[h] = word_without<T>(w[h], taken_bits);
                 mx = fmaxf(mx, u4_max_nan<sizeof(T)>(w[h]));
             }
-            run_words<T, 4>(rest, w, mx, p.scale);
+            rest.words<T, 4>(w, mx, p.scale);
         });
     }
     // the blocks that were not looked at again
@@ -480,13 +483,13 @@ __device__ __forceinline__ void top_pick(const TopLogitsParams& p, int row, uint
             }
             chosen = a < nb && s_blk[a] == i;
         }
-        if (!chosen && s_keys[i]) rest.add(order_float(s_keys[i]), s_sums[i], p.scale);
+        if (!chosen && s_keys[i]) rest.sum(order_float(s_keys[i]), s_sums[i], p.scale);
     }
     runs_cta(rest, taken, p.scale, s_run);
     if (tid == 0) {
-        p.tail_out[row] = run_log(rest, p.inv_t);
-        taken.add(rest.m, rest.s, p.scale);
-        if (p.lse_out) p.lse_out[row] = run_log(taken, p.inv_t);
+        p.tail_out[row] = run_log(rest, p.scale, p.inv_t);
+        taken.sum(rest.m, rest.s, p.scale);
+        if (p.lse_out) p.lse_out[row] = run_log(taken, p.scale, p.inv_t);
         if (!(taken.s > 0.0f)) atomicOr(p.status, SPEC_DEV_NONFINITE);   // no finite entry
     }
 }
@@ -507,14 +510,17 @@ static cudaError_t top_launch(TopLogitsParams p, cudaStream_t stream) {
     p.pieces = (p.n_blocks + kTopWarps * p.batch - 1) / (kTopWarps * p.batch);
     const long grid = (long)p.rows * p.pieces;
     if (grid > 0x7fffffffL) return cudaErrorInvalidConfiguration;
-    const size_t smem = ((size_t)p.n_blocks * 2 + (size_t)p.K * 33) * 4;
+    const size_t smem = ((size_t)p.n_blocks * 2 + (size_t)p.K * 32) * 4;
     p.pick_apart = p.rows >= kTopApart;
     if (smem > 28 * 1024) {
-        const void* kern = p.pick_apart ? (const void*)top_pick_kernel<T> : (const void*)top_kernel<T>;
+        const void* kern = p.pick_apart ? (const void*)top_pick_kernel<T>
+                                        : (SegWords<T, true>::fits(p.ld, p.V) ? (const void*)top_kernel<T, true>
+                                                                              : (const void*)top_kernel<T, false>);
         const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
     }
-    top_kernel<T><<<(unsigned)grid, kTopThreads, p.pick_apart ? 0 : smem, stream>>>(p);
+    if (SegWords<T, true>::fits(p.ld, p.V)) top_kernel<T, true><<<(unsigned)grid, kTopThreads, p.pick_apart ? 0 : smem, stream>>>(p);
+    else top_kernel<T, false><<<(unsigned)grid, kTopThreads, p.pick_apart ? 0 : smem, stream>>>(p);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || !p.pick_apart) return e;
     cudaLaunchConfig_t cfg = {};
