@@ -27,6 +27,7 @@ constexpr int kTopBatch = 8;                       // blocks a warp loads at onc
 constexpr int kTopSlack = 32;                      // blocks beyond K that the bisection may leave
 constexpr int kTopBlkMax = SPEC_MAX_TEACHER + kTopSlack;
 constexpr int kTopApart = 32;                      // rows from which the picks are a launch of their own
+constexpr int kTopAgain = 4;                       // words a thread holds when it looks again
 constexpr int kTopCandMax = SPEC_MAX_TEACHER * 8;  // entries to rank
 
 // Blocks of a row of V entries, whatever its offset in its first word.
@@ -360,21 +361,21 @@ __device__ __forceinline__ void top_pick(const TopLogitsParams& p, int row, uint
         }
         return word_without<T>(w, above);
     };
-    auto over_blocks = [&](auto&& body) {   // a warp's share of the chosen blocks, four loads at a time
-        for (int q0 = warp; q0 < nb; q0 += 4 * kTopWarps) {
-            uint4 w[4];
+    auto over_blocks = [&](auto&& body) {   // a warp's share of the chosen blocks, kTopAgain loads at a time
+        for (int q0 = warp; q0 < nb; q0 += kTopAgain * kTopWarps) {
+            uint4 w[kTopAgain];
 #pragma unroll
-            for (int h = 0; h < 4; ++h)
+            for (int h = 0; h < kTopAgain; ++h)
                 w[h] = q0 + h * kTopWarps < nb ? word_at(s_blk[q0 + h * kTopWarps], lane) : make_uint4(ninf, ninf, ninf, ninf);
             body(q0, w);
         }
     };
     const float least = key_floor(floor_key);   // (a key of 1 stands for the lowest float: every finite entry)
     // the words that hold such an entry are noted, the others summed
-    over_blocks([&](int q0, uint4 (&w)[4]) {
+    over_blocks([&](int q0, uint4 (&w)[kTopAgain]) {
         float mx = -INFINITY;
 #pragma unroll
-        for (int h = 0; h < 4; ++h) {
+        for (int h = 0; h < kTopAgain; ++h) {
             const float wm = u4_max_nan<sizeof(T)>(w[h]);
             const bool hit = wm >= least;
             const unsigned who = __ballot_sync(0xffffffffu, hit);
@@ -382,7 +383,7 @@ __device__ __forceinline__ void top_pick(const TopLogitsParams& p, int row, uint
             if (hit) w[h] = make_uint4(ninf, ninf, ninf, ninf);
             else mx = fmaxf(mx, wm);
         }
-        rest.words<T, 4>(w, mx, p.scale);
+        rest.words<T, kTopAgain>(w, mx, p.scale);
     });
     __syncthreads();
     // then looked at in parallel, a thread each, in the blocks' order
@@ -407,8 +408,8 @@ __device__ __forceinline__ void top_pick(const TopLogitsParams& p, int row, uint
         if (!exact_blocks) nb = pick_largest(s_keys, p.n_blocks, K, s_blk, floor_key, s_part, slot);
         __syncthreads();
         uint32_t* s_wkeys = s_keys + 2 * p.n_blocks;   // [K * 32]
-        over_blocks([&](int q0, uint4 (&w)[4]) {
-            for (int h = 0; h < 4 && q0 + h * kTopWarps < nb; ++h)
+        over_blocks([&](int q0, uint4 (&w)[kTopAgain]) {
+            for (int h = 0; h < kTopAgain && q0 + h * kTopWarps < nb; ++h)
                 s_wkeys[(q0 + h * kTopWarps) * 32 + lane] = value_key(u4_max_nan<sizeof(T)>(w[h]));
         });
         if (tid == 0) s_n = 0;
@@ -421,17 +422,17 @@ __device__ __forceinline__ void top_pick(const TopLogitsParams& p, int row, uint
         __syncthreads();
         n = s_n;   // (s_word is free again)
     }
-    // ranks, a candidate's comparisons shared by two threads
-    for (int i = tid; i < n; i += kTopThreads) s_word[i] = 0;
-    __syncthreads();
-    constexpr int kHalf = kTopThreads / 2;
-    const int j0 = tid < kHalf ? 0 : n / 2, j1 = tid < kHalf ? n / 2 : n;
-    for (int i = tid & (kHalf - 1); i < n; i += kHalf) {
-        const unsigned long long key = s_cand[i];
+    // ranks: eight threads share a candidate's comparisons, a warp sees four candidates
+    for (int i0 = 0; i0 < n; i0 += kTopThreads / 8) {
+        const int i = i0 + tid / 8;
+        const unsigned long long key = i < n ? s_cand[i] : 0ull;
         int rank = 0;
-#pragma unroll 8
-        for (int j = j0; j < j1; ++j) rank += s_cand[j] > key ? 1 : 0;
-        atomicAdd(&s_word[i], rank);
+#pragma unroll 4
+        for (int j = tid & 7; j < n; j += 8) rank += s_cand[j] > key ? 1 : 0;
+        rank += __shfl_xor_sync(0xffffffffu, rank, 1);
+        rank += __shfl_xor_sync(0xffffffffu, rank, 2);
+        rank += __shfl_xor_sync(0xffffffffu, rank, 4);
+        if ((tid & 7) == 0 && i < n) s_word[i] = rank;
     }
     __syncthreads();
     for (int i = tid; i < n; i += kTopThreads) {
@@ -455,10 +456,10 @@ __device__ __forceinline__ void top_pick(const TopLogitsParams& p, int row, uint
     if (exact_words) {   // the chosen blocks' entries that were not taken, over again
         const unsigned long long kth = s_kth;   // 0 when every finite entry was taken
         rest = Run();
-        over_blocks([&](int q0, uint4 (&w)[4]) {
+        over_blocks([&](int q0, uint4 (&w)[kTopAgain]) {
             float mx = -INFINITY;
 #pragma unroll
-            for (int h = 0; h < 4; ++h) {
+            for (int h = 0; h < kTopAgain; ++h) {
                 if (q0 + h * kTopWarps >= nb) continue;
                 const int e = in.entry(s_blk[q0 + h * kTopWarps] * 32 + lane);
                 uint32_t taken_bits = 0u;
@@ -468,7 +469,7 @@ __device__ __forceinline__ void top_pick(const TopLogitsParams& p, int row, uint
                 w[h] = word_without<T>(w[h], taken_bits);
                 mx = fmaxf(mx, u4_max_nan<sizeof(T)>(w[h]));
             }
-            rest.words<T, 4>(w, mx, p.scale);
+            rest.words<T, kTopAgain>(w, mx, p.scale);
         });
     }
     // the blocks that were not looked at again
