@@ -60,7 +60,7 @@ size_t spec_workspace_bytes(spec_op op, int B, int gamma, int V, int r) {
         if (B < 1 || B > SPEC_MAX_TEACHER_ROWS || gamma < 1 || gamma > SPEC_MAX_TEACHER || V < 1 ||
             V > SPEC_MAX_V_TEACHER)
             return 0;
-        return op == SPEC_OP_TOP_LOGITS ? top_logits_workspace_bytes(B, V) : distill_workspace_bytes(B, V);
+        return op == SPEC_OP_TOP_LOGITS ? top_logits_workspace_bytes(B, gamma, V) : distill_workspace_bytes(B, V);
     }
     if (B < 1 || gamma < 1 || gamma > SPEC_MAX_GAMMA || V < 1 || V > SPEC_MAX_V) return 0;
     switch (op) {
@@ -558,7 +558,7 @@ spec_status spec_top_logits(const void* logits, spec_dtype dtype, int rows, int 
     if (!(temperature > 0.0f && temperature < INFINITY)) return SPEC_ERR_INVALID_ARG;
     if (!logits || !values_out || !ids_out || !tail_out) return SPEC_ERR_INVALID_ARG;
     if (!aligned16(logits)) return SPEC_ERR_ALIGN;
-    if (!workspace || workspace_bytes < top_logits_workspace_bytes(rows, V)) return SPEC_ERR_WORKSPACE;
+    if (!workspace || workspace_bytes < top_logits_workspace_bytes(rows, K, V)) return SPEC_ERR_WORKSPACE;
     TopLogitsParams p;
     memset(&p, 0, sizeof(p));
     p.logits = logits;

@@ -259,7 +259,7 @@ struct TopLogitsParams {
     unsigned* done;            // [rows] pieces finished (0 between calls)
     float2* blocks;            // [rows, n_blocks] (maximum, sum)
 };
-size_t top_logits_workspace_bytes(int rows, int V);
+size_t top_logits_workspace_bytes(int rows, int K, int V);
 cudaError_t top_logits_launch(TopLogitsParams p, void* ws, cudaStream_t stream);
 
 // spec_distill

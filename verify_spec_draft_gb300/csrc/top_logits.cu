@@ -1,9 +1,9 @@
 // top_logits.cu - each row's K largest logits and the log-sum-exp of the rest
 // (spec_top_logits): a teacher row in the compact form that spec_distill reads.
 //
-// CTAs stream pieces of the rows: a warp-wide load (32 words of 16 bytes, 512 bytes) is a
-// block, and each block leaves its maximum and the sum of its weights relative to it
-// (row_words.cuh).  Then each row is picked from: the K largest entries lie in blocks whose
+// CTAs stream pieces of the rows: a warp-wide load (32 words of 16 bytes) is a block, or eight of
+// them where a row has fewer than twice K, and each block leaves its maximum and the sum of
+// its weights relative to it (row_words.cuh).  Then each row is picked from: the K largest entries lie in blocks whose
 // maxima are among the K largest, so a bisection over the block maxima that ends as soon as K
 // to K + 32 of them lie at or above the pivot names the blocks to look at again, and their
 // entries at or above the pivot (a few more than K as a rule) are ranked.
@@ -27,13 +27,15 @@ constexpr int kTopBatch = 8;                       // blocks a warp loads at onc
 constexpr int kTopSlack = 32;                      // blocks beyond K that the bisection may leave
 constexpr int kTopBlkMax = SPEC_MAX_TEACHER + kTopSlack;
 constexpr int kTopApart = 32;                      // rows from which the picks are a launch of their own
+constexpr int kTopMany = 2;                        // blocks per entry asked for, at least
 constexpr int kTopAgain = 4;                       // words a thread holds when it looks again
 constexpr int kTopCandMax = SPEC_MAX_TEACHER * 8;  // entries to rank
 
-// Blocks of a row of V entries, whatever its offset in its first word.
-__host__ __device__ inline int top_blocks(int V, int elt_bytes) {
+// Blocks of `lanes` words of a row of V entries, whatever its offset in its first word, in
+// whole warps' loads.
+__host__ __device__ inline int top_blocks(int V, int elt_bytes, int lanes) {
     const int E = 16 / elt_bytes;
-    return ((V + 2 * E - 2) / E + 31) / 32;
+    return ((V + 2 * E - 2) / E + 31) / 32 * (32 / lanes);
 }
 
 __device__ __forceinline__ float warp_max_nan(float x) {
@@ -61,17 +63,18 @@ __device__ __forceinline__ float warp_sum8(float (&v)[8]) {
 }
 
 // s_keys: the blocks' keys [n_blocks] and sums [n_blocks], then room for 32 words per entry.
-template <typename T>
+template <typename T, int LANES>
 __device__ __forceinline__ void top_pick(const TopLogitsParams& p, int row, uint32_t* s_keys);
 
 // The blocks of one piece, then, in the CTA that finishes its row's last piece, the pick.
-template <typename T, bool ALIGNED>
+template <typename T, bool ALIGNED, int LANES>
 __global__ void __launch_bounds__(kTopThreads) top_kernel(TopLogitsParams p) {
+    static_assert(LANES == 32 || LANES == 4, "a block is a warp's load or an eighth of it");
     extern __shared__ __align__(16) uint32_t s_keys[];
     const int row = blockIdx.x / p.pieces, piece = blockIdx.x - row * p.pieces;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const SegWords<T, ALIGNED> in(reinterpret_cast<const T*>(p.logits) + (long)row * p.ld, p.V);
-    const int blk0 = (piece * kTopWarps + warp) * p.batch;   // batch <= kTopBatch blocks of this warp
+    const int blk0 = (piece * kTopWarps + warp) * p.batch;   // batch <= kTopBatch loads of this warp
     const int n = in.n();
     const uint32_t ninf = NegInf<T>::word;
     uint4 w[kTopBatch];
@@ -88,32 +91,48 @@ __global__ void __launch_bounds__(kTopThreads) top_kernel(TopLogitsParams p) {
     float m[kTopBatch], s[kTopBatch];
 #pragma unroll
     for (int q = 0; q < kTopBatch; ++q) {
-        m[q] = warp_max_nan(u4_max_nan<sizeof(T)>(w[q]));
+        m[q] = u4_max_nan<sizeof(T)>(w[q]);
+        if (LANES == 32) {
+            m[q] = warp_max_nan(m[q]);
+        } else {
+            m[q] = f_max_nan(m[q], __shfl_xor_sync(0xffffffffu, m[q], 1));
+            m[q] = f_max_nan(m[q], __shfl_xor_sync(0xffffffffu, m[q], 2));
+        }
         const uint4 one[1] = {w[q]};
         s[q] = words_sum<T, 1>(one, m[q], p.scale);
     }
-    const float sum = warp_sum8(s);
-    const int mine = lane >> 2;
-    float mx = m[0];
+    float2* out = p.blocks + (long)row * p.n_blocks;
+    if (LANES == 32) {
+        const float sum = warp_sum8(s);
+        const int mine = lane >> 2;
+        float mx = m[0];
 #pragma unroll
-    for (int q = 1; q < kTopBatch; ++q) mx = mine == q ? m[q] : mx;
-    if ((lane & 3) == 0 && mine < p.batch && blk0 + mine < p.n_blocks)
-        __stcg(&p.blocks[(long)row * p.n_blocks + blk0 + mine], make_float2(mx, sum));
+        for (int q = 1; q < kTopBatch; ++q) mx = mine == q ? m[q] : mx;
+        if ((lane & 3) == 0 && mine < p.batch && blk0 + mine < p.n_blocks) __stcg(&out[blk0 + mine], make_float2(mx, sum));
+    } else {
+#pragma unroll
+        for (int q = 0; q < kTopBatch; ++q) {
+            s[q] += __shfl_xor_sync(0xffffffffu, s[q], 1);
+            s[q] += __shfl_xor_sync(0xffffffffu, s[q], 2);
+            const int b = (blk0 + q) * 8 + (lane >> 2);
+            if ((lane & 3) == 0 && q < p.batch && b < p.n_blocks) __stcg(&out[b], make_float2(m[q], s[q]));
+        }
+    }
     if (p.pick_apart) {
         pdl_launch_dependents();
         return;
     }
     if (!last_block_done(&p.done[row], (unsigned)p.pieces)) return;
     if (threadIdx.x == 0) p.done[row] = 0u;
-    top_pick<T>(p, row, s_keys);
+    top_pick<T, LANES>(p, row, s_keys);
 }
 
 // The picks of all rows, launched behind the scan as its programmatic dependent.
-template <typename T>
+template <typename T, int LANES>
 __global__ void __launch_bounds__(kTopThreads) top_pick_kernel(TopLogitsParams p) {
     extern __shared__ __align__(16) uint32_t s_keys[];
     pdl_wait_primary();
-    top_pick<T>(p, blockIdx.x, s_keys);
+    top_pick<T, LANES>(p, blockIdx.x, s_keys);
 }
 
 // Sum of one int per thread over the CTA; `slot` alternates between calls.
@@ -178,6 +197,11 @@ __device__ __forceinline__ int pick_largest(const uint32_t* keys, int n, int K, 
     floor_key = t;
     __syncthreads();
     return n_gt + admit;
+}
+
+// Words of a block: 32, or 4 where that leaves a row fewer than kTopMany K blocks.
+__host__ __device__ inline int top_lanes(int V, int elt_bytes, int K) {
+    return top_blocks(V, elt_bytes, 32) < kTopMany * K ? 4 : 32;
 }
 
 // A key that is 0 for -inf and grows with the value otherwise.
@@ -255,14 +279,13 @@ __device__ __forceinline__ void list_above(const uint32_t* keys, int n, uint32_t
     __syncthreads();
 }
 
-template <typename T>
+template <typename T, int LANES>
 __device__ __forceinline__ void top_pick(const TopLogitsParams& p, int row, uint32_t* s_keys) {
-    constexpr int E = 16 / (int)sizeof(T);
+    constexpr int E = 16 / (int)sizeof(T), PER = 32 / LANES;   // blocks of a warp's load
     __shared__ unsigned long long s_cand[kTopCandMax];
-    __shared__ float s_sorted[kTopCandMax];
-    __shared__ int s_word[kTopCandMax];                      // words looked at; then the candidates' ranks
+    __shared__ int s_word[kTopCandMax];                      // listed words to look at
     __shared__ unsigned s_hit[kTopBlkMax];
-    __shared__ int s_blk[kTopBlkMax], s_part[2 * kTopWarps], s_n, s_bad;
+    __shared__ int s_blk[kTopBlkMax], s_part[2 * kTopWarps], s_bad;
     __shared__ uint32_t s_lo, s_hi;
     __shared__ unsigned long long s_kth;
     __shared__ float4 s_run[kTopWarps];
@@ -274,14 +297,14 @@ __device__ __forceinline__ void top_pick(const TopLogitsParams& p, int row, uint
     int32_t* ids = p.ids_out + (long)row * K;
     const uint32_t ninf = NegInf<T>::word;
     auto word_at = [&](int b, int l) {   // word l of block b
-        const int i = b * 32 + l;
+        const int i = b * LANES + l;
         return i < in.n ? in.load(i) : make_uint4(ninf, ninf, ninf, ninf);
     };
     float* s_sums = reinterpret_cast<float*>(s_keys + p.n_blocks);
     int slot = 0;
 
     if (tid == 0) {
-        s_n = s_bad = 0;
+        s_bad = 0;
         s_kth = 0ull;
         s_lo = 0xffffffffu;
         s_hi = 0u;
@@ -349,119 +372,157 @@ __device__ __forceinline__ void top_pick(const TopLogitsParams& p, int row, uint
     // the chosen blocks once more: entries at or above the pivot are candidates, the others
     // belong to the rest
     Run rest, taken;
-    // a word's entries from `least` on are pushed; the word without them
-    auto push = [&](int b, int l, const uint4& w, float least) {
-        uint32_t above = 0u;
-#pragma unroll
-        for (int k = 0; k < E; ++k) above |= word_entry<T>(w, k) >= least ? 1u << k : 0u;
-        int at = atomicAdd(&s_n, __popc(above));
-        for (uint32_t a = above; a; a &= a - 1u, ++at) {
-            const int k = __ffs(a) - 1;
-            if (at < kTopCandMax) s_cand[at] = argmax_key(word_pick<T>(w, k), (uint32_t)(in.entry(b * 32 + l) + k));
-        }
-        return word_without<T>(w, above);
+    // The chosen blocks' words in the list's order, 32 at a time (a warp's load): `u`, lane.
+    auto listed_word = [&](int u, int l) {
+        const int i = u * PER + l / LANES;
+        return i < nb ? word_at(s_blk[i], l % LANES) : make_uint4(ninf, ninf, ninf, ninf);
     };
-    auto over_blocks = [&](auto&& body) {   // a warp's share of the chosen blocks, kTopAgain loads at a time
-        for (int q0 = warp; q0 < nb; q0 += kTopAgain * kTopWarps) {
+    auto over_blocks = [&](auto&& body) {   // a warp's share of them, kTopAgain loads at a time
+        for (int u0 = warp; u0 * PER < nb; u0 += kTopAgain * kTopWarps) {
             uint4 w[kTopAgain];
 #pragma unroll
-            for (int h = 0; h < kTopAgain; ++h)
-                w[h] = q0 + h * kTopWarps < nb ? word_at(s_blk[q0 + h * kTopWarps], lane) : make_uint4(ninf, ninf, ninf, ninf);
-            body(q0, w);
+            for (int h = 0; h < kTopAgain; ++h) w[h] = listed_word(u0 + h * kTopWarps, lane);
+            body(u0, w);
         }
     };
-    const float least = key_floor(floor_key);   // (a key of 1 stands for the lowest float: every finite entry)
-    // the words that hold such an entry are noted, the others summed
-    over_blocks([&](int q0, uint4 (&w)[kTopAgain]) {
+    // Entries of listed words from `least` on become candidates, in the words' order; `body` gets
+    // the word without them.  Returns the candidates' number (which may pass the room).
+    auto candidates = [&](int n_words, float least, auto&& body) {
+        int n = 0;
+        for (int i0 = 0; i0 < n_words; i0 += kTopThreads) {
+            const int i = i0 + tid, at_word = i < n_words ? s_word[i] : 0;
+            uint4 w = make_uint4(ninf, ninf, ninf, ninf);
+            if (i < n_words) w = listed_word(at_word >> 5, at_word & 31);
+            uint32_t above = 0u;
+#pragma unroll
+            for (int k = 0; k < E; ++k) above |= word_entry<T>(w, k) >= least ? 1u << k : 0u;
+            int at = n + cta_prefix(__popc(above), s_part, slot);
+            n += cta_sum(__popc(above), s_part, slot);
+            const int e0 = in.entry(s_blk[(at_word >> 5) * PER + (at_word & 31) / LANES] * LANES + (at_word & 31) % LANES);
+            for (uint32_t a = above; a; a &= a - 1u, ++at) {
+                const int k = __ffs(a) - 1;
+                if (at < kTopCandMax) s_cand[at] = argmax_key(word_pick<T>(w, k), (uint32_t)(e0 + k));
+            }
+            body(word_without<T>(w, above));
+        }
+        __syncthreads();
+        return n;
+    };
+    // the words that hold an entry at or above the pivot are noted, the others summed
+    float least = key_floor(floor_key);   // (a key of 1 stands for the lowest float: every finite entry)
+    over_blocks([&](int u0, uint4 (&w)[kTopAgain]) {
         float mx = -INFINITY;
 #pragma unroll
         for (int h = 0; h < kTopAgain; ++h) {
             const float wm = u4_max_nan<sizeof(T)>(w[h]);
             const bool hit = wm >= least;
             const unsigned who = __ballot_sync(0xffffffffu, hit);
-            if (lane == 0 && q0 + h * kTopWarps < nb) s_hit[q0 + h * kTopWarps] = who;
+            if (lane == 0 && (u0 + h * kTopWarps) * PER < nb) s_hit[u0 + h * kTopWarps] = who;
             if (hit) w[h] = make_uint4(ninf, ninf, ninf, ninf);
             else mx = fmaxf(mx, wm);
         }
         rest.words<T, kTopAgain>(w, mx, p.scale);
     });
     __syncthreads();
-    // then looked at in parallel, a thread each, in the blocks' order
-    unsigned who = tid < nb ? s_hit[tid] : 0u;
+    // then looked at in parallel, a thread each
+    unsigned who = tid * PER < nb ? s_hit[tid] : 0u;
     const int n_hit = cta_sum(__popc(who), s_part, slot);
     int at = cta_prefix(__popc(who), s_part, slot);
     for (; who; who &= who - 1u, ++at)
         if (at < kTopCandMax) s_word[at] = tid * 32 + __ffs(who) - 1;
     __syncthreads();
-    for (int i = tid; i < n_hit && i < kTopCandMax; i += kTopThreads) {
-        const int b = s_blk[s_word[i] >> 5], l = s_word[i] & 31;
-        const uint4 one[1] = {push(b, l, word_at(b, l), least)};
-        rest.words<T, 1>(one, u4_max_nan<sizeof(T)>(one[0]), p.scale);
-    }
-    __syncthreads();
-    int n = s_n;
-    const bool exact_words = n > kTopCandMax || n_hit > kTopCandMax;
+    int n = kTopCandMax + 1;
+    if (n_hit <= kTopCandMax)
+        n = candidates(n_hit, least, [&](const uint4& w) {
+            const uint4 one[1] = {w};
+            rest.words<T, 1>(one, u4_max_nan<sizeof(T)>(w), p.scale);
+        });
+    const bool exact_words = n > kTopCandMax;
     if (exact_words) {
         // equal values in numbers: the K largest word maxima of (exactly) K blocks, in the
         // blocks' order
         __syncthreads();
         if (!exact_blocks) nb = pick_largest(s_keys, p.n_blocks, K, s_blk, floor_key, s_part, slot);
         __syncthreads();
-        uint32_t* s_wkeys = s_keys + 2 * p.n_blocks;   // [K * 32]
-        over_blocks([&](int q0, uint4 (&w)[kTopAgain]) {
-            for (int h = 0; h < kTopAgain && q0 + h * kTopWarps < nb; ++h)
-                s_wkeys[(q0 + h * kTopWarps) * 32 + lane] = value_key(u4_max_nan<sizeof(T)>(w[h]));
+        uint32_t* s_wkeys = s_keys + 2 * p.n_blocks;   // [K * LANES]
+        over_blocks([&](int u0, uint4 (&w)[kTopAgain]) {
+#pragma unroll
+            for (int h = 0; h < kTopAgain; ++h) {
+                const int i = (u0 + h * kTopWarps) * 32 + lane;
+                if (i < nb * LANES) s_wkeys[i] = value_key(u4_max_nan<sizeof(T)>(w[h]));
+            }
         });
-        if (tid == 0) s_n = 0;
         __syncthreads();
-        const int nw = pick_largest(s_wkeys, nb * 32, K, s_word, floor_key, s_part, slot);
-        for (int i = tid; i < nw; i += kTopThreads) {
-            const int b = s_blk[s_word[i] >> 5], l = s_word[i] & 31;
-            push(b, l, word_at(b, l), key_floor(floor_key));
+        const int nw = pick_largest(s_wkeys, nb * LANES, K, s_word, floor_key, s_part, slot);
+        n = candidates(nw, key_floor(floor_key), [](const uint4&) {});
+    }
+    // Many more candidates than K (few blocks, or equal values): a bisection over them first, so
+    // that few are ranked.
+    uint32_t pivot = 0u;
+    if (n > 2 * K + kTopSlack) {
+        uint32_t a = 0xffffffffu, b = 0u;
+        for (int i = tid; i < n; i += kTopThreads) {
+            a = min(a, (uint32_t)(s_cand[i] >> 32));
+            b = max(b, (uint32_t)(s_cand[i] >> 32));
+        }
+        if (tid == 0) {
+            s_lo = 0xffffffffu;
+            s_hi = 0u;
         }
         __syncthreads();
-        n = s_n;   // (s_word is free again)
+        atomicMin(&s_lo, a);
+        atomicMax(&s_hi, b);
+        __syncthreads();
+        uint32_t l = s_lo, h = s_hi;   // count(l) >= K; stops where count(h + 1) < K
+        int c = n;
+        while (l < h && c > K + kTopSlack) {
+            const uint32_t mid = l + (h - l) / 2u + 1u;
+            int cnt = 0;
+            for (int i = tid; i < n; i += kTopThreads) cnt += (uint32_t)(s_cand[i] >> 32) >= mid ? 1 : 0;
+            cnt = cta_sum(cnt, s_part, slot);
+            if (cnt >= K) { l = mid; c = cnt; }
+            else h = mid - 1u;
+        }
+        pivot = l;
     }
     // ranks: eight threads share a candidate's comparisons, a warp sees four candidates
     for (int i0 = 0; i0 < n; i0 += kTopThreads / 8) {
         const int i = i0 + tid / 8;
         const unsigned long long key = i < n ? s_cand[i] : 0ull;
-        int rank = 0;
+        const bool ranked = i < n && (uint32_t)(key >> 32) >= pivot;
+        int rank = K;
+        if (__any_sync(0xffffffffu, ranked)) {
+            int r = 0;
 #pragma unroll 4
-        for (int j = tid & 7; j < n; j += 8) rank += s_cand[j] > key ? 1 : 0;
-        rank += __shfl_xor_sync(0xffffffffu, rank, 1);
-        rank += __shfl_xor_sync(0xffffffffu, rank, 2);
-        rank += __shfl_xor_sync(0xffffffffu, rank, 4);
-        if ((tid & 7) == 0 && i < n) s_word[i] = rank;
-    }
-    __syncthreads();
-    for (int i = tid; i < n; i += kTopThreads) {
-        const unsigned long long key = s_cand[i];
-        const int rank = s_word[i];
+            for (int j = tid & 7; j < n; j += 8) r += s_cand[j] > key ? 1 : 0;
+            r += __shfl_xor_sync(0xffffffffu, r, 1);
+            r += __shfl_xor_sync(0xffffffffu, r, 2);
+            r += __shfl_xor_sync(0xffffffffu, r, 4);
+            if (ranked) rank = r;
+        }
+        if ((tid & 7) != 0 || i >= n) continue;
         const float x = key_value(key);
-        s_sorted[rank] = x;
         if (rank < K) {
             values[rank] = x;
             ids[rank] = (int)key_index(key);
             if (rank == K - 1) s_kth = key;
+            taken.entry(x, p.scale);
+        } else if (!exact_words) {
+            rest.entry(x, p.scale);
         }
     }
     __syncthreads();
-    // summed in the order of their ranks: the candidates came in any order
-    for (int i = tid; i < n; i += kTopThreads) {
-        if (i < K) taken.entry(s_sorted[i], p.scale);
-        else if (!exact_words) rest.entry(s_sorted[i], p.scale);
-    }
     for (int k = n + tid; k < K; k += kTopThreads) { values[k] = -INFINITY; ids[k] = -1; }
     if (exact_words) {   // the chosen blocks' entries that were not taken, over again
         const unsigned long long kth = s_kth;   // 0 when every finite entry was taken
         rest = Run();
-        over_blocks([&](int q0, uint4 (&w)[kTopAgain]) {
+        over_blocks([&](int u0, uint4 (&w)[kTopAgain]) {
             float mx = -INFINITY;
 #pragma unroll
             for (int h = 0; h < kTopAgain; ++h) {
-                if (q0 + h * kTopWarps >= nb) continue;
-                const int e = in.entry(s_blk[q0 + h * kTopWarps] * 32 + lane);
+                const int i = (u0 + h * kTopWarps) * PER + lane / LANES;
+                if (i >= nb) continue;
+                const int e = in.entry(s_blk[i] * LANES + lane % LANES);
                 uint32_t taken_bits = 0u;
 #pragma unroll
                 for (int k = 0; k < E; ++k)
@@ -497,32 +558,34 @@ __device__ __forceinline__ void top_pick(const TopLogitsParams& p, int row, uint
 
 static size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
-size_t top_logits_workspace_bytes(int rows, int V) {
-    return kWsHeaderBytes + align256((size_t)rows * sizeof(unsigned)) + (size_t)rows * top_blocks(V, 4) * sizeof(float2);
+size_t top_logits_workspace_bytes(int rows, int K, int V) {
+    const int f32 = top_lanes(V, 4, K), bf16 = top_lanes(V, 2, K);
+    const int a = top_blocks(V, 4, f32), b = top_blocks(V, 2, bf16);
+    return kWsHeaderBytes + align256((size_t)rows * sizeof(unsigned)) + (size_t)rows * (a > b ? a : b) * sizeof(float2);
 }
 
-template <typename T>
-static cudaError_t top_launch(TopLogitsParams p, cudaStream_t stream) {
-    p.n_blocks = top_blocks(p.V, sizeof(T));
-    // a warp's blocks: eight (the most loads in flight) unless that leaves SMs without a CTA
+template <typename T, int LANES>
+static cudaError_t top_launch_lanes(TopLogitsParams p, cudaStream_t stream) {
+    p.n_blocks = top_blocks(p.V, sizeof(T), LANES);
+    const int loads = p.n_blocks * LANES / 32;
+    // a warp's loads: eight (the most in flight) unless that leaves SMs without a CTA
     p.batch = kTopBatch;
-    while (p.batch > 1 && (long)p.rows * ((p.n_blocks + kTopWarps * p.batch - 1) / (kTopWarps * p.batch)) < device_sm_count())
+    while (p.batch > 1 && (long)p.rows * ((loads + kTopWarps * p.batch - 1) / (kTopWarps * p.batch)) < device_sm_count())
         p.batch /= 2;
-    p.pieces = (p.n_blocks + kTopWarps * p.batch - 1) / (kTopWarps * p.batch);
+    p.pieces = (loads + kTopWarps * p.batch - 1) / (kTopWarps * p.batch);
     const long grid = (long)p.rows * p.pieces;
     if (grid > 0x7fffffffL) return cudaErrorInvalidConfiguration;
-    const size_t smem = ((size_t)p.n_blocks * 2 + (size_t)p.K * 32) * 4;
+    const bool aligned = SegWords<T, true>::fits(p.ld, p.V);
+    const void* scan = aligned ? (const void*)top_kernel<T, true, LANES> : (const void*)top_kernel<T, false, LANES>;
+    const void* pick = (const void*)top_pick_kernel<T, LANES>;
+    const size_t smem = ((size_t)p.n_blocks * 2 + (size_t)p.K * LANES) * 4;
     p.pick_apart = p.rows >= kTopApart;
     if (smem > 28 * 1024) {
-        const void* kern = p.pick_apart ? (const void*)top_pick_kernel<T>
-                                        : (SegWords<T, true>::fits(p.ld, p.V) ? (const void*)top_kernel<T, true>
-                                                                              : (const void*)top_kernel<T, false>);
-        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        const cudaError_t e = cudaFuncSetAttribute(p.pick_apart ? pick : scan, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
     }
-    if (SegWords<T, true>::fits(p.ld, p.V)) top_kernel<T, true><<<(unsigned)grid, kTopThreads, p.pick_apart ? 0 : smem, stream>>>(p);
-    else top_kernel<T, false><<<(unsigned)grid, kTopThreads, p.pick_apart ? 0 : smem, stream>>>(p);
-    const cudaError_t e = cudaGetLastError();
+    void* args[] = {&p};
+    const cudaError_t e = cudaLaunchKernel(scan, dim3((unsigned)grid), dim3(kTopThreads), args, p.pick_apart ? 0 : smem, stream);
     if (e != cudaSuccess || !p.pick_apart) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)p.rows);
@@ -534,7 +597,11 @@ static cudaError_t top_launch(TopLogitsParams p, cudaStream_t stream) {
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, top_pick_kernel<T>, p);
+    return cudaLaunchKernelEx(&cfg, top_pick_kernel<T, LANES>, p);
+}
+template <typename T>
+static cudaError_t top_launch(const TopLogitsParams& p, cudaStream_t stream) {
+    return top_lanes(p.V, sizeof(T), p.K) == 32 ? top_launch_lanes<T, 32>(p, stream) : top_launch_lanes<T, 4>(p, stream);
 }
 
 cudaError_t top_logits_launch(TopLogitsParams p, void* ws, cudaStream_t stream) {
