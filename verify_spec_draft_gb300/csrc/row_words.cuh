@@ -77,6 +77,15 @@ __device__ __forceinline__ float word_entry(const uint4& w, int k) {
     return __uint_as_float(h[k & 3]);
 }
 
+// The same for a k known at run time only.
+template <typename T>
+__device__ __forceinline__ float word_pick(const uint4& w, int k) {
+    const int r = sizeof(T) == 2 ? k >> 1 : k;
+    const uint32_t h = (r & 2) ? ((r & 1) ? w.w : w.z) : ((r & 1) ? w.y : w.x);
+    if (sizeof(T) == 2) return __uint_as_float((k & 1) ? (h & 0xffff0000u) : (h << 16));
+    return __uint_as_float(h);
+}
+
 // Bits [e, e + 32) of a bit string, e >= 0 (one word past the end may be read).
 __device__ __forceinline__ uint32_t bits_at(const uint32_t* w, int e) {
     return __funnelshift_r(w[e >> 5], w[(e >> 5) + 1], e & 31);
@@ -161,6 +170,14 @@ __device__ __forceinline__ float ref_log(float m, float s, float c, float inv_t)
     const float x = m * c;
     return x > -INFINITY ? (x + log2f(s)) * 0.69314718055994531f : fmaf(m, inv_t, logf(s));
 }
+// A word's weights relative to a reference that overflows when scaled: out of line, since
+// hardly any row has one and the streaming loops are short without it.
+template <typename T>
+__device__ __noinline__ float word_sum_low(uint4 w, float m, float c) {
+    float s = 0.0f;
+    for (int k = 0; k < 16 / (int)sizeof(T); ++k) s += ex2((word_pick<T>(w, k) - m) * c);
+    return s;
+}
 // The sum of the weights of N words relative to m (0 for m = -inf).
 template <typename T, int N>
 __device__ __forceinline__ float words_sum(const uint4 (&w)[N], float m, float c) {
@@ -175,24 +192,14 @@ __device__ __forceinline__ float words_sum(const uint4 (&w)[N], float m, float c
             for (int k = 0; k < 16 / (int)sizeof(T); k += 2)
                 acc[(k >> 1) & 1] = f2_add(acc[(k >> 1) & 1],
                     f2_ex2(f2_fma(f2_pack(word_entry<T>(w[h], k), word_entry<T>(w[h], k + 1)), cc, mm)));
-    } else if (m > -INFINITY) {
-        const f2x mm = f2_pack(-m, -m);
-        for (int h = 0; h < N; ++h)
-            for (int k = 0; k < 16 / (int)sizeof(T); k += 2)
-                acc[0] = f2_add(acc[0],
-                    f2_ex2(f2_mul(f2_add(f2_pack(word_entry<T>(w[h], k), word_entry<T>(w[h], k + 1)), mm), cc)));
+    } else {
+        if (!(m > -INFINITY)) return 0.0f;
+        float s = 0.0f;
+        for (int h = 0; h < N; ++h) s += word_sum_low<T>(w[h], m, c);
+        return s;
     }
     const float2 a = f2_unpack(acc[0]), b = f2_unpack(acc[1]);
     return (a.x + a.y) + (b.x + b.y);
-}
-
-// The same for a k known at run time only.
-template <typename T>
-__device__ __forceinline__ float word_pick(const uint4& w, int k) {
-    const int r = sizeof(T) == 2 ? k >> 1 : k;
-    const uint32_t h = (r & 2) ? ((r & 1) ? w.w : w.z) : ((r & 1) ? w.y : w.x);
-    if (sizeof(T) == 2) return __uint_as_float((k & 1) ? (h & 0xffff0000u) : (h << 16));
-    return __uint_as_float(h);
 }
 
 // -inf in the entries of a word whose bit is set.

@@ -63,7 +63,7 @@ __device__ __forceinline__ float warp_sum8(float (&v)[8]) {
 }
 
 // s_keys: the blocks' keys [n_blocks] and sums [n_blocks], then room for 32 words per entry.
-template <typename T, int LANES>
+template <typename T, bool ALIGNED, int LANES>
 __device__ __forceinline__ void top_pick(const TopLogitsParams& p, int row, uint32_t* s_keys);
 
 // The blocks of one piece, then, in the CTA that finishes its row's last piece, the pick.
@@ -124,15 +124,15 @@ __global__ void __launch_bounds__(kTopThreads) top_kernel(TopLogitsParams p) {
     }
     if (!last_block_done(&p.done[row], (unsigned)p.pieces)) return;
     if (threadIdx.x == 0) p.done[row] = 0u;
-    top_pick<T, LANES>(p, row, s_keys);
+    top_pick<T, ALIGNED, LANES>(p, row, s_keys);
 }
 
 // The picks of all rows, launched behind the scan as its programmatic dependent.
-template <typename T, int LANES>
+template <typename T, bool ALIGNED, int LANES>
 __global__ void __launch_bounds__(kTopThreads) top_pick_kernel(TopLogitsParams p) {
     extern __shared__ __align__(16) uint32_t s_keys[];
     pdl_wait_primary();
-    top_pick<T, LANES>(p, blockIdx.x, s_keys);
+    top_pick<T, ALIGNED, LANES>(p, blockIdx.x, s_keys);
 }
 
 // Sum of one int per thread over the CTA; `slot` alternates between calls.
@@ -168,7 +168,7 @@ __device__ __forceinline__ int cta_prefix(int v, int* s_part, int& slot) {
 
 // The (at most) K largest of keys[0..n) that are not 0, equal keys by the lower index, as
 // ascending indices in list[].  Returns their number; `floor_key` is the smallest of them.
-__device__ __forceinline__ int pick_largest(const uint32_t* keys, int n, int K, int* list, uint32_t& floor_key,
+__device__ __noinline__ int pick_largest(const uint32_t* keys, int n, int K, int* list, uint32_t& floor_key,
                                             int* s_part, int& slot) {
     const int per = (n + kTopThreads - 1) / kTopThreads;
     const int lo = min(n, (int)threadIdx.x * per), hi = min(n, lo + per);
@@ -279,11 +279,11 @@ __device__ __forceinline__ void list_above(const uint32_t* keys, int n, uint32_t
     __syncthreads();
 }
 
-template <typename T, int LANES>
+template <typename T, bool ALIGNED, int LANES>
 __device__ __forceinline__ void top_pick(const TopLogitsParams& p, int row, uint32_t* s_keys) {
     constexpr int E = 16 / (int)sizeof(T), PER = 32 / LANES;   // blocks of a warp's load
     __shared__ unsigned long long s_cand[kTopCandMax];
-    __shared__ int s_word[kTopCandMax];                      // listed words to look at
+    __shared__ int s_word[kTopCandMax];                      // listed words to look at, then ranks
     __shared__ unsigned s_hit[kTopBlkMax];
     __shared__ int s_blk[kTopBlkMax], s_part[2 * kTopWarps], s_bad;
     __shared__ uint32_t s_lo, s_hi;
@@ -291,14 +291,14 @@ __device__ __forceinline__ void top_pick(const TopLogitsParams& p, int row, uint
     __shared__ float4 s_run[kTopWarps];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int K = p.K;
-    const RowWords<T> in(reinterpret_cast<const T*>(p.logits) + (long)row * p.ld, p.V);
+    const SegWords<T, ALIGNED> in(reinterpret_cast<const T*>(p.logits) + (long)row * p.ld, p.V);
     const float2* blk = p.blocks + (long)row * p.n_blocks;
     float* values = p.values_out + (long)row * K;
     int32_t* ids = p.ids_out + (long)row * K;
     const uint32_t ninf = NegInf<T>::word;
     auto word_at = [&](int b, int l) {   // word l of block b
         const int i = b * LANES + l;
-        return i < in.n ? in.load(i) : make_uint4(ninf, ninf, ninf, ninf);
+        return i < in.n() ? in.load(i) : make_uint4(ninf, ninf, ninf, ninf);
     };
     float* s_sums = reinterpret_cast<float*>(s_keys + p.n_blocks);
     int slot = 0;
@@ -490,17 +490,22 @@ __device__ __forceinline__ void top_pick(const TopLogitsParams& p, int row, uint
         const int i = i0 + tid / 8;
         const unsigned long long key = i < n ? s_cand[i] : 0ull;
         const bool ranked = i < n && (uint32_t)(key >> 32) >= pivot;
-        int rank = K;
-        if (__any_sync(0xffffffffu, ranked)) {
-            int r = 0;
-#pragma unroll 4
-            for (int j = tid & 7; j < n; j += 8) r += s_cand[j] > key ? 1 : 0;
-            r += __shfl_xor_sync(0xffffffffu, r, 1);
-            r += __shfl_xor_sync(0xffffffffu, r, 2);
-            r += __shfl_xor_sync(0xffffffffu, r, 4);
-            if (ranked) rank = r;
+        if (!__any_sync(0xffffffffu, ranked)) {
+            if ((tid & 7) == 0 && i < n) s_word[i] = K;
+            continue;
         }
-        if ((tid & 7) != 0 || i >= n) continue;
+        int r = 0;
+#pragma unroll 4
+        for (int j = tid & 7; j < n; j += 8) r += s_cand[j] > key ? 1 : 0;
+        r += __shfl_xor_sync(0xffffffffu, r, 1);
+        r += __shfl_xor_sync(0xffffffffu, r, 2);
+        r += __shfl_xor_sync(0xffffffffu, r, 4);
+        if ((tid & 7) == 0 && i < n) s_word[i] = ranked ? r : K;
+    }
+    __syncthreads();
+    for (int i = tid; i < n; i += kTopThreads) {
+        const unsigned long long key = s_cand[i];
+        const int rank = s_word[i];
         const float x = key_value(key);
         if (rank < K) {
             values[rank] = x;
@@ -577,11 +582,11 @@ static cudaError_t top_launch_lanes(TopLogitsParams p, cudaStream_t stream) {
     if (grid > 0x7fffffffL) return cudaErrorInvalidConfiguration;
     const bool aligned = SegWords<T, true>::fits(p.ld, p.V);
     const void* scan = aligned ? (const void*)top_kernel<T, true, LANES> : (const void*)top_kernel<T, false, LANES>;
-    const void* pick = (const void*)top_pick_kernel<T, LANES>;
+    const auto pick = aligned ? top_pick_kernel<T, true, LANES> : top_pick_kernel<T, false, LANES>;
     const size_t smem = ((size_t)p.n_blocks * 2 + (size_t)p.K * LANES) * 4;
     p.pick_apart = p.rows >= kTopApart;
     if (smem > 28 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(p.pick_apart ? pick : scan, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        const cudaError_t e = cudaFuncSetAttribute(p.pick_apart ? (const void*)pick : scan, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
     }
     void* args[] = {&p};
@@ -597,7 +602,7 @@ static cudaError_t top_launch_lanes(TopLogitsParams p, cudaStream_t stream) {
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, top_pick_kernel<T, LANES>, p);
+    return cudaLaunchKernelEx(&cfg, pick, p);
 }
 template <typename T>
 static cudaError_t top_launch(const TopLogitsParams& p, cudaStream_t stream) {
