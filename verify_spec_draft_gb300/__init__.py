@@ -177,14 +177,18 @@ def _need_rows(t, name, device=None):
     return ld or V
 
 
-def _addr(t, name, device, dtype, shape):
-    """The address of an optional contiguous tensor, checked as _need does (which says what
-    is wrong); None for None."""
-    if t is None:
-        return None
-    if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
-        _need(t, name, device, dtype, shape)
-    return t.data_ptr()
+def _addrs(device, names, tensors, dtypes, shapes):
+    """The addresses of optional contiguous tensors (None for None), checked as _need does,
+    which says what is wrong; one loop, since a call's checks are most of its host time."""
+    index, out = device.index, []
+    for name, t, dtype, shape in zip(names, tensors, dtypes, shapes):
+        if t is None:
+            out.append(None)
+            continue
+        if t.dtype is not dtype or t.get_device() != index or t.shape != shape or not t.is_contiguous():
+            _need(t, name, device, dtype, shape)
+        out.append(t.data_ptr())
+    return out
 
 
 _HERE = contextlib.nullcontext()
@@ -588,6 +592,10 @@ def draft_block_topk(logits, anchor, U, Wt, top_k, top_p, seeds, ws=None, out=No
 # ---------------------------------------------------------------------------------
 # the rows before verification, and what a drafter learns from them
 # ---------------------------------------------------------------------------------
+_PROCESS_NAMES = ("history", "lengths", "prompt_lengths", "block", "repetition", "frequency", "presence",
+                  "temperature", "bias_ids", "bias_values", "mask")
+
+
 def process_logits(logits, history=None, lengths=None, prompt_lengths=None, block=None, repetition=None,
                    frequency=None, presence=None, bias_ids=None, bias_values=None, mask=None, temperature=None,
                    ws=None, out=None, stream=None):
@@ -618,16 +626,13 @@ def process_logits(logits, history=None, lengths=None, prompt_lengths=None, bloc
         nb = bias_ids.shape[1]
     W = (V + 31) // 32
     mask_rows, masks = (R, (B, R, W)) if mask is not None and mask.dim() == 3 else (1, (B, W))
-    a_hist = _addr(history, "history", dev, i32, (B, Lmax))
-    a_block = _addr(block, "block", dev, i32, (B, R - 1))
-    a_ids = _addr(bias_ids, "bias_ids", dev, i32, (B, nb))
-    a_values = _addr(bias_values, "bias_values", dev, f32, (B, nb))
-    a_mask = _addr(mask, "mask", dev, i32, masks)
-    per = (B,)
-    args = (_addr(lengths, "lengths", dev, i32, per), _addr(prompt_lengths, "prompt_lengths", dev, i32, per),
-            a_block if R > 1 else None, _addr(repetition, "repetition", dev, f32, per),
-            _addr(frequency, "frequency", dev, f32, per), _addr(presence, "presence", dev, f32, per),
-            _addr(temperature, "temperature", dev, f32, per))
+    per, biases = (B,), (B, nb)
+    (a_hist, a_len, a_prompt, a_block, a_rep, a_freq, a_pres, a_temp, a_ids, a_values, a_mask) = _addrs(
+        dev, _PROCESS_NAMES,
+        (history, lengths, prompt_lengths, block, repetition, frequency, presence, temperature, bias_ids,
+         bias_values, mask),
+        (i32, i32, i32, i32, f32, f32, f32, f32, i32, f32, i32),
+        ((B, Lmax), per, per, (B, R - 1), per, per, per, per, biases, biases, masks))
     if out is None:
         with _made_on(stream):
             out = dict(logits=_rows_like(logits, ld))
@@ -637,9 +642,9 @@ def process_logits(logits, history=None, lengths=None, prompt_lengths=None, bloc
         with _made_on(stream):
             ws = workspace(OP_PROCESS_LOGITS, B, R, V, 0, dev, stream)
     code = lib.spec_process_logits(
-        logits.data_ptr(), _dtype_code(logits), B, R, V, ld, a_hist if Lmax else None, Lmax, *args,
-        a_ids if nb else None, a_values if nb else None, nb, a_mask, mask_rows, out["logits"].data_ptr(),
-        ws.data_ptr(), ws.numel(), _stream(stream))
+        logits.data_ptr(), _dtype_code(logits), B, R, V, ld, a_hist if Lmax else None, Lmax, a_len, a_prompt,
+        a_block if R > 1 else None, a_rep, a_freq, a_pres, a_temp, a_ids if nb else None, a_values if nb else None,
+        nb, a_mask, mask_rows, out["logits"].data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream))
     if code != OK:
         raise SpecError(code, "spec_process_logits")
     out["ws"] = ws
@@ -689,11 +694,12 @@ def distill(student, values, ids, tail=None, weight=None, temperature=1.0, grad=
     lead, V = shape[:-1], shape[-1]
     rows = student.numel() // V if V else 0
     K = ids.shape[-1] if ids is not None and ids.dim() else 0
+    if ids is None or values is None:
+        raise ValueError("values and ids are required")
     named = (*lead, K)
-    a_ids = _addr(_need(ids, "ids"), "ids", dev, torch.int32, named)
-    a_values = _addr(_need(values, "values"), "values", dev, values.dtype, named)
-    a_tail = _addr(tail, "tail", dev, torch.float32, lead)
-    a_weight = _addr(weight, "weight", dev, torch.float32, lead)
+    a_values, a_ids, a_tail, a_weight = _addrs(
+        dev, ("values", "ids", "tail", "weight"), (values, ids, tail, weight),
+        (values.dtype, torch.int32, torch.float32, torch.float32), (named, named, lead, lead))
     if out is None:
         with _made_on(stream):
             out = dict(loss=torch.empty(lead, dtype=torch.float32, device=dev),
