@@ -10,9 +10,9 @@
 // q_T is summed over the entries that no id names, never formed as 1 - sum q_k, so a rest
 // of 1e-9 still has its logarithm.
 //
-// Weights and sums are taken relative to a maximum (row_words.cuh), and logarithms of p and q
-// are differences from the two maxima, so the loss keeps float32's absolute accuracy
-// whatever the logits' offset.
+// Weights and sums are taken relative to a maximum, and logarithms of p and q are differences
+// from the two maxima, so the loss keeps float32's absolute accuracy whatever the logits'
+// offset.
 #include "internal.h"
 #include "row_words.cuh"
 
@@ -33,15 +33,32 @@ __device__ __forceinline__ float warp_max_nan(float x) {
     asm volatile("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
     return r;
 }
-// (maximum, sum of weights relative to it) pairs merged; NaN shows in the maximum.  ref_lanes: over
-// the N lanes that differ in their low bits.
-__device__ __forceinline__ float2 ref_merge(float2 a, float2 b, float c) {
+// Pairs (m2, s): s is the sum of the weights 2^(x c - m2) of some entries and m2 their maximum
+// times c, rounded once, so that two pairs meet by one subtraction.  NaN shows in m2.  A
+// maximum that overflows when scaled, which only rows filled with the type's lowest value
+// have, counts as kLow, its entries' weights taken from differences before the scaling.
+constexpr float kLow = -3.402823466e38f;
+template <typename T>
+__device__ __forceinline__ float lowest() { return sizeof(T) == 2 ? -3.38953139e38f : kLow; }
+__device__ __forceinline__ float scaled(float m, float c) { return m > -INFINITY ? fmaxf(m * c, kLow) : m; }
+// log2 of entry x's weight relative to m2
+template <typename T>
+__device__ __forceinline__ float rel(float x, float m2, float c) {
+    return m2 > kLow ? fmaf(x, c, -m2) : (x - lowest<T>()) * c;
+}
+// ln of s 2^m2
+template <typename T>
+__device__ __forceinline__ float pair_log(float m2, float s, float inv_t) {
+    return m2 > kLow ? (m2 + log2f(s)) * 0.69314718055994531f : fmaf(lowest<T>(), inv_t, logf(s));
+}
+__device__ __forceinline__ float2 pair_merge(float2 a, float2 b) {
     const float m = f_max_nan(a.x, b.x);
     float s = 0.0f;
-    if (a.x != -INFINITY) s += a.y * ex2(ref_diff(a.x, m, c));
-    if (b.x != -INFINITY) s += b.y * ex2(ref_diff(b.x, m, c));
+    if (a.x != -INFINITY) s += a.y * ex2(a.x - m);
+    if (b.x != -INFINITY) s += b.y * ex2(b.x - m);
     return make_float2(m, s);
 }
+// Over the N lanes that differ in their low bits.
 template <int N>
 __device__ __forceinline__ float lanes_max_nan(float m) {
 #pragma unroll
@@ -55,19 +72,20 @@ __device__ __forceinline__ float lanes_sum(float s) {
     return s;
 }
 template <int N>
-__device__ __forceinline__ float2 ref_lanes(float2 v, float c) {
-    const float m = lanes_max_nan<N>(v.x);
-    return make_float2(m, lanes_sum<N>(v.x == -INFINITY ? 0.0f : v.y * ex2(ref_diff(v.x, m, c))));
+__device__ __forceinline__ float2 pair_lanes(float2 v) {
+    const float m = N == 32 ? warp_max_nan(v.x) : lanes_max_nan<N>(v.x);
+    return make_float2(m, lanes_sum<N>(v.x == -INFINITY ? 0.0f : v.y * ex2(v.x - m)));
 }
 // The pair of one entry per lane.
-__device__ __forceinline__ float2 ref_entries(float x, float c) {
-    const float m = lanes_max_nan<32>(x);
-    return make_float2(m, lanes_sum<32>(x == -INFINITY ? 0.0f : ex2(ref_rel(x, m, c))));
+template <typename T>
+__device__ __forceinline__ float2 pair_entries(float x, float c) {
+    const float m2 = scaled(warp_max_nan(x), c);
+    return make_float2(m2, lanes_sum<32>(x == -INFINITY ? 0.0f : ex2(rel<T>(x, m2, c))));
 }
 // The teacher's pairs: (maximum, sum of e^(x - maximum)).
 template <int N>
 __device__ __forceinline__ float2 teacher_lanes(float2 v) {
-    const float m = lanes_max_nan<N>(v.x);
+    const float m = N == 32 ? warp_max_nan(v.x) : lanes_max_nan<N>(v.x);
     return make_float2(m, lanes_sum<N>(v.x == -INFINITY ? 0.0f : v.y * __expf(v.x - m)));
 }
 
@@ -77,14 +95,15 @@ constexpr uint32_t kBadToken = 0x7fc0dead;   // a NaN that says: an id is listed
 // The loss of a named entry (teacher's logit a, student's z) and of the rest.  top, P: the
 // teacher's pair, in units of 1; (M, Z) the student's, (mT, sT) that of its unnamed entries.
 struct RowStats { float M, Z, mT, sT, top, P; };
+template <typename T>
 __device__ __forceinline__ float entry_loss(const RowStats& r, float a, float z, float c, float inv_t) {
     const float lt = fmaf(a, inv_t, -r.top), pk = __expf(lt) / r.P;
-    return pk > 0.0f ? pk * ((lt - logf(r.P)) - (ref_rel(z, r.M, c) - log2f(r.Z)) * kLn2) : 0.0f;
+    return pk > 0.0f ? pk * ((lt - logf(r.P)) - (rel<T>(z, r.M, c) - log2f(r.Z)) * kLn2) : 0.0f;
 }
-__device__ __forceinline__ float rest_loss(const RowStats& r, float aT, float c) {
+__device__ __forceinline__ float rest_loss(const RowStats& r, float aT) {
     const float pT = __expf(aT - r.top) / r.P;
     if (!(pT > 0.0f)) return 0.0f;
-    const float lq = r.mT > -INFINITY ? (ref_diff(r.mT, r.M, c) + log2f(r.sT) - log2f(r.Z)) * kLn2 : -INFINITY;
+    const float lq = r.mT > -INFINITY ? (r.mT - r.M + log2f(r.sT) - log2f(r.Z)) * kLn2 : -INFINITY;
     return pT * (((aT - r.top) - logf(r.P)) - lq);
 }
 
@@ -151,10 +170,10 @@ __global__ void __launch_bounds__(kDistThreads) distill_loss_kernel(DistillParam
     for (int q = 0; q < kDistWords; ++q) m = f_max_nan(m, u4_max_nan<sizeof(T)>(w[q]));
     m = warp_max_nan(m);   // a NaN or +inf shows in the maximum
     const float s = warp_sum(words_sum<T, kDistWords>(w, m, p.scale));
-    if (lane == 0) s_run[tid >> 5] = make_float2(m, s);
+    if (lane == 0) s_run[tid >> 5] = make_float2(scaled(m, p.scale), s);
     __syncthreads();
     if (tid < 32) {
-        float2 t = ref_lanes<kDistWarps>(s_run[lane % kDistWarps], p.scale);
+        float2 t = pair_lanes<kDistWarps>(s_run[lane % kDistWarps]);
         if (s_twice) t.x = __uint_as_float(kBadToken);
         if (lane == 0) __stcg(&p.parts[(long)row * p.pieces + piece], t);
     }
@@ -185,12 +204,12 @@ __device__ __forceinline__ void distill_finish(const DistillParams& p, int row, 
     for (int i = tid; i < p.pieces; i += kDistThreads) {
         const float2 v = __ldcg(&p.parts[(long)row * p.pieces + i]);
         if (__float_as_uint(v.x) == kBadToken) flag |= 1;
-        t = ref_merge(t, v, p.scale);
+        t = pair_merge(t, v);
     }
     if (!(a * p.inv_t < INFINITY) || !(aT < INFINITY) || !(fabsf(wt) < INFINITY)) flag |= 2;
     if (tid == 0) s_flag = 0;
-    t = ref_lanes<32>(t, p.scale);
-    const float2 n = ref_entries(z, p.scale);
+    t = pair_lanes<32>(t);
+    const float2 n = pair_entries<T>(z, p.scale);
     const float2 y = teacher_lanes<32>(make_float2(a * p.inv_t, 1.0f));
     if (lane == 0) {
         s_tail[warp] = t;
@@ -200,15 +219,15 @@ __device__ __forceinline__ void distill_finish(const DistillParams& p, int row, 
     __syncthreads();
     if (flag) atomicOr(&s_flag, flag);
     // every warp puts the whole together
-    const float2 T2 = ref_lanes<kDistWarps>(s_tail[lane % kDistWarps], p.scale);
-    const float2 A = ref_merge(T2, ref_lanes<kDistWarps>(s_top[lane % kDistWarps], p.scale), p.scale);
+    const float2 T2 = pair_lanes<kDistWarps>(s_tail[lane % kDistWarps]);
+    const float2 A = pair_merge(T2, pair_lanes<kDistWarps>(s_top[lane % kDistWarps]));
     const int w = lane & 15;
     const float2 N = teacher_lanes<16>(w < kDistWarps ? s_teach[w] : (w == kDistWarps ? make_float2(aT, 1.0f) : none));
     const RowStats r = {A.x, A.y, T2.x, T2.y, N.x, N.y};
     float l = 0.0f;
     if (r.top > -INFINITY) {
-        if (there) l = entry_loss(r, a, z, p.scale, p.inv_t);
-        if (tid == 0) l += rest_loss(r, aT, p.scale);
+        if (there) l = entry_loss<T>(r, a, z, p.scale, p.inv_t);
+        if (tid == 0) l += rest_loss(r, aT);
     }
     l = warp_sum(l);
     if (lane == 0) s_loss[warp] = l;
@@ -218,7 +237,7 @@ __device__ __forceinline__ void distill_finish(const DistillParams& p, int row, 
         l = s_loss[0];
         for (int i = 1; i < kDistWarps; ++i) l += s_loss[i];
         p.loss_out[row] = bad ? NAN : l;
-        if (p.lse_out) p.lse_out[row] = bad ? NAN : ref_log(r.M, r.Z, p.scale, p.inv_t);
+        if (p.lse_out) p.lse_out[row] = bad ? NAN : pair_log<T>(r.M, r.Z, p.inv_t);
         if (s_flag & 1) atomicOr(p.status, SPEC_DEV_TOKEN);
         if ((s_flag & 2) || (bad && !(s_flag & 1))) atomicOr(p.status, SPEC_DEV_NONFINITE);
     }
@@ -231,7 +250,7 @@ __device__ __forceinline__ void distill_finish(const DistillParams& p, int row, 
 // to the write of the gradient, so the logits are read once and the gradient is written once.
 // The warps of a CTA have four jobs and meet at mbarriers only:
 //   dense     A(i): the slice's (maximum, sum) over the entries that no id names;
-//             B(i): every logit in the slot becomes its gradient, 2^((z - m) c) times one
+//             B(i): every logit in the slot becomes its gradient, 2^(z c - m2) times one
 //             factor.  In the order A(0) A(1) B(0) A(2) B(1) ..
 //   exchange  posts the slice's statistics, waits for the other slices', forms the factor
 //   entries   one thread per teacher entry: takes the named logits out of the slice (-inf),
@@ -286,10 +305,10 @@ __device__ __forceinline__ void named_sync() { asm volatile("bar.sync 1, %0;" ::
 
 // What is known of a row once its slices' statistics are together.
 struct FuseRow {
-    float ref;        // unnamed entries: gradient 2^((z - ref) c) factor
+    float ref;        // unnamed entries: gradient 2^(z c - ref) factor
     float factor;
-    float M, Z;       // all entries: maximum, sum
-    float mT, sT;     // the unnamed ones'
+    float M, Z;       // all entries: their pair
+    float mT, sT;     // the unnamed ones' pair
     float top, P;     // the teacher's normaliser
     int skip, bad;
 };
@@ -383,12 +402,12 @@ __global__ void __launch_bounds__(kFuseThreads, kFuseOcc) distill_fused_kernel(D
                         // a thread's own running maximum; a batch of -inf adds nothing
                         bm = f_max_nan(bm, m);
                         if (bm != m) {
-                            s = m == -INFINITY ? 0.0f : s * ex2(ref_diff(m, bm, c));
+                            s = m == -INFINITY ? 0.0f : s * ex2(scaled(m, c) - scaled(bm, c));
                             m = bm;
                         }
                         s += words_sum<T, kFuseBatch>(w, m, c);
                     }
-                    const float2 t = ref_lanes<32>(make_float2(m, s), c);
+                    const float2 t = pair_lanes<32>(make_float2(scaled(m, c), s));
                     if (lane == 0) s_tail[i & 1][warp] = t;
                 }
                 __syncwarp();
@@ -399,10 +418,10 @@ __global__ void __launch_bounds__(kFuseThreads, kFuseOcc) distill_fused_kernel(D
                 uint4* slot = slot_of(j);
                 wait(&s_known[j & 1], j >> 1);
                 const FuseRow& row = s_row[j & 1];
-                const float x = row.ref * c;
+                const float x = row.ref;
                 if (row.skip) {
                     for (int l = tid; l < n; l += kFuseDense) slot[l] = make_uint4(0u, 0u, 0u, 0u);
-                } else if (x > -INFINITY) {
+                } else if (x > kLow) {
                     const f2x mm = f2_pack(-x, -x), ff = f2_pack(row.factor, row.factor);
 #pragma unroll 4
                     for (int l = tid; l < n; l += kFuseDense) {
@@ -422,7 +441,7 @@ __global__ void __launch_bounds__(kFuseThreads, kFuseOcc) distill_fused_kernel(D
                         const uint4 w = slot[l];
                         float d[E];
 #pragma unroll
-                        for (int k = 0; k < E; ++k) d[k] = ex2((word_entry<T>(w, k) - row.ref) * c) * row.factor;
+                        for (int k = 0; k < E; ++k) d[k] = ex2(rel<T>(word_entry<T>(w, k), x, c)) * row.factor;
                         slot[l] = word_of<T>(d);
                     }
                 }
@@ -481,7 +500,7 @@ __global__ void __launch_bounds__(kFuseThreads, kFuseOcc) distill_fused_kernel(D
             if (e.wt != 0.0f) {
                 const float a = known_id(e) ? e.a * p.inv_t : -INFINITY;
                 const float2 t = teacher_lanes<32>(make_float2(a, 1.0f));
-                const float2 z = ref_entries(rank == 0 ? e.z : -INFINITY, c);
+                const float2 z = pair_entries<T>(rank == 0 ? e.z : -INFINITY, c);
                 if (lane == 0) {
                     s_teach[par][warp] = t;
                     s_top[par][warp] = z;
@@ -519,13 +538,13 @@ __global__ void __launch_bounds__(kFuseThreads, kFuseOcc) distill_fused_kernel(D
                 const bool taught = r.top > -INFINITY;
                 const float lt = known_id(cur) && taught ? fmaf(cur.a, p.inv_t, -r.top) : -INFINITY;
                 const float pk = taught ? __expf(lt) / r.P : 0.0f;
-                d = r.bad ? NAN : (taught ? (ex2(ref_rel(cur.z, r.M, c)) / r.Z - pk) * (cur.wt * p.inv_t) : 0.0f);
+                d = r.bad ? NAN : (taught ? (ex2(rel<T>(cur.z, r.M, c)) / r.Z - pk) * (cur.wt * p.inv_t) : 0.0f);
                 if (rank == 0) {
                     const RowStats st = {r.M, r.Z, r.mT, r.sT, r.top, r.P};
                     float l = 0.0f;
                     if (taught) {
-                        if (known_id(cur)) l = entry_loss(st, cur.a, cur.z, c, p.inv_t);
-                        if (k == 0) l += rest_loss(st, cur.aT, c);
+                        if (known_id(cur)) l = entry_loss<T>(st, cur.a, cur.z, c, p.inv_t);
+                        if (k == 0) l += rest_loss(st, cur.aT);
                     }
                     l = warp_sum(l);
                     if (lane == 0) s_loss[warp] = l;
@@ -537,7 +556,7 @@ __global__ void __launch_bounds__(kFuseThreads, kFuseOcc) distill_fused_kernel(D
                     float l = s_loss[0];
                     for (int q = 1; q < kNamedWarps; ++q) l += s_loss[q];
                     p.loss_out[row] = skip ? 0.0f : (r.bad ? NAN : l);
-                    if (p.lse_out) p.lse_out[row] = skip ? 0.0f : (r.bad ? NAN : ref_log(r.M, r.Z, p.scale, p.inv_t));
+                    if (p.lse_out) p.lse_out[row] = skip ? 0.0f : (r.bad ? NAN : pair_log<T>(r.M, r.Z, p.inv_t));
                 }
             }
             wait(&s_dense[par], i >> 1);
@@ -564,7 +583,7 @@ __global__ void __launch_bounds__(kFuseThreads, kFuseOcc) distill_fused_kernel(D
             const bool skip = wt == 0.0f;
             // the teacher's normaliser, and the named logits' (slice 0 has them)
             const float2 tt = teacher_lanes<8>(skip ? none : ((lane & 7) < kNamedWarps ? s_teach[par][lane & 7] : ((lane & 7) == kNamedWarps ? make_float2(aT, 1.0f) : none)));
-            const float2 nn = ref_lanes<4>(skip ? none : s_top[par][lane & 3], c);
+            const float2 nn = pair_lanes<4>(skip ? none : s_top[par][lane & 3]);
             static_assert(kNamedWarps == 4 && kDenseWarps <= 16, "the lanes' layout");
             const int flag = s_flag[par];
             float2 T2 = none, N2 = none;
@@ -574,7 +593,7 @@ __global__ void __launch_bounds__(kFuseThreads, kFuseOcc) distill_fused_kernel(D
                 unsigned long long* rec = recs + (size_t)(live % kFuseRing) * p.group_size * kFuseRecord;
                 const unsigned tag = epoch + 1u + live;
                 ++live;
-                float2 t = ref_lanes<16>((lane & 15) < kDenseWarps ? s_tail[par][lane & 15] : none, c);
+                float2 t = pair_lanes<16>((lane & 15) < kDenseWarps ? s_tail[par][lane & 15] : none);
                 if (flag || dead) t.x = flag & 1 ? __uint_as_float(kBadToken) : NAN;
                 if (lane < (rank == 0 ? 4 : 2))
                     post_word(rec + (size_t)rank * kFuseRecord + lane, lane == 0 ? t.x : (lane == 1 ? t.y : (lane == 2 ? nn.x : nn.y)), tag);
@@ -598,18 +617,18 @@ __global__ void __launch_bounds__(kFuseThreads, kFuseOcc) distill_fused_kernel(D
                         }
                     }
                     token |= (uint32_t)v[0] == kBadToken;
-                    T2 = ref_merge(T2, make_float2(__uint_as_float((uint32_t)v[0]), __uint_as_float((uint32_t)v[1])), c);
+                    T2 = pair_merge(T2, make_float2(__uint_as_float((uint32_t)v[0]), __uint_as_float((uint32_t)v[1])));
                     if (r == 0) N2 = make_float2(__uint_as_float((uint32_t)v[2]), __uint_as_float((uint32_t)v[3]));
                 }
                 late = __any_sync(0xffffffffu, late);
                 token = __any_sync(0xffffffffu, token);
                 if (late) dead = true;
-                T2 = ref_lanes<32>(T2, c);
+                T2 = pair_lanes<32>(T2);
                 N2.x = __shfl_sync(0xffffffffu, N2.x, 0);
                 N2.y = __shfl_sync(0xffffffffu, N2.y, 0);
             }
             if (lane == 0) {
-                const float2 A = ref_merge(T2, N2, c);
+                const float2 A = pair_merge(T2, N2);
                 const bool bad = !skip && (late || !(A.x < INFINITY) || A.x == -INFINITY);
                 const bool taught = tt.x > -INFINITY, some = T2.x > -INFINITY;
                 const float pT = taught ? __fdividef(__expf(aT - tt.x), tt.y) : 0.0f;
@@ -617,7 +636,7 @@ __global__ void __launch_bounds__(kFuseThreads, kFuseOcc) distill_fused_kernel(D
                 r.ref = some ? T2.x : 0.0f;
                 r.factor = 0.0f;
                 if (taught && some)
-                    r.factor = wt * p.inv_t * (__fdividef(ex2(ref_diff(T2.x, A.x, c)), A.y) - (pT > 0.0f ? __fdividef(pT, T2.y) : 0.0f));
+                    r.factor = wt * p.inv_t * (__fdividef(ex2(T2.x - A.x), A.y) - (pT > 0.0f ? __fdividef(pT, T2.y) : 0.0f));
                 if (bad) r.factor = NAN;
                 r.M = A.x;
                 r.Z = A.y;
