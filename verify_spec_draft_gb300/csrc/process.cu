@@ -36,25 +36,23 @@ __host__ __device__ inline size_t process_smem(int seg) {
 
 constexpr int kProcBatch = 4;   // words a thread holds while it waits for the ones behind
 
-// One batch of a row: the words kProcThreads apart from word i0 + tid, and their mask bits,
-// a byte per word.
+// One batch of a row: the words kProcThreads apart from word i0 + tid, and their mask words as
+// they were loaded (nothing here waits for a load).
 template <typename T, bool ALIGNED>
 struct ProcBatch {
     uint4 w[kProcBatch];
-    uint32_t allowed;
-    __device__ __forceinline__ void load(const SegWords<T, ALIGNED>& in, const uint32_t* mask, int mask_left, int i0) {
-        allowed = 0xffffffffu;
+    uint32_t mask[kProcBatch];
+    __device__ __forceinline__ void load(const SegWords<T, ALIGNED>& in, const uint32_t* m, int mask_left, int i0) {
 #pragma unroll
         for (int q = 0; q < kProcBatch; ++q) {
             const int i = i0 + q * kProcThreads + (int)threadIdx.x;
             if (i < in.n()) w[q] = in.load(i);
         }
-        if (mask) {
-            allowed = 0u;
+        if (m) {
 #pragma unroll
             for (int q = 0; q < kProcBatch; ++q) {
                 const int i = i0 + q * kProcThreads + (int)threadIdx.x;
-                if (i < in.n()) allowed |= in.allowed(mask, mask_left, i) << (8 * q);
+                if (i < in.n()) mask[q] = in.mask_word(m, mask_left, i);
             }
         }
     }
@@ -86,7 +84,7 @@ __device__ __forceinline__ uint4 word_masked(const uint4& w, uint32_t allowed) {
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
             // bits 2r and 2r + 1 to bits 15 and 31, then each over its half word
-            const uint32_t v = (allowed & 0xffu) * ((1u << (15 - 2 * r)) | (1u << (30 - 2 * r)));
+            const uint32_t v = allowed * ((1u << (15 - 2 * r)) | (1u << (30 - 2 * r)));
             uint32_t m;   // bytes 1 and 3 by their top bits (prmt's sign replication), twice each
             asm("prmt.b32 %0, %1, 0, 0xbb99;" : "=r"(m) : "r"(v));
             h[r] = (h[r] & m) | (NegInf<T>::word & ~m);
@@ -162,6 +160,7 @@ __global__ void __launch_bounds__(kProcThreads, kProcOcc) process_kernel(Process
             if (i < m) atomicOr(&s_state[t - c0], kInPrompt);
             else atomicAdd(&s_state[t - c0], 1u);
             mark(t - c0);
+            atomicOr(&s_seen[(t - c0) >> 5], 1u << ((t - c0) & 31));
         }
         bad_token |= (unsigned)t >= (unsigned)p.V;
     };
@@ -199,12 +198,12 @@ __global__ void __launch_bounds__(kProcThreads, kProcOcc) process_kernel(Process
         s_bias[tid] = bias_of(st);
     }
     __syncthreads();
-    for (int i = tid; i < p.seg; i += kProcThreads) {   // seg is whole warps: no partial ballot
-        const uint32_t st = s_state[i], c = st & kCountMask;
-        const unsigned seen = __ballot_sync(0xffffffffu, (st & (kInPrompt | kCountMask)) != 0u);
-        if (st) s_add[i] = (bias_of(st) - fmaf(freq, (float)c, c ? pres : 0.0f)) * tinv;
-        if ((tid & 31) == 0) s_seen[i >> 5] = seen;
-    }
+    for (int i = tid; i < p.seg / 32; i += kProcThreads)
+        for (uint32_t w = s_bits[i]; w; w &= w - 1u) {
+            const int at = i * 32 + __ffs(w) - 1;
+            const uint32_t st = s_state[at], c = st & kCountMask;
+            s_add[at] = (bias_of(st) - fmaf(freq, (float)c, c ? pres : 0.0f)) * tinv;
+        }
     __syncthreads();
 
     for (int j = j0; j < j1; ++j) {
@@ -230,7 +229,6 @@ __global__ void __launch_bounds__(kProcThreads, kProcOcc) process_kernel(Process
             for (int q = 0; q < kProcBatch; ++q) {
                 const int i = i0 + q * kProcThreads + tid;
                 if (i >= in.n()) break;
-                const uint32_t allowed = cur.allowed >> (8 * q);
                 uint4 o;
                 if (in.bits(s_bits, i)) {
                     const uint32_t seen = in.bits(s_seen, i);
@@ -245,7 +243,7 @@ __global__ void __launch_bounds__(kProcThreads, kProcOcc) process_kernel(Process
                 } else {
                     o = tinv == 1.0f ? cur.w[q] : word_scaled<T>(cur.w[q], tinv);
                 }
-                if (p.mask) o = word_masked<T>(o, allowed);
+                if (p.mask) o = word_masked<T>(o, in.allowed(cur.mask[q], i));
                 in.store(out, i, o);
             }
             cur = nxt;

@@ -114,16 +114,17 @@ struct SegWords {
         asm volatile("st.global.L1::no_allocate.v4.u32 [%0], {%1,%2,%3,%4};"
                      :: "l"(reinterpret_cast<uint4*>(q) + i), "r"(w.x), "r"(w.y), "r"(w.z), "r"(w.w) : "memory");
     }
-    // the mask bits of word i, bit k for entry k; `left` words of mask from the segment's first
-    __device__ __forceinline__ uint32_t allowed(const uint32_t* mask, int left, int i) const {
-        if (ALIGNED) {
-            const uint8_t* m = reinterpret_cast<const uint8_t*>(mask);
-            return E == 8 ? (uint32_t)__ldg(m + i) : ((uint32_t)__ldg(m + (i >> 1)) >> (4 * (i & 1))) & 15u;
-        }
+    // the bits of a mask that go with word i, as loaded, and then bit k for entry k; `left` words
+    // of mask from the segment's first
+    __device__ __forceinline__ uint32_t mask_word(const uint32_t* mask, int left, int i) const {
+        if (ALIGNED) return (uint32_t)__ldg(reinterpret_cast<const uint8_t*>(mask) + (E == 8 ? i : i >> 1));
         const int e = entry(i), e0 = max(e, 0), at = e0 & 31;
         const uint32_t lo = __ldg(mask + (e0 >> 5));
         const uint32_t hi = at + E > 32 && (e0 >> 5) + 1 < left ? __ldg(mask + (e0 >> 5) + 1) : 0u;
         return (__funnelshift_r(lo, hi, at) << (e0 - e)) & ((1u << E) - 1u);
+    }
+    __device__ __forceinline__ uint32_t allowed(uint32_t loaded, int i) const {
+        return ALIGNED && E == 4 ? (loaded >> (4 * (i & 1))) & 15u : loaded;
     }
     // the entries of word i in the segment's array
     __device__ __forceinline__ void floats(const float* a, int i, float (&o)[E]) const {
