@@ -236,7 +236,7 @@ struct ProcessParams {
     unsigned* status;
     // chosen at launch
     int seg;                   // vocabulary entries per CTA (a multiple of its threads)
-    int n_seg, n_row_split;
+    int n_seg, rows_per_cta, n_row_split;
     int hist_vec;              // histories start on 16 bytes
 };
 cudaError_t process_launch(ProcessParams p, cudaStream_t stream);

@@ -113,7 +113,7 @@ __global__ void __launch_bounds__(kProcThreads, kProcOcc) process_kernel(Process
     const int b = rem / p.n_row_split, rs = rem - b * p.n_row_split;
     const int c0 = sg * p.seg;
     const int len = min(p.seg, p.V - c0);
-    const int j0 = (int)((long)p.R * rs / p.n_row_split), j1 = (int)((long)p.R * (rs + 1) / p.n_row_split);
+    const int j0 = rs * p.rows_per_cta, j1 = min(p.R, j0 + p.rows_per_cta);
     const int tid = threadIdx.x;
     const bool report = sg == 0 && rs == 0;   // one CTA per request raises its flags
 
@@ -166,14 +166,19 @@ __global__ void __launch_bounds__(kProcThreads, kProcOcc) process_kernel(Process
     };
     const int32_t* hist = p.history + (long)b * p.Lmax;
     const int n4 = p.hist_vec ? n / 4 : 0;   // whole 16-byte words of tokens
+    unsigned worst = 0u;   // of the tokens, for the CTA that reports
 #pragma unroll 4
     for (int i = tid; i < n4; i += kProcThreads) {
-        const int4 t = __ldg(reinterpret_cast<const int4*>(hist) + i);
-        count(t.x, 4 * i);
-        count(t.y, 4 * i + 1);
-        count(t.z, 4 * i + 2);
-        count(t.w, 4 * i + 3);
+        const uint4 t = __ldg(reinterpret_cast<const uint4*>(hist) + i);
+        if (report) worst = max(max(worst, max(t.x, t.y)), max(t.z, t.w));
+        // four tokens at once: hardly any is in the segment
+        if (min(min(t.x - c0, t.y - c0), min(t.z - c0, t.w - c0)) >= (unsigned)len) continue;
+        count((int)t.x, 4 * i);
+        count((int)t.y, 4 * i + 1);
+        count((int)t.z, 4 * i + 2);
+        count((int)t.w, 4 * i + 3);
     }
+    bad_token |= worst >= (unsigned)p.V;
     for (int i = 4 * n4 + tid; i < n; i += kProcThreads) count(__ldg(hist + i), i);
     if (p.block && tid < p.R - 1) {
         if (tid < j0) count(s_blk[tid], p.Lmax);   // drafted before this CTA's first row
@@ -251,34 +256,51 @@ __global__ void __launch_bounds__(kProcThreads, kProcOcc) process_kernel(Process
     }
 }
 
-// Work split.  A CTA takes a segment of the vocabulary for a range of rows; its time is its
-// words, and what it costs to scan the history once.  All CTAs are equal, so the time is
-// (waves of resident CTAs) x (words of one): the split with the least of it is taken, among
-// equals the one with the fewest CTAs (each scans the history).
+// Work split.  A CTA takes a segment of the vocabulary for r rows of a request.  In units of the
+// time in which a resident CTA streams one word while all slots are taken (3.3 ns), it costs
+//   to begin    1200, and a 14th per token of history, half per bias, a 36th per entry cleared,
+//   a row       its words, 400 at least (a row's loads take that long, however few) and 110
+//               for every batch of words behind the first, or less of them where slots
+//               stay empty: down to three tenths.
+// CTAs beyond the slots run in further waves, whose beginnings mostly hide behind the streams
+// of other CTAs.  The split of least cost is taken; measured against all splits at eight
+// sizes, it came within 7 percent of the best.
+static long process_cost(const ProcessParams& p, int E, long slots, int r, long n, int* seg_out) {
+    const int seg = (int)((p.V + n - 1) / n + 127) / 128 * 128;
+    const long ctas = (long)((p.V + seg - 1) / seg) * ((p.R + r - 1) / r) * p.B;
+    const long words = seg / E + 110 * ((seg / E - 1) / (kProcBatch * kProcThreads));
+    const long waves = (ctas + slots - 1) / slots, last = ctas - (waves - 1) * slots;
+    const long begin = 1200 + p.Lmax / 14 + p.nb / 2 + seg / 36;
+    long thin = words * last / slots;
+    if (thin < words * 3 / 10) thin = words * 3 / 10;
+    *seg_out = seg;
+    return begin + begin * 35 / 100 * (waves - 1) + r * ((waves - 1) * (words > 400 ? words : 400) + (thin > 400 ? thin : 400));
+}
+
 cudaError_t process_launch(ProcessParams p, cudaStream_t stream) {
     const int E = p.dtype == SPEC_BF16 ? 8 : 4;
-    constexpr int kMaxSeg = 13184;   // 56 KB of shared memory: four CTAs of an SM
+    constexpr int kMaxSeg = 8832;   // 37 KB of shared memory; larger ones leave no L1 (serving step 56 us, not 51)
     const long slots = (long)device_sm_count() * kProcOcc;
-    const long scan = 64 + (p.Lmax + p.nb) / 8;   // the scan, in words that stream in the same time
-    const int least = (p.V + kMaxSeg - 1) / kMaxSeg;
-    const int most = (p.V + 128 * E - 1) / (128 * E) > least ? (p.V + 128 * E - 1) / (128 * E) : least;
+    const long least = (p.V + kMaxSeg - 1) / kMaxSeg;
+    const long most = (p.V + 128 * E - 1) / (128 * E) > least ? (p.V + 128 * E - 1) / (128 * E) : least;
     long best = -1;
-    for (int split = 1; split <= p.R; ++split) {
-        for (int waves = 1; waves <= 4; ++waves) {
-            long n = slots * waves / ((long)p.B * split);
+    for (int r = 1;; r = 2 * r < p.R ? 2 * r : p.R) {
+        const long per = (long)p.B * ((p.R + r - 1) / r);
+        for (int waves = 1; waves <= 3; ++waves) {
+            long n = slots * waves / per;
             n = n < least ? least : (n > most ? most : n);
-            const int seg = (int)((p.V + n - 1) / n + 127) / 128 * 128;
-            n = (p.V + seg - 1) / seg;
-            const long ctas = n * split * p.B;
-            const long cost = (ctas + slots - 1) / slots * ((long)((p.R + split - 1) / split) * (seg / E) + scan);
+            int seg;
+            const long cost = process_cost(p, E, slots, r, n, &seg);
             if (best < 0 || cost < best) {
                 best = cost;
                 p.seg = seg;
-                p.n_seg = (int)n;
-                p.n_row_split = split;
+                p.rows_per_cta = r;
             }
         }
+        if (r == p.R) break;
     }
+    p.n_seg = (p.V + p.seg - 1) / p.seg;
+    p.n_row_split = (p.R + p.rows_per_cta - 1) / p.rows_per_cta;
     p.hist_vec = p.Lmax % 4 == 0 && (reinterpret_cast<uintptr_t>(p.history) & 15u) == 0;
     const size_t smem = process_smem(p.seg);
     const long grid = (long)p.B * p.n_seg * p.n_row_split;
