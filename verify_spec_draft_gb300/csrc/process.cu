@@ -28,10 +28,12 @@ constexpr uint32_t kCountBits = 20, kCountMask = (1u << kCountBits) - 1u;
 constexpr uint32_t kSlotMask = 0x7ffu, kInPrompt = 0x80000000u;
 
 // The kernel's shared memory: a word per entry of the segment, two strings of a bit per entry
-// (and a word more, which bits_at reads), and for the block's tokens the token, its count
-// and its bias.
+// (each with eight words of room before it, kProcRoom), and for the block's tokens the
+// token, its count and its bias.
+constexpr int kProcRoom = 8;
+__host__ __device__ inline int process_words(int seg) { return seg + 2 * (seg / 32) + 4 * kProcRoom; }
 __host__ __device__ inline size_t process_smem(int seg) {
-    return ((size_t)seg + 2 * (seg / 32 + 4) + 3 * SPEC_MAX_GAMMA) * sizeof(uint32_t);
+    return ((size_t)process_words(seg) + 3 * SPEC_MAX_GAMMA) * sizeof(uint32_t);
 }
 
 constexpr int kProcBatch = 4;   // words a thread holds while it waits for the ones behind
@@ -100,11 +102,11 @@ template <typename T, bool ALIGNED>
 __global__ void __launch_bounds__(kProcThreads, kProcOcc) process_kernel(ProcessParams p) {
     constexpr int E = 16 / (int)sizeof(T);
     extern __shared__ __align__(16) uint32_t s_proc[];
-    uint32_t* s_state = s_proc;                                            // [seg]
-    float* s_add = reinterpret_cast<float*>(s_proc);                       // the same words, later
-    uint32_t* s_bits = s_proc + p.seg;                                     // [seg / 32 + 1] has something
-    uint32_t* s_seen = s_bits + p.seg / 32 + 4;                            // [seg / 32 + 1]
-    int32_t* s_blk = reinterpret_cast<int32_t*>(s_seen + p.seg / 32 + 4);  // [R - 1] tokens
+    uint32_t* s_state = s_proc + kProcRoom;                                // [seg]
+    float* s_add = reinterpret_cast<float*>(s_state);                      // the same words, later
+    uint32_t* s_bits = s_state + p.seg + kProcRoom;                        // [seg / 32] has something
+    uint32_t* s_seen = s_bits + p.seg / 32 + kProcRoom;                    // [seg / 32]
+    int32_t* s_blk = reinterpret_cast<int32_t*>(s_proc + process_words(p.seg));   // [R - 1] tokens
     int32_t* s_cnt = s_blk + SPEC_MAX_GAMMA;                               // [R - 1] counts once drafted
     float* s_bias = reinterpret_cast<float*>(s_cnt + SPEC_MAX_GAMMA);      // [R - 1]
     // segment by segment: the first ones, where frequent tokens tend to be, start first
@@ -139,8 +141,8 @@ __global__ void __launch_bounds__(kProcThreads, kProcOcc) process_kernel(Process
     m = max(0, min(m, n));
 
     // words and bits, 16 bytes at a time
-    for (int i = tid; i < (p.seg + 2 * (p.seg / 32 + 4)) / 4; i += kProcThreads)
-        reinterpret_cast<uint4*>(s_state)[i] = make_uint4(0u, 0u, 0u, 0u);
+    for (int i = tid; i < process_words(p.seg) / 4; i += kProcThreads)
+        reinterpret_cast<uint4*>(s_proc)[i] = make_uint4(0u, 0u, 0u, 0u);
     if (p.block && tid < p.R - 1) s_blk[tid] = p.block[(long)b * (p.R - 1) + tid];
     __syncthreads();
     auto mark = [&](int at) { atomicOr(&s_bits[at >> 5], 1u << (at & 31)); };

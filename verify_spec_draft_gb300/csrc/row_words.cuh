@@ -15,6 +15,35 @@ template <typename T> struct NegInf;
 template <> struct NegInf<float> { static constexpr uint32_t word = 0xff800000u; };
 template <> struct NegInf<bf16_t> { static constexpr uint32_t word = 0xff80ff80u; };
 
+// The words that are not whole, out of line: entries [e, e + E) of a row of V entries, -inf
+// outside it, and the way back.
+template <typename T>
+__device__ __noinline__ uint4 edge_load(const T* p, int e, int V) {
+    constexpr int E = 16 / (int)sizeof(T);
+    uint32_t h[4] = {NegInf<T>::word, NegInf<T>::word, NegInf<T>::word, NegInf<T>::word};
+#pragma unroll
+    for (int k = 0; k < E; ++k) {
+        if (e + k < 0 || e + k >= V) continue;
+        if (sizeof(T) == 2) {
+            const uint32_t v = reinterpret_cast<const unsigned short*>(p)[e + k];
+            h[k >> 1] = (k & 1) ? (h[k >> 1] & 0xffffu) | (v << 16) : (h[k >> 1] & 0xffff0000u) | v;
+        } else {
+            h[k & 3] = reinterpret_cast<const uint32_t*>(p)[e + k];
+        }
+    }
+    return make_uint4(h[0], h[1], h[2], h[3]);
+}
+template <typename T>
+__device__ __noinline__ void edge_store(T* q, int e, int V, uint4 w) {
+    const uint32_t h[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int k = 0; k < 16 / (int)sizeof(T); ++k) {
+        if (e + k < 0 || e + k >= V) continue;
+        if (sizeof(T) == 2) reinterpret_cast<unsigned short*>(q)[e + k] = (unsigned short)(h[k >> 1] >> (16 * (k & 1)));
+        else reinterpret_cast<uint32_t*>(q)[e + k] = h[k & 3];
+    }
+}
+
 template <typename T>
 struct RowWords {
     static constexpr int E = 16 / (int)sizeof(T);
@@ -28,44 +57,22 @@ struct RowWords {
           n(len > 0 ? (int)(((long)mis + len + E - 1) / E) : 0) {}
 
     __device__ __forceinline__ int entry(int i) const { return i * E - mis; }
-    __device__ __forceinline__ bool whole(int i) const { return entry(i) >= 0 && entry(i) + E <= V; }
-
-    __device__ __forceinline__ uint32_t raw(int e) const {   // entry e's bits, -inf outside the row
-        if (e < 0 || e >= V) return NegInf<T>::word & (sizeof(T) == 2 ? 0xffffu : 0xffffffffu);
-        if (sizeof(T) == 2) return reinterpret_cast<const unsigned short*>(p)[e];
-        return reinterpret_cast<const uint32_t*>(p)[e];
+    __device__ __forceinline__ bool whole(int i) const {   // all but the first and the last are
+        return (unsigned)(i - 1) < (unsigned)max(n - 2, 0) || (entry(i) >= 0 && entry(i) + E <= V);
     }
     // word i, entries outside the row as -inf
     __device__ __forceinline__ uint4 load(int i) const {
-        if (whole(i)) {
-            uint4 v;
-            asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-                         : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p + entry(i)) : "memory");
-            return v;
-        }
-        const int e = entry(i);
-        if (sizeof(T) == 2)
-            return make_uint4(raw(e) | (raw(e + 1) << 16), raw(e + 2) | (raw(e + 3) << 16),
-                              raw(e + 4) | (raw(e + 5) << 16), raw(e + 6) | (raw(e + 7) << 16));
-        return make_uint4(raw(e), raw(e + 1), raw(e + 2), raw(e + 3));
+        if (!whole(i)) return edge_load<T>(p, entry(i), V);
+        uint4 v;
+        asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p + entry(i)) : "memory");
+        return v;
     }
     // word i into the row `q` of the same length and offset
     __device__ __forceinline__ void store(T* q, int i, const uint4& w) const {
-        const int e = entry(i);
-        if (whole(i)) {
-            asm volatile("st.global.L1::no_allocate.v4.u32 [%0], {%1,%2,%3,%4};"
-                         :: "l"(q + e), "r"(w.x), "r"(w.y), "r"(w.z), "r"(w.w) : "memory");
-            return;
-        }
-        const uint32_t h[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int k = 0; k < E; ++k) {
-            if (e + k < 0 || e + k >= V) continue;
-            if (sizeof(T) == 2)
-                reinterpret_cast<unsigned short*>(q)[e + k] = (unsigned short)(h[k >> 1] >> (16 * (k & 1)));
-            else
-                reinterpret_cast<uint32_t*>(q)[e + k] = h[k & 3];
-        }
+        if (!whole(i)) return edge_store<T>(q, entry(i), V, w);
+        asm volatile("st.global.L1::no_allocate.v4.u32 [%0], {%1,%2,%3,%4};"
+                     :: "l"(q + entry(i)), "r"(w.x), "r"(w.y), "r"(w.z), "r"(w.w) : "memory");
     }
 };
 
@@ -126,7 +133,8 @@ struct SegWords {
     __device__ __forceinline__ uint32_t allowed(uint32_t loaded, int i) const {
         return ALIGNED && E == 4 ? (loaded >> (4 * (i & 1))) & 15u : loaded;
     }
-    // the entries of word i in the segment's array
+    // the entries of word i in the segment's array, which has E entries of room before it and
+    // as many behind it
     __device__ __forceinline__ void floats(const float* a, int i, float (&o)[E]) const {
 #pragma unroll
         for (int k = 0; k < E; k += 4) {
@@ -135,22 +143,18 @@ struct SegWords {
                 o[k] = v.x; o[k + 1] = v.y; o[k + 2] = v.z; o[k + 3] = v.w;
             } else {
 #pragma unroll
-                for (int h = k; h < k + 4; ++h) {
-                    const int e = entry(i) + h;
-                    o[h] = e >= 0 && e < r.V ? a[e] : 0.0f;
-                }
+                for (int h = k; h < k + 4; ++h) o[h] = a[entry(i) + h];
             }
         }
     }
-    // the bits of word i that are set in the segment's bit string
+    // the bits of word i in the segment's bit string, which has a clear word before it and
+    // behind it
     __device__ __forceinline__ uint32_t bits(const uint32_t* bits, int i) const {
         if (ALIGNED) {
             const uint8_t* m = reinterpret_cast<const uint8_t*>(bits);
             return E == 8 ? (uint32_t)m[i] : ((uint32_t)m[i >> 1] >> (4 * (i & 1))) & 15u;
         }
-        const int e = entry(i), e0 = max(e, 0);
-        const int behind = min(E, r.V - e);   // entries of the word up to the row's end
-        return (bits_at(bits, e0) << (e0 - e)) & ((1u << behind) - 1u);
+        return bits_at(bits - 1, entry(i) + 32) & ((1u << E) - 1u);
     }
 };
 
