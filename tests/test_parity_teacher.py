@@ -256,6 +256,41 @@ def test_distill_hard_label_is_cross_entropy(spec):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("V,K,named", [(5000, 3, 1e-3), (60001, 5, 1e-4), (131072, 2, 3e-5)])
+def test_distill_little_named_mass(spec, dtype, V, K, named):
+    """The rests hold nearly all of both rows, so the loss is far below 1 and its own digits
+    count.  With p_N, q_N the named masses, a weight's relative error e moves the loss by e of
+    its own mass (through the sums) and by e |ln p - ln q| of it (through the terms), the
+    rest's weight by e |p_N - q_N|; a rest's gradient, q / q_T (p_N - q_N), by e (p_N + q_N) and
+    e of itself.  Two roundings of the result are added."""
+    z = rows_of(4, V, dtype, seed=V) / 3
+    ids = torch.randint(0, V // K, (4, K), dtype=torch.int32, generator=torch.Generator().manual_seed(V)).cuda()
+    ids += torch.arange(K, dtype=torch.int32, device="cuda") * (V // K)
+    values = (torch.arange(K) + 1.0).div(K).mul(named).log().expand(4, K).contiguous().cuda()
+    tl = torch.zeros(4, device="cuda")
+    ref = ot.distill(f64(z), f64(values), ids.cpu().numpy(), f64(tl), None, 1.0)
+    for grad in (False, True):
+        out = vsd.distill(z, values, ids, tail=tl, grad=grad)
+        for r in range(4):
+            e = eps(z[r], 1.0) + eps(values[r], 1.0)
+            p, q, qt = ref["p"][r][:-1], ref["q"][r], ref["qt"][r]
+            qn = q[ids[r].cpu().numpy()]
+            far = np.abs(np.log(p) - np.log(qn)).max()
+            both = p.sum() + qn.sum()
+            want = ref["loss"][r]
+            bar = e * both * (2 + far) + 2.0 ** -23 * want
+            assert want < 0.01
+            assert abs(float(out["loss"][r]) - want) <= bar, (r, float(out["loss"][r]), want, bar)
+            if grad:
+                rest = np.ones(V, bool)
+                rest[ids[r].cpu().numpy()] = False
+                g = ref["grad"][r][rest]
+                step = 2.0 ** -8 if dtype == BF16 else 2.0 ** -24
+                bar = q[rest] / qt * 2 * e * both + (2 * e + 2 * step) * np.abs(g) + 1e-37
+                assert (np.abs(f64(out["grad"][r])[rest] - g) <= bar).all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
 def test_distill_bf16_values_and_empty_slots(spec, dtype):
     z = rows_of(4, 5000, dtype, seed=21)
     values, ids, tl = teacher_of(z, 30, 1.0, True, seed=22, values_dtype=BF16)

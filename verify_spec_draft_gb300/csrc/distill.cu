@@ -92,17 +92,43 @@ __device__ __forceinline__ float2 teacher_lanes(float2 v) {
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr uint32_t kBadToken = 0x7fc0dead;   // a NaN that says: an id is listed twice
 
-// The loss of a named entry (teacher's logit a, student's z) and of the rest.  top, P: the
-// teacher's pair, in units of 1; (M, Z) the student's, (mT, sT) that of its unnamed entries.
-struct RowStats { float M, Z, mT, sT, top, P; };
+// What the rows' ends share.  (M, Z): the student's pair, (mT, sT) that of its unnamed entries;
+// top, e, eT: the teacher's maximum, and the weights of its named entries and of its rest
+// against it, P = e + eT; f the student's named weight against M.
+//
+// The share of the rest that the student has too much is
+//     q_T - p_T = f_T / Z - e_T / P = (f_T e - e_T f) / (Z P),        f_T = sT 2^(mT - M),
+// where the rest's own share is left out: with little named mass both shares are nearly 1,
+// and their difference would keep none of its digits.  G is that without (sT / (Z P)).  The
+// rest's part of the loss, p_T (ln p_T - ln q_T) = -p_T ln(1 + (q_T - p_T) / p_T), goes by it
+// too, unless the shares are far apart: then the logarithms are taken one by one, for f_T may
+// be too small for a float.
+struct RowEnds { float M, Z, mT, sT, top, e, eT, P, G; };
+__device__ __forceinline__ RowEnds row_ends(float2 T2, float2 N2, float2 teach, float aT) {
+    RowEnds r;
+    const float2 A = pair_merge(T2, N2);
+    r.M = A.x;
+    r.Z = A.y;
+    r.mT = T2.x;
+    r.sT = T2.y;
+    r.top = f_max_nan(teach.x, aT);
+    r.e = teach.x > -INFINITY ? teach.y * __expf(teach.x - r.top) : 0.0f;
+    r.eT = aT > -INFINITY ? __expf(aT - r.top) : 0.0f;
+    r.P = r.e + r.eT;
+    const float f = N2.x > -INFINITY ? N2.y * ex2(N2.x - A.x) : 0.0f;
+    r.G = T2.x > -INFINITY ? fmaf(ex2(T2.x - A.x), r.e, -__fdividef(r.eT * f, T2.y)) : 0.0f;
+    return r;
+}
 template <typename T>
-__device__ __forceinline__ float entry_loss(const RowStats& r, float a, float z, float c, float inv_t) {
+__device__ __forceinline__ float entry_loss(const RowEnds& r, float a, float z, float c, float inv_t) {
     const float lt = fmaf(a, inv_t, -r.top), pk = __expf(lt) / r.P;
     return pk > 0.0f ? pk * ((lt - logf(r.P)) - (rel<T>(z, r.M, c) - log2f(r.Z)) * kLn2) : 0.0f;
 }
-__device__ __forceinline__ float rest_loss(const RowStats& r, float aT) {
-    const float pT = __expf(aT - r.top) / r.P;
+__device__ __forceinline__ float rest_loss(const RowEnds& r, float aT) {
+    const float pT = r.eT / r.P;
     if (!(pT > 0.0f)) return 0.0f;
+    const float d = r.mT > -INFINITY ? r.sT * r.G / (r.Z * r.eT) : -1.0f;
+    if (fabsf(d) < 0.5f) return -pT * log1pf(d);
     const float lq = r.mT > -INFINITY ? (r.mT - r.M + log2f(r.sT) - log2f(r.Z)) * kLn2 : -INFINITY;
     return pT * (((aT - r.top) - logf(r.P)) - lq);
 }
@@ -220,10 +246,8 @@ __device__ __forceinline__ void distill_finish(const DistillParams& p, int row, 
     if (flag) atomicOr(&s_flag, flag);
     // every warp puts the whole together
     const float2 T2 = pair_lanes<kDistWarps>(s_tail[lane % kDistWarps]);
-    const float2 A = pair_merge(T2, pair_lanes<kDistWarps>(s_top[lane % kDistWarps]));
-    const int w = lane & 15;
-    const float2 N = teacher_lanes<16>(w < kDistWarps ? s_teach[w] : (w == kDistWarps ? make_float2(aT, 1.0f) : none));
-    const RowStats r = {A.x, A.y, T2.x, T2.y, N.x, N.y};
+    const float2 N2 = pair_lanes<kDistWarps>(s_top[lane % kDistWarps]);
+    const RowEnds r = row_ends(T2, N2, teacher_lanes<kDistWarps>(s_teach[lane % kDistWarps]), aT);
     float l = 0.0f;
     if (r.top > -INFINITY) {
         if (there) l = entry_loss<T>(r, a, z, p.scale, p.inv_t);
@@ -233,7 +257,7 @@ __device__ __forceinline__ void distill_finish(const DistillParams& p, int row, 
     if (lane == 0) s_loss[warp] = l;
     __syncthreads();
     if (tid == 0) {
-        const bool bad = s_flag || !(A.x < INFINITY) || A.x == -INFINITY;
+        const bool bad = s_flag || !(r.M < INFINITY) || r.M == -INFINITY;
         l = s_loss[0];
         for (int i = 1; i < kDistWarps; ++i) l += s_loss[i];
         p.loss_out[row] = bad ? NAN : l;
@@ -304,12 +328,9 @@ __device__ __forceinline__ void bulk_s2g_wait() { asm volatile("cp.async.bulk.wa
 __device__ __forceinline__ void named_sync() { asm volatile("bar.sync 1, %0;" :: "n"(kFuseNamed) : "memory"); }
 
 // What is known of a row once its slices' statistics are together.
-struct FuseRow {
+struct FuseRow : RowEnds {
     float ref;        // unnamed entries: gradient 2^(z c - ref) factor
     float factor;
-    float M, Z;       // all entries: their pair
-    float mT, sT;     // the unnamed ones' pair
-    float top, P;     // the teacher's normaliser
     int skip, bad;
 };
 
@@ -540,11 +561,10 @@ __global__ void __launch_bounds__(kFuseThreads, kFuseOcc) distill_fused_kernel(D
                 const float pk = taught ? __expf(lt) / r.P : 0.0f;
                 d = r.bad ? NAN : (taught ? (ex2(rel<T>(cur.z, r.M, c)) / r.Z - pk) * (cur.wt * p.inv_t) : 0.0f);
                 if (rank == 0) {
-                    const RowStats st = {r.M, r.Z, r.mT, r.sT, r.top, r.P};
                     float l = 0.0f;
                     if (taught) {
-                        if (known_id(cur)) l = entry_loss<T>(st, cur.a, cur.z, c, p.inv_t);
-                        if (k == 0) l += rest_loss(st, cur.aT);
+                        if (known_id(cur)) l = entry_loss<T>(r, cur.a, cur.z, c, p.inv_t);
+                        if (k == 0) l += rest_loss(r, cur.aT);
                     }
                     l = warp_sum(l);
                     if (lane == 0) s_loss[warp] = l;
@@ -581,8 +601,8 @@ __global__ void __launch_bounds__(kFuseThreads, kFuseOcc) distill_fused_kernel(D
             wait(&s_stated[par], i >> 1);
             const float wt = s_wt[par], aT = s_aT[par];
             const bool skip = wt == 0.0f;
-            // the teacher's normaliser, and the named logits' (slice 0 has them)
-            const float2 tt = teacher_lanes<8>(skip ? none : ((lane & 7) < kNamedWarps ? s_teach[par][lane & 7] : ((lane & 7) == kNamedWarps ? make_float2(aT, 1.0f) : none)));
+            // the teacher's named entries, the student's (slice 0 has them)
+            const float2 tn = teacher_lanes<4>(skip ? none : s_teach[par][lane & 3]);
             const float2 nn = pair_lanes<4>(skip ? none : s_top[par][lane & 3]);
             static_assert(kNamedWarps == 4 && kDenseWarps <= 16, "the lanes' layout");
             const int flag = s_flag[par];
@@ -628,22 +648,12 @@ __global__ void __launch_bounds__(kFuseThreads, kFuseOcc) distill_fused_kernel(D
                 N2.y = __shfl_sync(0xffffffffu, N2.y, 0);
             }
             if (lane == 0) {
-                const float2 A = pair_merge(T2, N2);
-                const bool bad = !skip && (late || !(A.x < INFINITY) || A.x == -INFINITY);
-                const bool taught = tt.x > -INFINITY, some = T2.x > -INFINITY;
-                const float pT = taught ? __fdividef(__expf(aT - tt.x), tt.y) : 0.0f;
                 FuseRow r;
-                r.ref = some ? T2.x : 0.0f;
-                r.factor = 0.0f;
-                if (taught && some)
-                    r.factor = wt * p.inv_t * (__fdividef(ex2(T2.x - A.x), A.y) - (pT > 0.0f ? __fdividef(pT, T2.y) : 0.0f));
+                static_cast<RowEnds&>(r) = row_ends(T2, N2, skip ? none : tn, skip ? -INFINITY : aT);
+                const bool bad = !skip && (late || !(r.M < INFINITY) || r.M == -INFINITY);
+                r.ref = r.mT > -INFINITY ? r.mT : 0.0f;
+                r.factor = r.top > -INFINITY ? wt * p.inv_t * __fdividef(r.G, r.Z * r.P) : 0.0f;
                 if (bad) r.factor = NAN;
-                r.M = A.x;
-                r.Z = A.y;
-                r.mT = T2.x;
-                r.sT = T2.y;
-                r.top = tt.x;
-                r.P = tt.y;
                 r.skip = skip;
                 r.bad = bad;
                 s_row[par] = r;
