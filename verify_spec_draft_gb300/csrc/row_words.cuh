@@ -100,6 +100,8 @@ __device__ __forceinline__ uint32_t bits_at(const uint32_t* w, int e) {
 
 // The words of a row or of a segment of one.  ALIGNED: the segment starts on 16 bytes and is a whole
 // number of words, as every segment does when rows are whole words apart and V is whole words.
+// Without the tests for a row's ends the distillation loss of 448 rows of 248,320 bf16 takes
+// 37.5 us instead of 44.3, the 64 largest of 256 rows 32.7 instead of 34.8.
 template <typename T, bool ALIGNED>
 struct SegWords {
     static constexpr int E = 16 / (int)sizeof(T);

@@ -20,16 +20,22 @@ kernel, on inputs larger than L2 (129 MB) but only a few hundred MB on the devic
   sampler    spec_draft_block at T=1 on the anchor-branch workload, 1024 branches x W=7
              (3.56 GB of logits): for launch lists only (one metric, one pass)
   budget     spec_verify_budget, B=32, gamma=16, budget 256, a linear cost curve (2 KB)
+  process    spec_process_logits on verify_t1's 256 target rows with the block's tokens,
+             histories of 8192, masks and 300 biases (127 MB in, as much out)
+  top        spec_top_logits, K 64, on the same 256 rows (127 MB)
+  distill    spec_distill, K 64, on e2etv's 448 draft rows, the loss alone (222 MB in)
+  distill_grad  the same with the gradient (222 MB in, 222 MB out)
 """
 
 import argparse
 
 import torch
 
-from . import draft_block, draft_block_topk, e2etv, load, synth, tree_verify, verify, verify_budget, verify_topk
+from . import (distill, draft_block, draft_block_topk, e2etv, load, process_logits, synth, top_logits, tree_verify,
+               verify, verify_budget, verify_topk)
 
 CASES = ("draft", "draft_t1", "verify_t0", "verify_t1", "verify_topk", "e2etv", "tree_verify", "draft_topk",
-         "draft_pos", "sampler", "budget")
+         "draft_pos", "sampler", "budget", "process", "top", "distill", "distill_grad")
 
 
 def main(argv=None):
@@ -96,6 +102,31 @@ def main(argv=None):
         ref = draft_block_topk(inp["draft"], inp["anchor"], inp["U"], inp["Wt"], 20, 0.95, inp["seeds"])
         run = lambda: draft_block_topk(inp["draft"], inp["anchor"], inp["U"], inp["Wt"], 20, 0.95, inp["seeds"],
                                        ws=ref["ws"], out=ref)
+    elif args.case == "process":
+        inp = synth.config_inputs(4, device=dev)
+        B, R, V = inp["target"].shape
+        g = torch.Generator(device=dev)
+        g.manual_seed(1004)
+        ids = lambda *shape: torch.randint(0, V, shape, generator=g, device=dev, dtype=torch.int32)
+        some = lambda lo, hi: lo + (hi - lo) * torch.rand(B, generator=g, device=dev)
+        kw = dict(history=ids(B, 8192), prompt_lengths=torch.full((B,), 2048, dtype=torch.int32, device=dev),
+                  block=ids(B, R - 1), repetition=some(1.0, 1.3), frequency=some(0.0, 0.5), presence=some(0.0, 0.5),
+                  temperature=some(0.5, 1.2), bias_ids=ids(B, 300),
+                  bias_values=torch.randn((B, 300), generator=g, device=dev),
+                  mask=torch.randint(-2**31, 2**31, (B, R, (V + 31) // 32), generator=g, device=dev).to(torch.int32))
+        ref = process_logits(inp["target"], **kw)
+        run = lambda: process_logits(inp["target"], ws=ref["ws"], out=ref, **kw)
+    elif args.case == "top":
+        rows = synth.config_inputs(4, device=dev)["target"]
+        ref = top_logits(rows, 64)
+        run = lambda: top_logits(rows, 64, ws=ref["ws"], out=ref)
+    elif args.case in ("distill", "distill_grad"):
+        c = synth.CONFIGS[5]
+        t, d = synth.e2etv_rows(64, c.gamma, c.V, c.draft_sigma, c.dtype, c.seed, dev)
+        top = top_logits(t, 64)
+        kw = dict(tail=top["tail"], grad=args.case == "distill_grad")
+        ref = distill(d, top["values"], top["ids"], **kw)
+        run = lambda: distill(d, top["values"], top["ids"], ws=ref["ws"], out=ref, **kw)
     else:
         c = synth.CONFIGS[5]
         n_branches = 64
