@@ -18,9 +18,9 @@
 // ones that were not taken; it is never a difference of two sums, so a rest of 1e-12 of
 // the row keeps its relative accuracy.
 //
-// Bound: 256 rows of 248,320 bf16, K 64, take 33 us, 3.9 TB/s of what has to be read and 58 %
+// Bound: 256 rows of 248,320 bf16, K 64, take 30.4 us, 4.2 TB/s of what has to be read and 62 %
 // of a copy's rate.  The scan goes at the memory's pace (23 us by itself, from cold caches,
-// 5.5 TB/s); the picks are latency, some 10 us of steps that wait for one another (the maxima,
+// 5.5 TB/s); the picks are latency, some 8 us of steps that wait for one another (the maxima,
 // the bisection, the chosen blocks, the ranks) with a fifth of the warps there.  A full
 // selection over the block maxima took 76 us in all, reading the chosen blocks twice 61.
 #include "internal.h"
@@ -34,15 +34,16 @@ constexpr int kTopBatch = 8;                       // blocks a warp loads at onc
 constexpr int kTopSlack = 32;                      // blocks beyond K that the bisection may leave
 constexpr int kTopBlkMax = SPEC_MAX_TEACHER + kTopSlack;
 // Rows from which the picks are a launch of their own, not the last piece's CTA's: of 248,320
-// bf16, K 20, 256 rows then take 31.0 us instead of 36.9, 64 rows 15.0 instead of 16.8; 1 and 16
-// rows 10.9 and 11.6 instead of 11.4 and 12.6, but a second launch costs the host 1.5 us, and the
-// host is what holds so short a call.
+// bf16, K 20, 256 rows took 31.0 us that way instead of 36.9, 64 rows 15.0 instead of 16.8; 1 and
+// 16 rows 10.9 and 11.6 instead of 11.4 and 12.6, but a second launch costs the host 1.5 us, and
+// the host is what holds so short a call.
 constexpr int kTopApart = 32;
 // Blocks per entry asked for, at least (smaller blocks otherwise): 256 rows of 32,000, K 128,
-// take 17 us where 62 blocks of 32 words take 103; 64 rows of 151,936, K 128, with their 594
-// blocks take 18 us where blocks of 4 words take 23.
+// took 17 us where 125 blocks of 32 words took 103; 64 rows of 151,936, K 128, with their 594
+// blocks took 18 us where blocks of 4 words took 23.
 constexpr int kTopMany = 2;
 constexpr int kTopAgain = 4;                       // words a thread holds when it looks again
+constexpr int kTopRecords = 4;                     // blocks' records a thread loads at once
 constexpr int kTopCandMax = SPEC_MAX_TEACHER * 8;  // entries to rank
 
 // Blocks of `lanes` words of a row of V entries, whatever its offset in its first word, in
@@ -142,8 +143,11 @@ __global__ void __launch_bounds__(kTopThreads) top_kernel(TopLogitsParams p) {
 }
 
 // The picks of all rows, launched behind the scan as its programmatic dependent.
+// Rows that a SM picks from at once.  Four leave the registers to request words ahead (256 rows of
+// 248,320 bf16: 30.8 us, with five 31.9), which rows that are not whole words have no use for (611
+// rows of 50,257 float32: 42 us with four, 38 with five).
 template <typename T, bool ALIGNED, int LANES>
-__global__ void __launch_bounds__(kTopThreads) top_pick_kernel(TopLogitsParams p) {
+__global__ void __launch_bounds__(kTopThreads, ALIGNED ? 4 : 5) top_pick_kernel(TopLogitsParams p) {
     extern __shared__ __align__(16) uint32_t s_keys[];
     pdl_wait_primary();
     top_pick<T, ALIGNED, LANES>(p, blockIdx.x, s_keys);
@@ -162,8 +166,26 @@ __device__ __forceinline__ int cta_sum(int v, int* s_part, int& slot) {
     for (int i = 0; i < kTopWarps; ++i) t += s[i];
     return t;
 }
-// Exclusive prefix over the threads of the CTA.
-__device__ __forceinline__ int cta_prefix(int v, int* s_part, int& slot) {
+// Two such sums.
+__device__ __forceinline__ int2 cta_sums(int a, int b, int2* s_pair, int& slot) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    a = __reduce_add_sync(0xffffffffu, a);
+    b = __reduce_add_sync(0xffffffffu, b);
+    int2* s = s_pair + slot * kTopWarps;
+    slot ^= 1;
+    if (lane == 0) s[warp] = make_int2(a, b);
+    __syncthreads();
+    int2 t = make_int2(0, 0);
+#pragma unroll
+    for (int i = 0; i < kTopWarps; ++i) {
+        const int2 v = s[i];
+        t.x += v.x;
+        t.y += v.y;
+    }
+    return t;
+}
+// Exclusive prefix over the threads of the CTA, and the total.
+__device__ __forceinline__ int cta_prefix(int v, int& total, int* s_part, int& slot) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int x = v;
 #pragma unroll
@@ -175,8 +197,13 @@ __device__ __forceinline__ int cta_prefix(int v, int* s_part, int& slot) {
     slot ^= 1;
     if (lane == 31) s[warp] = x;
     __syncthreads();
-    int base = 0;
-    for (int i = 0; i < warp; ++i) base += s[i];
+    int base = 0, t = 0;
+#pragma unroll
+    for (int i = 0; i < kTopWarps; ++i) {
+        if (i == warp) base = t;
+        t += s[i];
+    }
+    total = t;
     return base + x - v;
 }
 
@@ -198,9 +225,9 @@ __device__ __noinline__ int pick_largest(const uint32_t* keys, int n, int K, int
         gt += keys[i] > t ? 1 : 0;
         tie += (t != 0u && keys[i] == t) ? 1 : 0;
     }
-    const int n_gt = cta_sum(gt, s_part, slot), n_tie = cta_sum(tie, s_part, slot);
+    int n_gt, n_tie;
+    int g = cta_prefix(gt, n_gt, s_part, slot), e = cta_prefix(tie, n_tie, s_part, slot);
     const int admit = min(n_tie, K - n_gt);
-    int g = cta_prefix(gt, s_part, slot), e = cta_prefix(tie, s_part, slot);
     for (int i = lo; i < hi; ++i) {
         if (keys[i] > t) { list[g + min(e, admit)] = i; ++g; }
         else if (t != 0u && keys[i] == t) {
@@ -300,6 +327,7 @@ __device__ __forceinline__ void top_pick(const TopLogitsParams& p, int row, uint
     __shared__ int s_word[kTopCandMax];                      // listed words to look at, then ranks
     __shared__ unsigned s_hit[kTopBlkMax];
     __shared__ int s_blk[kTopBlkMax], s_part[2 * kTopWarps], s_bad;
+    __shared__ int2 s_pair[2 * kTopWarps];
     __shared__ uint32_t s_lo, s_hi;
     __shared__ unsigned long long s_kth;
     __shared__ float4 s_run[kTopWarps];
@@ -327,16 +355,27 @@ __device__ __forceinline__ void top_pick(const TopLogitsParams& p, int row, uint
     bool bad = false;
     uint32_t klo = 0xffffffffu, khi = 0u;
     int cnt = 0;
-    for (int i = tid; i < p.n_blocks; i += kTopThreads) {
-        const float2 ms = __ldcg(&blk[i]);
-        bad |= bad_logit(ms.x);
-        const uint32_t key = value_key(ms.x);
-        s_keys[i] = key;
-        s_sums[i] = ms.y;
-        if (key) {
-            klo = min(klo, key);
-            khi = max(khi, key);
-            ++cnt;
+    for (int i0 = tid; i0 < p.n_blocks; i0 += kTopRecords * kTopThreads) {
+        float2 ms[kTopRecords];
+#pragma unroll
+        for (int h = 0; h < kTopRecords; ++h) {
+            const int i = i0 + h * kTopThreads;
+            ms[h] = i < p.n_blocks ? __ldcg(&blk[i]) : make_float2(-INFINITY, 0.0f);
+        }
+#pragma unroll
+        for (int h = 0; h < kTopRecords; ++h) {
+            const int i = i0 + h * kTopThreads;
+            bad |= bad_logit(ms[h].x);
+            const uint32_t key = value_key(ms[h].x);
+            if (i < p.n_blocks) {
+                s_keys[i] = key;
+                s_sums[i] = ms[h].y;
+            }
+            if (key) {
+                klo = min(klo, key);
+                khi = max(khi, key);
+                ++cnt;
+            }
         }
     }
     klo = __reduce_min_sync(0xffffffffu, klo);
@@ -368,9 +407,9 @@ __device__ __forceinline__ void top_pick(const TopLogitsParams& p, int row, uint
             c12 += (key >= t1 ? 1 : 0) + (key >= t2 ? 65536 : 0);
             c3 += key >= t3 ? 1 : 0;
         }
-        c12 = cta_sum(c12, s_part, slot);
-        c3 = cta_sum(c3, s_part, slot);
-        const int c1 = c12 & 0xffff, c2 = c12 >> 16;
+        const int2 c = cta_sums(c12, c3, s_pair, slot);
+        const int c1 = c.x & 0xffff, c2 = c.x >> 16;
+        c3 = c.y;
         if (c3 >= K) { lo = t3; n_above = c3; }
         else if (c2 >= K) { lo = t2; n_above = c2; hi = t3; }
         else if (c1 >= K) { lo = t1; n_above = c1; hi = t2; }
@@ -391,11 +430,14 @@ __device__ __forceinline__ void top_pick(const TopLogitsParams& p, int row, uint
         const int i = u * PER + l / LANES;
         return i < nb ? word_at(s_blk[i], l % LANES) : make_uint4(ninf, ninf, ninf, ninf);
     };
+    auto load_blocks = [&](int u0, uint4 (&w)[kTopAgain]) {
+#pragma unroll
+        for (int h = 0; h < kTopAgain; ++h) w[h] = listed_word(u0 + h * kTopWarps, lane);
+    };
     auto over_blocks = [&](auto&& body) {   // a warp's share of them, kTopAgain loads at a time
         for (int u0 = warp; u0 * PER < nb; u0 += kTopAgain * kTopWarps) {
             uint4 w[kTopAgain];
-#pragma unroll
-            for (int h = 0; h < kTopAgain; ++h) w[h] = listed_word(u0 + h * kTopWarps, lane);
+            load_blocks(u0, w);
             body(u0, w);
         }
     };
@@ -410,8 +452,9 @@ __device__ __forceinline__ void top_pick(const TopLogitsParams& p, int row, uint
             uint32_t above = 0u;
 #pragma unroll
             for (int k = 0; k < E; ++k) above |= word_entry<T>(w, k) >= least ? 1u << k : 0u;
-            int at = n + cta_prefix(__popc(above), s_part, slot);
-            n += cta_sum(__popc(above), s_part, slot);
+            int more;
+            int at = n + cta_prefix(__popc(above), more, s_part, slot);
+            n += more;
             const int e0 = in.entry(s_blk[(at_word >> 5) * PER + (at_word & 31) / LANES] * LANES + (at_word & 31) % LANES);
             for (uint32_t a = above; a; a &= a - 1u, ++at) {
                 const int k = __ffs(a) - 1;
@@ -424,7 +467,29 @@ __device__ __forceinline__ void top_pick(const TopLogitsParams& p, int row, uint
     };
     // the words that hold an entry at or above the pivot are noted, the others summed
     float least = key_floor(floor_key);   // (a key of 1 stands for the lowest float: every finite entry)
-    over_blocks([&](int u0, uint4 (&w)[kTopAgain]) {
+    // The words behind are requested before these are worked on where the loads are plain ones;
+    // the others' registers would take places from other rows (see top_pick_kernel).
+    constexpr bool AHEAD = ALIGNED;
+    uint4 w[kTopAgain], ahead[kTopAgain];
+    load_blocks(warp, w);
+    // meanwhile the sums of the blocks that are not looked at again
+    Run others;
+    if (!exact_blocks) {
+        uint32_t most = 0u;
+        for (int i = tid; i < p.n_blocks; i += kTopThreads) {
+            const uint32_t key = s_keys[i];
+            if (key < lo) most = max(most, key);
+        }
+        if (most) {
+            others.m = order_float(most);
+            for (int i = tid; i < p.n_blocks; i += kTopThreads) {
+                const uint32_t key = s_keys[i];
+                if (key && key < lo) others.s += s_sums[i] * ex2(ref_diff(order_float(key), others.m, p.scale));
+            }
+        }
+    }
+    for (int u0 = warp; u0 * PER < nb; u0 += kTopAgain * kTopWarps) {
+        if (AHEAD) load_blocks(u0 + kTopAgain * kTopWarps, ahead);
         float mx = -INFINITY;
 #pragma unroll
         for (int h = 0; h < kTopAgain; ++h) {
@@ -436,12 +501,18 @@ __device__ __forceinline__ void top_pick(const TopLogitsParams& p, int row, uint
             else mx = fmaxf(mx, wm);
         }
         rest.words<T, kTopAgain>(w, mx, p.scale);
-    });
+        if (AHEAD) {
+#pragma unroll
+            for (int h = 0; h < kTopAgain; ++h) w[h] = ahead[h];
+        } else {
+            load_blocks(u0 + kTopAgain * kTopWarps, w);
+        }
+    }
     __syncthreads();
     // then looked at in parallel, a thread each
     unsigned who = tid * PER < nb ? s_hit[tid] : 0u;
-    const int n_hit = cta_sum(__popc(who), s_part, slot);
-    int at = cta_prefix(__popc(who), s_part, slot);
+    int n_hit;
+    int at = cta_prefix(__popc(who), n_hit, s_part, slot);
     for (; who; who &= who - 1u, ++at)
         if (at < kTopCandMax) s_word[at] = tid * 32 + __ffs(who) - 1;
     __syncthreads();
@@ -499,22 +570,20 @@ __device__ __forceinline__ void top_pick(const TopLogitsParams& p, int row, uint
         }
         pivot = l;
     }
-    // ranks: eight threads share a candidate's comparisons, a warp sees four candidates
-    for (int i0 = 0; i0 < n; i0 += kTopThreads / 8) {
-        const int i = i0 + tid / 8;
+    // ranks: as many threads share a candidate's comparisons, one to eight of them, as leave
+    // one pass over the candidates
+    const int share = n > kTopThreads / 2 ? 0 : (n > kTopThreads / 4 ? 1 : (n > kTopThreads / 8 ? 2 : 3));
+    for (int i0 = 0; i0 < n; i0 += kTopThreads >> share) {
+        const int i = i0 + (tid >> share);
         const unsigned long long key = i < n ? s_cand[i] : 0ull;
         const bool ranked = i < n && (uint32_t)(key >> 32) >= pivot;
-        if (!__any_sync(0xffffffffu, ranked)) {
-            if ((tid & 7) == 0 && i < n) s_word[i] = K;
-            continue;
-        }
         int r = 0;
-#pragma unroll 4
-        for (int j = tid & 7; j < n; j += 8) r += s_cand[j] > key ? 1 : 0;
-        r += __shfl_xor_sync(0xffffffffu, r, 1);
-        r += __shfl_xor_sync(0xffffffffu, r, 2);
-        r += __shfl_xor_sync(0xffffffffu, r, 4);
-        if ((tid & 7) == 0 && i < n) s_word[i] = ranked ? r : K;
+        if (__any_sync(0xffffffffu, ranked)) {
+#pragma unroll 8
+            for (int j = tid & ((1 << share) - 1); j < n; j += 1 << share) r += s_cand[j] > key ? 1 : 0;
+        }
+        for (int o = 0; o < share; ++o) r += __shfl_xor_sync(0xffffffffu, r, 1 << o);
+        if ((tid & ((1 << share) - 1)) == 0 && i < n) s_word[i] = ranked ? r : K;
     }
     __syncthreads();
     for (int i = tid; i < n; i += kTopThreads) {
@@ -552,20 +621,19 @@ __device__ __forceinline__ void top_pick(const TopLogitsParams& p, int row, uint
             rest.words<T, kTopAgain>(w, mx, p.scale);
         });
     }
-    // the blocks that were not looked at again
-    for (int i = tid; i < p.n_blocks; i += kTopThreads) {
-        bool chosen = s_keys[i] >= lo;
-        if (exact_blocks || exact_words) {   // is i in the ascending list?
+    if (exact_blocks || exact_words) {   // the blocks that were not looked at again: not in the ascending list
+        if (exact_words) others = Run();
+        for (int i = tid; i < p.n_blocks; i += kTopThreads) {
             int a = 0, b = nb;
             while (a < b) {
                 const int mid = (a + b) >> 1;
                 if (s_blk[mid] < i) a = mid + 1;
                 else b = mid;
             }
-            chosen = a < nb && s_blk[a] == i;
+            if (!(a < nb && s_blk[a] == i) && s_keys[i]) others.sum(order_float(s_keys[i]), s_sums[i], p.scale);
         }
-        if (!chosen && s_keys[i]) rest.sum(order_float(s_keys[i]), s_sums[i], p.scale);
     }
+    rest.sum(others.m, others.s, p.scale);
     runs_cta(rest, taken, p.scale, s_run);
     if (tid == 0) {
         p.tail_out[row] = run_log(rest, p.scale, p.inv_t);
