@@ -276,17 +276,21 @@ __device__ __forceinline__ void distill_finish(const DistillParams& p, int row, 
 //
 // A row is split over a group of G CTAs; each holds its slice in shared memory from the read
 // to the write of the gradient, so the logits are read once and the gradient is written once.
-// The warps of a CTA have four jobs and meet at mbarriers only:
+// The warps of a CTA have five jobs and meet at mbarriers only:
 //   dense     A(i): the slice's (maximum, sum) over the entries that no id names;
 //             B(i): every logit in the slot becomes its gradient, 2^(z c - m2) times one
 //             factor.  In the order A(0) A(1) B(0) A(2) B(1) ..
+//   take      one thread per teacher entry: takes the named logits out of the slice (-inf), the
+//             teacher's row
 //   exchange  posts the slice's statistics, waits for the other slices', forms the factor
-//   entries   one thread per teacher entry: takes the named logits out of the slice (-inf),
-//             the teacher's row, the loss, and puts the named entries' gradients in after B(i)
+//   fix       one thread per teacher entry: puts the named entries' gradients in after B(i),
+//             then forms the loss
 //   copies    slices in and out
 // So the row behind is reduced while the statistics of the row before travel (2000 to 4000
-// cycles on a loaded memory system, about as long as A and B), and three slots keep one
-// slice arriving and one leaving meanwhile.
+// cycles on a loaded memory system, about as long as A and B), its named entries are out by
+// then, and three or four slots keep one slice arriving and one leaving meanwhile.  With take
+// and fix in the same warps, A(i + 2) waited for fix(i): 2000 rows of 20,000 bf16 took 48 us,
+// not 42.
 //
 // The exchange: a record per CTA in global memory, each 64-bit word a value and a tag that no
 // earlier row or call has used, so a word is valid when its tag is and nothing else has to
@@ -295,22 +299,23 @@ __device__ __forceinline__ void distill_finish(const DistillParams& p, int row, 
 // (j - 1)th.  In place of the logits the gradient is safe for the same reason: a slice is
 // written after every record of its row has arrived, and a record holds what was read.
 //
-// Bound by memory, a read and a write of each logit: 1792 rows of 248,320 bf16 take 309 us, 5.75
-// TB/s, 86 % of a copy's rate.  What is missing is residency: with 210 KB of slices in an SM and
+// Bound by memory, a read and a write of each logit: 1792 rows of 248,320 bf16 take 292 to
+// 309 us from one GPU to another, 5.75 TB/s and more, 86 to 91 % of a copy's rate.  What is missing is residency: with 210 KB of slices in an SM and
 // 3.5 us a row, the slot that waits for the exchange is one of three that would otherwise load
-// or store.  Reading the rows twice takes 392 us; slices in registers with the whole CTA waiting
+// or store.  Short rows are bound by the steps from A(i) to B(i), 1.5 us a row.  Of the 1792
+// rows' variants, reading the rows twice takes 392 us; slices in registers with the whole CTA waiting
 // on the exchange 834; two CTAs per SM with three slots of 32 KB 335, three CTAs 372 to 427;
 // four slots of 56 KB 345; the reduction and the gradient in separate warps 440; 256, 320, 448
 // or 512 dense threads 307 to 315.
 // ---------------------------------------------------------------------------------
 constexpr int kFuseDense = 384;                            // threads of the dense warps
-constexpr int kFuseNamed = SPEC_MAX_TEACHER;               // threads of the entries' warps
-constexpr int kFuseThreads = kFuseDense + kFuseNamed + 64; // and a warp each to exchange and to copy
+constexpr int kFuseNamed = SPEC_MAX_TEACHER;               // threads of either job on the entries
+constexpr int kFuseThreads = kFuseDense + 2 * kFuseNamed + 64;   // and a warp each to exchange and to copy
 constexpr int kDenseWarps = kFuseDense / 32, kNamedWarps = kFuseNamed / 32;
 constexpr int kFuseOcc = 1;                                // CTAs per SM
 constexpr int kFuseBatch = 4;                              // words a dense thread holds at once
 constexpr int kFuseSlice = 4480;                           // most words of a slice (70 KB)
-constexpr int kFuseSlots = 3;                              // slices in shared memory
+constexpr int kFuseRoom = 3 * kFuseSlice;                  // words of slices in shared memory
 constexpr int kFuseRecord = 4;                             // words of a record
 constexpr int kFuseRing = 2;                               // exchanges a record's place lasts
 constexpr int kFuseMaxCtas = 512;
@@ -337,14 +342,19 @@ __device__ __forceinline__ void bulk_s2g(void* dst, const void* src, unsigned by
 }
 __device__ __forceinline__ void bulk_s2g_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 __device__ __forceinline__ void bulk_s2g_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
-__device__ __forceinline__ void named_sync() { asm volatile("bar.sync 1, %0;" :: "n"(kFuseNamed) : "memory"); }
+template <int BAR>   // the warps of a job on the entries
+__device__ __forceinline__ void named_sync() { asm volatile("bar.sync %0, %1;" :: "n"(BAR), "n"(kFuseNamed) : "memory"); }
 
 // What is known of a row once its slices' statistics are together.
 struct FuseRow : RowEnds {
     float ref;        // unnamed entries: gradient 2^(z c - ref) factor
     float factor;
+    float wt, aT;     // the row's weight, the teacher's rest
     int skip, bad;
 };
+// What becomes of a named entry: the logits of student and teacher, its id and its place in
+// the slice (-1: none).
+struct FuseEntry { float z, a; int id, at; };
 
 // The slice of a row that one CTA holds: words [0, n) of it, whole words [a, b).
 template <typename T>
@@ -358,22 +368,24 @@ struct Slice {
     }
 };
 
-template <typename T>
+template <typename T, int SLOTS>
 __global__ void __launch_bounds__(kFuseThreads, kFuseOcc) distill_fused_kernel(DistillParams p) {
     constexpr int E = 16 / (int)sizeof(T);
     extern __shared__ __align__(128) uint8_t s_slots[];
     // full: a slice has arrived; ready: its named entries are out; reduced: A is done; stated:
     // the teacher's statistics are there; known: the row's FuseRow is; dense: B is done;
-    // fixed: the named entries' gradients are in.  A barrier's place comes back after two rows
-    // (slots: three): what a waiter waits for always needs, through the others, that it has
-    // left the wait two (three) rows before.
-    __shared__ __align__(8) uint64_t s_full[kFuseSlots], s_fixed[kFuseSlots];
-    __shared__ __align__(8) uint64_t s_ready[2], s_reduced[2], s_stated[2], s_known[2], s_dense[2];
+    // fixed: the named entries' gradients are in.  What comes back with its slot does so after
+    // the slot's last user, fixed; what comes back two rows on (by parity) after known, which
+    // `take` waits for.  So no waiter can miss a phase, and no shared word is written before
+    // its readers are done.
+    __shared__ __align__(8) uint64_t s_full[SLOTS], s_fixed[SLOTS], s_known[SLOTS], s_dense[SLOTS];
+    __shared__ __align__(8) uint64_t s_ready[2], s_reduced[2], s_stated[2];
     __shared__ uint32_t s_bits[kFuseSlice * E / 32];         // the slice's entries named so far
     __shared__ float2 s_tail[2][kDenseWarps], s_top[2][kNamedWarps], s_teach[2][kNamedWarps];
-    __shared__ float s_loss[kNamedWarps], s_wt[2], s_aT[2];
+    __shared__ float s_loss[2][kNamedWarps], s_wt[2], s_aT[2];
     __shared__ int s_flag[2];
-    __shared__ FuseRow s_row[2];
+    __shared__ FuseRow s_row[SLOTS];
+    __shared__ FuseEntry s_entry[SLOTS][kFuseNamed];
     const int tid = threadIdx.x, lane = tid & 31;
     const int group = blockIdx.x / p.group_size, rank = blockIdx.x - group * p.group_size;
     const int n_it = (p.rows - group + p.n_groups - 1) / p.n_groups;
@@ -385,19 +397,19 @@ __global__ void __launch_bounds__(kFuseThreads, kFuseOcc) distill_fused_kernel(D
         return Slice<T>(reinterpret_cast<const T*>(p.student) + (long)row_of(i) * p.ld, p.V, rank * p.slice, p.slice);
     };
     auto grad_of = [&](int i) { return reinterpret_cast<T*>(p.grad_out) + (long)row_of(i) * p.ld; };
-    auto slot_of = [&](int i) { return reinterpret_cast<uint4*>(s_slots) + (size_t)(i % kFuseSlots) * p.slice; };
+    auto slot_of = [&](int i) { return reinterpret_cast<uint4*>(s_slots) + (size_t)(i % SLOTS) * p.slice; };
 
     if (tid == 0) {
-        for (int q = 0; q < kFuseSlots; ++q) {
+        for (int q = 0; q < SLOTS; ++q) {
             mbar_init(&s_full[q], 1);
             mbar_init(&s_fixed[q], kFuseNamed);
+            mbar_init(&s_known[q], 1);
+            mbar_init(&s_dense[q], kDenseWarps);
         }
         for (int q = 0; q < 2; ++q) {
             mbar_init(&s_ready[q], kFuseNamed);
             mbar_init(&s_reduced[q], kDenseWarps);
             mbar_init(&s_stated[q], kNamedWarps);
-            mbar_init(&s_known[q], 1);
-            mbar_init(&s_dense[q], kDenseWarps);
             s_flag[q] = 0;
         }
         fence_mbar_init();
@@ -417,7 +429,7 @@ __global__ void __launch_bounds__(kFuseThreads, kFuseOcc) distill_fused_kernel(D
             if (i < n_it) {   // A(i)
                 const int n = slice_of(i).n;
                 const uint4* slot = slot_of(i);
-                wait(&s_full[i % kFuseSlots], i / kFuseSlots);
+                wait(&s_full[i % SLOTS], i / SLOTS);
                 wait(&s_ready[i & 1], i >> 1);
                 if (s_wt[i & 1] != 0.0f) {
                     float m = -INFINITY, s = 0.0f;
@@ -449,8 +461,8 @@ __global__ void __launch_bounds__(kFuseThreads, kFuseOcc) distill_fused_kernel(D
             if (i >= 1) {     // B(i - 1)
                 const int j = i - 1, n = slice_of(j).n;
                 uint4* slot = slot_of(j);
-                wait(&s_known[j & 1], j >> 1);
-                const FuseRow& row = s_row[j & 1];
+                wait(&s_known[j % SLOTS], j / SLOTS);
+                const FuseRow& row = s_row[j % SLOTS];
                 const float x = row.ref;
                 if (row.skip) {
                     for (int l = tid; l < n; l += kFuseDense) slot[l] = make_uint4(0u, 0u, 0u, 0u);
@@ -480,17 +492,17 @@ __global__ void __launch_bounds__(kFuseThreads, kFuseOcc) distill_fused_kernel(D
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive1(&s_dense[j & 1]);
+                if (lane == 0) mbar_arrive1(&s_dense[j % SLOTS]);
             }
         }
     } else if (tid < kFuseDense + kFuseNamed) {
-        // ---------------------------------------------------------------- entries
+        // ------------------------------------------------------------------- take
         const int k = tid - kFuseDense, warp = k >> 5;
-        // thread k's teacher entry of a row, the student's logit there (where it is known), its
-        // place in the slice (-1 outside), and what the row's entries share
-        struct Entry { int id; float a, z; int at; float wt, aT; };
+        // thread k's teacher entry of a row, the student's logit there (where it is known), and
+        // what the row's entries share
+        struct Entry { int id; float a, z; float wt, aT; };
         auto load = [&](int i, Entry& e) {
-            e.id = e.at = -1;
+            e.id = -1;
             e.a = e.z = e.aT = -INFINITY;
             e.wt = 0.0f;
             if (i >= n_it) return;
@@ -511,99 +523,93 @@ __global__ void __launch_bounds__(kFuseThreads, kFuseOcc) distill_fused_kernel(D
             if (sizeof(T) == 2) e.z = to_float((bf16_t)*reinterpret_cast<const volatile unsigned short*>(z));
             else e.z = to_float(*reinterpret_cast<const volatile float*>(z));
         };
-        // the named entries out of the slice, the teacher's statistics
-        auto prepare = [&](int i, Entry& e) {
+        Entry cur, nxt, far;
+        load(0, cur);
+        load(1, nxt);
+        gather(0, cur);
+        for (int i = 0; i < n_it; ++i) {
             const int par = i & 1;
+            gather(i + 1, nxt);
+            load(i + 2, far);
+            named_sync<1>();   // the bits are clear again
             const Slice<T> sl = slice_of(i);
-            const int at = e.id - sl.in.entry(sl.first);
-            e.at = known_id(e) && at >= 0 && at < sl.n * E ? at : -1;
+            const int in_slice = cur.id - sl.in.entry(sl.first);
+            const int at = known_id(cur) && in_slice >= 0 && in_slice < sl.n * E ? in_slice : -1;
             int f = 0;
-            if (e.at >= 0 && (atomicOr(&s_bits[at >> 5], 1u << (at & 31)) >> (at & 31)) & 1u) f = 1;   // listed twice
+            if (at >= 0 && (atomicOr(&s_bits[at >> 5], 1u << (at & 31)) >> (at & 31)) & 1u) f = 1;   // listed twice
+            if (i >= 2) wait(&s_known[(i - 2) % SLOTS], (i - 2) / SLOTS);
             if (k == 0) {
-                s_wt[par] = e.wt;
-                s_aT[par] = e.aT;
+                s_wt[par] = cur.wt;
+                s_aT[par] = cur.aT;
             }
-            wait(&s_full[i % kFuseSlots], i / kFuseSlots);
-            if (e.at >= 0 && e.wt != 0.0f) {
-                T* x = reinterpret_cast<T*>(slot_of(i)) + e.at;
-                e.z = to_float(*x);
+            wait(&s_full[i % SLOTS], i / SLOTS);
+            if (at >= 0 && cur.wt != 0.0f) {
+                T* x = reinterpret_cast<T*>(slot_of(i)) + at;
+                cur.z = to_float(*x);
                 *x = sizeof(T) == 2 ? (T)0xff80u : (T)-INFINITY;
             }
             mbar_arrive1(&s_ready[par]);
-            if (e.wt != 0.0f) {
-                const float a = known_id(e) ? e.a * p.inv_t : -INFINITY;
+            s_entry[i % SLOTS][k] = {cur.z, cur.a, cur.id, at};
+            if (cur.wt != 0.0f) {
+                const float a = known_id(cur) ? cur.a * p.inv_t : -INFINITY;
                 const float2 t = teacher_lanes<32>(make_float2(a, 1.0f));
-                const float2 z = pair_entries<T>(rank == 0 ? e.z : -INFINITY, c);
+                const float2 z = pair_entries<T>(rank == 0 ? cur.z : -INFINITY, c);
                 if (lane == 0) {
                     s_teach[par][warp] = t;
                     s_top[par][warp] = z;
                 }
                 if (rank == 0) {
-                    f |= (e.id < -1 || e.id >= p.V) ? 1 : 0;
-                    if (!(a < INFINITY) || !(e.aT < INFINITY) || !(fabsf(e.wt) < INFINITY)) f |= 2;
+                    f |= (cur.id < -1 || cur.id >= p.V) ? 1 : 0;
+                    if (!(a < INFINITY) || !(cur.aT < INFINITY) || !(fabsf(cur.wt) < INFINITY)) f |= 2;
                 }
                 if (f) atomicOr(&s_flag[par], f);
             }
             __syncwarp();
             if (lane == 0) mbar_arrive1(&s_stated[par]);
-            named_sync();   // every entry's bit has been looked at
-            if (e.at >= 0) s_bits[e.at >> 5] = 0u;
-        };
-        Entry cur, nxt, far;
-        load(0, cur);
-        load(1, nxt);
-        load(2, far);
-        gather(0, cur);
-        prepare(0, cur);
-        gather(1, nxt);
+            named_sync<1>();   // every entry's bit has been looked at
+            if (at >= 0) s_bits[at >> 5] = 0u;
+            cur = nxt;
+            nxt = far;
+        }
+    } else if (tid < kFuseDense + 2 * kFuseNamed) {
+        // -------------------------------------------------------------------- fix
+        const int k = tid - kFuseDense - kFuseNamed, warp = k >> 5;
         for (int i = 0; i < n_it; ++i) {
             const int row = row_of(i), par = i & 1;
-            const bool skip = cur.wt == 0.0f;
-            named_sync();   // the bits are clear again
-            if (i + 1 < n_it) prepare(i + 1, nxt);
-            gather(i + 2, far);
-            Entry more;
-            load(i + 3, more);
-            wait(&s_known[par], i >> 1);
-            const FuseRow r = s_row[par];
+            wait(&s_known[i % SLOTS], i / SLOTS);
+            const FuseRow r = s_row[i % SLOTS];
+            const FuseEntry e = s_entry[i % SLOTS][k];
+            const bool taught = r.top > -INFINITY, named = e.id >= 0 && e.id < p.V;
             float d = 0.0f;
-            if (!skip) {
-                const bool taught = r.top > -INFINITY;
-                const float lt = known_id(cur) && taught ? fmaf(cur.a, p.inv_t, -r.top) : -INFINITY;
-                const float pk = taught ? __expf(lt) / r.P : 0.0f;
-                d = r.bad ? NAN : (taught ? (ex2(rel<T>(cur.z, r.M, c)) / r.Z - pk) * (cur.wt * p.inv_t) : 0.0f);
-                if (rank == 0) {
-                    float l = 0.0f;
-                    if (taught) {
-                        if (known_id(cur)) l = entry_loss<T>(r, cur.a, cur.z, c, p.inv_t);
-                        if (k == 0) l += rest_loss(r, cur.aT);
-                    }
-                    l = warp_sum(l);
-                    if (lane == 0) s_loss[warp] = l;
-                }
+            if (!r.skip && e.at >= 0) {
+                const float pk = taught ? __expf(fmaf(e.a, p.inv_t, -r.top)) / r.P : 0.0f;
+                d = r.bad ? NAN : (taught ? (ex2(rel<T>(e.z, r.M, c)) / r.Z - pk) * (r.wt * p.inv_t) : 0.0f);
             }
-            if (rank == 0) {
-                named_sync();
-                if (k == 0) {
-                    float l = s_loss[0];
-                    for (int q = 1; q < kNamedWarps; ++q) l += s_loss[q];
-                    p.loss_out[row] = skip ? 0.0f : (r.bad ? NAN : l);
-                    if (p.lse_out) p.lse_out[row] = skip ? 0.0f : (r.bad ? NAN : pair_log<T>(r.M, r.Z, p.inv_t));
-                }
-            }
-            wait(&s_dense[par], i >> 1);
-            if (cur.at >= 0 && !skip) {
-                T* x = reinterpret_cast<T*>(slot_of(i)) + cur.at;
+            wait(&s_dense[i % SLOTS], i / SLOTS);
+            if (e.at >= 0 && !r.skip) {
+                T* x = reinterpret_cast<T*>(slot_of(i)) + e.at;
                 if (sizeof(T) == 2) *x = (T)__bfloat16_as_ushort(__float2bfloat16_rn(d));
                 else *x = (T)d;
             }
             fence_proxy_async_smem();
-            mbar_arrive1(&s_fixed[i % kFuseSlots]);
-            cur = nxt;
-            nxt = far;
-            far = more;
+            mbar_arrive1(&s_fixed[i % SLOTS]);
+            if (rank != 0) continue;
+            float l = 0.0f;   // the loss, behind what the slice waits for
+            if (!r.skip && taught) {
+                if (named) l = entry_loss<T>(r, e.a, e.z, c, p.inv_t);
+                if (k == 0) l += rest_loss(r, r.aT);
+            }
+            l = warp_sum(l);
+            if (lane == 0) s_loss[par][warp] = l;
+            named_sync<2>();
+            if (k == 0) {
+                l = s_loss[par][0];
+                for (int q = 1; q < kNamedWarps; ++q) l += s_loss[par][q];
+                p.loss_out[row] = r.skip ? 0.0f : (r.bad ? NAN : l);
+                if (p.lse_out) p.lse_out[row] = r.skip ? 0.0f : (r.bad ? NAN : pair_log<T>(r.M, r.Z, p.inv_t));
+            }
         }
-    } else if (tid < kFuseDense + kFuseNamed + 32) {
+    } else if (tid < kFuseDense + 2 * kFuseNamed + 32) {
         // --------------------------------------------------------------- exchange
         unsigned long long* recs = p.records + (size_t)group * kFuseRing * p.group_size * kFuseRecord;
         const float2 none = make_float2(-INFINITY, 0.0f);
@@ -621,7 +627,13 @@ __global__ void __launch_bounds__(kFuseThreads, kFuseOcc) distill_fused_kernel(D
             float2 T2 = none, N2 = none;
             bool token = false, late = false;
             wait(&s_reduced[par], i >> 1);
-            if (!skip) {
+            if (!skip && p.group_size == 1) {   // nobody to exchange with
+                T2 = pair_lanes<16>((lane & 15) < kDenseWarps ? s_tail[par][lane & 15] : none);
+                if (flag || dead) T2.x = NAN;
+                N2 = nn;
+                token = flag & 1;
+                late = dead;
+            } else if (!skip) {
                 unsigned long long* rec = recs + (size_t)(live % kFuseRing) * p.group_size * kFuseRecord;
                 const unsigned tag = epoch + 1u + live;
                 ++live;
@@ -668,9 +680,11 @@ __global__ void __launch_bounds__(kFuseThreads, kFuseOcc) distill_fused_kernel(D
                 if (bad) r.factor = NAN;
                 r.skip = skip;
                 r.bad = bad;
-                s_row[par] = r;
+                r.wt = wt;
+                r.aT = aT;
+                s_row[i % SLOTS] = r;
                 s_flag[par] = 0;
-                mbar_arrive1(&s_known[par]);
+                mbar_arrive1(&s_known[i % SLOTS]);
                 unsigned raise = 0u;
                 if (flag & 1) raise |= SPEC_DEV_TOKEN;
                 if ((flag & 2) || (bad && rank == 0 && !token && !late)) raise |= SPEC_DEV_NONFINITE;
@@ -682,7 +696,7 @@ __global__ void __launch_bounds__(kFuseThreads, kFuseOcc) distill_fused_kernel(D
     } else {
         // ----------------------------------------------------------------- copies
         auto issue = [&](int i) {   // the warp: row i's slice on its way to its slot
-            uint64_t* bar = &s_full[i % kFuseSlots];
+            uint64_t* bar = &s_full[i % SLOTS];
             const Slice<T> sl = slice_of(i);
             const bool on = !(p.weight && p.weight[row_of(i)] == 0.0f);
             if (on && lane < 2) {   // the words that are not whole
@@ -700,9 +714,9 @@ __global__ void __launch_bounds__(kFuseThreads, kFuseOcc) distill_fused_kernel(D
                 }
             }
         };
-        for (int i = 0; i < kFuseSlots && i < n_it; ++i) issue(i);
+        for (int i = 0; i < SLOTS && i < n_it; ++i) issue(i);
         for (int i = 0; i < n_it; ++i) {
-            wait(&s_fixed[i % kFuseSlots], i / kFuseSlots);
+            wait(&s_fixed[i % SLOTS], i / SLOTS);
             const Slice<T> sl = slice_of(i);
             if (lane == 0 && sl.a < sl.b)
                 bulk_s2g(grad_of(i) + sl.in.entry(sl.first + sl.a), slot_of(i) + sl.a, (unsigned)(sl.b - sl.a) * 16u);
@@ -710,11 +724,11 @@ __global__ void __launch_bounds__(kFuseThreads, kFuseOcc) distill_fused_kernel(D
                 const int l = lane == 0 ? 0 : sl.b;
                 if (lane == 0 ? sl.a > 0 : sl.b < sl.n) sl.in.store(grad_of(i), sl.first + l, slot_of(i)[l]);
             }
-            if (i + kFuseSlots < n_it) {
+            if (i + SLOTS < n_it) {
                 if (lane == 0) bulk_s2g_wait_read();
                 fence_proxy_async_smem();   // the words that were not whole, before the copy that may cover them
                 __syncwarp();
-                issue(i + kFuseSlots);
+                issue(i + SLOTS);
             }
         }
         if (lane == 0) {
@@ -746,13 +760,15 @@ static cudaError_t fused_launch(DistillParams p, cudaStream_t stream) {
     p.n_groups = groups;
     p.group_size = size;
     p.slice = (words + size - 1) / size;
-    const size_t smem = (size_t)kFuseSlots * p.slice * 16;
-    const cudaError_t e = cudaFuncSetAttribute(distill_fused_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               kFuseSlots * kFuseSlice * 16);
+    // a fourth slot where there is room for one: 1000 rows of 20,001 float32 take 41 us instead of
+    // 43, 2000 of 20,000 bf16 39 instead of 42 (smaller slices for its sake cost more than it gives)
+    const int slots = 4 * p.slice <= kFuseRoom ? 4 : 3;
+    const void* kern = slots == 4 ? (const void*)distill_fused_kernel<T, 4> : (const void*)distill_fused_kernel<T, 3>;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kFuseRoom * 16);
     if (e != cudaSuccess) return e;
     void* args[] = {&p};
-    return cudaLaunchCooperativeKernel((const void*)distill_fused_kernel<T>, dim3(groups * size), dim3(kFuseThreads), args,
-                                       smem, stream);
+    return cudaLaunchCooperativeKernel(kern, dim3(groups * size), dim3(kFuseThreads), args, (size_t)slots * p.slice * 16,
+                                       stream);
 }
 
 static size_t align256(size_t n) { return (n + 255) / 256 * 256; }
