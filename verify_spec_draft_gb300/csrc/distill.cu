@@ -299,14 +299,14 @@ __device__ __forceinline__ void distill_finish(const DistillParams& p, int row, 
 // (j - 1)th.  In place of the logits the gradient is safe for the same reason: a slice is
 // written after every record of its row has arrived, and a record holds what was read.
 //
-// Bound by memory, a read and a write of each logit: 1792 rows of 248,320 bf16 take 292 to
-// 309 us from one GPU to another, 5.75 TB/s and more, 86 to 91 % of a copy's rate.  What is missing is residency: with 210 KB of slices in an SM and
-// 3.5 us a row, the slot that waits for the exchange is one of three that would otherwise load
-// or store.  Short rows are bound by the steps from A(i) to B(i), 1.5 us a row.  Of the 1792
-// rows' variants, reading the rows twice takes 392 us; slices in registers with the whole CTA waiting
-// on the exchange 834; two CTAs per SM with three slots of 32 KB 335, three CTAs 372 to 427;
-// four slots of 56 KB 345; the reduction and the gradient in separate warps 440; 256, 320, 448
-// or 512 dense threads 307 to 315.
+// Bound by memory, a read and a write of each logit: 1792 rows of 248,320 bf16 take 292 to 309 us
+// from one GPU to another, 5.75 TB/s and more, 86 to 91 % of a copy's rate.  What is missing is
+// residency: with 210 KB of slices in an SM and 3.5 us a row, the slot that waits for the
+// exchange is one of three that would otherwise load or store.  Short rows are bound by the
+// steps from A(i) to B(i), 1.5 us a row.  For the 1792 rows, reading them twice takes 392 us;
+// slices in registers with the whole CTA waiting on the exchange 834; two CTAs per SM with three
+// slots of 32 KB 335, three CTAs 372 to 427; four slots of 56 KB 345; the reduction and the
+// gradient in separate warps 440; 256, 320 or 512 dense threads 2 to 5 % longer.
 // ---------------------------------------------------------------------------------
 constexpr int kFuseDense = 384;                            // threads of the dense warps
 constexpr int kFuseNamed = SPEC_MAX_TEACHER;               // threads of either job on the entries
