@@ -140,3 +140,29 @@ def test_calls_on_two_streams(spec):
         assert torch.equal(c["loss"], loss["loss"])
         for m in (a, b, c):
             assert vsd.device_status(m["ws"]) == 0
+
+
+def test_outputs_and_workspaces_of_another_call(spec):
+    """What a caller passes to be written is refused where it does not fit, before anything runs."""
+    z = torch.randn((6, 1000), generator=torch.Generator().manual_seed(1)).cuda()
+    top = vsd.top_logits(z, 20)
+    with pytest.raises(ValueError):
+        vsd.top_logits(z, 64, out=top)                                    # room for 20
+    for name in ("values", "tail", "lse"):
+        with pytest.raises(ValueError):
+            vsd.top_logits(z, 20, out=dict(top, **{name: top[name].double()}))
+    with pytest.raises(ValueError):
+        vsd.top_logits(z, 20, out=dict(top, ids=top["ids"].long()))
+    d = vsd.distill(z, top["values"], top["ids"], tail=top["tail"], grad=True)
+    for bad in (dict(loss=d["loss"][:5]), dict(lse=d["lse"].cpu()), dict(loss=None), dict(grad=d["grad"][:, :999])):
+        with pytest.raises(ValueError):
+            vsd.distill(z, top["values"], top["ids"], tail=top["tail"], grad=True, out=dict(d, **bad))
+    host = torch.zeros(1 << 20, dtype=torch.uint8)
+    with pytest.raises(ValueError):
+        vsd.top_logits(z, 20, ws=host)
+    with pytest.raises(ValueError):
+        vsd.distill(z, top["values"], top["ids"], ws=host)
+    with pytest.raises(ValueError):
+        vsd.process_logits(z.view(1, 6, 1000), ws=host)
+    again = vsd.top_logits(z, 20, out=dict(values=top["values"], ids=top["ids"], tail=top["tail"], lse=None))
+    assert again["lse"] is None

@@ -191,6 +191,21 @@ def _addrs(device, names, tensors, dtypes, shapes):
     return out
 
 
+def _need_out(out, device, **want):
+    """The caller's outputs, checked as _need does; lse may be left out."""
+    for name, (dtype, shape) in want.items():
+        t = out.get(name)
+        if t is not None or name != "lse":
+            _need(t, name, device, dtype, shape)
+
+
+def _ws_bytes(ws, device):
+    """A workspace's size, which the library compares with what it needs."""
+    if ws.get_device() != device.index:
+        raise ValueError(f"the workspace is on {ws.device}, expected {device}")
+    return ws.numel()
+
+
 _HERE = contextlib.nullcontext()
 
 
@@ -644,7 +659,7 @@ def process_logits(logits, history=None, lengths=None, prompt_lengths=None, bloc
     code = lib.spec_process_logits(
         logits.data_ptr(), _dtype_code(logits), B, R, V, ld, a_hist if Lmax else None, Lmax, a_len, a_prompt,
         a_block if R > 1 else None, a_rep, a_freq, a_pres, a_temp, a_ids if nb else None, a_values if nb else None,
-        nb, a_mask, mask_rows, out["logits"].data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream))
+        nb, a_mask, mask_rows, out["logits"].data_ptr(), ws.data_ptr(), _ws_bytes(ws, dev), _stream(stream))
     if code != OK:
         raise SpecError(code, "spec_process_logits")
     out["ws"] = ws
@@ -668,13 +683,17 @@ def top_logits(logits, k, temperature=1.0, ws=None, out=None, stream=None):
                        ids=torch.empty(sized, dtype=torch.int32, device=dev),
                        tail=torch.empty(lead, dtype=torch.float32, device=dev),
                        lse=torch.empty(lead, dtype=torch.float32, device=dev))
+    else:
+        _need_out(out, dev, values=(torch.float32, (*lead, k)), ids=(torch.int32, (*lead, k)),
+                  tail=(torch.float32, lead), lse=(torch.float32, lead))
     if ws is None:
         with _made_on(stream):
             ws = workspace(OP_TOP_LOGITS, rows, k, V, 0, dev, stream)
     lse = out.get("lse")
     code = lib.spec_top_logits(logits.data_ptr(), _dtype_code(logits), rows, V, ld, k, float(temperature),
                                out["values"].data_ptr(), out["ids"].data_ptr(), out["tail"].data_ptr(),
-                               None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream))
+                               None if lse is None else lse.data_ptr(), ws.data_ptr(), _ws_bytes(ws, dev),
+                               _stream(stream))
     if code != OK:
         raise SpecError(code, "spec_top_logits")
     out["ws"] = ws
@@ -706,8 +725,10 @@ def distill(student, values, ids, tail=None, weight=None, temperature=1.0, grad=
                        lse=torch.empty(lead, dtype=torch.float32, device=dev))
             if grad:
                 out["grad"] = _rows_like(student, ld)
-    elif grad:
-        _need_same_rows(out["grad"], "grad", student, ld)
+    else:
+        _need_out(out, dev, loss=(torch.float32, lead), lse=(torch.float32, lead))
+        if grad:
+            _need_same_rows(out["grad"], "grad", student, ld)
     if ws is None:
         with _made_on(stream):
             ws = workspace(OP_DISTILL, rows, K, V, 0, dev, stream)
@@ -715,7 +736,7 @@ def distill(student, values, ids, tail=None, weight=None, temperature=1.0, grad=
     code = lib.spec_distill(student.data_ptr(), _dtype_code(student), rows, V, ld, a_values, _dtype_code(values),
                             a_ids, K, a_tail, a_weight, float(temperature), out["loss"].data_ptr(),
                             None if lse is None else lse.data_ptr(), out["grad"].data_ptr() if grad else None,
-                            ws.data_ptr(), ws.numel(), _stream(stream))
+                            ws.data_ptr(), _ws_bytes(ws, dev), _stream(stream))
     if code != OK:
         raise SpecError(code, "spec_distill")
     out["ws"] = ws
