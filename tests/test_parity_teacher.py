@@ -95,6 +95,16 @@ def test_top_distributions(spec, dtype, kind, V, K):
     check_top(z, K, 1.0, vsd.top_logits(z, K))
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("R,V,K", [(40, 151936, 128), (33, 151937, 128), (160, 33024, 100), (700, 4000, 20)])
+def test_top_many_rows(spec, dtype, R, V, K):
+    """Rows enough for picks of their own launch, chosen blocks enough for several looks."""
+    z = rows_of(R, V, dtype, seed=V + K, kind="coarse" if R == 33 else "gaussian")
+    out = vsd.top_logits(z, K)
+    check_top(z, K, 1.0, out)
+    assert vsd.device_status(out["ws"]) == 0
+
+
 @pytest.mark.parametrize("dtype,V,ld", [(F32, 1001, 1003), (BF16, 1001, 1009), (BF16, 5000, 5008)])
 def test_top_row_stride(spec, dtype, V, ld):
     z = rows_of(6, V, dtype, seed=2, ld=ld)
@@ -359,6 +369,31 @@ def test_distill_workspace_reuse(spec):
         for k in ("loss", "lse", "grad"):
             assert torch.equal(first[k], again[k])
     check_distill(z, values, ids, tl, None, 1.0, first)
+
+
+@pytest.mark.parametrize("R,V,K,dtype", [(1700, 1003, 12, BF16), (1100, 17005, 20, F32), (1000, 30001, 128, BF16),
+                                         (230, 60000, 64, F32), (200, 151937, 33, BF16)])
+def test_distill_many_rows_per_group(spec, R, V, K, dtype):
+    """Rows behind one another in the same CTAs, some of them skipped: every 37th row and the
+    last ones against the oracle, twice the same bits."""
+    z = rows_of(8, V, dtype, seed=V).repeat(R // 8 + 1, 1)[:R].contiguous()
+    z += torch.randint(-3, 4, (R, 1), generator=torch.Generator().manual_seed(R)).cuda()   # (small whole numbers)
+    top = vsd.top_logits(z + torch.tensor(0.5, dtype=dtype, device="cuda"), K)
+    ids = top["ids"].clone()
+    ids[::3] = (ids[::3] + 1) % V
+    ids = torch.where((ids.sort(1).values.diff(dim=1) == 0).any(1, keepdim=True), top["ids"], ids)
+    weight = torch.randn(R, generator=torch.Generator().manual_seed(V)).cuda()
+    weight[torch.rand(R, generator=torch.Generator().manual_seed(K)) < 0.2] = 0.0
+    args = dict(tail=top["tail"], weight=weight, grad=True)
+    out = vsd.distill(z, top["values"], ids, **args)
+    assert vsd.device_status(out["ws"]) == 0
+    at = torch.cat([torch.arange(0, R, 37), torch.arange(R - 4, R)]).cuda()
+    check_distill(z[at], top["values"][at], ids[at], top["tail"][at], weight[at], 1.0,
+                  {k: out[k][at] for k in ("loss", "lse", "grad")})
+    first = {k: out[k].clone() for k in ("loss", "lse", "grad")}
+    again = vsd.distill(z, top["values"], ids, ws=out["ws"], out=out, **args)
+    for k in first:
+        assert torch.equal(first[k], again[k])
 
 
 def test_distill_refusals(spec):
