@@ -628,6 +628,7 @@ spec_status spec_process_logits(const void *logits, spec_dtype dtype, int B, int
  *                   never taken: slots left over hold id -1 and value -inf.
  *     tail          ln sum exp(z_v / t) over the entries not taken (-inf when none is left)
  *     lse           ln sum exp(z_v / t) over all entries
+ *                   (either is -inf or +inf where it lies beyond float32's range)
  *   logits      [rows] rows of V entries, ld entries apart (ld >= V), float32 or bf16.
  *   values_out  float32 [rows, K]; ids_out int32 [rows, K]; tail_out float32 [rows];
  *               lse_out float32 [rows] (nullable).

@@ -160,27 +160,32 @@ struct SegWords {
     }
 };
 
-// Weights relative to a reference, in base 2: entry x of a row scaled by c = log2(e) / t weighs
-// 2^(x c - m c), where m c is rounded once and x c is exact inside an FFMA (ref_rel).  Sums that
-// belong to different references are brought together by the difference of the same rounded
-// m c (ref_diff), so that rounding cancels.  A reference so low that m c overflows (a row
-// filled with the type's lowest value) takes differences before the scaling.
-__device__ __forceinline__ float ref_diff(float a, float b, float c) {   // log2 weight of a relative to b >= a
+// Weights relative to a reference m, in base 2: entry x of a row scaled by c = log2(e) / t weighs
+// 2^(x c - R(m)).  While |m c| is at most kRefNear, R(m) is m c rounded once, x c is exact inside
+// an FFMA (ref_rel), and sums that belong to different references are brought together by the
+// difference of the same rounded m c (ref_diff), so that rounding cancels: it moves all weights
+// by one factor, at most 2^4.  Beyond (rows masked with -1e10, -1e30 or the type's lowest value,
+// large logits over a small temperature) that factor would leave float32's range, and m c itself
+// can overflow.  There R(m) is m c exactly: differences are taken before the scaling.
+constexpr float kRefNear = 67108864.0f;   // 2^26: its products are rounded by 4 at most
+__device__ __forceinline__ bool ref_near(float y) { return fabsf(y) <= kRefNear; }
+__device__ __forceinline__ float ref_diff(float a, float b, float c) {   // R(a) - R(b), b >= a, b > -inf
     const float x = a * c, y = b * c;
-    return fminf(x, y) > -INFINITY ? x - y : (a - b) * c;
+    if (ref_near(y)) return ref_near(x) ? x - y : fmaf(a, c, -y);
+    return ref_near(x) ? -fmaf(b, c, -x) : (a - b) * c;
 }
 __device__ __forceinline__ float ref_rel(float x, float m, float c) {    // log2 weight of entry x relative to m >= x
     const float y = m * c;
-    return y > -INFINITY ? fmaf(x, c, -y) : (x - m) * c;
+    return ref_near(y) ? fmaf(x, c, -y) : (x - m) * c;
 }
-__device__ __forceinline__ float ref_log(float m, float s, float c, float inv_t) {   // ln of s 2^(m c)
+__device__ __forceinline__ float ref_log(float m, float s, float c, float inv_t) {   // ln of s 2^R(m)
     const float x = m * c;
-    return x > -INFINITY ? (x + log2f(s)) * 0.69314718055994531f : fmaf(m, inv_t, logf(s));
+    return ref_near(x) ? (x + log2f(s)) * 0.69314718055994531f : fmaf(m, inv_t, logf(s));
 }
-// A word's weights relative to a reference that overflows when scaled: out of line, since
-// hardly any row has one and the streaming loops are short without it.
+// A word's weights relative to a reference beyond kRefNear: out of line, since hardly any row has
+// one and the streaming loops are short without it.
 template <typename T>
-__device__ __noinline__ float word_sum_low(uint4 w, float m, float c) {
+__device__ __noinline__ float word_sum_far(uint4 w, float m, float c) {
     float s = 0.0f;
     for (int k = 0; k < 16 / (int)sizeof(T); ++k) s += ex2((word_pick<T>(w, k) - m) * c);
     return s;
@@ -191,7 +196,7 @@ __device__ __forceinline__ float words_sum(const uint4 (&w)[N], float m, float c
     const float x = m * c;
     f2x acc[2] = {f2_pack(0.0f, 0.0f), f2_pack(0.0f, 0.0f)};
     const f2x cc = f2_pack(c, c);
-    if (x > -INFINITY) {
+    if (ref_near(x)) {
         const f2x mm = f2_pack(-x, -x);
 #pragma unroll
         for (int h = 0; h < N; ++h)
@@ -202,7 +207,7 @@ __device__ __forceinline__ float words_sum(const uint4 (&w)[N], float m, float c
     } else {
         if (!(m > -INFINITY)) return 0.0f;
         float s = 0.0f;
-        for (int h = 0; h < N; ++h) s += word_sum_low<T>(w[h], m, c);
+        for (int h = 0; h < N; ++h) s += word_sum_far<T>(w[h], m, c);
         return s;
     }
     const float2 a = f2_unpack(acc[0]), b = f2_unpack(acc[1]);
