@@ -83,3 +83,111 @@ def test_top_border(spec, V, K, t):
     np.testing.assert_array_equal(out["ids"].cpu().numpy(), ref["ids"])
     for k in ("tail", "lse"):
         check_log(f64(out[k]), ref[k])
+
+
+# ---------------------------------------------------------------------------------
+def check_distill(z, values, ids, tail, t, out):
+    """A probability is off by E = 2 EPS + the teacher's 2^-24 (4 max|a / t| + 100), relative; a loss, sum
+    p (ln p - ln q), by 2 E (1 + sum p |ln p - ln q|), a gradient by 2 E / t of the terms it is made of,
+    and by the rounding to its type.  Loss and gradient do not depend on what is added to a row, so
+    the row's maximum is taken off first, and q_v / q_T is formed against the rest's own maximum: next to
+    1e30 float64 has no room for a ln n."""
+    z, values, ids = f64(z), f64(values), ids.cpu().numpy()
+    check_log(f64(out["lse"]), np.array([ot.lse(row / t) for row in z]))
+    z = z - z.max(1, keepdims=True)
+    with np.errstate(all="ignore"):   # (the oracle's own q_v / q_T, which is not used)
+        ref = ot.distill(z, values, ids, None if tail is None else f64(tail), None, t)
+    a = np.abs(values[ids >= 0]).max() / t
+    if tail is not None:
+        a = max(a, np.abs(f64(tail)).max())
+    e = 2 * EPS + 2.0 ** -24 * (4 * a + 100)
+    step = 0.0
+    if "grad" in out:
+        step = 2.0 ** -8 if out["grad"].dtype == BF16 else 2.0 ** -23
+    for r in range(z.shape[0]):
+        p, q = ref["p"][r], ref["q"][r]
+        lq = z[r] / t - ref["lse"][r]
+        rest = np.ones(z.shape[1], bool)
+        rest[ids[r][ids[r] >= 0]] = False
+        lqt = ot.lse(lq[rest])
+        share = np.zeros(z.shape[1])
+        if rest.any():
+            share[rest] = np.exp((z[r][rest] - z[r][rest].max()) / t)
+            share /= share.sum()
+        lqb = np.append(np.where(ids[r] >= 0, lq[np.maximum(ids[r], 0)], 0.0), lqt)
+        on = p > 0
+        size = (p[on] * np.abs(np.log(p[on]) - lqb[on])).sum()
+        with np.errstate(over="ignore"):
+            want = float(np.float32(ref["loss"][r]))
+        got = float(out["loss"][r])
+        if np.isinf(want):
+            assert got == want, (r, got)
+        else:
+            assert abs(got - want) <= 2 * e * (1 + size), (r, got, want)
+        if "grad" not in out:
+            continue
+        parts = q + p[-1] * share
+        for k, v in enumerate(ids[r]):
+            if v >= 0:
+                parts[v] += p[k]
+        g = ref["grad"][r]
+        g[rest] = (q - p[-1] * share)[rest] / t
+        bad = np.abs(f64(out["grad"][r]) - g) > 2 * e / t * parts + step * np.abs(g) + 1e-37
+        assert not bad.any(), (r, np.nonzero(bad)[0][:5], f64(out["grad"][r])[bad][:5], g[bad][:5])
+
+
+def named_in(z, kind, K, seed):
+    """K ids a row, among them every entry that the mask of `kind` allows."""
+    g = torch.Generator().manual_seed(seed)
+    R, V = z.shape
+    ids = torch.full((R, K), -1, dtype=torch.int32)
+    for r in range(R):
+        pick = torch.randperm(V, generator=g)
+        if kind in ("rest", "levels"):
+            allowed = (z[r].float().cpu().abs() < 1e6).nonzero()[:, 0]
+            pick = torch.cat([allowed, pick[~torch.isin(pick, allowed)]])
+        n = min(K, V)
+        ids[r, :n] = pick[:n].to(torch.int32)
+    return ids.cuda()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("kind", ["rest", "whole", "levels", "two", "high"])
+@pytest.mark.parametrize("R,V,K", [(3, 9000, 12), (2, 33001, 16), (170, 1100, 20), (2, 50, 12)])
+def test_distill(spec, dtype, kind, R, V, K):
+    for far in FAR:
+        for t in (1.0, 0.25, 3.0):
+            z = far_rows(kind, R, V, far, dtype, t)
+            ids = named_in(z, kind, K, seed=V)
+            values = torch.randn(ids.shape, generator=torch.Generator().manual_seed(K)).cuda()
+            for tail in (None, torch.full((R,), -0.5, device="cuda")):
+                for grad in (False, True):
+                    out = vsd.distill(z, values, ids, tail=tail, temperature=t, grad=grad)
+                    check_distill(z, values, ids, tail, t, out)
+                    assert vsd.device_status(out["ws"]) == 0
+
+
+@pytest.mark.parametrize("t", [1.0, 0.3, 7.0])
+@pytest.mark.parametrize("V,K", [(9000, 20), (33001, 100)])
+def test_distill_border(spec, V, K, t):
+    z = far_rows("border", 4, V, 0.0, F32, t)
+    ids = named_in(z, "border", K, seed=V)
+    values = torch.randn(ids.shape, generator=torch.Generator().manual_seed(K)).cuda()
+    for tail in (None, torch.full((4,), 1.5, device="cuda")):
+        for grad in (False, True):
+            out = vsd.distill(z, values, ids, tail=tail, temperature=t, grad=grad)
+            check_distill(z, values, ids, tail, t, out)
+            assert vsd.device_status(out["ws"]) == 0
+
+
+def test_processed_rows_are_learned_from(spec):
+    """Rows masked with the type's lowest value, over a temperature by process_logits, whose grammar
+    allows fewer tokens than the teacher has entries."""
+    V, K = 5003, 16
+    x = far_rows("rest", 6, V, LOW, F32, 1.0)
+    y = vsd.process_logits(x[None], temperature=torch.tensor([1.3]).cuda())["logits"][0]
+    ids = named_in(y, "rest", K, seed=1)
+    values = torch.randn(ids.shape, generator=torch.Generator().manual_seed(2)).cuda()
+    out = vsd.distill(y, values, ids, grad=True)
+    check_distill(y, values, ids, None, 1.0, out)
+    assert vsd.device_status(out["ws"]) == 0

@@ -33,30 +33,14 @@ __device__ __forceinline__ float warp_max_nan(float x) {
     asm volatile("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
     return r;
 }
-// Pairs (m2, s): s is the sum of the weights 2^(x c - m2) of some entries and m2 their maximum
-// times c, rounded once, so that two pairs meet by one subtraction.  NaN shows in m2.  A
-// maximum that overflows when scaled, which only rows filled with the type's lowest value
-// have, counts as kLow, its entries' weights taken from differences before the scaling.
-constexpr float kLow = -3.402823466e38f;
-template <typename T>
-__device__ __forceinline__ float lowest() { return sizeof(T) == 2 ? -3.38953139e38f : kLow; }
-__device__ __forceinline__ float scaled(float m, float c) { return m > -INFINITY ? fmaxf(m * c, kLow) : m; }
-// log2 of entry x's weight relative to m2
-template <typename T>
-__device__ __forceinline__ float rel(float x, float m2, float c) {
-    return m2 > kLow ? fmaf(x, c, -m2) : (x - lowest<T>()) * c;
+// Pairs (m, s): the maximum of some entries and the sum of their weights relative to it
+// (row_words.cuh); empty: (-inf, 0).  NaN shows in m.
+__device__ __forceinline__ float pair_weight(float2 v, float m, float c) {   // v's sum relative to m >= v.x
+    return v.x == -INFINITY ? 0.0f : v.y * ex2(ref_rel(v.x, m, c));
 }
-// ln of s 2^m2
-template <typename T>
-__device__ __forceinline__ float pair_log(float m2, float s, float inv_t) {
-    return m2 > kLow ? (m2 + log2f(s)) * 0.69314718055994531f : fmaf(lowest<T>(), inv_t, logf(s));
-}
-__device__ __forceinline__ float2 pair_merge(float2 a, float2 b) {
+__device__ __forceinline__ float2 pair_merge(float2 a, float2 b, float c) {
     const float m = f_max_nan(a.x, b.x);
-    float s = 0.0f;
-    if (a.x != -INFINITY) s += a.y * ex2(a.x - m);
-    if (b.x != -INFINITY) s += b.y * ex2(b.x - m);
-    return make_float2(m, s);
+    return make_float2(m, pair_weight(a, m, c) + pair_weight(b, m, c));
 }
 // Over the N lanes that differ in their low bits.
 template <int N>
@@ -72,15 +56,14 @@ __device__ __forceinline__ float lanes_sum(float s) {
     return s;
 }
 template <int N>
-__device__ __forceinline__ float2 pair_lanes(float2 v) {
+__device__ __forceinline__ float2 pair_lanes(float2 v, float c) {
     const float m = N == 32 ? warp_max_nan(v.x) : lanes_max_nan<N>(v.x);
-    return make_float2(m, lanes_sum<N>(v.x == -INFINITY ? 0.0f : v.y * ex2(v.x - m)));
+    return make_float2(m, lanes_sum<N>(pair_weight(v, m, c)));
 }
 // The pair of one entry per lane.
-template <typename T>
 __device__ __forceinline__ float2 pair_entries(float x, float c) {
-    const float m2 = scaled(warp_max_nan(x), c);
-    return make_float2(m2, lanes_sum<32>(x == -INFINITY ? 0.0f : ex2(rel<T>(x, m2, c))));
+    const float m = warp_max_nan(x);
+    return make_float2(m, lanes_sum<32>(x == -INFINITY ? 0.0f : ex2(ref_rel(x, m, c))));
 }
 // The teacher's pairs: (maximum, sum of e^(x - maximum)).
 template <int N>
@@ -89,7 +72,6 @@ __device__ __forceinline__ float2 teacher_lanes(float2 v) {
     return make_float2(m, lanes_sum<N>(v.x == -INFINITY ? 0.0f : v.y * __expf(v.x - m)));
 }
 
-constexpr float kLn2 = 0.69314718055994531f;
 constexpr uint32_t kBadToken = 0x7fc0dead;   // a NaN that says: an id is listed twice
 
 // What the rows' ends share.  (M, Z): the student's pair, (mT, sT) that of its unnamed entries;
@@ -97,16 +79,16 @@ constexpr uint32_t kBadToken = 0x7fc0dead;   // a NaN that says: an id is listed
 // against it, P = e + eT; f the student's named weight against M.
 //
 // The share of the rest that the student has too much is
-//     q_T - p_T = f_T / Z - e_T / P = (f_T e - e_T f) / (Z P),        f_T = sT 2^(mT - M),
+//     q_T - p_T = f_T / Z - e_T / P = (f_T e - e_T f) / (Z P),    f_T = sT 2^((mT - M) c),
 // where the rest's own share is left out: with little named mass both shares are nearly 1,
 // and their difference would keep none of its digits.  G is that without (sT / (Z P)).  The
 // rest's part of the loss, p_T (ln p_T - ln q_T) = -p_T ln(1 + (q_T - p_T) / p_T), goes by it
 // too, unless the shares are far apart: then the logarithms are taken one by one, for f_T may
 // be too small for a float.
 struct RowEnds { float M, Z, mT, sT, top, e, eT, P, G; };
-__device__ __forceinline__ RowEnds row_ends(float2 T2, float2 N2, float2 teach, float aT) {
+__device__ __forceinline__ RowEnds row_ends(float2 T2, float2 N2, float2 teach, float aT, float c) {
     RowEnds r;
-    const float2 A = pair_merge(T2, N2);
+    const float2 A = pair_merge(T2, N2, c);
     r.M = A.x;
     r.Z = A.y;
     r.mT = T2.x;
@@ -115,21 +97,31 @@ __device__ __forceinline__ RowEnds row_ends(float2 T2, float2 N2, float2 teach, 
     r.e = teach.x > -INFINITY ? teach.y * __expf(teach.x - r.top) : 0.0f;
     r.eT = aT > -INFINITY ? __expf(aT - r.top) : 0.0f;
     r.P = r.e + r.eT;
-    const float f = N2.x > -INFINITY ? N2.y * ex2(N2.x - A.x) : 0.0f;
-    r.G = T2.x > -INFINITY ? fmaf(ex2(T2.x - A.x), r.e, -__fdividef(r.eT * f, T2.y)) : 0.0f;
+    const float f = pair_weight(N2, A.x, c);
+    r.G = T2.x > -INFINITY ? fmaf(ex2(ref_rel(T2.x, A.x, c)), r.e, -__fdividef(r.eT * f, T2.y)) : 0.0f;
     return r;
 }
-template <typename T>
-__device__ __forceinline__ float entry_loss(const RowEnds& r, float a, float z, float c, float inv_t) {
-    const float lt = fmaf(a, inv_t, -r.top), pk = __expf(lt) / r.P;
-    return pk > 0.0f ? pk * ((lt - logf(r.P)) - (rel<T>(z, r.M, c) - log2f(r.Z)) * kLn2) : 0.0f;
+// p (M - x) / t, for a finite x so far below M that the difference overflows over t.  By halves, since
+// M - x may overflow as well; the logarithms of the sums do not show beside it.
+static __device__ __noinline__ float far_loss(float p, float M, float x, float inv_t) {
+    return (2.0f * p * inv_t) * (0.5f * M - 0.5f * x);
 }
-__device__ __forceinline__ float rest_loss(const RowEnds& r, float aT) {
+__device__ __forceinline__ float entry_loss(const RowEnds& r, float a, float z, float inv_t) {
+    const float lt = fmaf(a, inv_t, -r.top), pk = __expf(lt) / r.P;
+    if (!(pk > 0.0f)) return 0.0f;
+    const float lz = (z - r.M) * inv_t;
+    if (lz == -INFINITY && z > -INFINITY) return far_loss(pk, r.M, z, inv_t);
+    return pk * ((lt - logf(r.P)) - (lz - logf(r.Z)));
+}
+__device__ __forceinline__ float rest_loss(const RowEnds& r, float aT, float inv_t) {
     const float pT = r.eT / r.P;
     if (!(pT > 0.0f)) return 0.0f;
-    const float d = r.mT > -INFINITY ? r.sT * r.G / (r.Z * r.eT) : -1.0f;
+    const bool some = r.mT > -INFINITY;
+    const float d = some ? r.sT * r.G / (r.Z * r.eT) : -1.0f;
     if (fabsf(d) < 0.5f) return -pT * log1pf(d);
-    const float lq = r.mT > -INFINITY ? (r.mT - r.M + log2f(r.sT) - log2f(r.Z)) * kLn2 : -INFINITY;
+    const float lm = (r.mT - r.M) * inv_t;
+    if (lm == -INFINITY && some) return far_loss(pT, r.M, r.mT, inv_t);
+    const float lq = some ? lm + logf(r.sT) - logf(r.Z) : -INFINITY;
     return pT * (((aT - r.top) - logf(r.P)) - lq);
 }
 
@@ -200,10 +192,10 @@ __global__ void __launch_bounds__(kDistThreads) distill_loss_kernel(DistillParam
     for (int q = 0; q < kDistWords; ++q) m = f_max_nan(m, u4_max_nan<sizeof(T)>(w[q]));
     m = warp_max_nan(m);   // a NaN or +inf shows in the maximum
     const float s = warp_sum(words_sum<T, kDistWords>(w, m, p.scale));
-    if (lane == 0) s_run[tid >> 5] = make_float2(scaled(m, p.scale), s);
+    if (lane == 0) s_run[tid >> 5] = make_float2(m, s * ref_fix(m, p.scale));
     __syncthreads();
     if (tid < 32) {
-        float2 t = pair_lanes<kDistWarps>(s_run[lane % kDistWarps]);
+        float2 t = pair_lanes<kDistWarps>(s_run[lane % kDistWarps], p.scale);
         if (s_twice) t.x = __uint_as_float(kBadToken);
         if (lane == 0) __stcg(&p.parts[(long)row * p.pieces + piece], t);
     }
@@ -234,12 +226,12 @@ __device__ __forceinline__ void distill_finish(const DistillParams& p, int row, 
     for (int i = tid; i < p.pieces; i += kDistThreads) {
         const float2 v = __ldcg(&p.parts[(long)row * p.pieces + i]);
         if (__float_as_uint(v.x) == kBadToken) flag |= 1;
-        t = pair_merge(t, v);
+        t = pair_merge(t, v, p.scale);
     }
     if (!(a * p.inv_t < INFINITY) || !(aT < INFINITY) || !(fabsf(wt) < INFINITY)) flag |= 2;
     if (tid == 0) s_flag = 0;
-    t = pair_lanes<32>(t);
-    const float2 n = pair_entries<T>(z, p.scale);
+    t = pair_lanes<32>(t, p.scale);
+    const float2 n = pair_entries(z, p.scale);
     const float2 y = teacher_lanes<32>(make_float2(a * p.inv_t, 1.0f));
     if (lane == 0) {
         s_tail[warp] = t;
@@ -249,13 +241,13 @@ __device__ __forceinline__ void distill_finish(const DistillParams& p, int row, 
     __syncthreads();
     if (flag) atomicOr(&s_flag, flag);
     // every warp puts the whole together
-    const float2 T2 = pair_lanes<kDistWarps>(s_tail[lane % kDistWarps]);
-    const float2 N2 = pair_lanes<kDistWarps>(s_top[lane % kDistWarps]);
-    const RowEnds r = row_ends(T2, N2, teacher_lanes<kDistWarps>(s_teach[lane % kDistWarps]), aT);
+    const float2 T2 = pair_lanes<kDistWarps>(s_tail[lane % kDistWarps], p.scale);
+    const float2 N2 = pair_lanes<kDistWarps>(s_top[lane % kDistWarps], p.scale);
+    const RowEnds r = row_ends(T2, N2, teacher_lanes<kDistWarps>(s_teach[lane % kDistWarps]), aT, p.scale);
     float l = 0.0f;
     if (r.top > -INFINITY) {
-        if (there) l = entry_loss<T>(r, a, z, p.scale, p.inv_t);
-        if (tid == 0) l += rest_loss(r, aT);
+        if (there) l = entry_loss(r, a, z, p.inv_t);
+        if (tid == 0) l += rest_loss(r, aT, p.inv_t);
     }
     l = warp_sum(l);
     if (lane == 0) s_loss[warp] = l;
@@ -265,7 +257,7 @@ __device__ __forceinline__ void distill_finish(const DistillParams& p, int row, 
         l = s_loss[0];
         for (int i = 1; i < kDistWarps; ++i) l += s_loss[i];
         p.loss_out[row] = bad ? NAN : l;
-        if (p.lse_out) p.lse_out[row] = bad ? NAN : pair_log<T>(r.M, r.Z, p.inv_t);
+        if (p.lse_out) p.lse_out[row] = bad ? NAN : ref_log(r.M, r.Z, p.inv_t);
         if (s_flag & 1) atomicOr(p.status, SPEC_DEV_TOKEN);
         if ((s_flag & 2) || (bad && !(s_flag & 1))) atomicOr(p.status, SPEC_DEV_NONFINITE);
     }
@@ -347,7 +339,7 @@ __device__ __forceinline__ void named_sync() { asm volatile("bar.sync %0, %1;" :
 
 // What is known of a row once its slices' statistics are together.
 struct FuseRow : RowEnds {
-    float ref;        // unnamed entries: gradient 2^(z c - ref) factor
+    float ref;        // R(mT).  Unnamed entries: gradient 2^(z c - ref) factor, beyond kRefNear 2^((z - mT) c) factor
     float factor;
     float wt, aT;     // the row's weight, the teacher's rest
     int skip, bad;
@@ -447,12 +439,12 @@ __global__ void __launch_bounds__(kFuseThreads, kFuseOcc) distill_fused_kernel(D
                         // a thread's own running maximum; a batch of -inf adds nothing
                         bm = f_max_nan(bm, m);
                         if (bm != m) {
-                            s = m == -INFINITY ? 0.0f : s * ex2(scaled(m, c) - scaled(bm, c));
+                            s = m == -INFINITY ? 0.0f : s * ex2(ref_step(m, bm, c));
                             m = bm;
                         }
                         s += words_sum<T, kFuseBatch>(w, m, c);
                     }
-                    const float2 t = pair_lanes<32>(make_float2(scaled(m, c), s));
+                    const float2 t = pair_lanes<32>(make_float2(m, s * ref_fix(m, c)), c);
                     if (lane == 0) s_tail[i & 1][warp] = t;
                 }
                 __syncwarp();
@@ -466,7 +458,7 @@ __global__ void __launch_bounds__(kFuseThreads, kFuseOcc) distill_fused_kernel(D
                 const float x = row.ref;
                 if (row.skip) {
                     for (int l = tid; l < n; l += kFuseDense) slot[l] = make_uint4(0u, 0u, 0u, 0u);
-                } else if (x > kLow) {
+                } else if (ref_near(x)) {
                     const f2x mm = f2_pack(-x, -x), ff = f2_pack(row.factor, row.factor);
 #pragma unroll 4
                     for (int l = tid; l < n; l += kFuseDense) {
@@ -481,12 +473,12 @@ __global__ void __launch_bounds__(kFuseThreads, kFuseOcc) distill_fused_kernel(D
                         }
                         slot[l] = word_of<T>(d);
                     }
-                } else {   // unnamed entries at the type's lowest value
+                } else {   // the unnamed entries are far from zero
                     for (int l = tid; l < n; l += kFuseDense) {
                         const uint4 w = slot[l];
                         float d[E];
 #pragma unroll
-                        for (int k = 0; k < E; ++k) d[k] = ex2(rel<T>(word_entry<T>(w, k), x, c)) * row.factor;
+                        for (int k = 0; k < E; ++k) d[k] = ex2((word_entry<T>(w, k) - row.mT) * c) * row.factor;
                         slot[l] = word_of<T>(d);
                     }
                 }
@@ -553,7 +545,7 @@ __global__ void __launch_bounds__(kFuseThreads, kFuseOcc) distill_fused_kernel(D
             if (cur.wt != 0.0f) {
                 const float a = known_id(cur) ? cur.a * p.inv_t : -INFINITY;
                 const float2 t = teacher_lanes<32>(make_float2(a, 1.0f));
-                const float2 z = pair_entries<T>(rank == 0 ? cur.z : -INFINITY, c);
+                const float2 z = pair_entries(rank == 0 ? cur.z : -INFINITY, c);
                 if (lane == 0) {
                     s_teach[par][warp] = t;
                     s_top[par][warp] = z;
@@ -583,7 +575,7 @@ __global__ void __launch_bounds__(kFuseThreads, kFuseOcc) distill_fused_kernel(D
             float d = 0.0f;
             if (!r.skip && e.at >= 0) {
                 const float pk = taught ? __expf(fmaf(e.a, p.inv_t, -r.top)) / r.P : 0.0f;
-                d = r.bad ? NAN : (taught ? (ex2(rel<T>(e.z, r.M, c)) / r.Z - pk) * (r.wt * p.inv_t) : 0.0f);
+                d = r.bad ? NAN : (taught ? (ex2(ref_rel(e.z, r.M, c)) / r.Z - pk) * (r.wt * p.inv_t) : 0.0f);
             }
             wait(&s_dense[i % SLOTS], i / SLOTS);
             if (e.at >= 0 && !r.skip) {
@@ -596,8 +588,8 @@ __global__ void __launch_bounds__(kFuseThreads, kFuseOcc) distill_fused_kernel(D
             if (rank != 0) continue;
             float l = 0.0f;   // the loss, behind what the slice waits for
             if (!r.skip && taught) {
-                if (named) l = entry_loss<T>(r, e.a, e.z, c, p.inv_t);
-                if (k == 0) l += rest_loss(r, r.aT);
+                if (named) l = entry_loss(r, e.a, e.z, p.inv_t);
+                if (k == 0) l += rest_loss(r, r.aT, p.inv_t);
             }
             l = warp_sum(l);
             if (lane == 0) s_loss[par][warp] = l;
@@ -606,7 +598,7 @@ __global__ void __launch_bounds__(kFuseThreads, kFuseOcc) distill_fused_kernel(D
                 l = s_loss[par][0];
                 for (int q = 1; q < kNamedWarps; ++q) l += s_loss[par][q];
                 p.loss_out[row] = r.skip ? 0.0f : (r.bad ? NAN : l);
-                if (p.lse_out) p.lse_out[row] = r.skip ? 0.0f : (r.bad ? NAN : pair_log<T>(r.M, r.Z, p.inv_t));
+                if (p.lse_out) p.lse_out[row] = r.skip ? 0.0f : (r.bad ? NAN : ref_log(r.M, r.Z, p.inv_t));
             }
         }
     } else if (tid < kFuseDense + 2 * kFuseNamed + 32) {
@@ -621,14 +613,14 @@ __global__ void __launch_bounds__(kFuseThreads, kFuseOcc) distill_fused_kernel(D
             const bool skip = wt == 0.0f;
             // the teacher's named entries, the student's (slice 0 has them)
             const float2 tn = teacher_lanes<4>(skip ? none : s_teach[par][lane & 3]);
-            const float2 nn = pair_lanes<4>(skip ? none : s_top[par][lane & 3]);
+            const float2 nn = pair_lanes<4>(skip ? none : s_top[par][lane & 3], c);
             static_assert(kNamedWarps == 4 && kDenseWarps <= 16, "the lanes' layout");
             const int flag = s_flag[par];
             float2 T2 = none, N2 = none;
             bool token = false, late = false;
             wait(&s_reduced[par], i >> 1);
             if (!skip && p.group_size == 1) {   // nobody to exchange with
-                T2 = pair_lanes<16>((lane & 15) < kDenseWarps ? s_tail[par][lane & 15] : none);
+                T2 = pair_lanes<16>((lane & 15) < kDenseWarps ? s_tail[par][lane & 15] : none, c);
                 if (flag || dead) T2.x = NAN;
                 N2 = nn;
                 token = flag & 1;
@@ -637,7 +629,7 @@ __global__ void __launch_bounds__(kFuseThreads, kFuseOcc) distill_fused_kernel(D
                 unsigned long long* rec = recs + (size_t)(live % kFuseRing) * p.group_size * kFuseRecord;
                 const unsigned tag = epoch + 1u + live;
                 ++live;
-                float2 t = pair_lanes<16>((lane & 15) < kDenseWarps ? s_tail[par][lane & 15] : none);
+                float2 t = pair_lanes<16>((lane & 15) < kDenseWarps ? s_tail[par][lane & 15] : none, c);
                 if (flag || dead) t.x = flag & 1 ? __uint_as_float(kBadToken) : NAN;
                 if (lane < (rank == 0 ? 4 : 2))
                     post_word(rec + (size_t)rank * kFuseRecord + lane, lane == 0 ? t.x : (lane == 1 ? t.y : (lane == 2 ? nn.x : nn.y)), tag);
@@ -661,22 +653,22 @@ __global__ void __launch_bounds__(kFuseThreads, kFuseOcc) distill_fused_kernel(D
                         }
                     }
                     token |= (uint32_t)v[0] == kBadToken;
-                    T2 = pair_merge(T2, make_float2(__uint_as_float((uint32_t)v[0]), __uint_as_float((uint32_t)v[1])));
+                    T2 = pair_merge(T2, make_float2(__uint_as_float((uint32_t)v[0]), __uint_as_float((uint32_t)v[1])), c);
                     if (r == 0) N2 = make_float2(__uint_as_float((uint32_t)v[2]), __uint_as_float((uint32_t)v[3]));
                 }
                 late = __any_sync(0xffffffffu, late);
                 token = __any_sync(0xffffffffu, token);
                 if (late) dead = true;
-                T2 = pair_lanes<32>(T2);
+                T2 = pair_lanes<32>(T2, c);
                 N2.x = __shfl_sync(0xffffffffu, N2.x, 0);
                 N2.y = __shfl_sync(0xffffffffu, N2.y, 0);
             }
             if (lane == 0) {
                 FuseRow r;
-                static_cast<RowEnds&>(r) = row_ends(T2, N2, skip ? none : tn, skip ? -INFINITY : aT);
+                static_cast<RowEnds&>(r) = row_ends(T2, N2, skip ? none : tn, skip ? -INFINITY : aT, c);
                 const bool bad = !skip && (late || !(r.M < INFINITY) || r.M == -INFINITY);
-                r.ref = r.mT > -INFINITY ? r.mT : 0.0f;
-                r.factor = r.top > -INFINITY ? wt * p.inv_t * __fdividef(r.G, r.Z * r.P) : 0.0f;
+                r.ref = r.mT > -INFINITY ? r.mT * c : 0.0f;
+                r.factor = r.top > -INFINITY ? wt * p.inv_t * __fdividef(r.G, r.Z * r.P) * ref_fix(r.mT, c) : 0.0f;
                 if (bad) r.factor = NAN;
                 r.skip = skip;
                 r.bad = bad;

@@ -160,27 +160,31 @@ struct SegWords {
     }
 };
 
-// Weights relative to a reference m, in base 2: entry x of a row scaled by c = log2(e) / t weighs
-// 2^(x c - R(m)).  While |m c| is at most kRefNear, R(m) is m c rounded once, x c is exact inside
-// an FFMA (ref_rel), and sums that belong to different references are brought together by the
-// difference of the same rounded m c (ref_diff), so that rounding cancels: it moves all weights
-// by one factor, at most 2^4.  Beyond (rows masked with -1e10, -1e30 or the type's lowest value,
-// large logits over a small temperature) that factor would leave float32's range, and m c itself
-// can overflow.  There R(m) is m c exactly: differences are taken before the scaling.
-constexpr float kRefNear = 67108864.0f;   // 2^26: its products are rounded by 4 at most
+// Weights relative to a reference m, in base 2: entry x of a row weighs 2^((x - m) c), c = log2(e) / t,
+// and sums that belong to different references are brought together by the same expression
+// (ref_rel).  The streaming loops form 2^(x c - R(m)) instead, with R(m) = m c rounded once and x c
+// exact inside an FFMA; what the rounding has moved all of a sum's weights by, 2^4 at most while
+// |m c| <= kRefNear, is taken back once per sum (ref_fix).  Beyond (rows masked with -1e10, -1e30 or
+// the type's lowest value, large logits over a small temperature) it would leave float32's range,
+// and m c itself can overflow: there the loops take the difference first as well, out of line.
+constexpr float kRefNear = 67108864.0f;   // 2^26
 __device__ __forceinline__ bool ref_near(float y) { return fabsf(y) <= kRefNear; }
-__device__ __forceinline__ float ref_diff(float a, float b, float c) {   // R(a) - R(b), b >= a, b > -inf
+__device__ __forceinline__ float ref_rel(float x, float m, float c) { return (x - m) * c; }   // log2 weight of x, m > -inf
+__device__ __forceinline__ float ref_fix(float m, float c) {   // takes words_sum's R(m) to m
+    const float y = m * c;
+    return ref_near(y) ? ex2(-fmaf(m, c, -y)) : 1.0f;
+}
+// ln of a sum relative to m
+__device__ __forceinline__ float ref_log(float m, float s, float inv_t) { return fmaf(m, inv_t, logf(s)); }
+// log2 of what a sum of words_sum's relative to a is worth relative to b >= a > -inf
+static __device__ __noinline__ float ref_step_far(float a, float b, float c) {
     const float x = a * c, y = b * c;
-    if (ref_near(y)) return ref_near(x) ? x - y : fmaf(a, c, -y);
+    if (ref_near(y)) return fmaf(a, c, -y);
     return ref_near(x) ? -fmaf(b, c, -x) : (a - b) * c;
 }
-__device__ __forceinline__ float ref_rel(float x, float m, float c) {    // log2 weight of entry x relative to m >= x
-    const float y = m * c;
-    return ref_near(y) ? fmaf(x, c, -y) : (x - m) * c;
-}
-__device__ __forceinline__ float ref_log(float m, float s, float c, float inv_t) {   // ln of s 2^R(m)
-    const float x = m * c;
-    return ref_near(x) ? (x + log2f(s)) * 0.69314718055994531f : fmaf(m, inv_t, logf(s));
+__device__ __forceinline__ float ref_step(float a, float b, float c) {
+    const float x = a * c, y = b * c;
+    return ref_near(x) && ref_near(y) ? x - y : ref_step_far(a, b, c);
 }
 // A word's weights relative to a reference beyond kRefNear: out of line, since hardly any row has
 // one and the streaming loops are short without it.
@@ -190,7 +194,7 @@ __device__ __noinline__ float word_sum_far(uint4 w, float m, float c) {
     for (int k = 0; k < 16 / (int)sizeof(T); ++k) s += ex2((word_pick<T>(w, k) - m) * c);
     return s;
 }
-// The sum of the weights of N words relative to m (0 for m = -inf).
+// The sum of the weights of N words relative to m, R(m) within kRefNear (0 for m = -inf).
 template <typename T, int N>
 __device__ __forceinline__ float words_sum(const uint4 (&w)[N], float m, float c) {
     const float x = m * c;

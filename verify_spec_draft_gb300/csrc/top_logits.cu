@@ -123,14 +123,14 @@ __global__ void __launch_bounds__(kTopThreads) top_kernel(TopLogitsParams p) {
         float mx = m[0];
 #pragma unroll
         for (int q = 1; q < kTopBatch; ++q) mx = mine == q ? m[q] : mx;
-        if ((lane & 3) == 0 && mine < p.batch && blk0 + mine < p.n_blocks) __stcg(&out[blk0 + mine], make_float2(mx, sum));
+        if ((lane & 3) == 0 && mine < p.batch && blk0 + mine < p.n_blocks) __stcg(&out[blk0 + mine], make_float2(mx, sum * ref_fix(mx, p.scale)));
     } else {
 #pragma unroll
         for (int q = 0; q < kTopBatch; ++q) {
             s[q] += __shfl_xor_sync(0xffffffffu, s[q], 1);
             s[q] += __shfl_xor_sync(0xffffffffu, s[q], 2);
             const int b = (blk0 + q) * 8 + (lane >> 2);
-            if ((lane & 3) == 0 && q < p.batch && b < p.n_blocks) __stcg(&out[b], make_float2(m[q], s[q]));
+            if ((lane & 3) == 0 && q < p.batch && b < p.n_blocks) __stcg(&out[b], make_float2(m[q], s[q] * ref_fix(m[q], p.scale)));
         }
     }
     if (p.pick_apart) {
@@ -258,7 +258,7 @@ struct Run {
     float m = -INFINITY, s = 0.0f;
     __device__ __forceinline__ void raise(float x, float c) {
         if (!(x > m)) return;
-        s = m == -INFINITY ? 0.0f : s * ex2(ref_diff(m, x, c));
+        s = m == -INFINITY ? 0.0f : s * ex2(ref_rel(m, x, c));
         m = x;
     }
     __device__ __forceinline__ void entry(float x, float c) {   // one entry
@@ -269,32 +269,32 @@ struct Run {
     __device__ __forceinline__ void sum(float x, float w, float c) {   // a sum relative to x
         if (x == -INFINITY) return;
         raise(x, c);
-        s += w * ex2(ref_diff(x, m, c));
+        s += w * ex2(ref_rel(x, m, c));
     }
     template <typename T, int N>
     __device__ __forceinline__ void words(const uint4 (&w)[N], float mx, float c) {   // their maximum is mx
         raise(mx, c);
-        s += words_sum<T, N>(w, m, c);
+        s += words_sum<T, N>(w, m, c) * ref_fix(m, c);
     }
 };
 // The CTA's totals of two runs, in the first warp.
 __device__ __forceinline__ void runs_cta(Run& x, Run& y, float c, float4* s_run) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const float mx = warp_max(x.m), my = warp_max(y.m);
-    const float sx = warp_sum(x.m == -INFINITY ? 0.0f : x.s * ex2(ref_diff(x.m, mx, c)));
-    const float sy = warp_sum(y.m == -INFINITY ? 0.0f : y.s * ex2(ref_diff(y.m, my, c)));
+    const float sx = warp_sum(x.m == -INFINITY ? 0.0f : x.s * ex2(ref_rel(x.m, mx, c)));
+    const float sy = warp_sum(y.m == -INFINITY ? 0.0f : y.s * ex2(ref_rel(y.m, my, c)));
     if (lane == 0) s_run[warp] = make_float4(mx, sx, my, sy);
     __syncthreads();
     if (warp != 0) return;
     const float4 v = lane < kTopWarps ? s_run[lane] : make_float4(-INFINITY, 0.0f, -INFINITY, 0.0f);
     x.m = warp_max(v.x);
     y.m = warp_max(v.z);
-    x.s = warp_sum(v.x == -INFINITY ? 0.0f : v.y * ex2(ref_diff(v.x, x.m, c)));
-    y.s = warp_sum(v.z == -INFINITY ? 0.0f : v.w * ex2(ref_diff(v.z, y.m, c)));
+    x.s = warp_sum(v.x == -INFINITY ? 0.0f : v.y * ex2(ref_rel(v.x, x.m, c)));
+    y.s = warp_sum(v.z == -INFINITY ? 0.0f : v.w * ex2(ref_rel(v.z, y.m, c)));
 }
 // ln of the sum
-__device__ __forceinline__ float run_log(const Run& r, float c, float inv_t) {
-    return r.s > 0.0f ? ref_log(r.m, r.s, c, inv_t) : -INFINITY;
+__device__ __forceinline__ float run_log(const Run& r, float inv_t) {
+    return r.s > 0.0f ? ref_log(r.m, r.s, inv_t) : -INFINITY;
 }
 
 // The indices of keys[0..n) at or above `t` in list[], in an order that depends on them alone.
@@ -484,7 +484,7 @@ __device__ __forceinline__ void top_pick(const TopLogitsParams& p, int row, uint
             others.m = order_float(most);
             for (int i = tid; i < p.n_blocks; i += kTopThreads) {
                 const uint32_t key = s_keys[i];
-                if (key && key < lo) others.s += s_sums[i] * ex2(ref_diff(order_float(key), others.m, p.scale));
+                if (key && key < lo) others.s += s_sums[i] * ex2(ref_rel(order_float(key), others.m, p.scale));
             }
         }
     }
@@ -636,9 +636,9 @@ __device__ __forceinline__ void top_pick(const TopLogitsParams& p, int row, uint
     rest.sum(others.m, others.s, p.scale);
     runs_cta(rest, taken, p.scale, s_run);
     if (tid == 0) {
-        p.tail_out[row] = run_log(rest, p.scale, p.inv_t);
+        p.tail_out[row] = run_log(rest, p.inv_t);
         taken.sum(rest.m, rest.s, p.scale);
-        if (p.lse_out) p.lse_out[row] = run_log(taken, p.scale, p.inv_t);
+        if (p.lse_out) p.lse_out[row] = run_log(taken, p.inv_t);
         if (!(taken.s > 0.0f)) atomicOr(p.status, SPEC_DEV_NONFINITE);   // no finite entry
     }
 }
