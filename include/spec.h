@@ -664,7 +664,7 @@ spec_status spec_top_logits(const void *logits, spec_dtype dtype, int rows, int 
  *   weight      float32 [rows], nullable (1).  A row of weight 0 is not read: its loss, lse
  *               and gradient are 0.
  *   loss_out    float32 [rows], not weighted; lse_out float32 [rows] (nullable):
- *               ln sum exp(z_v / t).
+ *               ln sum exp(z_v / t) (-inf or +inf where it lies beyond float32's range).
  *   grad_out    the student's layout and type; NULL for the loss alone; may be student
  *               itself, which it then replaces.
  *   workspace   spec_workspace_bytes(SPEC_OP_DISTILL, rows, K, V, 0).

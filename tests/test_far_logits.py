@@ -86,18 +86,19 @@ def test_top_border(spec, V, K, t):
 
 
 # ---------------------------------------------------------------------------------
-def check_distill(z, values, ids, tail, t, out):
+def check_distill(z, values, ids, tail, t, out, largest=None):
     """A probability is off by E = 2 EPS + the teacher's 2^-24 (4 max|a / t| + 100), relative; a loss, sum
     p (ln p - ln q), by 2 E (1 + sum p |ln p - ln q|), a gradient by 2 E / t of the terms it is made of,
     and by the rounding to its type.  Loss and gradient do not depend on what is added to a row, so
     the row's maximum is taken off first, and q_v / q_T is formed against the rest's own maximum: next to
-    1e30 float64 has no room for a ln n."""
+    1e30 float64 has no room for a ln n.  `largest`: the teacher's |a / t| that
+    counts, where only differences do."""
     z, values, ids = f64(z), f64(values), ids.cpu().numpy()
     check_log(f64(out["lse"]), np.array([ot.lse(row / t) for row in z]))
     z = z - z.max(1, keepdims=True)
     with np.errstate(all="ignore"):   # (the oracle's own q_v / q_T, which is not used)
         ref = ot.distill(z, values, ids, None if tail is None else f64(tail), None, t)
-    a = np.abs(values[ids >= 0]).max() / t
+    a = np.abs(values[ids >= 0]).max() / t if largest is None else largest
     if tail is not None:
         a = max(a, np.abs(f64(tail)).max())
     e = 2 * EPS + 2.0 ** -24 * (4 * a + 100)
@@ -190,4 +191,54 @@ def test_processed_rows_are_learned_from(spec):
     values = torch.randn(ids.shape, generator=torch.Generator().manual_seed(2)).cuda()
     out = vsd.distill(y, values, ids, grad=True)
     check_distill(y, values, ids, None, 1.0, out)
+    assert vsd.device_status(out["ws"]) == 0
+
+
+# ---------------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("R,V,K", [(3, 9000, 12), (170, 1100, 20), (2, 50, 50)])
+def test_teacher_far_from_zero(spec, dtype, R, V, K):
+    """A teacher without a rest is renormalised, so only the differences of its values count: they
+    are exact, and the probabilities off by EPS, whatever is added to them."""
+    g = torch.Generator().manual_seed(V)
+    z = (torch.randn((R, V), generator=g) * 3).to(dtype).cuda()
+    ids = named_in(z, "whole", K, seed=K)
+    steps = torch.randint(0, 9, (R, K), generator=g)
+    for at, ulp in ((3e5, 0.25), (-1e7, 1.0), (-1e10, 0.0), (-1e30, 0.0), (LOW, 0.0), (3e38, 0.0), (-3e38, 2.0 ** 104)):
+        for t in (1.0, 0.3, 3.0):
+            values = (at - ulp * steps if at > LOW else torch.full((R, K), at)).float()
+            values[:, 0] = at
+            values[R - 1, 1:] = -torch.inf                 # one entry has all of it
+            ref = torch.where(values > -torch.inf, values - values.max(1, keepdim=True).values, values)
+            for grad in (False, True):
+                out = vsd.distill(z, values.cuda(), ids, temperature=t, grad=grad)
+                check_distill(z, ref.clamp(min=-1e6).cuda(), ids, None, t, out, largest=40.0)
+                assert vsd.device_status(out["ws"]) == 0
+
+
+def test_teacher_far_from_zero_with_a_rest(spec):
+    """Whichever of the buckets has the mass, what there is adds up: the gradient's rows sum to 0."""
+    g = torch.Generator().manual_seed(3)
+    z = (torch.randn((4, 3001), generator=g) * 3).cuda()
+    ids = named_in(z, "whole", 12, seed=4)
+    for at in (-1e10, -1e30, LOW, 3e38):
+        for t in (1.0, 0.3, 3.0):
+            values = torch.full((4, 12), at, device="cuda")
+            tail = torch.tensor([min(max(at / t, LOW), -LOW), 0.0, LOW, -LOW], device="cuda")
+            out = vsd.distill(z, values, ids, tail=tail, temperature=t, grad=True)
+            assert vsd.device_status(out["ws"]) == 0
+            assert torch.isfinite(out["grad"]).all() and not torch.isnan(out["loss"]).any()
+            # 3001 entries of at most 1 / t, each off by 2 EPS of itself
+            assert (out["grad"].double().sum(1).abs() <= 4 * EPS / t).all()
+
+
+def test_own_far_teacher(spec):
+    """A masked row and its own top logits, at the type's lowest value over a temperature."""
+    x = far_rows("rest", 4, 5003, LOW, F32, 1.0)
+    x[1] = LOW
+    y = vsd.process_logits(x[None], temperature=torch.tensor([1.3]).cuda())["logits"][0]
+    top = vsd.top_logits(y, 16)
+    out = vsd.distill(y, top["values"], top["ids"], grad=True)
+    ref = (top["values"] - top["values"].max(1, keepdim=True).values).clamp(min=-1e6)
+    check_distill(y, ref, top["ids"], None, 1.0, out, largest=40.0)
     assert vsd.device_status(out["ws"]) == 0

@@ -65,18 +65,15 @@ __device__ __forceinline__ float2 pair_entries(float x, float c) {
     const float m = warp_max_nan(x);
     return make_float2(m, lanes_sum<32>(x == -INFINITY ? 0.0f : ex2(ref_rel(x, m, c))));
 }
-// The teacher's pairs: (maximum, sum of e^(x - maximum)).
-template <int N>
-__device__ __forceinline__ float2 teacher_lanes(float2 v) {
-    const float m = N == 32 ? warp_max_nan(v.x) : lanes_max_nan<N>(v.x);
-    return make_float2(m, lanes_sum<N>(v.x == -INFINITY ? 0.0f : v.y * __expf(v.x - m)));
-}
-
+constexpr float kMaxFloat = 3.402823466e38f;
 constexpr uint32_t kBadToken = 0x7fc0dead;   // a NaN that says: an id is listed twice
 
 // What the rows' ends share.  (M, Z): the student's pair, (mT, sT) that of its unnamed entries;
-// top, e, eT: the teacher's maximum, and the weights of its named entries and of its rest
-// against it, P = e + eT; f the student's named weight against M.
+// amax: the teacher's largest named logit; top: the larger of it over t and the rest's aT; lag: how
+// far amax / t lies below that; e, eT: the weights of the named entries and of the rest against
+// top, P = e + eT; f the student's named weight against M.  Named entries are taken from
+// amax before the scaling, so that their shares do not depend on how far from zero the teacher's
+// logits are; amax / t itself, which only a rest is compared with, stops at the largest float.
 //
 // The share of the rest that the student has too much is
 //     q_T - p_T = f_T / Z - e_T / P = (f_T e - e_T f) / (Z P),    f_T = sT 2^((mT - M) c),
@@ -85,21 +82,28 @@ constexpr uint32_t kBadToken = 0x7fc0dead;   // a NaN that says: an id is listed
 // rest's part of the loss, p_T (ln p_T - ln q_T) = -p_T ln(1 + (q_T - p_T) / p_T), goes by it
 // too, unless the shares are far apart: then the logarithms are taken one by one, for f_T may
 // be too small for a float.
-struct RowEnds { float M, Z, mT, sT, top, e, eT, P, G; };
-__device__ __forceinline__ RowEnds row_ends(float2 T2, float2 N2, float2 teach, float aT, float c) {
+struct RowEnds { float M, Z, mT, sT, amax, top, lag, e, eT, P, G; };
+__device__ __forceinline__ RowEnds row_ends(float2 T2, float2 N2, float2 teach, float aT, float c, float inv_t) {
     RowEnds r;
     const float2 A = pair_merge(T2, N2, c);
     r.M = A.x;
     r.Z = A.y;
     r.mT = T2.x;
     r.sT = T2.y;
-    r.top = f_max_nan(teach.x, aT);
-    r.e = teach.x > -INFINITY ? teach.y * __expf(teach.x - r.top) : 0.0f;
+    r.amax = teach.x;
+    const float a = teach.x > -INFINITY ? fminf(fmaxf(teach.x * inv_t, -kMaxFloat), kMaxFloat) : teach.x;
+    r.top = f_max_nan(a, aT);
+    r.lag = a - r.top;
+    r.e = teach.x > -INFINITY ? teach.y * __expf(r.lag) : 0.0f;
     r.eT = aT > -INFINITY ? __expf(aT - r.top) : 0.0f;
     r.P = r.e + r.eT;
     const float f = pair_weight(N2, A.x, c);
     r.G = T2.x > -INFINITY ? fmaf(ex2(ref_rel(T2.x, A.x, c)), r.e, -__fdividef(r.eT * f, T2.y)) : 0.0f;
     return r;
+}
+// ln of a named entry's weight against top
+__device__ __forceinline__ float entry_log(const RowEnds& r, float a, float inv_t) {
+    return a > -INFINITY ? fmaf(a - r.amax, inv_t, r.lag) : -INFINITY;
 }
 // p (M - x) / t, for a finite x so far below M that the difference overflows over t.  By halves, since
 // M - x may overflow as well; the logarithms of the sums do not show beside it.
@@ -107,7 +111,7 @@ static __device__ __noinline__ float far_loss(float p, float M, float x, float i
     return (2.0f * p * inv_t) * (0.5f * M - 0.5f * x);
 }
 __device__ __forceinline__ float entry_loss(const RowEnds& r, float a, float z, float inv_t) {
-    const float lt = fmaf(a, inv_t, -r.top), pk = __expf(lt) / r.P;
+    const float lt = entry_log(r, a, inv_t), pk = __expf(lt) / r.P;
     if (!(pk > 0.0f)) return 0.0f;
     const float lz = (z - r.M) * inv_t;
     if (lz == -INFINITY && z > -INFINITY) return far_loss(pk, r.M, z, inv_t);
@@ -228,11 +232,11 @@ __device__ __forceinline__ void distill_finish(const DistillParams& p, int row, 
         if (__float_as_uint(v.x) == kBadToken) flag |= 1;
         t = pair_merge(t, v, p.scale);
     }
-    if (!(a * p.inv_t < INFINITY) || !(aT < INFINITY) || !(fabsf(wt) < INFINITY)) flag |= 2;
+    if (!(a < INFINITY) || !(aT < INFINITY) || !(fabsf(wt) < INFINITY)) flag |= 2;
     if (tid == 0) s_flag = 0;
     t = pair_lanes<32>(t, p.scale);
     const float2 n = pair_entries(z, p.scale);
-    const float2 y = teacher_lanes<32>(make_float2(a * p.inv_t, 1.0f));
+    const float2 y = pair_entries(a, p.scale);
     if (lane == 0) {
         s_tail[warp] = t;
         s_top[warp] = n;
@@ -243,7 +247,7 @@ __device__ __forceinline__ void distill_finish(const DistillParams& p, int row, 
     // every warp puts the whole together
     const float2 T2 = pair_lanes<kDistWarps>(s_tail[lane % kDistWarps], p.scale);
     const float2 N2 = pair_lanes<kDistWarps>(s_top[lane % kDistWarps], p.scale);
-    const RowEnds r = row_ends(T2, N2, teacher_lanes<kDistWarps>(s_teach[lane % kDistWarps]), aT, p.scale);
+    const RowEnds r = row_ends(T2, N2, pair_lanes<kDistWarps>(s_teach[lane % kDistWarps], p.scale), aT, p.scale, p.inv_t);
     float l = 0.0f;
     if (r.top > -INFINITY) {
         if (there) l = entry_loss(r, a, z, p.inv_t);
@@ -543,8 +547,8 @@ __global__ void __launch_bounds__(kFuseThreads, kFuseOcc) distill_fused_kernel(D
             mbar_arrive1(&s_ready[par]);
             s_entry[i % SLOTS][k] = {cur.z, cur.a, cur.id, at};
             if (cur.wt != 0.0f) {
-                const float a = known_id(cur) ? cur.a * p.inv_t : -INFINITY;
-                const float2 t = teacher_lanes<32>(make_float2(a, 1.0f));
+                const float a = known_id(cur) ? cur.a : -INFINITY;
+                const float2 t = pair_entries(a, c);
                 const float2 z = pair_entries(rank == 0 ? cur.z : -INFINITY, c);
                 if (lane == 0) {
                     s_teach[par][warp] = t;
@@ -574,7 +578,7 @@ __global__ void __launch_bounds__(kFuseThreads, kFuseOcc) distill_fused_kernel(D
             const bool taught = r.top > -INFINITY, named = e.id >= 0 && e.id < p.V;
             float d = 0.0f;
             if (!r.skip && e.at >= 0) {
-                const float pk = taught ? __expf(fmaf(e.a, p.inv_t, -r.top)) / r.P : 0.0f;
+                const float pk = taught ? __expf(entry_log(r, e.a, p.inv_t)) / r.P : 0.0f;
                 d = r.bad ? NAN : (taught ? (ex2(ref_rel(e.z, r.M, c)) / r.Z - pk) * (r.wt * p.inv_t) : 0.0f);
             }
             wait(&s_dense[i % SLOTS], i / SLOTS);
@@ -612,7 +616,7 @@ __global__ void __launch_bounds__(kFuseThreads, kFuseOcc) distill_fused_kernel(D
             const float wt = s_wt[par], aT = s_aT[par];
             const bool skip = wt == 0.0f;
             // the teacher's named entries, the student's (slice 0 has them)
-            const float2 tn = teacher_lanes<4>(skip ? none : s_teach[par][lane & 3]);
+            const float2 tn = pair_lanes<4>(skip ? none : s_teach[par][lane & 3], c);
             const float2 nn = pair_lanes<4>(skip ? none : s_top[par][lane & 3], c);
             static_assert(kNamedWarps == 4 && kDenseWarps <= 16, "the lanes' layout");
             const int flag = s_flag[par];
@@ -665,7 +669,7 @@ __global__ void __launch_bounds__(kFuseThreads, kFuseOcc) distill_fused_kernel(D
             }
             if (lane == 0) {
                 FuseRow r;
-                static_cast<RowEnds&>(r) = row_ends(T2, N2, skip ? none : tn, skip ? -INFINITY : aT, c);
+                static_cast<RowEnds&>(r) = row_ends(T2, N2, skip ? none : tn, skip ? -INFINITY : aT, c, p.inv_t);
                 const bool bad = !skip && (late || !(r.M < INFINITY) || r.M == -INFINITY);
                 r.ref = r.mT > -INFINITY ? r.mT * c : 0.0f;
                 r.factor = r.top > -INFINITY ? wt * p.inv_t * __fdividef(r.G, r.Z * r.P) * ref_fix(r.mT, c) : 0.0f;
