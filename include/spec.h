@@ -636,7 +636,8 @@ spec_status spec_process_logits(const void *logits, spec_dtype dtype, int B, int
  * A row that holds NaN or +inf gets ids -1 and NaN in the other outputs, a row with no
  * finite entry ids -1 and -inf (flag NONFINITE for both).
  * Limits: 1 <= rows <= SPEC_MAX_TEACHER_ROWS, 1 <= K <= SPEC_MAX_TEACHER,
- * 1 <= V <= SPEC_MAX_V_TEACHER, V <= ld < 2^31, temperature positive and finite.
+ * 1 <= V <= SPEC_MAX_V_TEACHER, V <= ld < 2^31, temperature positive, finite and not
+ * subnormal.
  */
 spec_status spec_top_logits(const void *logits, spec_dtype dtype, int rows, int V, int ld, int K,
                             float temperature, float *values_out, int32_t *ids_out, float *tail_out,

@@ -1,0 +1,40 @@
+"""Arguments of process_logits, top_logits and distill at and beyond their limits, without a GPU: every
+call here is refused before its first CUDA call."""
+
+import types
+
+import pytest
+
+import verify_spec_draft_gb300 as vsd
+from verify_spec_draft_gb300 import build
+
+A = 0x10000          # a 16-byte aligned fake device address
+INVALID, SHAPE, ALIGN = 1, 2, 4
+TINY = 2.0 ** -126   # the smallest normal float32
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if build.needs_build():
+        build.build()
+    return vsd.load()
+
+
+def top(lib, t=1.0, ws=A, logits=A):
+    return lib.spec_top_logits(logits, vsd.BF16, 4, 100, 100, 8, t, A, A, A, 0, ws, 1 << 24, None)
+
+
+def distill(lib, t=1.0, ws=A, student=A):
+    return lib.spec_distill(student, vsd.BF16, 4, 100, 100, A, vsd.F32, A, 8, 0, 0, t, A, 0, A, ws, 1 << 24, None)
+
+
+def process(lib, ws=A, logits=A):
+    return lib.spec_process_logits(logits, vsd.BF16, 2, 4, 100, 100, A, 16, A, A, A, A, A, A, A, A, A, 3, A, 4, A, ws,
+                                   1 << 20, None)
+
+
+@pytest.mark.parametrize("call", [top, distill])
+def test_subnormal_temperature(lib, call):
+    """Its reciprocal has no float32."""
+    assert call(lib, t=TINY / 2) == INVALID and call(lib, t=1e-45) == INVALID
+    assert call(lib, t=TINY, ws=0) != INVALID

@@ -242,3 +242,24 @@ def test_own_far_teacher(spec):
     ref = (top["values"] - top["values"].max(1, keepdim=True).values).clamp(min=-1e6)
     check_distill(y, ref, top["ids"], None, 1.0, out, largest=40.0)
     assert vsd.device_status(out["ws"]) == 0
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("t", [2.0 ** -126, 1e-30, 1e-10, 1e10, 1e30, 3e38])
+def test_temperatures(spec, dtype, t):
+    """From the smallest normal number to the largest."""
+    t = float(np.float32(t))
+    g = torch.Generator().manual_seed(6)
+    z = (torch.randn((3, 9001), generator=g) * 3).to(dtype).cuda()
+    out = vsd.top_logits(z, 20, temperature=t)
+    ref = ot.top_logits(f64(z), 20, t)
+    np.testing.assert_array_equal(out["ids"].cpu().numpy(), ref["ids"])
+    for k in ("tail", "lse"):
+        check_log(f64(out[k]), ref[k])
+    ids = named_in(z, "whole", 20, seed=7)
+    values = torch.randn(ids.shape, generator=g).cuda()
+    for grad in (False, True):
+        d = vsd.distill(z, values, ids, temperature=t, grad=grad)
+        check_distill(z, values - values.max(1, keepdim=True).values, ids, None, t, d, largest=40.0)
+        assert vsd.device_status(d["ws"]) == 0
+    assert vsd.device_status(out["ws"]) == 0

@@ -3,6 +3,7 @@
 // Every check that can fail is done here, on the host, before anything is enqueued;
 // conditions only the device can see go to the workspace status word.
 #include <cuda_runtime.h>
+#include <float.h>
 #include <stdint.h>
 #include <string.h>
 
@@ -35,6 +36,8 @@ spec_status record_cuda_error(cudaError_t e) { return cuda_status(e); }
 
 static bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 static bool dtype_ok(int d) { return d == SPEC_F32 || d == SPEC_BF16; }
+// The rows' temperature: 1 / t and log2(e) / t are float32 numbers.
+static bool temperature_ok(float t) { return t >= FLT_MIN && t < INFINITY; }
 static size_t dtype_size(int d) { return d == SPEC_F32 ? 4 : 2; }
 
 }  // namespace spec
@@ -555,7 +558,7 @@ spec_status spec_top_logits(const void* logits, spec_dtype dtype, int rows, int 
     if (rows < 1 || rows > SPEC_MAX_TEACHER_ROWS || K < 1 || K > SPEC_MAX_TEACHER || V < 1 ||
         V > SPEC_MAX_V_TEACHER || ld < V)
         return SPEC_ERR_SHAPE;
-    if (!(temperature > 0.0f && temperature < INFINITY)) return SPEC_ERR_INVALID_ARG;
+    if (!temperature_ok(temperature)) return SPEC_ERR_INVALID_ARG;
     if (!logits || !values_out || !ids_out || !tail_out) return SPEC_ERR_INVALID_ARG;
     if (!aligned16(logits)) return SPEC_ERR_ALIGN;
     if (!workspace || workspace_bytes < top_logits_workspace_bytes(rows, K, V)) return SPEC_ERR_WORKSPACE;
@@ -584,7 +587,7 @@ spec_status spec_distill(const void* student, spec_dtype dtype, int rows, int V,
     if (rows < 1 || rows > SPEC_MAX_TEACHER_ROWS || K < 1 || K > SPEC_MAX_TEACHER || V < 1 ||
         V > SPEC_MAX_V_TEACHER || ld < V)
         return SPEC_ERR_SHAPE;
-    if (!(temperature > 0.0f && temperature < INFINITY)) return SPEC_ERR_INVALID_ARG;
+    if (!temperature_ok(temperature)) return SPEC_ERR_INVALID_ARG;
     if (!student || !values || !ids || !loss_out) return SPEC_ERR_INVALID_ARG;
     if (!aligned16(student) || !aligned16(grad_out)) return SPEC_ERR_ALIGN;
     if (!workspace || workspace_bytes < distill_workspace_bytes(rows, V)) return SPEC_ERR_WORKSPACE;
