@@ -19,7 +19,9 @@
  * Dtypes.   Logits are float32 or bfloat16 (stored as raw 16-bit words); every
  *           reduction accumulates in float32.  Tokens are int32 in [0, V).
  * Align.    Every logits/weights base pointer must be 16-byte aligned (rejected
- *           with SPEC_ERR_ALIGN otherwise).  V need not be a multiple of anything:
+ *           with SPEC_ERR_ALIGN otherwise), and a workspace as cudaMalloc aligns it
+ *           (spec_process_logits, spec_top_logits and spec_distill reject one that is
+ *           not 16-byte aligned).  V need not be a multiple of anything:
  *           rows whose byte length is not a multiple of 16 take a scalar path.
  * Streams.  Calls enqueue work on `stream` (a cudaStream_t; NULL = legacy default
  *           stream) and never synchronise the host.

@@ -38,3 +38,10 @@ def test_subnormal_temperature(lib, call):
     """Its reciprocal has no float32."""
     assert call(lib, t=TINY / 2) == INVALID and call(lib, t=1e-45) == INVALID
     assert call(lib, t=TINY, ws=0) != INVALID
+
+
+@pytest.mark.parametrize("call", [top, distill, process])
+@pytest.mark.parametrize("off", [1, 4, 8])
+def test_workspace_alignment(lib, call, off):
+    """Its records are read and written as 8-byte words."""
+    assert call(lib, ws=A + off) == ALIGN

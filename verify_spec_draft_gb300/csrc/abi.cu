@@ -521,7 +521,7 @@ spec_status spec_process_logits(const void* logits, spec_dtype dtype, int B, int
     if (mask && mask_rows != 1 && mask_rows != R) return SPEC_ERR_SHAPE;
     if (!logits || !out || (Lmax > 0 && !history) || (n_bias > 0 && (!bias_ids || !bias_values)))
         return SPEC_ERR_INVALID_ARG;
-    if (!aligned16(logits) || !aligned16(out)) return SPEC_ERR_ALIGN;
+    if (!aligned16(logits) || !aligned16(out) || !aligned16(workspace)) return SPEC_ERR_ALIGN;
     if (!workspace || workspace_bytes < kWsHeaderBytes) return SPEC_ERR_WORKSPACE;
     ProcessParams p;
     memset(&p, 0, sizeof(p));
@@ -560,7 +560,7 @@ spec_status spec_top_logits(const void* logits, spec_dtype dtype, int rows, int 
         return SPEC_ERR_SHAPE;
     if (!temperature_ok(temperature)) return SPEC_ERR_INVALID_ARG;
     if (!logits || !values_out || !ids_out || !tail_out) return SPEC_ERR_INVALID_ARG;
-    if (!aligned16(logits)) return SPEC_ERR_ALIGN;
+    if (!aligned16(logits) || !aligned16(workspace)) return SPEC_ERR_ALIGN;
     if (!workspace || workspace_bytes < top_logits_workspace_bytes(rows, K, V)) return SPEC_ERR_WORKSPACE;
     TopLogitsParams p;
     memset(&p, 0, sizeof(p));
@@ -589,7 +589,7 @@ spec_status spec_distill(const void* student, spec_dtype dtype, int rows, int V,
         return SPEC_ERR_SHAPE;
     if (!temperature_ok(temperature)) return SPEC_ERR_INVALID_ARG;
     if (!student || !values || !ids || !loss_out) return SPEC_ERR_INVALID_ARG;
-    if (!aligned16(student) || !aligned16(grad_out)) return SPEC_ERR_ALIGN;
+    if (!aligned16(student) || !aligned16(grad_out) || !aligned16(workspace)) return SPEC_ERR_ALIGN;
     if (!workspace || workspace_bytes < distill_workspace_bytes(rows, V)) return SPEC_ERR_WORKSPACE;
     DistillParams p;
     memset(&p, 0, sizeof(p));
