@@ -45,3 +45,38 @@ def test_subnormal_temperature(lib, call):
 def test_workspace_alignment(lib, call, off):
     """Its records are read and written as 8-byte words."""
     assert call(lib, ws=A + off) == ALIGN
+
+
+class _Rows:
+    """Stands in for a bf16 CUDA tensor: all that a call looks at before it allocates."""
+    is_cuda, device = True, types.SimpleNamespace(type="cuda", index=0)
+
+    def __init__(self, shape, strides):
+        self.shape, self._strides = shape, strides
+
+    def dim(self):
+        return len(self.shape)
+
+    def numel(self):
+        n = 1
+        for x in self.shape:
+            n *= x
+        return n
+
+    def stride(self):
+        return self._strides
+
+
+@pytest.mark.parametrize("shape,strides", [
+    ((2, 100), ((1 << 32) + 100, 1)),         # a row stride that is 100 modulo 2^32
+    (((1 << 32) + 4, 100), (100, 1)),         # four rows modulo 2^32
+    ((2, (1 << 32) + 100), ((1 << 32) + 100, 1))])
+def test_sizes_past_32_bits(lib, shape, strides):
+    x = _Rows(shape, strides)
+    with pytest.raises(vsd.SpecError):
+        vsd.top_logits(x, 3)
+    with pytest.raises(vsd.SpecError):
+        vsd.distill(x, x, x)
+    x = _Rows((shape[0], 1, shape[1]), (strides[0], strides[0], 1))
+    with pytest.raises(vsd.SpecError):
+        vsd.process_logits(x)

@@ -177,6 +177,15 @@ def _need_rows(t, name, device=None):
     return ld or V
 
 
+_INT_MAX = 2**31 - 1
+
+
+def _need_ints(what, *sizes):
+    """Sizes that the C interface takes as 32-bit numbers: ctypes would pass them modulo 2^32."""
+    if max(sizes) > _INT_MAX:
+        raise SpecError(2, f"{what}{sizes}")
+
+
 def _addrs(device, names, tensors, dtypes, shapes):
     """The addresses of optional contiguous tensors (None for None), checked as _need does,
     which says what is wrong; one loop, since a call's checks are most of its host time."""
@@ -639,6 +648,7 @@ def process_logits(logits, history=None, lengths=None, prompt_lengths=None, bloc
         if bias_ids.dim() != 2:
             raise ValueError(f"bias_ids must be [{B}, n], got {tuple(bias_ids.shape)}")
         nb = bias_ids.shape[1]
+    _need_ints("process_logits", B, R, V, ld, Lmax, nb)
     W = (V + 31) // 32
     mask_rows, masks = (R, (B, R, W)) if mask is not None and mask.dim() == 3 else (1, (B, W))
     per, biases = (B,), (B, nb)
@@ -676,6 +686,7 @@ def top_logits(logits, k, temperature=1.0, ws=None, out=None, stream=None):
     dev, shape, k = logits.device, logits.shape, int(k)
     lead, V = shape[:-1], shape[-1]
     rows = logits.numel() // V if V else 0
+    _need_ints("top_logits", rows, V, ld, k)
     if out is None:
         with _made_on(stream):
             sized = (*lead, max(k, 0))
@@ -713,6 +724,7 @@ def distill(student, values, ids, tail=None, weight=None, temperature=1.0, grad=
     lead, V = shape[:-1], shape[-1]
     rows = student.numel() // V if V else 0
     K = ids.shape[-1] if ids is not None and ids.dim() else 0
+    _need_ints("distill", rows, V, ld, K)
     if ids is None or values is None:
         raise ValueError("values and ids are required")
     named = (*lead, K)
