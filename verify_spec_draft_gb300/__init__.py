@@ -233,6 +233,8 @@ def _rows_like(t, ld):
 
 
 def _need_same_rows(t, name, like, ld):
+    if t is None:
+        raise ValueError(f"{name} is required")
     if t.dtype is not like.dtype or t.shape != like.shape:
         raise ValueError(f"{name} must be {like.dtype} {tuple(like.shape)}, got {t.dtype} {tuple(t.shape)}")
     if _need_rows(t, name, like.device) != ld and t.numel() > t.shape[-1]:
@@ -662,7 +664,7 @@ def process_logits(logits, history=None, lengths=None, prompt_lengths=None, bloc
         with _made_on(stream):
             out = dict(logits=_rows_like(logits, ld))
     else:
-        _need_same_rows(out["logits"], "out", logits, ld)
+        _need_same_rows(out.get("logits"), "out's logits", logits, ld)
     if ws is None:
         with _made_on(stream):
             ws = workspace(OP_PROCESS_LOGITS, B, R, V, 0, dev, stream)
@@ -740,7 +742,7 @@ def distill(student, values, ids, tail=None, weight=None, temperature=1.0, grad=
     else:
         _need_out(out, dev, loss=(torch.float32, lead), lse=(torch.float32, lead))
         if grad:
-            _need_same_rows(out["grad"], "grad", student, ld)
+            _need_same_rows(out.get("grad"), "grad", student, ld)
     if ws is None:
         with _made_on(stream):
             ws = workspace(OP_DISTILL, rows, K, V, 0, dev, stream)
