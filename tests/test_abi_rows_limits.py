@@ -71,7 +71,8 @@ class _Rows:
     ((2, 100), ((1 << 32) + 100, 1)),         # a row stride that is 100 modulo 2^32
     (((1 << 32) + 4, 100), (100, 1)),         # four rows modulo 2^32
     ((2, (1 << 32) + 100), ((1 << 32) + 100, 1))])
-def test_sizes_past_32_bits(lib, shape, strides):
+def test_sizes_past_32_bits(lib, monkeypatch, shape, strides):
+    monkeypatch.setattr(vsd, "_current_device", lambda: 0, raising=False)
     x = _Rows(shape, strides)
     with pytest.raises(vsd.SpecError):
         vsd.top_logits(x, 3)
@@ -80,3 +81,34 @@ def test_sizes_past_32_bits(lib, shape, strides):
     x = _Rows((shape[0], 1, shape[1]), (strides[0], strides[0], 1))
     with pytest.raises(vsd.SpecError):
         vsd.process_logits(x)
+
+
+def test_rows_on_another_device(lib, monkeypatch):
+    """A call is made under the rows' device, whichever is current, and on its streams only."""
+    torch = pytest.importorskip("torch")
+    here, seen = [3], []
+
+    class under:
+        def __init__(self, device):
+            seen.append(device)
+
+        def __enter__(self):
+            self.was, here[0] = here[0], seen[-1].index
+
+        def __exit__(self, *a):
+            here[0] = self.was
+
+    monkeypatch.setattr(vsd, "_current_device", lambda: here[0])
+    monkeypatch.setattr(torch.cuda, "device", under)
+    x = _Rows(((1 << 32) + 4, 100), (100, 1))          # refused, but not before
+    y = _Rows(((1 << 32) + 4, 1, 100), (100, 100, 1))
+    for call in (lambda **kw: vsd.top_logits(x, 3, **kw), lambda **kw: vsd.distill(x, x, x, **kw),
+                 lambda **kw: vsd.process_logits(y, **kw)):
+        with pytest.raises(vsd.SpecError):
+            call()
+        assert seen.pop() is _Rows.device and not seen and here == [3]
+        with pytest.raises(ValueError):
+            call(stream=types.SimpleNamespace(device="another", cuda_stream=0))
+        with pytest.raises(vsd.SpecError):
+            call(stream=types.SimpleNamespace(device=_Rows.device, cuda_stream=0))
+        assert seen.pop() is _Rows.device

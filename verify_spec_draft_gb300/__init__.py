@@ -177,6 +177,18 @@ def _need_rows(t, name, device=None):
     return ld or V
 
 
+def _current_device():
+    return _torch()._C._cuda_getDevice()
+
+
+def _away(device, stream):
+    """Whether `device`, the rows', is not the one that calls launch on: then the call is made
+    again under it.  A caller's stream has to be one of its."""
+    if stream is not None and stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, the rows on {device}")
+    return _current_device() != device.index
+
+
 _INT_MAX = 2**31 - 1
 
 
@@ -638,6 +650,10 @@ def process_logits(logits, history=None, lengths=None, prompt_lengths=None, bloc
     if logits.dim() != 3:
         raise ValueError("logits must be [B, R, V]")
     dev, i32, f32 = logits.device, torch.int32, torch.float32
+    if _away(dev, stream):
+        with torch.cuda.device(dev):
+            return process_logits(logits, history, lengths, prompt_lengths, block, repetition, frequency, presence,
+                                  bias_ids, bias_values, mask, temperature, ws, out, stream)
     B, R, V = logits.shape
     Lmax = nb = 0
     if history is not None:
@@ -686,6 +702,9 @@ def top_logits(logits, k, temperature=1.0, ws=None, out=None, stream=None):
     lib = _lib or load()
     ld = _need_rows(logits, "logits")
     dev, shape, k = logits.device, logits.shape, int(k)
+    if _away(dev, stream):
+        with torch.cuda.device(dev):
+            return top_logits(logits, k, temperature, ws, out, stream)
     lead, V = shape[:-1], shape[-1]
     rows = logits.numel() // V if V else 0
     _need_ints("top_logits", rows, V, ld, k)
@@ -723,6 +742,9 @@ def distill(student, values, ids, tail=None, weight=None, temperature=1.0, grad=
     lib = _lib or load()
     ld = _need_rows(student, "student")
     dev, shape = student.device, student.shape
+    if _away(dev, stream):
+        with torch.cuda.device(dev):
+            return distill(student, values, ids, tail, weight, temperature, grad, ws, out, stream)
     lead, V = shape[:-1], shape[-1]
     rows = student.numel() // V if V else 0
     K = ids.shape[-1] if ids is not None and ids.dim() else 0
