@@ -645,6 +645,14 @@ __device__ __forceinline__ void top_pick(const TopLogitsParams& p, int row, uint
 
 static size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
+// A row's blocks' keys and sums and, where its ties need them, the chosen blocks' words.
+static size_t top_smem(int n_blocks, int K, int lanes) { return ((size_t)n_blocks * 2 + (size_t)K * lanes) * 4; }
+constexpr int kTopSmemPlain = 28 * 1024;   // what a kernel gets beside its own arrays without being asked for more
+// The most that any call needs, float32 rows of SPEC_MAX_V_TEACHER.  The attribute is always set to
+// this: it belongs to the kernel, and another host thread may set it between a call's own setting and
+// its launch.
+constexpr int kTopSmemMost = 81928;
+
 size_t top_logits_workspace_bytes(int rows, int K, int V) {
     const int f32 = top_lanes(V, 4, K), bf16 = top_lanes(V, 2, K);
     const int a = top_blocks(V, 4, f32), b = top_blocks(V, 2, bf16);
@@ -665,10 +673,11 @@ static cudaError_t top_launch_lanes(TopLogitsParams p, cudaStream_t stream) {
     const bool aligned = SegWords<T, true>::fits(p.ld, p.V);
     const void* scan = aligned ? (const void*)top_kernel<T, true, LANES> : (const void*)top_kernel<T, false, LANES>;
     const auto pick = aligned ? top_pick_kernel<T, true, LANES> : top_pick_kernel<T, false, LANES>;
-    const size_t smem = ((size_t)p.n_blocks * 2 + (size_t)p.K * LANES) * 4;
+    const size_t smem = top_smem(p.n_blocks, p.K, LANES);
+    if (smem > kTopSmemMost) return cudaErrorInvalidConfiguration;
     p.pick_apart = p.rows >= kTopApart;
-    if (smem > 28 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(p.pick_apart ? (const void*)pick : scan, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (smem > kTopSmemPlain) {
+        const cudaError_t e = cudaFuncSetAttribute(p.pick_apart ? (const void*)pick : scan, cudaFuncAttributeMaxDynamicSharedMemorySize, kTopSmemMost);
         if (e != cudaSuccess) return e;
     }
     void* args[] = {&p};
