@@ -28,11 +28,6 @@ __host__ __device__ inline int distill_pieces(int V, int elt_bytes) {
     return ((V + 2 * E - 2) / E + kDistPiece - 1) / kDistPiece;
 }
 
-__device__ __forceinline__ float warp_max_nan(float x) {
-    float r;
-    asm volatile("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
-    return r;
-}
 // Pairs (m, s): the maximum of some entries and the sum of their weights relative to it
 // (row_words.cuh); empty: (-inf, 0).  NaN shows in m.
 __device__ __forceinline__ float pair_weight(float2 v, float m, float c) {   // v's sum relative to m >= v.x
@@ -766,8 +761,6 @@ static cudaError_t fused_launch(DistillParams p, cudaStream_t stream) {
     return cudaLaunchCooperativeKernel(kern, dim3(groups * size), dim3(kFuseThreads), args, (size_t)slots * p.slice * 16,
                                        stream);
 }
-
-static size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
 constexpr size_t kFuseBytes = sizeof(FuseHeader) + sizeof(unsigned long long) * kFuseMaxCtas * kFuseRing * kFuseRecord;
 

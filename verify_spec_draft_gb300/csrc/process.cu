@@ -38,8 +38,8 @@ constexpr uint32_t kSlotMask = 0x7ffu, kInPrompt = 0x80000000u;
 // (each with eight words of room before it, kProcRoom), and for the block's tokens the
 // token, its count and its bias.
 constexpr int kProcRoom = 8;
-__host__ __device__ inline int process_words(int seg) { return seg + 2 * (seg / 32) + 4 * kProcRoom; }
-__host__ __device__ inline size_t process_smem(int seg) {
+__host__ __device__ constexpr int process_words(int seg) { return seg + 2 * (seg / 32) + 4 * kProcRoom; }
+__host__ __device__ constexpr size_t process_smem(int seg) {
     return ((size_t)process_words(seg) + 3 * SPEC_MAX_GAMMA) * sizeof(uint32_t);
 }
 
@@ -289,6 +289,7 @@ static long process_cost(const ProcessParams& p, int E, long slots, int r, long 
 cudaError_t process_launch(ProcessParams p, cudaStream_t stream) {
     const int E = p.dtype == SPEC_BF16 ? 8 : 4;
     constexpr int kMaxSeg = 8832;   // 37 KB of shared memory; larger ones leave no L1 (serving step 56 us, not 51)
+    static_assert(process_smem(kMaxSeg) <= 48 * 1024, "what a kernel gets without being asked for more");
     const long slots = (long)device_sm_count() * kProcOcc;
     const long least = (p.V + kMaxSeg - 1) / kMaxSeg;
     const long most = (p.V + 128 * E - 1) / (128 * E) > least ? (p.V + 128 * E - 1) / (128 * E) : least;
@@ -320,10 +321,6 @@ cudaError_t process_launch(ProcessParams p, cudaStream_t stream) {
     const void* kern = p.dtype == SPEC_BF16
                            ? (aligned ? (const void*)process_kernel<bf16_t, true> : (const void*)process_kernel<bf16_t, false>)
                            : (aligned ? (const void*)process_kernel<float, true> : (const void*)process_kernel<float, false>);
-    if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return e;
-    }
     void* args[] = {&p};
     return cudaLaunchKernel(kern, dim3((unsigned)grid), dim3(kProcThreads), args, smem, stream);
 }

@@ -11,6 +11,15 @@
 
 namespace spec {
 
+inline size_t align256(size_t n) { return (n + 255) / 256 * 256; }   // parts of a workspace
+
+// Larger over the warp, NaN when any lane has it.
+__device__ __forceinline__ float warp_max_nan(float x) {
+    float r;
+    asm volatile("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+    return r;
+}
+
 template <typename T> struct NegInf;
 template <> struct NegInf<float> { static constexpr uint32_t word = 0xff800000u; };
 template <> struct NegInf<bf16_t> { static constexpr uint32_t word = 0xff80ff80u; };

@@ -53,12 +53,6 @@ __host__ __device__ inline int top_blocks(int V, int elt_bytes, int lanes) {
     return ((V + 2 * E - 2) / E + 31) / 32 * (32 / lanes);
 }
 
-__device__ __forceinline__ float warp_max_nan(float x) {
-    float r;
-    asm volatile("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
-    return r;
-}
-
 // The sums over the warp of eight values per lane, two lanes' halves at a time: lane l ends
 // with the sum of value (l >> 2).
 __device__ __forceinline__ float warp_sum8(float (&v)[8]) {
@@ -642,8 +636,6 @@ __device__ __forceinline__ void top_pick(const TopLogitsParams& p, int row, uint
         if (!(taken.s > 0.0f)) atomicOr(p.status, SPEC_DEV_NONFINITE);   // no finite entry
     }
 }
-
-static size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
 // A row's blocks' keys and sums and, where its ties need them, the chosen blocks' words.
 static size_t top_smem(int n_blocks, int K, int lanes) { return ((size_t)n_blocks * 2 + (size_t)K * lanes) * 4; }
