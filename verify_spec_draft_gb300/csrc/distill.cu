@@ -290,6 +290,10 @@ __device__ __forceinline__ void distill_finish(const DistillParams& p, int row, 
 // (j - 1)th.  In place of the logits the gradient is safe for the same reason: a slice is
 // written after every record of its row has arrived, and a record holds what was read.
 //
+// A wait that runs out sets SPEC_DEV_TIMEOUT and s_gave_up, before whatever the waiter hands on.
+// From then on the CTA waits for nothing more, posts NaN, touches no slot, loads nothing more, and
+// writes NaN for the rows that it has not written, once its loads in flight have landed.
+//
 // Bound by memory, a read and a write of each logit: 1792 rows of 248,320 bf16 take 292 to 309 us
 // from one GPU to another, 5.75 TB/s and more, 86 to 91 % of a copy's rate.  What is missing is
 // residency: with 210 KB of slices in an SM and 3.5 us a row, the slot that waits for the
@@ -314,7 +318,10 @@ constexpr int kFuseMaxCtas = 512;
 struct FuseHeader {
     unsigned epoch;    // tags up to here have been used
     unsigned exits;    // CTAs that have left (0 between calls)
-    unsigned pad[62];
+    // 0 but in tests of a wait that runs out: how long one may take in us (0: kWaitLimitNs), and the
+    // exchange, from 1 on, whose record the first CTA keeps back.
+    unsigned patience, withheld;
+    unsigned pad[60];
 };
 
 __device__ __forceinline__ void post_word(unsigned long long* p, float v, unsigned tag) {
@@ -335,6 +342,22 @@ __device__ __forceinline__ void bulk_s2g_wait_read() { asm volatile("cp.async.bu
 __device__ __forceinline__ void bulk_s2g_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 template <int BAR>   // the warps of a job on the entries
 __device__ __forceinline__ void named_sync() { asm volatile("bar.sync %0, %1;" :: "n"(BAR), "n"(kFuseNamed) : "memory"); }
+
+__device__ __forceinline__ unsigned long long fuse_limit(const FuseHeader* h) {
+    const unsigned us = *(const volatile unsigned*)&h->patience;
+    return us ? us * 1000ull : kWaitLimitNs;
+}
+// The rest of a wait whose first try failed: false when it ran out, here or in another thread.  Out of
+// line, as a dozen copies of it are instructions that the jobs' chains wait for.
+static __device__ __noinline__ bool fuse_wait(uint64_t* bar, unsigned parity, unsigned* status, const FuseHeader* h,
+                                              volatile int* gave_up) {
+#pragma unroll 1
+    for (int i = 0; i < 8; ++i)
+        if (mbar_try_wait(bar, parity)) return true;
+    if (!*gave_up && mbar_wait(bar, parity, status, fuse_limit(h))) return true;
+    *gave_up = 1;
+    return false;
+}
 
 // What is known of a row once its slices' statistics are together.
 struct FuseRow : RowEnds {
@@ -374,7 +397,7 @@ __global__ void __launch_bounds__(kFuseThreads, kFuseOcc) distill_fused_kernel(D
     __shared__ uint32_t s_bits[kFuseSlice * E / 32];         // the slice's entries named so far
     __shared__ float2 s_tail[2][kDenseWarps], s_top[2][kNamedWarps], s_teach[2][kNamedWarps];
     __shared__ float s_loss[2][kNamedWarps], s_wt[2], s_aT[2];
-    __shared__ int s_flag[2];
+    __shared__ int s_flag[2], s_gave_up;
     __shared__ FuseRow s_row[SLOTS];
     __shared__ FuseEntry s_entry[SLOTS][kFuseNamed];
     const int tid = threadIdx.x, lane = tid & 31;
@@ -403,13 +426,15 @@ __global__ void __launch_bounds__(kFuseThreads, kFuseOcc) distill_fused_kernel(D
             mbar_init(&s_stated[q], kNamedWarps);
             s_flag[q] = 0;
         }
+        s_gave_up = 0;
         fence_mbar_init();
     }
     for (int i = tid; i < kFuseSlice * E / 32; i += kFuseThreads) s_bits[i] = 0u;
     __syncthreads();
-    bool dead = false;   // a wait ran out: nothing more is waited for
+    auto gave_up = [&] { return *(volatile int*)&s_gave_up != 0; };
+    bool dead = false;   // this thread's waits so far have not all ended well
     auto wait = [&](uint64_t* bar, int phase) {
-        if (!mbar_wait(bar, phase & 1, p.status, dead ? 0ull : kWaitLimitNs)) dead = true;
+        if (!dead && !mbar_try_wait(bar, phase & 1)) dead = !fuse_wait(bar, phase & 1, p.status, p.fuse, &s_gave_up);
     };
 
     if (tid < kFuseDense) {
@@ -443,6 +468,7 @@ __global__ void __launch_bounds__(kFuseThreads, kFuseOcc) distill_fused_kernel(D
                         }
                         s += words_sum<T, kFuseBatch>(w, m, c);
                     }
+                    if (dead) m = NAN;
                     const float2 t = pair_lanes<32>(make_float2(m, s * ref_fix(m, c)), c);
                     if (lane == 0) s_tail[i & 1][warp] = t;
                 }
@@ -455,7 +481,9 @@ __global__ void __launch_bounds__(kFuseThreads, kFuseOcc) distill_fused_kernel(D
                 wait(&s_known[j % SLOTS], j / SLOTS);
                 const FuseRow& row = s_row[j % SLOTS];
                 const float x = row.ref;
-                if (row.skip) {
+                if (dead) {
+                    // the slot is not this row's
+                } else if (row.skip) {
                     for (int l = tid; l < n; l += kFuseDense) slot[l] = make_uint4(0u, 0u, 0u, 0u);
                 } else if (ref_near(x)) {
                     const f2x mm = f2_pack(-x, -x), ff = f2_pack(row.factor, row.factor);
@@ -534,7 +562,7 @@ __global__ void __launch_bounds__(kFuseThreads, kFuseOcc) distill_fused_kernel(D
                 s_aT[par] = cur.aT;
             }
             wait(&s_full[i % SLOTS], i / SLOTS);
-            if (at >= 0 && cur.wt != 0.0f) {
+            if (!dead && at >= 0 && cur.wt != 0.0f) {
                 T* x = reinterpret_cast<T*>(slot_of(i)) + at;
                 cur.z = to_float(*x);
                 *x = sizeof(T) == 2 ? (T)0xff80u : (T)-INFINITY;
@@ -549,6 +577,7 @@ __global__ void __launch_bounds__(kFuseThreads, kFuseOcc) distill_fused_kernel(D
                     s_teach[par][warp] = t;
                     s_top[par][warp] = z;
                 }
+                if (dead) f |= 4;
                 if (rank == 0) {
                     f |= (cur.id < -1 || cur.id >= p.V) ? 1 : 0;
                     if (!(a < INFINITY) || !(cur.aT < INFINITY) || !(fabsf(cur.wt) < INFINITY)) f |= 2;
@@ -577,7 +606,8 @@ __global__ void __launch_bounds__(kFuseThreads, kFuseOcc) distill_fused_kernel(D
                 d = r.bad ? NAN : (taught ? (ex2(ref_rel(e.z, r.M, c)) / r.Z - pk) * (r.wt * p.inv_t) : 0.0f);
             }
             wait(&s_dense[i % SLOTS], i / SLOTS);
-            if (e.at >= 0 && !r.skip) {
+            const bool lost = gave_up();   // then what was read above may be anything
+            if (!lost && e.at >= 0 && !r.skip) {
                 T* x = reinterpret_cast<T*>(slot_of(i)) + e.at;
                 if (sizeof(T) == 2) *x = (T)__bfloat16_as_ushort(__float2bfloat16_rn(d));
                 else *x = (T)d;
@@ -586,7 +616,7 @@ __global__ void __launch_bounds__(kFuseThreads, kFuseOcc) distill_fused_kernel(D
             mbar_arrive1(&s_fixed[i % SLOTS]);
             if (rank != 0) continue;
             float l = 0.0f;   // the loss, behind what the slice waits for
-            if (!r.skip && taught) {
+            if (!lost && !r.skip && taught) {
                 if (named) l = entry_loss(r, e.a, e.z, p.inv_t);
                 if (k == 0) l += rest_loss(r, r.aT, p.inv_t);
             }
@@ -596,8 +626,9 @@ __global__ void __launch_bounds__(kFuseThreads, kFuseOcc) distill_fused_kernel(D
             if (k == 0) {
                 l = s_loss[par][0];
                 for (int q = 1; q < kNamedWarps; ++q) l += s_loss[par][q];
-                p.loss_out[row] = r.skip ? 0.0f : (r.bad ? NAN : l);
-                if (p.lse_out) p.lse_out[row] = r.skip ? 0.0f : (r.bad ? NAN : ref_log(r.M, r.Z, p.inv_t));
+                const bool bad = gave_up() || (!r.skip && r.bad);
+                p.loss_out[row] = bad ? NAN : (r.skip ? 0.0f : l);
+                if (p.lse_out) p.lse_out[row] = bad ? NAN : (r.skip ? 0.0f : ref_log(r.M, r.Z, p.inv_t));
             }
         }
     } else if (tid < kFuseDense + 2 * kFuseNamed + 32) {
@@ -605,6 +636,7 @@ __global__ void __launch_bounds__(kFuseThreads, kFuseOcc) distill_fused_kernel(D
         unsigned long long* recs = p.records + (size_t)group * kFuseRing * p.group_size * kFuseRecord;
         const float2 none = make_float2(-INFINITY, 0.0f);
         unsigned live = 0;       // exchanges so far: rows that count
+        const unsigned withheld = *(volatile unsigned*)&p.fuse->withheld;
         for (int i = 0; i < n_it; ++i) {
             const int par = i & 1;
             wait(&s_stated[par], i >> 1);
@@ -630,7 +662,7 @@ __global__ void __launch_bounds__(kFuseThreads, kFuseOcc) distill_fused_kernel(D
                 ++live;
                 float2 t = pair_lanes<16>((lane & 15) < kDenseWarps ? s_tail[par][lane & 15] : none, c);
                 if (flag || dead) t.x = flag & 1 ? __uint_as_float(kBadToken) : NAN;
-                if (lane < (rank == 0 ? 4 : 2))
+                if (lane < (rank == 0 ? 4 : 2) && (live != withheld || blockIdx.x != 0))
                     post_word(rec + (size_t)rank * kFuseRecord + lane, lane == 0 ? t.x : (lane == 1 ? t.y : (lane == 2 ? nn.x : nn.y)), tag);
                 const unsigned long long t0 = global_timer_ns();
                 for (int r = lane; r < p.group_size; r += 32) {
@@ -646,7 +678,7 @@ __global__ void __launch_bounds__(kFuseThreads, kFuseOcc) distill_fused_kernel(D
                         for (int q = 0; q < kFuseRecord; ++q)
                             if (q < 2 || r == 0) here &= (unsigned)(v[q] >> 32) == tag;
                         if (here) break;
-                        if (dead || late || (((++spins) & 63u) == 0 && global_timer_ns() - t0 > kWaitLimitNs)) {
+                        if (dead || late || (((++spins) & 63u) == 0 && global_timer_ns() - t0 > fuse_limit(p.fuse))) {
                             late = true;
                             break;
                         }
@@ -657,7 +689,10 @@ __global__ void __launch_bounds__(kFuseThreads, kFuseOcc) distill_fused_kernel(D
                 }
                 late = __any_sync(0xffffffffu, late);
                 token = __any_sync(0xffffffffu, token);
-                if (late) dead = true;
+                if (late) {
+                    *(volatile int*)&s_gave_up = 1;
+                    dead = true;
+                }
                 T2 = pair_lanes<32>(T2, c);
                 N2.x = __shfl_sync(0xffffffffu, N2.x, 0);
                 N2.y = __shfl_sync(0xffffffffu, N2.y, 0);
@@ -705,9 +740,11 @@ __global__ void __launch_bounds__(kFuseThreads, kFuseOcc) distill_fused_kernel(D
                 }
             }
         };
-        for (int i = 0; i < SLOTS && i < n_it; ++i) issue(i);
-        for (int i = 0; i < n_it; ++i) {
+        int i = 0;
+        for (int q = 0; q < SLOTS && q < n_it; ++q) issue(q);
+        for (; i < n_it; ++i) {
             wait(&s_fixed[i % SLOTS], i / SLOTS);
+            if (__any_sync(0xffffffffu, gave_up())) break;
             const Slice<T> sl = slice_of(i);
             if (lane == 0 && sl.a < sl.b)
                 bulk_s2g(grad_of(i) + sl.in.entry(sl.first + sl.a), slot_of(i) + sl.a, (unsigned)(sl.b - sl.a) * 16u);
@@ -720,6 +757,15 @@ __global__ void __launch_bounds__(kFuseThreads, kFuseOcc) distill_fused_kernel(D
                 fence_proxy_async_smem();   // the words that were not whole, before the copy that may cover them
                 __syncwarp();
                 issue(i + SLOTS);
+            }
+        }
+        if (i < n_it) {   // a wait has run out
+            for (int q = i; q < i + SLOTS && q < n_it; ++q)
+                mbar_wait(&s_full[q % SLOTS], (q / SLOTS) & 1, p.status, kWaitLimitNs);
+            for (; i < n_it; ++i) {
+                const Slice<T> sl = slice_of(i);
+                const uint32_t nan = sizeof(T) == 2 ? 0x7fff7fffu : 0x7fffffffu;
+                for (int l = lane; l < sl.n; l += 32) sl.in.store(grad_of(i), sl.first + l, make_uint4(nan, nan, nan, nan));
             }
         }
         if (lane == 0) {
