@@ -606,8 +606,10 @@ spec_status spec_tree_verify(const void *target_logits, spec_dtype target_dtype,
  * A masked entry is -inf whatever it held (NaN, +inf); a row whose mask leaves nothing is
  * all -inf, which verification reports as a row without a distribution.  A token outside
  * [0, V) (a bias id below -1) or a length outside its range raises flag TOKEN and counts
- * for nothing; a repetition or temperature that is not positive and finite, or a frequency
- * or presence that is not finite, makes the request's allowed entries NaN (flag NONFINITE).
+ * for nothing; a repetition or temperature that is not positive and finite, or so far from 1
+ * that 1 / temperature, repetition / temperature or 1 / (repetition temperature) is no
+ * normal float32 number, or a frequency or presence that is not finite, makes the request's
+ * allowed entries NaN (flag NONFINITE).
  * Limits: 1 <= B <= 65535, 1 <= R <= SPEC_MAX_GAMMA + 1, 1 <= V <= SPEC_MAX_V,
  * 0 <= Lmax <= SPEC_MAX_HISTORY, 0 <= n_bias <= SPEC_MAX_BIASES, V <= ld < 2^31.
  */

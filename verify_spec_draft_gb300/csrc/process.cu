@@ -24,6 +24,8 @@
 // issue slots 70 % busy meanwhile.  The same in one pass per row (every row's own counts) took
 // 90 us, entries touched one at a time instead of by whole words 55, two batches of words in
 // turn instead of one requested ahead 62, batches of 2 or 3 words 63 to 66.
+#include <float.h>
+
 #include "internal.h"
 #include "row_words.cuh"
 
@@ -193,12 +195,14 @@ __global__ void __launch_bounds__(kProcThreads, kProcOcc) process_kernel(Process
         if (tid < j0) count(s_blk[tid], p.Lmax);   // drafted before this CTA's first row
         else bad_token |= (unsigned)s_blk[tid] >= (unsigned)p.V;
     }
-    const bool valid = rep > 0.0f && rep < INFINITY && temp > 0.0f && temp < INFINITY && fabsf(freq) < INFINITY &&
-                       fabsf(pres) < INFINITY;
+    float tinv = 1.0f / temp, f_pos = tinv / rep, f_neg = tinv * rep;   // the latter a seen entry's, by its sign
+    // the factors are normal numbers: a logit of 0 or -inf stays what it is
+    const float least = fminf(tinv, fminf(f_pos, f_neg)), most = fmaxf(tinv, fmaxf(f_pos, f_neg));
+    const bool valid = rep > 0.0f && rep < INFINITY && temp > 0.0f && temp < INFINITY && least >= FLT_MIN &&
+                       most <= FLT_MAX && fabsf(freq) < INFINITY && fabsf(pres) < INFINITY;
     if (report && bad_token) atomicOr(p.status, SPEC_DEV_TOKEN);
     if (report && !valid && tid == 0) atomicOr(p.status, SPEC_DEV_NONFINITE);
-    const float tinv = valid ? 1.0f / temp : NAN;
-    const float f_pos = tinv / rep, f_neg = tinv * rep;   // a seen entry's factor, by its sign
+    if (!valid) tinv = f_pos = f_neg = NAN;
     __syncthreads();
     auto bias_of = [&](uint32_t st) {
         const uint32_t slot = (st >> kCountBits) & kSlotMask;
