@@ -280,8 +280,8 @@ __device__ __forceinline__ void distill_finish(const DistillParams& p, int row, 
 // So the row behind is reduced while the statistics of the row before travel (2000 to 4000
 // cycles on a loaded memory system, about as long as A and B), its named entries are out by
 // then, and three or four slots keep one slice arriving and one leaving meanwhile.  With take
-// and fix in the same warps, A(i + 2) waited for fix(i): 2000 rows of 20,000 bf16 took 48 us,
-// not 42.
+// and fix in the same warps, A(i + 2) waited for fix(i): 2000 rows of 20,000 bf16 took 48 us and
+// not 42, today 40.
 //
 // The exchange: a record per CTA in global memory, each 64-bit word a value and a tag that no
 // earlier row or call has used, so a word is valid when its tag is and nothing else has to
@@ -294,14 +294,15 @@ __device__ __forceinline__ void distill_finish(const DistillParams& p, int row, 
 // From then on the CTA waits for nothing more, posts NaN, touches no slot, loads nothing more, and
 // writes NaN for the rows that it has not written, once its loads in flight have landed.
 //
-// Bound by memory, a read and a write of each logit: 1792 rows of 248,320 bf16 take 292 to 309 us
-// from one GPU to another, 5.75 TB/s and more, 86 to 91 % of a copy's rate.  What is missing is
+// Bound by memory, a read and a write of each logit: 1792 rows of 248,320 bf16 take 297 to 320 us
+// from one GPU to another.  One row in ten has weight 0 there and is written but not read, so that
+// 1.69 GB move, at 5.3 to 5.7 TB/s, 79 to 85 % of a copy's rate.  What is missing is
 // residency: with 210 KB of slices in an SM and 3.5 us a row, the slot that waits for the
 // exchange is one of three that would otherwise load or store.  Short rows are bound by the
-// steps from A(i) to B(i), 1.5 us a row.  For the 1792 rows, reading them twice takes 392 us;
-// slices in registers with the whole CTA waiting on the exchange 834; two CTAs per SM with three
-// slots of 32 KB 335, three CTAs 372 to 427; four slots of 56 KB 345; the reduction and the
-// gradient in separate warps 440; 256, 320 or 512 dense threads 2 to 5 % longer.
+// steps from A(i) to B(i), 1.5 us a row.  For the 1792 rows, when they took 292 to 309, reading them
+// twice took 392 us; slices in registers with the whole CTA waiting on the exchange 834; two
+// CTAs per SM with three slots of 32 KB 335, three CTAs 372 to 427; four slots of 56 KB 345; the
+// reduction and the gradient in separate warps 440; 256, 320 or 512 dense threads 2 to 5 % longer.
 // ---------------------------------------------------------------------------------
 constexpr int kFuseDense = 384;                            // threads of the dense warps
 constexpr int kFuseNamed = SPEC_MAX_TEACHER;               // threads of either job on the entries
@@ -797,7 +798,7 @@ static cudaError_t fused_launch(DistillParams p, cudaStream_t stream) {
     p.n_groups = groups;
     p.group_size = size;
     p.slice = (words + size - 1) / size;
-    // a fourth slot where there is room for one: 1000 rows of 20,001 float32 take 41 us instead of
+    // a fourth slot where there is room for one: 1000 rows of 20,001 float32 took 41 us instead of
     // 43, 2000 of 20,000 bf16 39 instead of 42 (smaller slices for its sake cost more than it gives)
     const int slots = 4 * p.slice <= kFuseRoom ? 4 : 3;
     const void* kern = slots == 4 ? (const void*)distill_fused_kernel<T, 4> : (const void*)distill_fused_kernel<T, 3>;

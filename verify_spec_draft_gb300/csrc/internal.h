@@ -235,7 +235,7 @@ struct ProcessParams {
     int mask_rows, mask_words;
     unsigned* status;
     // chosen at launch
-    int seg;                   // vocabulary entries per CTA (a multiple of its threads)
+    int seg;                   // vocabulary entries per CTA (a multiple of 128)
     int n_seg, rows_per_cta, n_row_split;
     int hist_vec;              // histories start on 16 bytes
 };

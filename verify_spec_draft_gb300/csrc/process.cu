@@ -18,12 +18,13 @@
 // + A.  Between rows the next block token's entry is renewed, so a history is scanned once
 // per segment and not once per row.
 //
-// Bound: bytes (each logit read and written once, a bit of mask), then instructions.  16 requests
-// of 8 rows of 248,320 bf16 with histories of 4096, masks and biases take 51 us of GPU time,
-// 5.15 TB/s of what has to move and 77 % of a copy's rate; 41 M warp instructions keep the
-// issue slots 70 % busy meanwhile.  The same in one pass per row (every row's own counts) took
-// 90 us, entries touched one at a time instead of by whole words 55, two batches of words in
-// turn instead of one requested ahead 62, batches of 2 or 3 words 63 to 66.
+// Bound: bytes (each logit read and written once, a bit of mask), then instructions.  32 requests
+// of 8 rows of 248,320 bf16 with histories of 8192, masks and 300 biases take 51 us of GPU time,
+// 5.15 TB/s of what has to move and 77 % of a copy's rate; 48 M warp instructions keep the
+// issue slots 72 % busy meanwhile.  Batches of 2 or 3 words take 57 and 59, entries touched one at
+// a time instead of by whole words 55.  Against earlier stages of the kernel: one pass per row
+// (every row's own counts) took 90; two batches of words in turn, not one requested ahead,
+// changed nothing at 62.
 #include <float.h>
 
 #include "internal.h"
@@ -32,7 +33,7 @@
 namespace spec {
 
 constexpr int kProcThreads = 256;
-constexpr int kProcOcc = 4;   // CTAs per SM (the serving step above: 3 take 72 us, 6 take 69)
+constexpr int kProcOcc = 4;   // CTAs per SM (the step above: 3 take 58 us, 5 take 63, 6 take 78)
 constexpr uint32_t kCountBits = 20, kCountMask = (1u << kCountBits) - 1u;
 constexpr uint32_t kSlotMask = 0x7ffu, kInPrompt = 0x80000000u;
 

@@ -19,8 +19,8 @@
 // the row keeps its relative accuracy.
 //
 // Bound: 256 rows of 248,320 bf16, K 64, take 30.4 us, 4.2 TB/s of what has to be read and 62 %
-// of a copy's rate.  The scan goes at the memory's pace (23 us by itself, from cold caches,
-// 5.5 TB/s); the picks are latency, some 8 us of steps that wait for one another (the maxima,
+// of a copy's rate.  The scan goes at the memory's pace (24 us by itself, from cold caches,
+// 5.3 TB/s); the picks are latency, some 8 us of steps that wait for one another (the maxima,
 // the bisection, the chosen blocks, the ranks) with a fifth of the warps there.  A full
 // selection over the block maxima took 76 us in all, reading the chosen blocks twice 61.
 #include "internal.h"
