@@ -677,6 +677,8 @@ spec_status spec_top_logits(const void *logits, spec_dtype dtype, int rows, int 
  * student row with NaN, +inf or no finite entry, and a teacher row with NaN or +inf, gets
  * NaN in its outputs (flag NONFINITE); an id outside [-1, V) or listed twice does too (flag
  * TOKEN).  Where the teacher gives mass to what the student rules out, the loss is +inf.
+ * With grad_out the CTAs of a row wait for one another; what a wait that runs out (flag
+ * TIMEOUT) kept from being computed is NaN.
  * Limits: those of spec_top_logits.
  */
 spec_status spec_distill(const void *student, spec_dtype dtype, int rows, int V, int ld,
