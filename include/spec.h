@@ -20,7 +20,7 @@
  *           reduction accumulates in float32.  Tokens are int32 in [0, V).
  * Align.    Every logits/weights base pointer must be 16-byte aligned (rejected
  *           with SPEC_ERR_ALIGN otherwise), and a workspace as cudaMalloc aligns it
- *           (spec_process_logits, spec_top_logits and spec_distill reject one that is
+ *           (spec_process_logits and what is declared behind it reject one that is
  *           not 16-byte aligned).  V need not be a multiple of anything:
  *           rows whose byte length is not a multiple of 16 take a scalar path.
  * Streams.  Calls enqueue work on `stream` (a cudaStream_t; NULL = legacy default
@@ -93,7 +93,10 @@ typedef enum {
     /* 8 is not an operation */
     SPEC_OP_PROCESS_LOGITS = 9,
     SPEC_OP_TOP_LOGITS = 10,
-    SPEC_OP_DISTILL = 11
+    SPEC_OP_DISTILL = 11,
+    SPEC_OP_POLICY_LOSS = 12,
+    SPEC_OP_MARKOV_GRAD = 13,
+    SPEC_OP_ADAMW = 14
 } spec_op;
 
 /* Device status flags (OR-ed into the workspace status word). */
@@ -114,7 +117,11 @@ typedef enum {
 #define SPEC_MAX_BIASES 2047          /* spec_process_logits: biased tokens per request */
 #define SPEC_MAX_TEACHER 128          /* spec_top_logits / spec_distill: entries per row */
 #define SPEC_MAX_V_TEACHER (1 << 20)  /* spec_top_logits / spec_distill: vocabulary size */
-#define SPEC_MAX_TEACHER_ROWS (1 << 24)   /* spec_top_logits / spec_distill: rows       */
+#define SPEC_MAX_TEACHER_ROWS (1 << 24)   /* spec_top_logits / spec_distill / spec_policy_loss: rows */
+#define SPEC_MAX_MARKOV_ROWS (1 << 16)    /* spec_markov_grad: B * gamma                */
+#define SPEC_MAX_V_MARKOV (1 << 20)       /* spec_markov_grad: vocabulary size          */
+#define SPEC_MAX_ADAMW_TENSORS (1 << 16)  /* spec_adamw: tensors of one call            */
+#define SPEC_ADAMW_BLOCK 128              /* spec_adamw: entries that share an 8-bit state's scale */
 
 /*
  * spec_workspace_bytes - workspace size for one operation (host only, pure).
@@ -131,6 +138,9 @@ typedef enum {
  *          per request, V, r = 0).
  *          SPEC_OP_TOP_LOGITS / SPEC_OP_DISTILL: B = rows, gamma = entries per row, V,
  *          r unused.
+ *          SPEC_OP_POLICY_LOSS: the status word only (pass B = rows, gamma = 1, V, r = 0).
+ *          SPEC_OP_MARKOV_GRAD: B requests, gamma positions, V, r.
+ *          SPEC_OP_ADAMW: the header only (pass B = tensors, gamma = V = 1, r = 0).
  *          For SPEC_OP_DRAFT the size covers one launch's slice of requests, which
  *          spec_draft_block reuses across the slices of a larger batch.
  * Returns 0 for arguments outside the supported ranges.
@@ -686,6 +696,119 @@ spec_status spec_distill(const void *student, spec_dtype dtype, int rows, int V,
                          const float *tail, const float *weight, float temperature, float *loss_out,
                          float *lse_out, void *grad_out, void *workspace, size_t workspace_bytes,
                          spec_stream_t stream);
+
+/*
+ * spec_policy_loss - the clipped policy loss of sampled tokens with a KL term, and its
+ * gradient on request: a drafter (or a target) trained on its own blocks.
+ *
+ * A row z holds the logits that token x is judged by; with q = softmax(z / t), lp = ln q_x,
+ * u = exp(lp - old_logp), A the advantage and d = ref_logp - lp,
+ *     loss  = -min(u A, clip(u, 1 - clip_low, 1 + clip_high) A) + kl (e^d - d - 1)
+ *     slope = d loss / d lp
+ *           = (A >= 0 ? u <= 1 + clip_high : u >= 1 - clip_low) ? -u A : 0, plus kl (1 - e^d)
+ *     grad  = weight * d loss / d z_v = (weight / t) slope ([v = x] - q_v)
+ *   logits      [rows] rows of V entries, ld entries apart (ld >= V), float32 or bf16.
+ *   tokens      int32 [rows]: x.
+ *   old_logp    float32 [rows]: ln of the probability that x was drawn with.
+ *   advantage   float32 [rows].
+ *   ref_logp    float32 [rows]: ln of the reference's probability of x; not read when
+ *               kl = 0, when it may be NULL.
+ *   weight      float32 [rows], nullable (1).  A row of weight 0 is not read, nor are its
+ *               other inputs: its loss, logp and gradient are 0.
+ *   clip_low, clip_high   0 <= clip_low <= 1, clip_high >= 0, finite;  kl >= 0, finite.
+ *   loss_out    float32 [rows], not weighted; logp_out float32 [rows]: lp.
+ *   grad_out    the logits' layout and type; NULL for the loss alone; may be logits itself,
+ *               which it then replaces.
+ *   workspace   spec_workspace_bytes(SPEC_OP_POLICY_LOSS, rows, 1, V, 0): the status word.
+ * A row with NaN, +inf or no finite entry, or whose old_logp, advantage, ref_logp or weight
+ * is not finite, gets NaN in its outputs (flag NONFINITE); a token outside [0, V) does too
+ * (flag TOKEN).  A token of probability 0 has lp = -inf, and where a KL term meets it loss
+ * +inf.  A row whose slope (or (weight / t) slope) is not finite, that one or one with u A
+ * beyond float32's range, gets a gradient of NaN (flag NONFINITE).
+ * Limits: 1 <= rows <= SPEC_MAX_TEACHER_ROWS, 1 <= V <= SPEC_MAX_V_TEACHER, V <= ld < 2^31,
+ * temperature positive, finite and not subnormal.
+ */
+spec_status spec_policy_loss(const void *logits, spec_dtype dtype, int rows, int V, int ld,
+                             const int32_t *tokens, const float *old_logp, const float *advantage,
+                             const float *ref_logp, const float *weight, float temperature,
+                             float clip_low, float clip_high, float kl, float *loss_out,
+                             float *logp_out, void *grad_out, void *workspace,
+                             size_t workspace_bytes, spec_stream_t stream);
+
+/*
+ * spec_markov_grad - the gradients of the Markov bias weights: from the gradient of the biased
+ * rows (spec_e2etv's, spec_distill's or spec_policy_loss's) to U's and Wt's.
+ *
+ * spec_draft_block's rows are z_j = l_j + sum_k U[x_{j-1}, k] Wt[:, k], x_0 the anchor.  With
+ * dz the gradient of the rows,
+ *     dWt[v, k] = sum over rows (b, j) of dz[b, j, v] U[x_{j-1}, k]
+ *     dU[x, k]  = sum over rows with x_{j-1} = x of sum_v dz[b, j, v] Wt[v, k]
+ * in float32, rounded once to the outputs' type.  Every entry of both outputs is written.
+ * Sums are formed in an order that the sizes alone fix: a call replays bit for bit.
+ *   grad          [B, gamma] rows of V entries, ld entries apart (ld >= V), float32 or bf16.
+ *   anchor        int32 [B]; tokens int32 [B, gamma] (the last of a request is not read; NULL
+ *                 when gamma = 1).  A row whose x_{j-1} is -1 (a block that ended early)
+ *                 counts for nothing, and its dz is not used; one that is outside [-1, V)
+ *                 does too and raises flag TOKEN.
+ *   U, Wt         [V, r], weights_dtype; 1 <= r <= SPEC_MAX_RANK.
+ *   dU_out, dWt_out  [V, r], out_dtype (float32 or bf16); neither may overlap an input.
+ *   workspace     spec_workspace_bytes(SPEC_OP_MARKOV_GRAD, B, gamma, V, r).
+ * A NaN or an infinity in a row's dz or in a weight goes where the formulas take it.
+ * Limits: 1 <= gamma <= SPEC_MAX_GAMMA, 1 <= B * gamma <= SPEC_MAX_MARKOV_ROWS,
+ * 1 <= V <= SPEC_MAX_V_MARKOV, V <= ld < 2^31.
+ */
+spec_status spec_markov_grad(const void *grad, spec_dtype grad_dtype, int B, int gamma, int V, int ld,
+                             const int32_t *anchor, const int32_t *tokens, const void *U,
+                             const void *Wt, spec_dtype weights_dtype, int r, void *dU_out,
+                             void *dWt_out, spec_dtype out_dtype, void *workspace,
+                             size_t workspace_bytes, spec_stream_t stream);
+
+/*
+ * spec_adamw - one AdamW step over many tensors at once, with states in 32 bits or in 8.
+ *
+ * With g the gradient (times *grad_scale), T the step's number, counted from 1:
+ *     m = beta1 m + (1 - beta1) g
+ *     v = beta2 v + (1 - beta2) g g
+ *     p = p (1 - lr weight_decay) - lr (m / (1 - beta1^T)) / (sqrt(v / (1 - beta2^T)) + eps)
+ * in float32.  A tensor of n entries:
+ *   param, grad   float32 or bf16 (param_dtype, grad_dtype).
+ *   master        float32 [n]: p of a bf16 param, which gets p rounded; NULL for a float32
+ *                 param, which is p itself.
+ *   state_bits    32: m and v are float32 [n].
+ *                 8: m and v are e4m3 codes [n], v's of sqrt(v) (its sign bit 0), against
+ *                 m_scale and v_scale, float32 [ceil(n / SPEC_ADAMW_BLOCK)]: entry i is
+ *                 code * scale[i / SPEC_ADAMW_BLOCK].  A step's scale is the power of two that
+ *                 brings the block's largest magnitude into [128, 256), 2^-126 at least.
+ *                 Codes are rounded at random, up with the probability of what is left: a
+ *                 change by 1 - beta2 is far below a code's spacing, and rounding to nearest
+ *                 would undo it at every step.  A sqrt(v) above 0 keeps a code above 0.
+ * The random bits are Philox4x32-10's (Salmon et al., SC'11) with key (seed's low word, high
+ * word) and counter (i / 4's low word, high word, T, index of the tensor): word i % 4, its low
+ * 16 bits for m and its high 16 for v.  Any step replays bit for bit.
+ *   tensors       HOST array [n_tensors], read during the call.
+ *   step          int32 device [1]: steps taken so far; the call makes it T = step + 1.
+ *   grad_scale    float32 device [1], nullable (1): e.g. a clip factor.
+ *   lr >= 0, 0 <= beta1 < 1, 0 <= beta2 < 1, eps >= FLT_MIN, weight_decay >= 0, finite.
+ *   workspace     spec_workspace_bytes(SPEC_OP_ADAMW, n_tensors, 1, 1, 0): the header.
+ * Tensors may not overlap.  Pointers need only their type's alignment (16 bytes are faster,
+ * as is a multiple of 4 entries).  An entry whose gradient is not finite, or whose m or v
+ * would not be, stays as it is (8-bit states: within its block's new scale), flag NONFINITE.
+ * Limits: 0 <= n_tensors <= SPEC_MAX_ADAMW_TENSORS, 0 <= n < 2^40, step in [0, 2^31 - 2]
+ * (outside, nothing is updated: flag TOKEN).
+ */
+typedef struct {
+    void *param;
+    float *master;
+    const void *grad;
+    void *m, *v;
+    float *m_scale, *v_scale;
+    int64_t n;
+    int32_t param_dtype, grad_dtype, state_bits, pad;
+} spec_adamw_tensor;
+spec_status spec_adamw(const spec_adamw_tensor *tensors, int n_tensors, int32_t *step, double lr,
+                       double beta1, double beta2, double eps, double weight_decay,
+                       const float *grad_scale, uint64_t seed, void *workspace,
+                       size_t workspace_bytes, spec_stream_t stream);
 
 #ifdef __cplusplus
 }

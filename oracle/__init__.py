@@ -32,9 +32,12 @@ the pages step by step, in their order and notation:
   logits rows of a block.
 * ``teacher`` - a row's largest logits with the log-sum-exp of the rest, and the
   distillation loss and gradient from them.
+* ``policy``  - the clipped policy loss of sampled tokens with a KL term, and its gradient.
+* ``markov``  - the gradients of the Markov bias weights from the rows' gradient.
+* ``adamw``   - one AdamW step, with states in 32 bits or in 8.
 
 Pins (tests that tie each function to the pages or to mathematics rather than to
 itself) live in ``tests/test_oracle_*.py``; each function's docstring names them.
 """
 
-from . import philox, draft, verify, e2etv, schedule, anchors, topk, tree, process, teacher  # noqa: F401
+from . import philox, draft, verify, e2etv, schedule, anchors, topk, tree, process, teacher, policy, markov, adamw  # noqa: F401

@@ -1,0 +1,165 @@
+"""markov_grad against the float64 oracle (one GB300)."""
+
+import numpy as np
+import pytest
+import torch
+
+import verify_spec_draft_gb300 as vsd
+from oracle import markov as om
+
+pytestmark = pytest.mark.gpu
+F32, BF16 = torch.float32, torch.bfloat16
+
+
+def inputs(B, G, V, r, gdt, wdt, seed=0, pad=0, same=False):
+    rng = np.random.default_rng(seed)
+    dz = torch.from_numpy((rng.normal(size=(B, G, V)) * np.exp(rng.normal(size=(B, G, V)))).astype(np.float32)).to(gdt)
+    if pad:
+        room = torch.full((B, G, V + pad), 3.0, dtype=gdt)
+        room[..., :V] = dz
+        dz = room[..., :V]
+    U, Wt = (torch.from_numpy(rng.normal(size=(V, r)).astype(np.float32)).to(wdt) for _ in range(2))
+    x = np.minimum((V ** rng.random((B, G + 1))).astype(np.int32) - 1, V - 1)
+    if same:
+        x[:] = V // 2
+    ends = rng.integers(1, 3 * G + 2, (B, 1))
+    ends[0] = G + 1
+    x = np.where(np.arange(G + 1)[None] < ends, x, -1).astype(np.int32)
+    return dz, torch.from_numpy(x[:, 0].copy()), torch.from_numpy(x[:, 1:].copy()), U, Wt
+
+
+def on_gpu(dz, *rest):
+    """dz with its row stride kept"""
+    if dz.is_contiguous():
+        return (dz.cuda(), *(t.cuda() for t in rest))
+    B, G, V = dz.shape
+    ld = dz.stride(-2)
+    room = torch.full((B, G, ld), float("nan"), dtype=dz.dtype, device="cuda")
+    room[..., :V] = dz.cuda()
+    return (room[..., :V], *(t.cuda() for t in rest))
+
+
+def check(got, want, n, V, out):
+    """Bars in roundings e = 2^-24 of the sums of magnitudes.  dWt sums n products: n + 16 at most, the 16
+    for what a tensor core drops within a step.  dU sums V products in parts and then the rows: with 8 parts
+    or steps of 16 that lose two roundings each, V / 8 + 64 at most.  The output's rounding is half a step."""
+    e = 2.0 ** -24
+    half = 2.0 ** -8 if out == BF16 else e
+    tiny = 2.0 ** -134 if out == BF16 else 0.0
+    for k, terms in (("Wt", n + 16), ("U", V / 8 + 64 + n / 8)):
+        g, w = got[k].double().cpu().numpy(), want[k]
+        assert g.shape == w.shape
+        bar = terms * e * want[k + "_abs"] * (1 + half) + half * np.abs(w) + tiny
+        assert (np.abs(g - w) <= bar).all(), (k, np.abs(g - w).max(), (np.abs(g - w) / np.maximum(bar, 1e-300)).max())
+
+
+@pytest.mark.parametrize("gdt,wdt,out", [(F32, F32, F32), (BF16, BF16, BF16), (BF16, BF16, F32), (F32, BF16, BF16),
+                                         (BF16, F32, F32)])
+@pytest.mark.parametrize("B,G,V,r", [(1, 1, 1, 1), (1, 1, 5, 3), (2, 3, 130, 8), (3, 7, 1000, 64), (1, 7, 2048, 256),
+                                     (20, 7, 515, 128), (5, 64, 333, 17), (40, 5, 1024, 192)])
+def test_sizes_and_types(spec, B, G, V, r, gdt, wdt, out):
+    a = inputs(B, G, V, r, gdt, wdt, seed=B * 100 + r)
+    got = vsd.markov_grad(*on_gpu(*a), dtype=out)
+    want = om.markov_grad(*(t.double().numpy() if t.is_floating_point() else t.numpy() for t in a))
+    check(got, want, B * G, V, out)
+    assert got["U"].dtype == out and vsd.device_status(got["ws"]) == 0
+    untouched = torch.ones(V, dtype=torch.bool)
+    prev = torch.cat([a[1][:, None], a[2][:, :-1]], 1).reshape(-1).long()
+    untouched[prev[prev >= 0]] = False
+    assert (got["U"].cpu()[untouched] == 0).all()
+    # the same call again, with outputs and workspace given, bit for bit
+    again = vsd.markov_grad(*on_gpu(*a), ws=got["ws"], out={k: torch.full_like(got[k], 5.0) for k in ("U", "Wt")})
+    assert torch.equal(again["U"], got["U"]) and torch.equal(again["Wt"], got["Wt"])
+
+
+@pytest.mark.parametrize("V,pad,r", [(1000, 8, 64), (1000, 1, 64), (1001, 0, 128), (1001, 7, 64), (50257, 0, 64),
+                                     (4096, 3, 256)])
+def test_row_strides(spec, V, pad, r):
+    """Rows at any offset; what lies between them (NaN here) is not read into anything."""
+    a = inputs(4, 7, V, r, BF16, BF16, seed=V + pad, pad=pad)
+    got = vsd.markov_grad(*on_gpu(*a), dtype=F32)
+    want = om.markov_grad(*(t.double().numpy() if t.is_floating_point() else t.numpy() for t in a))
+    check(got, want, 28, V, F32)
+
+
+@pytest.mark.parametrize("dt,r", [(F32, 20), (BF16, 64)])
+def test_one_token_everywhere(spec, dt, r):
+    a = inputs(30, 9, 700, r, dt, dt, seed=4, same=True)
+    got = vsd.markov_grad(*on_gpu(*a), dtype=F32)
+    want = om.markov_grad(*(t.double().numpy() if t.is_floating_point() else t.numpy() for t in a))
+    check(got, want, 270, 700, F32)
+
+
+@pytest.mark.parametrize("dt,r", [(F32, 20), (BF16, 64), (BF16, 128)])
+def test_rows_without_a_token(spec, dt, r):
+    """Their dz may hold anything; tokens out of range are reported."""
+    a = list(inputs(6, 5, 900, r, dt, dt, seed=5))
+    a[1][2] = -1
+    a[2][2] = -1
+    prev = torch.cat([a[1][:, None], a[2][:, :-1]], 1)
+    assert (prev < 0).sum() >= 5
+    a[0][prev < 0] = torch.nan
+    got = vsd.markov_grad(*on_gpu(*a), dtype=F32)
+    want = om.markov_grad(*(t.double().numpy() if t.is_floating_point() else t.numpy() for t in a))
+    check(got, want, 30, 900, F32)
+    assert vsd.device_status(got["ws"]) == 0
+    a[2][0, 0] = 900
+    a[1][1] = -7
+    a[0][0, 1] = torch.inf
+    a[0][1, 0] = torch.nan
+    got = vsd.markov_grad(*on_gpu(*a), dtype=F32)
+    want = om.markov_grad(*(t.double().numpy() if t.is_floating_point() else t.numpy() for t in a))
+    check(got, want, 30, 900, F32)
+    assert vsd.device_status(got["ws"]) == vsd.DEV_TOKEN
+
+
+@pytest.mark.parametrize("dt", [F32, BF16])
+def test_nothing_counts(spec, dt):
+    a = list(inputs(3, 4, 300, 64, dt, dt, seed=6))
+    a[1][:], a[2][:] = -1, -1
+    got = vsd.markov_grad(*on_gpu(*a))
+    assert (got["U"] == 0).all() and (got["Wt"] == 0).all() and vsd.device_status(got["ws"]) == 0
+
+
+def test_gamma_one_needs_no_tokens(spec):
+    a = inputs(9, 1, 600, 64, BF16, BF16, seed=7)
+    g = on_gpu(*a)
+    one, two = vsd.markov_grad(*g), vsd.markov_grad(g[0], g[1], None, g[3], g[4])
+    assert torch.equal(one["U"], two["U"]) and torch.equal(one["Wt"], two["Wt"])
+
+
+@pytest.mark.parametrize("B,G,V,r", [(256, 7, 20000, 256), (61, 15, 31111, 192), (1, 7, 248320, 256)])
+def test_larger(spec, B, G, V, r):
+    """Against float64 products on the GPU."""
+    a = inputs(B, G, V, r, BF16, BF16, seed=8)
+    g = on_gpu(*a)
+    got = vsd.markov_grad(*g, dtype=F32)
+    prev = torch.cat([g[1][:, None], g[2][:, :-1]], 1).reshape(-1).long()
+    on = prev >= 0
+    d, u, w = g[0].reshape(-1, V)[on].double(), g[3][prev[on]].double(), g[4].double()
+    want = {}
+    for k, f in (("", lambda t: t), ("_abs", torch.abs)):
+        want["Wt" + k] = (f(d).t() @ f(u)).cpu().numpy()
+        z = torch.zeros((V, r), dtype=torch.float64, device="cuda")
+        want["U" + k] = z.index_add_(0, prev[on], f(d) @ f(w)).cpu().numpy()
+    check(got, want, B * G, V, F32)
+
+
+def test_refusals(spec):
+    dz, anchor, tokens, U, Wt = on_gpu(*inputs(3, 4, 100, 8, F32, F32))
+    for bad in ((dz[0], anchor, tokens, U, Wt), (dz, anchor, None, U, Wt), (dz, anchor, tokens[:, :3], U, Wt),
+                (dz, anchor.long(), tokens, U, Wt), (dz, anchor, tokens, U[:99], Wt[:99]), (dz, anchor, tokens, U, Wt[:, :4]),
+                (dz, anchor, tokens, U, Wt.to(BF16)), (dz, anchor, tokens, U, None), (dz, anchor.cpu(), tokens, U, Wt)):
+        with pytest.raises(ValueError):
+            vsd.markov_grad(*bad)
+    with pytest.raises(TypeError):
+        vsd.markov_grad(dz, anchor, tokens, U.half(), Wt.half())
+    with pytest.raises(TypeError):
+        vsd.markov_grad(dz, anchor, tokens, U, Wt, dtype=torch.float16)
+    with pytest.raises(ValueError):
+        vsd.markov_grad(dz, anchor, tokens, U, Wt, out=dict(U=torch.empty_like(U)))
+    with pytest.raises(ValueError):
+        vsd.markov_grad(dz, anchor, tokens, U, Wt, out=dict(U=torch.empty_like(U), Wt=torch.empty_like(Wt).to(BF16)))
+    with pytest.raises(vsd.SpecError):
+        need = vsd.workspace_bytes(vsd.OP_MARKOV_GRAD, 3, 4, 100, 8)
+        vsd.markov_grad(dz, anchor, tokens, U, Wt, ws=torch.zeros(need - 1, dtype=torch.uint8, device="cuda"))

@@ -29,6 +29,7 @@ F32, BF16 = 0, 1
 OP_DRAFT, OP_VERIFY, OP_E2ETV, OP_DRAFT_VERIFY, OP_BRANCH_PLAN, OP_VERIFY_TOPK, OP_TREE_VERIFY, OP_DRAFT_TOPK = (
     0, 1, 2, 3, 4, 5, 6, 7)
 OP_PROCESS_LOGITS, OP_TOP_LOGITS, OP_DISTILL = 9, 10, 11
+OP_POLICY_LOSS, OP_MARKOV_GRAD, OP_ADAMW = 12, 13, 14
 DEV_TIMEOUT, DEV_NONFINITE, DEV_TOKEN = 1, 2, 4
 
 # C signatures of include/spec.h, as ctypes types
@@ -65,8 +66,23 @@ SIGNATURES = {
                                _vp]),
     "spec_distill": (_i32, [_vp, _i32, _i32, _i32, _i32, _vp, _i32, _vp, _i32, _vp, _vp, ctypes.c_float, _vp, _vp,
                             _vp, _vp, _sz, _vp]),
+    "spec_policy_loss": (_i32, [_vp, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _vp, ctypes.c_float, ctypes.c_float,
+                                ctypes.c_float, ctypes.c_float, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "spec_markov_grad": (_i32, [_vp, _i32, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _i32, _i32, _vp, _vp, _i32,
+                                _vp, _sz, _vp]),
+    "spec_adamw": (_i32, [_vp, _i32, _vp, ctypes.c_double, ctypes.c_double, ctypes.c_double, ctypes.c_double,
+                          ctypes.c_double, _vp, ctypes.c_uint64, _vp, _sz, _vp]),
 }
 
+
+class AdamwTensor(ctypes.Structure):
+    """spec_adamw_tensor of include/spec.h."""
+    _fields_ = [(name, ctypes.c_void_p) for name in ("param", "master", "grad", "m", "v", "m_scale", "v_scale")] + [
+        ("n", ctypes.c_int64), ("param_dtype", ctypes.c_int32), ("grad_dtype", ctypes.c_int32),
+        ("state_bits", ctypes.c_int32), ("pad", ctypes.c_int32)]
+
+
+ADAMW_BLOCK = 128   # entries that share an 8-bit state's scale
 _lib = None
 
 
@@ -777,3 +793,197 @@ def distill(student, values, ids, tail=None, weight=None, temperature=1.0, grad=
         raise SpecError(code, "spec_distill")
     out["ws"] = ws
     return out
+
+
+# ---------------------------------------------------------------------------------
+# a drafter's training step
+# ---------------------------------------------------------------------------------
+def policy_loss(logits, tokens, old_logp, advantage, ref_logp=None, weight=None, temperature=1.0, clip=(0.2, 0.2),
+                kl=0.0, grad=False, ws=None, out=None, stream=None):
+    """spec_policy_loss.  logits [..., V] f32/bf16 (rows may lie further apart than V); tokens
+    int32 [...]; old_logp, advantage, ref_logp (needed where kl > 0) and weight (or None) float32
+    [...]; clip the ratio's room below and above 1.  Returns a dict of device tensors: loss and
+    logp float32 [...] and, with ``grad``, grad of the logits' type and layout (``out["grad"]``
+    may be logits itself)."""
+    torch = _torch()
+    lib = _lib or load()
+    ld = _need_rows(logits, "logits")
+    dev, shape = logits.device, logits.shape
+    if _away(dev, stream):
+        with torch.cuda.device(dev):
+            return policy_loss(logits, tokens, old_logp, advantage, ref_logp, weight, temperature, clip, kl, grad, ws,
+                               out, stream)
+    lead, V = shape[:-1], shape[-1]
+    rows = logits.numel() // V if V else 0
+    _need_ints("policy_loss", rows, V, ld)
+    if tokens is None or old_logp is None or advantage is None:
+        raise ValueError("tokens, old_logp and advantage are required")
+    if kl > 0 and ref_logp is None:
+        raise ValueError("ref_logp is required where kl > 0")
+    low, high = clip
+    f32 = torch.float32
+    a_tok, a_old, a_adv, a_ref, a_weight = _addrs(
+        dev, ("tokens", "old_logp", "advantage", "ref_logp", "weight"), (tokens, old_logp, advantage, ref_logp, weight),
+        (torch.int32, f32, f32, f32, f32), (lead,) * 5)
+    if out is None:
+        with _made_on(stream):
+            out = dict(loss=torch.empty(lead, dtype=f32, device=dev), logp=torch.empty(lead, dtype=f32, device=dev))
+            if grad:
+                out["grad"] = _rows_like(logits, ld)
+    else:
+        _need_out(out, dev, loss=(f32, lead), logp=(f32, lead))
+        if grad:
+            _need_same_rows(out.get("grad"), "grad", logits, ld)
+    if ws is None:
+        with _made_on(stream):
+            ws = workspace(OP_POLICY_LOSS, rows, 1, V, 0, dev, stream)
+    code = lib.spec_policy_loss(
+        logits.data_ptr(), _dtype_code(logits), rows, V, ld, a_tok, a_old, a_adv, a_ref, a_weight, float(temperature),
+        float(low), float(high), float(kl), out["loss"].data_ptr(), out["logp"].data_ptr(),
+        out["grad"].data_ptr() if grad else None, ws.data_ptr(), _ws_bytes(ws, dev), _stream(stream))
+    if code != OK:
+        raise SpecError(code, "spec_policy_loss")
+    out["ws"] = ws
+    return out
+
+
+def markov_grad(grad, anchor, tokens, U, Wt, dtype=None, ws=None, out=None, stream=None):
+    """spec_markov_grad.  grad [B, gamma, V] f32/bf16, the biased rows' gradient (rows may lie
+    further apart than V); anchor int32 [B] and tokens int32 [B, gamma] as draft_block takes and
+    gives them (-1: the rows behind count for nothing; tokens may be None where gamma is 1);
+    U, Wt [V, r] f32/bf16; ``dtype`` the outputs' type, the weights' by default.  Returns a dict
+    of device tensors: U and Wt [V, r], their gradients."""
+    torch = _torch()
+    lib = _lib or load()
+    ld = _need_rows(grad, "grad")
+    if grad.dim() != 3:
+        raise ValueError("grad must be [B, gamma, V]")
+    dev = grad.device
+    if _away(dev, stream):
+        with torch.cuda.device(dev):
+            return markov_grad(grad, anchor, tokens, U, Wt, dtype, ws, out, stream)
+    B, gamma, V = grad.shape
+    if U is None or Wt is None or anchor is None or (tokens is None and gamma != 1):
+        raise ValueError("anchor, tokens, U and Wt are required")
+    if U.dim() != 2 or U.shape[0] != V:
+        raise ValueError(f"U must be [{V}, r], got {tuple(U.shape)}")
+    r = U.shape[1]
+    _need_ints("markov_grad", B, gamma, V, ld, r)
+    wdt = _dtype_code(U)
+    a_anchor, a_tokens, a_U, a_Wt = _addrs(dev, ("anchor", "tokens", "U", "Wt"), (anchor, tokens, U, Wt),
+                                           (torch.int32, torch.int32, U.dtype, U.dtype),
+                                           ((B,), (B, gamma), U.shape, U.shape))
+    if out is None:
+        with _made_on(stream):
+            out = {k: torch.empty((V, r), dtype=dtype or U.dtype, device=dev) for k in ("U", "Wt")}
+    else:
+        dtype = dtype or (U.dtype if out.get("U") is None else out["U"].dtype)
+        _need_out(out, dev, U=(dtype, (V, r)), Wt=(dtype, (V, r)))
+    odt = _dtype_code(out["U"])
+    if ws is None:
+        with _made_on(stream):
+            ws = workspace(OP_MARKOV_GRAD, B, gamma, V, r, dev, stream)
+    code = lib.spec_markov_grad(
+        grad.data_ptr(), _dtype_code(grad), B, gamma, V, ld, a_anchor, a_tokens, a_U, a_Wt, wdt, r,
+        out["U"].data_ptr(), out["Wt"].data_ptr(), odt, ws.data_ptr(), _ws_bytes(ws, dev), _stream(stream))
+    if code != OK:
+        raise SpecError(code, "spec_markov_grad")
+    out["ws"] = ws
+    return out
+
+
+def adamw_state(param, bits=32, master=None):
+    """A parameter's state for adamw: a dict of device tensors, m and v (zeros), in 8 bits also
+    m_scale and v_scale, for a bf16 parameter its float32 master (the parameter's values, or
+    the tensor given)."""
+    torch = _torch()
+    dev, shape = param.device, param.shape
+    if bits == 32:
+        s = {k: torch.zeros(shape, dtype=torch.float32, device=dev) for k in ("m", "v")}
+    elif bits == 8:
+        blocks = (param.numel() + ADAMW_BLOCK - 1) // ADAMW_BLOCK
+        s = {k: torch.zeros(shape, dtype=torch.float8_e4m3fn, device=dev) for k in ("m", "v")}
+        s.update({k: torch.zeros((blocks,), dtype=torch.float32, device=dev) for k in ("m_scale", "v_scale")})
+    else:
+        raise ValueError(f"a state has 32 or 8 bits, got {bits}")
+    if _dtype_code(param) == BF16:
+        s["master"] = param.float() if master is None else master
+    elif master is not None:
+        raise ValueError("a float32 parameter has no master")
+    return s
+
+
+class AdamwTable:
+    """What adamw steps over: the tensors of adamw_table, and their addresses for the library."""
+
+    def __init__(self, params, grads, states, device, entries):
+        self.params, self.grads, self.states, self.device, self.entries = params, grads, states, device, entries
+
+    def __len__(self):
+        return len(self.params)
+
+
+def adamw_table(params, grads, states):
+    """The tensors of an AdamW step, checked once and kept: lists of parameters (f32/bf16), of
+    their gradients (f32/bf16, read anew at every step) and of their states (adamw_state's dicts;
+    32 and 8 bits may be mixed).  Steps write the parameters and states in place."""
+    torch = _torch()
+    params, grads, states = list(params), list(grads), list(states)
+    if not len(params) == len(grads) == len(states):
+        raise ValueError(f"{len(params)} parameters, {len(grads)} gradients and {len(states)} states")
+    if not params:
+        raise ValueError("an empty table")
+    if len(params) > 65536:
+        raise SpecError(2, f"adamw_table({len(params)} tensors)")
+    dev = params[0].device
+    f32, f8 = torch.float32, torch.float8_e4m3fn
+    entries = (AdamwTensor * len(params))()
+    for i, (p, g, s, e) in enumerate(zip(params, grads, states, entries)):
+        _need(p, f"parameter {i}", dev)
+        e.param_dtype = _dtype_code(p)
+        _need(g, f"gradient {i}", dev, None, p.shape)
+        e.grad_dtype = _dtype_code(g)
+        for k in ("m", "v"):
+            if s.get(k) is None:
+                raise ValueError(f"state {i} has no {k}")
+        packed = s["m"].dtype == f8
+        for k in ("m", "v"):
+            _need(s[k], f"state {i}'s {k}", dev, f8 if packed else f32, p.shape)
+            if packed:
+                _need(s.get(k + "_scale"), f"state {i}'s {k}_scale", dev, f32,
+                      ((p.numel() + ADAMW_BLOCK - 1) // ADAMW_BLOCK,))
+        if e.param_dtype == BF16:
+            _need(s.get("master"), f"state {i}'s master", dev, f32, p.shape)
+            e.master = s["master"].data_ptr()
+        elif s.get("master") is not None:
+            raise ValueError(f"state {i}: a float32 parameter has no master")
+        e.param, e.grad, e.m, e.v, e.n = p.data_ptr(), g.data_ptr(), s["m"].data_ptr(), s["v"].data_ptr(), p.numel()
+        e.state_bits = 8 if packed else 32
+        if packed:
+            e.m_scale, e.v_scale = s["m_scale"].data_ptr(), s["v_scale"].data_ptr()
+    return AdamwTable(params, grads, states, dev, entries)
+
+
+def adamw(table, step, lr, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, grad_scale=None, seed=0, ws=None,
+          stream=None):
+    """spec_adamw: one AdamW step over an adamw_table, in place.  step int32 [1] on the device,
+    the steps taken so far, which the call counts up; grad_scale float32 [1] on the device or None,
+    a factor of all gradients; seed the 8-bit states' random rounding.  Returns a dict: step."""
+    torch = _torch()
+    lib = _lib or load()
+    dev = table.device
+    if _away(dev, stream):
+        with torch.cuda.device(dev):
+            return adamw(table, step, lr, betas, eps, weight_decay, grad_scale, seed, ws, stream)
+    a_step, a_scale = _addrs(dev, ("step", "grad_scale"), (step, grad_scale), (torch.int32, torch.float32), ((1,), (1,)))
+    if a_step is None:
+        raise ValueError("step is required")
+    if ws is None:
+        with _made_on(stream):
+            ws = workspace(OP_ADAMW, len(table), 1, 1, 0, dev, stream)
+    code = lib.spec_adamw(table.entries, len(table), a_step, float(lr), float(betas[0]), float(betas[1]), float(eps),
+                          float(weight_decay), a_scale, int(seed) & 0xFFFFFFFFFFFFFFFF, ws.data_ptr(),
+                          _ws_bytes(ws, dev), _stream(stream))
+    if code != OK:
+        raise SpecError(code, "spec_adamw")
+    return dict(step=step, ws=ws)

@@ -65,6 +65,20 @@ size_t spec_workspace_bytes(spec_op op, int B, int gamma, int V, int r) {
             return 0;
         return op == SPEC_OP_TOP_LOGITS ? top_logits_workspace_bytes(B, gamma, V) : distill_workspace_bytes(B, V);
     }
+    if (op == SPEC_OP_POLICY_LOSS) {   // B rows
+        if (B < 1 || B > SPEC_MAX_TEACHER_ROWS || V < 1 || V > SPEC_MAX_V_TEACHER) return 0;
+        return kWsHeaderBytes;
+    }
+    if (op == SPEC_OP_MARKOV_GRAD) {
+        if (B < 1 || gamma < 1 || gamma > SPEC_MAX_GAMMA || (long)B * gamma > SPEC_MAX_MARKOV_ROWS || V < 1 ||
+            V > SPEC_MAX_V_MARKOV || r < 1 || r > SPEC_MAX_RANK)
+            return 0;
+        return markov_grad_workspace_bytes(B, gamma, V, r);
+    }
+    if (op == SPEC_OP_ADAMW) {   // B tensors
+        if (B < 0 || B > SPEC_MAX_ADAMW_TENSORS) return 0;
+        return kWsHeaderBytes;
+    }
     if (B < 1 || gamma < 1 || gamma > SPEC_MAX_GAMMA || V < 1 || V > SPEC_MAX_V) return 0;
     switch (op) {
         case SPEC_OP_DRAFT:
@@ -612,4 +626,119 @@ spec_status spec_distill(const void* student, spec_dtype dtype, int rows, int V,
     return cuda_status(distill_launch(p, workspace, (cudaStream_t)stream));
 }
 
+spec_status spec_policy_loss(const void* logits, spec_dtype dtype, int rows, int V, int ld, const int32_t* tokens,
+                             const float* old_logp, const float* advantage, const float* ref_logp, const float* weight,
+                             float temperature, float clip_low, float clip_high, float kl, float* loss_out,
+                             float* logp_out, void* grad_out, void* workspace, size_t workspace_bytes,
+                             spec_stream_t stream) {
+    if (!dtype_ok(dtype)) return SPEC_ERR_DTYPE;
+    if (rows < 1 || rows > SPEC_MAX_TEACHER_ROWS || V < 1 || V > SPEC_MAX_V_TEACHER || ld < V) return SPEC_ERR_SHAPE;
+    if (!temperature_ok(temperature) || !(clip_low >= 0.0f && clip_low <= 1.0f) ||
+        !(clip_high >= 0.0f && clip_high < INFINITY) || !(kl >= 0.0f && kl < INFINITY))
+        return SPEC_ERR_INVALID_ARG;
+    if (!logits || !tokens || !old_logp || !advantage || !loss_out || !logp_out || (kl > 0.0f && !ref_logp))
+        return SPEC_ERR_INVALID_ARG;
+    if (!aligned16(logits) || !aligned16(grad_out) || !aligned16(workspace)) return SPEC_ERR_ALIGN;
+    if (!workspace || workspace_bytes < kWsHeaderBytes) return SPEC_ERR_WORKSPACE;
+    PolicyParams p;
+    memset(&p, 0, sizeof(p));
+    p.logits = logits;
+    p.dtype = dtype;
+    p.rows = rows;
+    p.V = V;
+    p.ld = ld;
+    p.tokens = tokens;
+    p.old_logp = old_logp;
+    p.advantage = advantage;
+    p.ref_logp = kl > 0.0f ? ref_logp : nullptr;
+    p.weight = weight;
+    p.scale = (float)(1.4426950408889634074 / (double)temperature);
+    p.inv_t = (float)(1.0 / (double)temperature);
+    p.low = (float)(1.0 - (double)clip_low);
+    p.high = (float)(1.0 + (double)clip_high);
+    p.kl = kl;
+    p.loss_out = loss_out;
+    p.logp_out = logp_out;
+    p.grad_out = grad_out;
+    p.status = &reinterpret_cast<WsHeader*>(workspace)->status;
+    return cuda_status(policy_launch(p, (cudaStream_t)stream));
+}
+
+spec_status spec_markov_grad(const void* grad, spec_dtype grad_dtype, int B, int gamma, int V, int ld,
+                             const int32_t* anchor, const int32_t* tokens, const void* U, const void* Wt,
+                             spec_dtype weights_dtype, int r, void* dU_out, void* dWt_out, spec_dtype out_dtype,
+                             void* workspace, size_t workspace_bytes, spec_stream_t stream) {
+    if (!dtype_ok(grad_dtype) || !dtype_ok(weights_dtype) || !dtype_ok(out_dtype)) return SPEC_ERR_DTYPE;
+    if (B < 1 || gamma < 1 || gamma > SPEC_MAX_GAMMA || (long)B * gamma > SPEC_MAX_MARKOV_ROWS || V < 1 ||
+        V > SPEC_MAX_V_MARKOV || ld < V || r < 1 || r > SPEC_MAX_RANK)
+        return SPEC_ERR_SHAPE;
+    if (!grad || !anchor || (gamma > 1 && !tokens) || !U || !Wt || !dU_out || !dWt_out) return SPEC_ERR_INVALID_ARG;
+    if (!aligned16(grad) || !aligned16(U) || !aligned16(Wt) || !aligned16(dU_out) || !aligned16(dWt_out) ||
+        !aligned16(workspace))
+        return SPEC_ERR_ALIGN;
+    if (!workspace || workspace_bytes < markov_grad_workspace_bytes(B, gamma, V, r)) return SPEC_ERR_WORKSPACE;
+    MarkovParams p;
+    memset(&p, 0, sizeof(p));
+    p.grad = grad;
+    p.gdt = grad_dtype;
+    p.B = B;
+    p.gamma = gamma;
+    p.V = V;
+    p.ld = ld;
+    p.r = r;
+    p.anchor = anchor;
+    p.tokens = tokens;
+    p.U = U;
+    p.Wt = Wt;
+    p.wdt = weights_dtype;
+    p.odt = out_dtype;
+    p.dU_out = dU_out;
+    p.dWt_out = dWt_out;
+    return cuda_status(markov_grad_launch(p, workspace, (cudaStream_t)stream));
+}
+
+spec_status spec_adamw(const spec_adamw_tensor* tensors, int n_tensors, int32_t* step, double lr, double beta1,
+                       double beta2, double eps, double weight_decay, const float* grad_scale, uint64_t seed,
+                       void* workspace, size_t workspace_bytes, spec_stream_t stream) {
+    if (n_tensors < 0 || n_tensors > SPEC_MAX_ADAMW_TENSORS) return SPEC_ERR_SHAPE;
+    if (!step || (n_tensors > 0 && !tensors)) return SPEC_ERR_INVALID_ARG;
+    if (!(lr >= 0.0 && lr <= FLT_MAX) || !(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0) ||
+        !(eps >= FLT_MIN && eps <= FLT_MAX) || !(weight_decay >= 0.0 && lr * weight_decay <= FLT_MAX))
+        return SPEC_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(step) & 3u) || (reinterpret_cast<uintptr_t>(grad_scale) & 3u) || !aligned16(workspace))
+        return SPEC_ERR_ALIGN;
+    for (int i = 0; i < n_tensors; ++i) {
+        const spec_adamw_tensor& t = tensors[i];
+        if (!dtype_ok(t.param_dtype) || !dtype_ok(t.grad_dtype) || (t.state_bits != 32 && t.state_bits != 8))
+            return SPEC_ERR_DTYPE;
+        if (t.n < 0 || t.n >= (1ll << 40)) return SPEC_ERR_SHAPE;
+        if (t.n == 0) continue;
+        const bool half = t.param_dtype == SPEC_BF16, packed = t.state_bits == 8;
+        if (!t.param || !t.grad || !t.m || !t.v || half != (t.master != nullptr) || packed != (t.m_scale != nullptr) ||
+            packed != (t.v_scale != nullptr))
+            return SPEC_ERR_INVALID_ARG;
+        const uintptr_t words = (half ? 0 : reinterpret_cast<uintptr_t>(t.param)) | reinterpret_cast<uintptr_t>(t.master) |
+                                (t.grad_dtype == SPEC_BF16 ? 0 : reinterpret_cast<uintptr_t>(t.grad)) |
+                                (packed ? 0 : reinterpret_cast<uintptr_t>(t.m) | reinterpret_cast<uintptr_t>(t.v)) |
+                                reinterpret_cast<uintptr_t>(t.m_scale) | reinterpret_cast<uintptr_t>(t.v_scale);
+        if ((words & 3u) || ((reinterpret_cast<uintptr_t>(t.param) | reinterpret_cast<uintptr_t>(t.grad)) & 1u))
+            return SPEC_ERR_ALIGN;
+    }
+    if (!workspace || workspace_bytes < kWsHeaderBytes) return SPEC_ERR_WORKSPACE;
+    AdamwCall c;
+    c.tensors = tensors;
+    c.n_tensors = n_tensors;
+    c.step = step;
+    c.lr = lr;
+    c.beta1 = beta1;
+    c.beta2 = beta2;
+    c.eps = eps;
+    c.weight_decay = weight_decay;
+    c.grad_scale = grad_scale;
+    c.seed = seed;
+    c.ws = workspace;
+    return cuda_status(adamw_launch(c, (cudaStream_t)stream));
+}
+
 }  // extern "C"
+

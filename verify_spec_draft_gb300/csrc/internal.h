@@ -292,6 +292,54 @@ struct DistillParams {
 size_t distill_workspace_bytes(int rows, int V);
 cudaError_t distill_launch(DistillParams p, void* ws, cudaStream_t stream);
 
+// spec_policy_loss
+struct PolicyParams {
+    const void* logits;        // rows of `ld` entries apart, V used
+    int dtype;
+    int rows, V, ld;
+    const int32_t* tokens;     // [rows]
+    const float* old_logp;     // [rows]
+    const float* advantage;    // [rows]
+    const float* ref_logp;     // [rows] (nullptr: no KL term)
+    const float* weight;       // [rows] (nullable: 1)
+    float scale, inv_t;        // log2(e) / temperature, 1 / temperature
+    float low, high, kl;       // 1 - clip_low, 1 + clip_high
+    float* loss_out;           // [rows]
+    float* logp_out;           // [rows]
+    void* grad_out;            // the logits' layout (nullable; may be logits itself)
+    unsigned* status;
+    int slice;                 // words of a row per CTA (chosen at launch)
+};
+cudaError_t policy_launch(PolicyParams p, cudaStream_t stream);
+
+// spec_markov_grad
+struct MarkovParams {
+    const void* grad;          // rows of `ld` entries apart, V used
+    int gdt;
+    int B, gamma, V, ld, r;
+    const int32_t* anchor;     // [B]
+    const int32_t* tokens;     // [B, gamma]
+    const void* U;             // [V, r]
+    const void* Wt;            // [V, r]
+    int wdt, odt;
+    void* dU_out;              // [V, r]
+    void* dWt_out;             // [V, r]
+};
+size_t markov_grad_workspace_bytes(int B, int gamma, int V, int r);
+cudaError_t markov_grad_launch(const MarkovParams& p, void* ws, cudaStream_t stream);
+
+// spec_adamw
+struct AdamwCall {
+    const spec_adamw_tensor* tensors;
+    int n_tensors;
+    int32_t* step;
+    double lr, beta1, beta2, eps, weight_decay;
+    const float* grad_scale;
+    uint64_t seed;
+    void* ws;
+};
+cudaError_t adamw_launch(const AdamwCall& c, cudaStream_t stream);
+
 int device_sm_count();
 
 cudaError_t verify_budget_launch(const float* conf, int B, int gamma, int budget, const float* cost,

@@ -1,0 +1,222 @@
+// markov.cu - the gradients of the Markov bias weights (spec_markov_grad).
+//
+// The biased rows are z_i = l_i + Wt U[x_i] (x_i the token before position i), so with dz the
+// rows' gradient and n = B gamma rows
+//     dWt = dz^T Ux          [V, r], Ux the gathered rows U[x_i]       contraction over n
+//     dX  = dz Wt            [n, r]                                    contraction over V
+//     dU[x] = the sum of dX's rows with x_i = x, in the rows' order
+// Four steps on the stream: the rows' tokens in order, with Ux beside them; dWt; dX in parts of
+// the vocabulary; and dU, which joins the parts of each token's rows.
+#include "internal.h"
+#include "row_words.cuh"
+
+namespace spec {
+
+constexpr int kMarkovTile = 64;                  // outputs of a tile's side
+constexpr int kMarkovStep = 16;                  // terms of a contraction step
+constexpr int kMarkovThreads = 256;
+constexpr int kMarkovMaxParts = 256;
+
+struct MarkovBind {
+    unsigned* status;
+    int32_t* order;          // [n] the rows by (token, row); rows without a token behind all others
+    int32_t* token;          // [n] their tokens in that order (V: none)
+    int32_t* of_row;         // [n] the rows' tokens (V: none)
+    float* dx;               // [parts][n][r]
+    int parts;
+};
+
+// Parts of the vocabulary that dX is summed in: as many as fill the device.
+static int markov_parts(int n, int r, int V, int sms) {
+    const int tiles = ((n + kMarkovTile - 1) / kMarkovTile) * ((r + kMarkovTile - 1) / kMarkovTile);
+    int parts = (4 * sms + tiles - 1) / tiles;
+    const int most = (V + 127) / 128;
+    if (parts > most) parts = most;
+    return parts < 1 ? 1 : (parts > kMarkovMaxParts ? kMarkovMaxParts : parts);
+}
+
+// Row i's place among the rows by (token, row), counted: n comparisons a row, 8 lanes a row.
+__global__ void __launch_bounds__(kMarkovThreads) markov_order_kernel(MarkovParams p, MarkovBind b) {
+    __shared__ int32_t s_tok[1024];
+    const int n = p.B * p.gamma;
+    auto token_of = [&](int i, bool* bad) {
+        const int q = i / p.gamma, j = i - q * p.gamma;
+        const int t = j == 0 ? p.anchor[q] : p.tokens[(long)q * p.gamma + j - 1];
+        if (t < -1 || t >= p.V) *bad = true;
+        return t < 0 || t >= p.V ? p.V : t;
+    };
+    const int sub = threadIdx.x & 7, i = blockIdx.x * (kMarkovThreads / 8) + (threadIdx.x >> 3);
+    bool bad = false;
+    const int mine = i < n ? token_of(i, &bad) : 0;
+    bool other = false;
+    int rank = 0;
+    for (int lo = 0; lo < n; lo += 1024) {
+        __syncthreads();
+        for (int k = threadIdx.x; k < 1024; k += kMarkovThreads) s_tok[k] = lo + k < n ? token_of(lo + k, &other) : 0x7fffffff;
+        __syncthreads();
+        const int m = min(1024, n - lo);
+        for (int k = sub; k < m; k += 8) {
+            const int t = s_tok[k];
+            rank += t < mine || (t == mine && lo + k < i) ? 1 : 0;
+        }
+    }
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) rank += __shfl_xor_sync(0xffffffffu, rank, o);
+    if (i < n && sub == 0) {
+        b.order[rank] = i;
+        b.token[rank] = mine;
+        b.of_row[i] = mine;
+        if (bad) atomicOr(b.status, SPEC_DEV_TOKEN);
+    }
+}
+
+template <typename T> __device__ __forceinline__ void put(void* o, long i, float x);
+template <> __device__ __forceinline__ void put<float>(void* o, long i, float x) { reinterpret_cast<float*>(o)[i] = x; }
+template <> __device__ __forceinline__ void put<bf16_t>(void* o, long i, float x) {
+    reinterpret_cast<unsigned short*>(o)[i] = __bfloat16_as_ushort(__float2bfloat16_rn(x));
+}
+__device__ __forceinline__ void put(void* o, int dtype, long i, float x) {
+    if (dtype == SPEC_BF16) put<bf16_t>(o, i, x);
+    else put<float>(o, i, x);
+}
+
+// A 64 x 64 tile of sums on CUDA cores, 4 x 4 outputs a thread: s_a[step][a], s_b[step][b].
+__device__ __forceinline__ void tile_step(const float (*s_a)[kMarkovTile + 4], const float (*s_b)[kMarkovTile + 4],
+                                          float (&acc)[4][4], int ty, int tx) {
+#pragma unroll
+    for (int k = 0; k < kMarkovStep; ++k) {
+        const float4 a = *reinterpret_cast<const float4*>(&s_a[k][ty * 4]), b = *reinterpret_cast<const float4*>(&s_b[k][tx * 4]);
+        const float x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int h = 0; h < 4; ++h)
+#pragma unroll
+            for (int w = 0; w < 4; ++w) acc[h][w] = fmaf(x[h], y[w], acc[h][w]);
+    }
+}
+
+// dWt's tile [64 entries, 64 k], and dU's rows of those entries set to 0.
+template <typename G, typename W>
+__global__ void __launch_bounds__(kMarkovThreads) markov_wt_kernel(MarkovParams p, MarkovBind b) {
+    __shared__ __align__(16) float s_a[kMarkovStep][kMarkovTile + 4], s_b[kMarkovStep][kMarkovTile + 4];
+    const int n = p.B * p.gamma, tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
+    const int v0 = blockIdx.x * kMarkovTile, k0 = blockIdx.y * kMarkovTile;
+    const G* dz = reinterpret_cast<const G*>(p.grad);
+    const W* U = reinterpret_cast<const W*>(p.U);
+    float acc[4][4] = {};
+    for (int i0 = 0; i0 < n; i0 += kMarkovStep) {
+        __syncthreads();
+        for (int e = tid; e < kMarkovStep * kMarkovTile; e += kMarkovThreads) {
+            const int i = i0 + e / kMarkovTile, c = e % kMarkovTile;
+            const int t = i < n ? b.of_row[i] : p.V;
+            const bool on = t < p.V;
+            s_a[e / kMarkovTile][c] = on && v0 + c < p.V ? load_one(dz + (long)i * p.ld + v0 + c) : 0.0f;
+            s_b[e / kMarkovTile][c] = on && k0 + c < p.r ? load_one(U + (long)t * p.r + k0 + c) : 0.0f;
+        }
+        __syncthreads();
+        tile_step(s_a, s_b, acc, ty, tx);
+    }
+#pragma unroll
+    for (int h = 0; h < 4; ++h)
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            const int v = v0 + ty * 4 + h, k = k0 + tx * 4 + w;
+            if (v >= p.V || k >= p.r) continue;
+            put(p.dWt_out, p.odt, (long)v * p.r + k, acc[h][w]);
+            put(p.dU_out, p.odt, (long)v * p.r + k, 0.0f);
+        }
+}
+
+// dX's tile [64 rows, 64 k] over one part of the vocabulary.
+template <typename G, typename W>
+__global__ void __launch_bounds__(kMarkovThreads) markov_dx_kernel(MarkovParams p, MarkovBind b) {
+    __shared__ __align__(16) float s_a[kMarkovStep][kMarkovTile + 4], s_b[kMarkovStep][kMarkovTile + 4];
+    const int n = p.B * p.gamma, tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
+    const int i0 = blockIdx.x * kMarkovTile, k0 = blockIdx.y * kMarkovTile, part = blockIdx.z;
+    const int lo = (int)((long)p.V * part / b.parts), hi = (int)((long)p.V * (part + 1) / b.parts);
+    const G* dz = reinterpret_cast<const G*>(p.grad);
+    const W* Wt = reinterpret_cast<const W*>(p.Wt);
+    float acc[4][4] = {};
+    for (int v0 = lo; v0 < hi; v0 += kMarkovStep) {
+        __syncthreads();
+        for (int e = tid; e < kMarkovStep * kMarkovTile; e += kMarkovThreads) {
+            const int a = e % kMarkovStep, i = i0 + e / kMarkovStep, v = v0 + a;
+            s_a[a][e / kMarkovStep] = i < n && v < hi && b.of_row[i] < p.V ? load_one(dz + (long)i * p.ld + v) : 0.0f;
+            const int c = e % kMarkovTile, u = v0 + e / kMarkovTile;
+            s_b[e / kMarkovTile][c] = u < hi && k0 + c < p.r ? load_one(Wt + (long)u * p.r + k0 + c) : 0.0f;
+        }
+        __syncthreads();
+        tile_step(s_a, s_b, acc, ty, tx);
+    }
+#pragma unroll
+    for (int h = 0; h < 4; ++h)
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            const int i = i0 + ty * 4 + h, k = k0 + tx * 4 + w;
+            if (i < n && k < p.r) b.dx[((long)part * n + i) * p.r + k] = acc[h][w];
+        }
+}
+
+// dU's rows: the CTA at a token's first place among the ordered rows sums that token's.
+__global__ void __launch_bounds__(kMarkovThreads) markov_u_kernel(MarkovParams p, MarkovBind b) {
+    const int n = p.B * p.gamma, at = blockIdx.x;
+    const int t = b.token[at];
+    if (t >= p.V || (at > 0 && b.token[at - 1] == t)) return;
+    int end = at + 1;
+    while (end < n && b.token[end] == t) ++end;
+    for (int k = threadIdx.x; k < p.r; k += kMarkovThreads) {
+        float s = 0.0f;
+        for (int q = at; q < end; ++q) {
+            const long i = b.order[q];
+            float x = 0.0f;
+            for (int part = 0; part < b.parts; ++part) x += b.dx[((long)part * n + i) * p.r + k];
+            s += x;
+        }
+        put(p.dU_out, p.odt, (long)t * p.r + k, s);
+    }
+}
+
+static size_t markov_bind(MarkovBind& b, void* ws, int n, int r, int V) {
+    uint8_t* w = reinterpret_cast<uint8_t*>(ws);
+    b.status = &reinterpret_cast<WsHeader*>(ws)->status;
+    size_t at = kWsHeaderBytes;
+    b.order = reinterpret_cast<int32_t*>(w + at);
+    at += align256((size_t)n * 4);
+    b.token = reinterpret_cast<int32_t*>(w + at);
+    at += align256((size_t)n * 4);
+    b.of_row = reinterpret_cast<int32_t*>(w + at);
+    at += align256((size_t)n * 4);
+    b.dx = reinterpret_cast<float*>(w + at);
+    at += align256((size_t)b.parts * n * r * 4);
+    return at;
+}
+
+size_t markov_grad_workspace_bytes(int B, int gamma, int V, int r) {
+    MarkovBind b;
+    b.parts = markov_parts(B * gamma, r, V, 152);
+    return markov_bind(b, nullptr, B * gamma, r, V);
+}
+
+template <typename G, typename W>
+static void markov_typed(const MarkovParams& p, const MarkovBind& b, cudaStream_t stream) {
+    const int n = p.B * p.gamma;
+    auto tiles = [](int x) { return (unsigned)((x + kMarkovTile - 1) / kMarkovTile); };
+    markov_wt_kernel<G, W><<<dim3(tiles(p.V), tiles(p.r)), kMarkovThreads, 0, stream>>>(p, b);
+    markov_dx_kernel<G, W><<<dim3(tiles(n), tiles(p.r), (unsigned)b.parts), kMarkovThreads, 0, stream>>>(p, b);
+}
+
+cudaError_t markov_grad_launch(const MarkovParams& p, void* ws, cudaStream_t stream) {
+    const int n = p.B * p.gamma;
+    MarkovBind b;
+    b.parts = markov_parts(n, p.r, p.V, 152);
+    markov_bind(b, ws, n, p.r, p.V);
+    markov_order_kernel<<<(n + kMarkovThreads / 8 - 1) / (kMarkovThreads / 8), kMarkovThreads, 0, stream>>>(p, b);
+    const bool g16 = p.gdt == SPEC_BF16, w16 = p.wdt == SPEC_BF16;
+    if (g16 && w16) markov_typed<bf16_t, bf16_t>(p, b, stream);
+    else if (g16) markov_typed<bf16_t, float>(p, b, stream);
+    else if (w16) markov_typed<float, bf16_t>(p, b, stream);
+    else markov_typed<float, float>(p, b, stream);
+    markov_u_kernel<<<n, kMarkovThreads, 0, stream>>>(p, b);
+    return cudaGetLastError();
+}
+
+}  // namespace spec
