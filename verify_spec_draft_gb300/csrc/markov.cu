@@ -7,8 +7,7 @@
 //     dU[x] = the sum of dX's rows with x_i = x, in the rows' order
 // Four steps on the stream: the rows' tokens in order, with Ux beside them; dWt; dX in parts of
 // the vocabulary; and dU, which joins the parts of each token's rows.
-#include "internal.h"
-#include "row_words.cuh"
+#include "markov.cuh"
 
 namespace spec {
 
@@ -16,15 +15,6 @@ constexpr int kMarkovTile = 64;                  // outputs of a tile's side
 constexpr int kMarkovStep = 16;                  // terms of a contraction step
 constexpr int kMarkovThreads = 256;
 constexpr int kMarkovMaxParts = 256;
-
-struct MarkovBind {
-    unsigned* status;
-    int32_t* order;          // [n] the rows by (token, row); rows without a token behind all others
-    int32_t* token;          // [n] their tokens in that order (V: none)
-    int32_t* of_row;         // [n] the rows' tokens (V: none)
-    float* dx;               // [parts][n][r]
-    int parts;
-};
 
 // Parts of the vocabulary that dX is summed in: as many as fill the device.
 static int markov_parts(int n, int r, int V, int sms) {
@@ -36,8 +26,9 @@ static int markov_parts(int n, int r, int V, int sms) {
 }
 
 // Row i's place among the rows by (token, row), counted: n comparisons a row, 8 lanes a row.
-__global__ void __launch_bounds__(kMarkovThreads) markov_order_kernel(MarkovParams p, MarkovBind b) {
+__global__ void __launch_bounds__(kMarkovThreads) markov_order_kernel(MarkovParams p, MarkovBind b, bool gather) {
     __shared__ int32_t s_tok[1024];
+    __shared__ unsigned s_bits[8];
     const int n = p.B * p.gamma;
     auto token_of = [&](int i, bool* bad) {
         const int q = i / p.gamma, j = i - q * p.gamma;
@@ -68,16 +59,23 @@ __global__ void __launch_bounds__(kMarkovThreads) markov_order_kernel(MarkovPara
         b.of_row[i] = mine;
         if (bad) atomicOr(b.status, SPEC_DEV_TOKEN);
     }
-}
-
-template <typename T> __device__ __forceinline__ void put(void* o, long i, float x);
-template <> __device__ __forceinline__ void put<float>(void* o, long i, float x) { reinterpret_cast<float*>(o)[i] = x; }
-template <> __device__ __forceinline__ void put<bf16_t>(void* o, long i, float x) {
-    reinterpret_cast<unsigned short*>(o)[i] = __bfloat16_as_ushort(__float2bfloat16_rn(x));
-}
-__device__ __forceinline__ void put(void* o, int dtype, long i, float x) {
-    if (dtype == SPEC_BF16) put<bf16_t>(o, i, x);
-    else put<float>(o, i, x);
+    if (!gather) return;
+    // the rows without a token, a CTA's 32 rows a half word of their step's 64
+    const unsigned any = __ballot_sync(0xffffffffu, i < n && mine >= p.V);
+    unsigned bits = 0u;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) bits |= ((any >> (8 * q)) & 1u) << q;
+    if ((threadIdx.x & 31) == 0) s_bits[threadIdx.x >> 5] = bits;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        unsigned w = 0u;
+        for (int q = 0; q < 8; ++q) w |= s_bits[q] << (4 * q);
+        reinterpret_cast<unsigned*>(b.none)[blockIdx.x] = w;
+    }
+    if (i >= n) return;
+    const uint4* u = reinterpret_cast<const uint4*>(reinterpret_cast<const bf16_t*>(p.U) + (long)mine * p.r);
+    uint4* o = reinterpret_cast<uint4*>(b.ux + (long)i * p.r);
+    for (int k = sub; k < p.r / 8; k += 8) o[k] = mine < p.V ? __ldg(u + k) : make_uint4(0u, 0u, 0u, 0u);
 }
 
 // A 64 x 64 tile of sums on CUDA cores, 4 x 4 outputs a thread: s_a[step][a], s_b[step][b].
@@ -185,8 +183,14 @@ static size_t markov_bind(MarkovBind& b, void* ws, int n, int r, int V) {
     at += align256((size_t)n * 4);
     b.of_row = reinterpret_cast<int32_t*>(w + at);
     at += align256((size_t)n * 4);
+    b.none = reinterpret_cast<unsigned long long*>(w + at);
+    at += align256((size_t)(n + 63) / 64 * 8);
+    b.ux = reinterpret_cast<bf16_t*>(w + at);
+    at += align256((size_t)n * r * 2);
     b.dx = reinterpret_cast<float*>(w + at);
-    at += align256((size_t)b.parts * n * r * 4);
+    const size_t plain = (size_t)b.parts * n * r * 4;
+    const size_t pairs = (size_t)(kMarkovPairs + (n + 255) / 256) * 256 * (r > 128 ? 256 : 128) * 4;
+    at += align256(plain > pairs ? plain : pairs);
     return at;
 }
 
@@ -209,7 +213,10 @@ cudaError_t markov_grad_launch(const MarkovParams& p, void* ws, cudaStream_t str
     MarkovBind b;
     b.parts = markov_parts(n, p.r, p.V, 152);
     markov_bind(b, ws, n, p.r, p.V);
-    markov_order_kernel<<<(n + kMarkovThreads / 8 - 1) / (kMarkovThreads / 8), kMarkovThreads, 0, stream>>>(p, b);
+    const bool tc = markov_tc_supported(p);
+    // (a CTA's rows are half a step's: both halves' words are written)
+    markov_order_kernel<<<2 * ((n + 63) / 64), kMarkovThreads, 0, stream>>>(p, b, tc);
+    if (tc) return markov_tc_launch(p, b, stream);
     const bool g16 = p.gdt == SPEC_BF16, w16 = p.wdt == SPEC_BF16;
     if (g16 && w16) markov_typed<bf16_t, bf16_t>(p, b, stream);
     else if (g16) markov_typed<bf16_t, float>(p, b, stream);

@@ -1,0 +1,381 @@
+// markov_tc.cu - spec_markov_grad's two products on the tcgen05 tensor cores (bf16 operands).
+//
+//     WT:  dWt [V, r] = dz^T Ux     a tile of 256 entries, contraction over the rows
+//     DX:  dX  [n, r] = dz Wt       a tile of 256 rows, contraction over the vocabulary
+// Both are one kernel over items (an output tile and a range of 64-term steps).  A pair of CTAs
+// forms a tile with cta_group::2 (M = 256, N = r up to 128 or 256): each CTA brings its 128 rows
+// of A and half of B's columns, so B crosses from L2 once per pair, and the accumulator's
+// two halves lie in the two CTAs' TMEM.  Per CTA, 19 warps:
+//   warp 0   TMA producer: [64 x 64] boxes (128-byte swizzle) into a ring of stages.  dz is stored
+//            with the vocabulary contiguous: as WT's A it is M-major, as DX's K-major, from the
+//            same boxes; Ux and Wt are N-major.
+//   warp 1   TMEM; in the pair's first CTA the MMA issuer
+//   warp 2   relay: a stage that has arrived here is reported to the first CTA's issuer, after the
+//            rows without a token (whose dz may hold anything) have been set to 0 (WT)
+//   warps 3-18  epilogue: a thread owns one row and a quarter of the columns
+// A tensor core's sums drop what falls below the accumulator's last bit, so a chain of steps
+// ends after kMtcChunk of them: the epilogue adds it to float32 registers while the next one runs
+// in the other half of TMEM.
+#include "markov.cuh"
+#include "tc_common.cuh"
+
+namespace spec {
+
+constexpr int kMtcStep = 64;                       // terms of a stage
+constexpr int kMtcBox = kMtcStep * 64 * 2;         // bytes of a [64 x 64] box
+constexpr int kMtcChunk = 32;                      // steps that one accumulator takes
+constexpr int kMtcEpi = 16;
+constexpr int kMtcThreads = 32 * (3 + kMtcEpi);
+
+template <int NT> struct Mtc {                     // NT: columns, r rounded up to 128 or 256
+    static constexpr int boxes = 2 + NT / 128;     // of a stage: A 128 x 64, B 64 x NT / 2
+    static constexpr int bytes = boxes * kMtcBox;
+    static constexpr int stages = NT == 256 ? 6 : 8;
+    static constexpr uint32_t tmem = 2 * NT;
+    static constexpr int smem = stages * bytes + 1024;
+};
+
+// Shared-memory descriptor of an operand whose M or N runs along the 128 bytes of a swizzled row:
+// 64-entry blocks a box apart (leading offset), groups of 8 terms 1024 bytes apart (stride offset).
+__device__ __forceinline__ uint64_t sw128_mn_desc(uint32_t saddr) {
+    return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)(kMtcBox >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+           (1ull << 46) | (2ull << 61);
+}
+
+__device__ __forceinline__ uint32_t peer_addr(const void* p, unsigned rank) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+    return a;
+}
+__device__ __forceinline__ void remote_arrive(uint64_t* bar, unsigned rank) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" :: "r"(peer_addr(bar, rank)) : "memory");
+}
+__device__ __forceinline__ bool cluster_try_wait(uint64_t* bar, unsigned parity) {
+    uint32_t ok;
+    asm volatile("{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+                 " selp.u32 %0, 1, 0, p;\n}" : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity) : "memory");
+    return ok != 0;
+}
+// A wait for what either CTA of the pair does; false when it ran out.
+__device__ __forceinline__ bool pair_wait(uint64_t* bar, unsigned parity, unsigned* status) {
+    if (cluster_try_wait(bar, parity)) return true;
+    const unsigned long long t0 = global_timer_ns();
+    while (!cluster_try_wait(bar, parity)) {
+        if (global_timer_ns() - t0 > kWaitLimitNs) {
+            atomicOr(status, SPEC_DEV_TIMEOUT);
+            return false;
+        }
+    }
+    return true;
+}
+__device__ __forceinline__ void pair_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void umma2_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n"
+        :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
+}
+// One arrival at this barrier of `ctas` (a bit each) when every MMA issued so far completes.
+__device__ __forceinline__ void umma2_commit(uint64_t* bar, unsigned short ctas = 3) {
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+                 :: "r"(smem_u32(bar)), "h"(ctas) : "memory");
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
+    uint32_t r[16];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+                 "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+                 : "r"(taddr));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// 8 values of a row, 16 bytes of bf16 or 32 of float32 (r is a multiple of 8).
+__device__ __forceinline__ void put8(void* o, int dtype, long at, const float* x) {
+    if (dtype == SPEC_BF16) {
+        uint32_t h[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(h[k]) : "f"(x[2 * k + 1]), "f"(x[2 * k]));
+        *reinterpret_cast<uint4*>(reinterpret_cast<bf16_t*>(o) + at) = make_uint4(h[0], h[1], h[2], h[3]);
+    } else {
+        float4* q = reinterpret_cast<float4*>(reinterpret_cast<float*>(o) + at);
+        q[0] = make_float4(x[0], x[1], x[2], x[3]);
+        q[1] = make_float4(x[4], x[5], x[6], x[7]);
+    }
+}
+
+// Item `it` of a pair: its tile and its steps [k0, k1).
+struct MtcItem { int tile, k0, k1; };
+template <bool DX>
+__device__ __forceinline__ bool mtc_item(const MarkovTc& a, int pair, int it, MtcItem& o) {
+    if (!DX) {   // whole tiles, one in a_pairs
+        o.tile = pair + it * a.pairs;
+        o.k0 = 0;
+        o.k1 = a.steps;
+        return o.tile < a.tiles;
+    }
+    // the pair's share of all tiles' steps, cut where a tile ends
+    const long lo = mtc_begin(a, pair), hi = mtc_begin(a, pair + 1);
+    const long first = lo / a.steps + it;
+    if (lo >= hi || first * a.steps >= hi) return false;
+    o.tile = (int)first;
+    o.k0 = (int)(it == 0 ? lo - first * a.steps : 0);
+    o.k1 = (int)min((long)a.steps, hi - first * a.steps);
+    return true;
+}
+
+template <bool DX, int NT>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMtcThreads, 1)
+    markov_tc_kernel(const __grid_constant__ MarkovParams p, const __grid_constant__ MarkovBind b,
+                     const __grid_constant__ MarkovTc a, const __grid_constant__ CUtensorMap zmap,
+                     const __grid_constant__ CUtensorMap bmap) {
+    typedef Mtc<NT> C;
+    constexpr int S = C::stages;
+    extern __shared__ uint8_t mtc_raw[];
+    uint8_t* ring = mtc_raw + ((1024u - (smem_u32(mtc_raw) & 1023u)) & 1023u);
+    __shared__ __align__(8) uint64_t s_full[S], s_ready[S], s_empty[S], s_tfull[2], s_tempty[2], s_drain;
+    __shared__ uint32_t s_tmem;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const unsigned rank = blockIdx.x & 1u;
+    const int pair = (int)(blockIdx.x >> 1);
+    // DX: rows of tile t from 256 t on; WT: entries
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; ++s) {
+            mbar_init(&s_full[s], 1);
+            mbar_init(&s_ready[s], 2);
+            mbar_init(&s_empty[s], 1);
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&s_tfull[s], 1);
+            mbar_init(&s_tempty[s], 2 * kMtcEpi);
+        }
+        mbar_init(&s_drain, 1);
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;"
+                     :: "r"(smem_u32(&s_tmem)), "r"(C::tmem) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    pair_sync();
+    tc_fence_after();
+    const uint32_t tmem = s_tmem;
+    MtcItem item;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            uint32_t i = 0;
+            bool ok = true;
+            for (int it = 0; ok && mtc_item<DX>(a, pair, it, item); ++it) {
+                const int m0 = item.tile * 256 + (int)rank * 128;
+                for (int k = item.k0; k < item.k1; ++k, ++i) {
+                    const uint32_t s = i % S;
+                    ok = pair_wait(&s_empty[s], ((i / S) & 1u) ^ 1u, b.status);
+                    if (!ok) break;
+                    uint8_t* d = ring + (size_t)s * C::bytes;
+                    mbar_arrive_expect_tx(&s_full[s], C::bytes);
+                    if (DX) {
+                        tma_load_2d(d, &zmap, k * kMtcStep, m0, &s_full[s]);
+                        tma_load_2d(d + kMtcBox, &zmap, k * kMtcStep, m0 + 64, &s_full[s]);
+                    } else {
+                        tma_load_2d(d, &zmap, m0, k * kMtcStep, &s_full[s]);
+                        tma_load_2d(d + kMtcBox, &zmap, m0 + 64, k * kMtcStep, &s_full[s]);
+                    }
+#pragma unroll
+                    for (int j = 0; j < NT / 128; ++j)
+                        tma_load_2d(d + (2 + j) * kMtcBox, &bmap, (int)rank * (NT / 2) + j * 64, k * kMtcStep, &s_full[s]);
+                }
+            }
+            // nothing may still be on its way when the CTA ends, a copy or the issuer's arrival
+            for (uint32_t q = i > S ? i - S : 0; q < i; ++q) {
+                mbar_wait(&s_full[q % S], (q / S) & 1u, b.status, kWaitLimitNs);
+                ok = ok && pair_wait(&s_empty[q % S], (q / S) & 1u, b.status);
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0 && rank == 0) {
+            // M = 256 over the pair; B N-major, A M-major in WT
+            constexpr uint32_t idesc = idesc_bf16_f32(256, NT) | (1u << 16) | (DX ? 0u : 1u << 15);
+            uint32_t i = 0, c = 0;
+            bool ok = true;
+            for (int it = 0; ok && mtc_item<DX>(a, pair, it, item); ++it) {
+                for (int k = item.k0; ok && k < item.k1; ++c) {
+                    const uint32_t buf = c & 1u, d = tmem + buf * NT;
+                    ok = pair_wait(&s_tempty[buf], ((c >> 1) & 1u) ^ 1u, b.status);
+                    const int end = min(item.k1, k + kMtcChunk);
+                    tc_fence_after();
+                    for (bool first = true; ok && k < end; ++k, ++i, first = false) {
+                        const uint32_t s = i % S;
+                        ok = pair_wait(&s_ready[s], (i / S) & 1u, b.status);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint32_t sa = smem_u32(ring + (size_t)s * C::bytes), sb = sa + 2 * kMtcBox;
+#pragma unroll
+                        for (int q = 0; q < kMtcStep / 16; ++q) {
+                            const uint64_t da = DX ? sw128_desc(sa + q * 32) : sw128_mn_desc(sa + q * 2048);
+                            umma2_f16(d, da, sw128_mn_desc(sb + q * 2048), idesc, first && q == 0 ? 0u : 1u);
+                        }
+                        umma2_commit(&s_empty[s]);
+                    }
+                    umma2_commit(&s_tfull[buf]);
+                }
+            }
+            umma2_commit(&s_drain, 1);
+            pair_wait(&s_drain, 0, b.status);
+        }
+    } else if (warp == 2) {
+        uint32_t i = 0;
+        bool ok = true;
+        for (int it = 0; ok && mtc_item<DX>(a, pair, it, item); ++it) {
+            for (int k = item.k0; k < item.k1; ++k, ++i) {
+                const uint32_t s = i % S;
+                ok = mbar_wait(&s_full[s], (i / S) & 1u, b.status, kWaitLimitNs);
+                if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+                if (!DX) {
+                    unsigned long long none = b.none[k];   // rows of the step without a token
+                    if (none) {
+                        uint4* z = reinterpret_cast<uint4*>(ring + (size_t)s * C::bytes);
+                        for (; none; none &= none - 1) {   // a row is 8 words of each of the two boxes
+                            const int row = __ffsll((long long)none) - 1;
+                            if (lane < 16) z[(lane >> 3) * (kMtcBox / 16) + row * 8 + (lane & 7)] = make_uint4(0u, 0u, 0u, 0u);
+                        }
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                    }
+                }
+                if (lane == 0) remote_arrive(&s_ready[s], 0);
+            }
+        }
+    } else {
+        constexpr int W = NT / 4;                          // columns of a thread
+        const int quad = warp & 3, group = (warp - 3) >> 2;
+        const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16) + group * W;
+        uint32_t c = 0;
+        bool ok = true;
+        for (int it = 0; ok && mtc_item<DX>(a, pair, it, item); ++it) {
+            float acc[W];
+#pragma unroll
+            for (int q = 0; q < W; ++q) acc[q] = 0.0f;
+            for (int k = item.k0; ok && k < item.k1; k += kMtcChunk, ++c) {
+                const uint32_t buf = c & 1u;
+                ok = pair_wait(&s_tfull[buf], (c >> 1) & 1u, b.status);
+                if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+                tc_fence_after();
+#pragma unroll
+                for (int q = 0; q < W; q += 16) {
+                    float v[16];
+                    tmem_ld16(lane_base + buf * NT + q, v);
+#pragma unroll
+                    for (int h = 0; h < 16; ++h) acc[q + h] += v[h];
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) remote_arrive(&s_tempty[buf], 0);
+            }
+            if (!ok) break;
+            const int m = (int)rank * 128 + quad * 32 + lane, k0 = group * W;
+            if (DX) {
+                float* o = b.dx + ((size_t)(pair + item.tile) * 256 + m) * NT + k0;
+#pragma unroll
+                for (int q = 0; q < W; q += 4)
+                    *reinterpret_cast<float4*>(o + q) = make_float4(acc[q], acc[q + 1], acc[q + 2], acc[q + 3]);
+            } else {
+                const int v = item.tile * 256 + m;
+                if (v < p.V) {
+                    const float zero[8] = {};
+#pragma unroll
+                    for (int q = 0; q < W; q += 8)
+                        if (k0 + q < p.r) {
+                            put8(p.dWt_out, p.odt, (long)v * p.r + k0 + q, acc + q);
+                            put8(p.dU_out, p.odt, (long)v * p.r + k0 + q, zero);
+                        }
+                }
+            }
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    pair_sync();   // nobody's barriers or TMEM are in use any more
+    if (warp == 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" :: "r"(tmem), "r"(C::tmem) : "memory");
+    }
+}
+
+// dU's rows from the parts of dX: the CTA at a token's first place among the ordered rows.
+__global__ void __launch_bounds__(256) markov_tc_u_kernel(MarkovParams p, MarkovBind b, MarkovTc a, int NT) {
+    const int n = p.B * p.gamma, at = blockIdx.x;
+    const int t = b.token[at];
+    if (t >= p.V || (at > 0 && b.token[at - 1] == t)) return;
+    for (int k = threadIdx.x; k < p.r; k += 256) {
+        float s = 0.0f;
+        for (int q = at; q < n && b.token[q] == t; ++q) {
+            const int i = b.order[q], tile = i >> 8;
+            const long lo = (long)tile * a.steps, hi = lo + a.steps - 1;
+            const int p0 = mtc_pair_of(a, lo), p1 = mtc_pair_of(a, hi);
+            float x = 0.0f;
+#pragma unroll 4
+            for (int pr = p0; pr <= p1; ++pr) x += b.dx[((size_t)(pr + tile) * 256 + (i & 255)) * NT + k];
+            s += x;
+        }
+        put(p.dU_out, p.odt, (long)t * p.r + k, s);
+    }
+}
+
+static bool mtc_map(CUtensorMap* m, const void* base, int width, long rows, long pitch_bytes) {
+    const cuuint64_t dims[2] = {(cuuint64_t)width, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)pitch_bytes};
+    const cuuint32_t box[2] = {64, 64};
+    const cuuint32_t estr[2] = {1, 1};
+    EncodeTiledFn f = encode_tiled();
+    return f && f(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int NT>
+static cudaError_t mtc_launch(const MarkovParams& p, const MarkovBind& b, cudaStream_t stream) {
+    const int n = p.B * p.gamma;
+    CUtensorMap zmap, umap, wmap;
+    // one row: its pitch is not used, but has to be whole 16-byte words
+    const long pitch = n > 1 ? (long)p.ld * 2 : ((long)p.ld * 2 + 15) / 16 * 16;
+    if (!mtc_map(&zmap, p.grad, p.V, n, pitch) || !mtc_map(&umap, b.ux, p.r, n, (long)p.r * 2) ||
+        !mtc_map(&wmap, p.Wt, p.r, p.V, (long)p.r * 2))
+        return cudaErrorInvalidValue;
+    int sms = device_sm_count();
+    if (sms > 2 * kMarkovPairs) sms = 2 * kMarkovPairs;
+    MarkovTc wt, dx;
+    wt.tiles = (p.V + 255) / 256;
+    wt.steps = (n + kMtcStep - 1) / kMtcStep;
+    wt.pairs = wt.tiles < sms / 2 ? wt.tiles : sms / 2;
+    dx.tiles = (n + 255) / 256;
+    dx.steps = (p.V + kMtcStep - 1) / kMtcStep;
+    const long units = (long)dx.tiles * dx.steps;
+    dx.pairs = units < sms / 2 ? (int)units : sms / 2;
+    auto kw = markov_tc_kernel<false, NT>;
+    auto kx = markov_tc_kernel<true, NT>;
+    cudaError_t e = cudaFuncSetAttribute(kw, cudaFuncAttributeMaxDynamicSharedMemorySize, Mtc<NT>::smem);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(kx, cudaFuncAttributeMaxDynamicSharedMemorySize, Mtc<NT>::smem);
+    if (e != cudaSuccess) return e;
+    kw<<<2 * wt.pairs, kMtcThreads, Mtc<NT>::smem, stream>>>(p, b, wt, zmap, umap);
+    kx<<<2 * dx.pairs, kMtcThreads, Mtc<NT>::smem, stream>>>(p, b, dx, zmap, wmap);
+    markov_tc_u_kernel<<<n, 256, 0, stream>>>(p, b, dx, NT);
+    return cudaGetLastError();
+}
+
+bool markov_tc_supported(const MarkovParams& p) {
+    return p.gdt == SPEC_BF16 && p.wdt == SPEC_BF16 && p.r % 8 == 0 && (p.ld % 8 == 0 || p.B * p.gamma == 1);
+}
+
+cudaError_t markov_tc_launch(const MarkovParams& p, const MarkovBind& b, cudaStream_t stream) {
+    return p.r > 128 ? mtc_launch<256>(p, b, stream) : mtc_launch<128>(p, b, stream);
+}
+
+}  // namespace spec
