@@ -25,57 +25,63 @@ static int markov_parts(int n, int r, int V, int sms) {
     return parts < 1 ? 1 : (parts > kMarkovMaxParts ? kMarkovMaxParts : parts);
 }
 
-// Row i's place among the rows by (token, row), counted: n comparisons a row, 8 lanes a row.
+constexpr int kOrderTile = 2048;                 // tokens compared at a time
+
+// Row i's place among the rows by (token, row), counted: n comparisons a row, a warp a row.  With
+// `gather` a second half of the grid copies the rows U[x_i] and marks the rows without a token.
 __global__ void __launch_bounds__(kMarkovThreads) markov_order_kernel(MarkovParams p, MarkovBind b, bool gather) {
-    __shared__ int32_t s_tok[1024];
-    __shared__ unsigned s_bits[8];
-    const int n = p.B * p.gamma;
+    __shared__ int32_t s_tok[kOrderTile];
+    const int n = p.B * p.gamma, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     auto token_of = [&](int i, bool* bad) {
         const int q = i / p.gamma, j = i - q * p.gamma;
         const int t = j == 0 ? p.anchor[q] : p.tokens[(long)q * p.gamma + j - 1];
         if (t < -1 || t >= p.V) *bad = true;
         return t < 0 || t >= p.V ? p.V : t;
     };
-    const int sub = threadIdx.x & 7, i = blockIdx.x * (kMarkovThreads / 8) + (threadIdx.x >> 3);
     bool bad = false;
+    const int rows = kMarkovThreads / 32, ranks = (n + rows - 1) / rows;
+    if ((int)blockIdx.x >= ranks) {   // (a CTA of 64 rows, so that it has a whole word of marks)
+        const int i0 = ((int)blockIdx.x - ranks) * 64;
+        if (warp == 0) {
+            const unsigned lo = __ballot_sync(0xffffffffu, i0 + lane < n && token_of(i0 + lane, &bad) >= p.V);
+            const unsigned hi = __ballot_sync(0xffffffffu, i0 + 32 + lane < n && token_of(i0 + 32 + lane, &bad) >= p.V);
+            if (lane == 0) b.none[i0 >> 6] = (unsigned long long)hi << 32 | lo;
+        }
+        for (int i = i0 + warp; i < min(n, i0 + 64); i += rows) {
+            const int t = token_of(i, &bad);
+            const uint4* u = reinterpret_cast<const uint4*>(reinterpret_cast<const bf16_t*>(p.U) + (long)t * p.r);
+            uint4* o = reinterpret_cast<uint4*>(b.ux + (long)i * p.r);
+            if (lane < p.r / 8) o[lane] = t < p.V ? __ldg(u + lane) : make_uint4(0u, 0u, 0u, 0u);
+        }
+        return;
+    }
+    const int i = blockIdx.x * rows + warp;
     const int mine = i < n ? token_of(i, &bad) : 0;
-    bool other = false;
+    if (bad && lane == 0) atomicOr(b.status, SPEC_DEV_TOKEN);
     int rank = 0;
-    for (int lo = 0; lo < n; lo += 1024) {
+    for (int lo = 0; lo < n; lo += kOrderTile) {
         __syncthreads();
-        for (int k = threadIdx.x; k < 1024; k += kMarkovThreads) s_tok[k] = lo + k < n ? token_of(lo + k, &other) : 0x7fffffff;
+#pragma unroll
+        for (int k = threadIdx.x; k < kOrderTile; k += kMarkovThreads)
+            if (lo + k < n) s_tok[k] = token_of(lo + k, &bad);
         __syncthreads();
-        const int m = min(1024, n - lo);
-        for (int k = sub; k < m; k += 8) {
+        const int m = min(kOrderTile, n - lo);
+#pragma unroll 4
+        for (int k = lane; k < m; k += 32) {
             const int t = s_tok[k];
             rank += t < mine || (t == mine && lo + k < i) ? 1 : 0;
         }
     }
-#pragma unroll
-    for (int o = 1; o < 8; o <<= 1) rank += __shfl_xor_sync(0xffffffffu, rank, o);
-    if (i < n && sub == 0) {
+    rank = (int)__reduce_add_sync(0xffffffffu, (unsigned)rank);
+    if (i < n && lane == 0) {
         b.order[rank] = i;
         b.token[rank] = mine;
         b.of_row[i] = mine;
-        if (bad) atomicOr(b.status, SPEC_DEV_TOKEN);
     }
-    if (!gather) return;
-    // the rows without a token, a CTA's 32 rows a half word of their step's 64
-    const unsigned any = __ballot_sync(0xffffffffu, i < n && mine >= p.V);
-    unsigned bits = 0u;
-#pragma unroll
-    for (int q = 0; q < 4; ++q) bits |= ((any >> (8 * q)) & 1u) << q;
-    if ((threadIdx.x & 31) == 0) s_bits[threadIdx.x >> 5] = bits;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        unsigned w = 0u;
-        for (int q = 0; q < 8; ++q) w |= s_bits[q] << (4 * q);
-        reinterpret_cast<unsigned*>(b.none)[blockIdx.x] = w;
-    }
-    if (i >= n) return;
-    const uint4* u = reinterpret_cast<const uint4*>(reinterpret_cast<const bf16_t*>(p.U) + (long)mine * p.r);
-    uint4* o = reinterpret_cast<uint4*>(b.ux + (long)i * p.r);
-    for (int k = sub; k < p.r / 8; k += 8) o[k] = mine < p.V ? __ldg(u + k) : make_uint4(0u, 0u, 0u, 0u);
+}
+static void markov_order(const MarkovParams& p, const MarkovBind& b, bool gather, cudaStream_t stream) {
+    const int n = p.B * p.gamma, rows = kMarkovThreads / 32;
+    markov_order_kernel<<<(n + rows - 1) / rows + (gather ? (n + 63) / 64 : 0), kMarkovThreads, 0, stream>>>(p, b, gather);
 }
 
 // A 64 x 64 tile of sums on CUDA cores, 4 x 4 outputs a thread: s_a[step][a], s_b[step][b].
@@ -150,27 +156,49 @@ __global__ void __launch_bounds__(kMarkovThreads) markov_dx_kernel(MarkovParams 
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
             const int i = i0 + ty * 4 + h, k = k0 + tx * 4 + w;
-            if (i < n && k < p.r) b.dx[((long)part * n + i) * p.r + k] = acc[h][w];
+            if (i < n && k < markov_pitch(p.r)) b.dx[((long)part * n + i) * markov_pitch(p.r) + k] = acc[h][w];
         }
 }
 
-// dU's rows: the CTA at a token's first place among the ordered rows sums that token's.
-__global__ void __launch_bounds__(kMarkovThreads) markov_u_kernel(MarkovParams p, MarkovBind b) {
+// dU's rows: the CTA at a token's first place among the ordered rows joins that token's.  Its terms
+// are (row, part) in order; 16-byte columns go over lanes and the terms over groups of threads, whose
+// sums meet in order.
+constexpr int kJoinThreads = 512;
+__global__ void __launch_bounds__(kJoinThreads) markov_join_kernel(MarkovParams p, MarkovBind b, MarkovJoin a) {
+    __shared__ float4 s_sum[kJoinThreads];
     const int n = p.B * p.gamma, at = blockIdx.x;
     const int t = b.token[at];
     if (t >= p.V || (at > 0 && b.token[at - 1] == t)) return;
-    int end = at + 1;
-    while (end < n && b.token[end] == t) ++end;
-    for (int k = threadIdx.x; k < p.r; k += kMarkovThreads) {
-        float s = 0.0f;
-        for (int q = at; q < end; ++q) {
-            const long i = b.order[q];
-            float x = 0.0f;
-            for (int part = 0; part < b.parts; ++part) x += b.dx[((long)part * n + i) * p.r + k];
-            s += x;
-        }
-        put(p.dU_out, p.odt, (long)t * p.r + k, s);
+    int end = n;   // the last row of this token, found by halves: tokens are in order
+    for (int lo = at + 1; lo < end;) {
+        const int mid = (lo + end) >> 1;
+        if (b.token[mid] == t) lo = mid + 1; else end = mid;
     }
+    const int quads = (p.r + 3) / 4, groups = kJoinThreads / quads;
+    const int k = threadIdx.x % quads, g = threadIdx.x / quads;
+    const int terms = (end - at) * a.parts;
+    float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (g < groups) {
+        const int lo = (int)((long)terms * g / groups), hi = (int)((long)terms * (g + 1) / groups);
+#pragma unroll 8
+        for (int e = lo; e < hi; ++e) {
+            const int q = e / a.parts, part = e - q * a.parts, i = b.order[at + q];
+            const float4 x = *reinterpret_cast<const float4*>(b.dx + (part * a.part_stride + i) * a.pitch + 4 * k);
+            s.x += x.x; s.y += x.y; s.z += x.z; s.w += x.w;
+        }
+        s_sum[g * quads + k] = s;
+    }
+    __syncthreads();
+    if (g != 0) return;
+    for (int q = 1; q < groups; ++q) {
+        const float4 x = s_sum[q * quads + k];
+        s.x += x.x; s.y += x.y; s.z += x.z; s.w += x.w;
+    }
+    const float o[4] = {s.x, s.y, s.z, s.w};
+    for (int h = 0; h < 4 && 4 * k + h < p.r; ++h) put(p.dU_out, p.odt, (long)t * p.r + 4 * k + h, o[h]);
+}
+void markov_join(const MarkovParams& p, const MarkovBind& b, const MarkovJoin& a, cudaStream_t stream) {
+    markov_join_kernel<<<p.B * p.gamma, kJoinThreads, 0, stream>>>(p, b, a);
 }
 
 static size_t markov_bind(MarkovBind& b, void* ws, int n, int r, int V) {
@@ -188,9 +216,10 @@ static size_t markov_bind(MarkovBind& b, void* ws, int n, int r, int V) {
     b.ux = reinterpret_cast<bf16_t*>(w + at);
     at += align256((size_t)n * r * 2);
     b.dx = reinterpret_cast<float*>(w + at);
-    const size_t plain = (size_t)b.parts * n * r * 4;
-    const size_t pairs = (size_t)(kMarkovPairs + (n + 255) / 256) * 256 * (r > 128 ? 256 : 128) * 4;
-    at += align256(plain > pairs ? plain : pairs);
+    const size_t plain = (size_t)b.parts * n * markov_pitch(r) * 4;
+    const MarkovTc dx = markov_tc_dx(n, V);
+    const size_t tiles = (size_t)dx.tiles * dx.parts * 256 * (r > 128 ? 256 : 128) * 4;
+    at += align256(plain > tiles ? plain : tiles);
     return at;
 }
 
@@ -214,15 +243,14 @@ cudaError_t markov_grad_launch(const MarkovParams& p, void* ws, cudaStream_t str
     b.parts = markov_parts(n, p.r, p.V, 152);
     markov_bind(b, ws, n, p.r, p.V);
     const bool tc = markov_tc_supported(p);
-    // (a CTA's rows are half a step's: both halves' words are written)
-    markov_order_kernel<<<2 * ((n + 63) / 64), kMarkovThreads, 0, stream>>>(p, b, tc);
+    markov_order(p, b, tc, stream);
     if (tc) return markov_tc_launch(p, b, stream);
     const bool g16 = p.gdt == SPEC_BF16, w16 = p.wdt == SPEC_BF16;
     if (g16 && w16) markov_typed<bf16_t, bf16_t>(p, b, stream);
     else if (g16) markov_typed<bf16_t, float>(p, b, stream);
     else if (w16) markov_typed<float, bf16_t>(p, b, stream);
     else markov_typed<float, float>(p, b, stream);
-    markov_u_kernel<<<n, kMarkovThreads, 0, stream>>>(p, b);
+    markov_join(p, b, {b.parts, n, markov_pitch(p.r)}, stream);
     return cudaGetLastError();
 }
 

@@ -19,20 +19,11 @@ struct MarkovBind {
     int parts;
 };
 
-// A tensor-core product's items: tiles of 256 outputs over `steps` steps each, dealt to pairs.
-struct MarkovTc { int tiles, steps, pairs; };
-// The contraction over the vocabulary has few tiles, so all their steps in a line are cut into equal
-// shares: pair q has steps [mtc_begin(q), mtc_begin(q + 1)), and its part of a tile is kept at place
-// q + tile.
-__host__ __device__ inline long mtc_begin(const MarkovTc& a, int q) { return (long)a.tiles * a.steps * q / a.pairs; }
-__host__ __device__ inline int mtc_pair_of(const MarkovTc& a, long step) {   // the pair whose share step is in
-    const long all = (long)a.tiles * a.steps;
-    int q = (int)((step * a.pairs + a.pairs - 1) / all);
-    if (q > a.pairs - 1) q = a.pairs - 1;
-    while (q > 0 && mtc_begin(a, q) > step) --q;
-    while (q + 1 < a.pairs && mtc_begin(a, q + 1) <= step) ++q;
-    return q;
-}
+// A tensor-core product's items: tiles of 256 outputs, each in `parts` ranges of its steps.  Item
+// i is part i / tiles of tile i % tiles, and the pairs take them in order, so the tiles that
+// run at the same time go through the same steps and read B's rows from memory once.
+struct MarkovTc { int tiles, steps, parts; };
+__host__ __device__ inline int mtc_begin(const MarkovTc& a, int part) { return (int)((long)a.steps * part / a.parts); }
 
 template <typename T> __device__ __forceinline__ void put(void* o, long i, float x);
 template <> __device__ __forceinline__ void put<float>(void* o, long i, float x) { reinterpret_cast<float*>(o)[i] = x; }
@@ -44,6 +35,12 @@ __device__ __forceinline__ void put(void* o, int dtype, long i, float x) {
     else put<float>(o, i, x);
 }
 
+// Where the join finds row i's part: dx[(part * part_stride + i) * pitch], 16 bytes aligned.
+struct MarkovJoin { int parts; long part_stride; int pitch; };
+__host__ __device__ inline int markov_pitch(int r) { return (r + 3) & ~3; }
+void markov_join(const MarkovParams& p, const MarkovBind& b, const MarkovJoin& a, cudaStream_t stream);
+
+MarkovTc markov_tc_dx(int n, int V);
 bool markov_tc_supported(const MarkovParams& p);
 cudaError_t markov_tc_launch(const MarkovParams& p, const MarkovBind& b, cudaStream_t stream);
 

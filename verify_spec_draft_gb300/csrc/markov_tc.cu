@@ -30,9 +30,11 @@ constexpr int kMtcThreads = 32 * (3 + kMtcEpi);
 template <int NT> struct Mtc {                     // NT: columns, r rounded up to 128 or 256
     static constexpr int boxes = 2 + NT / 128;     // of a stage: A 128 x 64, B 64 x NT / 2
     static constexpr int bytes = boxes * kMtcBox;
-    static constexpr int stages = NT == 256 ? 6 : 8;
+    static constexpr int stages = NT == 256 ? 6 : 7;
     static constexpr uint32_t tmem = 2 * NT;
-    static constexpr int smem = stages * bytes + 1024;
+    static constexpr int scratch = kMtcEpi * 2048;
+    static constexpr int smem = stages * bytes + scratch + 1024;
+    static_assert(smem + 512 <= 227 * 1024, "shared memory");
 };
 
 // Shared-memory descriptor of an operand whose M or N runs along the 128 bytes of a swizzled row:
@@ -48,11 +50,11 @@ __device__ __forceinline__ uint32_t peer_addr(const void* p, unsigned rank) {
     return a;
 }
 __device__ __forceinline__ void remote_arrive(uint64_t* bar, unsigned rank) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" :: "r"(peer_addr(bar, rank)) : "memory");
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" :: "r"(peer_addr(bar, rank)) : "memory");
 }
 __device__ __forceinline__ bool cluster_try_wait(uint64_t* bar, unsigned parity) {
     uint32_t ok;
-    asm volatile("{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+    asm volatile("{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
                  " selp.u32 %0, 1, 0, p;\n}" : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity) : "memory");
     return ok != 0;
 }
@@ -95,38 +97,15 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
     for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-// 8 values of a row, 16 bytes of bf16 or 32 of float32 (r is a multiple of 8).
-__device__ __forceinline__ void put8(void* o, int dtype, long at, const float* x) {
-    if (dtype == SPEC_BF16) {
-        uint32_t h[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(h[k]) : "f"(x[2 * k + 1]), "f"(x[2 * k]));
-        *reinterpret_cast<uint4*>(reinterpret_cast<bf16_t*>(o) + at) = make_uint4(h[0], h[1], h[2], h[3]);
-    } else {
-        float4* q = reinterpret_cast<float4*>(reinterpret_cast<float*>(o) + at);
-        q[0] = make_float4(x[0], x[1], x[2], x[3]);
-        q[1] = make_float4(x[4], x[5], x[6], x[7]);
-    }
-}
-
-// Item `it` of a pair: its tile and its steps [k0, k1).
-struct MtcItem { int tile, k0, k1; };
-template <bool DX>
-__device__ __forceinline__ bool mtc_item(const MarkovTc& a, int pair, int it, MtcItem& o) {
-    if (!DX) {   // whole tiles, one in a_pairs
-        o.tile = pair + it * a.pairs;
-        o.k0 = 0;
-        o.k1 = a.steps;
-        return o.tile < a.tiles;
-    }
-    // the pair's share of all tiles' steps, cut where a tile ends
-    const long lo = mtc_begin(a, pair), hi = mtc_begin(a, pair + 1);
-    const long first = lo / a.steps + it;
-    if (lo >= hi || first * a.steps >= hi) return false;
-    o.tile = (int)first;
-    o.k0 = (int)(it == 0 ? lo - first * a.steps : 0);
-    o.k1 = (int)min((long)a.steps, hi - first * a.steps);
-    return true;
+// Item `it` of a pair: its tile, its steps [k0, k1) and its number.
+struct MtcItem { int tile, k0, k1, number; };
+__device__ __forceinline__ bool mtc_item(const MarkovTc& a, int it, MtcItem& o) {
+    o.number = (int)(blockIdx.x >> 1) + it * (int)(gridDim.x >> 1);
+    const int part = o.number / a.tiles;
+    o.tile = o.number - part * a.tiles;
+    o.k0 = mtc_begin(a, part);
+    o.k1 = mtc_begin(a, part + 1);
+    return part < a.parts;
 }
 
 template <bool DX, int NT>
@@ -142,8 +121,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMtcThreads, 1)
     __shared__ uint32_t s_tmem;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const unsigned rank = blockIdx.x & 1u;
-    const int pair = (int)(blockIdx.x >> 1);
-    // DX: rows of tile t from 256 t on; WT: entries
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
             mbar_init(&s_full[s], 1);
@@ -173,7 +150,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMtcThreads, 1)
         if (lane == 0) {
             uint32_t i = 0;
             bool ok = true;
-            for (int it = 0; ok && mtc_item<DX>(a, pair, it, item); ++it) {
+            for (int it = 0; ok && mtc_item(a, it, item); ++it) {
                 const int m0 = item.tile * 256 + (int)rank * 128;
                 for (int k = item.k0; k < item.k1; ++k, ++i) {
                     const uint32_t s = i % S;
@@ -205,7 +182,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMtcThreads, 1)
             constexpr uint32_t idesc = idesc_bf16_f32(256, NT) | (1u << 16) | (DX ? 0u : 1u << 15);
             uint32_t i = 0, c = 0;
             bool ok = true;
-            for (int it = 0; ok && mtc_item<DX>(a, pair, it, item); ++it) {
+            for (int it = 0; ok && mtc_item(a, it, item); ++it) {
                 for (int k = item.k0; ok && k < item.k1; ++c) {
                     const uint32_t buf = c & 1u, d = tmem + buf * NT;
                     ok = pair_wait(&s_tempty[buf], ((c >> 1) & 1u) ^ 1u, b.status);
@@ -233,7 +210,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMtcThreads, 1)
     } else if (warp == 2) {
         uint32_t i = 0;
         bool ok = true;
-        for (int it = 0; ok && mtc_item<DX>(a, pair, it, item); ++it) {
+        for (int it = 0; ok && mtc_item(a, it, item); ++it) {
             for (int k = item.k0; k < item.k1; ++k, ++i) {
                 const uint32_t s = i % S;
                 ok = mbar_wait(&s_full[s], (i / S) & 1u, b.status, kWaitLimitNs);
@@ -259,7 +236,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMtcThreads, 1)
         const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16) + group * W;
         uint32_t c = 0;
         bool ok = true;
-        for (int it = 0; ok && mtc_item<DX>(a, pair, it, item); ++it) {
+        for (int it = 0; ok && mtc_item(a, it, item); ++it) {
             float acc[W];
 #pragma unroll
             for (int q = 0; q < W; ++q) acc[q] = 0.0f;
@@ -280,23 +257,57 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMtcThreads, 1)
                 if (lane == 0) remote_arrive(&s_tempty[buf], 0);
             }
             if (!ok) break;
-            const int m = (int)rank * 128 + quad * 32 + lane, k0 = group * W;
+            const int k0 = group * W;
             if (DX) {
-                float* o = b.dx + ((size_t)(pair + item.tile) * 256 + m) * NT + k0;
+                const int m = (int)rank * 128 + quad * 32 + lane;
+                float* o = b.dx + ((size_t)item.number * 256 + m) * NT + k0;
 #pragma unroll
                 for (int q = 0; q < W; q += 4)
                     *reinterpret_cast<float4*>(o + q) = make_float4(acc[q], acc[q + 1], acc[q + 2], acc[q + 3]);
             } else {
-                const int v = item.tile * 256 + m;
-                if (v < p.V) {
-                    const float zero[8] = {};
+                // the thread's columns, 64 bytes at a time, through the warp's 2 KB, so that 4 lanes write
+                // a row's 64 bytes (a 16-byte word a lane of 32 different rows took 284 us of 235)
+                const int v0 = item.tile * 256 + (int)rank * 128 + quad * 32;
+                uint4* sc = reinterpret_cast<uint4*>(ring + (size_t)S * C::bytes) + (warp - 3) * 128;
+                const bool half = p.odt == SPEC_BF16;
+                const int per = half ? 8 : 4;                  // columns of a word
 #pragma unroll
-                    for (int q = 0; q < W; q += 8)
-                        if (k0 + q < p.r) {
-                            put8(p.dWt_out, p.odt, (long)v * p.r + k0 + q, acc + q);
-                            put8(p.dU_out, p.odt, (long)v * p.r + k0 + q, zero);
+                for (int q = 0; q < W; q += 16) {
+                    if (half && (q & 16)) continue;
+                    uint4 w[4];
+#pragma unroll
+                    for (int h = 0; h < 4; ++h) {
+                        if (half) {
+                            uint32_t x[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const int at = (q + 8 * h + 2 * e) % W;
+                                asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(x[e]) : "f"(acc[at + 1]), "f"(acc[at]));
+                            }
+                            w[h] = make_uint4(x[0], x[1], x[2], x[3]);
+                        } else {
+                            w[h] = make_uint4(__float_as_uint(acc[q + 4 * h]), __float_as_uint(acc[q + 4 * h + 1]),
+                                              __float_as_uint(acc[q + 4 * h + 2]), __float_as_uint(acc[q + 4 * h + 3]));
                         }
+                        sc[lane * 4 + (h ^ ((lane >> 1) & 3))] = w[h];
+                    }
+                    __syncwarp();
+#pragma unroll
+                    for (int h = 0; h < 4; ++h) {
+                        const int row = h * 8 + (lane >> 2), word = lane & 3;
+                        const uint4 x = sc[row * 4 + (word ^ ((row >> 1) & 3))];
+                        const int k = k0 + q + word * per;
+                        if (v0 + row < p.V && k < p.r) {
+                            uint8_t* o = reinterpret_cast<uint8_t*>(p.dWt_out) + ((long)(v0 + row) * p.r + k) * (half ? 2 : 4);
+                            *reinterpret_cast<uint4*>(o) = x;
+                        }
+                    }
+                    __syncwarp();
                 }
+                // dU's rows of the same entries, which lie one behind the other, as 0
+                const long from = (long)v0 * p.r, to = (long)min(p.V, v0 + 32) * p.r;
+                uint4* u = reinterpret_cast<uint4*>(p.dU_out);
+                for (long e = from / per + group * 32 + lane; e < to / per; e += 4 * 32) u[e] = make_uint4(0u, 0u, 0u, 0u);
             }
         }
     }
@@ -306,26 +317,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMtcThreads, 1)
     if (warp == 1) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" :: "r"(tmem), "r"(C::tmem) : "memory");
-    }
-}
-
-// dU's rows from the parts of dX: the CTA at a token's first place among the ordered rows.
-__global__ void __launch_bounds__(256) markov_tc_u_kernel(MarkovParams p, MarkovBind b, MarkovTc a, int NT) {
-    const int n = p.B * p.gamma, at = blockIdx.x;
-    const int t = b.token[at];
-    if (t >= p.V || (at > 0 && b.token[at - 1] == t)) return;
-    for (int k = threadIdx.x; k < p.r; k += 256) {
-        float s = 0.0f;
-        for (int q = at; q < n && b.token[q] == t; ++q) {
-            const int i = b.order[q], tile = i >> 8;
-            const long lo = (long)tile * a.steps, hi = lo + a.steps - 1;
-            const int p0 = mtc_pair_of(a, lo), p1 = mtc_pair_of(a, hi);
-            float x = 0.0f;
-#pragma unroll 4
-            for (int pr = p0; pr <= p1; ++pr) x += b.dx[((size_t)(pr + tile) * 256 + (i & 255)) * NT + k];
-            s += x;
-        }
-        put(p.dU_out, p.odt, (long)t * p.r + k, s);
     }
 }
 
@@ -349,25 +340,35 @@ static cudaError_t mtc_launch(const MarkovParams& p, const MarkovBind& b, cudaSt
     if (!mtc_map(&zmap, p.grad, p.V, n, pitch) || !mtc_map(&umap, b.ux, p.r, n, (long)p.r * 2) ||
         !mtc_map(&wmap, p.Wt, p.r, p.V, (long)p.r * 2))
         return cudaErrorInvalidValue;
-    int sms = device_sm_count();
-    if (sms > 2 * kMarkovPairs) sms = 2 * kMarkovPairs;
-    MarkovTc wt, dx;
-    wt.tiles = (p.V + 255) / 256;
-    wt.steps = (n + kMtcStep - 1) / kMtcStep;
-    wt.pairs = wt.tiles < sms / 2 ? wt.tiles : sms / 2;
-    dx.tiles = (n + 255) / 256;
-    dx.steps = (p.V + kMtcStep - 1) / kMtcStep;
-    const long units = (long)dx.tiles * dx.steps;
-    dx.pairs = units < sms / 2 ? (int)units : sms / 2;
+    const int pairs = device_sm_count() / 2 > 0 ? device_sm_count() / 2 : 1;
+    const MarkovTc dx = markov_tc_dx(n, p.V), wt = {(p.V + 255) / 256, (n + kMtcStep - 1) / kMtcStep, 1};
+    const int items = dx.tiles * dx.parts;
     auto kw = markov_tc_kernel<false, NT>;
     auto kx = markov_tc_kernel<true, NT>;
     cudaError_t e = cudaFuncSetAttribute(kw, cudaFuncAttributeMaxDynamicSharedMemorySize, Mtc<NT>::smem);
     if (e == cudaSuccess) e = cudaFuncSetAttribute(kx, cudaFuncAttributeMaxDynamicSharedMemorySize, Mtc<NT>::smem);
     if (e != cudaSuccess) return e;
-    kw<<<2 * wt.pairs, kMtcThreads, Mtc<NT>::smem, stream>>>(p, b, wt, zmap, umap);
-    kx<<<2 * dx.pairs, kMtcThreads, Mtc<NT>::smem, stream>>>(p, b, dx, zmap, wmap);
-    markov_tc_u_kernel<<<n, 256, 0, stream>>>(p, b, dx, NT);
+    kw<<<2 * (wt.tiles < pairs ? wt.tiles : pairs), kMtcThreads, Mtc<NT>::smem, stream>>>(p, b, wt, zmap, umap);
+    kx<<<2 * (items < pairs ? items : pairs), kMtcThreads, Mtc<NT>::smem, stream>>>(p, b, dx, zmap, wmap);
+    markov_join(p, b, {dx.parts, (long)dx.tiles * 256, NT}, stream);
     return cudaGetLastError();
+}
+
+// The parts of the contraction over the vocabulary: the fewest steps in a line over all pairs, an item's
+// start and end counted as 12, a part's share in the join as 1/4 a tile (1792 rows: 10 parts of 7 tiles on 76
+// pairs; one share of all steps per pair, whatever its tile, read Wt from memory 7 times: 269 us).
+MarkovTc markov_tc_dx(int n, int V) {
+    MarkovTc a = {(n + 255) / 256, (V + kMtcStep - 1) / kMtcStep, 1};
+    double best = 0.0;
+    for (int s = 1; s <= 128 && s <= a.steps && (s == 1 || s * a.tiles <= 4 * kMarkovPairs); ++s) {
+        const double rounds = (s * a.tiles + kMarkovPairs - 1) / kMarkovPairs;
+        const double cost = rounds * ((a.steps + s - 1) / s + 12.0) + 0.25 * s * a.tiles;
+        if (s == 1 || cost < best) {
+            best = cost;
+            a.parts = s;
+        }
+    }
+    return a;
 }
 
 bool markov_tc_supported(const MarkovParams& p) {
