@@ -6,24 +6,43 @@
 
 namespace spec {
 
-constexpr int kMarkovPairs = 76;                 // most CTA pairs of a tensor-core product
+constexpr int kMarkovPairs = 76;                 // CTA pairs that a tensor-core product is cut for
+constexpr int kMarkovSmall = 8;                  // rows that one pass over the weights takes
+constexpr int kMarkovSlabs = 304;                // most slabs of that pass
+constexpr int kJoinRun = 8;                      // rows of a token that one CTA joins
+constexpr size_t kMarkovStage = 96u << 20;       // bytes that are staged at a time, about
 
 struct MarkovBind {
     unsigned* status;
     int32_t* order;          // [n] the rows by (token, row); rows without a token behind all others
     int32_t* token;          // [n] their tokens in that order (V: none)
-    int32_t* of_row;         // [n] the rows' tokens (V: none)
+    int2* run;               // [n] there: where the token's rows begin, and how many they are
     unsigned long long* none;   // [ceil(n / 64)] rows without a token, a bit each
-    bf16_t* ux;              // [n, r] U[x_i], 0 for a row without a token (tensor cores)
-    float* dx;               // dX in parts: [parts][n][r], or the pairs' tiles
-    int parts;
+    bf16_t* ux;              // [planes][n][r8] U[x_i], 0 for a row without a token
+    float* part;             // dX in parts
+    float* runs;             // [n][r4] sums over kJoinRun rows of a token
+    bf16_t* zs;              // staged dz   [planes][n][columns]
+    bf16_t* ws;              // staged Wt   [planes][columns][r8]
 };
+
+__host__ __device__ inline int round8(int r) { return (r + 7) & ~7; }
+__host__ __device__ inline int round4(int r) { return (r + 3) & ~3; }
 
 // A tensor-core product's items: tiles of 256 outputs, each in `parts` ranges of its steps.  Item
 // i is part i / tiles of tile i % tiles, and the pairs take them in order, so the tiles that
-// run at the same time go through the same steps and read B's rows from memory once.
-struct MarkovTc { int tiles, steps, parts; };
-__host__ __device__ inline int mtc_begin(const MarkovTc& a, int part) { return (int)((long)a.steps * part / a.parts); }
+// run at the same time go through the same steps and read B's rows from memory once.  With
+// operands in several planes (float32 values as sums of bf16) the steps run through the pairs of
+// planes, `steps` of them each.
+struct MarkovTc {
+    int tiles, steps, parts;
+    int terms;               // pairs of planes
+    unsigned planes;         // their numbers, 2 bits for A and 2 for B each, from the lowest
+    int v0, v1;              // the entries that this launch covers
+    int add;                 // parts are added to what is there
+};
+__host__ __device__ inline int mtc_begin(const MarkovTc& a, int part) {
+    return (int)((long)a.steps * a.terms * part / a.parts);
+}
 
 template <typename T> __device__ __forceinline__ void put(void* o, long i, float x);
 template <> __device__ __forceinline__ void put<float>(void* o, long i, float x) { reinterpret_cast<float*>(o)[i] = x; }
@@ -35,13 +54,27 @@ __device__ __forceinline__ void put(void* o, int dtype, long i, float x) {
     else put<float>(o, i, x);
 }
 
-// Where the join finds row i's part: dx[(part * part_stride + i) * pitch], 16 bytes aligned.
-struct MarkovJoin { int parts; long part_stride; int pitch; };
-__host__ __device__ inline int markov_pitch(int r) { return (r + 3) & ~3; }
-void markov_join(const MarkovParams& p, const MarkovBind& b, const MarkovJoin& a, cudaStream_t stream);
+// A float32 value as a sum of bf16 ones, 24 bits in three; what is not finite stays in the first.
+__device__ __forceinline__ float bf16_part(float x) {
+    const float a = __bfloat162float(__float2bfloat16_rn(x));
+    return fabsf(a) < INFINITY || !(fabsf(x) < INFINITY) ? a : __bfloat162float(__float2bfloat16_rz(x));
+}
+__device__ __forceinline__ void bf16_parts(float x, float (&o)[3]) {
+    o[0] = bf16_part(x);
+    const float r = fabsf(o[0]) < INFINITY ? x - o[0] : 0.0f;
+    o[1] = bf16_part(r);
+    o[2] = bf16_part(r - o[1]);
+}
 
-MarkovTc markov_tc_dx(int n, int V);
-bool markov_tc_supported(const MarkovParams& p);
-cudaError_t markov_tc_launch(const MarkovParams& p, const MarkovBind& b, cudaStream_t stream);
+// Where the join finds row i's part: part[(p * part_stride + i) * pitch], 16 bytes aligned.
+struct MarkovJoin { int parts; long part_stride; int pitch; };
+
+// The entries of a staged slice: about kMarkovStage bytes of three planes of dz and Wt.
+__host__ inline int markov_slice(int n, int r, int V) {
+    const size_t most = kMarkovStage / ((size_t)(n + round8(r)) * 6) / 256 * 256;
+    return most < 256 ? 256 : (most < (size_t)V ? (int)most : V);
+}
+MarkovTc markov_tc_dx(int n, int columns);
+cudaError_t markov_tc_launch(const MarkovParams& p, const MarkovBind& b, MarkovJoin* join, cudaStream_t stream);
 
 }  // namespace spec

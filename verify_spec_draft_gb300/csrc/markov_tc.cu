@@ -1,4 +1,4 @@
-// markov_tc.cu - spec_markov_grad's two products on the tcgen05 tensor cores (bf16 operands).
+// markov_tc.cu - spec_markov_grad's two products on the tcgen05 tensor cores.
 //
 //     WT:  dWt [V, r] = dz^T Ux     a tile of 256 entries, contraction over the rows
 //     DX:  dX  [n, r] = dz Wt       a tile of 256 rows, contraction over the vocabulary
@@ -16,6 +16,11 @@
 // A tensor core's sums drop what falls below the accumulator's last bit, so a chain of steps
 // ends after kMtcChunk of them: the epilogue adds it to float32 registers while the next one runs
 // in the other half of TMEM.
+//
+// Operands are bf16.  A float32 one is split into three (bf16_parts), 24 bits in all, and the product
+// is the sum of those pairs of parts that reach 2^-24 of it: 3 with one such operand, 6 with two.
+// dz whose rows do not start on 16 bytes cannot be copied by TMA; it, and what is split, goes through
+// a staged copy, a slice of the vocabulary at a time that stays in L2.
 #include "markov.cuh"
 #include "tc_common.cuh"
 
@@ -99,6 +104,11 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
 
 // Item `it` of a pair: its tile, its steps [k0, k1) and its number.
 struct MtcItem { int tile, k0, k1, number; };
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+        :: "r"(smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar)) : "memory");
+}
 __device__ __forceinline__ bool mtc_item(const MarkovTc& a, int it, MtcItem& o) {
     o.number = (int)(blockIdx.x >> 1) + it * (int)(gridDim.x >> 1);
     const int part = o.number / a.tiles;
@@ -158,16 +168,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMtcThreads, 1)
                     if (!ok) break;
                     uint8_t* d = ring + (size_t)s * C::bytes;
                     mbar_arrive_expect_tx(&s_full[s], C::bytes);
-                    if (DX) {
-                        tma_load_2d(d, &zmap, k * kMtcStep, m0, &s_full[s]);
-                        tma_load_2d(d + kMtcBox, &zmap, k * kMtcStep, m0 + 64, &s_full[s]);
-                    } else {
-                        tma_load_2d(d, &zmap, m0, k * kMtcStep, &s_full[s]);
-                        tma_load_2d(d + kMtcBox, &zmap, m0 + 64, k * kMtcStep, &s_full[s]);
-                    }
+                    // (a division a step, of a small number: k / a.steps is the pair of planes)
+                    const int term = k / a.steps, at = (k - term * a.steps) * kMtcStep;
+                    const int za = (int)(a.planes >> (4 * term)) & 3, zb = (int)(a.planes >> (4 * term + 2)) & 3;
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        if (DX) tma_load_3d(d + j * kMtcBox, &zmap, at, m0 + 64 * j, za, &s_full[s]);
+                        else tma_load_3d(d + j * kMtcBox, &zmap, m0 + 64 * j, at, za, &s_full[s]);
 #pragma unroll
                     for (int j = 0; j < NT / 128; ++j)
-                        tma_load_2d(d + (2 + j) * kMtcBox, &bmap, (int)rank * (NT / 2) + j * 64, k * kMtcStep, &s_full[s]);
+                        tma_load_3d(d + (2 + j) * kMtcBox, &bmap, (int)rank * (NT / 2) + j * 64, at, zb, &s_full[s]);
                 }
             }
             // nothing may still be on its way when the CTA ends, a copy or the issuer's arrival
@@ -216,7 +226,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMtcThreads, 1)
                 ok = mbar_wait(&s_full[s], (i / S) & 1u, b.status, kWaitLimitNs);
                 if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
                 if (!DX) {
-                    unsigned long long none = b.none[k];   // rows of the step without a token
+                    unsigned long long none = b.none[k % a.steps];   // rows of the step without a token
                     if (none) {
                         uint4* z = reinterpret_cast<uint4*>(ring + (size_t)s * C::bytes);
                         for (; none; none &= none - 1) {   // a row is 8 words of each of the two boxes
@@ -260,14 +270,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMtcThreads, 1)
             const int k0 = group * W;
             if (DX) {
                 const int m = (int)rank * 128 + quad * 32 + lane;
-                float* o = b.dx + ((size_t)item.number * 256 + m) * NT + k0;
+                float* o = b.part + ((size_t)item.number * 256 + m) * NT + k0;
 #pragma unroll
-                for (int q = 0; q < W; q += 4)
-                    *reinterpret_cast<float4*>(o + q) = make_float4(acc[q], acc[q + 1], acc[q + 2], acc[q + 3]);
+                for (int q = 0; q < W; q += 4) {
+                    float4 x = make_float4(acc[q], acc[q + 1], acc[q + 2], acc[q + 3]);
+                    if (a.add) {
+                        const float4 y = *reinterpret_cast<const float4*>(o + q);
+                        x.x += y.x; x.y += y.y; x.z += y.z; x.w += y.w;
+                    }
+                    *reinterpret_cast<float4*>(o + q) = x;
+                }
             } else {
                 // the thread's columns, 64 bytes at a time, through the warp's 2 KB, so that 4 lanes write
                 // a row's 64 bytes (a 16-byte word a lane of 32 different rows took 284 us of 235)
-                const int v0 = item.tile * 256 + (int)rank * 128 + quad * 32;
+                const int v0 = a.v0 + item.tile * 256 + (int)rank * 128 + quad * 32;
                 uint4* sc = reinterpret_cast<uint4*>(ring + (size_t)S * C::bytes) + (warp - 3) * 128;
                 const bool half = p.odt == SPEC_BF16;
                 const int per = half ? 8 : 4;                  // columns of a word
@@ -297,17 +313,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMtcThreads, 1)
                         const int row = h * 8 + (lane >> 2), word = lane & 3;
                         const uint4 x = sc[row * 4 + (word ^ ((row >> 1) & 3))];
                         const int k = k0 + q + word * per;
-                        if (v0 + row < p.V && k < p.r) {
-                            uint8_t* o = reinterpret_cast<uint8_t*>(p.dWt_out) + ((long)(v0 + row) * p.r + k) * (half ? 2 : 4);
-                            *reinterpret_cast<uint4*>(o) = x;
+                        if (v0 + row < a.v1 && k < p.r) {
+                            const long o = (long)(v0 + row) * p.r + k;
+                            if (p.r % 8 == 0) {
+                                *reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(p.dWt_out) + o * (half ? 2 : 4)) = x;
+                            } else {
+                                const uint32_t y[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) {
+                                    if (e >= per || k + e >= p.r) break;
+                                    if (half) reinterpret_cast<bf16_t*>(p.dWt_out)[o + e] = (bf16_t)(y[(e >> 1) & 3] >> (16 * (e & 1)));
+                                    else reinterpret_cast<uint32_t*>(p.dWt_out)[o + e] = y[e & 3];
+                                }
+                            }
                         }
                     }
                     __syncwarp();
                 }
                 // dU's rows of the same entries, which lie one behind the other, as 0
-                const long from = (long)v0 * p.r, to = (long)min(p.V, v0 + 32) * p.r;
+                // (they start on 64 bytes, as 32 entries do; the last may end anywhere)
+                const long from = (long)v0 * p.r, to = (long)min(a.v1, v0 + 32) * p.r;
                 uint4* u = reinterpret_cast<uint4*>(p.dU_out);
                 for (long e = from / per + group * 32 + lane; e < to / per; e += 4 * 32) u[e] = make_uint4(0u, 0u, 0u, 0u);
+                const long left = to / per * per + lane;
+                if (group == 0 && from < to && left < to) put(p.dU_out, p.odt, left, 0.0f);
             }
         }
     }
@@ -320,45 +349,122 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMtcThreads, 1)
     }
 }
 
-static bool mtc_map(CUtensorMap* m, const void* base, int width, long rows, long pitch_bytes) {
-    const cuuint64_t dims[2] = {(cuuint64_t)width, (cuuint64_t)rows};
-    const cuuint64_t strides[1] = {(cuuint64_t)pitch_bytes};
-    const cuuint32_t box[2] = {64, 64};
-    const cuuint32_t estr[2] = {1, 1};
+// Columns [v0, v0 + columns) of dz's rows, or rows of the weights, as bf16 planes whose rows are `pitch`
+// entries apart (a multiple of 8).  A thread takes 8 columns; bf16 rows of any offset are read as 16-byte
+// words, two of them shifted into place.
+template <typename T, int PLANES>
+__global__ void __launch_bounds__(256) markov_stage_kernel(const T* src, long ld, int rows, int columns, int pitch, bf16_t* out) {
+    const int words = (columns + 7) / 8;
+    const long all = (long)rows * words, step = (long)gridDim.x * 256;
+    for (long e = (long)blockIdx.x * 256 + threadIdx.x; e < all; e += step) {
+        const int row = (int)(e / words), c = (int)(e - (long)row * words) * 8;
+        const T* from = src + row * ld;
+        uint4 w[PLANES];
+        if constexpr (sizeof(T) == 2) {
+            const RowWords<T> in(from, columns);
+            uint4 a = in.load(c / 8), b = make_uint4(0u, 0u, 0u, 0u);
+            if (in.mis && c / 8 + 1 < in.n) b = in.load(c / 8 + 1);
+            uint32_t h[9] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, 0u};
+            const int s = in.mis;   // entries to the left of the row's first
+            if (s & 4)
+#pragma unroll
+                for (int k = 0; k < 6; ++k) h[k] = h[k + 2];
+            if (s & 2)
+#pragma unroll
+                for (int k = 0; k < 5; ++k) h[k] = h[k + 1];
+            if (s & 1)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) h[k] = __funnelshift_r(h[k], h[k + 1], 16);
+            w[0] = make_uint4(h[0], h[1], h[2], h[3]);
+        } else {
+            float x[8], y[8][3];
+            if (c + 8 <= columns && (reinterpret_cast<uintptr_t>(from + c) & 15u) == 0) {
+                const float4 a = __ldcs(reinterpret_cast<const float4*>(from + c)), b = __ldcs(reinterpret_cast<const float4*>(from + c) + 1);
+                x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+                x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+            } else {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) x[k] = c + k < columns ? load_one(from + c + k) : 0.0f;
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) bf16_parts(x[k], y[k]);
+#pragma unroll
+            for (int q = 0; q < PLANES; ++q) {
+                const float z[8] = {y[0][q], y[1][q], y[2][q], y[3][q], y[4][q], y[5][q], y[6][q], y[7][q]};
+                w[q] = word_of<bf16_t>(z);
+            }
+        }
+#pragma unroll
+        for (int q = 0; q < PLANES; ++q) *reinterpret_cast<uint4*>(out + ((long)q * rows + row) * pitch + c) = w[q];
+    }
+}
+static void mtc_stage(const void* src, int dtype, long at, long ld, int rows, int columns, int pitch, bf16_t* out, cudaStream_t stream) {
+    const long all = ((long)rows * ((columns + 7) / 8) + 255) / 256, most = 8l * device_sm_count();
+    const unsigned grid = (unsigned)(all < most ? all : most);
+    if (dtype == SPEC_BF16) markov_stage_kernel<bf16_t, 1><<<grid, 256, 0, stream>>>(reinterpret_cast<const bf16_t*>(src) + at, ld, rows, columns, pitch, out);
+    else markov_stage_kernel<float, 3><<<grid, 256, 0, stream>>>(reinterpret_cast<const float*>(src) + at, ld, rows, columns, pitch, out);
+}
+
+static bool mtc_map(CUtensorMap* m, const void* base, int width, long rows, long pitch, int planes) {
+    const cuuint64_t dims[3] = {(cuuint64_t)width, (cuuint64_t)rows, (cuuint64_t)planes};
+    const cuuint64_t strides[2] = {(cuuint64_t)pitch * 2, (cuuint64_t)pitch * 2 * (cuuint64_t)rows};
+    const cuuint32_t box[3] = {64, 64, 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
     EncodeTiledFn f = encode_tiled();
-    return f && f(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
+    return f && f(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int NT>
-static cudaError_t mtc_launch(const MarkovParams& p, const MarkovBind& b, cudaStream_t stream) {
-    const int n = p.B * p.gamma;
-    CUtensorMap zmap, umap, wmap;
-    // one row: its pitch is not used, but has to be whole 16-byte words
-    const long pitch = n > 1 ? (long)p.ld * 2 : ((long)p.ld * 2 + 15) / 16 * 16;
-    if (!mtc_map(&zmap, p.grad, p.V, n, pitch) || !mtc_map(&umap, b.ux, p.r, n, (long)p.r * 2) ||
-        !mtc_map(&wmap, p.Wt, p.r, p.V, (long)p.r * 2))
-        return cudaErrorInvalidValue;
+static cudaError_t mtc_launch(const MarkovParams& p, const MarkovBind& b, MarkovJoin* join, cudaStream_t stream) {
+    const int n = p.B * p.gamma, r8 = round8(p.r);
+    const bool z16 = p.gdt == SPEC_BF16, w16 = p.wdt == SPEC_BF16;
+    const bool stage_z = !z16 || p.ld % 8 != 0, stage_w = !w16 || p.r != r8;
+    const int columns = stage_z || stage_w ? markov_slice(n, p.r, p.V) : p.V;
     const int pairs = device_sm_count() / 2 > 0 ? device_sm_count() / 2 : 1;
-    const MarkovTc dx = markov_tc_dx(n, p.V), wt = {(p.V + 255) / 256, (n + kMtcStep - 1) / kMtcStep, 1};
-    const int items = dx.tiles * dx.parts;
+    MarkovTc dx = markov_tc_dx(n, columns);
+    dx.terms = z16 ? (w16 ? 1 : 3) : (w16 ? 3 : 6);
+    // (A's part, B's part) of each term, the smallest products first
+    if (z16) dx.planes = w16 ? 0u : 0x048u;
+    else dx.planes = w16 ? 0x012u : 0x041528u;
     auto kw = markov_tc_kernel<false, NT>;
     auto kx = markov_tc_kernel<true, NT>;
     cudaError_t e = cudaFuncSetAttribute(kw, cudaFuncAttributeMaxDynamicSharedMemorySize, Mtc<NT>::smem);
     if (e == cudaSuccess) e = cudaFuncSetAttribute(kx, cudaFuncAttributeMaxDynamicSharedMemorySize, Mtc<NT>::smem);
     if (e != cudaSuccess) return e;
-    kw<<<2 * (wt.tiles < pairs ? wt.tiles : pairs), kMtcThreads, Mtc<NT>::smem, stream>>>(p, b, wt, zmap, umap);
-    kx<<<2 * (items < pairs ? items : pairs), kMtcThreads, Mtc<NT>::smem, stream>>>(p, b, dx, zmap, wmap);
-    markov_join(p, b, {dx.parts, (long)dx.tiles * 256, NT}, stream);
+    CUtensorMap zmap, umap, wmap;
+    if (!mtc_map(&umap, b.ux, p.r, n, r8, w16 ? 1 : 3)) return cudaErrorInvalidValue;
+    for (int v0 = 0; v0 < p.V; v0 += columns) {
+        const int width = columns < p.V - v0 ? columns : p.V - v0;
+        if (stage_z) mtc_stage(p.grad, p.gdt, v0, p.ld, n, width, round8(width), b.zs, stream);
+        if (stage_w) mtc_stage(p.Wt, p.wdt, (long)v0 * p.r, p.r, width, p.r, r8, b.ws, stream);
+        if (!mtc_map(&zmap, stage_z ? b.zs : reinterpret_cast<const bf16_t*>(p.grad) + v0, width, n, stage_z ? round8(width) : p.ld, z16 ? 1 : 3) ||
+            !mtc_map(&wmap, stage_w ? b.ws : reinterpret_cast<const bf16_t*>(p.Wt) + (long)v0 * p.r, p.r, width, r8, w16 ? 1 : 3))
+            return cudaErrorInvalidValue;
+        MarkovTc wt = dx;
+        wt.tiles = (width + 255) / 256;
+        wt.steps = (n + kMtcStep - 1) / kMtcStep;
+        wt.parts = 1;
+        wt.v0 = v0;
+        wt.v1 = v0 + width;
+        dx.steps = (width + kMtcStep - 1) / kMtcStep;
+        dx.v0 = v0;
+        dx.v1 = v0 + width;
+        dx.add = v0 > 0;
+        const int items = dx.tiles * dx.parts;
+        kw<<<2 * (wt.tiles < pairs ? wt.tiles : pairs), kMtcThreads, Mtc<NT>::smem, stream>>>(p, b, wt, zmap, umap);
+        kx<<<2 * (items < pairs ? items : pairs), kMtcThreads, Mtc<NT>::smem, stream>>>(p, b, dx, zmap, wmap);
+    }
+    *join = {dx.parts, (long)dx.tiles * 256, NT};
     return cudaGetLastError();
 }
 
 // The parts of the contraction over the vocabulary: the fewest steps in a line over all pairs, an item's
 // start and end counted as 12, a part's share in the join as 1/4 a tile (1792 rows: 10 parts of 7 tiles on 76
 // pairs; one share of all steps per pair, whatever its tile, read Wt from memory 7 times: 269 us).
-MarkovTc markov_tc_dx(int n, int V) {
-    MarkovTc a = {(n + 255) / 256, (V + kMtcStep - 1) / kMtcStep, 1};
+MarkovTc markov_tc_dx(int n, int columns) {
+    MarkovTc a = {(n + 255) / 256, (columns + kMtcStep - 1) / kMtcStep, 1, 1, 0u, 0, columns, 0};
     double best = 0.0;
     for (int s = 1; s <= 128 && s <= a.steps && (s == 1 || s * a.tiles <= 4 * kMarkovPairs); ++s) {
         const double rounds = (s * a.tiles + kMarkovPairs - 1) / kMarkovPairs;
@@ -371,12 +477,8 @@ MarkovTc markov_tc_dx(int n, int V) {
     return a;
 }
 
-bool markov_tc_supported(const MarkovParams& p) {
-    return p.gdt == SPEC_BF16 && p.wdt == SPEC_BF16 && p.r % 8 == 0 && (p.ld % 8 == 0 || p.B * p.gamma == 1);
-}
-
-cudaError_t markov_tc_launch(const MarkovParams& p, const MarkovBind& b, cudaStream_t stream) {
-    return p.r > 128 ? mtc_launch<256>(p, b, stream) : mtc_launch<128>(p, b, stream);
+cudaError_t markov_tc_launch(const MarkovParams& p, const MarkovBind& b, MarkovJoin* join, cudaStream_t stream) {
+    return p.r > 128 ? mtc_launch<256>(p, b, join, stream) : mtc_launch<128>(p, b, join, stream);
 }
 
 }  // namespace spec
