@@ -16,56 +16,53 @@ constexpr int kMarkovThreads = 256;
 constexpr int kMarkovWarps = kMarkovThreads / 32;
 constexpr int kOrderTile = 2048;                 // tokens compared at a time
 
-// Row i's place among the rows by (token, row), counted: n comparisons a row, a warp a row.  A
-// second half of the grid copies the rows U[x_i] for the tensor cores and marks the rows without
-// a token.
+// The token before row i's position (V: none, or one that is out of range, which is bad).
+__device__ __forceinline__ int markov_token(const MarkovParams& p, int i, bool* bad) {
+    const int q = i / p.gamma, j = i - q * p.gamma;
+    const int t = j == 0 ? p.anchor[q] : p.tokens[(long)q * p.gamma + j - 1];
+    if (t < -1 || t >= p.V) *bad = true;
+    return t < 0 || t >= p.V ? p.V : t;
+}
+
+// Row i's place among the rows by (token, row), counted: n comparisons a row, a warp a row.  The warp
+// copies the row U[x_i] for the tensor cores as well; a CTA's 8 rows are a byte of the marks.
 template <typename W>
 __global__ void __launch_bounds__(kMarkovThreads) markov_order_kernel(MarkovParams p, MarkovBind b, int planes) {
     __shared__ int32_t s_tok[kOrderTile];
+    __shared__ unsigned s_none;
     const int n = p.B * p.gamma, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    auto token_of = [&](int i, bool* bad) {
-        const int q = i / p.gamma, j = i - q * p.gamma;
-        const int t = j == 0 ? p.anchor[q] : p.tokens[(long)q * p.gamma + j - 1];
-        if (t < -1 || t >= p.V) *bad = true;
-        return t < 0 || t >= p.V ? p.V : t;
-    };
+    const int i = blockIdx.x * kMarkovWarps + warp, r8 = round8(p.r);
     bool bad = false;
-    const int ranks = (n + kMarkovWarps - 1) / kMarkovWarps;
-    if ((int)blockIdx.x >= ranks) {   // (a CTA of 64 rows, so that it has a whole word of marks)
-        const int i0 = ((int)blockIdx.x - ranks) * 64, r8 = round8(p.r);
-        if (warp == 0) {
-            const unsigned lo = __ballot_sync(0xffffffffu, i0 + lane < n && token_of(i0 + lane, &bad) >= p.V);
-            const unsigned hi = __ballot_sync(0xffffffffu, i0 + 32 + lane < n && token_of(i0 + 32 + lane, &bad) >= p.V);
-            if (lane == 0) b.none[i0 >> 6] = (unsigned long long)hi << 32 | lo;
-        }
-        for (int i = i0 + warp; i < min(n, i0 + 64); i += kMarkovWarps) {
-            const int t = token_of(i, &bad);
-            const W* u = reinterpret_cast<const W*>(p.U) + (long)t * p.r;
-            if (planes == 1 && p.r == r8) {
-                const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-                if (lane < r8 / 8)
-                    reinterpret_cast<uint4*>(b.ux + (long)i * r8)[lane] = t < p.V ? __ldg(reinterpret_cast<const uint4*>(u) + lane) : zero;
-            } else {
-                for (int k = lane; k < r8; k += 32) {
-                    float x[3];
-                    bf16_parts(t < p.V && k < p.r ? load_one(u + k) : 0.0f, x);
+    const int mine = i < n ? markov_token(p, i, &bad) : 0;
+    if (threadIdx.x == 0) s_none = 0u;
+    __syncthreads();
+    if (lane == 0) {
+        if (bad) atomicOr(b.status, SPEC_DEV_TOKEN);
+        if (i < n && mine >= p.V) atomicOr(&s_none, 1u << warp);
+    }
+    if (i < n) {
+        const W* u = reinterpret_cast<const W*>(p.U) + (long)mine * p.r;
+        if (planes == 1 && p.r == r8) {
+            const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+            if (lane < r8 / 8)
+                reinterpret_cast<uint4*>(b.ux + (long)i * r8)[lane] = mine < p.V ? __ldg(reinterpret_cast<const uint4*>(u) + lane) : zero;
+        } else {
+            for (int k = lane; k < r8; k += 32) {
+                float x[3];
+                bf16_parts(mine < p.V && k < p.r ? load_one(u + k) : 0.0f, x);
 #pragma unroll
-                    for (int q = 0; q < 3; ++q)
-                        if (q < planes) put<bf16_t>(b.ux, ((long)q * n + i) * r8 + k, x[q]);
-                }
+                for (int q = 0; q < 3; ++q)
+                    if (q < planes) put<bf16_t>(b.ux, ((long)q * n + i) * r8 + k, x[q]);
             }
         }
-        return;
     }
-    const int i = blockIdx.x * kMarkovWarps + warp;
-    const int mine = i < n ? token_of(i, &bad) : 0;
-    if (bad && lane == 0) atomicOr(b.status, SPEC_DEV_TOKEN);
     int less = 0, same = 0, before = 0;   // tokens below this one, rows of it, those of them before this one
     for (int lo = 0; lo < n; lo += kOrderTile) {
         __syncthreads();
+        bool other = false;
 #pragma unroll
         for (int k = threadIdx.x; k < kOrderTile; k += kMarkovThreads)
-            if (lo + k < n) s_tok[k] = token_of(lo + k, &bad);
+            if (lo + k < n) s_tok[k] = markov_token(p, lo + k, &other);
         __syncthreads();
         const int m = min(kOrderTile, n - lo);
 #pragma unroll 4
@@ -84,6 +81,7 @@ __global__ void __launch_bounds__(kMarkovThreads) markov_order_kernel(MarkovPara
         b.token[less + before] = mine;
         b.run[less + before] = make_int2(less, same);
     }
+    if (threadIdx.x == 0) b.none[blockIdx.x] = (uint8_t)s_none;
 }
 
 // A few rows: one pass over the vocabulary forms both products.  A warp takes an entry v, its lanes
@@ -92,14 +90,14 @@ __global__ void __launch_bounds__(kMarkovThreads) markov_order_kernel(MarkovPara
 // r = 256: the tensor cores would spend their steps of 64 rows on zeros.
 template <typename G, typename W, int C>
 __global__ void __launch_bounds__(kMarkovThreads) markov_small_kernel(MarkovParams p, MarkovBind b) {
-    constexpr int N = kMarkovSmall, kV = 64;       // entries of a turn
+    constexpr int N = kMarkovSmall, kV = kMarkovTurn;
     __shared__ __align__(16) float s_d[kV][N];
     __shared__ float s_x[kMarkovWarps][32 * C];
     __shared__ int s_row[N];
     const int n = p.B * p.gamma, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    if (tid < N) s_row[tid] = p.V;
-    __syncthreads();
-    if (tid < n) s_row[b.order[tid]] = b.token[tid];
+    bool bad = false;
+    if (tid < N) s_row[tid] = tid < n ? markov_token(p, tid, &bad) : p.V;
+    if (bad && blockIdx.x == 0) atomicOr(b.status, SPEC_DEV_TOKEN);
     __syncthreads();
     const G* dz = reinterpret_cast<const G*>(p.grad);
     float u[N][C], x[N][C];
@@ -167,8 +165,8 @@ __global__ void __launch_bounds__(kMarkovThreads) markov_small_kernel(MarkovPara
 }
 
 // dU's rows: the CTA at every kJoinRun-th of a token's ordered rows sums the parts of that many; where
-// they are all, that is dU's row, otherwise the sum is kept for markov_runs_kernel.  Terms are (row, part) in
-// order; 16-byte columns go over lanes and the terms over groups of threads, whose sums meet in order.
+// they are all, that is dU's row, otherwise the sum is kept for markov_runs_kernel.  16-byte columns go over
+// lanes and the parts over groups of threads, whose sums meet in order.
 constexpr int kJoinThreads = 256;
 __device__ __forceinline__ void join_out(const MarkovParams& p, int t, int k, const float4& s) {
     const float o[4] = {s.x, s.y, s.z, s.w};
@@ -186,26 +184,52 @@ __device__ __forceinline__ bool join_meet(float4* s_sum, float4& s, int k, int g
     }
     return true;
 }
+template <bool SMALL>   // (kMarkovSmall rows at most: their order is found here)
 __global__ void __launch_bounds__(kJoinThreads) markov_join_kernel(MarkovParams p, MarkovBind b, MarkovJoin a) {
     __shared__ float4 s_sum[kJoinThreads];
-    const int at = blockIdx.x, t = b.token[at];
-    const int2 run = b.run[at];
-    if (t >= p.V || (at - run.x) % kJoinRun != 0) return;
-    const int rows = min(kJoinRun, run.x + run.y - at);
+    const int at = blockIdx.x;
+    int t, rows, all, index[kJoinRun];
+    if (SMALL) {
+        static_assert(kMarkovSmall == kJoinRun, "a CTA joins all rows of a token");
+        const int n = p.B * p.gamma;
+        bool bad = false;
+        t = markov_token(p, at, &bad);
+        rows = 0;
+#pragma unroll
+        for (int i = 0; i < kMarkovSmall; ++i) {
+            if (i >= n || markov_token(p, i, &bad) != t) continue;
+            if (i < at) return;   // that one's
+#pragma unroll
+            for (int q = 0; q < kJoinRun; ++q)
+                if (q == rows) index[q] = i;
+            ++rows;
+        }
+        all = rows;
+    } else {
+        const int2 run = b.run[at];
+        t = b.token[at];
+        if ((at - run.x) % kJoinRun != 0) return;
+        rows = min(kJoinRun, run.x + run.y - at);
+        all = run.y;
+#pragma unroll
+        for (int q = 0; q < kJoinRun; ++q) index[q] = b.order[at + min(q, rows - 1)];
+    }
+    if (t >= p.V) return;
     const int quads = round4(p.r) / 4, groups = kJoinThreads / quads;
-    const int k = threadIdx.x % quads, g = threadIdx.x / quads, terms = rows * a.parts;
+    const int k = threadIdx.x % quads, g = threadIdx.x / quads;
     float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (g < groups) {
-        const int lo = terms * g / groups, hi = terms * (g + 1) / groups;
-#pragma unroll 8
-        for (int e = lo; e < hi; ++e) {
-            const int q = e / a.parts, part = e - q * a.parts, i = b.order[at + q];
-            const float4 x = *reinterpret_cast<const float4*>(b.part + (part * a.part_stride + i) * a.pitch + 4 * k);
-            s.x += x.x; s.y += x.y; s.z += x.z; s.w += x.w;
-        }
+#pragma unroll 2
+        for (int part = g; part < a.parts; part += groups)
+#pragma unroll
+            for (int q = 0; q < kJoinRun; ++q) {
+                if (q >= rows) continue;
+                const float4 x = *reinterpret_cast<const float4*>(b.part + (part * a.part_stride + index[q]) * a.pitch + 4 * k);
+                s.x += x.x; s.y += x.y; s.z += x.z; s.w += x.w;
+            }
     }
     if (!join_meet(s_sum, s, k, g, quads, groups)) return;
-    if (run.y <= kJoinRun) join_out(p, t, k, s);
+    if (all <= kJoinRun) join_out(p, t, k, s);
     else reinterpret_cast<float4*>(b.runs + (long)at * round4(p.r))[k] = s;
 }
 // The tokens of more rows: a CTA looks at 32 places for where one begins.
@@ -245,22 +269,22 @@ static size_t markov_bind(MarkovBind& b, void* ws, int n, int r, int V) {
         at += align256(bytes);
         return q;
     };
-    b.order = reinterpret_cast<int32_t*>(take((size_t)n * 4));
-    b.token = reinterpret_cast<int32_t*>(take((size_t)n * 4));
-    b.run = reinterpret_cast<int2*>(take((size_t)n * 8));
-    b.runs = reinterpret_cast<float*>(take((size_t)n * round4(r) * 4));
     if (markov_small(n)) {
         b.part = reinterpret_cast<float*>(take((size_t)kMarkovSlabs * n * round4(r) * 4));
         return at;
     }
+    b.order = reinterpret_cast<int32_t*>(take((size_t)n * 4));
+    b.token = reinterpret_cast<int32_t*>(take((size_t)n * 4));
+    b.run = reinterpret_cast<int2*>(take((size_t)n * 8));
+    b.runs = reinterpret_cast<float*>(take((size_t)n * round4(r) * 4));
     const int columns = markov_slice(n, r, V);
-    b.none = reinterpret_cast<unsigned long long*>(take((size_t)(n + 63) / 64 * 8));
+    b.none = take((size_t)(n + 63) / 64 * 8);
     b.ux = reinterpret_cast<bf16_t*>(take((size_t)3 * n * round8(r) * 2));
     const MarkovTc whole = markov_tc_dx(n, V), part = markov_tc_dx(n, columns);
-    const size_t parts = whole.parts > part.parts ? whole.parts : part.parts;
-    b.part = reinterpret_cast<float*>(take(parts * whole.tiles * 256 * (r > 128 ? 256 : 128) * 4));
-    b.zs = reinterpret_cast<bf16_t*>(take((size_t)3 * n * round8(columns) * 2));
-    b.ws = reinterpret_cast<bf16_t*>(take((size_t)3 * columns * round8(r) * 2));
+    b.parts = whole.parts > part.parts ? whole.parts : part.parts;
+    b.part = reinterpret_cast<float*>(take((size_t)b.parts * whole.tiles * 256 * (r > 128 ? 256 : 128) * 4));
+    b.stage_bytes = (size_t)6 * ((size_t)n * round8(columns) + (size_t)columns * round8(r)) + 4096;
+    b.stage = reinterpret_cast<bf16_t*>(take(b.stage_bytes));
     return at;
 }
 
@@ -271,7 +295,7 @@ size_t markov_grad_workspace_bytes(int B, int gamma, int V, int r) {
 
 template <typename G, typename W>
 static int markov_small_launch(const MarkovParams& p, const MarkovBind& b, cudaStream_t stream) {
-    int slabs = (p.V + 63) / 64;
+    int slabs = (p.V + kMarkovTurn - 1) / kMarkovTurn;
     const int most = 2 * device_sm_count() < kMarkovSlabs ? 2 * device_sm_count() : kMarkovSlabs;
     if (slabs > most) slabs = most;
     const int C = (p.r + 31) / 32;
@@ -287,19 +311,20 @@ cudaError_t markov_grad_launch(const MarkovParams& p, void* ws, cudaStream_t str
     MarkovBind b;
     markov_bind(b, ws, n, p.r, p.V);
     const bool small = markov_small(n), g16 = p.gdt == SPEC_BF16, w16 = p.wdt == SPEC_BF16;
-    const unsigned grid = (n + kMarkovWarps - 1) / kMarkovWarps + (small ? 0 : (n + 63) / 64);
-    if (w16) markov_order_kernel<bf16_t><<<grid, kMarkovThreads, 0, stream>>>(p, b, 1);
-    else markov_order_kernel<float><<<grid, kMarkovThreads, 0, stream>>>(p, b, 3);
     MarkovJoin join = {0, n, round4(p.r)};
     if (small) {
         join.parts = g16 ? (w16 ? markov_small_launch<bf16_t, bf16_t>(p, b, stream) : markov_small_launch<bf16_t, float>(p, b, stream))
                          : (w16 ? markov_small_launch<float, bf16_t>(p, b, stream) : markov_small_launch<float, float>(p, b, stream));
-    } else {
-        const cudaError_t e = markov_tc_launch(p, b, &join, stream);
-        if (e != cudaSuccess) return e;
+        markov_join_kernel<true><<<n, kJoinThreads, 0, stream>>>(p, b, join);
+        return cudaGetLastError();
     }
-    markov_join_kernel<<<n, kJoinThreads, 0, stream>>>(p, b, join);
-    if (n > kJoinRun) markov_runs_kernel<<<(n + 31) / 32, kJoinThreads, 0, stream>>>(p, b);
+    const unsigned grid = (unsigned)((n + 63) / 64) * (64 / kMarkovWarps);   // whole words of marks
+    if (w16) markov_order_kernel<bf16_t><<<grid, kMarkovThreads, 0, stream>>>(p, b, 1);
+    else markov_order_kernel<float><<<grid, kMarkovThreads, 0, stream>>>(p, b, 3);
+    const cudaError_t e = markov_tc_launch(p, b, &join, stream);
+    if (e != cudaSuccess) return e;
+    markov_join_kernel<false><<<n, kJoinThreads, 0, stream>>>(p, b, join);
+    markov_runs_kernel<<<(n + 31) / 32, kJoinThreads, 0, stream>>>(p, b);
     return cudaGetLastError();
 }
 

@@ -9,6 +9,7 @@ namespace spec {
 constexpr int kMarkovPairs = 76;                 // CTA pairs that a tensor-core product is cut for
 constexpr int kMarkovSmall = 8;                  // rows that one pass over the weights takes
 constexpr int kMarkovSlabs = 304;                // most slabs of that pass
+constexpr int kMarkovTurn = 128;                 // entries that a CTA takes at a time
 constexpr int kJoinRun = 8;                      // rows of a token that one CTA joins
 constexpr size_t kMarkovStage = 96u << 20;       // bytes that are staged at a time, about
 
@@ -17,12 +18,13 @@ struct MarkovBind {
     int32_t* order;          // [n] the rows by (token, row); rows without a token behind all others
     int32_t* token;          // [n] their tokens in that order (V: none)
     int2* run;               // [n] there: where the token's rows begin, and how many they are
-    unsigned long long* none;   // [ceil(n / 64)] rows without a token, a bit each
+    uint8_t* none;           // [ceil(n / 64) * 8] rows without a token, a bit each
     bf16_t* ux;              // [planes][n][r8] U[x_i], 0 for a row without a token
     float* part;             // dX in parts
     float* runs;             // [n][r4] sums over kJoinRun rows of a token
-    bf16_t* zs;              // staged dz   [planes][n][columns]
-    bf16_t* ws;              // staged Wt   [planes][columns][r8]
+    int parts;               // most parts that there is room for
+    bf16_t* stage;           // slices of dz [planes][n][columns] and Wt [planes][columns][r8]
+    size_t stage_bytes;
 };
 
 __host__ __device__ inline int round8(int r) { return (r + 7) & ~7; }

@@ -162,14 +162,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMtcThreads, 1)
             bool ok = true;
             for (int it = 0; ok && mtc_item(a, it, item); ++it) {
                 const int m0 = item.tile * 256 + (int)rank * 128;
+                int term = item.k0 / a.steps, at = (item.k0 - term * a.steps) * kMtcStep;
                 for (int k = item.k0; k < item.k1; ++k, ++i) {
                     const uint32_t s = i % S;
                     ok = pair_wait(&s_empty[s], ((i / S) & 1u) ^ 1u, b.status);
                     if (!ok) break;
                     uint8_t* d = ring + (size_t)s * C::bytes;
                     mbar_arrive_expect_tx(&s_full[s], C::bytes);
-                    // (a division a step, of a small number: k / a.steps is the pair of planes)
-                    const int term = k / a.steps, at = (k - term * a.steps) * kMtcStep;
                     const int za = (int)(a.planes >> (4 * term)) & 3, zb = (int)(a.planes >> (4 * term + 2)) & 3;
 #pragma unroll
                     for (int j = 0; j < 2; ++j)
@@ -178,6 +177,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMtcThreads, 1)
 #pragma unroll
                     for (int j = 0; j < NT / 128; ++j)
                         tma_load_3d(d + (2 + j) * kMtcBox, &bmap, (int)rank * (NT / 2) + j * 64, at, zb, &s_full[s]);
+                    at += kMtcStep;
+                    if (at == a.steps * kMtcStep) {
+                        at = 0;
+                        ++term;
+                    }
                 }
             }
             // nothing may still be on its way when the CTA ends, a copy or the issuer's arrival
@@ -221,12 +225,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMtcThreads, 1)
         uint32_t i = 0;
         bool ok = true;
         for (int it = 0; ok && mtc_item(a, it, item); ++it) {
+            int row_step = item.k0 % a.steps;
             for (int k = item.k0; k < item.k1; ++k, ++i) {
                 const uint32_t s = i % S;
                 ok = mbar_wait(&s_full[s], (i / S) & 1u, b.status, kWaitLimitNs);
                 if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
                 if (!DX) {
-                    unsigned long long none = b.none[k % a.steps];   // rows of the step without a token
+                    unsigned long long none = reinterpret_cast<const unsigned long long*>(b.none)[row_step];   // rows of the step without a token
+                    if (++row_step == a.steps) row_step = 0;
                     if (none) {
                         uint4* z = reinterpret_cast<uint4*>(ring + (size_t)s * C::bytes);
                         for (; none; none &= none - 1) {   // a row is 8 words of each of the two boxes
@@ -354,14 +360,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMtcThreads, 1)
 // words, two of them shifted into place.
 template <typename T, int PLANES>
 __global__ void __launch_bounds__(256) markov_stage_kernel(const T* src, long ld, int rows, int columns, int pitch, bf16_t* out) {
-    const int words = (columns + 7) / 8;
-    const long all = (long)rows * words, step = (long)gridDim.x * 256;
-    for (long e = (long)blockIdx.x * 256 + threadIdx.x; e < all; e += step) {
-        const int row = (int)(e / words), c = (int)(e - (long)row * words) * 8;
+    const int c = (int)(blockIdx.x * blockDim.x + threadIdx.x) * 8;
+    if (c >= columns) return;
+#pragma unroll 4
+    for (int row = (int)(blockIdx.y * blockDim.y + threadIdx.y); row < rows; row += (int)(gridDim.y * blockDim.y)) {
         const T* from = src + row * ld;
         uint4 w[PLANES];
         if constexpr (sizeof(T) == 2) {
-            const RowWords<T> in(from, columns);
+            const RowWords<T> in(from, columns);   // (rows may start anywhere)
             uint4 a = in.load(c / 8), b = make_uint4(0u, 0u, 0u, 0u);
             if (in.mis && c / 8 + 1 < in.n) b = in.load(c / 8 + 1);
             uint32_t h[9] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, 0u};
@@ -399,10 +405,11 @@ __global__ void __launch_bounds__(256) markov_stage_kernel(const T* src, long ld
     }
 }
 static void mtc_stage(const void* src, int dtype, long at, long ld, int rows, int columns, int pitch, bf16_t* out, cudaStream_t stream) {
-    const long all = ((long)rows * ((columns + 7) / 8) + 255) / 256, most = 8l * device_sm_count();
-    const unsigned grid = (unsigned)(all < most ? all : most);
-    if (dtype == SPEC_BF16) markov_stage_kernel<bf16_t, 1><<<grid, 256, 0, stream>>>(reinterpret_cast<const bf16_t*>(src) + at, ld, rows, columns, pitch, out);
-    else markov_stage_kernel<float, 3><<<grid, 256, 0, stream>>>(reinterpret_cast<const float*>(src) + at, ld, rows, columns, pitch, out);
+    const dim3 block = columns <= 256 ? dim3(32, 8) : dim3(256, 1);   // a thread per 8 columns, 4 rows each
+    const unsigned x = (unsigned)((columns + 8 * block.x - 1) / (8 * block.x)), y = (unsigned)((rows + 4 * block.y - 1) / (4 * block.y));
+    const dim3 grid(x, y < 65535u ? y : 65535u);
+    if (dtype == SPEC_BF16) markov_stage_kernel<bf16_t, 1><<<grid, block, 0, stream>>>(reinterpret_cast<const bf16_t*>(src) + at, ld, rows, columns, pitch, out);
+    else markov_stage_kernel<float, 3><<<grid, block, 0, stream>>>(reinterpret_cast<const float*>(src) + at, ld, rows, columns, pitch, out);
 }
 
 static bool mtc_map(CUtensorMap* m, const void* base, int width, long rows, long pitch, int planes) {
@@ -421,9 +428,15 @@ static cudaError_t mtc_launch(const MarkovParams& p, const MarkovBind& b, Markov
     const int n = p.B * p.gamma, r8 = round8(p.r);
     const bool z16 = p.gdt == SPEC_BF16, w16 = p.wdt == SPEC_BF16;
     const bool stage_z = !z16 || p.ld % 8 != 0, stage_w = !w16 || p.r != r8;
-    const int columns = stage_z || stage_w ? markov_slice(n, p.r, p.V) : p.V;
+    // as many columns as the stage takes of what is staged
+    const size_t each = 2 * ((stage_z ? (size_t)n * (z16 ? 1 : 3) : 0) + (stage_w ? (size_t)r8 * (w16 ? 1 : 3) : 0));
+    const size_t room = each ? (b.stage_bytes - 512) / each / 256 * 256 : 0;
+    const int columns = each && room < (size_t)round8(p.V) ? (int)room : p.V;
+    bf16_t* zs = b.stage;
+    bf16_t* ws = b.stage + (stage_z ? (align256((size_t)n * (z16 ? 1 : 3) * round8(columns) * 2) / 2) : 0);
     const int pairs = device_sm_count() / 2 > 0 ? device_sm_count() / 2 : 1;
     MarkovTc dx = markov_tc_dx(n, columns);
+    if (dx.parts > b.parts) dx.parts = b.parts;
     dx.terms = z16 ? (w16 ? 1 : 3) : (w16 ? 3 : 6);
     // (A's part, B's part) of each term, the smallest products first
     if (z16) dx.planes = w16 ? 0u : 0x048u;
@@ -437,10 +450,10 @@ static cudaError_t mtc_launch(const MarkovParams& p, const MarkovBind& b, Markov
     if (!mtc_map(&umap, b.ux, p.r, n, r8, w16 ? 1 : 3)) return cudaErrorInvalidValue;
     for (int v0 = 0; v0 < p.V; v0 += columns) {
         const int width = columns < p.V - v0 ? columns : p.V - v0;
-        if (stage_z) mtc_stage(p.grad, p.gdt, v0, p.ld, n, width, round8(width), b.zs, stream);
-        if (stage_w) mtc_stage(p.Wt, p.wdt, (long)v0 * p.r, p.r, width, p.r, r8, b.ws, stream);
-        if (!mtc_map(&zmap, stage_z ? b.zs : reinterpret_cast<const bf16_t*>(p.grad) + v0, width, n, stage_z ? round8(width) : p.ld, z16 ? 1 : 3) ||
-            !mtc_map(&wmap, stage_w ? b.ws : reinterpret_cast<const bf16_t*>(p.Wt) + (long)v0 * p.r, p.r, width, r8, w16 ? 1 : 3))
+        if (stage_z) mtc_stage(p.grad, p.gdt, v0, p.ld, n, width, round8(width), zs, stream);
+        if (stage_w) mtc_stage(p.Wt, p.wdt, (long)v0 * p.r, p.r, width, p.r, r8, ws, stream);
+        if (!mtc_map(&zmap, stage_z ? zs : reinterpret_cast<const bf16_t*>(p.grad) + v0, width, n, stage_z ? round8(width) : p.ld, z16 ? 1 : 3) ||
+            !mtc_map(&wmap, stage_w ? ws : reinterpret_cast<const bf16_t*>(p.Wt) + (long)v0 * p.r, p.r, width, r8, w16 ? 1 : 3))
             return cudaErrorInvalidValue;
         MarkovTc wt = dx;
         wt.tiles = (width + 255) / 256;
