@@ -8,6 +8,7 @@
 #include "internal.h"
 #include "spec_device.cuh"
 
+#include <cuda_fp16.h>
 #include <string.h>
 #include <type_traits>
 
@@ -17,7 +18,10 @@ constexpr int kAdamThreads = 256;
 constexpr int kAdamWarps = kAdamThreads / 32;
 constexpr int kAdamUnroll = 2;                                   // blocks of a warp in flight
 constexpr int kAdamBlock = SPEC_ADAMW_BLOCK;
-constexpr int kAdamChunk = kAdamWarps * kAdamUnroll * kAdamBlock;   // entries of a CTA's turn
+constexpr int kAdamUnit = kAdamUnroll * kAdamBlock;              // entries of a warp's turn
+constexpr int kAdamChunk = kAdamWarps * kAdamUnit;               // entries of a CTA's turn
+constexpr int kAdamSpan = 16;                                    // most chunks in a row that a CTA takes
+constexpr int kAdamCtas = 4;                                     // per SM
 static_assert(kAdamBlock == 128, "a lane takes 4 entries of a block");
 
 enum { kAdamHalf = 1, kAdamGradHalf = 2, kAdamPacked = 4, kAdamVec = 8 };
@@ -36,213 +40,292 @@ template <int CAP>
 struct AdamwArgs {
     AdamwTensor t[CAP];
     int n, base;            // tensors of this launch, and the first one's index
-    unsigned chunks;
+    unsigned chunks, span;
     int advance;            // the call's last launch: step goes up
     int32_t* step;
     const float* grad_scale;
     double beta1, beta2;
     float lr, keep, eps;                // keep = 1 - lr weight_decay
     float b1, b1c, b2, b2c;             // beta, 1 - beta
-    uint32_t k0, k1;
+    uint32_t key[20];                   // Philox' round keys
     unsigned* status;
     unsigned* done;
 };
 
-// Philox4x32-10 (Salmon, Moraes, Dror, Shaw, SC'11, table 2)
-__device__ __forceinline__ uint4 philox4x32(uint32_t k0, uint32_t k1, uint64_t block, uint32_t c2, uint32_t c3) {
+// Philox4x32-10 (Salmon, Moraes, Dror, Shaw, SC'11, table 2); the round keys are the launch's.
+__device__ __forceinline__ uint4 philox4x32(const uint32_t* key, uint64_t block, uint32_t c2, uint32_t c3) {
     uint32_t c0 = (uint32_t)block, c1 = (uint32_t)(block >> 32);
 #pragma unroll
     for (int r = 0; r < 10; ++r) {
         const uint64_t a = (uint64_t)c0 * 0xD2511F53u, b = (uint64_t)c2 * 0xCD9E8D57u;
-        c0 = (uint32_t)(b >> 32) ^ c1 ^ k0;
+        c0 = (uint32_t)(b >> 32) ^ c1 ^ key[2 * r];
         c1 = (uint32_t)b;
-        c2 = (uint32_t)(a >> 32) ^ c3 ^ k1;
+        c2 = (uint32_t)(a >> 32) ^ c3 ^ key[2 * r + 1];
         c3 = (uint32_t)a;
-        k0 += 0x9E3779B9u;
-        k1 += 0xBB67AE85u;
     }
     return make_uint4(c0, c1, c2, c3);
 }
 
-// An e4m3 code's value (exact: its exponent and mantissa in a float's, then the bias).
-__device__ __forceinline__ float e4m3_value(uint32_t code) {
-    return __uint_as_float((code & 0x7fu) << 20 | (code & 0x80u) << 24) * 0x1p120f;
+// 4 entries as two pairs.
+struct Quad {
+    f2x a, b;
+    __device__ __forceinline__ Quad() {}
+    __device__ __forceinline__ Quad(f2x x, f2x y) : a(x), b(y) {}
+    __device__ __forceinline__ explicit Quad(float x) : a(f2_pack(x, x)), b(f2_pack(x, x)) {}
+    __device__ __forceinline__ Quad(float x, float y, float z, float w) : a(f2_pack(x, y)), b(f2_pack(z, w)) {}
+    __device__ __forceinline__ float4 get() const {
+        const float2 x = f2_unpack(a), y = f2_unpack(b);
+        return make_float4(x.x, x.y, y.x, y.y);
+    }
+};
+__device__ __forceinline__ Quad operator*(const Quad& x, const Quad& y) { return Quad(f2_mul(x.a, y.a), f2_mul(x.b, y.b)); }
+__device__ __forceinline__ Quad operator+(const Quad& x, const Quad& y) { return Quad(f2_add(x.a, y.a), f2_add(x.b, y.b)); }
+__device__ __forceinline__ Quad quad_fma(const Quad& x, const Quad& y, const Quad& z) {
+    return Quad(f2_fma(x.a, y.a, z.a), f2_fma(x.b, y.b, z.b));
 }
-// The code of |y| < 256, up with probability (what is left) / (the code's spacing), by 16
-// random bits added to the bits that go: below 2^-6 those of a fixed-point number, above it
-// the mantissa's, whose carry goes into the exponent.
+
+// e4m3 codes' values.
+__device__ __forceinline__ Quad e4m3_values(uint32_t codes) {
+    uint32_t lo, hi;
+    asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n cvt.rn.f16x2.e4m3x2 %1, b;\n}"
+        : "=r"(lo), "=r"(hi) : "r"(codes));
+    const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&lo)), y = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+    return Quad(x.x, x.y, y.x, y.y);
+}
+// The code of |y| < 256 in the top byte, up with probability (what is left) / (the code's spacing): 16
+// random bits (at bits 8-23) are added to the bits below, and the carry goes up.  A float's exponent
+// and mantissa, less the difference of the biases, are the code and 20 bits; below 2^-6, where
+// the spacing stays 2^-9, those of |y| + 2^-6 less its own code are.  Each is the larger where it holds.
 __device__ __forceinline__ uint32_t e4m3_random(float y, uint32_t random) {
-    const uint32_t u = __float_as_uint(y) & 0x7fffffffu;
-    const uint32_t normal = ((u + (random << 4)) >> 20) - 960u;
-    const uint32_t small = ((uint32_t)(__uint_as_float(u) * 0x1p25f) + random) >> 16;
-    return u >= 0x3c800000u ? normal : small;
+    const int n = (int)((__float_as_uint(y) & 0x7fffffffu) - (960u << 20));
+    const int d = (int)(__float_as_uint(__fadd_rz(fabsf(y), 0x1p-6f)) - (968u << 20));
+    return ((uint32_t)max(n, d) << 4) + random;
+}
+__device__ __forceinline__ uint32_t top_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    return __byte_perm(__byte_perm(a, b, 0x0073), __byte_perm(c, d, 0x0073), 0x5410);
 }
 
 struct AdamwHyper {
     float b1, b1c, b2, b2c, keep, eps, size, root, clip;
-    uint32_t k0, k1, T;
+    const uint32_t* key;
+    uint32_t T;
 };
 
-// One entry: m and v (`packed`: v is its root) replaced, the new parameter returned.  Products and
-// sums are rounded one by one, in the order of the formulas, so that a state held in 8 bits is
-// the same whatever a compiler fuses: a code must not depend on that.
+// 4 entries: m and v (PACKED: v is its root) and the parameter replaced.  Products and sums that a
+// state comes from are rounded one by one, in the order of the formulas, so that a code does not
+// depend on what a compiler fuses.  What the parameter alone sees (the root's and the quotient's
+// last bits, 2^-22 of a step) is not.
 template <bool PACKED>
-__device__ __forceinline__ float adam_entry(const AdamwHyper& h, float p, float g, float& m, float& v, bool& bad) {
-    g = __fmul_rn(g, h.clip);
-    const float v0 = PACKED ? __fmul_rn(v, v) : v;
-    const float m1 = __fadd_rn(__fmul_rn(m, h.b1), __fmul_rn(g, h.b1c));
-    const float v1 = __fadd_rn(__fmul_rn(v0, h.b2), __fmul_rn(__fmul_rn(g, h.b2c), g));
-    if (!(fabsf(m1) < INFINITY && v1 < INFINITY)) {   // g is not finite, or too large
-        bad = true;
-        return p;
-    }
-    const float r = PACKED ? __fsqrt_rn(v1) : sqrtf(v1);
-    m = m1;
-    v = PACKED ? r : v1;
-    return p * h.keep - h.size * __fdividef(m1, fmaf(r, h.root, h.eps));
-}
-
-// 4 neighbouring entries of an array, n of them in it (VEC: whole words where all are)
-template <bool VEC, typename T>
-__device__ __forceinline__ void load4(const T* a, int n, float (&o)[4]) {
-    if (VEC && n == 4) {
-        if constexpr (sizeof(T) == 4) {
-            const float4 w = __ldcs(reinterpret_cast<const float4*>(a));
-            o[0] = w.x; o[1] = w.y; o[2] = w.z; o[3] = w.w;
-        } else {
-            const uint2 w = __ldcs(reinterpret_cast<const uint2*>(a));
-            o[0] = __uint_as_float(w.x << 16); o[1] = __uint_as_float(w.x & 0xffff0000u);
-            o[2] = __uint_as_float(w.y << 16); o[3] = __uint_as_float(w.y & 0xffff0000u);
-        }
-        return;
-    }
-#pragma unroll
-    for (int k = 0; k < 4; ++k) o[k] = k < n ? to_float(a[k]) : 0.0f;
-}
-template <bool VEC>
-__device__ __forceinline__ uint32_t load4_codes(const uint8_t* a, int n) {
-    if (VEC && n == 4) return __ldcs(reinterpret_cast<const uint32_t*>(a));
-    uint32_t w = 0u;
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-        if (k < n) w |= (uint32_t)a[k] << (8 * k);
-    return w;
-}
-template <bool VEC>
-__device__ __forceinline__ void store4(float* a, int n, const float (&x)[4]) {
-    if (VEC && n == 4) {
-        __stcs(reinterpret_cast<float4*>(a), make_float4(x[0], x[1], x[2], x[3]));
-        return;
-    }
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-        if (k < n) a[k] = x[k];
-}
-template <bool VEC>
-__device__ __forceinline__ void store4_half(bf16_t* a, int n, const float (&x)[4]) {
-    uint32_t lo, hi;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(lo) : "f"(x[1]), "f"(x[0]));
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(hi) : "f"(x[3]), "f"(x[2]));
-    if (VEC && n == 4) {
-        __stcs(reinterpret_cast<uint2*>(a), make_uint2(lo, hi));
-        return;
-    }
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-        if (k < n) a[k] = (bf16_t)((k < 2 ? lo : hi) >> (16 * (k & 1)));
-}
-template <bool VEC>
-__device__ __forceinline__ void store4_codes(uint8_t* a, int n, uint32_t w) {
-    if (VEC && n == 4) {
-        __stcs(reinterpret_cast<uint32_t*>(a), w);
-        return;
-    }
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-        if (k < n) a[k] = (uint8_t)(w >> (8 * k));
-}
-
-// 4 entries of a block in 8 bits: `top` is the lanes' largest magnitude
-template <bool ROOT>
-__device__ __forceinline__ uint32_t pack4(const float (&x)[4], const uint32_t (&random)[4], float& scale) {
-    float top = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
-    const uint32_t u = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
-    const uint32_t e = (uint32_t)max((int)(u >> 23) - 7, 1);
-    const float down = __uint_as_float((254u - e) << 23);
-    scale = __uint_as_float(e << 23);
-    uint32_t w = 0u;
+__device__ __forceinline__ bool adam_quad(const AdamwHyper& h, Quad& p, Quad g, Quad& m, Quad& v) {
+    g = g * Quad(h.clip);
+    const Quad m1 = m * Quad(h.b1) + g * Quad(h.b1c);
+    const Quad v1 = (PACKED ? v * v : v) * Quad(h.b2) + g * Quad(h.b2c) * g;
+    const float4 w = v1.get();
+    float r[4] = {w.x, w.y, w.z, w.w}, q[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-        uint32_t code = e4m3_random(x[k] * down, random[k]);
-        if (ROOT) code = x[k] > 0.0f ? max(code, 1u) : code;
-        else code |= x[k] < 0.0f ? 0x80u : 0u;
-        w |= code << (8 * k);
+        if (PACKED) r[k] = __fsqrt_rn(r[k]);
+        else asm("sqrt.approx.f32 %0, %1;" : "=f"(r[k]) : "f"(r[k]));
     }
+    const Quad root(r[0], r[1], r[2], r[3]);
+    const float4 den = quad_fma(root, Quad(h.root), Quad(h.eps)).get();
+    const float e[4] = {den.x, den.y, den.z, den.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(q[k]) : "f"(e[k]));
+    const Quad p1 = quad_fma(m1 * Quad(q[0], q[1], q[2], q[3]), Quad(-h.size), p * Quad(h.keep));
+    // 0 unless a gradient is not finite, or too large
+    const float4 x = quad_fma(m1, Quad(0.0f), v1 * Quad(0.0f)).get();
+    const bool fine = (x.x + x.y) + (x.z + x.w) == 0.0f;
+    if (fine) {
+        p = p1;
+        m = m1;
+        v = PACKED ? root : v1;
+    } else {   // those entries stay
+        const float4 a = p.get(), b = m.get(), c = v.get(), a1 = p1.get(), b1 = m1.get(), c1 = (PACKED ? root : v1).get();
+        p = Quad(x.x == 0.0f ? a1.x : a.x, x.y == 0.0f ? a1.y : a.y, x.z == 0.0f ? a1.z : a.z, x.w == 0.0f ? a1.w : a.w);
+        m = Quad(x.x == 0.0f ? b1.x : b.x, x.y == 0.0f ? b1.y : b.y, x.z == 0.0f ? b1.z : b.z, x.w == 0.0f ? b1.w : b.w);
+        v = Quad(x.x == 0.0f ? c1.x : c.x, x.y == 0.0f ? c1.y : c.y, x.z == 0.0f ? c1.z : c.z, x.w == 0.0f ? c1.w : c.w);
+    }
+    return !fine;
+}
+
+// 4 entries of a block in 8 bits, their sign beside 7 bits (ROOT: none, and 0 only for 0: a root above 0
+// is 2^-75 at least, whose bits are above 2^24).  m takes the low half of a random word, v the high one.
+template <bool ROOT>
+__device__ __forceinline__ uint32_t pack4(const Quad& v, const uint4& random, float& scale) {
+    const float4 x = v.get();
+    const float top = fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(x.z), fabsf(x.w)));
+    const uint32_t u = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
+    const uint32_t e = (uint32_t)max((int)(u >> 23) - 7, 1);
+    scale = __uint_as_float(e << 23);
+    const float4 y4 = (v * Quad(__uint_as_float((254u - e) << 23))).get();
+    const float y[4] = {y4.x, y4.y, y4.z, y4.w}, z[4] = {x.x, x.y, x.z, x.w};
+    const uint32_t rnd[4] = {random.x, random.y, random.z, random.w};
+    uint32_t code[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        code[k] = e4m3_random(y[k], __byte_perm(rnd[k], 0u, ROOT ? 0x4324 : 0x4104));
+        if (ROOT) code[k] = max(code[k], min(__float_as_uint(z[k]), 1u << 24));
+    }
+    uint32_t w = top_bytes(code[0], code[1], code[2], code[3]);
+    if (!ROOT)
+        w |= top_bytes(__float_as_uint(z[0]), __float_as_uint(z[1]), __float_as_uint(z[2]), __float_as_uint(z[3])) & 0x80808080u;
     return w;
 }
 
-template <bool HALF, bool GRAD16, bool PACKED, bool VEC>
-__device__ __forceinline__ bool adam_blocks(const AdamwTensor& t, const AdamwHyper& h, int index, long at, int lane) {
+template <typename T> __device__ __forceinline__ Quad load4(const T* a) {
+    if constexpr (sizeof(T) == 4) {
+        const float4 w = __ldcs(reinterpret_cast<const float4*>(a));
+        return Quad(w.x, w.y, w.z, w.w);
+    } else {
+        const uint2 w = __ldcs(reinterpret_cast<const uint2*>(a));
+        return Quad(bf2_widen(w.x), bf2_widen(w.y));
+    }
+}
+__device__ __forceinline__ uint2 half4(const float4& x) {
+    uint2 w;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w.x) : "f"(x.y), "f"(x.x));
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w.y) : "f"(x.w), "f"(x.z));
+    return w;
+}
+
+// A warp's turn of whole blocks, every access a word of 4 entries.  Lane l holds the scales of the l-th
+// block from a line of 32 on; `block` is the turn's first one's place in it.  (Addresses are formed anew
+// at every turn: kept in registers, eight pointers spill.)
+template <bool HALF, bool GRAD16, bool PACKED>
+__device__ __forceinline__ bool adam_blocks(const AdamwTensor& t, const AdamwHyper& h, int index, long at, int lane,
+                                            int block, float& m_scale, float& v_scale) {
     typedef typename std::conditional<GRAD16, bf16_t, float>::type G;
-    float p[kAdamUnroll][4], g[kAdamUnroll][4], m[kAdamUnroll][4], v[kAdamUnroll][4];
+    Quad p[kAdamUnroll], g[kAdamUnroll], m[kAdamUnroll], v[kAdamUnroll];
     uint32_t cm[kAdamUnroll], cv[kAdamUnroll];
-    float sm[kAdamUnroll], sv[kAdamUnroll];
     bool bad = false;
+    const long first = at + lane * 4;
+    float* tp = t.p + first;
+    const G* tg = reinterpret_cast<const G*>(t.grad) + first;
+    uint8_t *m8 = reinterpret_cast<uint8_t*>(t.m) + first, *v8 = reinterpret_cast<uint8_t*>(t.v) + first;
+    float *m32 = reinterpret_cast<float*>(t.m) + first, *v32 = reinterpret_cast<float*>(t.v) + first;
 #pragma unroll
     for (int q = 0; q < kAdamUnroll; ++q) {
-        const long i = at + q * kAdamBlock + lane * 4;
-        const int n = (int)max(0l, min(4l, t.n - i));
-        load4<VEC>(t.p + i, n, p[q]);
-        load4<VEC>(reinterpret_cast<const G*>(t.grad) + i, n, g[q]);
+        p[q] = load4(tp + q * kAdamBlock);
+        g[q] = load4(tg + q * kAdamBlock);
         if (PACKED) {
-            cm[q] = load4_codes<VEC>(reinterpret_cast<const uint8_t*>(t.m) + i, n);
-            cv[q] = load4_codes<VEC>(reinterpret_cast<const uint8_t*>(t.v) + i, n);
-            const long b = at / kAdamBlock + q;
-            const bool some = b * kAdamBlock < t.n;
-            sm[q] = some ? t.m_scale[b] : 0.0f;
-            sv[q] = some ? t.v_scale[b] : 0.0f;
+            cm[q] = __ldcs(reinterpret_cast<const uint32_t*>(m8 + q * kAdamBlock));
+            cv[q] = __ldcs(reinterpret_cast<const uint32_t*>(v8 + q * kAdamBlock));
         } else {
-            load4<VEC>(reinterpret_cast<const float*>(t.m) + i, n, m[q]);
-            load4<VEC>(reinterpret_cast<const float*>(t.v) + i, n, v[q]);
+            m[q] = load4(m32 + q * kAdamBlock);
+            v[q] = load4(v32 + q * kAdamBlock);
         }
     }
 #pragma unroll
     for (int q = 0; q < kAdamUnroll; ++q) {
-        const long i = at + q * kAdamBlock + lane * 4;
-        const int n = (int)max(0l, min(4l, t.n - i));
-        float x[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            if (PACKED) {
-                m[q][k] = e4m3_value((cm[q] >> (8 * k)) & 0xffu) * sm[q];
-                v[q][k] = e4m3_value((cv[q] >> (8 * k)) & 0x7fu) * sv[q];
-            }
-            x[k] = adam_entry<PACKED>(h, p[q][k], g[q][k], m[q][k], v[q][k], bad);
-        }
-        store4<VEC>(t.p + i, n, x);
-        if (HALF) store4_half<VEC>(t.half + i, n, x);
         if (PACKED) {
-            const uint4 w = philox4x32(h.k0, h.k1, (uint64_t)i / 4, h.T, (uint32_t)index);
-            const uint32_t lo[4] = {w.x & 0xffffu, w.y & 0xffffu, w.z & 0xffffu, w.w & 0xffffu};
-            const uint32_t hi[4] = {w.x >> 16, w.y >> 16, w.z >> 16, w.w >> 16};
+            m[q] = e4m3_values(cm[q]) * Quad(__shfl_sync(0xffffffffu, m_scale, block + q));
+            v[q] = e4m3_values(cv[q]) * Quad(__shfl_sync(0xffffffffu, v_scale, block + q));
+        }
+        bad |= adam_quad<PACKED>(h, p[q], g[q], m[q], v[q]);
+        const float4 x = p[q].get();
+        __stcs(reinterpret_cast<float4*>(tp + q * kAdamBlock), x);
+        if (HALF) __stcs(reinterpret_cast<uint2*>(t.half + first + q * kAdamBlock), half4(x));
+        if (PACKED) {
+            const uint4 w = philox4x32(h.key, (uint64_t)(first + q * kAdamBlock) / 4, h.T, (uint32_t)index);
             float a, b;
-            const uint32_t wm = pack4<false>(m[q], lo, a), wv = pack4<true>(v[q], hi, b);
-            store4_codes<VEC>(reinterpret_cast<uint8_t*>(t.m) + i, n, wm);
-            store4_codes<VEC>(reinterpret_cast<uint8_t*>(t.v) + i, n, wv);
-            if (lane == 0 && n > 0) {
-                t.m_scale[at / kAdamBlock + q] = a;
-                t.v_scale[at / kAdamBlock + q] = b;
-            }
+            __stcs(reinterpret_cast<uint32_t*>(m8 + q * kAdamBlock), pack4<false>(m[q], w, a));
+            __stcs(reinterpret_cast<uint32_t*>(v8 + q * kAdamBlock), pack4<true>(v[q], w, b));
+            m_scale = lane == block + q ? a : m_scale;
+            v_scale = lane == block + q ? b : v_scale;
         } else {
-            store4<VEC>(reinterpret_cast<float*>(t.m) + i, n, m[q]);
-            store4<VEC>(reinterpret_cast<float*>(t.v) + i, n, v[q]);
+            __stcs(reinterpret_cast<float4*>(m32 + q * kAdamBlock), m[q].get());
+            __stcs(reinterpret_cast<float4*>(v32 + q * kAdamBlock), v[q].get());
+        }
+    }
+    return bad;
+}
+
+// A warp's turns from entry `at` on: `turns` of them, 32 blocks at a time, whose scales are a line.
+template <bool HALF, bool GRAD16, bool PACKED>
+__device__ __forceinline__ bool adam_turns(const AdamwTensor& t, const AdamwHyper& h, int index, long at, int turns, int lane) {
+    bool bad = false;
+    while (turns > 0) {
+        const int now = min(turns, 32 / kAdamUnroll);
+        const bool mine = PACKED && lane < now * kAdamUnroll;
+        const long b = at / kAdamBlock + lane;
+        float ms = mine ? t.m_scale[b] : 0.0f, vs = mine ? t.v_scale[b] : 0.0f;
+#pragma unroll 1
+        for (int q = 0; q < now; ++q, at += kAdamUnit)
+            bad |= adam_blocks<HALF, GRAD16, PACKED>(t, h, index, at, lane, q * kAdamUnroll, ms, vs);
+        if (mine) {
+            t.m_scale[b] = ms;
+            t.v_scale[b] = vs;
+        }
+        turns -= now;
+    }
+    return bad;
+}
+
+// A block entry by entry: a tensor's end, or one that does not lie on whole words.
+static __device__ __noinline__ bool adam_edge(const AdamwTensor& t, const AdamwHyper& h, int index, long at, int lane) {
+    float p[4], g[4], m[4], v[4];
+    const long first = at + lane * 4;
+    const int n = (int)max(0l, min(4l, t.n - first));
+    const bool packed = t.kind & kAdamPacked;
+    uint8_t *m8 = reinterpret_cast<uint8_t*>(t.m) + first, *v8 = reinterpret_cast<uint8_t*>(t.v) + first;
+    float *m32 = reinterpret_cast<float*>(t.m) + first, *v32 = reinterpret_cast<float*>(t.v) + first;
+    uint32_t cm = 0u, cv = 0u;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {   // (what is beyond the end is all 0, and stays)
+        p[k] = g[k] = m[k] = v[k] = 0.0f;
+        if (k >= n) continue;
+        p[k] = t.p[first + k];
+        g[k] = t.kind & kAdamGradHalf ? to_float(reinterpret_cast<const bf16_t*>(t.grad)[first + k])
+                                      : reinterpret_cast<const float*>(t.grad)[first + k];
+        if (packed) {
+            cm |= (uint32_t)m8[k] << (8 * k);
+            cv |= (uint32_t)v8[k] << (8 * k);
+        } else {
+            m[k] = m32[k];
+            v[k] = v32[k];
+        }
+    }
+    Quad pq(p[0], p[1], p[2], p[3]), mq(m[0], m[1], m[2], m[3]), vq(v[0], v[1], v[2], v[3]);
+    const Quad gq(g[0], g[1], g[2], g[3]);
+    bool bad;
+    if (packed) {
+        mq = e4m3_values(cm) * Quad(t.m_scale[at / kAdamBlock]);
+        vq = e4m3_values(cv) * Quad(t.v_scale[at / kAdamBlock]);
+        bad = adam_quad<true>(h, pq, gq, mq, vq);
+        const uint4 w = philox4x32(h.key, (uint64_t)first / 4, h.T, (uint32_t)index);
+        float a, b;
+        cm = pack4<false>(mq, w, a);
+        cv = pack4<true>(vq, w, b);
+        __syncwarp();   // every lane has read the scales
+        if (lane == 0) {
+            t.m_scale[at / kAdamBlock] = a;
+            t.v_scale[at / kAdamBlock] = b;
+        }
+    } else {
+        bad = adam_quad<false>(h, pq, gq, mq, vq);
+    }
+    const float4 x = pq.get(), y = mq.get(), z = vq.get();
+    const float xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w}, zs[4] = {z.x, z.y, z.z, z.w};
+    const uint2 hw = half4(x);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        if (k >= n) continue;
+        t.p[first + k] = xs[k];
+        if (t.kind & kAdamHalf) t.half[first + k] = (bf16_t)((k < 2 ? hw.x : hw.y) >> (16 * (k & 1)));
+        if (packed) {
+            m8[k] = (uint8_t)(cm >> (8 * k));
+            v8[k] = (uint8_t)(cv >> (8 * k));
+        } else {
+            m32[k] = ys[k];
+            v32[k] = zs[k];
         }
     }
     return bad;
 }
 
 template <int CAP>
-__global__ void __launch_bounds__(kAdamThreads, 3) adamw_kernel(const __grid_constant__ AdamwArgs<CAP> a) {
+__global__ void __launch_bounds__(kAdamThreads, kAdamCtas) adamw_kernel(const __grid_constant__ AdamwArgs<CAP> a) {
     __shared__ float s_size, s_root;
     __shared__ int s_step;
     if (threadIdx.x == 0) {
@@ -265,29 +348,40 @@ __global__ void __launch_bounds__(kAdamThreads, 3) adamw_kernel(const __grid_con
     h.b1 = a.b1; h.b1c = a.b1c; h.b2 = a.b2; h.b2c = a.b2c;
     h.keep = a.keep; h.eps = a.eps; h.size = s_size; h.root = s_root;
     h.clip = a.grad_scale ? *a.grad_scale : 1.0f;
-    h.k0 = a.k0; h.k1 = a.k1; h.T = (uint32_t)step + 1u;
+    h.key = a.key; h.T = (uint32_t)step + 1u;
     bool bad = false;
-    for (unsigned c = blockIdx.x; fine && c < a.chunks; c += gridDim.x) {
-        int lo = 0, hi = a.n - 1;   // the last tensor that begins at or before chunk c
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (a.t[mid].first <= c) lo = mid; else hi = mid - 1;
-        }
-        const AdamwTensor& t = a.t[lo];
-        const long at = (long)(c - t.first) * kAdamChunk + warp * (kAdamUnroll * kAdamBlock);
-        if (at >= t.n) continue;
-        const int index = a.base + lo;
-        switch (t.kind) {
-#define SPEC_ADAM_CASE(K)                                                                                   \
-    case K:                                                                                                 \
-        bad |= adam_blocks<((K) & kAdamHalf) != 0, ((K) & kAdamGradHalf) != 0, ((K) & kAdamPacked) != 0,    \
-                           ((K) & kAdamVec) != 0>(t, h, index, at, lane);                                   \
+    int at_tensor = 0;
+    // a.span chunks in a row at a time: what is looked up per tensor is spread over them
+    for (unsigned long long c0 = (unsigned long long)blockIdx.x * a.span; fine && c0 < a.chunks; c0 += (unsigned long long)gridDim.x * a.span) {
+        unsigned c = (unsigned)c0;
+        const unsigned end = (unsigned)min((unsigned long long)a.chunks, c0 + a.span);
+        while (c < end) {
+            while (at_tensor + 1 < a.n && a.t[at_tensor + 1].first <= c) ++at_tensor;   // the one that chunk c is of
+            const AdamwTensor& t = a.t[at_tensor];
+            const int index = a.base + at_tensor;
+            const unsigned kind = t.kind;
+            const long start = (long)(c - t.first) * kAdamChunk, left = t.n - start;
+            const int whole = kind & kAdamVec ? (int)min((long)(end - c), left / kAdamChunk) : 0;
+            if (whole == 0) {   // a tensor's end, or any part of one that is not aligned: its blocks over the warps
+                const long stop = min(t.n, start + kAdamChunk);
+                for (long e = start + warp * kAdamBlock; e < stop; e += kAdamWarps * kAdamBlock)
+                    bad |= adam_edge(t, h, index, e, lane);
+                ++c;
+                continue;
+            }
+            c += (unsigned)whole;
+            // a warp's entries lie in a row (a scale's sector, written by one warp in time: 394 us; by several: 480)
+            const long at = start + (long)warp * whole * kAdamUnit;
+            switch (kind & 7u) {
+#define SPEC_ADAM_CASE(K)                                                                                             \
+    case K:                                                                                                           \
+        bad |= adam_turns<((K) & kAdamHalf) != 0, ((K) & kAdamGradHalf) != 0, ((K) & kAdamPacked) != 0>(t, h, index,  \
+                                                                                                      at, whole, lane); \
         break;
-            SPEC_ADAM_CASE(0) SPEC_ADAM_CASE(1) SPEC_ADAM_CASE(2) SPEC_ADAM_CASE(3)
-            SPEC_ADAM_CASE(4) SPEC_ADAM_CASE(5) SPEC_ADAM_CASE(6) SPEC_ADAM_CASE(7)
-            SPEC_ADAM_CASE(8) SPEC_ADAM_CASE(9) SPEC_ADAM_CASE(10) SPEC_ADAM_CASE(11)
-            SPEC_ADAM_CASE(12) SPEC_ADAM_CASE(13) SPEC_ADAM_CASE(14) SPEC_ADAM_CASE(15)
+                SPEC_ADAM_CASE(0) SPEC_ADAM_CASE(1) SPEC_ADAM_CASE(2) SPEC_ADAM_CASE(3)
+                SPEC_ADAM_CASE(4) SPEC_ADAM_CASE(5) SPEC_ADAM_CASE(6) SPEC_ADAM_CASE(7)
 #undef SPEC_ADAM_CASE
+            }
         }
     }
     if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(a.status, SPEC_DEV_NONFINITE);
@@ -314,11 +408,13 @@ static cudaError_t adamw_typed(const AdamwCall& c, cudaStream_t stream) {
     a.b1c = (float)(1.0 - c.beta1);
     a.b2 = (float)c.beta2;
     a.b2c = (float)(1.0 - c.beta2);
-    a.k0 = (uint32_t)c.seed;
-    a.k1 = (uint32_t)(c.seed >> 32);
+    for (uint32_t r = 0; r < 10; ++r) {
+        a.key[2 * r] = (uint32_t)c.seed + r * 0x9E3779B9u;
+        a.key[2 * r + 1] = (uint32_t)(c.seed >> 32) + r * 0xBB67AE85u;
+    }
     a.status = &reinterpret_cast<WsHeader*>(c.ws)->status;
     a.done = &reinterpret_cast<WsHeader*>(c.ws)->done[0];
-    const unsigned most = (unsigned)device_sm_count() * 3u;
+    const unsigned most = (unsigned)(device_sm_count() * kAdamCtas);
     int i = 0;
     do {
         a.base = i;
@@ -348,7 +444,11 @@ static cudaError_t adamw_typed(const AdamwCall& c, cudaStream_t stream) {
         }
         a.chunks = (unsigned)chunks;
         a.advance = i >= c.n_tensors;
-        const unsigned grid = chunks < most ? (chunks ? (unsigned)chunks : 1u) : most;
+        // enough spans that the CTAs end within a few per cent of one another
+        const unsigned span = a.chunks / (most * 8u);
+        a.span = span < 1u ? 1u : (span < (unsigned)kAdamSpan ? span : (unsigned)kAdamSpan);
+        const unsigned spans = (a.chunks + a.span - 1) / a.span;
+        const unsigned grid = spans < most ? (spans ? spans : 1u) : most;
         adamw_kernel<CAP><<<grid, kAdamThreads, 0, stream>>>(a);
         const cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;
