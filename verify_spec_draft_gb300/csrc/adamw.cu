@@ -79,7 +79,11 @@ struct Quad {
     }
 };
 __device__ __forceinline__ Quad operator*(const Quad& x, const Quad& y) { return Quad(f2_mul(x.a, y.a), f2_mul(x.b, y.b)); }
-__device__ __forceinline__ Quad operator+(const Quad& x, const Quad& y) { return Quad(f2_add(x.a, y.a), f2_add(x.b, y.b)); }
+// (by fours: a product of pairs and a sum of pairs are fused, whatever their rounding is given as)
+__device__ __forceinline__ Quad operator+(const Quad& x, const Quad& y) {
+    const float4 a = x.get(), b = y.get();
+    return Quad(__fadd_rn(a.x, b.x), __fadd_rn(a.y, b.y), __fadd_rn(a.z, b.z), __fadd_rn(a.w, b.w));
+}
 __device__ __forceinline__ Quad quad_fma(const Quad& x, const Quad& y, const Quad& z) {
     return Quad(f2_fma(x.a, y.a, z.a), f2_fma(x.b, y.b, z.b));
 }
