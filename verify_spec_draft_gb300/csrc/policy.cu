@@ -13,9 +13,8 @@
 
 namespace spec {
 
-constexpr int kPolThreads = 256;
-constexpr int kPolWarps = kPolThreads / 32;
-constexpr int kPolBatch = 4;                       // words a thread takes at once
+constexpr int kPolThreads(int mode) { return mode == 0 ? 128 : 256; }
+constexpr int kPolBatch(int mode) { return mode == 1 ? 4 : 8; }   // words a thread takes at once
 constexpr int kPolChunks = 4;                      // copies of a slice
 constexpr int kPolMaxCluster = 16;
 
@@ -47,10 +46,14 @@ __device__ __forceinline__ unsigned cluster_size() {
 }
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_put(float2* here, unsigned rank, float2 v) {
-    uint32_t a;
+// A pair into the place `here` of CTA `rank`, whose barrier `bar` counts its 8 bytes.  (A cluster barrier
+// with release would wait for all of the last row's gradient to be written first.)
+__device__ __forceinline__ void cluster_put(float2* here, uint64_t* bar, unsigned rank, float2 v) {
+    uint32_t a, b;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(here)), "r"(rank));
-    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" :: "r"(a), "f"(v.x), "f"(v.y) : "memory");
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(b) : "r"(smem_u32(bar)), "r"(rank));
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];"
+                 :: "r"(a), "f"(v.x), "f"(v.y), "r"(b) : "memory");
 }
 
 // What the row's CTAs make of its statistics (each for itself).
@@ -98,193 +101,269 @@ __device__ __forceinline__ PolRow policy_row(const PolicyParams& p, float2 T, co
 }
 
 // MODE: 0 the loss alone; 1 with the gradient, the slice kept in shared memory; 2 with the gradient,
-// the slice read again (it is too large to keep)
-template <typename T, int MODE>
-__global__ void __launch_bounds__(kPolThreads) policy_kernel(const __grid_constant__ PolicyParams p) {
-    constexpr int E = 16 / (int)sizeof(T);
+// the slice read again (it is too large to keep).  A cluster takes one row in n_clusters; in MODE 1 the
+// next row's slice is on its way as soon as every thread has read the last of this one's.
+template <typename T, int MODE, bool ALIGNED>
+__global__ void __launch_bounds__(kPolThreads(MODE)) policy_kernel(const __grid_constant__ PolicyParams p) {
+    constexpr int E = 16 / (int)sizeof(T), TH = kPolThreads(MODE), WARPS = TH / 32, BATCH = kPolBatch(MODE);
     extern __shared__ __align__(128) uint8_t s_slice[];
-    __shared__ __align__(8) uint64_t s_full[kPolChunks];
-    __shared__ float2 s_pair[kPolMaxCluster], s_warp[kPolWarps];
+    __shared__ __align__(8) uint64_t s_full[kPolChunks], s_met[2];
+    __shared__ float2 s_pair[2][kPolMaxCluster], s_warp[WARPS];
     __shared__ PolRow s_row;
     __shared__ int s_late;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const unsigned rank = cluster_rank(), size = cluster_size();
-    const int row = (int)(blockIdx.x / size);
+    const int n_clusters = (int)(gridDim.x / size);
     const float c = p.scale;
-    cluster_arrive();   // so that no CTA writes into one that has not begun
-    const float wt = p.weight ? p.weight[row] : 1.0f;
-    const T* z = reinterpret_cast<const T*>(p.logits) + (long)row * p.ld;
-    T* d = reinterpret_cast<T*>(p.grad_out) + (long)row * p.ld;
-    const RowWords<T> in(z, p.V);
-    const int first = (int)rank * p.slice, n = max(0, min(in.n - first, p.slice));
-    if (wt == 0.0f) {
-        cluster_wait();
-        if (MODE)
-            for (int l = tid; l < n; l += kPolThreads) in.store(d, first + l, make_uint4(0u, 0u, 0u, 0u));
-        if (rank == 0 && tid == 0) p.loss_out[row] = p.logp_out[row] = 0.0f;
-        return;
-    }
-    // whole words [a, b) of the slice
-    const int a = n > 0 && !in.whole(first) ? 1 : 0;
-    const int b = n > a && !in.whole(first + n - 1) ? n - 1 : max(n, a);
     uint4* slot = reinterpret_cast<uint4*>(s_slice);
-    const int per = ((n + kPolChunks - 1) / kPolChunks + 7) & ~7;   // words of a copy
-    if (MODE == 1) {
+    if (tid == 0) {
+        for (int q = 0; q < kPolChunks; ++q) mbar_init(&s_full[q], 1);
+        for (int q = 0; q < 2; ++q) mbar_init(&s_met[q], 1);
+        s_late = 0;
+        fence_mbar_init();
+    }
+    __syncthreads();
+    cluster_arrive();   // so that no CTA writes into one that has not begun
+    // a row's slice: words [first, first + n) of the row, whole words [a, b) of those
+    auto row_of = [&](int row) { return SegWords<T, ALIGNED>(reinterpret_cast<const T*>(p.logits) + (long)row * p.ld, p.V); };
+    const int first = (int)rank * p.slice;
+    auto words_of = [&](const SegWords<T, ALIGNED>& in) { return max(0, min(in.n() - first, p.slice)); };
+    auto per_of = [&](int n) { return ((n + kPolChunks - 1) / kPolChunks + 7) & ~7; };   // words of a copy
+    auto weight_of = [&](int row) { return row < p.rows ? (p.weight ? p.weight[row] : 1.0f) : 0.0f; };
+    auto issue = [&](int row) {   // (all threads; the slot is free)
+        const SegWords<T, ALIGNED> in = row_of(row);
+        const int n = words_of(in), per = per_of(n);
+        const int a = !ALIGNED && n > 0 && !in.r.whole(first) ? 1 : 0;
+        const int b = !ALIGNED && n > a && !in.r.whole(first + n - 1) ? n - 1 : max(n, a);
         if (tid == 0) {
-            for (int q = 0; q < kPolChunks; ++q) mbar_init(&s_full[q], 1);
-            s_late = 0;
-            fence_mbar_init();
             for (int q = 0; q < kPolChunks; ++q) {
                 const int lo = max(a, q * per), hi = min(b, (q + 1) * per);
                 if (lo < hi) {
                     mbar_arrive_expect_tx(&s_full[q], (unsigned)(hi - lo) * 16u);
-                    bulk_g2s(slot + lo, in.p + in.entry(first + lo), (unsigned)(hi - lo) * 16u, &s_full[q]);
+                    bulk_g2s(slot + lo, in.r.p + in.entry(first + lo), (unsigned)(hi - lo) * 16u, &s_full[q]);
                 } else {
                     mbar_arrive1(&s_full[q]);
                 }
             }
-        } else if (tid == 1 && a > 0) {
+        } else if (tid == 32 && a > 0) {
             slot[0] = in.load(first);
-        } else if (tid == 2 && b < n) {
+        } else if (tid == 64 && b < n) {
             slot[b] = in.load(first + b);
         }
-    }
-    const int x = p.tokens[row];
-    const bool token_ok = x >= 0 && x < p.V;
-    PolInputs mine = {0.0f, 0.0f, 0.0f, wt, -INFINITY, token_ok};
-    if (tid == 0) {
-        mine.old = p.old_logp[row];
-        mine.A = p.advantage[row];
-        if (p.ref_logp) mine.ref = p.ref_logp[row];
-        // before any CTA writes, as the gradient may replace the row
-        if (token_ok) {
-            if (sizeof(T) == 2) mine.zx = to_float((bf16_t)*reinterpret_cast<const volatile unsigned short*>(z + x));
-            else mine.zx = to_float(*reinterpret_cast<const volatile float*>(z + x));
-        }
-    }
-    const int xe = token_ok ? x + in.mis : -1;
-    const int xl = token_ok ? xe / E - first : -1;      // x's word in the slice (or outside it)
-    const uint32_t xbit = token_ok ? 1u << (xe % E) : 0u;
-    __syncthreads();
-
-    float m = -INFINITY, s = 0.0f;
-    auto batch = [&](int l0, int end) {
-        uint4 w[kPolBatch];
-        const uint32_t ninf = NegInf<T>::word;
-        float bm = -INFINITY;
-#pragma unroll
-        for (int q = 0; q < kPolBatch; ++q) {
-            const int l = l0 + q * kPolThreads + tid;
-            if (l < end) w[q] = MODE == 1 ? slot[l] : in.load(first + l);
-            else w[q] = make_uint4(ninf, ninf, ninf, ninf);
-            if (l == xl) w[q] = word_without<T>(w[q], xbit);
-        }
-#pragma unroll
-        for (int q = 0; q < kPolBatch; ++q) bm = f_max_nan(bm, u4_max_nan<sizeof(T)>(w[q]));
-        bm = f_max_nan(bm, m);
-        if (bm != m) {
-            s = m == -INFINITY ? 0.0f : s * ex2(pol_step(m, bm, c));
-            m = bm;
-        }
-        s += words_sum<T, kPolBatch>(w, m, c);
     };
-    bool late = false;
-    if (MODE == 1) {
-        for (int q = 0; q < kPolChunks; ++q) {
-            late |= !mbar_wait(&s_full[q], 0, p.status, kWaitLimitNs);
-            const int end = min(n, (q + 1) * per);
-            for (int l0 = q * per; l0 < end && !late; l0 += kPolThreads * kPolBatch) batch(l0, end);
+    // Warp 0: this CTA's pair to all of the cluster's, and v becomes all of theirs together; false when one
+    // did not come in time.  Places are used in turn: the pairs of row i + 2 come after every CTA's of row
+    // i + 1, which it sends when it has read those of row i.
+    auto meet = [&](int i, float2& v) {
+        float2* pairs = s_pair[i & 1];
+        uint64_t* bar = &s_met[i & 1];
+        if (MODE == 0) {   // (for the first CTA alone)
+            if (lane == 0) cluster_put(&pairs[rank], bar, 0, v);
+            if (rank != 0) return true;
+        } else if (lane < (int)size) {
+            cluster_put(&pairs[rank], bar, lane, v);
         }
-        if (late) s_late = 1;
-    } else {
-        for (int l0 = 0; l0 < n; l0 += kPolThreads * kPolBatch) batch(l0, n);
-    }
-    if (late) m = NAN;
-    {
-        float2 v = make_float2(m, s * ref_fix(m, c));
-        const float wm = warp_max_nan(v.x);
-        v = make_float2(wm, warp_sum(pol_weight(v, wm, c)));
-        if (lane == 0) s_warp[warp] = v;
-    }
-    __syncthreads();
-    cluster_wait();
-    if (warp == 0) {
-        float2 v = lane < kPolWarps ? s_warp[lane] : make_float2(-INFINITY, 0.0f);
-        const float wm = warp_max_nan(v.x);
-        v = make_float2(wm, warp_sum(pol_weight(v, wm, c)));
-        if (lane < (int)size) cluster_put(&s_pair[rank], lane, v);
-    }
-    cluster_arrive();
-    cluster_wait();
-    if (warp == 0) {
-        float2 v = lane < (int)size ? s_pair[lane] : make_float2(-INFINITY, 0.0f);
-        const float wm = warp_max_nan(v.x);
-        v = make_float2(wm, warp_sum(pol_weight(v, wm, c)));
-        if (lane == 0 && (MODE || rank == 0)) {
-            const PolRow r = policy_row(p, v, mine);
-            s_row = r;
-            if (rank == 0) {
-                p.loss_out[row] = r.loss;
-                p.logp_out[row] = r.lp;
-                if (!token_ok) atomicOr(p.status, SPEC_DEV_TOKEN);
-                else if (r.bad || (MODE && r.slope_bad)) atomicOr(p.status, SPEC_DEV_NONFINITE);
+        if (lane == 0) mbar_arrive_expect_tx(bar, size * 8u);
+        const bool here = __all_sync(0xffffffffu, mbar_wait(bar, (i >> 1) & 1, p.status, kWaitLimitNs));
+        v = lane < (int)size ? pairs[lane] : make_float2(-INFINITY, 0.0f);
+        const float m = warp_max_nan(v.x);
+        v = make_float2(m, warp_sum(pol_weight(v, m, c)));
+        return here;
+    };
+    int row = (int)(blockIdx.x / size);
+    float wt = weight_of(row);
+    if (MODE == 1 && wt != 0.0f) issue(row);
+    bool begun = false;
+    int live = 0, copies = 0;   // rows that counted so far, and those whose copies were waited for
+    for (; row < p.rows; row += n_clusters) {
+        const SegWords<T, ALIGNED> in = row_of(row);
+        T* d = reinterpret_cast<T*>(p.grad_out) + (long)row * p.ld;
+        const int n = words_of(in), next = row + n_clusters;
+        const float next_wt = weight_of(next);
+        if (wt == 0.0f) {
+            if (MODE)
+                for (int l = tid; l < n; l += TH) in.store(d, first + l, make_uint4(0u, 0u, 0u, 0u));
+            if (rank == 0 && tid == 0) p.loss_out[row] = p.logp_out[row] = 0.0f;
+            if (MODE == 1 && next_wt != 0.0f) issue(next);   // nothing is in the slot
+            wt = next_wt;
+            continue;
+        }
+        const int x = p.tokens[row];
+        const bool token_ok = x >= 0 && x < p.V;
+        PolInputs mine = {0.0f, 0.0f, 0.0f, wt, -INFINITY, token_ok};
+        if (tid == 0) {
+            mine.old = p.old_logp[row];
+            mine.A = p.advantage[row];
+            if (p.ref_logp) mine.ref = p.ref_logp[row];
+            // before any CTA writes, as the gradient may replace the row
+            if (token_ok) {
+                const T* z = in.r.p + x;
+                if (sizeof(T) == 2) mine.zx = to_float((bf16_t)*reinterpret_cast<const volatile unsigned short*>(z));
+                else mine.zx = to_float(*reinterpret_cast<const volatile float*>(z));
             }
         }
-    }
-    if (!MODE) return;
-    __syncthreads();
-    if (MODE == 1 && s_late) {   // what has not arrived may still: out of its way, bounded
-        for (int q = 0; q < kPolChunks; ++q) mbar_wait(&s_full[q], 0, p.status, kWaitLimitNs);
-    }
-    const PolRow r = s_row;
-    const float f = -r.factor;
-    const bool near = ref_near(r.ref);
-    const f2x cc = f2_pack(c, c), mm = f2_pack(-r.ref, -r.ref), ff = f2_pack(f, f);
-#pragma unroll 4
-    for (int l = tid; l < n; l += kPolThreads) {
-        const uint4 w = MODE == 1 ? slot[l] : in.load(first + l);
-        float g[E];
-        if (near) {
+        const int xe = token_ok ? x + (ALIGNED ? 0 : in.r.mis) : -1;
+        const int xl = token_ok ? xe / E - first : -1;      // x's word in the slice (or outside it)
+        const uint32_t xbit = token_ok ? 1u << (xe % E) : 0u;
+        __syncthreads();   // (the words that are not whole)
+
+        float m = -INFINITY, s = 0.0f;
+        auto batch = [&](int l0, int end) {
+            uint4 w[BATCH];
+            const uint32_t ninf = NegInf<T>::word;
+            float bm = -INFINITY;
 #pragma unroll
-            for (int k = 0; k < E; k += 2) {
-                const float2 y = f2_unpack(f2_mul(
-                    f2_ex2(f2_fma(f2_pack(word_entry<T>(w, k), word_entry<T>(w, k + 1)), cc, mm)), ff));
-                g[k] = y.x;
-                g[k + 1] = y.y;
+            for (int q = 0; q < BATCH; ++q) {
+                const int l = l0 + q * TH + tid;
+                if (l < end) w[q] = MODE == 1 ? slot[l] : in.load(first + l);
+                else w[q] = make_uint4(ninf, ninf, ninf, ninf);
+                if (l == xl) w[q] = word_without<T>(w[q], xbit);
             }
+#pragma unroll
+            for (int q = 0; q < BATCH; ++q) bm = f_max_nan(bm, u4_max_nan<sizeof(T)>(w[q]));
+            bm = f_max_nan(bm, m);
+            if (bm != m) {
+                s = m == -INFINITY ? 0.0f : s * ex2(pol_step(m, bm, c));
+                m = bm;
+            }
+            s += words_sum<T, BATCH>(w, m, c);
+        };
+        bool late = false;
+        if (MODE == 1) {
+            const int per = per_of(n);
+            for (int q = 0; q < kPolChunks; ++q) {
+                late |= !mbar_wait(&s_full[q], copies & 1, p.status, kWaitLimitNs);
+                const int end = min(n, (q + 1) * per);
+                for (int l0 = q * per; l0 < end && !late; l0 += TH * BATCH) batch(l0, end);
+            }
+            ++copies;
+            if (late) s_late = 1;
         } else {
-#pragma unroll
-            for (int k = 0; k < E; ++k) g[k] = ex2((word_entry<T>(w, k) - r.m) * c) * f;
+            for (int l0 = 0; l0 < n; l0 += TH * BATCH) batch(l0, n);
         }
-        if (l == xl) {
-#pragma unroll
-            for (int k = 0; k < E; ++k) g[k] = (xbit >> k) & 1u ? r.at_token : g[k];
+        if (late) m = NAN;
+        {
+            float2 v = make_float2(m, s * ref_fix(m, c));
+            const float wm = warp_max_nan(v.x);
+            v = make_float2(wm, warp_sum(pol_weight(v, wm, c)));
+            if (lane == 0) s_warp[warp] = v;
         }
-        in.store(d, first + l, word_of<T>(g));
+        __syncthreads();
+        if (!begun) cluster_wait();
+        begun = true;
+        if (warp == 0) {
+            float2 v = lane < WARPS ? s_warp[lane] : make_float2(-INFINITY, 0.0f);
+            const float wm = warp_max_nan(v.x);
+            v = make_float2(wm, warp_sum(pol_weight(v, wm, c)));
+            // x's logit is here before the other CTAs learn of the pair, and may write over it
+            mine.zx = __shfl_sync(0xffffffffu, mine.zx, 0);
+            if (!meet(live, v)) v.x = NAN;
+            if (lane == 0 && (MODE || rank == 0)) {
+                const PolRow r = policy_row(p, v, mine);
+                s_row = r;
+                if (rank == 0) {
+                    p.loss_out[row] = r.loss;
+                    p.logp_out[row] = r.lp;
+                    if (!token_ok) atomicOr(p.status, SPEC_DEV_TOKEN);
+                    else if (r.bad || (MODE && r.slope_bad)) atomicOr(p.status, SPEC_DEV_NONFINITE);
+                }
+            }
+        }
+        ++live;
+        wt = next_wt;
+        if (!MODE) continue;
+        __syncthreads();
+        const PolRow r = s_row;
+        const float f = -r.factor;
+        const bool near = ref_near(r.ref);
+        const f2x cc = f2_pack(c, c), mm = f2_pack(-r.ref, -r.ref), ff = f2_pack(f, f);
+#pragma unroll 4
+        for (int l = tid; l < n; l += TH) {
+            const uint4 w = MODE == 1 ? slot[l] : in.load(first + l);
+            float g[E];
+            if (near) {
+#pragma unroll
+                for (int k = 0; k < E; k += 2) {
+                    const float2 y = f2_unpack(f2_mul(
+                        f2_ex2(f2_fma(f2_pack(word_entry<T>(w, k), word_entry<T>(w, k + 1)), cc, mm)), ff));
+                    g[k] = y.x;
+                    g[k + 1] = y.y;
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < E; ++k) g[k] = ex2((word_entry<T>(w, k) - r.m) * c) * f;
+            }
+            if (l == xl) {
+#pragma unroll
+                for (int k = 0; k < E; ++k) g[k] = (xbit >> k) & 1u ? r.at_token : g[k];
+            }
+            in.store(d, first + l, word_of<T>(g));
+        }
+        if (MODE == 1 && !ALIGNED) fence_proxy_async_smem();   // words written here, before the copy that may cover them
+        __syncthreads();   // the slot has been read, and s_row and s_warp
+        if (MODE == 1) {
+            if (s_late) break;   // (the same for every thread)
+            if (next_wt != 0.0f) issue(next);
+        }
+    }
+    if (!begun) cluster_wait();
+    if (MODE == 1 && row < p.rows) {
+        // a copy has not come in time: nothing of this CTA's may still be on its way when it ends, and the
+        // rest of its rows' slices have no gradient
+        for (int q = 0; q < kPolChunks; ++q) mbar_wait(&s_full[q], (copies - 1) & 1, p.status, kWaitLimitNs);
+        for (row += n_clusters; row < p.rows; row += n_clusters) {
+            const SegWords<T, ALIGNED> in = row_of(row);
+            const uint32_t nan = sizeof(T) == 2 ? 0x7fff7fffu : 0x7fffffffu;
+            const bool on = weight_of(row) != 0.0f;
+            T* d = reinterpret_cast<T*>(p.grad_out) + (long)row * p.ld;
+            for (int l = tid, n = words_of(in); l < n; l += TH)
+                in.store(d, first + l, on ? make_uint4(nan, nan, nan, nan) : make_uint4(0u, 0u, 0u, 0u));
+            if (!on) {
+                if (rank == 0 && tid == 0) p.loss_out[row] = p.logp_out[row] = 0.0f;
+                continue;
+            }
+            float2 v = make_float2(NAN, NAN);   // the row's other CTAs are told so
+            if (warp == 0) meet(live, v);
+            ++live;
+            if (rank == 0 && tid == 0) p.loss_out[row] = p.logp_out[row] = NAN;
+        }
+    }
+    if (MODE) {   // (a CTA's memory stays until the last pair that was sent to it is in)
+        cluster_arrive();
+        cluster_wait();
     }
 }
 
-// The cluster's size: slices of 64 KB at most, so that three CTAs share an SM (one loads while
-// another forms its gradient), and more CTAs per row where the rows are too few to fill the
-// device, down to a batch of words per thread.
+// The cluster's size.  With the gradient: slices of 64 KB at most, so that three CTAs share an SM and one loads
+// while another forms its gradient (1792 rows of 248,320 bf16: 313 us; slices of 32 KB, seven CTAs: 316).
+// The loss alone keeps nothing, so a CTA takes a whole row where the rows are enough to fill the
+// device (448 rows: two CTAs a row 38 us, eight 40).  More CTAs per row where the rows are few, down to
+// a batch of words per thread.
 template <typename T>
 static cudaError_t policy_typed(PolicyParams p, cudaStream_t stream) {
     constexpr int E = 16 / (int)sizeof(T);
     const int words = (p.V + 2 * E - 2) / E;   // whatever the row's offset
+    const int sms = device_sm_count();
     int size = 1;
-    while (size < kPolMaxCluster && (words + size - 1) / size > 4096) size *= 2;
-    while (size < 8 && (long)p.rows * size < device_sm_count() && words / (2 * size) >= kPolThreads) size *= 2;
+    if (p.grad_out) {
+        while (size < kPolMaxCluster && (words + size - 1) / size > 4096) size *= 2;
+        while (size < 8 && (long)p.rows * size < sms && words / (2 * size) >= 256) size *= 2;
+    } else {
+        while (size < kPolMaxCluster && (long)p.rows * size < 5 * sms && words / (2 * size) >= 512) size *= 2;
+    }
     p.slice = (words + size - 1) / size;
     const size_t bytes = (size_t)p.slice * 16;
     const int mode = !p.grad_out ? 0 : (bytes <= 220 * 1024 ? 1 : 2);
-    const void* kern = mode == 0 ? (const void*)policy_kernel<T, 0>
-                                 : (mode == 1 ? (const void*)policy_kernel<T, 1> : (const void*)policy_kernel<T, 2>);
+    const bool fits = SegWords<T, true>::fits(p.ld, p.V);
+    const void* kerns[3][2] = {{(const void*)policy_kernel<T, 0, false>, (const void*)policy_kernel<T, 0, true>},
+                               {(const void*)policy_kernel<T, 1, false>, (const void*)policy_kernel<T, 1, true>},
+                               {(const void*)policy_kernel<T, 2, false>, (const void*)policy_kernel<T, 2, true>}};
+    const void* kern = kerns[mode][fits];
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e == cudaSuccess && mode == 1) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 220 * 1024);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)p.rows * (unsigned)size);
-    cfg.blockDim = dim3(kPolThreads);
+    cfg.blockDim = dim3((unsigned)kPolThreads(mode));
     cfg.dynamicSmemBytes = mode == 1 ? bytes : 0;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -294,6 +373,17 @@ static cudaError_t policy_typed(PolicyParams p, cudaStream_t stream) {
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
+    int clusters = p.rows;
+    if (mode == 1 && (long)p.rows * size > 2 * sms) {
+        // as many as the device holds at once (the rest would wait for a whole share of the rows)
+        int most = 0;
+        cfg.gridDim = dim3((unsigned)size);
+        e = cudaOccupancyMaxActiveClusters(&most, kern, &cfg);
+        if (e != cudaSuccess) return e;
+        if (most < 1) return cudaErrorInvalidConfiguration;
+        if (clusters > most) clusters = most;
+    }
+    cfg.gridDim = dim3((unsigned)clusters * (unsigned)size);
     void* args[] = {&p};
     e = cudaLaunchKernelExC(&cfg, kern, args);
     return e != cudaSuccess ? e : cudaGetLastError();
