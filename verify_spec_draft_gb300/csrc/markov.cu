@@ -86,8 +86,8 @@ __global__ void __launch_bounds__(kMarkovThreads) markov_order_kernel(MarkovPara
 
 // A few rows: one pass over the vocabulary forms both products.  A warp takes an entry v, its lanes
 // the r columns: dWt[v] = sum_i dz[i, v] U[x_i] with the rows' U in registers, and dX's sums, one per row
-// and column, in registers too.  Bound by memory: Wt in, dWt and dU's zeros out.  7 rows, V = 248,320,
-// r = 256: the tensor cores would spend their steps of 64 rows on zeros.
+// and column, in registers too.  Bound by memory: Wt in, dWt and dU's zeros out.  7 rows, the tensor cores
+// would spend their steps of 64 rows on zeros.
 template <typename G, typename W, int C>
 __global__ void __launch_bounds__(kMarkovThreads) markov_small_kernel(MarkovParams p, MarkovBind b) {
     constexpr int N = kMarkovSmall, kV = kMarkovTurn;
@@ -258,7 +258,8 @@ __global__ void __launch_bounds__(kJoinThreads) markov_runs_kernel(MarkovParams 
     }
 }
 
-static bool markov_small(int n) { return n <= kMarkovSmall; }
+// (the sums' registers grow with r: 5 rows of r = 256 take 285 us here, 140 on the tensor cores)
+static bool markov_small(int n, int r) { return n <= kMarkovSmall && r <= 64; }
 
 static size_t markov_bind(MarkovBind& b, void* ws, int n, int r, int V) {
     uint8_t* w = reinterpret_cast<uint8_t*>(ws);
@@ -269,7 +270,7 @@ static size_t markov_bind(MarkovBind& b, void* ws, int n, int r, int V) {
         at += align256(bytes);
         return q;
     };
-    if (markov_small(n)) {
+    if (markov_small(n, r)) {
         b.part = reinterpret_cast<float*>(take((size_t)kMarkovSlabs * n * round4(r) * 4));
         return at;
     }
@@ -298,11 +299,8 @@ static int markov_small_launch(const MarkovParams& p, const MarkovBind& b, cudaS
     int slabs = (p.V + kMarkovTurn - 1) / kMarkovTurn;
     const int most = 2 * device_sm_count() < kMarkovSlabs ? 2 * device_sm_count() : kMarkovSlabs;
     if (slabs > most) slabs = most;
-    const int C = (p.r + 31) / 32;
-    if (C <= 1) markov_small_kernel<G, W, 1><<<slabs, kMarkovThreads, 0, stream>>>(p, b);
-    else if (C <= 2) markov_small_kernel<G, W, 2><<<slabs, kMarkovThreads, 0, stream>>>(p, b);
-    else if (C <= 4) markov_small_kernel<G, W, 4><<<slabs, kMarkovThreads, 0, stream>>>(p, b);
-    else markov_small_kernel<G, W, 8><<<slabs, kMarkovThreads, 0, stream>>>(p, b);
+    if (p.r <= 32) markov_small_kernel<G, W, 1><<<slabs, kMarkovThreads, 0, stream>>>(p, b);
+    else markov_small_kernel<G, W, 2><<<slabs, kMarkovThreads, 0, stream>>>(p, b);
     return slabs;
 }
 
@@ -310,7 +308,7 @@ cudaError_t markov_grad_launch(const MarkovParams& p, void* ws, cudaStream_t str
     const int n = p.B * p.gamma;
     MarkovBind b;
     markov_bind(b, ws, n, p.r, p.V);
-    const bool small = markov_small(n), g16 = p.gdt == SPEC_BF16, w16 = p.wdt == SPEC_BF16;
+    const bool small = markov_small(n, p.r), g16 = p.gdt == SPEC_BF16, w16 = p.wdt == SPEC_BF16;
     MarkovJoin join = {0, n, round4(p.r)};
     if (small) {
         join.parts = g16 ? (w16 ? markov_small_launch<bf16_t, bf16_t>(p, b, stream) : markov_small_launch<bf16_t, float>(p, b, stream))

@@ -28,7 +28,7 @@ namespace spec {
 
 constexpr int kMtcStep = 64;                       // terms of a stage
 constexpr int kMtcBox = kMtcStep * 64 * 2;         // bytes of a [64 x 64] box
-constexpr int kMtcChunk = 32;                      // steps that one accumulator takes
+constexpr int kMtcChunk = 8;                       // steps that one accumulator takes
 constexpr int kMtcEpi = 16;
 constexpr int kMtcThreads = 32 * (3 + kMtcEpi);
 
@@ -356,57 +356,88 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMtcThreads, 1)
 }
 
 // Columns [v0, v0 + columns) of dz's rows, or rows of the weights, as bf16 planes whose rows are `pitch`
-// entries apart (a multiple of 8).  A thread takes 8 columns; bf16 rows of any offset are read as 16-byte
-// words, two of them shifted into place.
+// entries apart (a multiple of 8).  A thread takes 8 columns of four rows at once; bf16 rows of any
+// offset are read as 16-byte words, two of them shifted into place.
+constexpr int kStageRows = 4;
+__device__ __forceinline__ uint4 shifted(const uint4& a, const uint4& b, int s) {   // from entry s of a on
+    uint32_t h[9] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, 0u};
+    if (s & 4)
+#pragma unroll
+        for (int k = 0; k < 6; ++k) h[k] = h[k + 2];
+    if (s & 2)
+#pragma unroll
+        for (int k = 0; k < 5; ++k) h[k] = h[k + 1];
+    if (s & 1)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) h[k] = __funnelshift_r(h[k], h[k + 1], 16);
+    return make_uint4(h[0], h[1], h[2], h[3]);
+}
 template <typename T, int PLANES>
 __global__ void __launch_bounds__(256) markov_stage_kernel(const T* src, long ld, int rows, int columns, int pitch, bf16_t* out) {
     const int c = (int)(blockIdx.x * blockDim.x + threadIdx.x) * 8;
     if (c >= columns) return;
-#pragma unroll 4
-    for (int row = (int)(blockIdx.y * blockDim.y + threadIdx.y); row < rows; row += (int)(gridDim.y * blockDim.y)) {
-        const T* from = src + row * ld;
-        uint4 w[PLANES];
+    const int step = (int)(gridDim.y * blockDim.y);
+    const bool inside = c >= 8 && c + 16 <= columns;   // every word that is touched lies in the row
+    for (int row0 = (int)(blockIdx.y * blockDim.y + threadIdx.y); row0 < rows; row0 += kStageRows * step) {
         if constexpr (sizeof(T) == 2) {
-            const RowWords<T> in(from, columns);   // (rows may start anywhere)
-            uint4 a = in.load(c / 8), b = make_uint4(0u, 0u, 0u, 0u);
-            if (in.mis && c / 8 + 1 < in.n) b = in.load(c / 8 + 1);
-            uint32_t h[9] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, 0u};
-            const int s = in.mis;   // entries to the left of the row's first
-            if (s & 4)
+            uint4 a[kStageRows], b[kStageRows];
+            int mis[kStageRows];
 #pragma unroll
-                for (int k = 0; k < 6; ++k) h[k] = h[k + 2];
-            if (s & 2)
-#pragma unroll
-                for (int k = 0; k < 5; ++k) h[k] = h[k + 1];
-            if (s & 1)
-#pragma unroll
-                for (int k = 0; k < 4; ++k) h[k] = __funnelshift_r(h[k], h[k + 1], 16);
-            w[0] = make_uint4(h[0], h[1], h[2], h[3]);
-        } else {
-            float x[8], y[8][3];
-            if (c + 8 <= columns && (reinterpret_cast<uintptr_t>(from + c) & 15u) == 0) {
-                const float4 a = __ldcs(reinterpret_cast<const float4*>(from + c)), b = __ldcs(reinterpret_cast<const float4*>(from + c) + 1);
-                x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-                x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-            } else {
-#pragma unroll
-                for (int k = 0; k < 8; ++k) x[k] = c + k < columns ? load_one(from + c + k) : 0.0f;
+            for (int q = 0; q < kStageRows; ++q) {
+                const int row = min(row0 + q * step, rows - 1);
+                const T* from = src + row * ld;
+                mis[q] = (int)((reinterpret_cast<uintptr_t>(from) & 15u) / 2u);
+                if (inside) {
+                    const uint4* w = reinterpret_cast<const uint4*>(from - mis[q] + c);
+                    a[q] = __ldg(w);
+                    b[q] = __ldg(w + 1);
+                }
             }
 #pragma unroll
-            for (int k = 0; k < 8; ++k) bf16_parts(x[k], y[k]);
+            for (int q = 0; q < kStageRows; ++q) {
+                const int row = row0 + q * step;
+                if (row >= rows) continue;
+                if (!inside) {
+                    const RowWords<T> in(src + row * ld, columns);
+                    a[q] = in.load(c / 8);
+                    if (in.mis && c / 8 + 1 < in.n) b[q] = in.load(c / 8 + 1);
+                    else b[q] = make_uint4(0u, 0u, 0u, 0u);
+                }
+                *reinterpret_cast<uint4*>(out + (long)row * pitch + c) = shifted(a[q], b[q], mis[q]);
+            }
+        } else {
+            float x[kStageRows][8];
 #pragma unroll
-            for (int q = 0; q < PLANES; ++q) {
-                const float z[8] = {y[0][q], y[1][q], y[2][q], y[3][q], y[4][q], y[5][q], y[6][q], y[7][q]};
-                w[q] = word_of<bf16_t>(z);
+            for (int q = 0; q < kStageRows; ++q) {
+                const T* from = src + min(row0 + q * step, rows - 1) * ld + c;
+                if (inside && (reinterpret_cast<uintptr_t>(from) & 15u) == 0) {
+                    const float4 a = __ldg(reinterpret_cast<const float4*>(from)), b = __ldg(reinterpret_cast<const float4*>(from) + 1);
+                    x[q][0] = a.x; x[q][1] = a.y; x[q][2] = a.z; x[q][3] = a.w;
+                    x[q][4] = b.x; x[q][5] = b.y; x[q][6] = b.z; x[q][7] = b.w;
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) x[q][k] = c + k < columns ? load_one(from + k) : 0.0f;
+                }
+            }
+#pragma unroll
+            for (int q = 0; q < kStageRows; ++q) {
+                const int row = row0 + q * step;
+                if (row >= rows) continue;
+                float y[8][3];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) bf16_parts(x[q][k], y[k]);
+#pragma unroll
+                for (int h = 0; h < PLANES; ++h) {
+                    const float z[8] = {y[0][h], y[1][h], y[2][h], y[3][h], y[4][h], y[5][h], y[6][h], y[7][h]};
+                    *reinterpret_cast<uint4*>(out + ((long)h * rows + row) * pitch + c) = word_of<bf16_t>(z);
+                }
             }
         }
-#pragma unroll
-        for (int q = 0; q < PLANES; ++q) *reinterpret_cast<uint4*>(out + ((long)q * rows + row) * pitch + c) = w[q];
     }
 }
 static void mtc_stage(const void* src, int dtype, long at, long ld, int rows, int columns, int pitch, bf16_t* out, cudaStream_t stream) {
     const dim3 block = columns <= 256 ? dim3(32, 8) : dim3(256, 1);   // a thread per 8 columns, 4 rows each
-    const unsigned x = (unsigned)((columns + 8 * block.x - 1) / (8 * block.x)), y = (unsigned)((rows + 4 * block.y - 1) / (4 * block.y));
+    const unsigned x = (unsigned)((columns + 8 * block.x - 1) / (8 * block.x)), y = (unsigned)((rows + kStageRows * block.y - 1) / (kStageRows * block.y));
     const dim3 grid(x, y < 65535u ? y : 65535u);
     if (dtype == SPEC_BF16) markov_stage_kernel<bf16_t, 1><<<grid, block, 0, stream>>>(reinterpret_cast<const bf16_t*>(src) + at, ld, rows, columns, pitch, out);
     else markov_stage_kernel<float, 3><<<grid, block, 0, stream>>>(reinterpret_cast<const float*>(src) + at, ld, rows, columns, pitch, out);
