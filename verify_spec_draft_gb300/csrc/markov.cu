@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(kJoinThreads) markov_join_kernel(MarkovParams 
 #pragma unroll
         for (int q = 0; q < kJoinRun; ++q) index[q] = b.order[at + min(q, rows - 1)];
     }
-    if (t >= p.V) return;
+    if (SMALL && t >= p.V) return;
     const int quads = round4(p.r) / 4, groups = kJoinThreads / quads;
     const int k = threadIdx.x % quads, g = threadIdx.x / quads;
     float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -229,12 +229,21 @@ __global__ void __launch_bounds__(kJoinThreads) markov_join_kernel(MarkovParams 
             }
     }
     if (!join_meet(s_sum, s, k, g, quads, groups)) return;
+    if (!SMALL && t >= p.V) {   // rows without a token: nothing but whether they are finite
+        if (!(fabsf(s.x + s.y + s.z + s.w) < INFINITY)) *(volatile unsigned*)b.unclean = 1u;
+        return;
+    }
     if (all <= kJoinRun) join_out(p, t, k, s);
     else reinterpret_cast<float4*>(b.runs + (long)at * round4(p.r))[k] = s;
 }
+void markov_join(const MarkovParams& p, const MarkovBind& b, const MarkovJoin& a, cudaStream_t stream) {
+    markov_join_kernel<false><<<p.B * p.gamma, kJoinThreads, 0, stream>>>(p, b, a);
+}
+
 // The tokens of more rows: a CTA looks at 32 places for where one begins.
 __global__ void __launch_bounds__(kJoinThreads) markov_runs_kernel(MarkovParams p, MarkovBind b) {
     __shared__ float4 s_sum[kJoinThreads];
+    if (blockIdx.x == 0 && threadIdx.x == 0) *b.unclean = 0u;
     const int n = p.B * p.gamma;
     const int quads = round4(p.r) / 4, groups = kJoinThreads / quads;
     const int k = threadIdx.x % quads, g = threadIdx.x / quads;
@@ -264,6 +273,7 @@ static bool markov_small(int n, int r) { return n <= kMarkovSmall && r <= 64; }
 static size_t markov_bind(MarkovBind& b, void* ws, int n, int r, int V) {
     uint8_t* w = reinterpret_cast<uint8_t*>(ws);
     b.status = &reinterpret_cast<WsHeader*>(ws)->status;
+    b.unclean = &reinterpret_cast<WsHeader*>(ws)->done[0];
     size_t at = kWsHeaderBytes;
     auto take = [&](size_t bytes) {
         uint8_t* q = w + at;
@@ -281,9 +291,8 @@ static size_t markov_bind(MarkovBind& b, void* ws, int n, int r, int V) {
     const int columns = markov_slice(n, r, V);
     b.none = take((size_t)(n + 63) / 64 * 8);
     b.ux = reinterpret_cast<bf16_t*>(take((size_t)3 * n * round8(r) * 2));
-    const MarkovTc whole = markov_tc_dx(n, V), part = markov_tc_dx(n, columns);
-    b.parts = whole.parts > part.parts ? whole.parts : part.parts;
-    b.part = reinterpret_cast<float*>(take((size_t)b.parts * whole.tiles * 256 * (r > 128 ? 256 : 128) * 4));
+    const int tiles = (n + 255) / 256;
+    b.part = reinterpret_cast<float*>(take((size_t)(tiles > kMarkovItems ? tiles : kMarkovItems) * 256 * (r > 128 ? 256 : 128) * 4));
     b.stage_bytes = (size_t)6 * ((size_t)n * round8(columns) + (size_t)columns * round8(r)) + 4096;
     b.stage = reinterpret_cast<bf16_t*>(take(b.stage_bytes));
     return at;
@@ -309,8 +318,8 @@ cudaError_t markov_grad_launch(const MarkovParams& p, void* ws, cudaStream_t str
     MarkovBind b;
     markov_bind(b, ws, n, p.r, p.V);
     const bool small = markov_small(n, p.r), g16 = p.gdt == SPEC_BF16, w16 = p.wdt == SPEC_BF16;
-    MarkovJoin join = {0, n, round4(p.r)};
     if (small) {
+        MarkovJoin join = {0, n, round4(p.r)};
         join.parts = g16 ? (w16 ? markov_small_launch<bf16_t, bf16_t>(p, b, stream) : markov_small_launch<bf16_t, float>(p, b, stream))
                          : (w16 ? markov_small_launch<float, bf16_t>(p, b, stream) : markov_small_launch<float, float>(p, b, stream));
         markov_join_kernel<true><<<n, kJoinThreads, 0, stream>>>(p, b, join);
@@ -319,9 +328,8 @@ cudaError_t markov_grad_launch(const MarkovParams& p, void* ws, cudaStream_t str
     const unsigned grid = (unsigned)((n + 63) / 64) * (64 / kMarkovWarps);   // whole words of marks
     if (w16) markov_order_kernel<bf16_t><<<grid, kMarkovThreads, 0, stream>>>(p, b, 1);
     else markov_order_kernel<float><<<grid, kMarkovThreads, 0, stream>>>(p, b, 3);
-    const cudaError_t e = markov_tc_launch(p, b, &join, stream);
+    const cudaError_t e = markov_tc_launch(p, b, stream);
     if (e != cudaSuccess) return e;
-    markov_join_kernel<false><<<n, kJoinThreads, 0, stream>>>(p, b, join);
     markov_runs_kernel<<<(n + 31) / 32, kJoinThreads, 0, stream>>>(p, b);
     return cudaGetLastError();
 }

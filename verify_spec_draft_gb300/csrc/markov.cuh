@@ -19,10 +19,10 @@ struct MarkovBind {
     int32_t* token;          // [n] their tokens in that order (V: none)
     int2* run;               // [n] there: where the token's rows begin, and how many they are
     uint8_t* none;           // [ceil(n / 64) * 8] rows without a token, a bit each
+    unsigned* unclean;       // whether one holds what is not finite (returned to 0 by markov_runs_kernel)
     bf16_t* ux;              // [planes][n][r8] U[x_i], 0 for a row without a token
     float* part;             // dX in parts
     float* runs;             // [n][r4] sums over kJoinRun rows of a token
-    int parts;               // most parts that there is room for
     bf16_t* stage;           // slices of dz [planes][n][columns] and Wt [planes][columns][r8]
     size_t stage_bytes;
 };
@@ -30,21 +30,20 @@ struct MarkovBind {
 __host__ __device__ inline int round8(int r) { return (r + 7) & ~7; }
 __host__ __device__ inline int round4(int r) { return (r + 3) & ~3; }
 
-// A tensor-core product's items: tiles of 256 outputs, each in `parts` ranges of its steps.  Item
-// i is part i / tiles of tile i % tiles, and the pairs take them in order, so the tiles that
-// run at the same time go through the same steps and read B's rows from memory once.  With
-// operands in several planes (float32 values as sums of bf16) the steps run through the pairs of
-// planes, `steps` of them each.
+// A tensor-core product's items: tiles of 256 outputs, each in `parts` parts of its steps.  Item i is
+// part i / tiles of tile i % tiles, and the product's pairs take them in order.  A part takes every
+// parts-th block of `block` steps, so that all pairs go along the contraction together: what one has
+// read from memory the others find in L2.  With operands in several planes (float32 values as
+// sums of bf16) a part's steps run through the pairs of planes.
 struct MarkovTc {
-    int tiles, steps, parts;
+    int tiles, steps, parts, block;
+    int first, pairs;        // its CTA pairs
     int terms;               // pairs of planes
     unsigned planes;         // their numbers, 2 bits for A and 2 for B each, from the lowest
     int v0, v1;              // the entries that this launch covers
     int add;                 // parts are added to what is there
 };
-__host__ __device__ inline int mtc_begin(const MarkovTc& a, int part) {
-    return (int)((long)a.steps * a.terms * part / a.parts);
-}
+constexpr int kMarkovItems = 2 * kMarkovPairs;   // most parts of dX in all, where there are fewer tiles
 
 template <typename T> __device__ __forceinline__ void put(void* o, long i, float x);
 template <> __device__ __forceinline__ void put<float>(void* o, long i, float x) { reinterpret_cast<float*>(o)[i] = x; }
@@ -76,7 +75,8 @@ __host__ inline int markov_slice(int n, int r, int V) {
     const size_t most = kMarkovStage / ((size_t)(n + round8(r)) * 6) / 256 * 256;
     return most < 256 ? 256 : (most < (size_t)V ? (int)most : V);
 }
-MarkovTc markov_tc_dx(int n, int columns);
-cudaError_t markov_tc_launch(const MarkovParams& p, const MarkovBind& b, MarkovJoin* join, cudaStream_t stream);
+void markov_join(const MarkovParams& p, const MarkovBind& b, const MarkovJoin& a, cudaStream_t stream);
+// both products and the join of dX's parts
+cudaError_t markov_tc_launch(const MarkovParams& p, const MarkovBind& b, cudaStream_t stream);
 
 }  // namespace spec

@@ -2,7 +2,8 @@
 //
 //     WT:  dWt [V, r] = dz^T Ux     a tile of 256 entries, contraction over the rows
 //     DX:  dX  [n, r] = dz Wt       a tile of 256 rows, contraction over the vocabulary
-// Both are one kernel over items (an output tile and a range of 64-term steps).  A pair of CTAs
+// Both run in one kernel, some pairs of CTAs on each, and go along the vocabulary together, so that
+// dz is read from memory once.  A pair of CTAs
 // forms a tile with cta_group::2 (M = 256, N = r up to 128 or 256): each CTA brings its 128 rows
 // of A and half of B's columns, so B crosses from L2 once per pair, and the accumulator's
 // two halves lie in the two CTAs' TMEM.  Per CTA, 19 warps:
@@ -10,8 +11,8 @@
 //            with the vocabulary contiguous: as WT's A it is M-major, as DX's K-major, from the
 //            same boxes; Ux and Wt are N-major.
 //   warp 1   TMEM; in the pair's first CTA the MMA issuer
-//   warp 2   relay: a stage that has arrived here is reported to the first CTA's issuer, after the
-//            rows without a token (whose dz may hold anything) have been set to 0 (WT)
+//   warp 2   (CLEAN) sets the rows without a token, whose dz may hold anything, to 0 in a stage that has
+//            arrived, before it is reported to the first CTA's issuer
 //   warps 3-18  epilogue: a thread owns one row and a quarter of the columns
 // A tensor core's sums drop what falls below the accumulator's last bit, so a chain of steps
 // ends after kMtcChunk of them: the epilogue adds it to float32 registers while the next one runs
@@ -23,6 +24,8 @@
 // a staged copy, a slice of the vocabulary at a time that stays in L2.
 #include "markov.cuh"
 #include "tc_common.cuh"
+
+#include <string.h>
 
 namespace spec {
 
@@ -102,27 +105,54 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
     for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-// Item `it` of a pair: its tile, its steps [k0, k1) and its number.
-struct MtcItem { int tile, k0, k1, number; };
-__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
+// Item `it` of a pair: its tile, part and number, its steps for one pair of planes and in all.
+struct MtcItem { int tile, part, number, n, all; };
+// A box of a pair's CTA; `bar`, the address of a barrier of either of the two.
+__device__ __forceinline__ void pair_load_3d(void* dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
     asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
-        :: "r"(smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar)) : "memory");
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2"
+        " [%0], [%1, {%2, %3, %4}], [%5];"
+        :: "r"(smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar) : "memory");
 }
 __device__ __forceinline__ bool mtc_item(const MarkovTc& a, int it, MtcItem& o) {
-    o.number = (int)(blockIdx.x >> 1) + it * (int)(gridDim.x >> 1);
-    const int part = o.number / a.tiles;
-    o.tile = o.number - part * a.tiles;
-    o.k0 = mtc_begin(a, part);
-    o.k1 = mtc_begin(a, part + 1);
-    return part < a.parts;
+    o.number = (int)(blockIdx.x >> 1) - a.first + it * a.pairs;
+    o.part = o.number / a.tiles;
+    o.tile = o.number - o.part * a.tiles;
+    const int blocks = (a.steps + a.block - 1) / a.block, mine = o.part < blocks ? (blocks - o.part + a.parts - 1) / a.parts : 0;
+    o.n = mine * a.block - (mine > 0 && (blocks - 1) % a.parts == o.part ? blocks * a.block - a.steps : 0);
+    o.all = o.n * a.terms;
+    return o.part < a.parts;
 }
+// An item's steps in order.
+struct MtcWalk {
+    int at, in_block, left, term;
+    __device__ __forceinline__ MtcWalk(const MarkovTc& a, const MtcItem& o) : term(0) { restart(a, o); }
+    __device__ __forceinline__ void restart(const MarkovTc& a, const MtcItem& o) {
+        at = o.part * a.block;
+        in_block = 0;
+        left = o.n;
+    }
+    __device__ __forceinline__ void next(const MarkovTc& a, const MtcItem& o) {
+        ++at;
+        if (++in_block == a.block) {
+            in_block = 0;
+            at += (a.parts - 1) * a.block;
+        }
+        if (--left == 0) {
+            ++term;
+            restart(a, o);
+        }
+    }
+};
 
-template <bool DX, int NT>
+// CLEAN: WT once more, with the rows without a token as 0, where one holds what is not finite (markov_join_kernel
+// finds it in dX); U's rows for them are 0, which is enough otherwise.  (Always: 438 us of 330.)
+template <int NT, bool CLEAN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMtcThreads, 1)
     markov_tc_kernel(const __grid_constant__ MarkovParams p, const __grid_constant__ MarkovBind b,
-                     const __grid_constant__ MarkovTc a, const __grid_constant__ CUtensorMap zmap,
-                     const __grid_constant__ CUtensorMap bmap) {
+                     const __grid_constant__ MarkovTc wt, const __grid_constant__ MarkovTc dx,
+                     const __grid_constant__ CUtensorMap zmap, const __grid_constant__ CUtensorMap umap,
+                     const __grid_constant__ CUtensorMap wmap) {
     typedef Mtc<NT> C;
     constexpr int S = C::stages;
     extern __shared__ uint8_t mtc_raw[];
@@ -131,10 +161,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMtcThreads, 1)
     __shared__ uint32_t s_tmem;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const unsigned rank = blockIdx.x & 1u;
+    const bool DX = (int)(blockIdx.x >> 1) >= dx.first;
+    const MarkovTc& a = DX ? dx : wt;
+    if (CLEAN && *b.unclean == 0u) return;
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
             mbar_init(&s_full[s], 1);
-            mbar_init(&s_ready[s], 2);
+            mbar_init(&s_ready[s], CLEAN ? 2 : 1);
             mbar_init(&s_empty[s], 1);
         }
         for (int s = 0; s < 2; ++s) {
@@ -162,45 +195,45 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMtcThreads, 1)
             bool ok = true;
             for (int it = 0; ok && mtc_item(a, it, item); ++it) {
                 const int m0 = item.tile * 256 + (int)rank * 128;
-                int term = item.k0 / a.steps, at = (item.k0 - term * a.steps) * kMtcStep;
-                for (int k = item.k0; k < item.k1; ++k, ++i) {
+                MtcWalk walk(a, item);
+                for (int k = 0; k < item.all; ++k, ++i) {
                     const uint32_t s = i % S;
                     ok = pair_wait(&s_empty[s], ((i / S) & 1u) ^ 1u, b.status);
                     if (!ok) break;
                     uint8_t* d = ring + (size_t)s * C::bytes;
-                    mbar_arrive_expect_tx(&s_full[s], C::bytes);
-                    const int za = (int)(a.planes >> (4 * term)) & 3, zb = (int)(a.planes >> (4 * term + 2)) & 3;
+                    // whom the copies report to: this CTA's warp 2, or the issuer, which expects both CTAs'
+                    const uint32_t bar = CLEAN ? smem_u32(&s_full[s]) : peer_addr(&s_ready[s], 0);
+                    if (CLEAN) mbar_arrive_expect_tx(&s_full[s], C::bytes);
+                    else if (rank == 0) mbar_arrive_expect_tx(&s_ready[s], 2 * C::bytes);
+                    const int at = walk.at * kMtcStep, za = (int)(a.planes >> (4 * walk.term)) & 3, zb = (int)(a.planes >> (4 * walk.term + 2)) & 3;
 #pragma unroll
                     for (int j = 0; j < 2; ++j)
-                        if (DX) tma_load_3d(d + j * kMtcBox, &zmap, at, m0 + 64 * j, za, &s_full[s]);
-                        else tma_load_3d(d + j * kMtcBox, &zmap, m0 + 64 * j, at, za, &s_full[s]);
+                        pair_load_3d(d + j * kMtcBox, &zmap, DX ? at : m0 + 64 * j, DX ? m0 + 64 * j : at, za, bar);
 #pragma unroll
                     for (int j = 0; j < NT / 128; ++j)
-                        tma_load_3d(d + (2 + j) * kMtcBox, &bmap, (int)rank * (NT / 2) + j * 64, at, zb, &s_full[s]);
-                    at += kMtcStep;
-                    if (at == a.steps * kMtcStep) {
-                        at = 0;
-                        ++term;
-                    }
+                        pair_load_3d(d + (2 + j) * kMtcBox, DX ? &wmap : &umap, (int)rank * (NT / 2) + j * 64, at, zb, bar);
+                    walk.next(a, item);
                 }
             }
-            // nothing may still be on its way when the CTA ends, a copy or the issuer's arrival
+            // nothing may still be on its way when the CTA ends, a copy or the issuer's arrival (which follows the
+            // copies; where that did not come in time, they have had a second)
             for (uint32_t q = i > S ? i - S : 0; q < i; ++q) {
-                mbar_wait(&s_full[q % S], (q / S) & 1u, b.status, kWaitLimitNs);
+                if (CLEAN) mbar_wait(&s_full[q % S], (q / S) & 1u, b.status, kWaitLimitNs);
                 ok = ok && pair_wait(&s_empty[q % S], (q / S) & 1u, b.status);
             }
         }
     } else if (warp == 1) {
         if (lane == 0 && rank == 0) {
             // M = 256 over the pair; B N-major, A M-major in WT
-            constexpr uint32_t idesc = idesc_bf16_f32(256, NT) | (1u << 16) | (DX ? 0u : 1u << 15);
+            const uint32_t idesc = idesc_bf16_f32(256, NT) | (1u << 16) | (DX ? 0u : 1u << 15);
+            const uint64_t a_step = DX ? 32 / 16 : 2048 / 16;   // 16 terms on: within the swizzled rows, or 16 rows
             uint32_t i = 0, c = 0;
             bool ok = true;
             for (int it = 0; ok && mtc_item(a, it, item); ++it) {
-                for (int k = item.k0; ok && k < item.k1; ++c) {
+                for (int k = 0; ok && k < item.all; ++c) {
                     const uint32_t buf = c & 1u, d = tmem + buf * NT;
                     ok = pair_wait(&s_tempty[buf], ((c >> 1) & 1u) ^ 1u, b.status);
-                    const int end = min(item.k1, k + kMtcChunk);
+                    const int end = min(item.all, k + kMtcChunk);
                     tc_fence_after();
                     for (bool first = true; ok && k < end; ++k, ++i, first = false) {
                         const uint32_t s = i % S;
@@ -208,11 +241,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMtcThreads, 1)
                         if (!ok) break;
                         tc_fence_after();
                         const uint32_t sa = smem_u32(ring + (size_t)s * C::bytes), sb = sa + 2 * kMtcBox;
+                        const uint64_t da = DX ? sw128_desc(sa) : sw128_mn_desc(sa), db = sw128_mn_desc(sb);
 #pragma unroll
-                        for (int q = 0; q < kMtcStep / 16; ++q) {
-                            const uint64_t da = DX ? sw128_desc(sa + q * 32) : sw128_mn_desc(sa + q * 2048);
-                            umma2_f16(d, da, sw128_mn_desc(sb + q * 2048), idesc, first && q == 0 ? 0u : 1u);
-                        }
+                        for (int q = 0; q < kMtcStep / 16; ++q)
+                            umma2_f16(d, da + q * a_step, db + q * (2048 / 16), idesc, first && q == 0 ? 0u : 1u);
                         umma2_commit(&s_empty[s]);
                     }
                     umma2_commit(&s_tfull[buf]);
@@ -223,25 +255,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMtcThreads, 1)
         }
     } else if (warp == 2) {
         uint32_t i = 0;
-        bool ok = true;
+        bool ok = CLEAN;
         for (int it = 0; ok && mtc_item(a, it, item); ++it) {
-            int row_step = item.k0 % a.steps;
-            for (int k = item.k0; k < item.k1; ++k, ++i) {
+            MtcWalk walk(a, item);
+            unsigned long long marks = 0;   // a lane's step of 32
+            for (int k = 0; k < item.all; ++k, ++i) {
                 const uint32_t s = i % S;
+                if ((walk.at & 31) == 0) marks = walk.at + lane < a.steps ? reinterpret_cast<const unsigned long long*>(b.none)[walk.at + lane] : 0;
+                unsigned long long none = __shfl_sync(0xffffffffu, marks, walk.at & 31);   // rows of the step without a token
+                walk.next(a, item);
                 ok = mbar_wait(&s_full[s], (i / S) & 1u, b.status, kWaitLimitNs);
                 if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-                if (!DX) {
-                    unsigned long long none = reinterpret_cast<const unsigned long long*>(b.none)[row_step];   // rows of the step without a token
-                    if (++row_step == a.steps) row_step = 0;
-                    if (none) {
-                        uint4* z = reinterpret_cast<uint4*>(ring + (size_t)s * C::bytes);
-                        for (; none; none &= none - 1) {   // a row is 8 words of each of the two boxes
-                            const int row = __ffsll((long long)none) - 1;
-                            if (lane < 16) z[(lane >> 3) * (kMtcBox / 16) + row * 8 + (lane & 7)] = make_uint4(0u, 0u, 0u, 0u);
-                        }
-                        fence_proxy_async_smem();
-                        __syncwarp();
+                if (none) {
+                    uint4* z = reinterpret_cast<uint4*>(ring + (size_t)s * C::bytes);
+                    for (; none; none &= none - 1) {   // a row is 8 words of each of the two boxes
+                        const int row = __ffsll((long long)none) - 1;
+                        if (lane < 16) z[(lane >> 3) * (kMtcBox / 16) + row * 8 + (lane & 7)] = make_uint4(0u, 0u, 0u, 0u);
                     }
+                    fence_proxy_async_smem();
+                    asm volatile("fence.acq_rel.cluster;" ::: "memory");
+                    __syncwarp();
                 }
                 if (lane == 0) remote_arrive(&s_ready[s], 0);
             }
@@ -256,7 +289,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMtcThreads, 1)
             float acc[W];
 #pragma unroll
             for (int q = 0; q < W; ++q) acc[q] = 0.0f;
-            for (int k = item.k0; ok && k < item.k1; k += kMtcChunk, ++c) {
+            for (int k = 0; ok && k < item.all; k += kMtcChunk, ++c) {
                 const uint32_t buf = c & 1u;
                 ok = pair_wait(&s_tfull[buf], (c >> 1) & 1u, b.status);
                 if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
@@ -336,6 +369,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMtcThreads, 1)
                     }
                     __syncwarp();
                 }
+                if (CLEAN) continue;
                 // dU's rows of the same entries, which lie one behind the other, as 0
                 // (they start on 64 bytes, as 32 entries do; the last may end anywhere)
                 const long from = (long)v0 * p.r, to = (long)min(a.v1, v0 + 32) * p.r;
@@ -357,7 +391,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMtcThreads, 1)
 
 // Columns [v0, v0 + columns) of dz's rows, or rows of the weights, as bf16 planes whose rows are `pitch`
 // entries apart (a multiple of 8).  A thread takes 8 columns of four rows at once; bf16 rows of any
-// offset are read as 16-byte words, two of them shifted into place.
+// offset are read as 16-byte words, two of them shifted into place.  Rows that `none` marks become 0.
 constexpr int kStageRows = 4;
 __device__ __forceinline__ uint4 shifted(const uint4& a, const uint4& b, int s) {   // from entry s of a on
     uint32_t h[9] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, 0u};
@@ -373,7 +407,8 @@ __device__ __forceinline__ uint4 shifted(const uint4& a, const uint4& b, int s) 
     return make_uint4(h[0], h[1], h[2], h[3]);
 }
 template <typename T, int PLANES>
-__global__ void __launch_bounds__(256) markov_stage_kernel(const T* src, long ld, int rows, int columns, int pitch, bf16_t* out) {
+__global__ void __launch_bounds__(256) markov_stage_kernel(const T* src, long ld, int rows, int columns, int pitch, bf16_t* out,
+                                                           const uint8_t* none) {
     const int c = (int)(blockIdx.x * blockDim.x + threadIdx.x) * 8;
     if (c >= columns) return;
     const int step = (int)(gridDim.y * blockDim.y);
@@ -403,7 +438,8 @@ __global__ void __launch_bounds__(256) markov_stage_kernel(const T* src, long ld
                     if (in.mis && c / 8 + 1 < in.n) b[q] = in.load(c / 8 + 1);
                     else b[q] = make_uint4(0u, 0u, 0u, 0u);
                 }
-                *reinterpret_cast<uint4*>(out + (long)row * pitch + c) = shifted(a[q], b[q], mis[q]);
+                const bool off = none && (none[row >> 3] >> (row & 7)) & 1;
+                *reinterpret_cast<uint4*>(out + (long)row * pitch + c) = off ? make_uint4(0u, 0u, 0u, 0u) : shifted(a[q], b[q], mis[q]);
             }
         } else {
             float x[kStageRows][8];
@@ -424,8 +460,9 @@ __global__ void __launch_bounds__(256) markov_stage_kernel(const T* src, long ld
                 const int row = row0 + q * step;
                 if (row >= rows) continue;
                 float y[8][3];
+                const bool off = none && (none[row >> 3] >> (row & 7)) & 1;
 #pragma unroll
-                for (int k = 0; k < 8; ++k) bf16_parts(x[q][k], y[k]);
+                for (int k = 0; k < 8; ++k) bf16_parts(off ? 0.0f : x[q][k], y[k]);
 #pragma unroll
                 for (int h = 0; h < PLANES; ++h) {
                     const float z[8] = {y[0][h], y[1][h], y[2][h], y[3][h], y[4][h], y[5][h], y[6][h], y[7][h]};
@@ -435,12 +472,13 @@ __global__ void __launch_bounds__(256) markov_stage_kernel(const T* src, long ld
         }
     }
 }
-static void mtc_stage(const void* src, int dtype, long at, long ld, int rows, int columns, int pitch, bf16_t* out, cudaStream_t stream) {
+static void mtc_stage(const void* src, int dtype, long at, long ld, int rows, int columns, int pitch, bf16_t* out,
+                      const uint8_t* none, cudaStream_t stream) {
     const dim3 block = columns <= 256 ? dim3(32, 8) : dim3(256, 1);   // a thread per 8 columns, 4 rows each
     const unsigned x = (unsigned)((columns + 8 * block.x - 1) / (8 * block.x)), y = (unsigned)((rows + kStageRows * block.y - 1) / (kStageRows * block.y));
     const dim3 grid(x, y < 65535u ? y : 65535u);
-    if (dtype == SPEC_BF16) markov_stage_kernel<bf16_t, 1><<<grid, block, 0, stream>>>(reinterpret_cast<const bf16_t*>(src) + at, ld, rows, columns, pitch, out);
-    else markov_stage_kernel<float, 3><<<grid, block, 0, stream>>>(reinterpret_cast<const float*>(src) + at, ld, rows, columns, pitch, out);
+    if (dtype == SPEC_BF16) markov_stage_kernel<bf16_t, 1><<<grid, block, 0, stream>>>(reinterpret_cast<const bf16_t*>(src) + at, ld, rows, columns, pitch, out, none);
+    else markov_stage_kernel<float, 3><<<grid, block, 0, stream>>>(reinterpret_cast<const float*>(src) + at, ld, rows, columns, pitch, out, none);
 }
 
 static bool mtc_map(CUtensorMap* m, const void* base, int width, long rows, long pitch, int planes) {
@@ -454,8 +492,46 @@ static bool mtc_map(CUtensorMap* m, const void* base, int width, long rows, long
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The pairs of each product and dX's parts: the fewest steps in a line, over the parts and the rounds that
+// dX's items take on its pairs.  A tile of dWt takes its steps, or the time its rows and dU's take to be written
+// (16 steps for 256 x 256 float32 of both); an item's start and end count as 12 steps, a part's share of the join
+// as a quarter.  A part takes blocks of as many steps as dWt's pairs pass meanwhile.
+static void mtc_plan(int n, int columns, int r, int out_size, int terms, int pairs, MarkovTc& wt, MarkovTc& dx) {
+    memset(&wt, 0, sizeof(wt));
+    memset(&dx, 0, sizeof(dx));
+    wt.tiles = (columns + 255) / 256;
+    wt.steps = wt.block = (n + kMtcStep - 1) / kMtcStep;
+    wt.parts = 1;
+    dx.tiles = (n + 255) / 256;
+    dx.steps = (columns + kMtcStep - 1) / kMtcStep;
+    wt.terms = dx.terms = terms;
+    double best = -1.0;
+    const double written = 16.0 * r * out_size / 1024.0;
+    for (int parts = 1; parts <= dx.steps && (parts == 1 || parts * dx.tiles <= kMarkovItems); ++parts)
+        for (int rounds = 1; rounds <= 4; ++rounds) {
+            const int items = parts * dx.tiles, dp = (items + rounds - 1) / rounds, wp = pairs - dp;
+            if (wp < 1 || (rounds > 1 && dp == (items + rounds - 2) / (rounds - 1))) continue;
+            const double tile = wt.steps * terms > written ? wt.steps * terms : written;
+            const double w = (double)((wt.tiles + wp - 1) / wp) * (tile + 1.0) + 12.0;
+            const double d = rounds * ((double)((dx.steps + parts - 1) / parts) * terms + 12.0);
+            const double cost = (w > d ? w : d) + 0.25 * items;
+            if (best < 0.0 || cost < best) {
+                best = cost;
+                dx.parts = parts;
+                dx.pairs = dp;
+            }
+        }
+    const int left = pairs - dx.pairs;
+    wt.first = 0;
+    wt.pairs = wt.tiles < left ? wt.tiles : left;
+    dx.first = wt.pairs;
+    const int pass = 4 * wt.pairs / dx.parts < 1 ? 1 : 4 * wt.pairs / dx.parts;   // (256 entries are 4 steps)
+    const int share = (dx.steps + dx.parts - 1) / dx.parts, blocks = (share + pass / 2) / pass < 1 ? 1 : (share + pass / 2) / pass;
+    dx.block = (share + blocks - 1) / blocks;
+}
+
 template <int NT>
-static cudaError_t mtc_launch(const MarkovParams& p, const MarkovBind& b, MarkovJoin* join, cudaStream_t stream) {
+static cudaError_t mtc_launch(const MarkovParams& p, const MarkovBind& b, cudaStream_t stream) {
     const int n = p.B * p.gamma, r8 = round8(p.r);
     const bool z16 = p.gdt == SPEC_BF16, w16 = p.wdt == SPEC_BF16;
     const bool stage_z = !z16 || p.ld % 8 != 0, stage_w = !w16 || p.r != r8;
@@ -465,64 +541,48 @@ static cudaError_t mtc_launch(const MarkovParams& p, const MarkovBind& b, Markov
     const int columns = each && room < (size_t)round8(p.V) ? (int)room : p.V;
     bf16_t* zs = b.stage;
     bf16_t* ws = b.stage + (stage_z ? (align256((size_t)n * (z16 ? 1 : 3) * round8(columns) * 2) / 2) : 0);
-    const int pairs = device_sm_count() / 2 > 0 ? device_sm_count() / 2 : 1;
-    MarkovTc dx = markov_tc_dx(n, columns);
-    if (dx.parts > b.parts) dx.parts = b.parts;
-    dx.terms = z16 ? (w16 ? 1 : 3) : (w16 ? 3 : 6);
+    const int pairs = device_sm_count() / 2 > kMarkovPairs ? kMarkovPairs : (device_sm_count() / 2 > 2 ? device_sm_count() / 2 : 2);
+    const int terms = z16 ? (w16 ? 1 : 3) : (w16 ? 3 : 6);
     // (A's part, B's part) of each term, the smallest products first
-    if (z16) dx.planes = w16 ? 0u : 0x048u;
-    else dx.planes = w16 ? 0x012u : 0x041528u;
-    auto kw = markov_tc_kernel<false, NT>;
-    auto kx = markov_tc_kernel<true, NT>;
-    cudaError_t e = cudaFuncSetAttribute(kw, cudaFuncAttributeMaxDynamicSharedMemorySize, Mtc<NT>::smem);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(kx, cudaFuncAttributeMaxDynamicSharedMemorySize, Mtc<NT>::smem);
+    const unsigned planes = z16 ? (w16 ? 0u : 0x048u) : (w16 ? 0x012u : 0x041528u);
+    MarkovTc wt, dx;
+    mtc_plan(n, columns, p.r, p.odt == SPEC_BF16 ? 2 : 4, terms, pairs, wt, dx);
+    wt.planes = dx.planes = planes;
+    auto kern = markov_tc_kernel<NT, false>;
+    auto clean = markov_tc_kernel<NT, true>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Mtc<NT>::smem);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(clean, cudaFuncAttributeMaxDynamicSharedMemorySize, Mtc<NT>::smem);
     if (e != cudaSuccess) return e;
     CUtensorMap zmap, umap, wmap;
     if (!mtc_map(&umap, b.ux, p.r, n, r8, w16 ? 1 : 3)) return cudaErrorInvalidValue;
     for (int v0 = 0; v0 < p.V; v0 += columns) {
         const int width = columns < p.V - v0 ? columns : p.V - v0;
-        if (stage_z) mtc_stage(p.grad, p.gdt, v0, p.ld, n, width, round8(width), zs, stream);
-        if (stage_w) mtc_stage(p.Wt, p.wdt, (long)v0 * p.r, p.r, width, p.r, r8, ws, stream);
+        if (stage_z) mtc_stage(p.grad, p.gdt, v0, p.ld, n, width, round8(width), zs, b.none, stream);
+        if (stage_w) mtc_stage(p.Wt, p.wdt, (long)v0 * p.r, p.r, width, p.r, r8, ws, nullptr, stream);
         if (!mtc_map(&zmap, stage_z ? zs : reinterpret_cast<const bf16_t*>(p.grad) + v0, width, n, stage_z ? round8(width) : p.ld, z16 ? 1 : 3) ||
             !mtc_map(&wmap, stage_w ? ws : reinterpret_cast<const bf16_t*>(p.Wt) + (long)v0 * p.r, p.r, width, r8, w16 ? 1 : 3))
             return cudaErrorInvalidValue;
-        MarkovTc wt = dx;
         wt.tiles = (width + 255) / 256;
-        wt.steps = (n + kMtcStep - 1) / kMtcStep;
-        wt.parts = 1;
-        wt.v0 = v0;
-        wt.v1 = v0 + width;
         dx.steps = (width + kMtcStep - 1) / kMtcStep;
-        dx.v0 = v0;
-        dx.v1 = v0 + width;
+        wt.v0 = dx.v0 = v0;
+        wt.v1 = dx.v1 = v0 + width;
         dx.add = v0 > 0;
-        const int items = dx.tiles * dx.parts;
-        kw<<<2 * (wt.tiles < pairs ? wt.tiles : pairs), kMtcThreads, Mtc<NT>::smem, stream>>>(p, b, wt, zmap, umap);
-        kx<<<2 * (items < pairs ? items : pairs), kMtcThreads, Mtc<NT>::smem, stream>>>(p, b, dx, zmap, wmap);
+        kern<<<2 * (wt.pairs + dx.pairs), kMtcThreads, Mtc<NT>::smem, stream>>>(p, b, wt, dx, zmap, umap, wmap);
     }
-    *join = {dx.parts, (long)dx.tiles * 256, NT};
+    markov_join(p, b, {dx.parts, (long)dx.tiles * 256, NT}, stream);
+    if (!stage_z) {   // (a staged row without a token is 0)
+        if (!mtc_map(&zmap, p.grad, p.V, n, p.ld, 1)) return cudaErrorInvalidValue;
+        wt.tiles = (p.V + 255) / 256;
+        wt.v0 = 0;
+        wt.v1 = p.V;
+        wt.pairs = dx.first = wt.tiles < pairs ? wt.tiles : pairs;
+        clean<<<2 * wt.pairs, kMtcThreads, Mtc<NT>::smem, stream>>>(p, b, wt, dx, zmap, umap, umap);
+    }
     return cudaGetLastError();
 }
 
-// The parts of the contraction over the vocabulary: the fewest steps in a line over all pairs, an item's
-// start and end counted as 12, a part's share in the join as 1/4 a tile (1792 rows: 10 parts of 7 tiles on 76
-// pairs; one share of all steps per pair, whatever its tile, read Wt from memory 7 times: 269 us).
-MarkovTc markov_tc_dx(int n, int columns) {
-    MarkovTc a = {(n + 255) / 256, (columns + kMtcStep - 1) / kMtcStep, 1, 1, 0u, 0, columns, 0};
-    double best = 0.0;
-    for (int s = 1; s <= 128 && s <= a.steps && (s == 1 || s * a.tiles <= 4 * kMarkovPairs); ++s) {
-        const double rounds = (s * a.tiles + kMarkovPairs - 1) / kMarkovPairs;
-        const double cost = rounds * ((a.steps + s - 1) / s + 12.0) + 0.25 * s * a.tiles;
-        if (s == 1 || cost < best) {
-            best = cost;
-            a.parts = s;
-        }
-    }
-    return a;
-}
-
-cudaError_t markov_tc_launch(const MarkovParams& p, const MarkovBind& b, MarkovJoin* join, cudaStream_t stream) {
-    return p.r > 128 ? mtc_launch<256>(p, b, join, stream) : mtc_launch<128>(p, b, join, stream);
+cudaError_t markov_tc_launch(const MarkovParams& p, const MarkovBind& b, cudaStream_t stream) {
+    return p.r > 128 ? mtc_launch<256>(p, b, stream) : mtc_launch<128>(p, b, stream);
 }
 
 }  // namespace spec
