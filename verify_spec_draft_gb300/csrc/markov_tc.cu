@@ -146,7 +146,7 @@ struct MtcWalk {
 };
 
 // CLEAN: WT once more, with the rows without a token as 0, where one holds what is not finite (markov_join_kernel
-// finds it in dX); U's rows for them are 0, which is enough otherwise.  (Always: 438 us of 330.)
+// finds it in dX); U's rows for them are 0, which is enough otherwise.  (Done always, by a relay of every stage, it cost 100 us of 440.)
 template <int NT, bool CLEAN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMtcThreads, 1)
     markov_tc_kernel(const __grid_constant__ MarkovParams p, const __grid_constant__ MarkovBind b,
@@ -494,8 +494,8 @@ static bool mtc_map(CUtensorMap* m, const void* base, int width, long rows, long
 
 // The pairs of each product and dX's parts: the fewest steps in a line, over the parts and the rounds that
 // dX's items take on its pairs.  A tile of dWt takes its steps, or the time its rows and dU's take to be written
-// (16 steps for 256 x 256 float32 of both); an item's start and end count as 12 steps, a part's share of the join
-// as a quarter.  A part takes blocks of as many steps as dWt's pairs pass meanwhile.
+// (8 steps for 256 x 256 float32 of both); an item's start and end count as 12 steps, a part's share of the join
+// as half a one.  A part takes blocks of as many steps as dWt's pairs pass meanwhile.
 static void mtc_plan(int n, int columns, int r, int out_size, int terms, int pairs, MarkovTc& wt, MarkovTc& dx) {
     memset(&wt, 0, sizeof(wt));
     memset(&dx, 0, sizeof(dx));
@@ -506,7 +506,7 @@ static void mtc_plan(int n, int columns, int r, int out_size, int terms, int pai
     dx.steps = (columns + kMtcStep - 1) / kMtcStep;
     wt.terms = dx.terms = terms;
     double best = -1.0;
-    const double written = 16.0 * r * out_size / 1024.0;
+    const double written = 8.0 * r * out_size / 1024.0;
     for (int parts = 1; parts <= dx.steps && (parts == 1 || parts * dx.tiles <= kMarkovItems); ++parts)
         for (int rounds = 1; rounds <= 4; ++rounds) {
             const int items = parts * dx.tiles, dp = (items + rounds - 1) / rounds, wp = pairs - dp;
@@ -514,7 +514,7 @@ static void mtc_plan(int n, int columns, int r, int out_size, int terms, int pai
             const double tile = wt.steps * terms > written ? wt.steps * terms : written;
             const double w = (double)((wt.tiles + wp - 1) / wp) * (tile + 1.0) + 12.0;
             const double d = rounds * ((double)((dx.steps + parts - 1) / parts) * terms + 12.0);
-            const double cost = (w > d ? w : d) + 0.25 * items;
+            const double cost = (w > d ? w : d) + 0.5 * items;
             if (best < 0.0 || cost < best) {
                 best = cost;
                 dx.parts = parts;
