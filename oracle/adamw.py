@@ -53,9 +53,9 @@ def philox4x32(key, counter):
     return c
 
 
-def random16(seed, n, T, tensor):
-    """The 16-bit random numbers of entries 0..n-1: (for m, for v)."""
-    i = np.arange(n, dtype=np.uint64)
+def random16(seed, n, T, tensor, first=0):
+    """The 16-bit random numbers of entries first..first+n-1: (for m, for v)."""
+    i = np.arange(n, dtype=np.uint64) + np.uint64(first)
     b = i // np.uint64(4)
     zero = np.zeros(n, dtype=np.uint64)
     w = philox4x32((seed & 0xFFFFFFFF, (seed >> 32) & 0xFFFFFFFF),

@@ -219,6 +219,34 @@ def test_tensors_without_entries(spec):
     assert int(step) == 2
 
 
+@pytest.mark.parametrize("bits", [32, 8])
+def test_entries_past_32_bits(spec, bits):
+    """A tensor of 2.2e9 entries: its ends and the entries around 2^31 against a short tensor's."""
+    n = (1 << 31) + 5003
+    p, g = torch.zeros(n, device="cuda"), torch.zeros(n, dtype=BF16, device="cuda")
+    s = vsd.adamw_state(p, bits)
+    parts = [slice(0, 1024), slice((1 << 31) - 1024, (1 << 31) + 1024), slice(n - 1024 - n % 128, n)]
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    for a in parts:
+        p[a], g[a] = torch.randn(a.stop - a.start, generator=gen, device="cuda"), torch.randn(a.stop - a.start, generator=gen, device="cuda")
+    before = [(p[a].clone(), g[a].clone(), {k: (x[a] if x.numel() == n else x[a.start // 128:(a.stop + 127) // 128]).clone()
+                                           for k, x in s.items()}) for a in parts]
+    r = vsd.adamw(vsd.adamw_table([p], [g], [s]), torch.zeros(1, dtype=torch.int32, device="cuda"), **HYPER)
+    assert vsd.device_status(r["ws"]) == 0
+    for a, b in zip(parts, before):
+        after = (p[a], {k: (x[a] if x.numel() == n else x[a.start // 128:(a.stop + 127) // 128]) for k, x in s.items()})
+        if bits == 32:
+            check_step(b, after, 1, **HYPER)
+        else:   # the random numbers are those of the entries' own places
+            keep = oa.random16
+            try:
+                oa.random16 = lambda seed, m, T, tensor: keep(seed, m, T, tensor, a.start)
+                check_step(b, after, 1, **HYPER)
+            finally:
+                oa.random16 = keep
+    assert (p[2048:1 << 20] == 0).all() and (s["m"][2048:1 << 20].float() == 0).all()
+
+
 def test_refusals(spec):
     p, g, s = make(300, F32, F32, 32, seed=6)
     h, hg, hs = make(300, BF16, BF16, 8, seed=6)

@@ -90,10 +90,11 @@ def test_one_token_everywhere(spec, dt, r):
     check(got, want, 270, 700, F32)
 
 
-@pytest.mark.parametrize("dt,r", [(F32, 20), (BF16, 64), (BF16, 128)])
-def test_rows_without_a_token(spec, dt, r):
+@pytest.mark.parametrize("dt,r,V", [(F32, 20, 900), (BF16, 64, 900), (BF16, 128, 900), (BF16, 64, 904), (BF16, 192, 904),
+                                    (F32, 100, 904)])
+def test_rows_without_a_token(spec, dt, r, V):
     """Their dz may hold anything; tokens out of range are reported."""
-    a = list(inputs(6, 5, 900, r, dt, dt, seed=5))
+    a = list(inputs(6, 5, V, r, dt, dt, seed=5))
     a[1][2] = -1
     a[2][2] = -1
     prev = torch.cat([a[1][:, None], a[2][:, :-1]], 1)
@@ -101,16 +102,31 @@ def test_rows_without_a_token(spec, dt, r):
     a[0][prev < 0] = torch.nan
     got = vsd.markov_grad(*on_gpu(*a), dtype=F32)
     want = om.markov_grad(*(t.double().numpy() if t.is_floating_point() else t.numpy() for t in a))
-    check(got, want, 30, 900, F32)
+    check(got, want, 30, V, F32)
     assert vsd.device_status(got["ws"]) == 0
-    a[2][0, 0] = 900
+    # the next call with this workspace, on rows that are all finite
+    clean = [t.clone() for t in a]
+    clean[0][prev < 0] = 1.0
+    again = vsd.markov_grad(*on_gpu(*clean), dtype=F32, ws=got["ws"])
+    assert torch.equal(again["U"], got["U"]) and torch.equal(again["Wt"], got["Wt"])
+    a[2][0, 0] = V
     a[1][1] = -7
     a[0][0, 1] = torch.inf
     a[0][1, 0] = torch.nan
     got = vsd.markov_grad(*on_gpu(*a), dtype=F32)
     want = om.markov_grad(*(t.double().numpy() if t.is_floating_point() else t.numpy() for t in a))
-    check(got, want, 30, 900, F32)
+    check(got, want, 30, V, F32)
     assert vsd.device_status(got["ws"]) == vsd.DEV_TOKEN
+
+
+@pytest.mark.parametrize("V,r", [(1, 1), (2, 7), (7, 65), (63, 8), (64, 256), (65, 130)])
+@pytest.mark.parametrize("dt", [F32, BF16])
+def test_tiny_vocabularies(spec, V, r, dt):
+    """Smaller than a box of the copies, with more rows than one pass takes."""
+    a = inputs(4, 5, V, r, dt, dt, seed=V)
+    got = vsd.markov_grad(*on_gpu(*a), dtype=F32)
+    want = om.markov_grad(*(t.double().numpy() if t.is_floating_point() else t.numpy() for t in a))
+    check(got, want, 20, V, F32)
 
 
 @pytest.mark.parametrize("dt", [F32, BF16])
@@ -128,10 +144,14 @@ def test_gamma_one_needs_no_tokens(spec):
     assert torch.equal(one["U"], two["U"]) and torch.equal(one["Wt"], two["Wt"])
 
 
-@pytest.mark.parametrize("B,G,V,r", [(256, 7, 20000, 256), (61, 15, 31111, 192), (1, 7, 248320, 256)])
-def test_larger(spec, B, G, V, r):
+# the training batch's width; odd rows in one slice and in several; float32 in several slices; one block; many
+# tiles of rows over few entries, in one round and in four
+@pytest.mark.parametrize("B,G,V,r,dt", [
+    (256, 7, 20000, 256, BF16), (61, 15, 31111, 192, BF16), (256, 7, 30001, 256, BF16), (100, 5, 40001, 64, F32),
+    (1, 7, 248320, 256, BF16), (1300, 7, 1500, 64, BF16), (1024, 64, 300, 8, BF16)])
+def test_larger(spec, B, G, V, r, dt):
     """Against float64 products on the GPU."""
-    a = inputs(B, G, V, r, BF16, BF16, seed=8)
+    a = inputs(B, G, V, r, dt, dt, seed=8)
     g = on_gpu(*a)
     got = vsd.markov_grad(*g, dtype=F32)
     prev = torch.cat([g[1][:, None], g[2][:, :-1]], 1).reshape(-1).long()
@@ -143,6 +163,28 @@ def test_larger(spec, B, G, V, r):
         z = torch.zeros((V, r), dtype=torch.float64, device="cuda")
         want["U" + k] = z.index_add_(0, prev[on], f(d) @ f(w)).cpu().numpy()
     check(got, want, B * G, V, F32)
+    assert vsd.device_status(got["ws"]) == 0
+
+
+def test_rows_past_32_bits(spec):
+    """2.2e9 entries of dz: the last rows, the last entries."""
+    B, G, V, r = 1250, 7, 248320, 64
+    dz = torch.zeros((B, G, V), dtype=BF16, device="cuda")
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    dz[B - 1] = torch.randn((G, V), generator=gen, device="cuda")
+    dz[:, :, V - 3:] = 0.5
+    U, Wt = (torch.randn((V, r), generator=gen, device="cuda").to(BF16) for _ in range(2))
+    anchor = torch.arange(B, dtype=torch.int32, device="cuda")
+    tokens = torch.full((B, G), V - 1, dtype=torch.int32, device="cuda")
+    got = vsd.markov_grad(dz, anchor, tokens, U, Wt, dtype=F32)
+    x = dz[B - 1, 0].double() @ Wt.double()
+    bar = (V / 8 + 64) * 2.0 ** -24 * (dz[B - 1, 0].double().abs() @ Wt.double().abs())
+    assert ((got["U"][B - 1].double() - x).abs() <= bar).all()
+    last = dz[:, :, V - 1].double().reshape(-1)
+    rows = U[torch.cat([anchor[:, None], tokens[:, :-1]], 1).reshape(-1).long()].double()
+    bar = (B * G + 16) * 2.0 ** -24 * (last.abs() @ rows.abs())
+    assert ((got["Wt"][V - 1].double() - last @ rows).abs() <= bar).all()
+    assert vsd.device_status(got["ws"]) == 0
 
 
 def test_refusals(spec):

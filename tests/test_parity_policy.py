@@ -48,6 +48,7 @@ def check(d, got, want, t, kl, grad=True):
     e = 2.0 ** -24
     z, x, w = d["z"].cpu().double().numpy(), d["x"].numpy(), d["w"].double().numpy()
     R, V = z.shape
+    np.seterr(invalid="ignore")   # rows without an answer are left out of the comparisons
     zt = (58 + V / 512) * e
     on = np.isfinite(want["loss"])
     gap = np.abs(z.max(1) - z[np.arange(R), np.clip(x, 0, V - 1)]) / t
@@ -189,9 +190,35 @@ def test_largest_rows(spec, dtype, V):
     assert torch.equal(again["grad"], got["grad"]) and torch.equal(again["loss"], got["loss"])
 
 
-def test_many_rows(spec):
-    d = inputs(2000, 301, BF16, seed=9)
+# more rows than the device holds at once, of one CTA each and of several; words that are not whole
+@pytest.mark.parametrize("R,V,dtype", [(2000, 301, BF16), (400, 40000, F32), (700, 12001, F32), (420, 70001, BF16)])
+def test_many_rows(spec, R, V, dtype):
+    d = inputs(R, V, dtype, seed=9)
+    d["w"][:3] = 0.0
+    d["w"][-1] = 0.0
     check(d, call(d), oracle(d), 1.0, 0.05)
+    check(d, call(d, grad=False, weight=False), oracle(d, weight=False), 1.0, 0.05, grad=False)
+
+
+def test_rows_past_32_bits(spec):
+    """2.2e9 entries: the last rows against the same rows alone."""
+    R, V = 8700, 248320
+    z = torch.zeros((R, V), dtype=BF16, device="cuda")
+    d = inputs(4, V, BF16, seed=13)
+    z[-4:] = d["z"].cuda()
+    x = torch.zeros(R, dtype=torch.int32, device="cuda")
+    x[-4:] = d["x"].cuda()
+    old, adv, w = (torch.zeros(R, device="cuda") for _ in range(3))
+    old[-4:], adv[-4:], w[-4:] = d["old"].cuda(), d["A"].cuda(), 0.25
+    w[0] = 0.25
+    got = vsd.policy_loss(z, x, old, adv, weight=w, grad=True)
+    alone = vsd.policy_loss(z[-4:], x[-4:].contiguous(), old[-4:].contiguous(), adv[-4:].contiguous(),
+                            weight=w[-4:].contiguous(), grad=True)
+    assert (got["grad"][1:-4] == 0).all() and got["logp"][1:-4].abs().sum() == 0
+    # the rows alone may be split among other CTAs: their sums' order differs, each within its bar
+    bar = 2 * (58 + V / 512) * 2.0 ** -24
+    assert (got["logp"][-4:] - alone["logp"]).abs().max() <= bar * 2
+    assert ((got["grad"][-4:].float() - alone["grad"].float()).abs() <= (2 * 2.0 ** -8 + 4 * bar) * alone["grad"].float().abs() + 1e-30).all()
 
 
 def test_gradient_against_differences(spec):

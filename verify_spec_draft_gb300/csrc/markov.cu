@@ -293,7 +293,7 @@ static size_t markov_bind(MarkovBind& b, void* ws, int n, int r, int V) {
     b.ux = reinterpret_cast<bf16_t*>(take((size_t)3 * n * round8(r) * 2));
     const int tiles = (n + 255) / 256;
     b.part = reinterpret_cast<float*>(take((size_t)(tiles > kMarkovItems ? tiles : kMarkovItems) * 256 * (r > 128 ? 256 : 128) * 4));
-    b.stage_bytes = (size_t)6 * ((size_t)n * round8(columns) + (size_t)columns * round8(r)) + 4096;
+    b.stage_bytes = (size_t)6 * (n + round8(r)) * round8(columns) + 4096;
     b.stage = reinterpret_cast<bf16_t*>(take(b.stage_bytes));
     return at;
 }

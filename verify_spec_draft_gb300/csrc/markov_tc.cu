@@ -537,8 +537,8 @@ static cudaError_t mtc_launch(const MarkovParams& p, const MarkovBind& b, cudaSt
     const bool stage_z = !z16 || p.ld % 8 != 0, stage_w = !w16 || p.r != r8;
     // as many columns as the stage takes of what is staged
     const size_t each = 2 * ((stage_z ? (size_t)n * (z16 ? 1 : 3) : 0) + (stage_w ? (size_t)r8 * (w16 ? 1 : 3) : 0));
-    const size_t room = each ? (b.stage_bytes - 512) / each / 256 * 256 : 0;
-    const int columns = each && room < (size_t)round8(p.V) ? (int)room : p.V;
+    const size_t room = each ? (b.stage_bytes - 512) / each : 0;
+    const int columns = each && room < (size_t)round8(p.V) ? (int)(room / 256 * 256) : p.V;
     bf16_t* zs = b.stage;
     bf16_t* ws = b.stage + (stage_z ? (align256((size_t)n * (z16 ? 1 : 3) * round8(columns) * 2) / 2) : 0);
     const int pairs = device_sm_count() / 2 > kMarkovPairs ? kMarkovPairs : (device_sm_count() / 2 > 2 ? device_sm_count() / 2 : 2);
