@@ -1,7 +1,8 @@
 /*
  * spec.h - C ABI of the GB300 (sm_103a) block-speculative-decoding hot path.
  *
- * Three operations on vocabulary-wide logit rows, each one or two CUDA kernels:
+ * Three operations on vocabulary-wide logit rows, each one or two CUDA kernels, and what a
+ * server and a training loop of such a drafter need beside them (further down):
  *
  *   spec_draft_block  DSpark low-rank Markov logit bias + softmax + argmax/sample
  *                     over a parallel drafter's gamma positions.
@@ -724,7 +725,8 @@ spec_status spec_distill(const void *student, spec_dtype dtype, int rows, int V,
  * is not finite, gets NaN in its outputs (flag NONFINITE); a token outside [0, V) does too
  * (flag TOKEN).  A token of probability 0 has lp = -inf, and where a KL term meets it loss
  * +inf.  A row whose slope (or (weight / t) slope) is not finite, that one or one with u A
- * beyond float32's range, gets a gradient of NaN (flag NONFINITE).
+ * beyond float32's range, gets a gradient of NaN (flag NONFINITE).  What a wait that ran out
+ * (flag TIMEOUT) kept from being computed is NaN.
  * Limits: 1 <= rows <= SPEC_MAX_TEACHER_ROWS, 1 <= V <= SPEC_MAX_V_TEACHER, V <= ld < 2^31,
  * temperature positive, finite and not subnormal.
  */
@@ -753,7 +755,8 @@ spec_status spec_policy_loss(const void *logits, spec_dtype dtype, int rows, int
  *   U, Wt         [V, r], weights_dtype; 1 <= r <= SPEC_MAX_RANK.
  *   dU_out, dWt_out  [V, r], out_dtype (float32 or bf16); neither may overlap an input.
  *   workspace     spec_workspace_bytes(SPEC_OP_MARKOV_GRAD, B, gamma, V, r).
- * A NaN or an infinity in a row's dz or in a weight goes where the formulas take it.
+ * A row's dz or a weight that is not finite makes the sums that it enters not finite.  What a
+ * wait that ran out (flag TIMEOUT) kept from being computed is not defined.
  * Limits: 1 <= gamma <= SPEC_MAX_GAMMA, 1 <= B * gamma <= SPEC_MAX_MARKOV_ROWS,
  * 1 <= V <= SPEC_MAX_V_MARKOV, V <= ld < 2^31.
  */

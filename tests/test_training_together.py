@@ -1,6 +1,8 @@
 """policy_loss, markov_grad and adamw as a drafter's training step uses them: behind draft_block and
 verify, in a graph, on several streams and threads."""
 
+import importlib.util
+import os
 import threading
 
 import numpy as np
@@ -223,3 +225,14 @@ def test_gradients_of_the_other_losses(spec):
         for k in ("U", "Wt"):
             err = np.abs(got[k].double().cpu().numpy() - want[k])
             assert (err <= (t.V / 8 + 64) * 2.0 ** -24 * want[k + "_abs"] + 2.0 ** -24 * np.abs(want[k])).all()
+
+
+@pytest.mark.parametrize("rank", [32, 64])
+def test_example_trains_its_bias(spec, rank):
+    """The example's drafter with a bias runs, and its calls report nothing."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    at = importlib.util.spec_from_file_location("online_distill", os.path.join(root, "examples", "online_distill.py"))
+    ex = importlib.util.module_from_spec(at)
+    at.loader.exec_module(ex)
+    loss, accepted = ex.run(steps=4, requests=3, gamma=4, vocab=5003, k=16, rank=rank, report=lambda s: None)
+    assert len(loss) == len(accepted) == 4 and np.isfinite(loss).all()

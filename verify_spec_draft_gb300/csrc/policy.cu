@@ -17,6 +17,8 @@ constexpr int kPolThreads(int mode) { return mode == 0 ? 128 : 256; }
 constexpr int kPolBatch(int mode) { return mode == 1 ? 4 : 8; }   // words a thread takes at once
 constexpr int kPolChunks = 4;                      // copies of a slice
 constexpr int kPolMaxCluster = 16;
+constexpr int kPolMost = 220 * 1024;               // bytes of a slice that can be kept
+constexpr int kPolSlice = 3392;                    // words of one that is kept where the rows are many
 
 // Pairs (m, s): the maximum of some entries and the sum of their weights relative to it
 // (row_words.cuh); empty: (-inf, 0).  NaN shows in m.
@@ -104,7 +106,7 @@ __device__ __forceinline__ PolRow policy_row(const PolicyParams& p, float2 T, co
 // the slice read again (it is too large to keep).  A cluster takes one row in n_clusters; in MODE 1 the
 // next row's slice is on its way as soon as every thread has read the last of this one's.
 template <typename T, int MODE, bool ALIGNED>
-__global__ void __launch_bounds__(kPolThreads(MODE)) policy_kernel(const __grid_constant__ PolicyParams p) {
+__global__ void __launch_bounds__(kPolThreads(MODE), MODE == 0 ? 6 : 4) policy_kernel(const __grid_constant__ PolicyParams p) {
     constexpr int E = 16 / (int)sizeof(T), TH = kPolThreads(MODE), WARPS = TH / 32, BATCH = kPolBatch(MODE);
     extern __shared__ __align__(128) uint8_t s_slice[];
     __shared__ __align__(8) uint64_t s_full[kPolChunks], s_met[2];
@@ -334,8 +336,9 @@ __global__ void __launch_bounds__(kPolThreads(MODE)) policy_kernel(const __grid_
     }
 }
 
-// The cluster's size.  With the gradient: slices of 64 KB at most, so that three CTAs share an SM and one loads
-// while another forms its gradient (1792 rows of 248,320 bf16: 313 us; slices of 32 KB, seven CTAs: 316).
+// The cluster's size.  With the gradient: slices of 53 KB at most, so that four CTAs share an SM and some load
+// while others form their gradient (1792 rows of 248,320 bf16: ten CTAs of 50 KB 299 us, eight of 62 KB and
+// three an SM 314, more and smaller ones 338 and up, as the registers hold four).
 // The loss alone keeps nothing, so a CTA takes a whole row where the rows are enough to fill the
 // device (448 rows: two CTAs a row 38 us, eight 40).  More CTAs per row where the rows are few, down to
 // a batch of words per thread.
@@ -346,21 +349,23 @@ static cudaError_t policy_typed(PolicyParams p, cudaStream_t stream) {
     const int sms = device_sm_count();
     int size = 1;
     if (p.grad_out) {
-        while (size < kPolMaxCluster && (words + size - 1) / size > 4096) size *= 2;
-        while (size < 8 && (long)p.rows * size < sms && words / (2 * size) >= 256) size *= 2;
+        size = (words + kPolSlice - 1) / kPolSlice;
+        if (size > kPolMaxCluster) size = kPolMaxCluster;
+        while (size <= 4 && (long)p.rows * size < sms && words / (2 * size) >= 256) size *= 2;
     } else {
         while (size < kPolMaxCluster && (long)p.rows * size < 5 * sms && words / (2 * size) >= 512) size *= 2;
     }
     p.slice = (words + size - 1) / size;
     const size_t bytes = (size_t)p.slice * 16;
-    const int mode = !p.grad_out ? 0 : (bytes <= 220 * 1024 ? 1 : 2);
+    const int mode = !p.grad_out ? 0 : (bytes <= kPolMost ? 1 : 2);
     const bool fits = SegWords<T, true>::fits(p.ld, p.V);
     const void* kerns[3][2] = {{(const void*)policy_kernel<T, 0, false>, (const void*)policy_kernel<T, 0, true>},
                                {(const void*)policy_kernel<T, 1, false>, (const void*)policy_kernel<T, 1, true>},
                                {(const void*)policy_kernel<T, 2, false>, (const void*)policy_kernel<T, 2, true>}};
     const void* kern = kerns[mode][fits];
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e == cudaSuccess && mode == 1) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 220 * 1024);
+    cudaError_t e = cudaSuccess;
+    if (size > 8) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e == cudaSuccess && mode == 1 && bytes > 48 * 1024) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kPolMost);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3((unsigned)kPolThreads(mode));

@@ -25,17 +25,24 @@ kernel, on inputs larger than L2 (129 MB) but only a few hundred MB on the devic
   top        spec_top_logits, K 64, on the same 256 rows (127 MB)
   distill    spec_distill, K 64, on e2etv's 448 draft rows, the loss alone (222 MB in)
   distill_grad  the same with the gradient (222 MB in, 222 MB out)
+  policy     spec_policy_loss with a KL term on the same 448 rows, the loss alone (222 MB in)
+  policy_grad   the same with the gradient (222 MB in, 222 MB out)
+  markov     spec_markov_grad, 256 x 7 rows, V=65536, r=256, bf16 (302 MB in, 67 MB out)
+  adamw      spec_adamw, two tables of 65536 x 256 bf16 with masters, bf16 gradients, 32-bit
+             states (940 MB moved)
+  adamw8     the same with 8-bit states (539 MB moved)
 """
 
 import argparse
 
 import torch
 
-from . import (distill, draft_block, draft_block_topk, e2etv, load, process_logits, synth, top_logits, tree_verify,
-               verify, verify_budget, verify_topk)
+from . import (adamw, adamw_state, adamw_table, distill, draft_block, draft_block_topk, e2etv, load, markov_grad,
+               policy_loss, process_logits, synth, top_logits, tree_verify, verify, verify_budget, verify_topk)
 
 CASES = ("draft", "draft_t1", "verify_t0", "verify_t1", "verify_topk", "e2etv", "tree_verify", "draft_topk",
-         "draft_pos", "sampler", "budget", "process", "top", "distill", "distill_grad")
+         "draft_pos", "sampler", "budget", "process", "top", "distill", "distill_grad",
+         "policy", "policy_grad", "markov", "adamw", "adamw8")
 
 
 def main(argv=None):
@@ -120,13 +127,40 @@ def main(argv=None):
         rows = synth.config_inputs(4, device=dev)["target"]
         ref = top_logits(rows, 64)
         run = lambda: top_logits(rows, 64, ws=ref["ws"], out=ref)
-    elif args.case in ("distill", "distill_grad"):
+    elif args.case in ("distill", "distill_grad",
+         "policy", "policy_grad", "markov", "adamw", "adamw8"):
         c = synth.CONFIGS[5]
         t, d = synth.e2etv_rows(64, c.gamma, c.V, c.draft_sigma, c.dtype, c.seed, dev)
         top = top_logits(t, 64)
         kw = dict(tail=top["tail"], grad=args.case == "distill_grad")
         ref = distill(d, top["values"], top["ids"], **kw)
         run = lambda: distill(d, top["values"], top["ids"], ws=ref["ws"], out=ref, **kw)
+    elif args.case in ("policy", "policy_grad"):
+        c = synth.CONFIGS[5]
+        t, d = synth.e2etv_rows(64, c.gamma, c.V, c.draft_sigma, c.dtype, c.seed, dev)
+        tokens = d.argmax(1).to(torch.int32)
+        old = policy_loss(d, tokens, torch.zeros(len(d), device=dev), torch.zeros(len(d), device=dev))["logp"]
+        adv = torch.linspace(-1, 1, len(d), device=dev)
+        kw = dict(ref_logp=old - 0.1, kl=0.05, grad=args.case == "policy_grad")
+        ref = policy_loss(d, tokens, old, adv, **kw)
+        run = lambda: policy_loss(d, tokens, old, adv, ws=ref["ws"], out=ref, **kw)
+    elif args.case == "markov":
+        B, G, V, r = 256, 7, 65536, 256
+        g = torch.Generator(device=dev)
+        g.manual_seed(1006)
+        grad = (torch.randn((B, G, V), generator=g, device=dev) * 1e-6).to(torch.bfloat16)
+        U, Wt = synth.markov_weights(V, r, torch.bfloat16, seed=6, device=dev)
+        ids = lambda *shape: torch.randint(0, V, shape, generator=g, device=dev, dtype=torch.int32)
+        anchor, tokens = ids(B), ids(B, G)
+        ref = markov_grad(grad, anchor, tokens, U, Wt)
+        run = lambda: markov_grad(grad, anchor, tokens, U, Wt, ws=ref["ws"], out=ref)
+    elif args.case in ("adamw", "adamw8"):
+        params = [w.to(torch.bfloat16) for w in synth.markov_weights(65536, 256, torch.float32, seed=6, device=dev)]
+        grads = [torch.randn_like(w) * 1e-3 for w in params]
+        table = adamw_table(params, grads, [adamw_state(w, 8 if args.case == "adamw8" else 32) for w in params])
+        step = torch.zeros(1, dtype=torch.int32, device=dev)
+        ref = adamw(table, step, lr=1e-3)
+        run = lambda: adamw(table, step, lr=1e-3, ws=ref["ws"])
     else:
         c = synth.CONFIGS[5]
         n_branches = 64
