@@ -127,8 +127,7 @@ def main(argv=None):
         rows = synth.config_inputs(4, device=dev)["target"]
         ref = top_logits(rows, 64)
         run = lambda: top_logits(rows, 64, ws=ref["ws"], out=ref)
-    elif args.case in ("distill", "distill_grad",
-         "policy", "policy_grad", "markov", "adamw", "adamw8"):
+    elif args.case in ("distill", "distill_grad"):
         c = synth.CONFIGS[5]
         t, d = synth.e2etv_rows(64, c.gamma, c.V, c.draft_sigma, c.dtype, c.seed, dev)
         top = top_logits(t, 64)
