@@ -11,6 +11,8 @@
 #include "internal.h"
 #include "row_words.cuh"
 
+#include <type_traits>
+
 namespace spec {
 
 constexpr int kPolThreads(int mode) { return mode == 0 ? 128 : 256; }
@@ -130,7 +132,8 @@ __global__ void __launch_bounds__(kPolThreads(MODE), MODE == 0 ? 6 : 4) policy_k
     auto row_of = [&](int row) { return SegWords<T, ALIGNED>(reinterpret_cast<const T*>(p.logits) + (long)row * p.ld, p.V); };
     const int first = (int)rank * p.slice;
     auto words_of = [&](const SegWords<T, ALIGNED>& in) { return max(0, min(in.n() - first, p.slice)); };
-    auto per_of = [&](int n) { return ((n + kPolChunks - 1) / kPolChunks + 7) & ~7; };   // words of a copy
+    // words of a copy: whole batches
+    auto per_of = [&](int n) { return (n + kPolChunks * TH * BATCH - 1) / (kPolChunks * TH * BATCH) * (TH * BATCH); };
     auto weight_of = [&](int row) { return row < p.rows ? (p.weight ? p.weight[row] : 1.0f) : 0.0f; };
     auto issue = [&](int row) {   // (all threads; the slot is free)
         const SegWords<T, ALIGNED> in = row_of(row);
@@ -210,25 +213,38 @@ __global__ void __launch_bounds__(kPolThreads(MODE), MODE == 0 ? 6 : 4) policy_k
         __syncthreads();   // (the words that are not whole)
 
         float m = -INFINITY, s = 0.0f;
-        auto batch = [&](int l0, int end) {
-            uint4 w[BATCH];
-            const uint32_t ninf = NegInf<T>::word;
-            float bm = -INFINITY;
+        // words [l0, end): whole batches of all threads, then one by one
+        auto take = [&](auto count, const uint4* w, float& m, float& s) {
+            constexpr int N = decltype(count)::value;
+            float bm = m;
 #pragma unroll
-            for (int q = 0; q < BATCH; ++q) {
-                const int l = l0 + q * TH + tid;
-                if (l < end) w[q] = MODE == 1 ? slot[l] : in.load(first + l);
-                else w[q] = make_uint4(ninf, ninf, ninf, ninf);
-                if (l == xl) w[q] = word_without<T>(w[q], xbit);
-            }
-#pragma unroll
-            for (int q = 0; q < BATCH; ++q) bm = f_max_nan(bm, u4_max_nan<sizeof(T)>(w[q]));
-            bm = f_max_nan(bm, m);
+            for (int q = 0; q < N; ++q) bm = f_max_nan(bm, u4_max_nan<sizeof(T)>(w[q]));
             if (bm != m) {
                 s = m == -INFINITY ? 0.0f : s * ex2(pol_step(m, bm, c));
                 m = bm;
             }
-            s += words_sum<T, BATCH>(w, m, c);
+            uint4 v[N];
+#pragma unroll
+            for (int q = 0; q < N; ++q) v[q] = w[q];
+            s += words_sum<T, N>(v, m, c);
+        };
+        auto word = [&](int l) {
+            uint4 w = MODE == 1 ? slot[l] : in.load(first + l);
+            if (l == xl) w = word_without<T>(w, xbit);
+            return w;
+        };
+        auto batch = [&](int l0, int end) {
+            for (; l0 + TH * BATCH <= end; l0 += TH * BATCH) {
+                uint4 w[BATCH];
+#pragma unroll
+                for (int q = 0; q < BATCH; ++q) w[q] = word(l0 + q * TH + tid);
+                take(std::integral_constant<int, BATCH>(), w, m, s);
+            }
+#pragma unroll 1
+            for (int l = l0 + tid; l < end; l += TH) {
+                const uint4 w[1] = {word(l)};
+                take(std::integral_constant<int, 1>(), w, m, s);
+            }
         };
         bool late = false;
         if (MODE == 1) {
@@ -236,12 +252,12 @@ __global__ void __launch_bounds__(kPolThreads(MODE), MODE == 0 ? 6 : 4) policy_k
             for (int q = 0; q < kPolChunks; ++q) {
                 late |= !mbar_wait(&s_full[q], copies & 1, p.status, kWaitLimitNs);
                 const int end = min(n, (q + 1) * per);
-                for (int l0 = q * per; l0 < end && !late; l0 += TH * BATCH) batch(l0, end);
+                if (!late) batch(q * per, end);
             }
             ++copies;
             if (late) s_late = 1;
         } else {
-            for (int l0 = 0; l0 < n; l0 += TH * BATCH) batch(l0, n);
+            batch(0, n);
         }
         if (late) m = NAN;
         {
