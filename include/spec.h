@@ -753,7 +753,8 @@ spec_status spec_policy_loss(const void *logits, spec_dtype dtype, int rows, int
  *                 counts for nothing, and its dz is not used; one that is outside [-1, V)
  *                 does too and raises flag TOKEN.
  *   U, Wt         [V, r], weights_dtype; 1 <= r <= SPEC_MAX_RANK.
- *   dU_out, dWt_out  [V, r], out_dtype (float32 or bf16); neither may overlap an input.
+ *   dU_out, dWt_out  [V, r], out_dtype (float32 or bf16); neither may overlap an input or the
+ *                 other.
  *   workspace     spec_workspace_bytes(SPEC_OP_MARKOV_GRAD, B, gamma, V, r).
  * A row's dz or a weight that is not finite makes the sums that it enters not finite.  What a
  * wait that ran out (flag TIMEOUT) kept from being computed is not defined.

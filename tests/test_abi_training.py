@@ -52,7 +52,7 @@ def test_policy_loss_argument_errors(lib):
 
 
 def test_markov_grad_argument_errors(lib):
-    def call(g=A, gdt=vsd.BF16, B=2, G=4, V=100, ld=100, anc=A, tok=A, U=A, Wt=A, wdt=vsd.BF16, r=8, dU=A, dW=A,
+    def call(g=A, gdt=vsd.BF16, B=2, G=4, V=100, ld=100, anc=A, tok=A, U=A, Wt=A, wdt=vsd.BF16, r=8, dU=2 * A, dW=3 * A,
              odt=vsd.F32, ws=A, wsb=1 << 30):
         return lib.spec_markov_grad(g, gdt, B, G, V, ld, anc, tok, U, Wt, wdt, r, dU, dW, odt, ws, wsb, None)
     assert call(gdt=2) == DTYPE and call(wdt=-1) == DTYPE and call(odt=7) == DTYPE
@@ -61,6 +61,8 @@ def test_markov_grad_argument_errors(lib):
         assert call(**bad) == SHAPE, bad
     for name in ("g", "anc", "tok", "U", "Wt", "dU", "dW"):
         assert call(**{name: 0}) == INVALID, name
+    for bad in (dict(dU=A), dict(dW=A), dict(dU=3 * A), dict(U=2 * A), dict(Wt=2 * A), dict(Wt=3 * A), dict(g=3 * A)):
+        assert call(**bad) == INVALID, bad          # an output that is an input, or the other output
     for name in ("g", "U", "Wt", "dU", "dW", "ws"):
         assert call(**{name: MIS}) == ALIGN, name
     need = lib.spec_workspace_bytes(vsd.OP_MARKOV_GRAD, 2, 4, 100, 8)

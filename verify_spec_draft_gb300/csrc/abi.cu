@@ -673,6 +673,9 @@ spec_status spec_markov_grad(const void* grad, spec_dtype grad_dtype, int B, int
         V > SPEC_MAX_V_MARKOV || ld < V || r < 1 || r > SPEC_MAX_RANK)
         return SPEC_ERR_SHAPE;
     if (!grad || !anchor || (gamma > 1 && !tokens) || !U || !Wt || !dU_out || !dWt_out) return SPEC_ERR_INVALID_ARG;
+    for (const void* o : {(const void*)dU_out, (const void*)dWt_out})
+        if (o == grad || o == U || o == Wt) return SPEC_ERR_INVALID_ARG;
+    if (dU_out == dWt_out) return SPEC_ERR_INVALID_ARG;
     if (!aligned16(grad) || !aligned16(U) || !aligned16(Wt) || !aligned16(dU_out) || !aligned16(dWt_out) ||
         !aligned16(workspace))
         return SPEC_ERR_ALIGN;

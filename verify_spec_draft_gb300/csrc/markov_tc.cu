@@ -57,6 +57,9 @@ __device__ __forceinline__ uint32_t peer_addr(const void* p, unsigned rank) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
     return a;
 }
+// An arrival in a CTA of the pair.  What it reports is not this thread's memory (TMEM that tcgen05.ld has waited
+// for, or a stage that copies have written), so it releases nothing beyond the CTA: at cluster scope it
+// would wait for the epilogue's stores (610 us of 284 then).
 __device__ __forceinline__ void remote_arrive(uint64_t* bar, unsigned rank) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" :: "r"(peer_addr(bar, rank)) : "memory");
 }
@@ -521,6 +524,10 @@ static void mtc_plan(int n, int columns, int r, int out_size, int terms, int pai
                 dx.pairs = dp;
             }
         }
+    if (best < 0.0) {   // more tiles than four rounds take on a smaller device
+        dx.parts = 1;
+        dx.pairs = pairs / 2;
+    }
     const int left = pairs - dx.pairs;
     wt.first = 0;
     wt.pairs = wt.tiles < left ? wt.tiles : left;
