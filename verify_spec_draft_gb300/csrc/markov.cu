@@ -84,83 +84,109 @@ __global__ void __launch_bounds__(kMarkovThreads) markov_order_kernel(MarkovPara
     if (threadIdx.x == 0) b.none[blockIdx.x] = (uint8_t)s_none;
 }
 
-// A few rows: one pass over the vocabulary forms both products.  A warp takes an entry v, its lanes
-// the r columns: dWt[v] = sum_i dz[i, v] U[x_i] with the rows' U in registers, and dX's sums, one per row
-// and column, in registers too.  Bound by memory: Wt in, dWt and dU's zeros out.  7 rows, the tensor cores
-// would spend their steps of 64 rows on zeros.
-template <typename G, typename W, int C>
-__global__ void __launch_bounds__(kMarkovThreads) markov_small_kernel(MarkovParams p, MarkovBind b) {
-    constexpr int N = kMarkovSmall, kV = kMarkovTurn;
-    __shared__ __align__(16) float s_d[kV][N];
-    __shared__ float s_x[kMarkovWarps][32 * C];
+// A few rows: one pass over the vocabulary forms both products.  A thread takes 4 columns of an entry v:
+// dWt[v] = sum_i dz[i, v] U[x_i] with U's rows in shared memory, and dX's sums of its columns in
+// registers, one per row, which the CTA's threads bring together at the end.  Bound by memory: Wt in, dWt and
+// dU's zeros out.  The tensor cores would spend their steps of 64 rows on zeros.
+template <typename T>
+__device__ __forceinline__ float4 quad_load(const T* a, int k, int r) {   // entries k..k + 3 of a row of r
+    if (r % 4 == 0) {
+        if constexpr (sizeof(T) == 4) {
+            return __ldg(reinterpret_cast<const float4*>(a + k));
+        } else {
+            const uint2 w = __ldg(reinterpret_cast<const uint2*>(a + k));
+            return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u),
+                               __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u));
+        }
+    }
+    return make_float4(load_one(a + k), k + 1 < r ? load_one(a + k + 1) : 0.0f, k + 2 < r ? load_one(a + k + 2) : 0.0f,
+                       k + 3 < r ? load_one(a + k + 3) : 0.0f);
+}
+__device__ __forceinline__ void quad_store(void* out, int dtype, long at, int k, int r, const float4& x) {
+    if (r % 4 == 0) {
+        if (dtype == SPEC_BF16) {
+            uint2 w;
+            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w.x) : "f"(x.y), "f"(x.x));
+            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w.y) : "f"(x.w), "f"(x.z));
+            *reinterpret_cast<uint2*>(reinterpret_cast<bf16_t*>(out) + at + k) = w;
+        } else {
+            *reinterpret_cast<float4*>(reinterpret_cast<float*>(out) + at + k) = x;
+        }
+        return;
+    }
+    const float o[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int h = 0; h < 4; ++h)
+        if (k + h < r) put(out, dtype, at + k + h, o[h]);
+}
+template <typename G, typename W>
+__global__ void __launch_bounds__(kMarkovThreads, 2) markov_small_kernel(MarkovParams p, MarkovBind b) {
+    constexpr int N = kMarkovSmall;
+    __shared__ __align__(16) float s_u[N][SPEC_MAX_RANK];
+    __shared__ float s_x[4 * N][kMarkovThreads + 1];
     __shared__ int s_row[N];
-    const int n = p.B * p.gamma, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int n = p.B * p.gamma, tid = threadIdx.x, pitch = round4(p.r), quads = pitch / 4;
+    const int entries = kMarkovThreads / quads;          // of a turn
+    const int k = tid % quads * 4, e = tid / quads;
     bool bad = false;
     if (tid < N) s_row[tid] = tid < n ? markov_token(p, tid, &bad) : p.V;
     if (bad && blockIdx.x == 0) atomicOr(b.status, SPEC_DEV_TOKEN);
     __syncthreads();
-    const G* dz = reinterpret_cast<const G*>(p.grad);
-    float u[N][C], x[N][C];
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-#pragma unroll
-        for (int c = 0; c < C; ++c) {
-            const int k = c * 32 + lane;
-            x[i][c] = 0.0f;
-            u[i][c] = s_row[i] < p.V && k < p.r ? load_one(reinterpret_cast<const W*>(p.U) + (long)s_row[i] * p.r + k) : 0.0f;
-        }
-    const int turns = (p.V + kV - 1) / kV;
-    for (int turn = blockIdx.x; turn < turns; turn += gridDim.x) {
-        const int v0 = turn * kV;
-        __syncthreads();
-        for (int e = tid; e < kV * N; e += kMarkovThreads) {
-            const int i = e / kV, v = v0 + e % kV;
-            s_d[e % kV][i] = v < p.V && s_row[i] < p.V ? load_one(dz + (long)i * p.ld + v) : 0.0f;
-        }
-        __syncthreads();
-#pragma unroll 4
-        for (int e = warp; e < kV; e += kMarkovWarps) {
-            const int v = v0 + e;
-            if (v >= p.V) break;
-            float w[C], o[C], d[N];
-            *reinterpret_cast<float4*>(d) = *reinterpret_cast<const float4*>(&s_d[e][0]);
-            *reinterpret_cast<float4*>(d + 4) = *reinterpret_cast<const float4*>(&s_d[e][4]);
-#pragma unroll
-            for (int c = 0; c < C; ++c) {
-                const int k = c * 32 + lane;
-                w[c] = k < p.r ? load_one(reinterpret_cast<const W*>(p.Wt) + (long)v * p.r + k) : 0.0f;
-                o[c] = 0.0f;
-            }
-#pragma unroll
-            for (int i = 0; i < N; ++i)
-#pragma unroll
-                for (int c = 0; c < C; ++c) {
-                    o[c] = fmaf(d[i], u[i][c], o[c]);
-                    x[i][c] = fmaf(d[i], w[c], x[i][c]);
-                }
-#pragma unroll
-            for (int c = 0; c < C; ++c) {
-                const int k = c * 32 + lane;
-                if (k >= p.r) continue;
-                put(p.dWt_out, p.odt, (long)v * p.r + k, o[c]);
-                put(p.dU_out, p.odt, (long)v * p.r + k, 0.0f);
-            }
-        }
+    for (int a = tid; a < N * pitch; a += kMarkovThreads) {
+        const int i = a / pitch, c = a - i * pitch;
+        s_u[i][c] = s_row[i] < p.V && c < p.r ? load_one(reinterpret_cast<const W*>(p.U) + (long)s_row[i] * p.r + c) : 0.0f;
     }
-    // the warps' sums of dX, in order
-    const int pitch = round4(p.r);
+    // a row without a token is read as the first one is, and counts as 0: no load waits for a test
+    const G* dz[N];
+    unsigned on = 0u;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        __syncthreads();
+        on |= s_row[i] < p.V ? 1u << i : 0u;
+        dz[i] = reinterpret_cast<const G*>(p.grad) + (s_row[i] < p.V ? (long)i * p.ld : 0l);
+    }
+    __syncthreads();
+    const W* Wt = reinterpret_cast<const W*>(p.Wt);
+    float4 x[N];
 #pragma unroll
-        for (int c = 0; c < C; ++c) s_x[warp][c * 32 + lane] = x[i][c];
-        __syncthreads();
-        if (i < n && tid < pitch) {
-            float s = 0.0f;
+    for (int i = 0; i < N; ++i) x[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (e < entries) {
+        const int step = (int)gridDim.x * entries;
+#pragma unroll 2
+        for (int v = (int)blockIdx.x * entries + e; v < p.V; v += step) {
+            const float4 w = quad_load(Wt + (long)v * p.r, k, p.r);
+            float d[N];
 #pragma unroll
-            for (int q = 0; q < kMarkovWarps; ++q) s += tid < 32 * C ? s_x[q][tid] : 0.0f;
-            b.part[((long)blockIdx.x * n + i) * pitch + tid] = s;
+            for (int i = 0; i < N; ++i) d[i] = load_one(dz[i] + v);
+#pragma unroll
+            for (int i = 0; i < N; ++i) d[i] = (on >> i) & 1u ? d[i] : 0.0f;
+            float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const float4 u = *reinterpret_cast<const float4*>(&s_u[i][k]);
+                o.x = fmaf(d[i], u.x, o.x); o.y = fmaf(d[i], u.y, o.y); o.z = fmaf(d[i], u.z, o.z); o.w = fmaf(d[i], u.w, o.w);
+                x[i].x = fmaf(d[i], w.x, x[i].x); x[i].y = fmaf(d[i], w.y, x[i].y);
+                x[i].z = fmaf(d[i], w.z, x[i].z); x[i].w = fmaf(d[i], w.w, x[i].w);
+            }
+            quad_store(p.dWt_out, p.odt, (long)v * p.r, k, p.r, o);
+            quad_store(p.dU_out, p.odt, (long)v * p.r, k, p.r, make_float4(0.0f, 0.0f, 0.0f, 0.0f));
         }
+    }
+    // the threads' sums of dX, in order
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        s_x[4 * i][tid] = x[i].x;
+        s_x[4 * i + 1][tid] = x[i].y;
+        s_x[4 * i + 2][tid] = x[i].z;
+        s_x[4 * i + 3][tid] = x[i].w;
+    }
+    __syncthreads();
+    for (int a = tid; a < n * pitch; a += kMarkovThreads) {
+        const int i = a / pitch, c = a - i * pitch;
+        const float* from = &s_x[4 * i + (c & 3)][c >> 2];
+        float s = 0.0f;
+#pragma unroll 4
+        for (int q = 0; q < entries; ++q) s += from[q * quads];
+        b.part[((long)blockIdx.x * n + i) * pitch + c] = s;
     }
 }
 
@@ -168,6 +194,7 @@ __global__ void __launch_bounds__(kMarkovThreads) markov_small_kernel(MarkovPara
 // they are all, that is dU's row, otherwise the sum is kept for markov_runs_kernel.  16-byte columns go over
 // lanes and the parts over groups of threads, whose sums meet in order.
 constexpr int kJoinThreads = 256;
+constexpr int kJoinMany = 1024;                  // of the few rows' many parts
 __device__ __forceinline__ void join_out(const MarkovParams& p, int t, int k, const float4& s) {
     const float o[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
@@ -185,8 +212,9 @@ __device__ __forceinline__ bool join_meet(float4* s_sum, float4& s, int k, int g
     return true;
 }
 template <bool SMALL>   // (kMarkovSmall rows at most: their order is found here)
-__global__ void __launch_bounds__(kJoinThreads) markov_join_kernel(MarkovParams p, MarkovBind b, MarkovJoin a) {
-    __shared__ float4 s_sum[kJoinThreads];
+__global__ void __launch_bounds__(SMALL ? kJoinMany : kJoinThreads) markov_join_kernel(MarkovParams p, MarkovBind b, MarkovJoin a) {
+    constexpr int TH = SMALL ? kJoinMany : kJoinThreads;
+    __shared__ float4 s_sum[TH];
     const int at = blockIdx.x;
     int t, rows, all, index[kJoinRun];
     if (SMALL) {
@@ -215,7 +243,7 @@ __global__ void __launch_bounds__(kJoinThreads) markov_join_kernel(MarkovParams 
         for (int q = 0; q < kJoinRun; ++q) index[q] = b.order[at + min(q, rows - 1)];
     }
     if (SMALL && t >= p.V) return;
-    const int quads = round4(p.r) / 4, groups = kJoinThreads / quads;
+    const int quads = round4(p.r) / 4, groups = TH / quads;
     const int k = threadIdx.x % quads, g = threadIdx.x / quads;
     float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (g < groups) {
@@ -267,8 +295,14 @@ __global__ void __launch_bounds__(kJoinThreads) markov_runs_kernel(MarkovParams 
     }
 }
 
-// (the sums' registers grow with r: 5 rows of r = 256 take 285 us here, 140 on the tensor cores)
-static bool markov_small(int n, int r) { return n <= kMarkovSmall && r <= 64; }
+// One pass for a few rows.  With float32 operands always, as the tensor cores would need them split (7 rows,
+// V = 50,000, r = 50: 24 us here, 68 there); with bf16 ones while the pass, some 11 us and 5.5 per million
+// columns, takes less than the tensor cores' 15 us and 0.22 per thousand entries (V = 248,320: r = 32 54 and
+// 73 us, r = 64 102 and 68).
+static bool markov_small(const MarkovParams& p) {
+    if (p.B * p.gamma > kMarkovSmall) return false;
+    return p.gdt != SPEC_BF16 || p.wdt != SPEC_BF16 || (long)(round4(p.r) - 40) * p.V <= 700000l;
+}
 
 static size_t markov_bind(MarkovBind& b, void* ws, int n, int r, int V) {
     uint8_t* w = reinterpret_cast<uint8_t*>(ws);
@@ -280,10 +314,6 @@ static size_t markov_bind(MarkovBind& b, void* ws, int n, int r, int V) {
         at += align256(bytes);
         return q;
     };
-    if (markov_small(n, r)) {
-        b.part = reinterpret_cast<float*>(take((size_t)kMarkovSlabs * n * round4(r) * 4));
-        return at;
-    }
     b.order = reinterpret_cast<int32_t*>(take((size_t)n * 4));
     b.token = reinterpret_cast<int32_t*>(take((size_t)n * 4));
     b.run = reinterpret_cast<int2*>(take((size_t)n * 8));
@@ -292,6 +322,8 @@ static size_t markov_bind(MarkovBind& b, void* ws, int n, int r, int V) {
     b.none = take((size_t)(n + 63) / 64 * 8);
     b.ux = reinterpret_cast<bf16_t*>(take((size_t)3 * n * round8(r) * 2));
     const int tiles = (n + 255) / 256;
+    // (a few rows' slabs are less: kMarkovSlabs n r of them)
+    static_assert(kMarkovSlabs * kMarkovSmall <= kMarkovItems * 128, "room for the slabs' parts");
     b.part = reinterpret_cast<float*>(take((size_t)(tiles > kMarkovItems ? tiles : kMarkovItems) * 256 * (r > 128 ? 256 : 128) * 4));
     b.stage_bytes = (size_t)6 * (n + round8(r)) * round8(columns) + 4096;
     b.stage = reinterpret_cast<bf16_t*>(take(b.stage_bytes));
@@ -305,11 +337,11 @@ size_t markov_grad_workspace_bytes(int B, int gamma, int V, int r) {
 
 template <typename G, typename W>
 static int markov_small_launch(const MarkovParams& p, const MarkovBind& b, cudaStream_t stream) {
-    int slabs = (p.V + kMarkovTurn - 1) / kMarkovTurn;
+    const int entries = kMarkovThreads / (round4(p.r) / 4);
+    int slabs = (p.V + entries - 1) / entries;
     const int most = 2 * device_sm_count() < kMarkovSlabs ? 2 * device_sm_count() : kMarkovSlabs;
     if (slabs > most) slabs = most;
-    if (p.r <= 32) markov_small_kernel<G, W, 1><<<slabs, kMarkovThreads, 0, stream>>>(p, b);
-    else markov_small_kernel<G, W, 2><<<slabs, kMarkovThreads, 0, stream>>>(p, b);
+    markov_small_kernel<G, W><<<slabs, kMarkovThreads, 0, stream>>>(p, b);
     return slabs;
 }
 
@@ -317,12 +349,12 @@ cudaError_t markov_grad_launch(const MarkovParams& p, void* ws, cudaStream_t str
     const int n = p.B * p.gamma;
     MarkovBind b;
     markov_bind(b, ws, n, p.r, p.V);
-    const bool small = markov_small(n, p.r), g16 = p.gdt == SPEC_BF16, w16 = p.wdt == SPEC_BF16;
+    const bool small = markov_small(p), g16 = p.gdt == SPEC_BF16, w16 = p.wdt == SPEC_BF16;
     if (small) {
         MarkovJoin join = {0, n, round4(p.r)};
         join.parts = g16 ? (w16 ? markov_small_launch<bf16_t, bf16_t>(p, b, stream) : markov_small_launch<bf16_t, float>(p, b, stream))
                          : (w16 ? markov_small_launch<float, bf16_t>(p, b, stream) : markov_small_launch<float, float>(p, b, stream));
-        markov_join_kernel<true><<<n, kJoinThreads, 0, stream>>>(p, b, join);
+        markov_join_kernel<true><<<n, kJoinMany, 0, stream>>>(p, b, join);
         return cudaGetLastError();
     }
     const unsigned grid = (unsigned)((n + 63) / 64) * (64 / kMarkovWarps);   // whole words of marks

@@ -9,7 +9,6 @@ namespace spec {
 constexpr int kMarkovPairs = 76;                 // CTA pairs that a tensor-core product is cut for
 constexpr int kMarkovSmall = 8;                  // rows that one pass over the weights takes
 constexpr int kMarkovSlabs = 304;                // most slabs of that pass
-constexpr int kMarkovTurn = 128;                 // entries that a CTA takes at a time
 constexpr int kJoinRun = 8;                      // rows of a token that one CTA joins
 constexpr size_t kMarkovStage = 96u << 20;       // bytes that are staged at a time, about
 
