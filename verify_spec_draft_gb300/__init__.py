@@ -827,7 +827,7 @@ def policy_loss(logits, tokens, old_logp, advantage, ref_logp=None, weight=None,
         (torch.int32, f32, f32, f32, f32), (lead,) * 5)
     if out is None:
         with _made_on(stream):
-            out = dict(loss=torch.empty(lead, dtype=f32, device=dev), logp=torch.empty(lead, dtype=f32, device=dev))
+            out = dict(loss=torch.empty_like(old_logp), logp=torch.empty_like(old_logp))   # float32 [...], as checked
             if grad:
                 out["grad"] = _rows_like(logits, ld)
     else:
@@ -875,7 +875,7 @@ def markov_grad(grad, anchor, tokens, U, Wt, dtype=None, ws=None, out=None, stre
                                            ((B,), (B, gamma), U.shape, U.shape))
     if out is None:
         with _made_on(stream):
-            out = {k: torch.empty((V, r), dtype=dtype or U.dtype, device=dev) for k in ("U", "Wt")}
+            out = dict(U=torch.empty_like(U, dtype=dtype), Wt=torch.empty_like(U, dtype=dtype))
     else:
         dtype = dtype or (U.dtype if out.get("U") is None else out["U"].dtype)
         _need_out(out, dev, U=(dtype, (V, r)), Wt=(dtype, (V, r)))
