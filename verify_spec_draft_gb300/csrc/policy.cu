@@ -346,10 +346,9 @@ __global__ void __launch_bounds__(kPolThreads(MODE), MODE == 0 ? 6 : 4) policy_k
             if (rank == 0 && tid == 0) p.loss_out[row] = p.logp_out[row] = NAN;
         }
     }
-    if (MODE) {   // (a CTA's memory stays until the last pair that was sent to it is in)
-        cluster_arrive();
-        cluster_wait();
-    }
+    // a CTA's memory stays until the last pair that was sent to it is in (the loss alone: the first CTA's)
+    cluster_arrive();
+    if (MODE || rank == 0) cluster_wait();
 }
 
 // The cluster's size.  With the gradient: slices of 53 KB at most, so that four CTAs share an SM and some load
