@@ -122,3 +122,21 @@ def test_binding_refuses(lib):
         vsd.adamw_state(x.double())
     s = vsd.adamw_state(torch.zeros(300, dtype=torch.bfloat16), bits=8)
     assert s["m"].dtype == torch.float8_e4m3fn and s["v_scale"].shape == (3,) and s["master"].dtype == torch.float32
+
+
+@pytest.mark.parametrize("spans, clash", [
+    ([(100, 10, True, "a"), (110, 10, True, "b"), (90, 10, False, "c")], None),
+    ([(100, 10, False, "a"), (100, 10, False, "b"), (105, 20, False, "c")], None),     # gradients are only read
+    ([(100, 0, True, "a"), (100, 10, True, "b"), (0, 0, True, "c"), (0, 0, True, "d")], None),
+    ([(100, 10, True, "a"), (100, 10, True, "b")], "b overlaps a"),
+    ([(100, 10, True, "a"), (100, 10, False, "b")], "b overlaps a"),
+    ([(100, 10, False, "a"), (100, 10, True, "b")], "b overlaps a"),
+    ([(100, 50, True, "a"), (110, 5, False, "b"), (140, 1, True, "c")], "b overlaps a"),
+    ([(100, 50, True, "a"), (150, 5, True, "b"), (140, 1, True, "c")], "c overlaps a"),
+    ([(100, 50, False, "a"), (110, 5, False, "b"), (149, 9, True, "c")], "c overlaps a"),
+])
+def test_a_table_uses_no_memory_twice(spans, clash):
+    if clash is None:
+        return vsd._distinct(spans)
+    with pytest.raises(ValueError, match=clash):
+        vsd._distinct(spans)

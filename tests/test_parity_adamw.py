@@ -271,3 +271,28 @@ def test_refusals(spec):
     with pytest.raises(vsd.SpecError):
         vsd.adamw(table, step, lr=0.1, ws=torch.zeros(16, dtype=torch.uint8, device="cuda"))
     assert int(step) == 0
+
+
+def test_memory_used_twice_is_refused(spec):
+    p, g = torch.zeros(256, device="cuda"), torch.ones(256, device="cuda")
+    state = lambda t: vsd.adamw_state(t, 8)
+    for bad in (([p, p], [g, g], [state(p), state(p)]), ([p], [p], [state(p)]),
+                ([p[:200], p[100:]], [g[:200], g[100:]], [state(p[:200]), state(p[100:])])):
+        with pytest.raises(ValueError, match="overlaps"):
+            vsd.adamw_table(*bad)
+    s = state(p)
+    with pytest.raises(ValueError, match="overlaps"):
+        vsd.adamw_table([p, p.clone()], [g, g], [s, s])
+    vsd.adamw_table([p[:100], p[100:]], [g[:100], g[:156]], [state(p[:100]), state(p[100:])])    # one gradient for two
+
+
+def test_a_table_keeps_its_memory(spec):
+    p = torch.zeros(1 << 20, device="cuda")
+    g = torch.ones(1 << 20, device="cuda")
+    table = vsd.adamw_table([p], [g], [vsd.adamw_state(p)])
+    at = p.data_ptr()
+    p.data = torch.full((1 << 20,), 5.0, device="cuda")
+    other = [torch.full((1 << 20,), 7.0, device="cuda") for _ in range(4)]     # would take what had been freed
+    assert all(o.data_ptr() != at for o in other)
+    vsd.adamw(table, torch.zeros(1, dtype=torch.int32, device="cuda"), lr=0.1)
+    assert (p == 5.0).all() and all((o == 7.0).all() for o in other)

@@ -83,6 +83,7 @@ class AdamwTensor(ctypes.Structure):
 
 
 ADAMW_BLOCK = 128   # entries that share an 8-bit state's scale
+_STATE = ("master", "m", "v", "m_scale", "v_scale")
 _lib = None
 
 
@@ -918,15 +919,32 @@ class AdamwTable:
 
     def __init__(self, params, grads, states, device, entries):
         self.params, self.grads, self.states, self.device, self.entries = params, grads, states, device, entries
+        # the memory that the addresses are of, whatever a tensor is given later (p.data = ...)
+        self.storages = [t.untyped_storage() for p, g, s in zip(params, grads, states)
+                         for t in (p, g, *map(s.get, _STATE)) if t is not None]
 
     def __len__(self):
         return len(self.params)
 
 
+def _distinct(spans):
+    """Refuses memory that a step writes and uses a second time (one parameter listed twice, tied
+    weights): spans are (address, bytes, written, name)."""
+    last = last_written = (0, None)     # where what lies furthest ends: of all so far, of the written ones
+    for at, size, written, name in sorted((s for s in spans if s[1] > 0), key=lambda s: s[0]):
+        end, other = last if written else last_written
+        if at < end:
+            raise ValueError(f"{name} overlaps {other}")
+        last = max(last, (at + size, name), key=lambda x: x[0])
+        if written:
+            last_written = max(last_written, (at + size, name), key=lambda x: x[0])
+
+
 def adamw_table(params, grads, states):
     """The tensors of an AdamW step, checked once and kept: lists of parameters (f32/bf16), of
     their gradients (f32/bf16, read anew at every step) and of their states (adamw_state's dicts;
-    32 and 8 bits may be mixed).  Steps write the parameters and states in place."""
+    32 and 8 bits may be mixed).  Steps write the parameters and states in place, so none of them may
+    overlap another tensor of the table; a tensor that is given other memory later needs a new table."""
     torch = _torch()
     params, grads, states = list(params), list(grads), list(states)
     if not len(params) == len(grads) == len(states):
@@ -938,6 +956,7 @@ def adamw_table(params, grads, states):
     dev = params[0].device
     f32, f8 = torch.float32, torch.float8_e4m3fn
     entries = (AdamwTensor * len(params))()
+    spans = []
     for i, (p, g, s, e) in enumerate(zip(params, grads, states, entries)):
         _need(p, f"parameter {i}", dev)
         e.param_dtype = _dtype_code(p)
@@ -961,6 +980,10 @@ def adamw_table(params, grads, states):
         e.state_bits = 8 if packed else 32
         if packed:
             e.m_scale, e.v_scale = s["m_scale"].data_ptr(), s["v_scale"].data_ptr()
+        used = [("parameter", p), ("gradient", g)] + [(f"{k} of state", s.get(k)) for k in _STATE]
+        spans += [(t.data_ptr(), t.numel() * t.element_size(), name != "gradient", f"{name} {i}")
+                  for name, t in used if t is not None]
+    _distinct(spans)
     return AdamwTable(params, grads, states, dev, entries)
 
 
