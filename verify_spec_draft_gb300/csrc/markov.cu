@@ -33,6 +33,7 @@ __global__ void __launch_bounds__(kMarkovThreads) markov_order_kernel(MarkovPara
     const int n = p.B * p.gamma, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int i = blockIdx.x * kMarkovWarps + warp, r8 = round8(p.r);
     bool bad = false;
+    pdl_launch_dependents();
     const int mine = i < n ? markov_token(p, i, &bad) : 0;
     if (threadIdx.x == 0) s_none = 0u;
     __syncthreads();
@@ -129,6 +130,7 @@ __global__ void __launch_bounds__(kMarkovThreads, 2) markov_small_kernel(MarkovP
     const int entries = kMarkovThreads / quads;          // of a turn
     const int k = tid % quads * 4, e = tid / quads;
     bool bad = false;
+    pdl_launch_dependents();
     if (tid < N) s_row[tid] = tid < n ? markov_token(p, tid, &bad) : p.V;
     if (bad && blockIdx.x == 0) atomicOr(b.status, SPEC_DEV_TOKEN);
     __syncthreads();
@@ -217,22 +219,29 @@ __global__ void __launch_bounds__(SMALL ? kJoinMany : kJoinThreads) markov_join_
     __shared__ float4 s_sum[TH];
     const int at = blockIdx.x;
     int t, rows, all, index[kJoinRun];
+    pdl_launch_dependents();
+    if (!SMALL) pdl_wait_primary();
     if (SMALL) {
         static_assert(kMarkovSmall == kJoinRun, "a CTA joins all rows of a token");
         const int n = p.B * p.gamma;
         bool bad = false;
         t = markov_token(p, at, &bad);
         rows = 0;
+        int first = at;
+#pragma unroll
+        for (int i = kMarkovSmall - 1; i >= 0; --i)
+            if (i < n && markov_token(p, i, &bad) == t) first = i;
 #pragma unroll
         for (int i = 0; i < kMarkovSmall; ++i) {
             if (i >= n || markov_token(p, i, &bad) != t) continue;
-            if (i < at) return;   // that one's
 #pragma unroll
             for (int q = 0; q < kJoinRun; ++q)
                 if (q == rows) index[q] = i;
             ++rows;
         }
         all = rows;
+        pdl_wait_primary();
+        if (t >= p.V || first < at) return;   // none, or that one's
     } else {
         const int2 run = b.run[at];
         t = b.token[at];
@@ -242,7 +251,6 @@ __global__ void __launch_bounds__(SMALL ? kJoinMany : kJoinThreads) markov_join_
 #pragma unroll
         for (int q = 0; q < kJoinRun; ++q) index[q] = b.order[at + min(q, rows - 1)];
     }
-    if (SMALL && t >= p.V) return;
     const int quads = round4(p.r) / 4, groups = TH / quads;
     const int k = threadIdx.x % quads, g = threadIdx.x / quads;
     float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -264,13 +272,14 @@ __global__ void __launch_bounds__(SMALL ? kJoinMany : kJoinThreads) markov_join_
     if (all <= kJoinRun) join_out(p, t, k, s);
     else reinterpret_cast<float4*>(b.runs + (long)at * round4(p.r))[k] = s;
 }
-void markov_join(const MarkovParams& p, const MarkovBind& b, const MarkovJoin& a, cudaStream_t stream) {
-    markov_join_kernel<false><<<p.B * p.gamma, kJoinThreads, 0, stream>>>(p, b, a);
+cudaError_t markov_join(const MarkovParams& p, const MarkovBind& b, const MarkovJoin& a, cudaStream_t stream) {
+    return launch_behind(markov_join_kernel<false>, dim3((unsigned)(p.B * p.gamma)), kJoinThreads, 0, stream, p, b, a);
 }
 
 // The tokens of more rows: a CTA looks at 32 places for where one begins.
 __global__ void __launch_bounds__(kJoinThreads) markov_runs_kernel(MarkovParams p, MarkovBind b) {
     __shared__ float4 s_sum[kJoinThreads];
+    pdl_wait_primary();
     if (blockIdx.x == 0 && threadIdx.x == 0) *b.unclean = 0u;
     const int n = p.B * p.gamma;
     const int quads = round4(p.r) / 4, groups = kJoinThreads / quads;
@@ -354,16 +363,15 @@ cudaError_t markov_grad_launch(const MarkovParams& p, void* ws, cudaStream_t str
         MarkovJoin join = {0, n, round4(p.r)};
         join.parts = g16 ? (w16 ? markov_small_launch<bf16_t, bf16_t>(p, b, stream) : markov_small_launch<bf16_t, float>(p, b, stream))
                          : (w16 ? markov_small_launch<float, bf16_t>(p, b, stream) : markov_small_launch<float, float>(p, b, stream));
-        markov_join_kernel<true><<<n, kJoinMany, 0, stream>>>(p, b, join);
-        return cudaGetLastError();
+        const cudaError_t e = launch_behind(markov_join_kernel<true>, dim3((unsigned)n), kJoinMany, 0, stream, p, b, join);
+        return e != cudaSuccess ? e : cudaGetLastError();
     }
     const unsigned grid = (unsigned)((n + 63) / 64) * (64 / kMarkovWarps);   // whole words of marks
     if (w16) markov_order_kernel<bf16_t><<<grid, kMarkovThreads, 0, stream>>>(p, b, 1);
     else markov_order_kernel<float><<<grid, kMarkovThreads, 0, stream>>>(p, b, 3);
-    const cudaError_t e = markov_tc_launch(p, b, stream);
-    if (e != cudaSuccess) return e;
-    markov_runs_kernel<<<(n + 31) / 32, kJoinThreads, 0, stream>>>(p, b);
-    return cudaGetLastError();
+    cudaError_t e = markov_tc_launch(p, b, stream);
+    if (e == cudaSuccess) e = launch_behind(markov_runs_kernel, dim3((unsigned)((n + 31) / 32)), kJoinThreads, 0, stream, p, b);
+    return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace spec

@@ -66,6 +66,23 @@ __device__ __forceinline__ void bf16_parts(float x, float (&o)[3]) {
     o[2] = bf16_part(r - o[1]);
 }
 
+// A kernel launched as the programmatic dependent of the one before it: it is set up meanwhile, and waits for
+// that one before it reads or writes anything but the call's inputs.
+template <typename... P, typename... A>
+inline cudaError_t launch_behind(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t stream, const A&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+
 // Where the join finds row i's part: part[(p * part_stride + i) * pitch], 16 bytes aligned.
 struct MarkovJoin { int parts; long part_stride; int pitch; };
 
@@ -74,7 +91,7 @@ __host__ inline int markov_slice(int n, int r, int V) {
     const size_t most = kMarkovStage / ((size_t)(n + round8(r)) * 6) / 256 * 256;
     return most < 256 ? 256 : (most < (size_t)V ? (int)most : V);
 }
-void markov_join(const MarkovParams& p, const MarkovBind& b, const MarkovJoin& a, cudaStream_t stream);
+cudaError_t markov_join(const MarkovParams& p, const MarkovBind& b, const MarkovJoin& a, cudaStream_t stream);
 // both products and the join of dX's parts
 cudaError_t markov_tc_launch(const MarkovParams& p, const MarkovBind& b, cudaStream_t stream);
 

@@ -59,7 +59,7 @@ __device__ __forceinline__ uint32_t peer_addr(const void* p, unsigned rank) {
 }
 // An arrival in a CTA of the pair.  What it reports is not this thread's memory (TMEM that tcgen05.ld has waited
 // for, or a stage that copies have written), so it releases nothing beyond the CTA: at cluster scope it
-// would wait for the epilogue's stores (610 us of 284 then).
+// would wait for the epilogue's stores (then 610 us for 284).
 __device__ __forceinline__ void remote_arrive(uint64_t* bar, unsigned rank) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" :: "r"(peer_addr(bar, rank)) : "memory");
 }
@@ -166,7 +166,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMtcThreads, 1)
     const unsigned rank = blockIdx.x & 1u;
     const bool DX = (int)(blockIdx.x >> 1) >= dx.first;
     const MarkovTc& a = DX ? dx : wt;
-    if (CLEAN && *b.unclean == 0u) return;
+    pdl_launch_dependents();
+    if (CLEAN) {
+        pdl_wait_primary();
+        if (*b.unclean == 0u) return;
+    }
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
             mbar_init(&s_full[s], 1);
@@ -191,6 +195,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMtcThreads, 1)
     tc_fence_after();
     const uint32_t tmem = s_tmem;
     MtcItem item;
+    if (!CLEAN) pdl_wait_primary();   // the rows' U, what is staged, and whoever still reads dX's parts
 
     if (warp == 0) {
         if (lane == 0) {
@@ -324,7 +329,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMtcThreads, 1)
                 }
             } else {
                 // the thread's columns, 64 bytes at a time, through the warp's 2 KB, so that 4 lanes write
-                // a row's 64 bytes (a 16-byte word a lane of 32 different rows took 284 us of 235)
+                // a row's 64 bytes (a 16-byte word a lane of 32 different rows took 284 us for 235)
                 const int v0 = a.v0 + item.tile * 256 + (int)rank * 128 + quad * 32;
                 uint4* sc = reinterpret_cast<uint4*>(ring + (size_t)S * C::bytes) + (warp - 3) * 128;
                 const bool half = p.odt == SPEC_BF16;
@@ -413,6 +418,7 @@ template <typename T, int PLANES>
 __global__ void __launch_bounds__(256) markov_stage_kernel(const T* src, long ld, int rows, int columns, int pitch, bf16_t* out,
                                                            const uint8_t* none) {
     const int c = (int)(blockIdx.x * blockDim.x + threadIdx.x) * 8;
+    pdl_launch_dependents();
     if (c >= columns) return;
     const int step = (int)(gridDim.y * blockDim.y);
     const bool inside = c >= 8 && c + 16 <= columns;   // every word that is touched lies in the row
@@ -574,18 +580,20 @@ static cudaError_t mtc_launch(const MarkovParams& p, const MarkovBind& b, cudaSt
         wt.v0 = dx.v0 = v0;
         wt.v1 = dx.v1 = v0 + width;
         dx.add = v0 > 0;
-        kern<<<2 * (wt.pairs + dx.pairs), kMtcThreads, Mtc<NT>::smem, stream>>>(p, b, wt, dx, zmap, umap, wmap);
+        e = launch_behind(kern, dim3(2u * (unsigned)(wt.pairs + dx.pairs)), kMtcThreads, Mtc<NT>::smem, stream, p, b, wt, dx, zmap, umap, wmap);
+        if (e != cudaSuccess) return e;
     }
-    markov_join(p, b, {dx.parts, (long)dx.tiles * 256, NT}, stream);
+    e = markov_join(p, b, {dx.parts, (long)dx.tiles * 256, NT}, stream);
+    if (e != cudaSuccess) return e;
     if (!stage_z) {   // (a staged row without a token is 0)
         if (!mtc_map(&zmap, p.grad, p.V, n, p.ld, 1)) return cudaErrorInvalidValue;
         wt.tiles = (p.V + 255) / 256;
         wt.v0 = 0;
         wt.v1 = p.V;
         wt.pairs = dx.first = wt.tiles < pairs ? wt.tiles : pairs;
-        clean<<<2 * wt.pairs, kMtcThreads, Mtc<NT>::smem, stream>>>(p, b, wt, dx, zmap, umap, umap);
+        e = launch_behind(clean, dim3(2u * (unsigned)wt.pairs), kMtcThreads, Mtc<NT>::smem, stream, p, b, wt, dx, zmap, umap, umap);
     }
-    return cudaGetLastError();
+    return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 cudaError_t markov_tc_launch(const MarkovParams& p, const MarkovBind& b, cudaStream_t stream) {
