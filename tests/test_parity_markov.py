@@ -205,3 +205,19 @@ def test_refusals(spec):
     with pytest.raises(vsd.SpecError):
         need = vsd.workspace_bytes(vsd.OP_MARKOV_GRAD, 3, 4, 100, 8)
         vsd.markov_grad(dz, anchor, tokens, U, Wt, ws=torch.zeros(need - 1, dtype=torch.uint8, device="cuda"))
+
+
+@pytest.mark.parametrize("gdt,wdt,out", [(F32, F32, F32), (BF16, BF16, BF16), (BF16, F32, F32)])
+@pytest.mark.parametrize("V,r", [(40000, 32), (39041, 31), (5003, 256), (20011, 250), (78000, 12), (45000, 28), (39000, 16),
+                                 (40001, 2)])
+def test_a_few_rows_many_turns(spec, V, r, gdt, wdt, out):
+    """Every CTA takes more than one turn, of 1 to 4 entries a thread; one row's dz is not finite and does not
+    count.  A thread adds V / 608 terms at most, a CTA 128 threads' and the join 304 CTAs' sums: fewer than the
+    roundings that check counts."""
+    a = list(inputs(2, 4, V, r, gdt, wdt, seed=V))
+    a[2][1, 1] = -1
+    a[0][1, 2] = torch.nan
+    got = vsd.markov_grad(*on_gpu(*a), dtype=out)
+    want = om.markov_grad(*(t.double().numpy() if t.is_floating_point() else t.numpy() for t in a))
+    check(got, want, 8, V, out)
+    assert vsd.device_status(got["ws"]) == 0

@@ -87,50 +87,86 @@ __global__ void __launch_bounds__(kMarkovThreads) markov_order_kernel(MarkovPara
 
 // A few rows: one pass over the vocabulary forms both products.  A thread takes 4 columns of an entry v:
 // dWt[v] = sum_i dz[i, v] U[x_i] with U's rows in shared memory, and dX's sums of its columns in
-// registers, one per row, which the CTA's threads bring together at the end.  Bound by memory: Wt in, dWt and
-// dU's zeros out.  The tensor cores would spend their steps of 64 rows on zeros.
-template <typename T>
-__device__ __forceinline__ float4 quad_load(const T* a, int k, int r) {   // entries k..k + 3 of a row of r
-    if (r % 4 == 0) {
-        if constexpr (sizeof(T) == 4) {
-            return __ldg(reinterpret_cast<const float4*>(a + k));
-        } else {
-            const uint2 w = __ldg(reinterpret_cast<const uint2*>(a + k));
-            return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u),
-                               __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u));
-        }
-    }
-    return make_float4(load_one(a + k), k + 1 < r ? load_one(a + k + 1) : 0.0f, k + 2 < r ? load_one(a + k + 2) : 0.0f,
-                       k + 3 < r ? load_one(a + k + 3) : 0.0f);
+// registers, one per row, which the CTA's threads bring together at the end.  The tensor cores would spend their
+// steps of 64 rows on zeros, and need float32 operands split (GPU time of the call, 7 rows, here and there:
+// V = 32,000, r = 32 float32 9.9 and 48 us; 248,320, 64 bf16, float32 out 35 and 64; 248,320, 256 bf16 91 and 82,
+// float32 out 116 and 123).  Bound by memory where V is large, Wt in, dWt and dU's zeros out (5.5 TB/s at the last),
+// and by issue slots beside it; by a chain of latencies where it is small.
+template <typename T> struct QuadWord { typedef uint2 type; };
+template <> struct QuadWord<float> { typedef float4 type; };
+__device__ __forceinline__ float4 quad_value(const float4& w) { return w; }
+__device__ __forceinline__ float4 quad_value(const uint2& w) {
+    return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u),
+                       __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u));
 }
-__device__ __forceinline__ void quad_store(void* out, int dtype, long at, int k, int r, const float4& x) {
-    if (r % 4 == 0) {
+template <bool VEC> __device__ __forceinline__ float4 quad_load(const float* a, int left) {   // entries a[0..3], `left` of them
+    if (VEC) return __ldg(reinterpret_cast<const float4*>(a));
+    return make_float4(__ldg(a), left > 1 ? __ldg(a + 1) : 0.0f, left > 2 ? __ldg(a + 2) : 0.0f, left > 3 ? __ldg(a + 3) : 0.0f);
+}
+template <bool VEC> __device__ __forceinline__ uint2 quad_load(const bf16_t* a, int left) {
+    if (VEC) return __ldg(reinterpret_cast<const uint2*>(a));
+    const unsigned short* h = reinterpret_cast<const unsigned short*>(a);
+    uint32_t x[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) x[q] = q < left ? __ldg(h + q) : 0u;
+    return make_uint2(x[0] | x[1] << 16, x[2] | x[3] << 16);
+}
+template <bool VEC> __device__ __forceinline__ void quad_store(void* out, int dtype, long at, int left, const float4& x) {
+    if (VEC) {
         if (dtype == SPEC_BF16) {
             uint2 w;
             asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w.x) : "f"(x.y), "f"(x.x));
             asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w.y) : "f"(x.w), "f"(x.z));
-            *reinterpret_cast<uint2*>(reinterpret_cast<bf16_t*>(out) + at + k) = w;
+            *reinterpret_cast<uint2*>(reinterpret_cast<bf16_t*>(out) + at) = w;
         } else {
-            *reinterpret_cast<float4*>(reinterpret_cast<float*>(out) + at + k) = x;
+            *reinterpret_cast<float4*>(reinterpret_cast<float*>(out) + at) = x;
         }
         return;
     }
     const float o[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
     for (int h = 0; h < 4; ++h)
-        if (k + h < r) put(out, dtype, at + k + h, o[h]);
+        if (h < left) put(out, dtype, at + h, o[h]);
 }
-template <typename G, typename W>
+constexpr int kSmallTurn = 4;                    // most entries of a thread in a turn
+constexpr int kSmallTile = 128;                  // most entries of a CTA's turn
+// FULL: rows of whole fours, and kSmallTurn entries a turn
+template <typename G, typename W, bool FULL>
 __global__ void __launch_bounds__(kMarkovThreads, 2) markov_small_kernel(MarkovParams p, MarkovBind b) {
-    constexpr int N = kMarkovSmall;
+    constexpr int N = kMarkovSmall, K = kSmallTurn, Z = N * kSmallTile / kMarkovThreads;
     __shared__ __align__(16) float s_u[N][SPEC_MAX_RANK];
-    __shared__ float s_x[4 * N][kMarkovThreads + 1];
+    __shared__ float s_x[4 * N][kMarkovThreads + 1];     // first, dz's values of two turns
     __shared__ int s_row[N];
+    float (*s_z)[N][kSmallTile] = reinterpret_cast<float (*)[N][kSmallTile]>(&s_x[0][0]);
     const int n = p.B * p.gamma, tid = threadIdx.x, pitch = round4(p.r), quads = pitch / 4;
-    const int entries = kMarkovThreads / quads;          // of a turn
+    const int entries = min(kMarkovThreads / quads, kSmallTile);   // side by side
+    const int turn = FULL ? K : min(K, kSmallTile / entries), tile = turn * entries;
     const int k = tid % quads * 4, e = tid / quads;
-    bool bad = false;
+    const W* Wt = reinterpret_cast<const W*>(p.Wt);
+    const G* dz = reinterpret_cast<const G*>(p.grad);
     pdl_launch_dependents();
+    // the next turn's values are on their way while this one's are used, the first ones' before the tokens are known
+    typename QuadWord<W>::type next_w[K];
+    G next_z[Z];
+    auto fetch = [&](int v0) {
+        const int c = tid % kSmallTile, i0 = tid / kSmallTile;
+#pragma unroll
+        for (int q = 0; q < Z; ++q) {
+            const int i = i0 + q * (kMarkovThreads / kSmallTile);
+            next_z[q] = G();
+            if (i < n && c < tile && v0 + c < p.V) next_z[q] = __ldg(dz + (long)i * p.ld + v0 + c);
+        }
+#pragma unroll
+        for (int q = 0; q < K; ++q) {
+            const int v = v0 + q * entries + e;
+            next_w[q] = typename QuadWord<W>::type();
+            if (e < entries && q < turn && v < p.V) next_w[q] = quad_load<FULL>(Wt + ((long)v * p.r + k), p.r - k);
+        }
+    };
+    const int step = (int)gridDim.x * tile;
+    int v0 = (int)blockIdx.x * tile;
+    fetch(v0);
+    bool bad = false;
     if (tid < N) s_row[tid] = tid < n ? markov_token(p, tid, &bad) : p.V;
     if (bad && blockIdx.x == 0) atomicOr(b.status, SPEC_DEV_TOKEN);
     __syncthreads();
@@ -138,41 +174,44 @@ __global__ void __launch_bounds__(kMarkovThreads, 2) markov_small_kernel(MarkovP
         const int i = a / pitch, c = a - i * pitch;
         s_u[i][c] = s_row[i] < p.V && c < p.r ? load_one(reinterpret_cast<const W*>(p.U) + (long)s_row[i] * p.r + c) : 0.0f;
     }
-    // a row without a token is read as the first one is, and counts as 0: no load waits for a test
-    const G* dz[N];
-    unsigned on = 0u;
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        on |= s_row[i] < p.V ? 1u << i : 0u;
-        dz[i] = reinterpret_cast<const G*>(p.grad) + (s_row[i] < p.V ? (long)i * p.ld : 0l);
-    }
-    __syncthreads();
-    const W* Wt = reinterpret_cast<const W*>(p.Wt);
-    float4 x[N];
+    float4 x[N], w[K];
 #pragma unroll
     for (int i = 0; i < N; ++i) x[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    if (e < entries) {
-        const int step = (int)gridDim.x * entries;
-#pragma unroll 2
-        for (int v = (int)blockIdx.x * entries + e; v < p.V; v += step) {
-            const float4 w = quad_load(Wt + (long)v * p.r, k, p.r);
-            float d[N];
+    for (int buf = 0; v0 < p.V; v0 += step, buf ^= 1) {
 #pragma unroll
-            for (int i = 0; i < N; ++i) d[i] = load_one(dz[i] + v);
+        for (int q = 0; q < Z; ++q) {   // (a row without a token counts as 0)
+            const int i = tid / kSmallTile + q * (kMarkovThreads / kSmallTile);
+            s_z[buf][i][tid % kSmallTile] = s_row[i] < p.V ? to_float(next_z[q]) : 0.0f;
+        }
 #pragma unroll
-            for (int i = 0; i < N; ++i) d[i] = (on >> i) & 1u ? d[i] : 0.0f;
-            float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int q = 0; q < K; ++q) w[q] = quad_value(next_w[q]);
+        __syncthreads();   // (and so the buffer that is written next has been read)
+        if (v0 + step < p.V) fetch(v0 + step);
+        if (e >= entries) continue;
+        float4 o[K];
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const float4 u = *reinterpret_cast<const float4*>(&s_u[i][k]);
-                o.x = fmaf(d[i], u.x, o.x); o.y = fmaf(d[i], u.y, o.y); o.z = fmaf(d[i], u.z, o.z); o.w = fmaf(d[i], u.w, o.w);
-                x[i].x = fmaf(d[i], w.x, x[i].x); x[i].y = fmaf(d[i], w.y, x[i].y);
-                x[i].z = fmaf(d[i], w.z, x[i].z); x[i].w = fmaf(d[i], w.w, x[i].w);
+        for (int q = 0; q < K; ++q) o[q] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const float4 u = *reinterpret_cast<const float4*>(&s_u[i][k]);
+#pragma unroll
+            for (int q = 0; q < K; ++q) {
+                if (q >= turn) continue;
+                const float z = s_z[buf][i][q * entries + e];
+                o[q].x = fmaf(z, u.x, o[q].x); o[q].y = fmaf(z, u.y, o[q].y); o[q].z = fmaf(z, u.z, o[q].z); o[q].w = fmaf(z, u.w, o[q].w);
+                x[i].x = fmaf(z, w[q].x, x[i].x); x[i].y = fmaf(z, w[q].y, x[i].y);
+                x[i].z = fmaf(z, w[q].z, x[i].z); x[i].w = fmaf(z, w[q].w, x[i].w);
             }
-            quad_store(p.dWt_out, p.odt, (long)v * p.r, k, p.r, o);
-            quad_store(p.dU_out, p.odt, (long)v * p.r, k, p.r, make_float4(0.0f, 0.0f, 0.0f, 0.0f));
+        }
+#pragma unroll
+        for (int q = 0; q < K; ++q) {
+            const int v = v0 + q * entries + e;
+            if (q >= turn || v >= p.V) continue;
+            quad_store<FULL>(p.dWt_out, p.odt, (long)v * p.r + k, p.r - k, o[q]);
+            quad_store<FULL>(p.dU_out, p.odt, (long)v * p.r + k, p.r - k, make_float4(0.0f, 0.0f, 0.0f, 0.0f));
         }
     }
+    __syncthreads();
     // the threads' sums of dX, in order
 #pragma unroll
     for (int i = 0; i < N; ++i) {
@@ -304,15 +343,6 @@ __global__ void __launch_bounds__(kJoinThreads) markov_runs_kernel(MarkovParams 
     }
 }
 
-// One pass for a few rows.  With float32 operands always, as the tensor cores would need them split (7 rows,
-// V = 50,000, r = 50: 24 us here, 68 there); with bf16 ones while the pass, some 11 us and 5.5 per million
-// columns, takes less than the tensor cores' 15 us and 0.22 per thousand entries (V = 248,320: r = 32 54 and
-// 73 us, r = 64 102 and 68).
-static bool markov_small(const MarkovParams& p) {
-    if (p.B * p.gamma > kMarkovSmall) return false;
-    return p.gdt != SPEC_BF16 || p.wdt != SPEC_BF16 || (long)(round4(p.r) - 40) * p.V <= 700000l;
-}
-
 static size_t markov_bind(MarkovBind& b, void* ws, int n, int r, int V) {
     uint8_t* w = reinterpret_cast<uint8_t*>(ws);
     b.status = &reinterpret_cast<WsHeader*>(ws)->status;
@@ -346,11 +376,13 @@ size_t markov_grad_workspace_bytes(int B, int gamma, int V, int r) {
 
 template <typename G, typename W>
 static int markov_small_launch(const MarkovParams& p, const MarkovBind& b, cudaStream_t stream) {
-    const int entries = kMarkovThreads / (round4(p.r) / 4);
-    int slabs = (p.V + entries - 1) / entries;
+    const int side = kMarkovThreads / (round4(p.r) / 4), entries = side < kSmallTile ? side : kSmallTile;
+    const int tile = entries * (kSmallTile / entries < kSmallTurn ? kSmallTile / entries : kSmallTurn);
+    int slabs = (p.V + tile - 1) / tile;
     const int most = 2 * device_sm_count() < kMarkovSlabs ? 2 * device_sm_count() : kMarkovSlabs;
     if (slabs > most) slabs = most;
-    markov_small_kernel<G, W><<<slabs, kMarkovThreads, 0, stream>>>(p, b);
+    if (p.r % 4 == 0 && tile == entries * kSmallTurn) markov_small_kernel<G, W, true><<<slabs, kMarkovThreads, 0, stream>>>(p, b);
+    else markov_small_kernel<G, W, false><<<slabs, kMarkovThreads, 0, stream>>>(p, b);
     return slabs;
 }
 
@@ -358,7 +390,7 @@ cudaError_t markov_grad_launch(const MarkovParams& p, void* ws, cudaStream_t str
     const int n = p.B * p.gamma;
     MarkovBind b;
     markov_bind(b, ws, n, p.r, p.V);
-    const bool small = markov_small(p), g16 = p.gdt == SPEC_BF16, w16 = p.wdt == SPEC_BF16;
+    const bool small = n <= kMarkovSmall, g16 = p.gdt == SPEC_BF16, w16 = p.wdt == SPEC_BF16;
     if (small) {
         MarkovJoin join = {0, n, round4(p.r)};
         join.parts = g16 ? (w16 ? markov_small_launch<bf16_t, bf16_t>(p, b, stream) : markov_small_launch<bf16_t, float>(p, b, stream))
