@@ -5,6 +5,9 @@
 // lane 4 neighbours of each, so every access is whole sectors and a block's largest magnitude is
 // one warp reduction.  The tensors' table lies in the kernel's parameters: nothing is copied to
 // the device, and a captured step replays as it is.
+// Bound by memory: 28 bytes an entry with a bf16 parameter and gradient, a master and 32-bit states (127 M entries
+// 567 to 578 us, 92 to 94 % of the measured copy rate), 16 with 8-bit ones (371 us, 83 %: the codes' rounding
+// takes the issue slots 66 % of the time).
 #include "internal.h"
 #include "spec_device.cuh"
 
@@ -374,7 +377,7 @@ __global__ void __launch_bounds__(kAdamThreads, kAdamCtas) adamw_kernel(const __
                 continue;
             }
             c += (unsigned)whole;
-            // a warp's entries lie in a row (a scale's sector, written by one warp in time: 394 us; by several: 480)
+            // a warp's entries lie in a row (a scale's sector, written by one warp in time: 394 us when this was chosen; by several: 480)
             const long at = start + (long)warp * whole * kAdamUnit;
             switch (kind & 7u) {
 #define SPEC_ADAM_CASE(K)                                                                                             \

@@ -22,6 +22,9 @@
 // is the sum of those pairs of parts that reach 2^-24 of it: 3 with one such operand, 6 with two.
 // dz whose rows do not start on 16 bytes cannot be copied by TMA; it, and what is split, goes through
 // a staged copy, a slice of the vocabulary at a time that stays in L2.
+//
+// Bound by the tensor cores: 1792 rows, V = 248,320, r = 256, bf16 take 310 us, 1.47 PFLOP/s or 75 % of the measured
+// matmul rate (dz and both weights' bytes alone 190 us); the two products one after the other took 398.
 #include "markov.cuh"
 #include "tc_common.cuh"
 
