@@ -69,10 +69,10 @@ __device__ __forceinline__ void bf16_parts(float x, float (&o)[3]) {
 // A kernel launched as the programmatic dependent of the one before it: it is set up meanwhile, and waits for
 // that one before it reads or writes anything but the call's inputs.
 template <typename... P, typename... A>
-inline cudaError_t launch_behind(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t stream, const A&... args) {
+inline cudaError_t launch_behind(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream, const A&... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
-    cfg.blockDim = dim3((unsigned)threads);
+    cfg.blockDim = block;
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr;

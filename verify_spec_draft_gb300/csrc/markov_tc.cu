@@ -440,6 +440,7 @@ __global__ void __launch_bounds__(256) markov_stage_kernel(const T* src, long ld
                     b[q] = __ldg(w + 1);
                 }
             }
+            pdl_wait_primary();   // the marks, and whoever still reads the last slice
 #pragma unroll
             for (int q = 0; q < kStageRows; ++q) {
                 const int row = row0 + q * step;
@@ -467,6 +468,7 @@ __global__ void __launch_bounds__(256) markov_stage_kernel(const T* src, long ld
                     for (int k = 0; k < 8; ++k) x[q][k] = c + k < columns ? load_one(from + k) : 0.0f;
                 }
             }
+            pdl_wait_primary();
 #pragma unroll
             for (int q = 0; q < kStageRows; ++q) {
                 const int row = row0 + q * step;
@@ -484,13 +486,14 @@ __global__ void __launch_bounds__(256) markov_stage_kernel(const T* src, long ld
         }
     }
 }
-static void mtc_stage(const void* src, int dtype, long at, long ld, int rows, int columns, int pitch, bf16_t* out,
+static cudaError_t mtc_stage(const void* src, int dtype, long at, long ld, int rows, int columns, int pitch, bf16_t* out,
                       const uint8_t* none, cudaStream_t stream) {
     const dim3 block = columns <= 256 ? dim3(32, 8) : dim3(256, 1);   // a thread per 8 columns, 4 rows each
     const unsigned x = (unsigned)((columns + 8 * block.x - 1) / (8 * block.x)), y = (unsigned)((rows + kStageRows * block.y - 1) / (kStageRows * block.y));
     const dim3 grid(x, y < 65535u ? y : 65535u);
-    if (dtype == SPEC_BF16) markov_stage_kernel<bf16_t, 1><<<grid, block, 0, stream>>>(reinterpret_cast<const bf16_t*>(src) + at, ld, rows, columns, pitch, out, none);
-    else markov_stage_kernel<float, 3><<<grid, block, 0, stream>>>(reinterpret_cast<const float*>(src) + at, ld, rows, columns, pitch, out, none);
+    if (dtype == SPEC_BF16)
+        return launch_behind(markov_stage_kernel<bf16_t, 1>, grid, block, 0, stream, reinterpret_cast<const bf16_t*>(src) + at, ld, rows, columns, pitch, out, none);
+    return launch_behind(markov_stage_kernel<float, 3>, grid, block, 0, stream, reinterpret_cast<const float*>(src) + at, ld, rows, columns, pitch, out, none);
 }
 
 static bool mtc_map(CUtensorMap* m, const void* base, int width, long rows, long pitch, int planes) {
@@ -573,8 +576,9 @@ static cudaError_t mtc_launch(const MarkovParams& p, const MarkovBind& b, cudaSt
     if (!mtc_map(&umap, b.ux, p.r, n, r8, w16 ? 1 : 3)) return cudaErrorInvalidValue;
     for (int v0 = 0; v0 < p.V; v0 += columns) {
         const int width = columns < p.V - v0 ? columns : p.V - v0;
-        if (stage_z) mtc_stage(p.grad, p.gdt, v0, p.ld, n, width, round8(width), zs, b.none, stream);
-        if (stage_w) mtc_stage(p.Wt, p.wdt, (long)v0 * p.r, p.r, width, p.r, r8, ws, nullptr, stream);
+        if (stage_z) e = mtc_stage(p.grad, p.gdt, v0, p.ld, n, width, round8(width), zs, b.none, stream);
+        if (stage_w && e == cudaSuccess) e = mtc_stage(p.Wt, p.wdt, (long)v0 * p.r, p.r, width, p.r, r8, ws, nullptr, stream);
+        if (e != cudaSuccess) return e;
         if (!mtc_map(&zmap, stage_z ? zs : reinterpret_cast<const bf16_t*>(p.grad) + v0, width, n, stage_z ? round8(width) : p.ld, z16 ? 1 : 3) ||
             !mtc_map(&wmap, stage_w ? ws : reinterpret_cast<const bf16_t*>(p.Wt) + (long)v0 * p.r, p.r, width, r8, w16 ? 1 : 3))
             return cudaErrorInvalidValue;
