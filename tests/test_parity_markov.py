@@ -221,3 +221,18 @@ def test_a_few_rows_many_turns(spec, V, r, gdt, wdt, out):
     want = om.markov_grad(*(t.double().numpy() if t.is_floating_point() else t.numpy() for t in a))
     check(got, want, 8, V, out)
     assert vsd.device_status(got["ws"]) == 0
+
+
+@pytest.mark.parametrize("B,G,V,r,dt", [(140, 64, 500, 8, BF16), (9001, 1, 90, 40, F32), (163, 63, 2000, 130, BF16)])
+def test_many_rows(spec, B, G, V, r, dt):
+    """More rows than are ordered by counting: tokens that come back in many blocks, rows without one and
+    tokens out of range."""
+    a = list(inputs(B, G, V, r, dt, dt, seed=B))
+    a[1][3], a[1][7] = -1, V
+    a[1][B // 2:B // 2 + 50] = 17
+    got = vsd.markov_grad(*on_gpu(*a), dtype=F32)
+    want = om.markov_grad(*(t.double().numpy() if t.is_floating_point() else t.numpy() for t in a))
+    check(got, want, B * G, V, F32)
+    assert vsd.device_status(got["ws"]) == vsd.DEV_TOKEN
+    again = vsd.markov_grad(*on_gpu(*a), dtype=F32)
+    assert torch.equal(again["U"], got["U"]) and torch.equal(again["Wt"], got["Wt"])

@@ -15,6 +15,7 @@ namespace spec {
 constexpr int kMarkovThreads = 256;
 constexpr int kMarkovWarps = kMarkovThreads / 32;
 constexpr int kOrderTile = 2048;                 // tokens compared at a time
+constexpr int kOrderCounted = 4096;              // most rows whose order is counted
 
 // The token before row i's position (V: none, or one that is out of range, which is bad).
 __device__ __forceinline__ int markov_token(const MarkovParams& p, int i, bool* bad) {
@@ -24,6 +25,105 @@ __device__ __forceinline__ int markov_token(const MarkovParams& p, int i, bool* 
     return t < 0 || t >= p.V ? p.V : t;
 }
 
+// The row U[x_i] for the tensor cores, by a warp (0 for a row without a token).
+template <typename W>
+__device__ __forceinline__ void markov_gather(const MarkovParams& p, const MarkovBind& b, int planes, int n, int i, int token, int lane) {
+    const int r8 = round8(p.r);
+    const W* u = reinterpret_cast<const W*>(p.U) + (long)token * p.r;
+    if (planes == 1 && p.r == r8) {
+        const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+        if (lane < r8 / 8)
+            reinterpret_cast<uint4*>(b.ux + (long)i * r8)[lane] = token < p.V ? __ldg(reinterpret_cast<const uint4*>(u) + lane) : zero;
+        return;
+    }
+    for (int k = lane; k < r8; k += 32) {
+        float x[3];
+        bf16_parts(token < p.V && k < p.r ? load_one(u + k) : 0.0f, x);
+#pragma unroll
+        for (int q = 0; q < 3; ++q)
+            if (q < planes) put<bf16_t>(b.ux, ((long)q * n + i) * r8 + k, x[q]);
+    }
+}
+
+// Many rows: blocks of kOrderBlock rows are sorted by (token, row) in shared memory, and a row's place is the sum
+// of its places among the blocks, found by halving (65,536 rows: some
+// 165 us for both kernels, 2385 by counting; 9216 rows 20, 8192 by counting 45; 4096 by counting 16).
+constexpr int kOrderBlock = 2048, kOrderMany = 1024;
+__global__ void __launch_bounds__(kOrderMany) markov_sort_kernel(MarkovParams p, MarkovBind b, unsigned long long* keys) {
+    __shared__ unsigned long long s_key[kOrderBlock];
+    const int n = p.B * p.gamma, lo = blockIdx.x * kOrderBlock, tid = threadIdx.x;
+    pdl_launch_dependents();
+    bool bad = false;
+    for (int k = tid; k < kOrderBlock; k += kOrderMany)   // (what is behind the last row comes last)
+        s_key[k] = lo + k < n ? ((unsigned long long)markov_token(p, lo + k, &bad) << 32) | (unsigned)(lo + k) : ~0ull;
+    if (bad) atomicOr(b.status, SPEC_DEV_TOKEN);
+    for (int size = 2; size <= kOrderBlock; size *= 2)
+        for (int step = size / 2; step > 0; step /= 2) {
+            __syncthreads();
+            const int i = tid / step * 2 * step + tid % step, j = i + step;
+            const unsigned long long x = s_key[i], y = s_key[j];
+            if ((x > y) == ((i & size) == 0)) {
+                s_key[i] = y;
+                s_key[j] = x;
+            }
+        }
+    __syncthreads();
+    for (int k = tid; k < kOrderBlock; k += kOrderMany)
+        if (lo + k < n) keys[lo + k] = s_key[k];
+}
+// keys of a sorted block below `key`
+__device__ __forceinline__ int keys_below(const unsigned long long* keys, int m, unsigned long long key) {
+    int lo = 0;
+    while (m > 0) {
+        const int half = m / 2;
+        if (keys[lo + half] < key) {
+            lo += half + 1;
+            m -= half + 1;
+        } else {
+            m = half;
+        }
+    }
+    return lo;
+}
+template <typename W>
+__global__ void __launch_bounds__(kMarkovThreads) markov_place_kernel(MarkovParams p, MarkovBind b, int planes, const unsigned long long* keys) {
+    __shared__ unsigned s_none;
+    const int n = p.B * p.gamma, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int i = blockIdx.x * kMarkovWarps + warp;
+    bool bad = false;
+    pdl_launch_dependents();
+    const int mine = i < n ? markov_token(p, i, &bad) : 0;
+    if (threadIdx.x == 0) s_none = 0u;
+    __syncthreads();
+    if (i < n) {
+        if (lane == 0 && mine >= p.V) atomicOr(&s_none, 1u << warp);
+        markov_gather<W>(p, b, planes, n, i, mine, lane);
+    }
+    pdl_wait_primary();
+    if (i < n) {   // a lane takes every 32nd block
+        unsigned less = 0u, same = 0u, before = 0u;
+        for (int lo = lane * kOrderBlock; lo < n; lo += 32 * kOrderBlock) {
+            const int m = min(kOrderBlock, n - lo);
+            const unsigned long long first = (unsigned long long)mine << 32;
+            const int at = keys_below(keys + lo, m, first), end = keys_below(keys + lo, m, first + (1ull << 32));
+            less += (unsigned)at;
+            same += (unsigned)(end - at);
+            if (lo + kOrderBlock <= i) before += (unsigned)(end - at);
+            else if (lo <= i) before += (unsigned)(keys_below(keys + lo, m, first | (unsigned)i) - at);
+        }
+        less = __reduce_add_sync(0xffffffffu, less);
+        same = __reduce_add_sync(0xffffffffu, same);
+        before = __reduce_add_sync(0xffffffffu, before);
+        if (lane == 0) {
+            b.order[less + before] = i;
+            b.token[less + before] = mine;
+            b.run[less + before] = make_int2((int)less, (int)same);
+        }
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) b.none[blockIdx.x] = (uint8_t)s_none;
+}
+
 // Row i's place among the rows by (token, row), counted: n comparisons a row, a warp a row.  The warp
 // copies the row U[x_i] for the tensor cores as well; a CTA's 8 rows are a byte of the marks.
 template <typename W>
@@ -31,7 +131,7 @@ __global__ void __launch_bounds__(kMarkovThreads) markov_order_kernel(MarkovPara
     __shared__ int32_t s_tok[kOrderTile];
     __shared__ unsigned s_none;
     const int n = p.B * p.gamma, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int i = blockIdx.x * kMarkovWarps + warp, r8 = round8(p.r);
+    const int i = blockIdx.x * kMarkovWarps + warp;
     bool bad = false;
     pdl_launch_dependents();
     const int mine = i < n ? markov_token(p, i, &bad) : 0;
@@ -41,22 +141,7 @@ __global__ void __launch_bounds__(kMarkovThreads) markov_order_kernel(MarkovPara
         if (bad) atomicOr(b.status, SPEC_DEV_TOKEN);
         if (i < n && mine >= p.V) atomicOr(&s_none, 1u << warp);
     }
-    if (i < n) {
-        const W* u = reinterpret_cast<const W*>(p.U) + (long)mine * p.r;
-        if (planes == 1 && p.r == r8) {
-            const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-            if (lane < r8 / 8)
-                reinterpret_cast<uint4*>(b.ux + (long)i * r8)[lane] = mine < p.V ? __ldg(reinterpret_cast<const uint4*>(u) + lane) : zero;
-        } else {
-            for (int k = lane; k < r8; k += 32) {
-                float x[3];
-                bf16_parts(mine < p.V && k < p.r ? load_one(u + k) : 0.0f, x);
-#pragma unroll
-                for (int q = 0; q < 3; ++q)
-                    if (q < planes) put<bf16_t>(b.ux, ((long)q * n + i) * r8 + k, x[q]);
-            }
-        }
-    }
+    if (i < n) markov_gather<W>(p, b, planes, n, i, mine, lane);
     int less = 0, same = 0, before = 0;   // tokens below this one, rows of it, those of them before this one
     for (int lo = 0; lo < n; lo += kOrderTile) {
         __syncthreads();
@@ -399,9 +484,18 @@ cudaError_t markov_grad_launch(const MarkovParams& p, void* ws, cudaStream_t str
         return e != cudaSuccess ? e : cudaGetLastError();
     }
     const unsigned grid = (unsigned)((n + 63) / 64) * (64 / kMarkovWarps);   // whole words of marks
-    if (w16) markov_order_kernel<bf16_t><<<grid, kMarkovThreads, 0, stream>>>(p, b, 1);
-    else markov_order_kernel<float><<<grid, kMarkovThreads, 0, stream>>>(p, b, 3);
-    cudaError_t e = markov_tc_launch(p, b, stream);
+    cudaError_t e = cudaSuccess;
+    if (n > kOrderCounted) {
+        unsigned long long* keys = reinterpret_cast<unsigned long long*>(b.runs);   // (not in use yet; 16 bytes a row at least)
+        markov_sort_kernel<<<(n + kOrderBlock - 1) / kOrderBlock, kOrderMany, 0, stream>>>(p, b, keys);
+        e = w16 ? launch_behind(markov_place_kernel<bf16_t>, dim3(grid), dim3(kMarkovThreads), 0, stream, p, b, 1, keys)
+                : launch_behind(markov_place_kernel<float>, dim3(grid), dim3(kMarkovThreads), 0, stream, p, b, 3, keys);
+    } else if (w16) {
+        markov_order_kernel<bf16_t><<<grid, kMarkovThreads, 0, stream>>>(p, b, 1);
+    } else {
+        markov_order_kernel<float><<<grid, kMarkovThreads, 0, stream>>>(p, b, 3);
+    }
+    if (e == cudaSuccess) e = markov_tc_launch(p, b, stream);
     if (e == cudaSuccess) e = launch_behind(markov_runs_kernel, dim3((unsigned)((n + 31) / 32)), kJoinThreads, 0, stream, p, b);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
