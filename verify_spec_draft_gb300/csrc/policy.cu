@@ -383,7 +383,8 @@ static cudaError_t policy_typed(PolicyParams p, cudaStream_t stream) {
     const void* kern = kerns[mode][fits];
     cudaError_t e = cudaSuccess;
     if (size > 8) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e == cudaSuccess && mode == 1 && bytes > 48 * 1024) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kPolMost);
+    // (always: what a launch gets without it, 48 KB, is for the slice and the kernel's own arrays together)
+    if (e == cudaSuccess && mode == 1) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kPolMost);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3((unsigned)kPolThreads(mode));
