@@ -660,7 +660,9 @@ spec_status spec_policy_loss(const void* logits, spec_dtype dtype, int rows, int
     p.loss_out = loss_out;
     p.logp_out = logp_out;
     p.grad_out = grad_out;
+    static_assert(sizeof(WsHeader) + sizeof(PolicyWait) <= kWsHeaderBytes, "room behind the header's counters");
     p.status = &reinterpret_cast<WsHeader*>(workspace)->status;
+    p.wait = reinterpret_cast<const PolicyWait*>(reinterpret_cast<WsHeader*>(workspace) + 1);
     return cuda_status(policy_launch(p, (cudaStream_t)stream));
 }
 

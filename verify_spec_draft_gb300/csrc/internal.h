@@ -293,6 +293,10 @@ size_t distill_workspace_bytes(int rows, int V);
 cudaError_t distill_launch(DistillParams p, void* ws, cudaStream_t stream);
 
 // spec_policy_loss
+struct PolicyWait {            // behind the header's counters; 0 but in a test of waits that run out
+    unsigned patience;         // us that a wait lasts
+    unsigned withheld;         // which of its pairs the first CTA keeps to itself, counted from 1
+};
 struct PolicyParams {
     const void* logits;        // rows of `ld` entries apart, V used
     int dtype;
@@ -308,6 +312,7 @@ struct PolicyParams {
     float* logp_out;           // [rows]
     void* grad_out;            // the logits' layout (nullable; may be logits itself)
     unsigned* status;
+    const PolicyWait* wait;
     int slice;                 // words of a row per CTA (chosen at launch)
 };
 cudaError_t policy_launch(PolicyParams p, cudaStream_t stream);

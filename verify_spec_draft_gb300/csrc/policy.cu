@@ -62,6 +62,22 @@ __device__ __forceinline__ void cluster_put(float2* here, uint64_t* bar, unsigne
                  :: "r"(a), "f"(v.x), "f"(v.y), "r"(b) : "memory");
 }
 
+// A wait of 1 s at most, or of the workspace's patience (us, 1000 at least) where that is not 0.
+__device__ __forceinline__ bool pol_wait(uint64_t* bar, unsigned parity, const PolicyParams& p) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const unsigned long long t0 = global_timer_ns();
+    while (!mbar_try_wait(bar, parity)) {
+        const unsigned long long waited = global_timer_ns() - t0;
+        if (waited < 1000000ull) continue;
+        const unsigned us = *(const volatile unsigned*)&p.wait->patience;
+        if (waited > (us ? us * 1000ull : kWaitLimitNs)) {
+            atomicOr(p.status, SPEC_DEV_TIMEOUT);
+            return false;
+        }
+    }
+    return true;
+}
+
 // What the row's CTAs make of its statistics (each for itself).
 struct PolRow {
     float loss, lp;
@@ -116,7 +132,8 @@ __global__ void __launch_bounds__(kPolThreads(MODE), MODE == 0 ? 6 : 4) policy_k
     __shared__ __align__(8) uint64_t s_full[kPolChunks], s_met[2];
     __shared__ float2 s_pair[2][kPolMaxCluster], s_warp[WARPS];
     __shared__ PolRow s_row;
-    __shared__ int s_late;
+    __shared__ int s_gone;          // a wait of this CTA has run out
+    __shared__ unsigned s_withheld;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const unsigned rank = cluster_rank(), size = cluster_size();
     const int n_clusters = (int)(gridDim.x / size);
@@ -125,11 +142,13 @@ __global__ void __launch_bounds__(kPolThreads(MODE), MODE == 0 ? 6 : 4) policy_k
     if (tid == 0) {
         for (int q = 0; q < kPolChunks; ++q) mbar_init(&s_full[q], 1);
         for (int q = 0; q < 2; ++q) mbar_init(&s_met[q], 1);
-        s_late = 0;
+        s_gone = 0;
+        s_withheld = 0u;
         fence_mbar_init();
     }
     __syncthreads();
     cluster_arrive();   // so that no CTA writes into one that has not begun
+    if (tid == 96 && blockIdx.x == 0) s_withheld = *(const volatile unsigned*)&p.wait->withheld;
     // a row's slice: words [first, first + n) of the row, whole words [a, b) of those
     auto row_of = [&](int row) { return SegWords<T, ALIGNED>(reinterpret_cast<const T*>(p.logits) + (long)row * p.ld, p.V); };
     const int first = (int)rank * p.slice;
@@ -160,18 +179,15 @@ __global__ void __launch_bounds__(kPolThreads(MODE), MODE == 0 ? 6 : 4) policy_k
     };
     // Warp 0: this CTA's pair to all of the cluster's, and v becomes all of theirs together; false when one
     // did not come in time.  Places are used in turn: the pairs of row i + 2 come after every CTA's of row
-    // i + 1, which it sends when it has read those of row i.
+    // i + 1, which it sends when it has read those of row i.  (A CTA that has waited in vain meets no more: its
+    // barrier's phase is still open, and may not be armed again.)
     auto meet = [&](int i, float2& v) {
         float2* pairs = s_pair[i & 1];
         uint64_t* bar = &s_met[i & 1];
-        if (MODE == 0) {   // (for the first CTA alone)
-            if (lane == 0) cluster_put(&pairs[rank], bar, 0, v);
-            if (rank != 0) return true;
-        } else if (lane < (int)size) {
-            cluster_put(&pairs[rank], bar, lane, v);
-        }
+        if (lane < (MODE == 0 ? 1 : (int)size) && s_withheld != (unsigned)i + 1u) cluster_put(&pairs[rank], bar, lane, v);
+        if (MODE == 0 && rank != 0) return true;   // (for the first CTA alone)
         if (lane == 0) mbar_arrive_expect_tx(bar, size * 8u);
-        const bool here = __all_sync(0xffffffffu, mbar_wait(bar, (i >> 1) & 1, p.status, kWaitLimitNs));
+        const bool here = __all_sync(0xffffffffu, pol_wait(bar, (i >> 1) & 1, p));
         v = lane < (int)size ? pairs[lane] : make_float2(-INFINITY, 0.0f);
         const float m = warp_max_nan(v.x);
         v = make_float2(m, warp_sum(pol_weight(v, m, c)));
@@ -182,6 +198,7 @@ __global__ void __launch_bounds__(kPolThreads(MODE), MODE == 0 ? 6 : 4) policy_k
     if (MODE == 1 && wt != 0.0f) issue(row);
     bool begun = false;
     int live = 0, copies = 0;   // rows that counted so far, and those whose copies were waited for
+    int lost = -1;              // (warp 0) the meeting that one of the cluster did not come to in time
     for (; row < p.rows; row += n_clusters) {
         const SegWords<T, ALIGNED> in = row_of(row);
         T* d = reinterpret_cast<T*>(p.grad_out) + (long)row * p.ld;
@@ -252,12 +269,12 @@ __global__ void __launch_bounds__(kPolThreads(MODE), MODE == 0 ? 6 : 4) policy_k
         if (MODE == 1) {
             const int per = per_of(n);
             for (int q = 0; q < kPolChunks; ++q) {
-                late |= !mbar_wait(&s_full[q], copies & 1, p.status, kWaitLimitNs);
+                late |= !pol_wait(&s_full[q], copies & 1, p);
                 const int end = min(n, (q + 1) * per);
                 if (!late) batch(q * per, end);
             }
             ++copies;
-            if (late) s_late = 1;
+            if (late) s_gone = 1;
         } else {
             batch(0, n);
         }
@@ -277,7 +294,11 @@ __global__ void __launch_bounds__(kPolThreads(MODE), MODE == 0 ? 6 : 4) policy_k
             v = make_float2(wm, warp_sum(pol_weight(v, wm, c)));
             // x's logit is here before the other CTAs learn of the pair, and may write over it
             mine.zx = __shfl_sync(0xffffffffu, mine.zx, 0);
-            if (!meet(live, v)) v.x = NAN;
+            if (!meet(live, v)) {
+                v.x = NAN;
+                lost = live;
+                if (lane == 0) s_gone = 1;
+            }
             if (lane == 0 && (MODE || rank == 0)) {
                 const PolRow r = policy_row(p, v, mine);
                 s_row = r;
@@ -322,15 +343,16 @@ __global__ void __launch_bounds__(kPolThreads(MODE), MODE == 0 ? 6 : 4) policy_k
         if (MODE == 1 && !ALIGNED) fence_proxy_async_smem();   // words written here, before the copy that may cover them
         __syncthreads();   // the slot has been read, and s_row and s_warp
         if (MODE == 1) {
-            if (s_late) break;   // (the same for every thread)
+            if (s_gone) break;   // (the same for every thread)
             if (next_wt != 0.0f) issue(next);
         }
     }
     if (!begun) cluster_wait();
     if (MODE == 1 && row < p.rows) {
-        // a copy has not come in time: nothing of this CTA's may still be on its way when it ends, and the
-        // rest of its rows' slices have no gradient
-        for (int q = 0; q < kPolChunks; ++q) mbar_wait(&s_full[q], (copies - 1) & 1, p.status, kWaitLimitNs);
+        // a copy or a pair has not come in time: nothing of this CTA's may still be on its way when it ends, and the
+        // rest of its rows' slices have no gradient.  The cluster's other CTAs wait for its next pair in vain, and
+        // do the same.
+        for (int q = 0; q < kPolChunks; ++q) pol_wait(&s_full[q], (copies - 1) & 1, p);
         for (row += n_clusters; row < p.rows; row += n_clusters) {
             const SegWords<T, ALIGNED> in = row_of(row);
             const uint32_t nan = sizeof(T) == 2 ? 0x7fff7fffu : 0x7fffffffu;
@@ -338,19 +360,16 @@ __global__ void __launch_bounds__(kPolThreads(MODE), MODE == 0 ? 6 : 4) policy_k
             T* d = reinterpret_cast<T*>(p.grad_out) + (long)row * p.ld;
             for (int l = tid, n = words_of(in); l < n; l += TH)
                 in.store(d, first + l, on ? make_uint4(nan, nan, nan, nan) : make_uint4(0u, 0u, 0u, 0u));
-            if (!on) {
-                if (rank == 0 && tid == 0) p.loss_out[row] = p.logp_out[row] = 0.0f;
-                continue;
-            }
-            float2 v = make_float2(NAN, NAN);   // the row's other CTAs are told so
-            if (warp == 0) meet(live, v);
-            ++live;
-            if (rank == 0 && tid == 0) p.loss_out[row] = p.logp_out[row] = NAN;
+            if (rank == 0 && tid == 0) p.loss_out[row] = p.logp_out[row] = on ? NAN : 0.0f;
         }
     }
     // a CTA's memory stays until the last pair that was sent to it is in (the loss alone: the first CTA's)
     cluster_arrive();
     if (MODE || rank == 0) cluster_wait();
+    // (one that was late may still be on its way)
+    if (warp == 0 && lost >= 0)
+        for (const unsigned long long t0 = global_timer_ns();
+             !mbar_try_wait(&s_met[lost & 1], (lost >> 1) & 1) && global_timer_ns() - t0 < 1000000ull;) {}
 }
 
 // The cluster's size.  With the gradient: slices of 53 KB at most, so that four CTAs share an SM and some load
