@@ -719,7 +719,9 @@ spec_status spec_distill(const void *student, spec_dtype dtype, int rows, int V,
  *   clip_low, clip_high   0 <= clip_low <= 1, clip_high >= 0, finite;  kl >= 0, finite.
  *   loss_out    float32 [rows], not weighted; logp_out float32 [rows]: lp.
  *   grad_out    the logits' layout and type; NULL for the loss alone; may be logits itself,
- *               which it then replaces.
+ *               which it then replaces.  An output that overlaps an input or another output in
+ *               any other way is refused (SPEC_ERR_INVALID_ARG); one's rows may lie between
+ *               the other's.
  *   workspace   spec_workspace_bytes(SPEC_OP_POLICY_LOSS, rows, 1, V, 0): the status word.
  * A row with NaN, +inf or no finite entry, or whose old_logp, advantage, ref_logp or weight
  * is not finite, gets NaN in its outputs (flag NONFINITE); a token outside [0, V) does too
@@ -753,8 +755,8 @@ spec_status spec_policy_loss(const void *logits, spec_dtype dtype, int rows, int
  *                 counts for nothing, and its dz is not used; one that is outside [-1, V)
  *                 does too and raises flag TOKEN.
  *   U, Wt         [V, r], weights_dtype; 1 <= r <= SPEC_MAX_RANK.
- *   dU_out, dWt_out  [V, r], out_dtype (float32 or bf16); neither may overlap an input or the
- *                 other.
+ *   dU_out, dWt_out  [V, r], out_dtype (float32 or bf16); one that overlaps an input or the
+ *                 other is refused (SPEC_ERR_INVALID_ARG).
  *   workspace     spec_workspace_bytes(SPEC_OP_MARKOV_GRAD, B, gamma, V, r).
  * A row's dz or a weight that is not finite makes the sums that it enters not finite.  What a
  * wait that ran out (flag TIMEOUT) kept from being computed is not defined.

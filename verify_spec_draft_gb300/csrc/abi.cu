@@ -40,6 +40,20 @@ static bool dtype_ok(int d) { return d == SPEC_F32 || d == SPEC_BF16; }
 static bool temperature_ok(float t) { return t >= FLT_MIN && t < INFINITY; }
 static size_t dtype_size(int d) { return d == SPEC_F32 ? 4 : 2; }
 
+// Whether an output shares memory with another argument.
+static uintptr_t address(const void* p) { return reinterpret_cast<uintptr_t>(p); }
+static bool spans_meet(uintptr_t a, size_t na, uintptr_t b, size_t nb) { return a < b + nb && b < a + na; }
+struct RowSpan { uintptr_t at; long rows; size_t pitch, bytes; };   // `bytes` of every `pitch`
+static bool rows_meet(const RowSpan& r, uintptr_t a, size_t n) {
+    const size_t i = a < r.at + r.bytes ? 0 : (a - r.at - r.bytes) / r.pitch + 1;   // the first row that ends behind a
+    return i < (size_t)r.rows && r.at + i * r.pitch < a + n;
+}
+// rows of one pitch and length: what lies between those of one may be the other's
+static bool rows_meet(const RowSpan& x, const RowSpan& y) {
+    const RowSpan &a = x.at < y.at ? x : y, &b = x.at < y.at ? y : x;
+    return rows_meet(a, b.at, b.bytes);   // (b's further rows lie to a's further ones as its first to a's first)
+}
+
 }  // namespace spec
 
 using namespace spec;
@@ -640,6 +654,19 @@ spec_status spec_policy_loss(const void* logits, spec_dtype dtype, int rows, int
         return SPEC_ERR_INVALID_ARG;
     if (!aligned16(logits) || !aligned16(grad_out) || !aligned16(workspace)) return SPEC_ERR_ALIGN;
     if (!workspace || workspace_bytes < kWsHeaderBytes) return SPEC_ERR_WORKSPACE;
+    const size_t entry = dtype_size(dtype), words = (size_t)rows * 4;
+    const RowSpan z = {address(logits), rows, ld * entry, V * entry}, dz = {address(grad_out), rows, ld * entry, V * entry};
+    for (const void* i : {(const void*)tokens, (const void*)old_logp, (const void*)advantage,
+                          (const void*)(kl > 0.0f ? ref_logp : nullptr), (const void*)weight})
+        if (i && (spans_meet(address(loss_out), words, address(i), words) || spans_meet(address(logp_out), words, address(i), words) ||
+                  (grad_out && rows_meet(dz, address(i), words))))
+            return SPEC_ERR_INVALID_ARG;
+    if (spans_meet(address(loss_out), words, address(logp_out), words) || rows_meet(z, address(loss_out), words) ||
+        rows_meet(z, address(logp_out), words))
+        return SPEC_ERR_INVALID_ARG;
+    if (grad_out && (rows_meet(dz, address(loss_out), words) || rows_meet(dz, address(logp_out), words) ||
+                     (grad_out != logits && rows_meet(z, dz))))
+        return SPEC_ERR_INVALID_ARG;
     PolicyParams p;
     memset(&p, 0, sizeof(p));
     p.logits = logits;
@@ -675,12 +702,18 @@ spec_status spec_markov_grad(const void* grad, spec_dtype grad_dtype, int B, int
         V > SPEC_MAX_V_MARKOV || ld < V || r < 1 || r > SPEC_MAX_RANK)
         return SPEC_ERR_SHAPE;
     if (!grad || !anchor || (gamma > 1 && !tokens) || !U || !Wt || !dU_out || !dWt_out) return SPEC_ERR_INVALID_ARG;
-    for (const void* o : {(const void*)dU_out, (const void*)dWt_out})
-        if (o == grad || o == U || o == Wt) return SPEC_ERR_INVALID_ARG;
-    if (dU_out == dWt_out) return SPEC_ERR_INVALID_ARG;
     if (!aligned16(grad) || !aligned16(U) || !aligned16(Wt) || !aligned16(dU_out) || !aligned16(dWt_out) ||
         !aligned16(workspace))
         return SPEC_ERR_ALIGN;
+    const size_t weights = (size_t)V * r * dtype_size(weights_dtype), out = (size_t)V * r * dtype_size(out_dtype);
+    const size_t entry = dtype_size(grad_dtype);
+    const RowSpan dz = {address(grad), (long)B * gamma, ld * entry, V * entry};
+    for (const void* o : {(const void*)dU_out, (const void*)dWt_out})
+        if (rows_meet(dz, address(o), out) || spans_meet(address(o), out, address(U), weights) ||
+            spans_meet(address(o), out, address(Wt), weights) || spans_meet(address(o), out, address(anchor), (size_t)B * 4) ||
+            (gamma > 1 && spans_meet(address(o), out, address(tokens), (size_t)B * gamma * 4)))
+            return SPEC_ERR_INVALID_ARG;
+    if (spans_meet(address(dU_out), out, address(dWt_out), out)) return SPEC_ERR_INVALID_ARG;
     if (!workspace || workspace_bytes < markov_grad_workspace_bytes(B, gamma, V, r)) return SPEC_ERR_WORKSPACE;
     MarkovParams p;
     memset(&p, 0, sizeof(p));
@@ -746,4 +779,3 @@ spec_status spec_adamw(const spec_adamw_tensor* tensors, int n_tensors, int32_t*
 }
 
 }  // extern "C"
-
