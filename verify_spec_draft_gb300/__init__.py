@@ -908,7 +908,7 @@ def adamw_state(param, bits=32, master=None):
     else:
         raise ValueError(f"a state has 32 or 8 bits, got {bits}")
     if _dtype_code(param) == BF16:
-        s["master"] = param.float() if master is None else master
+        s["master"] = param.detach().float() if master is None else master
     elif master is not None:
         raise ValueError("a float32 parameter has no master")
     return s
