@@ -922,6 +922,9 @@ class AdamwTable:
         # the memory that the addresses are of, whatever a tensor is given later (p.data = ...)
         self.storages = [t.untyped_storage() for p, g, s in zip(params, grads, states)
                          for t in (p, g, *map(s.get, _STATE)) if t is not None]
+        # parameters whose gradient is the one that a backward pass adds to
+        self.leaves = [(i, p, g) for i, (p, g) in enumerate(zip(params, grads))
+                       if p.requires_grad and p.is_leaf and p.grad is g]
 
     def __len__(self):
         return len(self.params)
@@ -944,7 +947,9 @@ def adamw_table(params, grads, states):
     """The tensors of an AdamW step, checked once and kept: lists of parameters (f32/bf16), of
     their gradients (f32/bf16, read anew at every step) and of their states (adamw_state's dicts;
     32 and 8 bits may be mixed).  Steps write the parameters and states in place, so none of them may
-    overlap another tensor of the table; a tensor that is given other memory later needs a new table."""
+    overlap another tensor of the table; a tensor that is given other memory later needs a new table.
+    So does a parameter whose .grad becomes another tensor: zero_grad has to keep it (set_to_none=False); a
+    step over a table made of p.grad refuses one that is not there any more."""
     torch = _torch()
     params, grads, states = list(params), list(grads), list(states)
     if not len(params) == len(grads) == len(states):
@@ -1001,6 +1006,9 @@ def adamw(table, step, lr, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, grad
     a_step, a_scale = _addrs(dev, ("step", "grad_scale"), (step, grad_scale), (torch.int32, torch.float32), ((1,), (1,)))
     if a_step is None:
         raise ValueError("step is required")
+    for i, p, g in table.leaves:
+        if p.grad is not g:
+            raise ValueError(f"parameter {i}'s gradient is not the table's any more (zero_grad(set_to_none=True)?)")
     if ws is None:
         with _made_on(stream):
             ws = workspace(OP_ADAMW, len(table), 1, 1, 0, dev, stream)
