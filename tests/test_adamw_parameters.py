@@ -1,4 +1,5 @@
-"""AdamW steps over parameters of an autograd graph: gradients that are no longer theirs (one GB300)."""
+"""AdamW steps over parameters of an autograd graph: gradients that are no longer theirs,
+and backward passes through parameters that have changed (one GB300)."""
 
 import pytest
 import torch
@@ -45,3 +46,15 @@ def test_gradients_of_the_callers_own(spec):
     vsd.adamw(t, step, lr=0.5, weight_decay=0.0)
     # m / (sqrt(v) + eps) is 1 but for eps and some roundings of 2^-24, and the parameter's own half step
     assert all((p.detach().float() - 0.5).abs().max() < 1e-6 + 0.5 * 2.0 ** -8 * (p.dtype == torch.bfloat16) for p in ps)
+
+
+def test_a_backward_pass_through_what_a_step_has_changed_is_refused(spec):
+    ps, t, step = table()
+    loss = sum((p.float() * p.float()).sum() for p in ps[:1]) + (ps[1] * ps[1]).float().sum()
+    vsd.adamw(t, step, lr=1e-2)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+    loss = sum((p * p).float().sum() for p in ps)
+    loss.backward()                                # of the parameters as they are now
+    vsd.adamw(t, step, lr=1e-2)
+    assert int(step) == 2

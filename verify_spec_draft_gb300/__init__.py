@@ -922,6 +922,8 @@ class AdamwTable:
         # the memory that the addresses are of, whatever a tensor is given later (p.data = ...)
         self.storages = [t.untyped_storage() for p, g, s in zip(params, grads, states)
                          for t in (p, g, *map(s.get, _STATE)) if t is not None]
+        # what autograd may hold for a backward pass
+        self.tracked = [p for p in params if p.requires_grad]
         # parameters whose gradient is the one that a backward pass adds to
         self.leaves = [(i, p, g) for i, (p, g) in enumerate(zip(params, grads))
                        if p.requires_grad and p.is_leaf and p.grad is g]
@@ -1017,4 +1019,6 @@ def adamw(table, step, lr, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, grad
                           _ws_bytes(ws, dev), _stream(stream))
     if code != OK:
         raise SpecError(code, "spec_adamw")
+    if table.tracked:   # so that a backward pass through what they were before is refused
+        torch.autograd.graph.increment_version(table.tracked)
     return dict(step=step, ws=ws)
