@@ -896,7 +896,8 @@ def markov_grad(grad, anchor, tokens, U, Wt, dtype=None, ws=None, out=None, stre
 def adamw_state(param, bits=32, master=None):
     """A parameter's state for adamw: a dict of device tensors, m and v (zeros), in 8 bits also
     m_scale and v_scale, for a bf16 parameter its float32 master (the parameter's values, or
-    the tensor given)."""
+    the tensor given).  Over many steps v in 8 bits settles 3 to 6 % above v in 32, and its root
+    scatters by some 15 % (spec_adamw says why)."""
     torch = _torch()
     dev, shape = param.device, param.shape
     if bits == 32:
