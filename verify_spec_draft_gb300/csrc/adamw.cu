@@ -190,10 +190,7 @@ template <typename T> __device__ __forceinline__ Quad load4(const T* a) {
     }
 }
 __device__ __forceinline__ uint2 half4(const float4& x) {
-    uint2 w;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w.x) : "f"(x.y), "f"(x.x));
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w.y) : "f"(x.w), "f"(x.z));
-    return w;
+    return make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
 }
 
 // A warp's turn of whole blocks, every access a word of 4 entries.  Lane l holds the scales of the l-th

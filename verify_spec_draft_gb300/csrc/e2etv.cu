@@ -96,13 +96,6 @@ __device__ __forceinline__ uint32_t bmax2(uint32_t a, uint32_t b) {
     return r;
 }
 
-// Two floats rounded to nearest-even bf16, lo in the low half.
-__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
 // Rows of one branch: staged in shared memory (stride cols) or read from global.
 struct Rows {
     const bf16_t* tgt;

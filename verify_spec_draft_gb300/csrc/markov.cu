@@ -199,10 +199,7 @@ template <bool VEC> __device__ __forceinline__ uint2 quad_load(const bf16_t* a, 
 template <bool VEC> __device__ __forceinline__ void quad_store(void* out, int dtype, long at, int left, const float4& x) {
     if (VEC) {
         if (dtype == SPEC_BF16) {
-            uint2 w;
-            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w.x) : "f"(x.y), "f"(x.x));
-            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w.y) : "f"(x.w), "f"(x.z));
-            *reinterpret_cast<uint2*>(reinterpret_cast<bf16_t*>(out) + at) = w;
+            *reinterpret_cast<uint2*>(reinterpret_cast<bf16_t*>(out) + at) = make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
         } else {
             *reinterpret_cast<float4*>(reinterpret_cast<float*>(out) + at) = x;
         }

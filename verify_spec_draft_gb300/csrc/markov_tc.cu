@@ -348,7 +348,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMtcThreads, 1)
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
                                 const int at = (q + 8 * h + 2 * e) % W;
-                                asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(x[e]) : "f"(acc[at + 1]), "f"(acc[at]));
+                                x[e] = pack_bf16x2(acc[at], acc[at + 1]);
                             }
                             w[h] = make_uint4(x[0], x[1], x[2], x[3]);
                         } else {

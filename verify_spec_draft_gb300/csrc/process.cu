@@ -80,7 +80,7 @@ __device__ __forceinline__ uint4 word_scaled(const uint4& w, float f) {
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
             const float2 y = f2_unpack(f2_mul(bf2_widen(h[r]), ff));
-            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(o[r]) : "f"(y.y), "f"(y.x));
+            o[r] = pack_bf16x2(y.x, y.y);
         }
     } else {
 #pragma unroll

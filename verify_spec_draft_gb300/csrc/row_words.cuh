@@ -246,7 +246,7 @@ __device__ __forceinline__ uint4 word_of(const float (&x)[16 / sizeof(T)]) {
     if constexpr (sizeof(T) == 2) {
         uint32_t h[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(h[k]) : "f"(x[2 * k + 1]), "f"(x[2 * k]));
+        for (int k = 0; k < 4; ++k) h[k] = pack_bf16x2(x[2 * k], x[2 * k + 1]);
         return make_uint4(h[0], h[1], h[2], h[3]);
     } else {
         return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));

@@ -195,6 +195,12 @@ __device__ __forceinline__ f2x f2_mul(f2x a, f2x b) {
 __device__ __forceinline__ f2x bf2_widen(uint32_t w) {
     return f2_pack(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
 }
+// Two floats rounded to nearest-even bf16, lo in the low half.
+__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
 // (2^x, 2^y) of a pair
 __device__ __forceinline__ f2x f2_ex2(f2x v) {
     const float2 a = f2_unpack(v);
