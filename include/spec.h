@@ -798,7 +798,10 @@ spec_status spec_markov_grad(const void *grad, spec_dtype grad_dtype, int B, int
  *   tensors       HOST array [n_tensors], read during the call.
  *   step          int32 device [1]: steps taken so far; the call makes it T = step + 1.
  *   grad_scale    float32 device [1], nullable (1): e.g. a clip factor.
- *   lr >= 0, 0 <= beta1 < 1, 0 <= beta2 < 1, eps >= FLT_MIN, weight_decay >= 0, finite.
+ *   lr >= 0, 0 <= beta1 < 1, 0 <= beta2 < 1, eps >= FLT_MIN, weight_decay >= 0, finite: numbers
+ *                 of the call and all its tensors.  Tensors with another rate or decay are a call of
+ *                 their own, with a step of its own; a captured call keeps the numbers that it was
+ *                 captured with.
  *   workspace     spec_workspace_bytes(SPEC_OP_ADAMW, n_tensors, 1, 1, 0): the header.
  * Tensors may not overlap.  Pointers need only their type's alignment (16 bytes are faster,
  * as is a multiple of 4 entries).  An entry whose gradient is not finite, or whose m or v

@@ -999,7 +999,10 @@ def adamw(table, step, lr, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, grad
           stream=None):
     """spec_adamw: one AdamW step over an adamw_table, in place.  step int32 [1] on the device,
     the steps taken so far, which the call counts up; grad_scale float32 [1] on the device or None,
-    a factor of all gradients; seed the 8-bit states' random rounding.  Returns a dict: step."""
+    a factor of all gradients; seed the 8-bit states' random rounding.  lr and weight_decay are the whole
+    table's (parameters with others need a table and a step of their own) and stay what they are in a
+    captured call.  A backward pass through parameters as they were before the step is refused by
+    torch, but not after a replayed graph, which raises no versions.  Returns a dict: step."""
     torch = _torch()
     lib = _lib or load()
     dev = table.device

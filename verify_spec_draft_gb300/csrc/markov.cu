@@ -174,9 +174,13 @@ __global__ void __launch_bounds__(kMarkovThreads) markov_order_kernel(MarkovPara
 // dWt[v] = sum_i dz[i, v] U[x_i] with U's rows in shared memory, and dX's sums of its columns in
 // registers, one per row, which the CTA's threads bring together at the end.  The tensor cores would spend their
 // steps of 64 rows on zeros, and need float32 operands split (GPU time of the call, 7 rows, here and there:
-// V = 32,000, r = 32 float32 9.9 and 48 us; 248,320, 64 bf16, float32 out 35 and 64; 248,320, 256 bf16 91 and 82,
-// float32 out 116 and 123).  Bound by memory where V is large, Wt in, dWt and dU's zeros out (5.5 TB/s at the last),
-// and by issue slots beside it; by a chain of latencies where it is small.
+// V = 32,000, r = 32 float32 9.9 and 48 us; bf16 weights and outputs at V = 248,320: r = 64 28 and 71, 128 49 and 62,
+// 192 73 and 83, 256 91 and 83, with float32 outputs 117 and 126; r = 256 at V = 151,936: 62 and 59, at 32,000: 25 and
+// 28).  Bound by memory where V is large, Wt in, dWt and dU's zeros out (5.5 TB/s with float32 outputs), and by
+// issue slots beside it; by a chain of latencies where it is small.
+// All calls of up to 8 rows come here, the one corner where the other way is 6 to 9 % shorter (r = 256, bf16 outputs,
+// large vocabularies) included: a block's gradient then has the same two launches and the same float32 sums
+// whatever the rank and the outputs' type.
 template <typename T> struct QuadWord { typedef uint2 type; };
 template <> struct QuadWord<float> { typedef float4 type; };
 __device__ __forceinline__ float4 quad_value(const float4& w) { return w; }

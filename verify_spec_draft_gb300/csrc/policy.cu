@@ -9,7 +9,8 @@
 // another's shared memory.  1 - q_x is summed over the other entries, so a token of probability
 // near 1 keeps its gradient's digits.
 // Bound by memory: a row in, its gradient out (1792 rows of 248,320 bf16, one in ten of weight 0: 285 us,
-// 88 % of the measured copy rate in what moves; 448 rows' loss alone: 37 us, 88 %).
+// 88 % of the measured copy rate in what moves; 448 rows' loss alone, where one in ten is not read either: 37 us,
+// 81 %; all 448 read: 36.5 us, 91 %, in float32 68 us, 98 %).
 #include "internal.h"
 #include "row_words.cuh"
 
