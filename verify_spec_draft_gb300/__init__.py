@@ -951,7 +951,7 @@ def adamw_table(params, grads, states):
     their gradients (f32/bf16, read anew at every step) and of their states (adamw_state's dicts;
     32 and 8 bits may be mixed).  Steps write the parameters and states in place, so none of them may
     overlap another tensor of the table; a tensor that is given other memory later needs a new table.
-    So does a parameter whose .grad becomes another tensor: zero_grad has to keep it (set_to_none=False); a
+    So does a parameter whose .grad becomes other memory: zero_grad has to keep it (set_to_none=False); a
     step over a table made of p.grad refuses one that is not there any more."""
     torch = _torch()
     params, grads, states = list(params), list(grads), list(states)
@@ -1013,7 +1013,7 @@ def adamw(table, step, lr, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, grad
     if a_step is None:
         raise ValueError("step is required")
     for i, p, g in table.leaves:
-        if p.grad is not g:
+        if p.grad is not g and (p.grad is None or p.grad.data_ptr() != g.data_ptr()):
             raise ValueError(f"parameter {i}'s gradient is not the table's any more (zero_grad(set_to_none=True)?)")
     if ws is None:
         with _made_on(stream):
